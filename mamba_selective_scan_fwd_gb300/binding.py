@@ -22,13 +22,15 @@ STATUS_NAMES = {0: "SS_OK", 1: "SS_ERR_INVALID_PROBLEM", 2: "SS_ERR_UNSUPPORTED"
                 4: "SS_ERR_CUDA", 5: "SS_ERR_DEVICE_TIMEOUT",
                 6: "SS_ERR_STAGING_FALLBACK"}
 
-# Every function include/ss.h declares.
+# Every function the headers under include/ declare.
 EXPORTS = ["ss_fwd", "ss_bwd", "ss_fwd_workspace_bytes", "ss_bwd_workspace_bytes", "ss_plan_info",
            "ss_status_string", "ss_abi_version", "ss_fwd_noalloc", "ss_saved_bytes", "ss_fwd_save",
            "ss_bwd_saved_workspace_bytes", "ss_bwd_saved", "ss_profile_events", "ss_fwd_ex", "ss_bwd_ex",
            "ss_decode_step", "ss_plan_segments", "ss_device_status", "ss_selftest_wait_timeout",
            "ss_set_copies_only", "ss_staging_uses_tma", "ss_measure_ex2_rate",
-           "ss_measure_fma_rate"]
+           "ss_measure_fma_rate",
+           "ss_la_fwd_workspace_bytes", "ss_la_fwd", "ss_la_bwd_workspace_bytes", "ss_la_bwd", "ss_la_step",
+           "ss_gnorm_fwd", "ss_gnorm_bwd_workspace_bytes", "ss_gnorm_bwd"]
 ABI_VERSION = 7
 
 # Size of the library-owned scratch behind ss_fwd_noalloc (SS_FWD_NOALLOC_MAX_SCRATCH_BYTES).
@@ -118,6 +120,19 @@ def lib() -> ctypes.CDLL:
     L.ss_staging_uses_tma.argtypes = [_I64] * 4 + [ctypes.c_int]
     L.ss_decode_step.restype = ctypes.c_int
     L.ss_decode_step.argtypes = [_P] * 8 + [ctypes.c_int, ctypes.c_int, _P, _P] + [_I64] * 3 + [ctypes.c_int, _P]
+    # include/ss_la.h (the descriptors are defined in linear_attention.py)
+    for fn in ("ss_la_fwd_workspace_bytes", "ss_la_bwd_workspace_bytes"):
+        getattr(L, fn).restype = _SZ
+        getattr(L, fn).argtypes = [_I64] * 6 + [ctypes.c_int]
+    for fn in ("ss_la_fwd", "ss_la_bwd", "ss_la_step"):
+        getattr(L, fn).restype = ctypes.c_int
+        getattr(L, fn).argtypes = [_P, _P]
+    L.ss_gnorm_fwd.restype = ctypes.c_int
+    L.ss_gnorm_fwd.argtypes = [_P] * 5 + [_I64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, _P]
+    L.ss_gnorm_bwd_workspace_bytes.restype = _SZ
+    L.ss_gnorm_bwd_workspace_bytes.argtypes = [_I64] * 3 + [ctypes.c_int]
+    L.ss_gnorm_bwd.restype = ctypes.c_int
+    L.ss_gnorm_bwd.argtypes = [_P] * 9 + [_I64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, _P, _SZ, _P]
     _lib = L
     return L
 

@@ -24,6 +24,9 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 SOURCES = ["api.cu", "dispatch.cu", "fwd_f32.cu", "fwd_bf16.cu", "fwd_f16.cu", "bwd_f32.cu",
            "bwd_bf16.cu", "bwd_f16.cu", "decode.cu", "fwd_noalloc.cu", "probe.cu"]
+# linear attention and its output norm (include/ss_la.h): kernels of their own, in
+# a folder of their own, outside source_digest() (which identifies the scan's kernels)
+LM_SOURCES = ["lm/la_api.cu", "lm/la_f32.cu", "lm/la_step.cu", "lm/gnorm.cu"]
 
 
 def nvcc() -> str:
@@ -35,13 +38,11 @@ def nvcc() -> str:
 
 def _digest() -> str:
     h = hashlib.sha256()
-    h.update(" ".join(ARCH + NVCC_FLAGS + SOURCES).encode())
-    deps = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
-    for name in deps:
-        with open(os.path.join(CSRC, name), "rb") as f:
-            h.update(name.encode() + f.read())
-    with open(os.path.join(ROOT, "include", "ss.h"), "rb") as f:
-        h.update(f.read())
+    h.update(" ".join(ARCH + NVCC_FLAGS + SOURCES + LM_SOURCES).encode())
+    for folder in (CSRC, os.path.join(CSRC, "lm"), os.path.join(ROOT, "include")):
+        for name in sorted(f for f in os.listdir(folder) if f.endswith((".cu", ".cuh", ".h"))):
+            with open(os.path.join(folder, name), "rb") as f:
+                h.update(name.encode() + f.read())
     return h.hexdigest()
 
 
@@ -56,8 +57,8 @@ def _code(text: str) -> str:
 
 
 def source_digest() -> str:
-    """Digest of the kernel sources (comments and layout ignored) and build flags:
-    changes whenever the compiled kernels may change, and only then."""
+    """Digest of the scan's kernel sources (comments and layout ignored) and build flags:
+    changes whenever its compiled kernels may change, and only then."""
     h = hashlib.sha256()
     h.update(" ".join(ARCH + NVCC_FLAGS + SOURCES).encode())
     deps = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
@@ -79,7 +80,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     exe = nvcc()
 
     def compile_one(src):
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
+        obj = os.path.join(BUILD, src.replace("/", "_").replace(".cu", ".o"))
         cmd = [exe, *ARCH, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         with open(obj + ".log", "w") as f:
@@ -90,8 +91,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
+    sources = SOURCES + LM_SOURCES
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = list(ex.map(compile_one, sources))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

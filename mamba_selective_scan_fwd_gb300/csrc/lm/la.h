@@ -1,0 +1,125 @@
+// Head-decay linear attention: arguments, launch plans and workspace layouts
+// shared by the C ABI (la_api.cu) and the kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../common.cuh"
+
+namespace ss {
+namespace la {
+
+// An input of [Bsz, L, heads, width]: the last two dimensions contiguous, the
+// first two with strides in elements.
+struct In {
+    const void* p;
+    int64_t token, batch;
+};
+
+struct Args {
+    In q, k, v, dy;          // dy: backward only
+    const float* g;          // [Bsz, L, H], or [H] when g_per_head
+    const float* h0;         // forward initial state, or null
+    const float* dlast;      // gradient of the last state, or null (backward)
+    const int32_t* lengths;  // [Bsz] or null
+    int64_t Bsz, L, H, G, N, P;
+    float scale;
+    int dtype, g_per_head;
+};
+
+constexpr int kSms = 152;
+constexpr int kMaxN = 128;
+
+// ---------------------------------------------------------------- FP32 path
+constexpr int kWalkP = 32;    // value channels per block of the token walk
+constexpr int kWalkT = 16;    // tokens staged at a time
+constexpr int kChunk32 = 64;  // tokens per chunk of the FP32 backward
+
+// The token walk: every (batch row, head, tile of value channels) is cut into
+// K segments of seg tokens (a multiple of a chunk).
+struct WalkPlan {
+    int64_t K, seg;
+};
+inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t chunk) {
+    // enough blocks for four on every SM, segments of at least four chunks
+    int64_t K = (4 * kSms + units - 1) / (units > 0 ? units : 1);
+    const int64_t most = L / (4 * chunk);
+    if (K > most) K = most;
+    if (K < 1) K = 1;
+    int64_t seg = ceil_div(ceil_div(L, K), chunk) * chunk;
+    return {ceil_div(L, seg), seg};
+}
+
+enum WalkMode { kWalkSum = 0, kWalkY = 1, kWalkStates = 2 };
+
+struct WalkArgs {
+    Args a;
+    WalkPlan plan;
+    const float* init;   // state before the walk's first token, or null
+    float* seg_state;    // [Bsz, H, K, N, P]: end states of the segments, then (after the carry) their start states
+    float* seg_decay;    // [Bsz, H, K]
+    void* y;             // kWalkY
+    float* last;         // state after the walk's last token, or null
+    float* chunk_state;  // kWalkStates: [Bsz, H, chunks, N, P] state before each chunk (in walking order)
+    int64_t chunks;
+};
+
+// Adds the incoming states up along the segments of a walk.
+struct CarryArgs {
+    float* seg_state;
+    const float* seg_decay;
+    const float* init;
+    int64_t BH, K, NP;
+    int reverse;
+};
+
+struct BwdArgs {
+    Args a;
+    const float* before;  // [Bsz, H, chunks, N, P] state before each chunk
+    const float* after;   // [Bsz, H, chunks, N, P] adjoint of the state after each chunk
+    int64_t chunks;
+    void *dq, *dk, *dv;
+    float* dg;            // [Bsz, L, H]
+    float *dq_part, *dk_part;  // [splits, Bsz, L, G, N] f32 when splits > 1
+    int splits;           // parts the heads of one group are divided into
+};
+
+cudaError_t launch_walk32(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st);
+cudaError_t launch_carry(const CarryArgs& c, cudaStream_t st);
+cudaError_t launch_bwd32(const BwdArgs& b, cudaStream_t st);
+cudaError_t launch_sum_parts(const float* part, void* out, int splits, int64_t n, int dtype, cudaStream_t st);
+// dg [rows, H] summed over rows into out [H]; part holds kDgParts * H floats
+constexpr int kDgParts = 64;
+cudaError_t launch_sum_rows(const float* dg, float* part, float* out, int64_t rows, int64_t H, cudaStream_t st);
+
+struct StepArgs {
+    const void *q, *k, *v;
+    const float* g;
+    float* state;
+    const int32_t* slots;
+    void* y;
+    int64_t q_batch, k_batch, v_batch;
+    int64_t Bsz, H, G, N, P, pool;
+    float scale;
+    int dtype, g_per_head;
+};
+cudaError_t launch_step(const StepArgs& s, cudaStream_t st);
+
+}  // namespace la
+
+struct GnormArgs {
+    const void *x, *z, *dout;
+    const float *weight, *bias;
+    void *out, *dx, *dz;
+    float *dweight, *dbias;
+    float* part;  // backward: [blocks, 2, C] partial sums
+    int64_t M, C, groups;
+    float eps;
+    int flags, dtype;
+};
+cudaError_t launch_gnorm_fwd(const GnormArgs& a, cudaStream_t st);
+cudaError_t launch_gnorm_bwd(const GnormArgs& a, cudaStream_t st);
+int64_t gnorm_bwd_blocks(int64_t M, int64_t C, int64_t groups);
+
+}  // namespace ss

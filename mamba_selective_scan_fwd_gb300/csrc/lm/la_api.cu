@@ -1,0 +1,298 @@
+// C ABI of the linear attention and the gated group norm (include/ss_la.h).
+// Everything is checked before the first CUDA call; on error nothing is
+// written.
+#include "la.h"
+#include "ss_la.h"
+
+using namespace ss;
+using namespace ss::la;
+
+namespace {
+
+bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+int check_dtype(int dtype) { return dtype == SS_F32 || dtype == SS_F16 || dtype == SS_BF16 ? SS_OK : SS_ERR_UNSUPPORTED; }
+
+int64_t elem(int dtype) { return dtype == SS_F32 ? 4 : 2; }
+
+int check_sizes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
+    if (Bsz < 0 || L < 0 || H < 1 || G < 1 || N < 1 || P < 1 || H % G != 0) return SS_ERR_INVALID_PROBLEM;
+    if (check_dtype(dtype) != SS_OK || N > kMaxN) return SS_ERR_UNSUPPORTED;
+    // products stay inside int64, grids inside 2^31 - 1 blocks
+    if (Bsz > (1 << 20) || L > (1ll << 31) || H > (1 << 16) || P > (1 << 16)) return SS_ERR_UNSUPPORTED;
+    if (Bsz * H * ceil_div(P, 16) > (1ll << 24) || Bsz * L > (1ll << 36)) return SS_ERR_UNSUPPORTED;
+    if (Bsz * ceil_div(L, kChunk32) * H > (1ll << 30)) return SS_ERR_UNSUPPORTED;
+    return SS_OK;
+}
+
+// A run of the workspace, in bytes from its start.
+struct Layout {
+    size_t total = 0;
+    size_t take(size_t bytes) {
+        const size_t at = total;
+        total = align_up(total + bytes, 256);
+        return at;
+    }
+};
+
+// The FP32 path's workspace.
+struct Walk32 {
+    WalkPlan plan;
+    size_t state, decay;
+};
+Walk32 walk32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P) {
+    Walk32 w;
+    w.plan = walk_plan(Bsz * H * ceil_div(P, kWalkP), L, kChunk32);
+    w.state = w.decay = 0;
+    if (w.plan.K > 1) {
+        w.state = l.take((size_t)Bsz * H * w.plan.K * N * P * 4);
+        w.decay = l.take((size_t)Bsz * H * w.plan.K * 4);
+    }
+    return w;
+}
+
+struct Bwd32 {
+    Walk32 walk;
+    int64_t chunks;
+    int splits;
+    size_t before, after, dq, dk, dg, rows;
+};
+// Parts the heads of a group are divided into, so that the chunk kernel has
+// about two blocks per SM; each part beyond the first costs one more f32 copy
+// of dq and dk.
+int head_splits(int64_t blocks, int64_t rep) {
+    int64_t s = ceil_div(2 * kSms, blocks);
+    if (s > rep) s = rep;
+    return (int)(s < 1 ? 1 : s);
+}
+Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
+    Bwd32 b;
+    b.walk = walk32_layout(l, Bsz, L, H, N, P);
+    b.chunks = ceil_div(L, kChunk32);
+    b.splits = head_splits(Bsz * b.chunks * G, H / G);
+    const size_t states = (size_t)Bsz * H * b.chunks * N * P * 4;
+    b.before = l.take(states);
+    b.after = l.take(states);
+    const size_t part = b.splits > 1 ? (size_t)b.splits * Bsz * L * G * N * 4 : 0;
+    b.dq = l.take(part);
+    b.dk = l.take(part);
+    b.dg = l.take((size_t)Bsz * L * H * 4);
+    b.rows = l.take((size_t)kDgParts * H * 4);
+    return b;
+}
+
+bool empty(int64_t Bsz, int64_t L) { return Bsz == 0 || L == 0; }
+
+// The state that no token changes: a copy of the incoming one, or zeros.
+int pass_state(float* to, const float* from, int64_t Bsz, int64_t H, int64_t N, int64_t P, cudaStream_t st) {
+    const size_t bytes = (size_t)Bsz * H * N * P * 4;
+    if (!to || bytes == 0) return SS_OK;
+    const cudaError_t e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, st)
+                               : cudaMemsetAsync(to, 0, bytes, st);
+    return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+// A walk over all segments: sums of the segments, their carries, then the walk itself.
+cudaError_t run_walk32(WalkArgs w, bool reverse, WalkMode mode, cudaStream_t st) {
+    if (w.plan.K > 1) {
+        cudaError_t e = launch_walk32(w, reverse, kWalkSum, st);
+        if (e != cudaSuccess) return e;
+        e = launch_carry({w.seg_state, w.seg_decay, w.init, w.a.Bsz * w.a.H, w.plan.K, w.a.N * w.a.P, reverse ? 1 : 0}, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_walk32(w, reverse, mode, st);
+}
+
+bool strides_ok(int64_t token, int64_t batch) { return token >= 0 && batch >= 0 && token <= (1ll << 40) && batch <= (1ll << 48); }
+
+}  // namespace
+
+extern "C" {
+
+size_t ss_la_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
+    if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
+    Layout l;
+    walk32_layout(l, Bsz, L, H, N, P);
+    return l.total;
+}
+
+int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
+    if (!d) return SS_ERR_INVALID_PROBLEM;
+    const int rc = check_sizes(d->Bsz, d->L, d->H, d->G, d->N, d->P, d->dtype);
+    if (rc != SS_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!strides_ok(d->q_token, d->q_batch) || !strides_ok(d->k_token, d->k_batch) || !strides_ok(d->v_token, d->v_batch))
+        return SS_ERR_INVALID_PROBLEM;
+    if (misaligned16(d->y) || misaligned16(d->h0) || misaligned16(d->last_state) || misaligned16(d->workspace))
+        return SS_ERR_UNSUPPORTED;
+    if (empty(d->Bsz, d->L)) return pass_state(d->last_state, d->h0, d->Bsz, d->H, d->N, d->P, st);
+    if (!d->q || !d->k || !d->v || !d->g || !d->y) return SS_ERR_INVALID_PROBLEM;
+    const size_t need = ss_la_fwd_workspace_bytes(d->Bsz, d->L, d->H, d->G, d->N, d->P, d->dtype);
+    if (d->workspace_bytes < need || (need > 0 && !d->workspace)) return SS_ERR_WORKSPACE_TOO_SMALL;
+    Args a = {};
+    a.q = {d->q, d->q_token, d->q_batch};
+    a.k = {d->k, d->k_token, d->k_batch};
+    a.v = {d->v, d->v_token, d->v_batch};
+    a.g = d->g;
+    a.h0 = d->h0;
+    a.lengths = d->lengths;
+    a.Bsz = d->Bsz; a.L = d->L; a.H = d->H; a.G = d->G; a.N = d->N; a.P = d->P;
+    a.scale = d->scale;
+    a.dtype = d->dtype;
+    a.g_per_head = d->g_per_head ? 1 : 0;
+    char* ws = static_cast<char*>(d->workspace);
+    Layout l;
+    const Walk32 wl = walk32_layout(l, a.Bsz, a.L, a.H, a.N, a.P);
+    WalkArgs w = {};
+    w.a = a;
+    w.plan = wl.plan;
+    w.init = a.h0;
+    w.seg_state = reinterpret_cast<float*>(ws + wl.state);
+    w.seg_decay = reinterpret_cast<float*>(ws + wl.decay);
+    w.y = d->y;
+    w.last = d->last_state;
+    return run_walk32(w, false, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+size_t ss_la_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
+    if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
+    Layout l;
+    bwd32_layout(l, Bsz, L, H, G, N, P);
+    return l.total;
+}
+
+int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
+    if (!d) return SS_ERR_INVALID_PROBLEM;
+    const int rc = check_sizes(d->Bsz, d->L, d->H, d->G, d->N, d->P, d->dtype);
+    if (rc != SS_OK) return rc;
+    if ((d->h0 == nullptr) != (d->dh0 == nullptr)) return SS_ERR_INVALID_PROBLEM;
+    if (!strides_ok(d->q_token, d->q_batch) || !strides_ok(d->k_token, d->k_batch) ||
+        !strides_ok(d->v_token, d->v_batch) || !strides_ok(d->dy_token, d->dy_batch))
+        return SS_ERR_INVALID_PROBLEM;
+    const void* ptrs[] = {d->h0, d->dlast_state, d->dq, d->dk, d->dv, d->dg, d->dh0, d->workspace};
+    for (const void* p : ptrs)
+        if (misaligned16(p)) return SS_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (empty(d->Bsz, d->L)) {
+        if (d->g_per_head) {
+            if (!d->dg) return SS_ERR_INVALID_PROBLEM;
+            if (cudaMemsetAsync(d->dg, 0, (size_t)d->H * 4, st) != cudaSuccess) return SS_ERR_CUDA;
+        }
+        return pass_state(d->dh0, d->dlast_state, d->Bsz, d->H, d->N, d->P, st);
+    }
+    if (!d->q || !d->k || !d->v || !d->g || !d->dy || !d->dq || !d->dk || !d->dv || !d->dg) return SS_ERR_INVALID_PROBLEM;
+    const size_t need = ss_la_bwd_workspace_bytes(d->Bsz, d->L, d->H, d->G, d->N, d->P, d->dtype);
+    if (d->workspace_bytes < need || !d->workspace) return SS_ERR_WORKSPACE_TOO_SMALL;
+    Args a = {};
+    a.q = {d->q, d->q_token, d->q_batch};
+    a.k = {d->k, d->k_token, d->k_batch};
+    a.v = {d->v, d->v_token, d->v_batch};
+    a.dy = {d->dy, d->dy_token, d->dy_batch};
+    a.g = d->g;
+    a.h0 = d->h0;
+    a.dlast = d->dlast_state;
+    a.lengths = d->lengths;
+    a.Bsz = d->Bsz; a.L = d->L; a.H = d->H; a.G = d->G; a.N = d->N; a.P = d->P;
+    a.scale = d->scale;
+    a.dtype = d->dtype;
+    a.g_per_head = d->g_per_head ? 1 : 0;
+    char* ws = static_cast<char*>(d->workspace);
+    Layout l;
+    const Bwd32 bl = bwd32_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    WalkArgs w = {};
+    w.a = a;
+    w.plan = bl.walk.plan;
+    w.seg_state = f32(bl.walk.state);
+    w.seg_decay = f32(bl.walk.decay);
+    w.chunks = bl.chunks;
+    w.init = a.h0;
+    w.chunk_state = f32(bl.before);
+    if (run_walk32(w, false, kWalkStates, st) != cudaSuccess) return SS_ERR_CUDA;
+    w.init = a.dlast;
+    w.chunk_state = f32(bl.after);
+    w.last = d->dh0;
+    if (run_walk32(w, true, kWalkStates, st) != cudaSuccess) return SS_ERR_CUDA;
+    BwdArgs b = {};
+    b.a = a;
+    b.before = f32(bl.before);
+    b.after = f32(bl.after);
+    b.chunks = bl.chunks;
+    b.dq = d->dq; b.dk = d->dk; b.dv = d->dv;
+    b.dg = a.g_per_head ? f32(bl.dg) : d->dg;
+    b.dq_part = f32(bl.dq);
+    b.dk_part = f32(bl.dk);
+    b.splits = bl.splits;
+    if (launch_bwd32(b, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (b.splits > 1) {
+        const int64_t n = a.Bsz * a.L * a.G * a.N;
+        if (launch_sum_parts(b.dq_part, d->dq, b.splits, n, a.dtype, st) != cudaSuccess ||
+            launch_sum_parts(b.dk_part, d->dk, b.splits, n, a.dtype, st) != cudaSuccess)
+            return SS_ERR_CUDA;
+    }
+    if (a.g_per_head && launch_sum_rows(b.dg, f32(bl.rows), d->dg, a.Bsz * a.L, a.H, st) != cudaSuccess)
+        return SS_ERR_CUDA;
+    return SS_OK;
+}
+
+int ss_la_step(const ss_la_step_desc* d, void* stream) {
+    if (!d) return SS_ERR_INVALID_PROBLEM;
+    const int rc = check_sizes(d->Bsz, 1, d->H, d->G, d->N, d->P, d->dtype);
+    if (rc != SS_OK) return rc;
+    if (d->pool < 0 || (!d->slots && d->pool < d->Bsz) || d->q_batch < 0 || d->k_batch < 0 || d->v_batch < 0)
+        return SS_ERR_INVALID_PROBLEM;
+    if (misaligned16(d->state) || misaligned16(d->y)) return SS_ERR_UNSUPPORTED;
+    if (d->Bsz == 0) return SS_OK;
+    if (!d->q || !d->k || !d->v || !d->g || !d->y || (!d->state && d->pool > 0)) return SS_ERR_INVALID_PROBLEM;
+    StepArgs s = {d->q, d->k, d->v, d->g, d->state, d->slots, d->y, d->q_batch, d->k_batch, d->v_batch,
+                  d->Bsz, d->H, d->G, d->N, d->P, d->pool, d->scale, d->dtype, d->g_per_head ? 1 : 0};
+    return launch_step(s, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+namespace {
+int check_gnorm(int64_t M, int64_t C, int64_t groups, float eps, int flags, int dtype, bool z) {
+    if (M < 0 || C < 1 || groups < 1 || C % groups != 0 || !(eps >= 0.0f)) return SS_ERR_INVALID_PROBLEM;
+    if (flags & ~(SS_GNORM_CENTER | SS_GNORM_GATE_FIRST)) return SS_ERR_INVALID_PROBLEM;
+    if ((flags & SS_GNORM_GATE_FIRST) && !z) return SS_ERR_INVALID_PROBLEM;
+    if (check_dtype(dtype) != SS_OK || C / groups > 8192 || C > (1 << 24) || M > (1ll << 36)) return SS_ERR_UNSUPPORTED;
+    return SS_OK;
+}
+}  // namespace
+
+int ss_gnorm_fwd(const void* x, const float* weight, const float* bias, const void* z, void* out, int64_t M, int64_t C,
+                 int64_t groups, float eps, int flags, int dtype, void* stream) {
+    const int rc = check_gnorm(M, C, groups, eps, flags, dtype, z != nullptr || M == 0);
+    if (rc != SS_OK) return rc;
+    if (M == 0) return SS_OK;
+    if (!x || !out) return SS_ERR_INVALID_PROBLEM;
+    GnormArgs a = {};
+    a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.out = out;
+    a.M = M; a.C = C; a.groups = groups;
+    a.eps = eps; a.flags = flags; a.dtype = dtype;
+    return launch_gnorm_fwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+size_t ss_gnorm_bwd_workspace_bytes(int64_t M, int64_t C, int64_t groups, int dtype) {
+    if (check_gnorm(M, C, groups, 0.0f, 0, dtype, true) != SS_OK) return 0;
+    return (size_t)gnorm_bwd_blocks(M, C, groups) * 2 * C * 4;
+}
+
+int ss_gnorm_bwd(const void* x, const float* weight, const float* bias, const void* z, const void* dout, void* dx,
+                 void* dz, float* dweight, float* dbias, int64_t M, int64_t C, int64_t groups, float eps, int flags,
+                 int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_gnorm(M, C, groups, eps, flags, dtype, z != nullptr || M == 0);
+    if (rc != SS_OK) return rc;
+    if ((weight == nullptr) != (dweight == nullptr) || (bias == nullptr) != (dbias == nullptr)) return SS_ERR_INVALID_PROBLEM;
+    if (M > 0 && (!x || !dout || !dx || (z == nullptr) != (dz == nullptr))) return SS_ERR_INVALID_PROBLEM;
+    if (misaligned16(workspace)) return SS_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < ss_gnorm_bwd_workspace_bytes(M, C, groups, dtype)) return SS_ERR_WORKSPACE_TOO_SMALL;
+    GnormArgs a = {};
+    a.x = x; a.z = z; a.dout = dout; a.weight = weight; a.bias = bias;
+    a.dx = dx; a.dz = dz; a.dweight = dweight; a.dbias = dbias;
+    a.part = static_cast<float*>(workspace);
+    a.M = M; a.C = C; a.groups = groups;
+    a.eps = eps; a.flags = flags; a.dtype = dtype;
+    return launch_gnorm_bwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+}  // extern "C"

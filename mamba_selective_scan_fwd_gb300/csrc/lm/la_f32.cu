@@ -1,0 +1,578 @@
+// Linear attention on the FP32 units: every io type, any N <= 128, P and
+// strides.  f32 inputs run here, and 16-bit inputs that the tensor-core path's
+// 16-byte rules exclude.
+//
+// The walk (forward, and the states the backward needs) is the recurrence
+// itself, token by token with the state in registers: 3 N P operations per
+// token and head, fewer than any chunked form takes without matrix units.  The
+// backward works on chunks of 64 tokens from the states at their borders.
+#include "la_dev.cuh"
+
+namespace ss {
+namespace la {
+namespace {
+
+// One block: kWalkP value channels of one head, one segment of tokens.  Lane =
+// value channel, warp = NR of the padded N state rows.
+//   forward   S <- e^g S + k v^T, y = scale q S
+//   reverse   X <- e^g (X + scale q dy^T), tokens last to first (X before the
+//             update is the adjoint of the state after the token)
+template <typename T, int NR, bool REV, int MODE>
+__global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
+    constexpr int NP = NR * 8;
+    constexpr int TT = kWalkT;
+    __shared__ __align__(16) float s_k[TT][NP];
+    __shared__ __align__(16) float s_q[MODE == kWalkY ? TT : 1][NP];
+    __shared__ float s_v[TT][kWalkP];
+    __shared__ float s_a[TT], s_g[TT];
+    __shared__ float s_y[MODE == kWalkY ? 8 : 1][TT][kWalkP];
+    const Args& a = w.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t ptiles = (a.P + kWalkP - 1) / kWalkP;
+    int64_t id = blockIdx.x;
+    const int64_t p0 = (id % ptiles) * kWalkP;
+    id /= ptiles;
+    const int64_t h = id % a.H;
+    id /= a.H;
+    const int64_t segs = MODE == kWalkSum ? w.plan.K - 1 : w.plan.K;
+    int64_t seg = id % segs;
+    const int64_t b = id / segs;
+    if (MODE == kWalkSum && REV) seg += 1;  // the segment walked last needs no sum
+    const int64_t hq = h / (a.H / a.G);
+    const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
+    const int64_t len = row_length(a, b);
+    const int64_t p = p0 + lane;
+    const int n0 = warp * NR;
+    const int64_t NPel = a.N * a.P;
+    const In& kin = REV ? a.q : a.k;
+    const In& vin = REV ? a.dy : a.v;
+    const T* kp = static_cast<const T*>(kin.p) + b * kin.batch + hq * a.N;
+    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
+    const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P;
+    const float kscale = REV ? a.scale : 1.0f;
+
+    float S[NR];
+    const float* init = nullptr;
+    if (MODE != kWalkSum) {
+        if (w.plan.K > 1) init = w.seg_state + ((b * a.H + h) * w.plan.K + seg) * NPel;
+        else if (w.init) init = w.init + (b * a.H + h) * NPel;
+    }
+#pragma unroll
+    for (int r = 0; r < NR; r++) S[r] = (init && n0 + r < a.N && p < a.P) ? init[(n0 + r) * a.P + p] : 0.0f;
+    auto put = [&](float* dst) {
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            if (n0 + r < a.N && p < a.P) dst[(n0 + r) * a.P + p] = S[r];
+    };
+
+    float total = 0.0f;  // thread 0 of a sum pass: the segment's log decay
+    const int64_t tiles = (t_end - t_begin + TT - 1) / TT;
+    for (int64_t i = 0; i < tiles; i++) {
+        const int64_t t0 = t_begin + (REV ? tiles - 1 - i : i) * TT;
+        if (MODE == kWalkStates) {
+            const int64_t c = t0 / kChunk32;
+            const bool first = REV ? (t0 + TT >= t_end || (t0 + TT) % kChunk32 == 0) : t0 % kChunk32 == 0;
+            if (first) put(w.chunk_state + ((b * a.H + h) * w.chunks + c) * NPel);
+        }
+        __syncthreads();
+        const int nv = (int)max((int64_t)0, min((int64_t)TT, min(len, t_end) - t0));  // tokens that count
+        for (int e = tid; e < TT * NP; e += 256) {
+            const int t = e / NP, n = e % NP;
+            s_k[t][n] = (t < nv && n < a.N) ? kscale * ldf(kp + (t0 + t) * kin.token + n) : 0.0f;
+            if (MODE == kWalkY) s_q[t][n] = (t < nv && n < a.N) ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
+        }
+        for (int e = tid; e < TT * kWalkP; e += 256) {
+            const int t = e / kWalkP, c = e % kWalkP;
+            s_v[t][c] = (t < nv && p0 + c < a.P) ? ldf(vp + (t0 + t) * vin.token + p0 + c) : 0.0f;
+        }
+        if (tid < TT) {
+            const float g = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
+            s_g[tid] = g;
+            s_a[tid] = expf(g);
+        }
+        __syncthreads();
+        if (MODE == kWalkSum && tid == 0)
+            for (int t = 0; t < nv; t++) total += s_g[t];
+#pragma unroll 2
+        for (int j = 0; j < nv; j++) {
+            const int t = REV ? nv - 1 - j : j;
+            const float av = s_a[t], v = s_v[t][lane];
+            float acc = 0.0f;
+#pragma unroll
+            for (int r = 0; r < NR; r += 4) {
+                const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + r]);
+                if (REV) {
+                    S[r] = av * fmaf(kk.x, v, S[r]);
+                    S[r + 1] = av * fmaf(kk.y, v, S[r + 1]);
+                    S[r + 2] = av * fmaf(kk.z, v, S[r + 2]);
+                    S[r + 3] = av * fmaf(kk.w, v, S[r + 3]);
+                } else {
+                    S[r] = fmaf(av, S[r], kk.x * v);
+                    S[r + 1] = fmaf(av, S[r + 1], kk.y * v);
+                    S[r + 2] = fmaf(av, S[r + 2], kk.z * v);
+                    S[r + 3] = fmaf(av, S[r + 3], kk.w * v);
+                }
+                if (MODE == kWalkY) {
+                    const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + r]);
+                    acc = fmaf(qq.x, S[r], acc);
+                    acc = fmaf(qq.y, S[r + 1], acc);
+                    acc = fmaf(qq.z, S[r + 2], acc);
+                    acc = fmaf(qq.w, S[r + 3], acc);
+                }
+            }
+            if (MODE == kWalkY) s_y[warp][t][lane] = acc;
+        }
+        if (MODE == kWalkY) {
+            __syncthreads();
+            T* yp = static_cast<T*>(w.y) + (b * a.L * a.H + h) * a.P;
+            for (int e = tid; e < TT * kWalkP; e += 256) {
+                const int t = e / kWalkP, c = e % kWalkP;
+                if (t0 + t < t_end && p0 + c < a.P) {
+                    float y = 0.0f;
+                    if (t < nv) {
+#pragma unroll
+                        for (int u = 0; u < 8; u++) y += s_y[u][t][c];
+                    }
+                    st(yp + (t0 + t) * a.H * a.P + p0 + c, a.scale * y);
+                }
+            }
+        }
+    }
+    if (MODE == kWalkSum) {
+        put(w.seg_state + ((b * a.H + h) * w.plan.K + seg) * NPel);
+        if (tid == 0 && p0 == 0) w.seg_decay[(b * a.H + h) * w.plan.K + seg] = total;
+    } else if (w.last && seg == (REV ? 0 : w.plan.K - 1)) {
+        put(w.last + (b * a.H + h) * NPel);
+    }
+}
+
+// seg_state: end state of each segment walked from zero -> the state each
+// segment starts from.
+__global__ void __launch_bounds__(256) k_carry(CarryArgs c) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= c.BH * c.NP) return;
+    const int64_t bh = e / c.NP, x = e % c.NP;
+    float S = c.init ? c.init[bh * c.NP + x] : 0.0f;
+    for (int64_t i = 0; i < c.K; i++) {
+        const int64_t s = c.reverse ? c.K - 1 - i : i;
+        float* at = c.seg_state + (bh * c.K + s) * c.NP + x;
+        const bool more = i + 1 < c.K;
+        const float own = more ? *at : 0.0f;
+        *at = S;
+        if (more) S = fmaf(expf(c.seg_decay[bh * c.K + s]), S, own);
+    }
+}
+
+// ---------------------------------------------------------------- backward, one chunk of one group of heads
+constexpr int kPT = 64;  // value channels per pass
+constexpr int kLdP = kPT + 4;
+
+template <int NB> struct Smem32 {
+    static constexpr int NP = NB * 16, LD = NP + 4;
+    float q[kChunk32][LD], k[kChunk32][LD];
+    float v[kChunk32][kLdP], dy[kChunk32][kLdP];
+    float E[kChunk32][kLdP], S[kChunk32][kLdP];  // decayed dy v^T and q k^T (rows i, columns j <= i)
+    float H[NP][kLdP], R[NP][kLdP];
+    Two c[kChunk32];
+    float a[kChunk32], b[kChunk32], col[8][kChunk32], red[8];
+};
+
+// Thread (ty, tx) of 16 x 16 holds rows ty + 16 r and columns tx + 16 s of
+// every product.  With c_i the cumulative log decay inside the chunk, cl its
+// end, H the state before and R the adjoint after the chunk (all per head):
+//   m_ij = scale e^{c_i - c_j} (j <= i),  E = m o (dy v^T),  S = m o (q k^T),  W = E o (q k^T)
+//   dq = E k + scale e^{c} (dy H^T),  dk = E^T q + e^{cl - c} (v R^T),  dv = S^T dy + e^{cl - c} (k R)
+//   dg_t = sum_{i >= t} a_i + sum_{j < t} (b_j + col_j - row_j) + e^{cl} <R, H>
+// with a_i, b_j the inter-chunk parts of q.dq and k.dk and row, col the sums
+// of W below the diagonal: col_j - row_j telescopes to the pairs that span t.
+template <typename T, int NB>
+__global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
+    extern __shared__ __align__(16) char raw[];
+    using Sm = Smem32<NB>;
+    Sm& s = *reinterpret_cast<Sm*>(raw);
+    constexpr int C = kChunk32, NP = Sm::NP;
+    const Args& a = w.a;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
+    int64_t id = blockIdx.x;
+    const int64_t split = id % w.splits;
+    id /= w.splits;
+    const int64_t gq = id % a.G;
+    id /= a.G;
+    const int64_t chunk = id % w.chunks, b = id / w.chunks;
+    const int64_t t0 = chunk * C;
+    const int64_t len = row_length(a, b);
+    const int nt = (int)min((int64_t)C, a.L - t0);
+    const int nv = (int)max((int64_t)0, min((int64_t)nt, len - t0));
+    const int64_t rep = a.H / a.G;
+    const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
+
+    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + t0 * a.q.token + gq * a.N;
+    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + t0 * a.k.token + gq * a.N;
+    for (int e = tid; e < C * NP; e += 256) {
+        const int t = e / NP, n = e % NP;
+        const bool on = t < nv && n < a.N;
+        s.q[t][n] = on ? ldf(qp + t * a.q.token + n) : 0.0f;
+        s.k[t][n] = on ? ldf(kp + t * a.k.token + n) : 0.0f;
+    }
+    float dq[4][NB], dk[4][NB];
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+        for (int n = 0; n < NB; n++) dq[r][n] = dk[r][n] = 0.0f;
+
+    for (int64_t h = h_lo; h < h_hi; h++) {
+        __syncthreads();
+        if (warp == 0) {
+            float x[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int t = lane * 2 + e;
+                x[e] = t < nv ? log_decay(a, b, t0 + t, h) * kLog2e : 0.0f;
+            }
+            Two c[2];
+            warp_cumsum<2>(x, c);
+            s.c[lane * 2] = c[0];
+            s.c[lane * 2 + 1] = c[1];
+        } else if (tid >= 64 && tid < 64 + C) {
+            s.a[tid - 64] = s.b[tid - 64] = 0.0f;
+        }
+        float through = 0.0f;
+        for (int64_t p0 = 0; p0 < a.P; p0 += kPT) {
+            __syncthreads();
+            const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + t0 * a.v.token + h * a.P + p0;
+            const T* yp = static_cast<const T*>(a.dy.p) + b * a.dy.batch + t0 * a.dy.token + h * a.P + p0;
+            for (int e = tid; e < C * kPT; e += 256) {
+                const int t = e / kPT, p = e % kPT;
+                const bool on = t < nv && p0 + p < a.P;
+                s.v[t][p] = on ? ldf(vp + t * a.v.token + p) : 0.0f;
+                s.dy[t][p] = on ? ldf(yp + t * a.dy.token + p) : 0.0f;
+            }
+            const int64_t at = ((b * a.H + h) * w.chunks + chunk) * a.N * a.P + p0;
+            for (int e = tid; e < NP * kPT; e += 256) {
+                const int n = e / kPT, p = e % kPT;
+                const bool on = n < a.N && p0 + p < a.P;
+                const float hv = on ? w.before[at + n * a.P + p] : 0.0f, rv = on ? w.after[at + n * a.P + p] : 0.0f;
+                s.H[n][p] = hv;
+                s.R[n][p] = rv;
+                through = fmaf(hv, rv, through);
+            }
+            __syncthreads();
+            {  // scores
+                float qk[4][4] = {}, yv[4][4] = {};
+                for (int n = 0; n < NP; n += 4) {
+                    float4 x[4], z[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = *reinterpret_cast<const float4*>(&s.q[ty + 16 * r][n]);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) z[r] = *reinterpret_cast<const float4*>(&s.k[tx + 16 * r][n]);
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++)
+                            qk[r][c] += x[r].x * z[c].x + x[r].y * z[c].y + x[r].z * z[c].z + x[r].w * z[c].w;
+                }
+                for (int p = 0; p < kPT; p += 4) {
+                    float4 x[4], z[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = *reinterpret_cast<const float4*>(&s.dy[ty + 16 * r][p]);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) z[r] = *reinterpret_cast<const float4*>(&s.v[tx + 16 * r][p]);
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++)
+                            yv[r][c] += x[r].x * z[c].x + x[r].y * z[c].y + x[r].z * z[c].z + x[r].w * z[c].w;
+                }
+                float col[4] = {};
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int i = ty + 16 * r;
+                    float row = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        const int j = tx + 16 * c;
+                        const float m = j <= i ? a.scale * ex2(two_diff(s.c[i], s.c[j])) : 0.0f;
+                        const float e = yv[r][c] * m;
+                        s.E[i][j] = e;
+                        s.S[i][j] = qk[r][c] * m;
+                        const float wv = j < i ? e * qk[r][c] : 0.0f;
+                        row += wv;
+                        col[c] += wv;
+                    }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) row += __shfl_xor_sync(kFull, row, o);
+                    if (tx == 0) s.b[i] -= row;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    col[c] += __shfl_xor_sync(kFull, col[c], 16);
+                    if (lane < 16) s.col[warp][tx + 16 * c] = col[c];
+                }
+            }
+            __syncthreads();
+            if (tid < C) {
+                float x = 0.0f;
+#pragma unroll
+                for (int u = 0; u < 8; u++) x += s.col[u][tid];
+                s.b[tid] += x;
+            }
+            __syncthreads();
+            const Two cl = s.c[C - 1];
+            {  // dv, and b from its inter-chunk part
+                float in[4][4] = {}, ac[4][4] = {};
+                for (int i = 0; i < C; i++) {
+                    float x[4], z[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = s.S[i][ty + 16 * r], z[r] = s.dy[i][tx + 16 * r];
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++) ac[r][c] = fmaf(x[r], z[c], ac[r][c]);
+                }
+                for (int n = 0; n < NP; n++) {
+                    float x[4], z[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = s.k[ty + 16 * r][n], z[r] = s.R[n][tx + 16 * r];
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++) in[r][c] = fmaf(x[r], z[c], in[r][c]);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int j = ty + 16 * r;
+                    const float d = ex2(two_diff(cl, s.c[j]));
+                    float bj = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        const int p = tx + 16 * c;
+                        const float x = d * in[r][c];
+                        bj = fmaf(s.v[j][p], x, bj);
+                        if (j < nt && p0 + p < a.P)
+                            st(static_cast<T*>(w.dv) + ((b * a.L + t0 + j) * a.H + h) * a.P + p0 + p,
+                               j < nv ? ac[r][c] + x : 0.0f);
+                    }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) bj += __shfl_xor_sync(kFull, bj, o);
+                    if (tx == 0) s.b[j] += bj;
+                }
+            }
+            {  // dq, and a from its inter-chunk part
+                for (int j = 0; j < C; j++) {
+                    float x[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = s.E[ty + 16 * r][j];
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        const float z = s.k[j][tx + 16 * n];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) dq[r][n] = fmaf(x[r], z, dq[r][n]);
+                    }
+                }
+                float in[4][NB] = {};
+                for (int p = 0; p < kPT; p++) {
+                    float x[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = s.dy[ty + 16 * r][p];
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        const float z = s.H[tx + 16 * n][p];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) in[r][n] = fmaf(x[r], z, in[r][n]);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int i = ty + 16 * r;
+                    const float d = a.scale * ex2(s.c[i].h + s.c[i].l);
+                    float ai = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        const float x = d * in[r][n];
+                        ai = fmaf(s.q[i][tx + 16 * n], x, ai);
+                        dq[r][n] += x;
+                    }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) ai += __shfl_xor_sync(kFull, ai, o);
+                    if (tx == 0) s.a[i] += ai;
+                }
+            }
+            {  // dk
+                for (int i = 0; i < C; i++) {
+                    float x[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = s.E[i][ty + 16 * r];
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        const float z = s.q[i][tx + 16 * n];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) dk[r][n] = fmaf(x[r], z, dk[r][n]);
+                    }
+                }
+                float in[4][NB] = {};
+                for (int p = 0; p < kPT; p++) {
+                    float x[4];
+#pragma unroll
+                    for (int r = 0; r < 4; r++) x[r] = s.v[ty + 16 * r][p];
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        const float z = s.R[tx + 16 * n][p];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) in[r][n] = fmaf(x[r], z, in[r][n]);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const float d = ex2(two_diff(cl, s.c[ty + 16 * r]));
+#pragma unroll
+                    for (int n = 0; n < NB; n++) dk[r][n] = fmaf(d, in[r][n], dk[r][n]);
+                }
+            }
+        }
+        // dg of this head
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(kFull, through, o);
+        if (lane == 0) s.red[warp] = through;
+        __syncthreads();
+        if (warp == 0) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; u++) sum += s.red[u];
+            const Two cl = s.c[C - 1];
+            sum *= ex2(cl.h + cl.l);
+            const float a0 = s.a[2 * lane], a1 = s.a[2 * lane + 1], b0 = s.b[2 * lane], b1 = s.b[2 * lane + 1];
+            float A = a0 + a1, B = b0 + b1;  // suffix of a, prefix of b over lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_down_sync(kFull, A, o), y = __shfl_up_sync(kFull, B, o);
+                if (lane + o < 32) A += x;
+                if (lane >= o) B += y;
+            }
+            const float Bx = __shfl_up_sync(kFull, B, 1), Ax = __shfl_down_sync(kFull, A, 1);
+            const float pre = lane > 0 ? Bx : 0.0f, suf = lane < 31 ? Ax : 0.0f;
+            const float g0 = (a0 + a1 + suf) + pre + sum, g1 = (a1 + suf) + (pre + b0) + sum;
+            const int t = 2 * lane;
+            if (t < nt) w.dg[(b * a.L + t0 + t) * a.H + h] = t < nv ? g0 : 0.0f;
+            if (t + 1 < nt) w.dg[(b * a.L + t0 + t + 1) * a.H + h] = t + 1 < nv ? g1 : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        const int t = ty + 16 * r;
+        if (t >= nt) continue;
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const int c = tx + 16 * n;
+            if (c >= a.N) continue;
+            const int64_t at = ((b * a.L + t0 + t) * a.G + gq) * a.N + c;
+            const float x = t < nv ? dq[r][n] : 0.0f, z = t < nv ? dk[r][n] : 0.0f;
+            if (w.splits > 1) {
+                const int64_t part = split * a.Bsz * a.L * a.G * a.N + at;
+                w.dq_part[part] = x;
+                w.dk_part[part] = z;
+            } else {
+                st(static_cast<T*>(w.dq) + at, x);
+                st(static_cast<T*>(w.dk) + at, z);
+            }
+        }
+    }
+}
+
+template <typename T> __global__ void __launch_bounds__(256) k_sum_parts(const float* part, T* out, int splits, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.0f;
+    for (int k = 0; k < splits; k++) s += part[k * n + i];
+    st(out + i, s);
+}
+
+// part[slice, h] = sum of the slice's rows (32 heads x 8 rows at a time)
+__global__ void __launch_bounds__(256) k_sum_rows(const float* x, float* part, int64_t rows, int64_t H) {
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t h = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t per = (rows + gridDim.y - 1) / gridDim.y;
+    const int64_t lo = blockIdx.y * per, hi = min(rows, lo + per);
+    float v = 0.0f;
+    if (h < H)
+        for (int64_t r = lo + warp; r < hi; r += 8) v += x[r * H + h];
+    s[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && h < H) {
+        float t = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; u++) t += s[u][lane];
+        part[blockIdx.y * H + h] = t;
+    }
+}
+
+template <typename T, int NR, bool REV> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+    const Args& a = w.a;
+    const int64_t segs = mode == kWalkSum ? w.plan.K - 1 : w.plan.K;
+    const unsigned grid = (unsigned)(ceil_div(a.P, kWalkP) * a.H * a.Bsz * segs);
+    if (mode == kWalkSum) k_walk32<T, NR, REV, kWalkSum><<<grid, 256, 0, st>>>(w);
+    else if (mode == kWalkStates) k_walk32<T, NR, REV, kWalkStates><<<grid, 256, 0, st>>>(w);
+    else if constexpr (!REV) k_walk32<T, NR, REV, kWalkY><<<grid, 256, 0, st>>>(w);
+    return cudaGetLastError();
+}
+
+template <typename T, bool REV> cudaError_t walk_n(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+    if (w.a.N <= 32) return walk_mode<T, 4, REV>(w, mode, st);
+    if (w.a.N <= 64) return walk_mode<T, 8, REV>(w, mode, st);
+    return walk_mode<T, 16, REV>(w, mode, st);
+}
+
+template <typename T> cudaError_t walk_io(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st) {
+    return reverse ? walk_n<T, true>(w, mode, st) : walk_n<T, false>(w, mode, st);
+}
+
+template <typename T, int NB> cudaError_t bwd_n(const BwdArgs& b, cudaStream_t st) {
+    const int bytes = (int)sizeof(Smem32<NB>);
+    const cudaError_t e = cudaFuncSetAttribute(k_bwd32<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k_bwd32<T, NB><<<(unsigned)(b.a.Bsz * b.chunks * b.a.G * b.splits), 256, bytes, st>>>(b);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t bwd_io(const BwdArgs& b, cudaStream_t st) {
+    if (b.a.N <= 32) return bwd_n<T, 2>(b, st);
+    if (b.a.N <= 64) return bwd_n<T, 4>(b, st);
+    return bwd_n<T, 8>(b, st);
+}
+
+}  // namespace
+
+cudaError_t launch_walk32(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st) {
+    if (w.a.dtype == 0) return walk_io<float>(w, reverse, mode, st);
+    if (w.a.dtype == 1) return walk_io<__half>(w, reverse, mode, st);
+    return walk_io<__nv_bfloat16>(w, reverse, mode, st);
+}
+
+cudaError_t launch_carry(const CarryArgs& c, cudaStream_t st) {
+    k_carry<<<(unsigned)ceil_div(c.BH * c.NP, 256), 256, 0, st>>>(c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_bwd32(const BwdArgs& b, cudaStream_t st) {
+    if (b.a.dtype == 0) return bwd_io<float>(b, st);
+    if (b.a.dtype == 1) return bwd_io<__half>(b, st);
+    return bwd_io<__nv_bfloat16>(b, st);
+}
+
+cudaError_t launch_sum_parts(const float* part, void* out, int splits, int64_t n, int dtype, cudaStream_t st) {
+    const unsigned grid = (unsigned)ceil_div(n, 256);
+    if (dtype == 0) k_sum_parts<float><<<grid, 256, 0, st>>>(part, static_cast<float*>(out), splits, n);
+    else if (dtype == 1) k_sum_parts<__half><<<grid, 256, 0, st>>>(part, static_cast<__half*>(out), splits, n);
+    else k_sum_parts<__nv_bfloat16><<<grid, 256, 0, st>>>(part, static_cast<__nv_bfloat16*>(out), splits, n);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_sum_rows(const float* dg, float* part, float* out, int64_t rows, int64_t H, cudaStream_t st) {
+    const unsigned gx = (unsigned)ceil_div(H, 32);
+    k_sum_rows<<<dim3(gx, kDgParts), 256, 0, st>>>(dg, part, rows, H);
+    k_sum_rows<<<dim3(gx, 1), 256, 0, st>>>(part, out, kDgParts, H);
+    return cudaGetLastError();
+}
+
+}  // namespace la
+}  // namespace ss
