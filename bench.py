@@ -96,7 +96,7 @@ TRAFFIC = {
     ("k_bwd_main", "mamba2.8b-layer-bf16"): 2948585216,  # 1596.0 + 85.5 MB read, 1238.2 + 28.9 MB written
     ("k_fwd_y", "mamba2.8b-layer-bf16"): 1573153792,     # 480.0 + 26.8 MB read, 1059.3 + 7.0 MB written
 }
-TRAFFIC_SRC_DIGEST = "2f86bc4c97822ea2"
+TRAFFIC_SRC_DIGEST = "e3773bb4658a0346"
 
 # timed end-to-end runs (their median is reported)
 E2E_RUNS = 5

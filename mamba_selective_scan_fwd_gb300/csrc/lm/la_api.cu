@@ -1,7 +1,10 @@
 // C ABI of the linear attention and the gated group norm (include/ss_la.h).
 // Everything is checked before the first CUDA call; on error nothing is
 // written.
+#include <cuda.h>
+
 #include "la.h"
+#include "la_tc.h"
 #include "ss_la.h"
 
 using namespace ss;
@@ -81,6 +84,88 @@ Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     return b;
 }
 
+// ---------------------------------------------------------------- tensor-core path
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// [Bsz, L, heads, width] as a map {width, heads, L, Bsz}, boxes of 64 columns
+// by 128 tokens in the 128-byte swizzle; what lies outside reads as zero.
+bool tc_map(EncodeTiledFn encode, CUtensorMap* m, const In& x, int64_t heads, int64_t width, int64_t L, int64_t Bsz, int dtype) {
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)Bsz};
+    // the stride of a dimension of one is never used, but has to be valid
+    const int64_t token = L > 1 ? x.token : heads * width, batch = Bsz > 1 ? x.batch : heads * width;
+    const cuuint64_t strides[3] = {(cuuint64_t)(width * 2), (cuuint64_t)(token * 2), (cuuint64_t)(batch * 2)};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)kChunkTc, 1}, step[4] = {1, 1, 1, 1};
+    return encode(m, dtype == SS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(x.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether these sizes may run on the tensor cores (their inputs too, if tc_input says so).
+bool tc_sizes(int64_t L, int64_t N, int64_t P, int dtype) { return dtype != SS_F32 && N % 8 == 0 && P % 8 == 0 && L < (1ll << 31); }
+
+// TMA's rules on an input: 16-byte units everywhere.
+bool tc_input(const In& x, int64_t L, int64_t Bsz) {
+    if (misaligned16(x.p)) return false;
+    if (L > 1 && (x.token % 8 != 0 || x.token < 8 || x.token >= (1ll << 38))) return false;
+    return Bsz <= 1 || (x.batch % 8 == 0 && x.batch >= 8 && x.batch < (1ll << 38));
+}
+
+struct WalkTc {
+    WalkPlan plan;
+    size_t state, decay;
+};
+WalkTc walktc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P) {
+    WalkTc w;
+    w.plan = tc_walk_plan(Bsz * H * ceil_div(P, kTileP), L);
+    w.state = w.decay = 0;
+    if (w.plan.K > 1) {
+        w.state = l.take((size_t)Bsz * H * w.plan.K * N * P * 4);
+        w.decay = l.take((size_t)Bsz * H * w.plan.K * 4);
+    }
+    return w;
+}
+
+// The sum pass of a walk cut in time, and the states its segments start from.
+cudaError_t tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st) {
+    if (w.plan.K == 1) return cudaSuccess;
+    const cudaError_t e = launch_tc_state(w, reverse, true, st);
+    if (e != cudaSuccess) return e;
+    return launch_carry({w.seg_state, w.seg_decay, w.init, w.a.Bsz * w.a.H, w.plan.K, w.a.N * w.a.P, reverse ? 1 : 0}, st);
+}
+
+// Forward on the tensor cores; *ran tells whether the inputs allow it.
+int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, bool* ran) {
+    *ran = false;
+    if (!tc_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) ||
+        !tc_input(a.v, a.L, a.Bsz))
+        return SS_OK;
+    const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!encode) return SS_OK;
+    TcWalkArgs w = {};
+    const In yo = {y, a.H * a.P, a.L * a.H * a.P};
+    if (!tc_map(encode, &w.maps.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &w.maps.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &w.maps.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &w.maps.y, yo, a.H, a.P, a.L, a.Bsz, a.dtype))
+        return SS_OK;
+    const int rc = device_status_word(&w.status);
+    if (rc != SS_OK) return rc;
+    Layout l;
+    const WalkTc wl = walktc_layout(l, a.Bsz, a.L, a.H, a.N, a.P);
+    w.a = a;
+    w.plan = wl.plan;
+    w.init = a.h0;
+    w.seg_state = reinterpret_cast<float*>(ws + wl.state);
+    w.seg_decay = reinterpret_cast<float*>(ws + wl.decay);
+    w.last = last;
+    *ran = true;
+    if (tc_carry(w, false, st) != cudaSuccess) return SS_ERR_CUDA;
+    return launch_tc_fwd(w, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
 bool empty(int64_t Bsz, int64_t L) { return Bsz == 0 || L == 0; }
 
 // The state that no token changes: a copy of the incoming one, or zeros.
@@ -111,9 +196,10 @@ extern "C" {
 
 size_t ss_la_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
-    Layout l;
+    Layout l, t;
     walk32_layout(l, Bsz, L, H, N, P);
-    return l.total;
+    if (tc_sizes(L, N, P, dtype)) walktc_layout(t, Bsz, L, H, N, P);
+    return l.total > t.total ? l.total : t.total;  // either path may run: strides and pointers decide
 }
 
 int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
@@ -141,6 +227,9 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
     a.dtype = d->dtype;
     a.g_per_head = d->g_per_head ? 1 : 0;
     char* ws = static_cast<char*>(d->workspace);
+    bool ran;
+    const int tc = tc_forward(a, d->y, d->last_state, ws, st, &ran);
+    if (ran || tc != SS_OK) return tc;
     Layout l;
     const Walk32 wl = walk32_layout(l, a.Bsz, a.L, a.H, a.N, a.P);
     WalkArgs w = {};

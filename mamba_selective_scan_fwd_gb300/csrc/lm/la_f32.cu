@@ -5,6 +5,8 @@
 // The walk (forward, and the states the backward needs) is the recurrence
 // itself, token by token with the state in registers: 3 N P operations per
 // token and head, fewer than any chunked form takes without matrix units.  The
+// decay enters as S + (e^g - 1) S: a rounded e^g near 1 would be off by the same
+// 2^-25 at every token and add up over a long memory.  The
 // backward works on chunks of 64 tokens from the states at their borders.
 #include "la_dev.cuh"
 
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
         if (tid < TT) {
             const float g = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
             s_g[tid] = g;
-            s_a[tid] = expf(g);
+            s_a[tid] = expm1f(g);
         }
         __syncthreads();
         if (MODE == kWalkSum && tid == 0)
@@ -102,15 +104,17 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
             for (int r = 0; r < NR; r += 4) {
                 const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + r]);
                 if (REV) {
-                    S[r] = av * fmaf(kk.x, v, S[r]);
-                    S[r + 1] = av * fmaf(kk.y, v, S[r + 1]);
-                    S[r + 2] = av * fmaf(kk.z, v, S[r + 2]);
-                    S[r + 3] = av * fmaf(kk.w, v, S[r + 3]);
+                    const float x0 = fmaf(kk.x, v, S[r]), x1 = fmaf(kk.y, v, S[r + 1]);
+                    const float x2 = fmaf(kk.z, v, S[r + 2]), x3 = fmaf(kk.w, v, S[r + 3]);
+                    S[r] = fmaf(av, x0, x0);
+                    S[r + 1] = fmaf(av, x1, x1);
+                    S[r + 2] = fmaf(av, x2, x2);
+                    S[r + 3] = fmaf(av, x3, x3);
                 } else {
-                    S[r] = fmaf(av, S[r], kk.x * v);
-                    S[r + 1] = fmaf(av, S[r + 1], kk.y * v);
-                    S[r + 2] = fmaf(av, S[r + 2], kk.z * v);
-                    S[r + 3] = fmaf(av, S[r + 3], kk.w * v);
+                    S[r] = fmaf(kk.x, v, fmaf(av, S[r], S[r]));
+                    S[r + 1] = fmaf(kk.y, v, fmaf(av, S[r + 1], S[r + 1]));
+                    S[r + 2] = fmaf(kk.z, v, fmaf(av, S[r + 2], S[r + 2]));
+                    S[r + 3] = fmaf(kk.w, v, fmaf(av, S[r + 3], S[r + 3]));
                 }
                 if (MODE == kWalkY) {
                     const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + r]);
