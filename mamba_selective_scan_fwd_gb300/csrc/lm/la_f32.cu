@@ -151,19 +151,30 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
 }
 
 // seg_state: end state of each segment walked from zero -> the state each
-// segment starts from.
+// segment starts from.  One thread per state element; eight segments' states are
+// on their way before the first is folded in (one memory wait per eight).
 __global__ void __launch_bounds__(256) k_carry(CarryArgs c) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= c.BH * c.NP) return;
-    const int64_t bh = e / c.NP, x = e % c.NP;
+    constexpr int U = 8;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y;
+    if (x >= c.NP) return;
     float S = c.init ? c.init[bh * c.NP + x] : 0.0f;
-    for (int64_t i = 0; i < c.K; i++) {
-        const int64_t s = c.reverse ? c.K - 1 - i : i;
-        float* at = c.seg_state + (bh * c.K + s) * c.NP + x;
-        const bool more = i + 1 < c.K;
-        const float own = more ? *at : 0.0f;
-        *at = S;
-        if (more) S = fmaf(expf(c.seg_decay[bh * c.K + s]), S, own);
+    for (int64_t i0 = 0; i0 < c.K; i0 += U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + u, s = bh * c.K + (c.reverse ? c.K - 1 - i : i);
+            own[u] = d[u] = 0.0f;
+            if (i + 1 < c.K) {  // the segment walked last has no sum
+                own[u] = c.seg_state[s * c.NP + x];
+                d[u] = expf(c.seg_decay[s]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + u, s = bh * c.K + (c.reverse ? c.K - 1 - i : i);
+            if (i < c.K) c.seg_state[s * c.NP + x] = S;
+            S = fmaf(d[u], S, own[u]);
+        }
     }
 }
 
@@ -553,7 +564,15 @@ cudaError_t launch_walk32(const WalkArgs& w, bool reverse, WalkMode mode, cudaSt
 }
 
 cudaError_t launch_carry(const CarryArgs& c, cudaStream_t st) {
-    k_carry<<<(unsigned)ceil_div(c.BH * c.NP, 256), 256, 0, st>>>(c);
+    // grid.y: at most 2^16 - 1 (batch row, head) pairs a launch
+    for (int64_t at = 0; at < c.BH; at += 65535) {
+        CarryArgs part = c;
+        part.BH = c.BH - at < 65535 ? c.BH - at : 65535;
+        part.seg_state += at * c.K * c.NP;
+        part.seg_decay += at * c.K;
+        if (part.init) part.init += at * c.NP;
+        k_carry<<<dim3((unsigned)ceil_div(c.NP, 256), (unsigned)part.BH), 256, 0, st>>>(part);
+    }
     return cudaGetLastError();
 }
 

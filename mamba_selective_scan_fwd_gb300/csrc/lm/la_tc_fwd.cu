@@ -33,15 +33,18 @@ struct Decays {
     Two total[4];   // log2 decay of each run
 };
 
-// All warps, x: log2 decay of token tid.  Returns rel (at most 0 for decays).
+// Both halves of the block (256 threads, token = tid % 128), x: the token's log2
+// decay.  Returns rel (at most 0 for decays).
 __device__ __forceinline__ float chunk_decays(Decays& d, float x) {
     const float in[1] = {x};
     Two c[1];
     warp_cumsum<1>(in, c);
     const Two end = {__shfl_sync(kFull, c[0].h, 31), __shfl_sync(kFull, c[0].l, 31)};
     const float rel = two_diff(end, c[0]);
-    d.tail[threadIdx.x] = ex2(rel);
-    if ((threadIdx.x & 31) == 31) d.total[threadIdx.x >> 5] = end;
+    if (threadIdx.x < C) {
+        d.tail[threadIdx.x] = ex2(rel);
+        if ((threadIdx.x & 31) == 31) d.total[threadIdx.x >> 5] = end;
+    }
     return rel;
 }
 // After a barrier: log2 decays from the chunk's start to the end of each run.
@@ -51,7 +54,8 @@ __device__ __forceinline__ void run_ends(const Decays& d, Two (&end)[4]) {
     for (int i = 1; i < 4; i++) end[i] = two_add(end[i - 1], d.total[i]);
 }
 __device__ __forceinline__ float load_g(const Args& a, int64_t b, int64_t h, int64_t t0, int nv) {
-    return (int)threadIdx.x < nv ? log_decay(a, b, t0 + threadIdx.x, h) * kLog2e : 0.0f;
+    const int t = threadIdx.x & (C - 1);
+    return t < nv ? log_decay(a, b, t0 + t, h) * kLog2e : 0.0f;
 }
 
 // Largest value of the block's threads (all get it); v >= 0.  Two block barriers.
@@ -60,15 +64,15 @@ __device__ __forceinline__ float block_max(float v, uint32_t* red) {
     asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = max(max(red[0], red[1]), max(red[2], red[3]));
+    m = max(max(max(red[0], red[1]), max(red[2], red[3])), max(max(red[4], red[5]), max(red[6], red[7])));
     __syncthreads();
     return __uint_as_float(m);
 }
 
-// Row `row` of a value tile, times w, as 16-bit parts (same layout).
-template <typename T> __device__ __forceinline__ void split_row(void* v, int row, float w, void* p0, void* p1, void* p2) {
+// Half of row `row` of a value tile, times w, as 16-bit parts (same layout).
+template <typename T> __device__ __forceinline__ void split_row(void* v, int row, int half, float w, void* p0, void* p1, void* p2) {
 #pragma unroll 2
-    for (int u = 0; u < 8; u++) {
+    for (int u = 4 * half; u < 4 * half + 4; u++) {
         const uint4 in = *unit(v, row, u);
         const uint32_t x[4] = {in.x, in.y, in.z, in.w};
         uint32_t r[3][4];
@@ -91,10 +95,10 @@ template <typename T> __device__ __forceinline__ void split_row(void* v, int row
     }
 }
 
-template <typename T> __device__ __forceinline__ float row_max(void* v, int row) {
+template <typename T> __device__ __forceinline__ float row_max(void* v, int row, int half) {
     float m = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 8; u++) {
+    for (int u = 4 * half; u < 4 * half + 4; u++) {
         const uint4 in = *unit(v, row, u);
         const uint32_t x[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
@@ -106,18 +110,18 @@ template <typename T> __device__ __forceinline__ float row_max(void* v, int row)
     return m;
 }
 
-// The state a thread holds: NB == 2, row tid, 64 columns; NB == 1, row
-// tid % 64, columns of half tid / 64.
+// The state a thread of 256 holds: NB == 2, row tid % 128, 32 of the 64 columns;
+// NB == 1, row tid % 64, 16 columns (the product's 128 rows hold the 64 twice).
 template <int NB> struct StateOf {
-    static constexpr int W = 32 * NB;
-    __device__ static int row() { return NB == 2 ? (int)threadIdx.x : (int)(threadIdx.x & 63); }
-    __device__ static int col() { return NB == 2 ? 0 : (int)(threadIdx.x >> 6) * 32; }
+    static constexpr int W = 16 * NB;
+    __device__ static int row() { return threadIdx.x & (64 * NB - 1); }
+    __device__ static int col() { return (int)(threadIdx.x / (64 * NB)) * W; }
 };
 
-template <int NB> __device__ __forceinline__ void load_state(const float* p, const Args& a, int64_t p0, float (&X)[32 * NB]) {
+template <int NB> __device__ __forceinline__ void load_state(const float* p, const Args& a, int64_t p0, float (&X)[16 * NB]) {
     const int n = StateOf<NB>::row(), c0 = StateOf<NB>::col();
 #pragma unroll
-    for (int c = 0; c < 32 * NB; c += 4) {
+    for (int c = 0; c < 16 * NB; c += 4) {
         float4 f = {0.0f, 0.0f, 0.0f, 0.0f};
         if (p && n < a.N && p0 + c0 + c < a.P) f = *reinterpret_cast<const float4*>(p + n * a.P + p0 + c0 + c);
         X[c] = f.x;
@@ -126,34 +130,33 @@ template <int NB> __device__ __forceinline__ void load_state(const float* p, con
         X[c + 3] = f.w;
     }
 }
-template <int NB> __device__ __forceinline__ void save_state(float* p, const Args& a, int64_t p0, const float (&X)[32 * NB]) {
+template <int NB> __device__ __forceinline__ void save_state(float* p, const Args& a, int64_t p0, const float (&X)[16 * NB]) {
     const int n = StateOf<NB>::row(), c0 = StateOf<NB>::col();
 #pragma unroll
-    for (int c = 0; c < 32 * NB; c += 4)
+    for (int c = 0; c < 16 * NB; c += 4)
         if (n < a.N && p0 + c0 + c < a.P)
             *reinterpret_cast<float4*>(p + n * a.P + p0 + c0 + c) = make_float4(X[c], X[c + 1], X[c + 2], X[c + 3]);
 }
-template <int NB> __device__ __forceinline__ float state_max(const float (&X)[32 * NB]) {
+template <int NB> __device__ __forceinline__ float state_max(const float (&X)[16 * NB]) {
     float m = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 32 * NB; c++) m = fmaxf(m, fabsf(X[c]));
+    for (int c = 0; c < 16 * NB; c++) m = fmaxf(m, fabsf(X[c]));
     return m;
 }
+__device__ __forceinline__ void tmem_ldw(uint32_t addr, float (&x)[16]) { tmem_ld16(addr, x); }
+__device__ __forceinline__ void tmem_ldw(uint32_t addr, float (&x)[32]) { tmem_ld32(addr, x); }
 // X <- d X + u * (the product in tensor memory)
-template <int NB> __device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float (&X)[32 * NB]) {
+template <int NB> __device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float (&X)[16 * NB]) {
+    float f[16 * NB];
+    tmem_ldw(tm + ((threadIdx.x & 96) << 16) + StateOf<NB>::col(), f);
 #pragma unroll
-    for (int c = 0; c < NB; c++) {
-        float f[32];
-        tmem_ld32(tm + ((threadIdx.x & 96) << 16) + StateOf<NB>::col() + 32 * c, f);
-#pragma unroll
-        for (int i = 0; i < 32; i++) X[32 * c + i] = fmaf(d, X[32 * c + i], u * f[i]);
-    }
+    for (int i = 0; i < 16 * NB; i++) X[i] = fmaf(d, X[i], u * f[i]);
 }
 // 16-bit rows [n][p] of X * s (and of what the rounding left): operand tiles
-template <typename T, int NB> __device__ __forceinline__ void put_state(void* hi, void* lo, float s, const float (&X)[32 * NB]) {
+template <typename T, int NB> __device__ __forceinline__ void put_state(void* hi, void* lo, float s, const float (&X)[16 * NB]) {
     const int n = StateOf<NB>::row(), u0 = StateOf<NB>::col() / 8;
 #pragma unroll
-    for (int u = 0; u < 4 * NB; u++) {
+    for (int u = 0; u < 2 * NB; u++) {
         uint32_t r[4], q[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -178,12 +181,12 @@ template <typename T, int NB> __device__ __forceinline__ void mma_state(uint32_t
             mma(tm, smem_desc(ka + s * 2048, NB == 2 ? 16384 : 0), smem_desc(smem_addr(w[p]) + s * 2048), desc, p + s > 0);
 }
 
-// Rows from nv on that a copy filled with tokens beyond the row's length: zero.
-template <int TILES> __device__ __forceinline__ void clear_row(char* const (&tiles)[TILES]) {
+// Half a row of each tile that a copy filled with a token beyond the row's length: zero.
+template <int TILES> __device__ __forceinline__ void clear_row(char* const (&tiles)[TILES], int row, int half) {
 #pragma unroll
     for (int i = 0; i < TILES; i++)
 #pragma unroll
-        for (int u = 0; u < 8; u++) *unit(tiles[i], threadIdx.x, u) = make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 4; u++) *unit(tiles[i], row, 4 * half + u) = make_uint4(0, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------- forward
@@ -192,14 +195,15 @@ template <int NB> struct FwdSmem {
                          x = y + 16384, total = x + (NB == 1 ? 16384 : 0);  // x: a part of w v that finds no room in q
 };
 
-template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd(const __grid_constant__ TcWalkArgs w) {
+template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = FwdSmem<NB>;
     __shared__ Decays s_d;
     __shared__ __align__(8) uint64_t s_ld, s_m1, s_m2;
-    __shared__ uint32_t s_tm, s_red[4];
+    __shared__ uint32_t s_tm, s_red[8];
     const Args& a = w.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // thread: token (and accumulator row) tok, half `half` of its columns
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, half = tid >> 7;
     int64_t id = blockIdx.x;
     const int64_t ptiles = (a.P + PT - 1) / PT;
     const int64_t p0 = (id % ptiles) * PT;
@@ -224,8 +228,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tm;
-    const uint32_t tS = tm, tP = tm, tOi = tm + 64, tOe = tm + 128, tU = tm + 192;
-    const uint32_t my = (uint32_t)(warp * 32) << 16;
+    // S, then (all of it read) P v and k^T (w v) in its place
+    const uint32_t tS = tm, tOi = tm, tU = tm + 64, tP = tm + 128, tOe = tm + 192;
+    const uint32_t my = (uint32_t)(run * 32) << 16;
 
     auto load = [&](int64_t t0) {
         mbar_expect_tx(&s_ld, (2 * NB + 1) * 16384);
@@ -238,7 +243,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd
     };
     if (tid == 0) load(t_begin);
 
-    float X[32 * NB];
+    float X[16 * NB];
     {
         const float* from = nullptr;
         if (w.plan.K > 1) from = w.seg_state + ((b * a.H + h) * w.plan.K + seg) * a.N * a.P;
@@ -258,13 +263,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd
         const float rel = chunk_decays(s_d, g);
         if (ch + 1 < chunks) g = load_g(a, b, h, t0 + C, valid(t0 + C));
         ok = mbar_wait(&s_ld, ch & 1);
-        if (ok && tid >= nv && t0 + tid < a.L) {
+        if (ok && tok >= nv && t0 + tok < a.L) {
             if (NB == 2) {
                 char* const t[5] = {Q, K, V, Q + 16384, K + 16384};
-                clear_row<5>(t);
+                clear_row<5>(t, tok, half);
             } else {
                 char* const t[3] = {Q, K, V};
-                clear_row<3>(t);
+                clear_row<3>(t, tok, half);
             }
         }
         fence_proxy_async_smem();
@@ -286,58 +291,61 @@ template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd
             mma_commit(&s_m1);
         }
         float vs = 1.0f;
-        if (kF16<T>) vs = f16_scale(block_max(row_max<T>(V, tid), s_red));
+        if (kF16<T>) vs = f16_scale(block_max(row_max<T>(V, tok, half), s_red));
         Two end[4];
         run_ends(s_d, end);
-        const Two mine = warp == 0 ? end[0] : (warp == 1 ? end[1] : (warp == 2 ? end[2] : end[3]));
+        const Two mine = run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3]));
         const float ci = (mine.h - rel) + mine.l, cl = end[3].h + end[3].l;
         const float wt = ex2(two_diff(end[3], mine) + rel);
         ok = mbar_wait(&s_m1, ch & 1);
         tc_fence_after();
-        // P, 32 columns at a time: off the diagonal e^{c_i - c_j} = e^{c_i - c_e} e^{c_e - c_j} with e the end
-        // of the 32 columns (both factors are at most 1 for decays), on it one exponential each
+        // P, by runs of 32 columns, 16 to each half of the block: left of the diagonal e^{c_i - c_j} =
+        // e^{c_i - c_e} e^{c_e - c_j} with e the end of the run (both factors are at most 1 for decays), on
+        // it one exponential each
         float ps = 1.0f;
         if (kF16<T>) {
             float m = 0.0f;
-            for (int cb = 0; cb <= warp; cb++) {
+            for (int cb = 0; cb <= run; cb++) {
                 float s[32];
                 tmem_ld32(tS + my + 32 * cb, s);
 #pragma unroll
                 for (int j = 0; j < 32; j++)
-                    if (32 * cb + j <= tid) m = fmaxf(m, fabsf(s[j]));
+                    if (32 * cb + j <= tok) m = fmaxf(m, fabsf(s[j]));
             }
             ps = f16_scale(m);
         }
         for (int cb = 0; cb < 4; cb++) {
-            uint32_t r[16];
-            if (cb <= warp) {
-                float s[32];
-                tmem_ld32(tS + my + 32 * cb, s);
-                if (cb < warp) {
+            uint32_t r[8];
+            if (cb <= run) {
+                float s[16];
+                const int c0 = 32 * cb + 16 * half;
+                tmem_ld16(tS + my + c0, s);
+                if (cb < run) {
                     const Two e = cb == 0 ? end[0] : (cb == 1 ? end[1] : end[2]);
                     const float f = ps * ex2(two_diff(mine, e) - rel);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(&s_d.tail[32 * cb + j]);
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(&s_d.tail[c0 + j]);
                         r[j / 2] = pack2<T>(s[j] * (f * t.x), s[j + 1] * (f * t.y));
                         r[j / 2 + 1] = pack2<T>(s[j + 2] * (f * t.z), s[j + 3] * (f * t.w));
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float r0 = __shfl_sync(kFull, rel, j), r1 = __shfl_sync(kFull, rel, j + 1);
-                        const float x = j <= lane ? s[j] * (ps * ex2(r0 - rel)) : 0.0f;
-                        const float y = j + 1 <= lane ? s[j + 1] * (ps * ex2(r1 - rel)) : 0.0f;
+                    for (int j = 0; j < 16; j += 2) {
+                        const int jj = 16 * half + j;
+                        const float r0 = __shfl_sync(kFull, rel, jj), r1 = __shfl_sync(kFull, rel, jj + 1);
+                        const float x = jj <= lane ? s[j] * (ps * ex2(r0 - rel)) : 0.0f;
+                        const float y = jj + 1 <= lane ? s[j + 1] * (ps * ex2(r1 - rel)) : 0.0f;
                         r[j / 2] = pack2<T>(x, y);
                     }
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; j++) r[j] = 0;
+                for (int j = 0; j < 8; j++) r[j] = 0;
             }
-            tmem_st16(tP + my + 16 * cb, r);
+            tmem_st8(tP + my + 16 * cb + 8 * half, r);
         }
-        split_row<T>(V, tid, wt * vs, W[0], W[1], W[2]);
+        split_row<T>(V, tok, half, wt * vs, W[0], W[1], W[2]);
         tmem_wait_st();
         tc_fence_before();
         fence_proxy_async_smem();
@@ -355,8 +363,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd
         tc_fence_after();
         if (tid == 0 && ok && ch + 1 < chunks) load(t0 + C);
         const float fe = a.scale * (ex2(ci) / hs), fi = a.scale / ps;
-#pragma unroll
-        for (int half = 0; half < 2; half++) {
+        {
             float e[32], o[32];
             tmem_ld32(tOe + my + 32 * half, e);
             tmem_ld32(tOi + my + 32 * half, o);
@@ -367,7 +374,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(128, 2) k_tc_fwd
                 for (int i = 0; i < 4; i++)
                     r[i] = pack2<T>(fmaf(fe, e[8 * u + 2 * i], fi * o[8 * u + 2 * i]),
                                     fmaf(fe, e[8 * u + 2 * i + 1], fi * o[8 * u + 2 * i + 1]));
-                *unit(Y, tid, 4 * half + u) = make_uint4(r[0], r[1], r[2], r[3]);
+                *unit(Y, tok, 4 * half + u) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
         add_product<NB>(tU, ex2(cl), 1.0f / vs, X);
@@ -405,14 +412,14 @@ template <int NB> struct StateSmem {
 };
 
 template <typename T, int NB, bool REV, bool SUM>
-__global__ void __launch_bounds__(128, 2) k_tc_state(const __grid_constant__ TcWalkArgs w) {
+__global__ void __launch_bounds__(256, 2) k_tc_state(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = StateSmem<NB>;
     __shared__ Decays s_d;
     __shared__ __align__(8) uint64_t s_ld, s_m;
-    __shared__ uint32_t s_tm, s_red[4];
+    __shared__ uint32_t s_tm, s_red[8];
     const Args& a = w.a;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, tok = tid & (C - 1), run = tok >> 5, half = tid >> 7;
     int64_t id = blockIdx.x;
     const int64_t ptiles = (a.P + PT - 1) / PT;
     const int64_t pt = id % ptiles, p0 = pt * PT;
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(128, 2) k_tc_state(const __grid_constant__ TcW
         tma_load_4d(V, REV ? &w.maps.dy : &w.maps.v, (int)p0, (int)h, (int)t0, (int)b, &s_ld);
     };
     if (tid == 0) load(start_of(0));
-    float X[32 * NB];
+    float X[16 * NB];
     {
         const float* from = nullptr;
         if (!SUM && w.plan.K > 1) from = w.seg_state + ((b * a.H + h) * w.plan.K + seg) * a.N * a.P;
@@ -481,24 +488,24 @@ __global__ void __launch_bounds__(128, 2) k_tc_state(const __grid_constant__ TcW
         const float rel = chunk_decays(s_d, g);
         if (ch + 1 < chunks) g = load_g(a, b, h, start_of(ch + 1), valid(start_of(ch + 1)));
         ok = mbar_wait(&s_ld, ch & 1);
-        if (ok && tid >= nv && t0 + tid < a.L) {
+        if (ok && tok >= nv && t0 + tok < a.L) {
             if (NB == 2) {
                 char* const t[3] = {K, V, K + 16384};
-                clear_row<3>(t);
+                clear_row<3>(t, tok, half);
             } else {
                 char* const t[2] = {K, V};
-                clear_row<2>(t);
+                clear_row<2>(t, tok, half);
             }
             fence_proxy_async_smem();
         }
         if (__syncthreads_or(!ok)) break;
         float vs = 1.0f;
-        if (kF16<T>) vs = f16_scale(block_max(row_max<T>(V, tid), s_red));
+        if (kF16<T>) vs = f16_scale(block_max(row_max<T>(V, tok, half), s_red));
         Two end[4];
         run_ends(s_d, end);
-        const Two mine = warp == 0 ? end[0] : (warp == 1 ? end[1] : (warp == 2 ? end[2] : end[3]));
+        const Two mine = run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3]));
         const float cl = end[3].h + end[3].l;
-        split_row<T>(V, tid, vs * ex2(REV ? (mine.h - rel) + mine.l : two_diff(end[3], mine) + rel), W[0], W[1], W[2]);
+        split_row<T>(V, tok, half, vs * ex2(REV ? (mine.h - rel) + mine.l : two_diff(end[3], mine) + rel), W[0], W[1], W[2]);
         fence_proxy_async_smem();
         __syncthreads();
         if (tid == 0) {
@@ -540,7 +547,7 @@ unsigned blocks(const TcWalkArgs& w, int64_t segs) {
 template <typename K> cudaError_t go(K kernel, int smem, unsigned grid, const TcWalkArgs& w, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, 128, smem, st>>>(w);
+    kernel<<<grid, 256, smem, st>>>(w);
     return cudaGetLastError();
 }
 
