@@ -114,26 +114,22 @@ bool tc_input(const In& x, int64_t L, int64_t Bsz) {
 }
 
 struct WalkTc {
-    WalkPlan plan;
+    TcPlan plan;
     size_t state, decay;
 };
 WalkTc walktc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P) {
     WalkTc w;
-    w.plan = tc_walk_plan(Bsz * H * ceil_div(P, kTileP), L);
-    w.state = w.decay = 0;
-    if (w.plan.K > 1) {
-        w.state = l.take((size_t)Bsz * H * w.plan.K * N * P * 4);
-        w.decay = l.take((size_t)Bsz * H * w.plan.K * 4);
-    }
+    w.plan = tc_plan(Bsz * H * ceil_div(P, kTileP), L);
+    w.state = l.take((size_t)w.plan.cut * w.plan.K * N * kTileP * 4);
+    w.decay = l.take((size_t)w.plan.cut * w.plan.K * 4);
     return w;
 }
 
 // The sum pass of a walk cut in time, and the states its segments start from.
 cudaError_t tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st) {
-    if (w.plan.K == 1) return cudaSuccess;
+    if (w.plan.cut == 0) return cudaSuccess;
     const cudaError_t e = launch_tc_state(w, reverse, true, st);
-    if (e != cudaSuccess) return e;
-    return launch_carry({w.seg_state, w.seg_decay, w.init, w.a.Bsz * w.a.H, w.plan.K, w.a.N * w.a.P, reverse ? 1 : 0}, st);
+    return e != cudaSuccess ? e : launch_tc_carry(w, reverse, st);
 }
 
 // Forward on the tensor cores; *ran tells whether the inputs allow it.

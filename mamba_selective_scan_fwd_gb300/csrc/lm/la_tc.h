@@ -15,21 +15,31 @@ struct TcMaps {
     CUtensorMap q, k, v, dy, y, dv;
 };
 
-// Segments of the tensor-core walk: two blocks run on an SM, so K is the
-// number of segments with the least rounds of blocks times chunks per segment;
-// cutting costs a second reading of k and v (the sum pass, about 0.6 of a walk)
-// and two more launches (about two chunks' time).
-inline WalkPlan tc_walk_plan(int64_t units, int64_t L) {
-    const int64_t chunks = ceil_div(L, kChunkTc), slots = 2 * kSms;
-    WalkPlan best = {1, chunks * kChunkTc};
-    double least = (double)ceil_div(units, slots) * chunks;
-    for (int64_t K = 2; K <= 256 && K <= chunks / 2; K++) {
-        const int64_t per = ceil_div(chunks, K), segs = ceil_div(chunks, per);
-        if (segs != K) continue;
-        const double cost = (double)ceil_div(units * K, slots) * per + 0.6 * ceil_div(units * (K - 1), slots) * per + 2;
-        if (cost < 0.95 * least) {
+// How a walk over units (batch row, head, 64 value channels; in this order, the
+// last fastest) is cut: the first `whole` units are one block each, the other
+// `cut` units K segments of seg tokens.  A cut unit's segments but the last are
+// walked twice: a sum pass gives the state each segment starts from.
+struct TcPlan {
+    int64_t whole, cut, K, seg;
+    int64_t blocks() const { return whole + cut * K; }
+};
+
+// Two blocks run on an SM: full rounds of whole units, and the last partial
+// round cut so that it fills the SMs, where that costs less than running it
+// uncut.  Costs in chunks' time: a round of blocks, half as much for the sum
+// pass, 3 for the two launches that cutting adds.
+inline TcPlan tc_plan(int64_t units, int64_t L) {
+    const int64_t chunks = ceil_div(L, kChunkTc), slots = 2 * kSms, rest = units % slots;
+    TcPlan best = {units, 0, 1, chunks * kChunkTc};
+    if (rest == 0) return best;
+    double least = (double)chunks;
+    for (int64_t K = 2; K <= 256 && K <= chunks; K++) {
+        const int64_t per = ceil_div(chunks, K);
+        if (ceil_div(chunks, per) != K) continue;
+        const double cost = (double)(ceil_div(rest * K, slots) * per) + 0.5 * (ceil_div(rest * (K - 1), slots) * per) + 3;
+        if (cost < least) {
             least = cost;
-            best = {K, per * kChunkTc};
+            best = {units - rest, rest, K, per * kChunkTc};
         }
     }
     return best;
@@ -38,10 +48,10 @@ inline WalkPlan tc_walk_plan(int64_t units, int64_t L) {
 struct TcWalkArgs {
     TcMaps maps;
     Args a;
-    WalkPlan plan;
+    TcPlan plan;
     const float* init;
-    float* seg_state;
-    float* seg_decay;
+    float* seg_state;  // [cut, K, N, 64]: end states of the segments, then (after the carry) their start states
+    float* seg_decay;  // [cut, K]
     float* last;
     void* images;        // [Bsz, H, ptiles, chunks] of (high, low) operand tiles of the state before each chunk
     float* image_scale;  // f16: the power of two each image was multiplied by
@@ -51,6 +61,7 @@ struct TcWalkArgs {
 
 cudaError_t launch_tc_fwd(const TcWalkArgs& w, cudaStream_t st);
 cudaError_t launch_tc_state(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st);
+cudaError_t launch_tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st);
 
 }  // namespace la
 

@@ -5,13 +5,17 @@
 // log decay inside the chunk, cl its end and H the state before it:
 //   S = q k^T,  P_ij = e^{c_i - c_j} S_ij (j <= i),  y = scale (e^{c_i} q H + P v)
 //   H <- e^{cl} H + k^T (e^{cl - c} v)
-// One block walks one segment of one (batch row, head, 64 value channels) and
-// keeps H in f32 registers (thread = one of the N rows): S, q H and k^T (w v)
-// are products of tiles that TMA brought, P is the left operand out of tensor
-// memory.  Roundings to 16 bits: P, and H as an operand of q H (one rounding of
+// One block walks one segment of one (batch row, head, 64 value channels): S,
+// q H and k^T (w v) are products of tiles that TMA brought, P is the left
+// operand out of tensor memory.  Two warpgroups share a chunk after S and q H:
+// the state half makes w v, adds k^T (w v) to H, which it keeps in f32 registers
+// (thread = one of the N rows), and writes the next chunk's H operand; the
+// output half makes P, P v and y.  Their chains overlap (a chunk took 10.5
+// thousand cycles when all threads did all of it in turn).  Roundings to 16 bits: P, and H as an operand of q H (one rounding of
 // terms of a 16-bit y each).  The state is f32: w v enters as two or three
 // 16-bit parts whose sum holds 22 to 24 bits.
 #include "la_tc.h"
+#include "../simd.cuh"
 #include "tc.cuh"
 
 namespace ss {
@@ -26,67 +30,78 @@ template <> constexpr bool kF16<__half> = true;
 // 16-bit parts of w v: 3 x 8 bits (bf16), 2 x 11 (f16)
 template <typename T> constexpr int kParts = kF16<T> ? 2 : 3;
 
-// The chunk's decays, by runs of 32 tokens (one warp's).  c_i = (the run's end)
-// - rel_i; rel is a thread's own, the rest is shared.
-struct Decays {
-    float tail[C];  // e^{rel}
-    Two total[4];   // log2 decay of each run
-};
-
-// Both halves of the block (256 threads, token = tid % 128), x: the token's log2
-// decay.  Returns rel (at most 0 for decays).
-__device__ __forceinline__ float chunk_decays(Decays& d, float x) {
+// The chunk's decays, by runs of 32 tokens (one warp's): c_i = (the run's end) -
+// rel_i with rel a thread's own.  Shared: tail = e^{rel} (where wanted) and the
+// log2 decay of each run.
+// A warpgroup (token = tid % 128), x: the token's log2 decay.  Returns rel (at
+// most 0 for decays).
+__device__ __forceinline__ float chunk_decays(float* tail, Two* total, float x) {
+    const int tok = threadIdx.x & (C - 1);
     const float in[1] = {x};
     Two c[1];
     warp_cumsum<1>(in, c);
     const Two end = {__shfl_sync(kFull, c[0].h, 31), __shfl_sync(kFull, c[0].l, 31)};
     const float rel = two_diff(end, c[0]);
-    if (threadIdx.x < C) {
-        d.tail[threadIdx.x] = ex2(rel);
-        if ((threadIdx.x & 31) == 31) d.total[threadIdx.x >> 5] = end;
-    }
+    if (tail) tail[tok] = ex2(rel);
+    if ((tok & 31) == 31) total[tok >> 5] = end;
     return rel;
 }
 // After a barrier: log2 decays from the chunk's start to the end of each run.
-__device__ __forceinline__ void run_ends(const Decays& d, Two (&end)[4]) {
-    end[0] = d.total[0];
+__device__ __forceinline__ void run_ends(const Two* total, Two (&end)[4]) {
+    end[0] = total[0];
 #pragma unroll
-    for (int i = 1; i < 4; i++) end[i] = two_add(end[i - 1], d.total[i]);
+    for (int i = 1; i < 4; i++) end[i] = two_add(end[i - 1], total[i]);
 }
 __device__ __forceinline__ float load_g(const Args& a, int64_t b, int64_t h, int64_t t0, int nv) {
     const int t = threadIdx.x & (C - 1);
     return t < nv ? log_decay(a, b, t0 + t, h) * kLog2e : 0.0f;
 }
 
-// Largest value of the block's threads (all get it); v >= 0.  Two block barriers.
-__device__ __forceinline__ float block_max(float v, uint32_t* red) {
+// Barrier of one warpgroup (128 threads): id 1 or 2.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Largest value of a warpgroup's threads (all get it); v >= 0.  Two barriers.
+__device__ __forceinline__ float group_max(float v, uint32_t* red, int id) {
     uint32_t m;
     asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = max(max(max(red[0], red[1]), max(red[2], red[3])), max(max(red[4], red[5]), max(red[6], red[7])));
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[(threadIdx.x >> 5) & 3] = m;
+    group_sync(id);
+    m = max(max(red[0], red[1]), max(red[2], red[3]));
+    group_sync(id);
     return __uint_as_float(m);
 }
 
-// Half of row `row` of a value tile, times w, as 16-bit parts (same layout).
-template <typename T> __device__ __forceinline__ void split_row(void* v, int row, int half, float w, void* p0, void* p1, void* p2) {
+// (x, y) as a pair of 16-bit values, and what the pair leaves of them.  bf16
+// truncates (the rest is exact, and keeps the sign), so that three parts hold
+// all 24 bits; f16 rounds, two parts hold 22.
+template <typename T> __device__ __forceinline__ uint32_t split2(float2& f) {
+    if (kF16<T>) {
+        const uint32_t r = pack2<T>(f.x, f.y);
+        const float2 g = unpack2<T>(r);
+        f = make_float2(f.x - g.x, f.y - g.y);
+        return r;
+    }
+    const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y);
+    f = make_float2(f.x - __uint_as_float(x & 0xffff0000u), f.y - __uint_as_float(y & 0xffff0000u));
+    return __byte_perm(x, y, 0x7632);
+}
+
+// Row `row` of a value tile, times w, as 16-bit parts (same layout).
+template <typename T> __device__ __forceinline__ void split_row(void* v, int row, float w, void* p0, void* p1, void* p2) {
 #pragma unroll 2
-    for (int u = 4 * half; u < 4 * half + 4; u++) {
+    for (int u = 0; u < 8; u++) {
         const uint4 in = *unit(v, row, u);
         const uint32_t x[4] = {in.x, in.y, in.z, in.w};
         uint32_t r[3][4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            float2 f = unpack2<T>(x[i]);
-            f.x *= w;
-            f.y *= w;
-#pragma unroll
-            for (int k = 0; k < kParts<T>; k++) {
-                r[k][i] = pack2<T>(f.x, f.y);
-                const float2 g = unpack2<T>(r[k][i]);
-                f.x -= g.x;
-                f.y -= g.y;
+            float2 f = mul2(unpack2<T>(x[i]), splat2(w));
+            r[0][i] = split2<T>(f);
+            if (kParts<T> == 3) {
+                r[1][i] = split2<T>(f);
+                r[2][i] = pack2<T>(f.x, f.y);
+            } else {
+                r[1][i] = pack2<T>(f.x, f.y);
             }
         }
         *unit(p0, row, u) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
@@ -95,10 +110,10 @@ template <typename T> __device__ __forceinline__ void split_row(void* v, int row
     }
 }
 
-template <typename T> __device__ __forceinline__ float row_max(void* v, int row, int half) {
+template <typename T> __device__ __forceinline__ float row_max(void* v, int row) {
     float m = 0.0f;
 #pragma unroll
-    for (int u = 4 * half; u < 4 * half + 4; u++) {
+    for (int u = 0; u < 8; u++) {
         const uint4 in = *unit(v, row, u);
         const uint32_t x[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
@@ -110,67 +125,141 @@ template <typename T> __device__ __forceinline__ float row_max(void* v, int row,
     return m;
 }
 
-// The state a thread of 256 holds: NB == 2, row tid % 128, 32 of the 64 columns;
-// NB == 1, row tid % 64, 16 columns (the product's 128 rows hold the 64 twice).
+// The state a thread of a warpgroup holds: NB == 2, row tid, 64 columns; NB ==
+// 1, row tid % 64, 32 columns (the product's 128 rows hold the 64 twice).
 template <int NB> struct StateOf {
-    static constexpr int W = 16 * NB;
+    static constexpr int W = 32 * NB;
     __device__ static int row() { return threadIdx.x & (64 * NB - 1); }
-    __device__ static int col() { return (int)(threadIdx.x / (64 * NB)) * W; }
+    __device__ static int col() { return NB == 2 ? 0 : (int)(threadIdx.x & 64) / 2; }
 };
 
-template <int NB> __device__ __forceinline__ void load_state(const float* p, const Args& a, int64_t p0, float (&X)[16 * NB]) {
+// A state tile in memory: rows of `stride` floats, `cols` of the 64 columns exist.
+struct StateTile {
+    const float* p;  // null: zero
+    int64_t rows, stride, cols;
+};
+template <int NB> __device__ __forceinline__ void load_state(const StateTile& s, float (&X)[32 * NB]) {
     const int n = StateOf<NB>::row(), c0 = StateOf<NB>::col();
 #pragma unroll
-    for (int c = 0; c < 16 * NB; c += 4) {
+    for (int c = 0; c < 32 * NB; c += 4) {
         float4 f = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p && n < a.N && p0 + c0 + c < a.P) f = *reinterpret_cast<const float4*>(p + n * a.P + p0 + c0 + c);
+        if (s.p && n < s.rows && c0 + c < s.cols) f = *reinterpret_cast<const float4*>(s.p + n * s.stride + c0 + c);
         X[c] = f.x;
         X[c + 1] = f.y;
         X[c + 2] = f.z;
         X[c + 3] = f.w;
     }
 }
-template <int NB> __device__ __forceinline__ void save_state(float* p, const Args& a, int64_t p0, const float (&X)[16 * NB]) {
+template <int NB> __device__ __forceinline__ void save_state(const StateTile& s, const float (&X)[32 * NB]) {
     const int n = StateOf<NB>::row(), c0 = StateOf<NB>::col();
 #pragma unroll
-    for (int c = 0; c < 16 * NB; c += 4)
-        if (n < a.N && p0 + c0 + c < a.P)
-            *reinterpret_cast<float4*>(p + n * a.P + p0 + c0 + c) = make_float4(X[c], X[c + 1], X[c + 2], X[c + 3]);
+    for (int c = 0; c < 32 * NB; c += 4)
+        if (n < s.rows && c0 + c < s.cols)
+            *reinterpret_cast<float4*>(const_cast<float*>(s.p) + n * s.stride + c0 + c) =
+                make_float4(X[c], X[c + 1], X[c + 2], X[c + 3]);
 }
-template <int NB> __device__ __forceinline__ float state_max(const float (&X)[16 * NB]) {
+
+// The walk a block takes, from its index.
+struct Walk {
+    int64_t b, h, hq, pt, p0, cut, seg, t_begin, t_end;
+    bool is_cut;
+
+    __device__ Walk(const TcWalkArgs& w, bool sum, bool reverse) {
+        const Args& a = w.a;
+        const int64_t ptiles = (a.P + PT - 1) / PT;
+        int64_t id = blockIdx.x, unit = id;
+        is_cut = sum || id >= w.plan.whole;
+        cut = seg = 0;
+        if (is_cut) {
+            if (!sum) id -= w.plan.whole;
+            cut = id % w.plan.cut;
+            seg = id / w.plan.cut + (sum && reverse ? 1 : 0);  // the segment walked last needs no sum
+            unit = w.plan.whole + cut;
+        }
+        pt = unit % ptiles;
+        p0 = pt * PT;
+        h = unit / ptiles % a.H;
+        b = unit / ptiles / a.H;
+        hq = h / (a.H / a.G);
+        t_begin = is_cut ? seg * w.plan.seg : 0;
+        t_end = is_cut ? min(a.L, t_begin + w.plan.seg) : a.L;
+    }
+    __device__ StateTile start(const TcWalkArgs& w) const {
+        if (is_cut) return segment(w);
+        return whole(w, w.init);
+    }
+    __device__ StateTile segment(const TcWalkArgs& w) const {
+        return {w.seg_state + (cut * w.plan.K + seg) * w.a.N * PT, w.a.N, PT, PT};
+    }
+    __device__ StateTile whole(const TcWalkArgs& w, const float* p) const {
+        return {p ? p + (b * w.a.H + h) * w.a.N * w.a.P + p0 : nullptr, w.a.N, w.a.P, w.a.P - p0};
+    }
+    __device__ bool ends(const TcWalkArgs& w, bool reverse) const {  // whether its last state is the walk's
+        return !is_cut || seg == (reverse ? 0 : w.plan.K - 1);
+    }
+};
+template <int NB> __device__ __forceinline__ float state_max(const float (&X)[32 * NB]) {
     float m = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 16 * NB; c++) m = fmaxf(m, fabsf(X[c]));
+    for (int c = 0; c < 32 * NB; c++) m = fmaxf(m, fabsf(X[c]));
     return m;
 }
-__device__ __forceinline__ void tmem_ldw(uint32_t addr, float (&x)[16]) { tmem_ld16(addr, x); }
-__device__ __forceinline__ void tmem_ldw(uint32_t addr, float (&x)[32]) { tmem_ld32(addr, x); }
-// X <- d X + u * (the product in tensor memory)
-template <int NB> __device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float (&X)[16 * NB]) {
-    float f[16 * NB];
-    tmem_ldw(tm + ((threadIdx.x & 96) << 16) + StateOf<NB>::col(), f);
+// X <- d X + u * (the sum of PARTS products, 64 columns apart in tensor memory)
+template <int NB, int PARTS> __device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float (&X)[32 * NB]) {
 #pragma unroll
-    for (int i = 0; i < 16 * NB; i++) X[i] = fmaf(d, X[i], u * f[i]);
+    for (int c = 0; c < NB; c++) {
+#pragma unroll
+        for (int p = 0; p < PARTS; p++) {
+            float f[32];
+            tmem_ld32(tm + ((threadIdx.x & 96) << 16) + StateOf<NB>::col() + 32 * c + 64 * p, f);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 x = make_float2(f[i], f[i + 1]);
+                float2 y = make_float2(X[32 * c + i], X[32 * c + i + 1]);
+                if (p == 0) y = mul2(splat2(d), y);
+                y = fma2(splat2(u), x, y);
+                X[32 * c + i] = y.x;
+                X[32 * c + i + 1] = y.y;
+            }
+        }
+    }
 }
-// 16-bit rows [n][p] of X * s (and of what the rounding left): operand tiles
-template <typename T, int NB> __device__ __forceinline__ void put_state(void* hi, void* lo, float s, const float (&X)[16 * NB]) {
+// 16-bit rows [n][p] of X * s: an operand tile
+template <typename T, int NB> __device__ __forceinline__ void put_state(void* to, float s, const float (&X)[32 * NB]) {
     const int n = StateOf<NB>::row(), u0 = StateOf<NB>::col() / 8;
 #pragma unroll
-    for (int u = 0; u < 2 * NB; u++) {
+    for (int u = 0; u < 4 * NB; u++) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float2 f = make_float2(X[8 * u + 2 * i], X[8 * u + 2 * i + 1]);
+            if (kF16<T>) f = mul2(f, splat2(s));
+            r[i] = pack2<T>(f.x, f.y);
+        }
+        *unit(to, n, u0 + u) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+// ... and of what the rounding left
+template <typename T, int NB> __device__ __forceinline__ void put_state2(void* hi, void* lo, float s, const float (&X)[32 * NB]) {
+    const int n = StateOf<NB>::row(), u0 = StateOf<NB>::col() / 8;
+#pragma unroll
+    for (int u = 0; u < 4 * NB; u++) {
         uint32_t r[4], q[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float x = X[8 * u + 2 * i] * s, y = X[8 * u + 2 * i + 1] * s;
-            r[i] = pack2<T>(x, y);
+            float2 f = make_float2(X[8 * u + 2 * i], X[8 * u + 2 * i + 1]);
+            if (kF16<T>) f = mul2(f, splat2(s));
+            r[i] = pack2<T>(f.x, f.y);
             const float2 g = unpack2<T>(r[i]);
-            q[i] = pack2<T>(x - g.x, y - g.y);
+            q[i] = pack2<T>(f.x - g.x, f.y - g.y);
         }
         *unit(hi, n, u0 + u) = make_uint4(r[0], r[1], r[2], r[3]);
-        if (lo) *unit(lo, n, u0 + u) = make_uint4(q[0], q[1], q[2], q[3]);
+        *unit(lo, n, u0 + u) = make_uint4(q[0], q[1], q[2], q[3]);
     }
 }
 
-// k^T (w v): rows n (both halves of the 128 rows the same 64 when NB == 1), columns p
+// k^T (w v): rows n (both halves of the 128 rows the same 64 when NB == 1), columns
+// p.  Its parts added up in 64 columns of tensor memory (w: one tile per part) ...
 template <typename T, int NB> __device__ __forceinline__ void mma_state(uint32_t tm, const void* k, const void* const (&w)[3]) {
     constexpr uint32_t desc = mma_desc<T>(128, PT, true, true);
     const uint32_t ka = smem_addr(k);
@@ -180,13 +269,21 @@ template <typename T, int NB> __device__ __forceinline__ void mma_state(uint32_t
         for (int s = 0; s < C / 16; s++)
             mma(tm, smem_desc(ka + s * 2048, NB == 2 ? 16384 : 0), smem_desc(smem_addr(w[p]) + s * 2048), desc, p + s > 0);
 }
+// ... or side by side (w: the parts' tiles one after the other), which reads k once
+template <typename T, int NB> __device__ __forceinline__ void mma_state_wide(uint32_t tm, const void* k, const void* w) {
+    constexpr uint32_t desc = mma_desc<T>(128, PT * kParts<T>, true, true);
+    const uint32_t ka = smem_addr(k), wa = smem_addr(w);
+#pragma unroll
+    for (int s = 0; s < C / 16; s++)
+        mma(tm, smem_desc(ka + s * 2048, NB == 2 ? 16384 : 0), smem_desc(wa + s * 2048, 16384), desc, s > 0);
+}
 
-// Half a row of each tile that a copy filled with a token beyond the row's length: zero.
-template <int TILES> __device__ __forceinline__ void clear_row(char* const (&tiles)[TILES], int row, int half) {
+// A row of each tile that a copy filled with a token beyond the batch row's length: zero.
+template <int TILES> __device__ __forceinline__ void clear_row(char* const (&tiles)[TILES], int row) {
 #pragma unroll
     for (int i = 0; i < TILES; i++)
 #pragma unroll
-        for (int u = 0; u < 4; u++) *unit(tiles[i], row, 4 * half + u) = make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 8; u++) *unit(tiles[i], row, u) = make_uint4(0, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------- forward
@@ -198,21 +295,17 @@ template <int NB> struct FwdSmem {
 template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = FwdSmem<NB>;
-    __shared__ Decays s_d;
-    __shared__ __align__(8) uint64_t s_ld, s_m1, s_m2;
-    __shared__ uint32_t s_tm, s_red[8];
+    __shared__ float s_tail[C];
+    __shared__ Two s_total[2][4];
+    // copies landed; S; q H; P v; k^T (w v)
+    __shared__ __align__(8) uint64_t s_ld, s_mS, s_mE, s_mO, s_mU;
+    __shared__ uint32_t s_tm, s_red[4];
+    __shared__ float s_hs[2];
     const Args& a = w.a;
-    // thread: token (and accumulator row) tok, half `half` of its columns
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, half = tid >> 7;
-    int64_t id = blockIdx.x;
-    const int64_t ptiles = (a.P + PT - 1) / PT;
-    const int64_t p0 = (id % ptiles) * PT;
-    id /= ptiles;
-    const int64_t h = id % a.H;
-    id /= a.H;
-    const int64_t seg = id % w.plan.K, b = id / w.plan.K;
-    const int64_t hq = h / (a.H / a.G);
-    const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
+    const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5;
+    const bool out = tid >= C;  // output half, else state half
+    const Walk at(w, false, false);
+    const int64_t b = at.b, h = at.h, hq = at.hq, p0 = at.p0, t_begin = at.t_begin, t_end = at.t_end;
     const int64_t len = row_length(a, b);
     const int chunks = (int)((t_end - t_begin + C - 1) / C);
     char *Q = sm + L::q, *K = sm + L::k, *V = sm + L::v, *H = sm + L::h, *Y = sm + L::y;
@@ -220,16 +313,18 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
 
     if (tid == 0) {
         mbar_init(&s_ld, 1);
-        mbar_init(&s_m1, 1);
-        mbar_init(&s_m2, 1);
+        mbar_init(&s_mS, 1);
+        mbar_init(&s_mE, 1);
+        mbar_init(&s_mO, 1);
+        mbar_init(&s_mU, 1);
         fence_proxy_async_smem();
     }
-    if (warp == 0) tmem_alloc(&s_tm, 256);
+    if (tid < 32) tmem_alloc(&s_tm, 256);
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tm;
-    // S, then (all of it read) P v and k^T (w v) in its place
-    const uint32_t tS = tm, tOi = tm, tU = tm + 64, tP = tm + 128, tOe = tm + 192;
+    // S; P in the place of its first 64 columns, P v in the others'
+    const uint32_t tS = tm, tP = tm, tO = tm + 64, tE = tm + 128, tU = tm + 192;
     const uint32_t my = (uint32_t)(run * 32) << 16;
 
     auto load = [&](int64_t t0) {
@@ -241,165 +336,198 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
         }
         tma_load_4d(V, &w.maps.v, (int)p0, (int)h, (int)t0, (int)b, &s_ld);
     };
-    if (tid == 0) load(t_begin);
-
-    float X[16 * NB];
-    {
-        const float* from = nullptr;
-        if (w.plan.K > 1) from = w.seg_state + ((b * a.H + h) * w.plan.K + seg) * a.N * a.P;
-        else if (w.init) from = w.init + (b * a.H + h) * a.N * a.P;
-        load_state<NB>(from, a, p0, X);
-    }
     auto valid = [&](int64_t t0) { return (int)max((int64_t)0, min((int64_t)C, len - t0)); };
+    if (tid == C) load(t_begin);
+
     float g = load_g(a, b, h, t_begin, valid(t_begin));
     bool ok = true;
     int ch = 0;
-    for (; ch < chunks; ch++) {
-        const int64_t t0 = t_begin + (int64_t)ch * C;
-        const int nv = valid(t0);
-        float hs = 1.0f;  // scale of H as an operand
-        if (kF16<T>) hs = f16_scale(block_max(state_max<NB>(X), s_red));
-        put_state<T, NB>(H, nullptr, hs, X);
-        const float rel = chunk_decays(s_d, g);
+    // both halves: chunk ch's decays (into end, rel), then its tiles
+    auto decays = [&](float* tail, Two* total, int64_t t0) {
+        const float rel = chunk_decays(tail, total, g);
         if (ch + 1 < chunks) g = load_g(a, b, h, t0 + C, valid(t0 + C));
-        ok = mbar_wait(&s_ld, ch & 1);
-        if (ok && tok >= nv && t0 + tok < a.L) {
-            if (NB == 2) {
-                char* const t[5] = {Q, K, V, Q + 16384, K + 16384};
-                clear_row<5>(t, tok, half);
-            } else {
-                char* const t[3] = {Q, K, V};
-                clear_row<3>(t, tok, half);
+        return rel;
+    };
+    auto end_of = [&](const Two (&end)[4]) { return run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3])); };
+    if (!out) {
+        float X[32 * NB];
+        load_state<NB>(at.start(w), X);
+        for (; ch < chunks; ch++) {
+            const uint32_t ph = ch & 1;
+            float hs = 1.0f;  // scale of H as an operand
+            if (kF16<T>) {
+                hs = f16_scale(group_max(state_max<NB>(X), s_red, 1));
+                if (tid == 0) s_hs[ph] = hs;
             }
-        }
-        fence_proxy_async_smem();
-        if (__syncthreads_or(!ok)) break;
-        if (tid == 0) {
+            put_state<T, NB>(H, hs, X);
+            const float rel = decays(nullptr, s_total[0], t_begin + (int64_t)ch * C);
+            ok = ok && mbar_wait(&s_ld, ph);
+            fence_proxy_async_smem();
+            if (__syncthreads_or(!ok)) break;
+            Two end[4];
+            run_ends(s_total[0], end);
+            const Two mine = end_of(end);
+            float vs = 1.0f;
+            if (kF16<T>) vs = f16_scale(group_max(row_max<T>(V, tok), s_red, 1));
+            const float wt = ex2(two_diff(end[3], mine) + rel), cl = end[3].h + end[3].l;
+            ok = mbar_wait(&s_mE, ph);  // q (and the last y's staging tile) make room for w v
+            split_row<T>(V, tok, wt * vs, W[0], W[1], W[2]);
+            fence_proxy_async_smem();
+            group_sync(1);
+            if (tid == 0) {
+                tc_fence_after();
+                const void* const parts[3] = {W[0], W[1], W[2]};
+                mma_state<T, NB>(tU, K, parts);
+                mma_commit(&s_mU);
+            }
+            ok = mbar_wait(&s_mU, ph) && ok;
             tc_fence_after();
-            constexpr uint32_t dS = mma_desc<T>(128, 128, false, false), dE = mma_desc<T>(128, PT, false, true);
-#pragma unroll
-            for (int s = 0; s < 4 * NB; s++) {
-                const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
-                mma(tS, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(K) + at), dS, s > 0);
-            }
-#pragma unroll
-            for (int s = 0; s < 4 * NB; s++) {
-                const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
-                mma(tOe, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(H) + s * 2048), dE, s > 0);
-            }
-            bulk_wait_read();  // the last y has left its staging tile, which a part of w v takes below
-            mma_commit(&s_m1);
+            add_product<NB, 1>(tU, ex2(cl), 1.0f / vs, X);
+            tc_fence_before();
         }
-        float vs = 1.0f;
-        if (kF16<T>) vs = f16_scale(block_max(row_max<T>(V, tok, half), s_red));
-        Two end[4];
-        run_ends(s_d, end);
-        const Two mine = run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3]));
-        const float ci = (mine.h - rel) + mine.l, cl = end[3].h + end[3].l;
-        const float wt = ex2(two_diff(end[3], mine) + rel);
-        ok = mbar_wait(&s_m1, ch & 1);
-        tc_fence_after();
-        // P, by runs of 32 columns, 16 to each half of the block: left of the diagonal e^{c_i - c_j} =
-        // e^{c_i - c_e} e^{c_e - c_j} with e the end of the run (both factors are at most 1 for decays), on
-        // it one exponential each
-        float ps = 1.0f;
-        if (kF16<T>) {
-            float m = 0.0f;
-            for (int cb = 0; cb <= run; cb++) {
-                float s[32];
-                tmem_ld32(tS + my + 32 * cb, s);
-#pragma unroll
-                for (int j = 0; j < 32; j++)
-                    if (32 * cb + j <= tok) m = fmaxf(m, fabsf(s[j]));
+        if (ch == chunks && w.last && at.ends(w, false)) save_state<NB>(at.whole(w, w.last), X);
+    } else {
+        for (; ch < chunks; ch++) {
+            const int64_t t0 = t_begin + (int64_t)ch * C;
+            const uint32_t ph = ch & 1;
+            const float rel = decays(s_tail, s_total[1], t0);
+            ok = ok && mbar_wait(&s_ld, ph);
+            if (ok && tok >= valid(t0) && t0 + tok < a.L) {
+                if (NB == 2) {
+                    char* const t[5] = {Q, K, V, Q + 16384, K + 16384};
+                    clear_row<5>(t, tok);
+                } else {
+                    char* const t[3] = {Q, K, V};
+                    clear_row<3>(t, tok);
+                }
             }
-            ps = f16_scale(m);
-        }
-        for (int cb = 0; cb < 4; cb++) {
-            uint32_t r[8];
-            if (cb <= run) {
-                float s[16];
-                const int c0 = 32 * cb + 16 * half;
-                tmem_ld16(tS + my + c0, s);
-                if (cb < run) {
-                    const Two e = cb == 0 ? end[0] : (cb == 1 ? end[1] : end[2]);
-                    const float f = ps * ex2(two_diff(mine, e) - rel);
+            fence_proxy_async_smem();
+            if (__syncthreads_or(!ok)) break;
+            Two end[4];
+            run_ends(s_total[1], end);
+            const Two mine = end_of(end);
+            if (tid == C) {
+                tc_fence_after();
+                constexpr uint32_t dS = mma_desc<T>(128, 128, false, false), dE = mma_desc<T>(128, PT, false, true);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(&s_d.tail[c0 + j]);
-                        r[j / 2] = pack2<T>(s[j] * (f * t.x), s[j + 1] * (f * t.y));
-                        r[j / 2 + 1] = pack2<T>(s[j + 2] * (f * t.z), s[j + 3] * (f * t.w));
+                for (int s = 0; s < 4 * NB; s++) {
+                    const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
+                    mma(tS, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(K) + at), dS, s > 0);
+                }
+                mma_commit(&s_mS);
+#pragma unroll
+                for (int s = 0; s < 4 * NB; s++) {
+                    const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
+                    mma(tE, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(H) + s * 2048), dE, s > 0);
+                }
+                bulk_wait_read();  // the last y has left its staging tile
+                mma_commit(&s_mE);
+            }
+            const float ci = (mine.h - rel) + mine.l;
+            ok = mbar_wait(&s_mS, ph);
+            tc_fence_after();
+            // P, by runs of 32 columns: left of the diagonal e^{c_i - c_j} = e^{c_i - c_e} e^{c_e - c_j} with e
+            // the end of the run (both factors are at most 1 for decays), on it one exponential each
+            float ps = 1.0f;
+            if (kF16<T>) {
+                float m = 0.0f;
+                for (int cb = 0; cb <= run; cb++) {
+                    float s[32];
+                    tmem_ld32(tS + my + 32 * cb, s);
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        if (32 * cb + j <= tok) m = fmaxf(m, fabsf(s[j]));
+                }
+                ps = f16_scale(m);
+            }
+            for (int cb = 0; cb < 4; cb++) {
+                uint32_t r[16];
+                if (cb <= run) {
+                    float s[32];
+                    tmem_ld32(tS + my + 32 * cb, s);
+                    if (cb < run) {
+                        const Two e = cb == 0 ? end[0] : (cb == 1 ? end[1] : end[2]);
+                        const float2 f = splat2(ps * ex2(two_diff(mine, e) - rel));
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(&s_tail[32 * cb + j]);
+                            const float2 x = mul2(make_float2(s[j], s[j + 1]), mul2(f, make_float2(t.x, t.y)));
+                            const float2 y = mul2(make_float2(s[j + 2], s[j + 3]), mul2(f, make_float2(t.z, t.w)));
+                            r[j / 2] = pack2<T>(x.x, x.y);
+                            r[j / 2 + 1] = pack2<T>(y.x, y.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float r0 = __shfl_sync(kFull, rel, j), r1 = __shfl_sync(kFull, rel, j + 1);
+                            const float x = j <= lane ? s[j] * (ps * ex2(r0 - rel)) : 0.0f;
+                            const float y = j + 1 <= lane ? s[j + 1] * (ps * ex2(r1 - rel)) : 0.0f;
+                            r[j / 2] = pack2<T>(x, y);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const int jj = 16 * half + j;
-                        const float r0 = __shfl_sync(kFull, rel, jj), r1 = __shfl_sync(kFull, rel, jj + 1);
-                        const float x = jj <= lane ? s[j] * (ps * ex2(r0 - rel)) : 0.0f;
-                        const float y = jj + 1 <= lane ? s[j + 1] * (ps * ex2(r1 - rel)) : 0.0f;
-                        r[j / 2] = pack2<T>(x, y);
-                    }
+                    for (int j = 0; j < 16; j++) r[j] = 0;
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; j++) r[j] = 0;
+                tmem_st16(tP + my + 16 * cb, r);
             }
-            tmem_st8(tP + my + 16 * cb + 8 * half, r);
-        }
-        split_row<T>(V, tok, half, wt * vs, W[0], W[1], W[2]);
-        tmem_wait_st();
-        tc_fence_before();
-        fence_proxy_async_smem();
-        if (__syncthreads_or(!ok)) break;
-        if (tid == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            group_sync(2);
+            if (tid == C) {
+                tc_fence_after();
+                constexpr uint32_t dV = mma_desc<T>(128, PT, false, true);
+#pragma unroll
+                for (int s = 0; s < C / 16; s++) mma_ts(tO, tP + 8 * s, smem_desc(smem_addr(V) + s * 2048), dV, s > 0);
+                mma_commit(&s_mO);
+            }
+            ok = mbar_wait(&s_mE, ph) && ok;
             tc_fence_after();
-            constexpr uint32_t dV = mma_desc<T>(128, PT, false, true);
+            const float fe = a.scale * (kF16<T> ? ex2(ci) / s_hs[ph] : ex2(ci)), fi = kF16<T> ? a.scale / ps : a.scale;
+            ok = mbar_wait(&s_mO, ph) && ok;
+            ok = mbar_wait(&s_mU, ph) && ok;  // w v has left the staging tile, k and v are done with
+            tc_fence_after();
+            if (tid == C && ok && ch + 1 < chunks) load(t0 + C);
 #pragma unroll
-            for (int s = 0; s < C / 16; s++) mma_ts(tOi, tP + 8 * s, smem_desc(smem_addr(V) + s * 2048), dV, s > 0);
-            const void* const parts[3] = {W[0], W[1], W[2]};
-            mma_state<T, NB>(tU, K, parts);
-            mma_commit(&s_m2);
-        }
-        ok = mbar_wait(&s_m2, ch & 1);
-        tc_fence_after();
-        if (tid == 0 && ok && ch + 1 < chunks) load(t0 + C);
-        const float fe = a.scale * (ex2(ci) / hs), fi = a.scale / ps;
-        {
-            float e[32], o[32];
-            tmem_ld32(tOe + my + 32 * half, e);
-            tmem_ld32(tOi + my + 32 * half, o);
+            for (int half = 0; half < 2; half++) {
+                float e[32], o[32];
+                tmem_ld32(tE + my + 32 * half, e);
+                tmem_ld32(tO + my + 32 * half, o);
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                uint32_t r[4];
+                for (int u = 0; u < 4; u++) {
+                    uint32_t r[4];
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    r[i] = pack2<T>(fmaf(fe, e[8 * u + 2 * i], fi * o[8 * u + 2 * i]),
-                                    fmaf(fe, e[8 * u + 2 * i + 1], fi * o[8 * u + 2 * i + 1]));
-                *unit(Y, tok, 4 * half + u) = make_uint4(r[0], r[1], r[2], r[3]);
+                    for (int i = 0; i < 4; i++) {
+                        const int c = 8 * u + 2 * i;
+                        const float2 x = fma2(splat2(fi), make_float2(o[c], o[c + 1]),
+                                              mul2(splat2(fe), make_float2(e[c], e[c + 1])));
+                        r[i] = pack2<T>(x.x, x.y);
+                    }
+                    *unit(Y, tok, 4 * half + u) = make_uint4(r[0], r[1], r[2], r[3]);
+                }
             }
-        }
-        add_product<NB>(tU, ex2(cl), 1.0f / vs, X);
-        tc_fence_before();
-        fence_proxy_async_smem();
-        if (__syncthreads_or(!ok)) break;
-        if (tid == 0) {
-            tma_store_4d(&w.maps.y, Y, (int)p0, (int)h, (int)t0, (int)b);
-            bulk_commit();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            group_sync(2);
+            if (tid == C) {
+                tma_store_4d(&w.maps.y, Y, (int)p0, (int)h, (int)t0, (int)b);
+                bulk_commit();
+            }
         }
     }
     if (ch < chunks) {  // a wait ran out: report, wait for what is in flight (within limits), leave
-        if (tid == 0) {
+        if (tid == C) {
             atomicOr(w.status, kDevWaitTimeout);
             mbar_wait(&s_ld, ch & 1);
             mbar_wait(&s_ld, (ch + 1) & 1);
-            mbar_wait(&s_m1, ch & 1);
-            mbar_wait(&s_m2, ch & 1);
+            mbar_wait(&s_mE, (ch + 1) & 1);
+            mbar_wait(&s_mO, (ch + 1) & 1);
+            mbar_wait(&s_mU, (ch + 1) & 1);
         }
-    } else if (w.last && seg == w.plan.K - 1) {
-        save_state<NB>(w.last + (b * a.H + h) * a.N * a.P, a, p0, X);
     }
-    if (tid == 0) bulk_wait_all();
+    if (tid == C) bulk_wait_all();
     __syncthreads();
-    if (warp == 0) tmem_free(tm, 256);
+    if (tid < 32) tmem_free(tm, 256);
 }
 
 // ---------------------------------------------------------------- states
@@ -412,26 +540,16 @@ template <int NB> struct StateSmem {
 };
 
 template <typename T, int NB, bool REV, bool SUM>
-__global__ void __launch_bounds__(256, 2) k_tc_state(const __grid_constant__ TcWalkArgs w) {
+__global__ void __launch_bounds__(128, 2) k_tc_state(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = StateSmem<NB>;
-    __shared__ Decays s_d;
+    __shared__ Two s_total[4];
     __shared__ __align__(8) uint64_t s_ld, s_m;
-    __shared__ uint32_t s_tm, s_red[8];
+    __shared__ uint32_t s_tm, s_red[4];
     const Args& a = w.a;
-    const int tid = threadIdx.x, warp = tid >> 5, tok = tid & (C - 1), run = tok >> 5, half = tid >> 7;
-    int64_t id = blockIdx.x;
-    const int64_t ptiles = (a.P + PT - 1) / PT;
-    const int64_t pt = id % ptiles, p0 = pt * PT;
-    id /= ptiles;
-    const int64_t h = id % a.H;
-    id /= a.H;
-    const int64_t segs = SUM ? w.plan.K - 1 : w.plan.K;
-    int64_t seg = id % segs;
-    const int64_t b = id / segs;
-    if (SUM && REV) seg += 1;
-    const int64_t hq = h / (a.H / a.G);
-    const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
+    const int tid = threadIdx.x, warp = tid >> 5, tok = tid, run = warp;
+    const Walk at(w, SUM, REV);
+    const int64_t b = at.b, h = at.h, hq = at.hq, p0 = at.p0, t_begin = at.t_begin, t_end = at.t_end;
     const int64_t len = row_length(a, b);
     const int chunks = (int)((t_end - t_begin + C - 1) / C);
     char *K = sm + L::k, *V = sm + L::v;
@@ -442,7 +560,7 @@ __global__ void __launch_bounds__(256, 2) k_tc_state(const __grid_constant__ TcW
         mbar_init(&s_m, 1);
         fence_proxy_async_smem();
     }
-    if (warp == 0) tmem_alloc(&s_tm, 64);
+    if (warp == 0) tmem_alloc(&s_tm, 256);
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tm;
@@ -456,13 +574,8 @@ __global__ void __launch_bounds__(256, 2) k_tc_state(const __grid_constant__ TcW
         tma_load_4d(V, REV ? &w.maps.dy : &w.maps.v, (int)p0, (int)h, (int)t0, (int)b, &s_ld);
     };
     if (tid == 0) load(start_of(0));
-    float X[16 * NB];
-    {
-        const float* from = nullptr;
-        if (!SUM && w.plan.K > 1) from = w.seg_state + ((b * a.H + h) * w.plan.K + seg) * a.N * a.P;
-        else if (!SUM && w.init) from = w.init + (b * a.H + h) * a.N * a.P;
-        load_state<NB>(from, a, p0, X);
-    }
+    float X[32 * NB];
+    load_state<NB>(SUM ? StateTile{nullptr, 0, 0, 0} : at.start(w), X);
     float total = 0.0f, g = load_g(a, b, h, start_of(0), valid(start_of(0)));
     bool ok = true;
     int ch = 0;
@@ -471,53 +584,52 @@ __global__ void __launch_bounds__(256, 2) k_tc_state(const __grid_constant__ TcW
         const int nv = valid(t0);
         if (!SUM) {
             float s = 1.0f;
-            if (kF16<T>) s = f16_scale(block_max(state_max<NB>(X), s_red));
-            put_state<T, NB>(W[0], W[1], s, X);
+            if (kF16<T>) s = f16_scale(group_max(state_max<NB>(X), s_red, 1));
+            put_state2<T, NB>(W[0], W[1], s, X);
             fence_proxy_async_smem();
             __syncthreads();
             if (tid == 0) {
-                const int64_t at = ((b * a.H + h) * ptiles + pt) * w.chunks + t0 / C;
-                char* to = static_cast<char*>(w.images) + at * (2 * NB * 8192);
+                const int64_t image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + t0 / C;
+                char* to = static_cast<char*>(w.images) + image * (2 * NB * 8192);
                 bulk_store(to, W[0], NB * 8192);
                 bulk_store(to + NB * 8192, W[1], NB * 8192);
                 bulk_commit();
-                if (kF16<T>) w.image_scale[at] = s;
+                if (kF16<T>) w.image_scale[image] = s;
                 bulk_wait_read();
             }
         }
-        const float rel = chunk_decays(s_d, g);
+        const float rel = chunk_decays(nullptr, s_total, g);
         if (ch + 1 < chunks) g = load_g(a, b, h, start_of(ch + 1), valid(start_of(ch + 1)));
         ok = mbar_wait(&s_ld, ch & 1);
         if (ok && tok >= nv && t0 + tok < a.L) {
             if (NB == 2) {
                 char* const t[3] = {K, V, K + 16384};
-                clear_row<3>(t, tok, half);
+                clear_row<3>(t, tok);
             } else {
                 char* const t[2] = {K, V};
-                clear_row<2>(t, tok, half);
+                clear_row<2>(t, tok);
             }
             fence_proxy_async_smem();
         }
         if (__syncthreads_or(!ok)) break;
         float vs = 1.0f;
-        if (kF16<T>) vs = f16_scale(block_max(row_max<T>(V, tok, half), s_red));
+        if (kF16<T>) vs = f16_scale(group_max(row_max<T>(V, tok), s_red, 1));
         Two end[4];
-        run_ends(s_d, end);
+        run_ends(s_total, end);
         const Two mine = run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3]));
         const float cl = end[3].h + end[3].l;
-        split_row<T>(V, tok, half, vs * ex2(REV ? (mine.h - rel) + mine.l : two_diff(end[3], mine) + rel), W[0], W[1], W[2]);
+        split_row<T>(V, tok, vs * ex2(REV ? (mine.h - rel) + mine.l : two_diff(end[3], mine) + rel), W[0], W[1], W[2]);
         fence_proxy_async_smem();
         __syncthreads();
         if (tid == 0) {
             tc_fence_after();
-            const void* const parts[3] = {W[0], W[1], W[2]};
-            mma_state<T, NB>(tm, K, parts);
+            mma_state_wide<T, NB>(tm, K, W[0]);
             mma_commit(&s_m);
         }
         ok = mbar_wait(&s_m, ch & 1);
         tc_fence_after();
         if (tid == 0 && ok && ch + 1 < chunks) load(start_of(ch + 1));
-        add_product<NB>(tm, ex2(cl), (REV ? a.scale : 1.0f) / vs, X);
+        add_product<NB, kParts<T>>(tm, ex2(cl), (REV ? a.scale : 1.0f) / vs, X);
         total += cl;
         tc_fence_before();
         if (__syncthreads_or(!ok)) break;
@@ -530,35 +642,62 @@ __global__ void __launch_bounds__(256, 2) k_tc_state(const __grid_constant__ TcW
             mbar_wait(&s_m, ch & 1);
         }
     } else if (SUM) {
-        save_state<NB>(w.seg_state + ((b * a.H + h) * w.plan.K + seg) * a.N * a.P, a, p0, X);
-        if (tid == 0 && pt == 0) w.seg_decay[(b * a.H + h) * w.plan.K + seg] = total / kLog2e;
-    } else if (w.last && seg == (REV ? 0 : w.plan.K - 1)) {
-        save_state<NB>(w.last + (b * a.H + h) * a.N * a.P, a, p0, X);
+        save_state<NB>(at.segment(w), X);
+        if (tid == 0) w.seg_decay[at.cut * w.plan.K + at.seg] = total / kLog2e;
+    } else if (w.last && at.ends(w, REV)) {
+        save_state<NB>(at.whole(w, w.last), X);
     }
     if (tid == 0) bulk_wait_all();
     __syncthreads();
-    if (warp == 0) tmem_free(tm, 64);
+    if (warp == 0) tmem_free(tm, 256);
 }
 
-unsigned blocks(const TcWalkArgs& w, int64_t segs) {
-    return (unsigned)(ceil_div(w.a.P, PT) * w.a.H * w.a.Bsz * segs);
+// seg_state: end state of each segment walked from zero -> the state each
+// segment starts from.  One thread per state element; eight segments' states are
+// on their way before the first is folded in.
+__global__ void __launch_bounds__(256) k_tc_carry(TcWalkArgs w, bool reverse) {
+    constexpr int U = 8;
+    const Args& a = w.a;
+    const int64_t K = w.plan.K, tile = a.N * PT, x = (int64_t)blockIdx.x * 256 + threadIdx.x, cut = blockIdx.y;
+    if (x >= tile) return;
+    const int64_t ptiles = (a.P + PT - 1) / PT, unit = w.plan.whole + cut;
+    const int64_t n = x / PT, p = unit % ptiles * PT + x % PT;
+    float S = w.init && p < a.P ? w.init[(unit / ptiles * a.N + n) * a.P + p] : 0.0f;
+    for (int64_t i0 = 0; i0 < K; i0 += U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + u, s = cut * K + (reverse ? K - 1 - i : i);
+            own[u] = d[u] = 0.0f;
+            if (i + 1 < K) {  // the segment walked last has no sum
+                own[u] = w.seg_state[s * tile + x];
+                d[u] = expf(w.seg_decay[s]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + u, s = cut * K + (reverse ? K - 1 - i : i);
+            if (i < K) w.seg_state[s * tile + x] = S;
+            S = fmaf(d[u], S, own[u]);
+        }
+    }
 }
 
-template <typename K> cudaError_t go(K kernel, int smem, unsigned grid, const TcWalkArgs& w, cudaStream_t st) {
+template <typename K> cudaError_t go(K kernel, int threads, int smem, unsigned grid, const TcWalkArgs& w, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, 256, smem, st>>>(w);
+    kernel<<<grid, threads, smem, st>>>(w);
     return cudaGetLastError();
 }
 
 template <typename T, int NB> cudaError_t fwd_n(const TcWalkArgs& w, cudaStream_t st) {
-    return go(k_tc_fwd<T, NB>, FwdSmem<NB>::total, blocks(w, w.plan.K), w, st);
+    return go(k_tc_fwd<T, NB>, 256, FwdSmem<NB>::total, (unsigned)w.plan.blocks(), w, st);
 }
 template <typename T, int NB> cudaError_t state_n(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st) {
-    const unsigned grid = blocks(w, sum ? w.plan.K - 1 : w.plan.K);
+    const unsigned grid = (unsigned)(sum ? w.plan.cut * (w.plan.K - 1) : w.plan.blocks());
     constexpr int smem = StateSmem<NB>::total;
-    if (reverse) return sum ? go(k_tc_state<T, NB, true, true>, smem, grid, w, st) : go(k_tc_state<T, NB, true, false>, smem, grid, w, st);
-    return sum ? go(k_tc_state<T, NB, false, true>, smem, grid, w, st) : go(k_tc_state<T, NB, false, false>, smem, grid, w, st);
+    if (reverse) return sum ? go(k_tc_state<T, NB, true, true>, 128, smem, grid, w, st) : go(k_tc_state<T, NB, true, false>, 128, smem, grid, w, st);
+    return sum ? go(k_tc_state<T, NB, false, true>, 128, smem, grid, w, st) : go(k_tc_state<T, NB, false, false>, 128, smem, grid, w, st);
 }
 
 }  // namespace
@@ -567,6 +706,12 @@ cudaError_t launch_tc_fwd(const TcWalkArgs& w, cudaStream_t st) {
     const bool wide = w.a.N > 64;
     if (w.a.dtype == 1) return wide ? fwd_n<__half, 2>(w, st) : fwd_n<__half, 1>(w, st);
     return wide ? fwd_n<__nv_bfloat16, 2>(w, st) : fwd_n<__nv_bfloat16, 1>(w, st);
+}
+
+cudaError_t launch_tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st) {
+    // cut < 2 * kSms blocks in y
+    k_tc_carry<<<dim3((unsigned)ceil_div(w.a.N * PT, 256), (unsigned)w.plan.cut), 256, 0, st>>>(w, reverse);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_tc_state(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st) {
