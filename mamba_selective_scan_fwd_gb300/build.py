@@ -26,7 +26,7 @@ SOURCES = ["api.cu", "dispatch.cu", "fwd_f32.cu", "fwd_bf16.cu", "fwd_f16.cu", "
            "bwd_bf16.cu", "bwd_f16.cu", "decode.cu", "fwd_noalloc.cu", "probe.cu"]
 # linear attention and its output norm (include/ss_la.h): kernels of their own, in
 # a folder of their own, outside source_digest() (which identifies the scan's kernels)
-LM_SOURCES = ["lm/la_api.cu", "lm/la_f32.cu", "lm/la_tc_fwd.cu", "lm/la_step.cu", "lm/gnorm.cu"]
+LM_SOURCES = ["lm/la_api.cu", "lm/la_f32.cu", "lm/la_tc_fwd.cu", "lm/la_tc_bwd.cu", "lm/la_step.cu", "lm/gnorm.cu"]
 
 
 def nvcc() -> str:

@@ -162,6 +162,100 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     return launch_tc_fwd(w, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
+struct BwdTc {
+    WalkTc walk;
+    int64_t chunks;
+    int splits;
+    size_t before, after, dq, dk, dg, rows;
+};
+BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
+    BwdTc b;
+    b.walk = walktc_layout(l, Bsz, L, H, N, P);
+    b.chunks = ceil_div(L, kChunkTc);
+    b.splits = tc_splits(Bsz * b.chunks * G, H / G);
+    const size_t images = (size_t)Bsz * H * ceil_div(P, kTileP) * b.chunks * (N > 64 ? 2 : 1) * 16384;
+    b.before = l.take(images);
+    b.after = l.take(images);
+    const size_t part = b.splits > 1 ? (size_t)b.splits * Bsz * L * G * N * 4 : 0;
+    b.dq = l.take(part);
+    b.dk = l.take(part);
+    b.dg = l.take((size_t)Bsz * L * H * 4);
+    b.rows = l.take((size_t)kDgParts * H * 4);
+    return b;
+}
+
+// What follows the chunk kernels of both paths: the parts' sums.
+int bwd_sums(const ss_la_bwd_desc& d, int splits, const float* dq_part, const float* dk_part, const float* dg, float* rows,
+             cudaStream_t st) {
+    if (splits > 1) {
+        const int64_t n = d.Bsz * d.L * d.G * d.N;
+        if (launch_sum_parts(dq_part, d.dq, splits, n, d.dtype, st) != cudaSuccess ||
+            launch_sum_parts(dk_part, d.dk, splits, n, d.dtype, st) != cudaSuccess)
+            return SS_ERR_CUDA;
+    }
+    if (d.g_per_head && launch_sum_rows(dg, rows, d.dg, d.Bsz * d.L, d.H, st) != cudaSuccess) return SS_ERR_CUDA;
+    return SS_OK;
+}
+
+// Whether the backward of these sizes may run on the tensor cores.
+bool tc_bwd_sizes(int64_t L, int64_t N, int64_t P, int dtype) { return tc_sizes(L, N, P, dtype) && dtype == SS_BF16; }
+
+// Backward on the tensor cores; *ran tells whether the inputs allow it.
+int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* ran) {
+    *ran = false;
+    if (!tc_bwd_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) ||
+        !tc_input(a.v, a.L, a.Bsz) || !tc_input(a.dy, a.L, a.Bsz))
+        return SS_OK;
+    const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!encode) return SS_OK;
+    TcWalkArgs w = {};
+    TcBwdArgs b = {};
+    const In dq = {d.dq, a.G * a.N, a.L * a.G * a.N}, dk = {d.dk, a.G * a.N, a.L * a.G * a.N},
+             dv = {d.dv, a.H * a.P, a.L * a.H * a.P};
+    if (!tc_map(encode, &b.maps.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.dy, a.dy, a.H, a.P, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.dq, dq, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.dk, dk, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.dv, dv, a.H, a.P, a.L, a.Bsz, a.dtype))
+        return SS_OK;
+    const int rc = device_status_word(&w.status);
+    if (rc != SS_OK) return rc;
+    char* ws = static_cast<char*>(d.workspace);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    Layout l;
+    const BwdTc bl = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
+    *ran = true;
+    w.maps.q = b.maps.q;
+    w.maps.k = b.maps.k;
+    w.maps.v = b.maps.v;
+    w.maps.dy = b.maps.dy;
+    w.a = a;
+    w.plan = bl.walk.plan;
+    w.seg_state = f32(bl.walk.state);
+    w.seg_decay = f32(bl.walk.decay);
+    w.chunks = bl.chunks;
+    w.init = a.h0;
+    w.images = ws + bl.before;
+    if (tc_carry(w, false, st) != cudaSuccess || launch_tc_state(w, false, false, st) != cudaSuccess) return SS_ERR_CUDA;
+    w.init = a.dlast;
+    w.images = ws + bl.after;
+    w.last = d.dh0;
+    if (tc_carry(w, true, st) != cudaSuccess || launch_tc_state(w, true, false, st) != cudaSuccess) return SS_ERR_CUDA;
+    b.a = a;
+    b.before = ws + bl.before;
+    b.after = ws + bl.after;
+    b.chunks = bl.chunks;
+    b.dg = a.g_per_head ? f32(bl.dg) : d.dg;
+    b.dq_part = f32(bl.dq);
+    b.dk_part = f32(bl.dk);
+    b.splits = bl.splits;
+    b.status = w.status;
+    if (launch_tc_bwd(b, st) != cudaSuccess) return SS_ERR_CUDA;
+    return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
+}
+
 bool empty(int64_t Bsz, int64_t L) { return Bsz == 0 || L == 0; }
 
 // The state that no token changes: a copy of the incoming one, or zeros.
@@ -241,9 +335,10 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
 
 size_t ss_la_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
-    Layout l;
+    Layout l, t;
     bwd32_layout(l, Bsz, L, H, G, N, P);
-    return l.total;
+    if (tc_bwd_sizes(L, N, P, dtype)) bwdtc_layout(t, Bsz, L, H, G, N, P);
+    return l.total > t.total ? l.total : t.total;
 }
 
 int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
@@ -281,6 +376,9 @@ int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
     a.scale = d->scale;
     a.dtype = d->dtype;
     a.g_per_head = d->g_per_head ? 1 : 0;
+    bool ran;
+    const int tc = tc_backward(a, *d, st, &ran);
+    if (ran || tc != SS_OK) return tc;
     char* ws = static_cast<char*>(d->workspace);
     Layout l;
     const Bwd32 bl = bwd32_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
@@ -309,15 +407,7 @@ int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
     b.dk_part = f32(bl.dk);
     b.splits = bl.splits;
     if (launch_bwd32(b, st) != cudaSuccess) return SS_ERR_CUDA;
-    if (b.splits > 1) {
-        const int64_t n = a.Bsz * a.L * a.G * a.N;
-        if (launch_sum_parts(b.dq_part, d->dq, b.splits, n, a.dtype, st) != cudaSuccess ||
-            launch_sum_parts(b.dk_part, d->dk, b.splits, n, a.dtype, st) != cudaSuccess)
-            return SS_ERR_CUDA;
-    }
-    if (a.g_per_head && launch_sum_rows(b.dg, f32(bl.rows), d->dg, a.Bsz * a.L, a.H, st) != cudaSuccess)
-        return SS_ERR_CUDA;
-    return SS_OK;
+    return bwd_sums(*d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
 }
 
 int ss_la_step(const ss_la_step_desc* d, void* stream) {

@@ -12,7 +12,7 @@ constexpr int kTileP = 64;     // value channels per block
 
 // 4-D maps {width, heads, L, Bsz}, boxes of 64 columns x 128 tokens.
 struct TcMaps {
-    CUtensorMap q, k, v, dy, y, dv;
+    CUtensorMap q, k, v, dy, y;
 };
 
 // How a walk over units (batch row, head, 64 value channels; in this order, the
@@ -58,6 +58,38 @@ struct TcWalkArgs {
     int64_t chunks;
     int* status;
 };
+
+// Parts the heads of a group are divided into in the backward, which runs one
+// block per SM: the fewest rounds of blocks times heads per block (each part
+// beyond the first costs an f32 copy of dq and dk, about a tenth of a head).
+inline int tc_splits(int64_t items, int64_t rep) {
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= rep && s <= 64; s++) {
+        const double cost = (double)ceil_div(items * s, kSms) * ceil_div(rep, s) + (s > 1 ? 0.5 + 0.1 * s : 0.0);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+struct TcBwdMaps {
+    CUtensorMap q, k, v, dy, dq, dk, dv;
+};
+
+struct TcBwdArgs {
+    TcBwdMaps maps;
+    Args a;
+    const void *before, *after;  // images of H and R (as TcWalkArgs::images)
+    int64_t chunks;
+    float* dg;                 // [Bsz, L, H]
+    float *dq_part, *dk_part;  // [splits, Bsz, L, G, N] f32 when splits > 1
+    int splits;
+    int* status;
+};
+cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st);
 
 cudaError_t launch_tc_fwd(const TcWalkArgs& w, cudaStream_t st);
 cudaError_t launch_tc_state(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st);
