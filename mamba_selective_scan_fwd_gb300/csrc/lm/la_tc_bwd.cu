@@ -43,39 +43,121 @@ __device__ __forceinline__ float column_sums(float (&x)[32]) {
     return x[0];
 }
 
-// 32 values of a tile's row (units 4 half .. 4 half + 3) as pairs
-__device__ __forceinline__ void read_row(void* tile, int row, int half, uint32_t (&x)[16]) {
+// 16 values of a tile's row (units 2 quarter, + 1) as pairs
+__device__ __forceinline__ void read_row(void* tile, int row, int quarter, uint32_t (&x)[8]) {
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-        const uint4 t = *unit(tile, row, 4 * half + u);
+    for (int u = 0; u < 2; u++) {
+        const uint4 t = *unit(tile, row, 2 * quarter + u);
         x[4 * u] = t.x;
         x[4 * u + 1] = t.y;
         x[4 * u + 2] = t.z;
         x[4 * u + 3] = t.w;
     }
 }
-__device__ __forceinline__ void write_row(void* tile, int row, int half, const uint32_t (&x)[16]) {
+__device__ __forceinline__ void write_row(void* tile, int row, int quarter, const uint32_t (&x)[8]) {
 #pragma unroll
-    for (int u = 0; u < 4; u++)
-        *unit(tile, row, 4 * half + u) = make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+    for (int u = 0; u < 2; u++)
+        *unit(tile, row, 2 * quarter + u) = make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
 }
 
-template <typename T, int NB> __global__ void __launch_bounds__(256, 1) k_tc_bwd(const __grid_constant__ TcBwdArgs w) {
+// A chunk's decays for the compute warps, by runs of 32 tokens; c: log2 decay up
+// to and with the token.
+struct Decays {
+    float c[C];     // c since the run's start
+    float head[C];  // 2^ of it
+    float tail[C];  // 2^(run's end - c)
+    float up[C];    // scale 2^c
+    float down[C];  // 2^(chunk's end - c)
+    float skip[3];  // 2^ from the end of run r to the start of run cb: (r, cb) = (0, 2), (1, 3), (0, 3)
+    float all;      // over the chunk
+};
+
+// One warp; g: log decays of tokens 4 lane .. 4 lane + 3.
+__device__ __forceinline__ void put_decays(Decays& d, const float (&g)[4], float scale) {
+    const int lane = threadIdx.x & 31;
+    float x[4];
+    Two c[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] = clamp_g(g[e]) * kLog2e;
+    warp_cumsum<4>(x, c);
+    const auto at = [&](int l) { return Two{__shfl_sync(kFull, c[3].h, l), __shfl_sync(kFull, c[3].l, l)}; };
+    const Two end = at(lane | 7), e0 = at(7), e1 = at(15), e2 = at(23), cl = at(31);
+    const Two start = lane < 8 ? Two{0.0f, 0.0f} : (lane < 16 ? e0 : (lane < 24 ? e1 : e2));
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const int t = 4 * lane + e;
+        const float in = two_diff(c[e], start);
+        d.c[t] = in;
+        d.head[t] = ex2a(in);
+        d.tail[t] = ex2a(two_diff(end, c[e]));
+        d.up[t] = scale * ex2a(c[e].h + c[e].l);
+        d.down[t] = ex2a(two_diff(cl, c[e]));
+    }
+    if (lane == 0) {
+        d.skip[0] = ex2a(two_diff(e1, e0));
+        d.skip[1] = ex2a(two_diff(e2, e1));
+        d.skip[2] = ex2a(two_diff(e2, e0));
+        d.all = ex2a(cl.h + cl.l);
+    }
+}
+
+// Where a block is: items blockIdx.x, + gridDim.x, ...; in each the heads h_lo ..
+// h_hi - 1 of one group, their value tiles.
+struct Place {
+    int64_t item;
+    int b, chunk, gq, split, h, h_lo, h_hi, pt;
+    int first, last, more;  // of its item's heads and tiles; whether another place follows
+
+    __device__ void mark(const TcBwdArgs& w, int ptiles, int64_t items) {
+        first = h == h_lo && pt == 0;
+        last = h + 1 == h_hi && pt + 1 == ptiles;
+        more = !last || item + gridDim.x < items;
+    }
+    __device__ void begin(const TcBwdArgs& w) {
+        const int rep = (int)(w.a.H / w.a.G);
+        int64_t id = item;
+        split = (int)(id % w.splits);
+        id /= w.splits;
+        gq = (int)(id % w.a.G);
+        id /= w.a.G;
+        chunk = (int)(id % w.chunks);
+        b = (int)(id / w.chunks);
+        h_lo = gq * rep + rep * split / w.splits;
+        h_hi = gq * rep + rep * (split + 1) / w.splits;
+        h = h_lo;
+        pt = 0;
+    }
+    __device__ void step(const TcBwdArgs& w, int ptiles, int64_t items) {  // if more
+        if (++pt == ptiles) {
+            pt = 0;
+            if (++h == h_hi) {
+                item += gridDim.x;
+                begin(w);
+            }
+        }
+        mark(w, ptiles, items);
+    }
+};
+
+// 16 compute warps (thread: row tok of every tile, a quarter of its columns)
+// and a warp that issues the copies and products and adds up dg.
+constexpr int kCompute = 512, kThreads = kCompute + 32;
+
+template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_tc_bwd(const __grid_constant__ TcBwdArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = BwdSmem<NB>;
     constexpr int NP = NB * 64;
-    __shared__ __align__(16) Two s_c[C];
-    __shared__ __align__(16) float s_head[C];
-    __shared__ float s_row[4][C], s_a[2][C], s_b[2][C], s_red[8];
-    __shared__ Two s_end[4];
+    __shared__ Decays s_decays[2];  // of iteration it at it & 1
+    __shared__ float s_row[4][C], s_a[4][C], s_b[4][C], s_red[16];
     // copies: v, dy (and q, k); states.  Products: S, D; dv, k R, q H; dq, dk
     __shared__ __align__(8) uint64_t s_ld, s_st, s_m1, s_m2, s_m3;
     __shared__ uint32_t s_tm;
+    __shared__ Place s_at[3];  // of iteration it at it % 3, the next one's too
     const Args& a = w.a;
-    const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, half = tid >> 7;
+    const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, quarter = tid >> 7;
     char *Q = sm + L::q, *K = sm + L::k, *V = sm + L::v, *DY = sm + L::dy, *H = sm + L::h, *R = sm + L::r, *E = sm + L::e,
          *DS = sm + L::ds;
-    const int64_t rep = a.H / a.G, ptiles = (a.P + PT - 1) / PT;
+    const int ptiles = (int)((a.P + PT - 1) / PT);
     const int64_t items = a.Bsz * w.chunks * a.G * w.splits;
 
     if (tid == 0) {
@@ -85,6 +167,11 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 1) k_tc_bwd
         mbar_init(&s_m2, 1);
         mbar_init(&s_m3, 1);
         fence_proxy_async_smem();
+        Place p;
+        p.item = blockIdx.x;
+        p.begin(w);
+        p.mark(w, ptiles, items);
+        s_at[0] = p;
     }
     if (tid < 32) tmem_alloc(&s_tm, 512);
     __syncthreads();
@@ -93,391 +180,368 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 1) k_tc_bwd
     // S^T, then P^T and q H in its place; D^T, then dv and k R; dq; dk
     const uint32_t tS = tm, tP = tm, tZ = tm + 64, tD = tm + 128, tV = tm + 128, tF = tm + 192, tQ = tm + 256,
                    tK = tm + 256 + NP;
-
-    // A block's work: items blockIdx.x, + gridDim.x, ...; in each the heads h_lo .. h_hi - 1, their value tiles
-    struct Place {
-        int64_t item, b, chunk, gq, split, h, h_lo, h_hi, pt;
-    };
-    auto begin = [&](Place& p) {
-        int64_t id = p.item;
-        p.split = id % w.splits;
-        id /= w.splits;
-        p.gq = id % a.G;
-        id /= a.G;
-        p.chunk = id % w.chunks;
-        p.b = id / w.chunks;
-        p.h_lo = p.gq * rep + rep * p.split / w.splits;
-        p.h_hi = p.gq * rep + rep * (p.split + 1) / w.splits;
-        p.h = p.h_lo;
-        p.pt = 0;
-    };
-    auto step = [&](Place& p) {  // the next place; false past the last
-        if (++p.pt < ptiles) return true;
-        p.pt = 0;
-        if (++p.h < p.h_hi) return true;
-        p.item += gridDim.x;
-        if (p.item >= items) return false;
-        begin(p);
-        return true;
-    };
-    auto load = [&](const Place& p) {
-        const int t0 = (int)(p.chunk * C);
-        const bool first = p.h == p.h_lo && p.pt == 0;
-        mbar_expect_tx(&s_ld, (first ? 2 * NB + 2 : 2) * 16384);
-        if (first)
-#pragma unroll
-            for (int n = 0; n < NB; n++) {
-                tma_load_4d(K + n * 16384, &w.maps.k, n * 64, (int)p.gq, t0, (int)p.b, &s_ld);
-                tma_load_4d(Q + n * 16384, &w.maps.q, n * 64, (int)p.gq, t0, (int)p.b, &s_ld);
-            }
-        tma_load_4d(V, &w.maps.v, (int)(p.pt * PT), (int)p.h, t0, (int)p.b, &s_ld);
-        tma_load_4d(DY, &w.maps.dy, (int)(p.pt * PT), (int)p.h, t0, (int)p.b, &s_ld);
-        constexpr int bytes = 2 * NB * 8192;
-        const int64_t image = ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk;
-        mbar_expect_tx(&s_st, 2 * bytes);
-        bulk_load(H, static_cast<const char*>(w.before) + image * bytes, bytes, &s_st);
-        bulk_load(R, static_cast<const char*>(w.after) + image * bytes, bytes, &s_st);
-    };
-    Place at;
-    at.item = blockIdx.x;
-    begin(at);
-    if (tid == 0) load(at);
     auto valid = [&](const Place& p) {
-        return (int)max((int64_t)0, min((int64_t)C, row_length(a, p.b) - p.chunk * C));
+        return (int)max((int64_t)0, min((int64_t)C, row_length(a, p.b) - (int64_t)p.chunk * C));
     };
-    auto load_g = [&](const Place& p, int nv) {
-        return tok < nv ? log_decay(a, p.b, p.chunk * C + tok, p.h) * kLog2e : 0.0f;
-    };
-    int nv = valid(at);
-    float g = load_g(at, nv), through = 0.0f;
     bool ok = true, more = true, failed = false;
     uint32_t it = 0;
-    for (; more; it++) {
-        const uint32_t ph = it & 1;
-        const int64_t t0 = at.chunk * C;
-        const bool first = at.h == at.h_lo && at.pt == 0, last = at.h + 1 == at.h_hi && at.pt + 1 == ptiles;
-        Place next = at;
-        more = step(next);
-        // decays: c_i and e^{c_i - (start of its run of 32)}
-        {
-            const float x[1] = {g};
-            Two c[1];
-            warp_cumsum<1>(x, c);
-            if (half == 0) {
-                s_head[tok] = ex2(c[0].h + c[0].l);
-                s_c[tok] = c[0];  // within the run; completed below
-                if (lane == 31) s_end[run] = c[0];
-            }
-        }
-        const int nv_next = more ? valid(next) : 0;
-        if (more) g = load_g(next, nv_next);
-        ok = mbar_wait(&s_ld, ph);
-        if (ok && tok >= nv && t0 + tok < a.L) {  // tokens beyond the row's length
-            const uint32_t zero[16] = {};
-            write_row(V, tok, half, zero);
-            write_row(DY, tok, half, zero);
+
+    if (tid >= kCompute) {  // ---------------- the issuing warp
+        auto load = [&](const Place& p) {
+            const int t0 = p.chunk * C;
+            const bool first = p.first;
+            mbar_expect_tx(&s_ld, (first ? 2 * NB + 2 : 2) * 16384);
             if (first)
 #pragma unroll
                 for (int n = 0; n < NB; n++) {
-                    write_row(Q + n * 16384, tok, half, zero);
-                    write_row(K + n * 16384, tok, half, zero);
+                    tma_load_4d(K + n * 16384, &w.maps.k, n * 64, p.gq, t0, p.b, &s_ld);
+                    tma_load_4d(Q + n * 16384, &w.maps.q, n * 64, p.gq, t0, p.b, &s_ld);
                 }
-        }
-        if (tid == 0) bulk_wait_read();  // the last dv (dq, dk) has left its staging tile
-        tc_fence_before();
-        fence_proxy_async_smem();
-        failed = __syncthreads_or(!ok);
-        if (failed) break;
-        if (tid == 0) {
-            tc_fence_after();
-            constexpr uint32_t d = mma_desc<T>(128, 128, false, false);
-#pragma unroll
-            for (int s = 0; s < 4 * NB; s++) {
-                const uint32_t o = (s >> 2) * 16384 + (s & 3) * 32;
-                mma(tS, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(Q) + o), d, s > 0);
-            }
-#pragma unroll
-            for (int s = 0; s < 4; s++)
-                mma(tD, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(DY) + s * 32), d, s > 0);
-            mma_commit(&s_m1);
-        }
-        Two end[4];
-        end[0] = s_end[0];
-#pragma unroll
-        for (int i = 1; i < 4; i++) end[i] = two_add(end[i - 1], s_end[i]);
-        const Two before = run == 0 ? Two{0.0f, 0.0f} : (run == 1 ? end[0] : (run == 2 ? end[1] : end[2]));
-        const Two mine = run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3]));
-        const Two cj = two_add(before, s_c[tok]);
-        const float up = a.scale * ex2(cj.h + cj.l), down = ex2(two_diff(end[3], cj)), tail = ex2(two_diff(mine, cj));
-        uint32_t vr[16];
-        {
-            uint32_t x[16];
-            read_row(DY, tok, half, x);
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const float2 f = mul2(unpack2<T>(x[i]), splat2(up));
-                x[i] = pack2<T>(f.x, f.y);
-            }
-            write_row(DS, tok, half, x);
-            read_row(V, tok, half, vr);
-        }
-        ok = mbar_wait(&s_m1, ph);
-        tc_fence_after();
-        {
-            uint32_t x[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const float2 f = mul2(unpack2<T>(vr[i]), splat2(down));
-                x[i] = pack2<T>(f.x, f.y);
-            }
-            write_row(V, tok, half, x);
-        }
-        // P, E and W by 32 x 32 blocks: row block `run`, column blocks 0 and 3 (half 0) or 1 and 2 (half 1)
-        uint32_t pr[2][16];
-        float col = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const int cb = k == 0 ? half : 3 - half;
-            uint32_t er[16];
-            if (cb >= run) {
-                float s[32], d[32], wv[32];
-                tmem_ld32(tS + my + 32 * cb, s);
-                tmem_ld32(tD + my + 32 * cb, d);
-                if (cb > run) {
-                    const Two start = cb == 1 ? end[0] : (cb == 2 ? end[1] : end[2]);
-                    const float2 f = splat2(tail * ex2(two_diff(start, mine)));
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(&s_head[32 * cb + j]);
-#pragma unroll
-                        for (int u = 0; u < 2; u++) {
-                            const int i = j + 2 * u;
-                            const float2 m = mul2(f, u == 0 ? make_float2(t.x, t.y) : make_float2(t.z, t.w));
-                            const float2 sv = make_float2(s[i], s[i + 1]);
-                            const float2 p = mul2(m, sv);
-                            const float2 e = mul2(mul2(m, splat2(a.scale)), make_float2(d[i], d[i + 1]));
-                            const float2 x = mul2(e, sv);
-                            pr[k][i / 2] = pack2<T>(p.x, p.y);
-                            er[i / 2] = pack2<T>(e.x, e.y);
-                            wv[i] = x.x;
-                            wv[i + 1] = x.y;
-                        }
-                    }
-                } else {
-                    const Two own = s_c[tok];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float4 c = *reinterpret_cast<const float4*>(&s_c[32 * cb + i]);
-                        const float m0 = i >= lane ? ex2(two_diff({c.x, c.y}, own)) : 0.0f;
-                        const float m1 = i + 1 >= lane ? ex2(two_diff({c.z, c.w}, own)) : 0.0f;
-                        const float e0 = i >= lane ? a.scale * m0 * d[i] : 0.0f;
-                        const float e1 = i + 1 >= lane ? a.scale * m1 * d[i + 1] : 0.0f;
-                        pr[k][i / 2] = pack2<T>(i >= lane ? m0 * s[i] : 0.0f, i + 1 >= lane ? m1 * s[i + 1] : 0.0f);
-                        er[i / 2] = pack2<T>(e0, e1);
-                        wv[i] = i > lane ? e0 * s[i] : 0.0f;
-                        wv[i + 1] = i + 1 > lane ? e1 * s[i + 1] : 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 32; i++) col += wv[i];
-                s_row[run][32 * cb + lane] = column_sums(wv);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; i++) pr[k][i] = er[i] = 0;
-            }
-            // E: row j, columns 32 cb .. + 31 of two 64-column tiles
-#pragma unroll
-            for (int u = 0; u < 4; u++)
-                *unit(E + (cb >> 1) * 16384, tok, (cb & 1) * 4 + u) = make_uint4(er[4 * u], er[4 * u + 1], er[4 * u + 2], er[4 * u + 3]);
-        }
-        tc_fence_before();
-        __syncthreads();  // S and D have been read
-        tc_fence_after();
-        tmem_st16(tP + my + 16 * half, pr[0]);
-        tmem_st16(tP + my + 16 * (3 - half), pr[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        fence_proxy_async_smem();
-        ok = mbar_wait(&s_st, ph) && ok;
-        failed = __syncthreads_or(!ok);
-        if (failed) break;
-        if (tid == 0) {
-            tc_fence_after();
-            constexpr uint32_t dV = mma_desc<T>(128, PT, false, true), dQ = mma_desc<T>(128, NP, true, true),
-                               dQs = mma_desc<T>(128, NP, false, false), dK = mma_desc<T>(128, NP, false, true);
-#pragma unroll
-            for (int s = 0; s < C / 16; s++) mma_ts(tV, tP + 8 * s, smem_desc(smem_addr(DY) + s * 2048), dV, s > 0);
-#pragma unroll
-            for (int s = 0; s < 8 * NB; s++) {  // k R and q H, high and low parts
-                const int n = s % (4 * NB);
-                const uint32_t o = (n >> 2) * 16384 + (n & 3) * 32, st = (s / (4 * NB)) * NB * 8192 + n * 2048;
-                mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(R) + st), dV, s > 0);
-                mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(H) + st), dV, s > 0);
-            }
-            mma_commit(&s_m2);
-#pragma unroll
-            for (int s = 0; s < C / 16; s++) {
-                mma(tQ, smem_desc(smem_addr(E) + s * 2048, 16384), smem_desc(smem_addr(K) + s * 2048, 16384), dQ, !first || s > 0);
-                mma(tK, smem_desc(smem_addr(E) + (s >> 2) * 16384 + (s & 3) * 32), smem_desc(smem_addr(Q) + s * 2048, 16384), dK,
-                    !first || s > 0);
-            }
-#pragma unroll
-            for (int s = 0; s < PT / 16; s++) {
-                mma(tQ, smem_desc(smem_addr(DS) + s * 32), smem_desc(smem_addr(H) + s * 32), dQs, true);
-                mma(tK, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(R) + s * 32), dQs, true);
-            }
-            mma_commit(&s_m3);
-        }
-        // <R, H> of this tile: rows n of both, high + low
-        if (at.pt == 0) through = 0.0f;
-        if (tok < NP) {
-            uint32_t h0[16], h1[16], r0[16], r1[16];
-            read_row(H, tok, half, h0);
-            read_row(H + NB * 8192, tok, half, h1);
-            read_row(R, tok, half, r0);
-            read_row(R + NB * 8192, tok, half, r1);
-            float2 acc = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                acc = fma2(add2(unpack2<T>(h0[i]), unpack2<T>(h1[i])), add2(unpack2<T>(r0[i]), unpack2<T>(r1[i])), acc);
-            through += acc.x + acc.y;
-        }
-        uint32_t dyr[16], dv[16];
-        read_row(DY, tok, half, dyr);
-        ok = mbar_wait(&s_m2, ph);
-        tc_fence_after();
-        {
-            float f[32], x[32];
-            tmem_ld32(tF + my + 32 * half, f);
-            tmem_ld32(tV + my + 32 * half, x);
-            float2 b = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const float2 y = mul2(splat2(down), make_float2(f[2 * i], f[2 * i + 1]));
-                b = fma2(y, unpack2<T>(vr[i]), b);
-                const float2 z = fma2(splat2(a.scale), make_float2(x[2 * i], x[2 * i + 1]), y);
-                dv[i] = pack2<T>(z.x, z.y);
-            }
-            float sb = b.x + b.y + col;
-            tmem_ld32(tZ + my + 32 * half, f);
-            float2 z = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 16; i++) z = fma2(make_float2(f[2 * i], f[2 * i + 1]), unpack2<T>(dyr[i]), z);
-            float sa = up * (z.x + z.y);
-            if (half == 0)  // row_i, from the row blocks up to its own
-                for (int r = 0; r <= run; r++) sb -= s_row[r][tok];
-            if (at.pt > 0) {
-                sa += s_a[half][tok];
-                sb += s_b[half][tok];
-            }
-            s_a[half][tok] = sa;
-            s_b[half][tok] = sb;
-        }
-        ok = mbar_wait(&s_m3, ph) && ok;
-        tc_fence_after();
-        write_row(DS, tok, half, dv);
-        tc_fence_before();
-        fence_proxy_async_smem();
-        float th = through;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) th += __shfl_xor_sync(kFull, th, o);
-        if (lane == 0) s_red[tid >> 5] = th;
-        failed = __syncthreads_or(!ok);
-        if (failed) break;
-        if (tid == 0) {
-            if (more) load(next);
-            tma_store_4d(&w.maps.dv, DS, (int)(at.pt * PT), (int)at.h, (int)t0, (int)at.b);
-            bulk_commit();
-        }
-        if (at.pt + 1 == ptiles && tid >= 224) {  // the last warp: dg of this head, tokens 4 lane .. 4 lane + 3
-            float sum = 0.0f, av[4], bv[4];
-#pragma unroll
-            for (int u = 0; u < 8; u++) sum += s_red[u];
-            sum *= ex2(end[3].h + end[3].l);
-            float A = 0.0f, B = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                av[e] = s_a[0][4 * lane + e] + s_a[1][4 * lane + e];
-                bv[e] = s_b[0][4 * lane + e] + s_b[1][4 * lane + e];
-                A += av[e];
-                B += bv[e];
-            }
-            float suf = A, pre = B;  // inclusive over lanes, from the right and from the left
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_down_sync(kFull, suf, o), y = __shfl_up_sync(kFull, pre, o);
-                if (lane + o < 32) suf += x;
-                if (lane >= o) pre += y;
-            }
-            pre -= B;
-            float before_t = pre;
+            tma_load_4d(V, &w.maps.v, p.pt * PT, p.h, t0, p.b, &s_ld);
+            tma_load_4d(DY, &w.maps.dy, p.pt * PT, p.h, t0, p.b, &s_ld);
+            constexpr int bytes = 2 * NB * 8192;
+            const int64_t image = ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk;
+            mbar_expect_tx(&s_st, 2 * bytes);
+            bulk_load(H, static_cast<const char*>(w.before) + image * bytes, bytes, &s_st);
+            bulk_load(R, static_cast<const char*>(w.after) + image * bytes, bytes, &s_st);
+        };
+        const bool lead = lane == 0;
+        Place at = s_at[0];
+        if (lead) load(at);
+        float g[4];
+        auto raw_g = [&](const Place& p) {
+            const int nv = valid(p);
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 const int t = 4 * lane + e;
-                if (t0 + t < a.L) w.dg[(at.b * a.L + t0 + t) * a.H + at.h] = t < nv ? suf + before_t + sum : 0.0f;
-                suf -= av[e];
-                before_t += bv[e];
+                g[e] = t < nv ? a.g[a.g_per_head ? (int64_t)p.h : ((p.b * a.L + (int64_t)p.chunk * C + t) * a.H + p.h)] : 0.0f;
             }
-        }
-        if (last) {  // dq and dk of the group (or of this part of its heads)
+        };
+        raw_g(at);
+        put_decays(s_decays[0], g, a.scale);
+        for (; more; it++) {
+            const uint32_t ph = it & 1;
+            const bool first = at.first, last = at.last;
+            Place next = at;
+            more = at.more;
+            if (more) {
+                next.step(w, ptiles, items);
+                if (lead) s_at[(it + 1) % 3] = next;
+                raw_g(next);
+            }
+            ok = mbar_wait(&s_ld, ph);
+            failed = __syncthreads_or(!ok);  // A
+            if (failed) break;
+            if (lead) {
+                tc_fence_after();
+                constexpr uint32_t d = mma_desc<T>(128, 128, false, false);
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const uint32_t from = k == 0 ? tQ : tK;
-                if (w.splits > 1) {
-                    float* to = (k == 0 ? w.dq_part : w.dk_part) + at.split * a.Bsz * a.L * a.G * a.N +
-                                ((at.b * a.L + t0 + tok) * a.G + at.gq) * a.N;
+                for (int s = 0; s < 4 * NB; s++) {
+                    const uint32_t o = (s >> 2) * 16384 + (s & 3) * 32;
+                    mma(tS, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(Q) + o), d, s > 0);
+                }
 #pragma unroll
-                    for (int c = 0; c < NB; c++) {
-                        float x[32];
-                        const int n0 = 32 * NB * half + 32 * c;
-                        tmem_ld32(from + my + n0, x);
-                        if (t0 + tok < a.L)
+                for (int s = 0; s < 4; s++)
+                    mma(tD, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(DY) + s * 32), d, s > 0);
+                bulk_wait_read();  // the last dv (dq, dk) has left E
+                mma_commit(&s_m1);
+            }
+            __syncwarp();
+            if (more) put_decays(s_decays[ph ^ 1], g, a.scale);
+            ok = mbar_wait(&s_st, ph);
+            __syncthreads();                 // S and D have been read
+            failed = __syncthreads_or(!ok);  // B
+            if (failed) break;
+            if (lead) {
+                tc_fence_after();
+                constexpr uint32_t dV = mma_desc<T>(128, PT, false, true), dQ = mma_desc<T>(128, NP, true, true),
+                                   dQs = mma_desc<T>(128, NP, false, false), dK = mma_desc<T>(128, NP, false, true);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                if (n0 + i < a.N)
-                                    *reinterpret_cast<float4*>(to + n0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                for (int s = 0; s < C / 16; s++) mma_ts(tV, tP + 8 * s, smem_desc(smem_addr(DY) + s * 2048), dV, s > 0);
+#pragma unroll
+                for (int s = 0; s < 8 * NB; s++) {  // k R and q H, high and low parts
+                    const int n = s % (4 * NB);
+                    const uint32_t o = (n >> 2) * 16384 + (n & 3) * 32, st = (s / (4 * NB)) * NB * 8192 + n * 2048;
+                    mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(R) + st), dV, s > 0);
+                    mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(H) + st), dV, s > 0);
+                }
+                mma_commit(&s_m2);
+#pragma unroll
+                for (int s = 0; s < C / 16; s++) {
+                    mma(tQ, smem_desc(smem_addr(E) + s * 2048, 16384), smem_desc(smem_addr(K) + s * 2048, 16384), dQ,
+                        !first || s > 0);
+                    mma(tK, smem_desc(smem_addr(E) + (s >> 2) * 16384 + (s & 3) * 32), smem_desc(smem_addr(Q) + s * 2048, 16384),
+                        dK, !first || s > 0);
+                }
+#pragma unroll
+                for (int s = 0; s < PT / 16; s++) {
+                    mma(tQ, smem_desc(smem_addr(DS) + s * 32), smem_desc(smem_addr(H) + s * 32), dQs, true);
+                    mma(tK, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(R) + s * 32), dQs, true);
+                }
+                mma_commit(&s_m3);
+            }
+            failed = __syncthreads_or(0);  // C
+            if (failed) break;
+            const int64_t t0 = (int64_t)at.chunk * C;
+            if (lead) {
+                if (more) load(next);
+                tma_store_4d(&w.maps.dv, E, at.pt * PT, at.h, (int)t0, at.b);
+                bulk_commit();
+            }
+            __syncwarp();
+            if (at.pt + 1 == ptiles) {  // dg of this head, tokens 4 lane .. 4 lane + 3
+                const int nv = valid(at);
+                float sum = 0.0f, av[4], bv[4];
+#pragma unroll
+                for (int u = 0; u < 16; u++) sum += s_red[u];
+                float A = 0.0f, B = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int t = 4 * lane + e;
+                    av[e] = (s_a[0][t] + s_a[1][t]) + (s_a[2][t] + s_a[3][t]);
+                    bv[e] = (s_b[0][t] + s_b[1][t]) + (s_b[2][t] + s_b[3][t]);
+                    A += av[e];
+                    B += bv[e];
+                }
+                float suf = A, pre = B;  // inclusive over lanes, from the right and from the left
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float x = __shfl_down_sync(kFull, suf, o), y = __shfl_up_sync(kFull, pre, o);
+                    if (lane + o < 32) suf += x;
+                    if (lane >= o) pre += y;
+                }
+                pre -= B;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int64_t t = 4 * lane + e;
+                    if (t0 + t < a.L) w.dg[(at.b * a.L + t0 + t) * a.H + at.h] = t < nv ? suf + pre + sum : 0.0f;
+                    suf -= av[e];
+                    pre += bv[e];
+                }
+            }
+            if (last && w.splits == 1) {  // dq and dk: see the compute warps
+                for (int k = 0; k < 2; k++) {
+                    if (NB == 2 || k == 0) {
+                        if (lead) bulk_wait_read();
+                        __syncthreads();  // E is free
                     }
-                } else {
-                    // NB == 1: a tile of E for each; NB == 2: E for dq, then for dk
-                    if (NB == 2 && k == 1) {
-                        if (tid == 0) bulk_wait_read();
-                        __syncthreads();
-                    }
-                    char* to = NB == 1 ? E + k * 16384 : E;
-#pragma unroll
-                    for (int c = 0; c < NB; c++) {
-                        float x[32];
-                        const int n0 = 32 * NB * half + 32 * c;
-                        tmem_ld32(from + my + n0, x);
-                        uint32_t r[16];
-#pragma unroll
-                        for (int i = 0; i < 16; i++) r[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
-                        write_row(to + (n0 >> 6) * 16384, tok, (n0 >> 5) & 1, r);
-                    }
-                    fence_proxy_async_smem();
-                    __syncthreads();
-                    if (tid == 0) {
-#pragma unroll
+                    __syncthreads();  // the tile is written
+                    if (lead) {
+                        char* from = NB == 1 ? E + k * 16384 : E;
                         for (int n = 0; n < NB; n++)
-                            tma_store_4d(k == 0 ? &w.maps.dq : &w.maps.dk, to + n * 16384, n * 64, (int)at.gq, (int)t0, (int)at.b);
+                            tma_store_4d(k == 0 ? &w.maps.dq : &w.maps.dk, from + n * 16384, n * 64, at.gq, (int)t0, at.b);
                         bulk_commit();
                     }
                 }
             }
+            at = next;
         }
-        at = next;
-        nv = nv_next;
-    }
-    if (failed) {  // a wait ran out: report, wait for what is in flight (within limits), leave
-        if (tid == 0) {
+        if (failed && lead) {  // a wait ran out: report, wait for what is in flight (within limits)
             atomicOr(w.status, kDevWaitTimeout);
             mbar_wait(&s_ld, it & 1);
             mbar_wait(&s_st, it & 1);
             mbar_wait(&s_m1, it & 1);
             mbar_wait(&s_m3, it & 1);
         }
+        if (lead) bulk_wait_all();
+    } else {  // ---------------- the compute warps
+        float through = 0.0f;
+        for (; more; it++) {
+            const uint32_t ph = it & 1;
+            const Place& at = s_at[it % 3];
+            const Decays& dec = s_decays[ph];
+            const int64_t t0 = (int64_t)at.chunk * C;
+            more = at.more;
+            const int nv = valid(at);
+            ok = mbar_wait(&s_ld, ph);
+            if (ok && tok >= nv && t0 + tok < a.L) {  // tokens beyond the row's length
+                const uint32_t zero[8] = {};
+                write_row(V, tok, quarter, zero);
+                write_row(DY, tok, quarter, zero);
+                if (at.first)
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        write_row(Q + n * 16384, tok, quarter, zero);
+                        write_row(K + n * 16384, tok, quarter, zero);
+                    }
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            failed = __syncthreads_or(!ok);  // A
+            if (failed) break;
+            const float down = dec.down[tok];
+            uint32_t vr[8];
+            read_row(V, tok, quarter, vr);
+            {
+                uint32_t x[8];
+                read_row(DY, tok, quarter, x);
+                const float up = dec.up[tok];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float2 f = mul2(unpack2<T>(x[i]), splat2(up));
+                    x[i] = pack2<T>(f.x, f.y);
+                }
+                write_row(DS, tok, quarter, x);
+            }
+            ok = mbar_wait(&s_m1, ph);
+            tc_fence_after();
+            {
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float2 f = mul2(unpack2<T>(vr[i]), splat2(down));
+                    x[i] = pack2<T>(f.x, f.y);
+                }
+                write_row(V, tok, quarter, x);
+            }
+            // P, E and W by 32 x 32 blocks: rows of `run`, columns of `quarter`
+            uint32_t pr[16], er[16];
+            float col = 0.0f;
+            const int cb = quarter;
+            if (cb >= run) {
+                float s[32], d[32];
+                tmem_ld32(tS + my + 32 * cb, s);
+                tmem_ld32(tD + my + 32 * cb, d);
+                // W keeps its diagonal: it is in a row's sum and in a column's, which dg subtracts
+                if (cb > run) {
+                    const float2 f = splat2(dec.tail[tok] * (cb == run + 1 ? 1.0f : dec.skip[cb - 2 + (cb - run == 3 ? 1 : 0)]));
+                    const float2 fs = mul2(f, splat2(a.scale));
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 t = *reinterpret_cast<const float2*>(&dec.head[32 * cb + j]);
+                        const float2 sv = make_float2(s[j], s[j + 1]);
+                        const float2 p = mul2(mul2(f, t), sv);
+                        const float2 e = mul2(mul2(fs, t), make_float2(d[j], d[j + 1]));
+                        const float2 x = mul2(e, sv);
+                        pr[j / 2] = pack2<T>(p.x, p.y);
+                        er[j / 2] = pack2<T>(e.x, e.y);
+                        s[j] = x.x;
+                        s[j + 1] = x.y;
+                    }
+                } else {
+                    const float own = dec.c[tok];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 c = add2(*reinterpret_cast<const float2*>(&dec.c[32 * cb + j]), splat2(-own));
+                        const float2 m = make_float2(j >= lane ? ex2a(c.x) : 0.0f, j + 1 >= lane ? ex2a(c.y) : 0.0f);
+                        const float2 sv = make_float2(s[j], s[j + 1]);
+                        const float2 p = mul2(m, sv);
+                        const float2 e = mul2(mul2(m, splat2(a.scale)), make_float2(d[j], d[j + 1]));
+                        const float2 x = mul2(e, sv);
+                        pr[j / 2] = pack2<T>(p.x, p.y);
+                        er[j / 2] = pack2<T>(e.x, e.y);
+                        s[j] = x.x;
+                        s[j + 1] = x.y;
+                    }
+                }
+                float2 sum = make_float2(s[0], s[1]);
+#pragma unroll
+                for (int i = 2; i < 32; i += 2) sum = add2(sum, make_float2(s[i], s[i + 1]));
+                col = sum.x + sum.y;
+                s_row[run][32 * cb + lane] = column_sums(s);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; i++) pr[i] = er[i] = 0;
+            }
+            // E: row j, columns 32 cb .. + 31 of two 64-column tiles
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                *unit(E + (cb >> 1) * 16384, tok, (cb & 1) * 4 + u) = make_uint4(er[4 * u], er[4 * u + 1], er[4 * u + 2], er[4 * u + 3]);
+            tc_fence_before();
+            __syncthreads();  // S and D have been read
+            tc_fence_after();
+            tmem_st16(tP + my + 16 * cb, pr);
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            ok = mbar_wait(&s_st, ph) && ok;
+            failed = __syncthreads_or(!ok);  // B
+            if (failed) break;
+            // <R, H> of this tile: rows n of both, high + low
+            if (at.pt == 0) through = 0.0f;
+            if (tok < NP) {
+                uint32_t h0[8], h1[8], r0[8], r1[8];
+                read_row(H, tok, quarter, h0);
+                read_row(H + NB * 8192, tok, quarter, h1);
+                read_row(R, tok, quarter, r0);
+                read_row(R + NB * 8192, tok, quarter, r1);
+                float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    acc = fma2(add2(unpack2<T>(h0[i]), unpack2<T>(h1[i])), add2(unpack2<T>(r0[i]), unpack2<T>(r1[i])), acc);
+                through += acc.x + acc.y;
+            }
+            float th = through;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) th += __shfl_xor_sync(kFull, th, o);
+            if (lane == 0) s_red[tid >> 5] = th * dec.all;
+            uint32_t dyr[8], dv[8];
+            read_row(DY, tok, quarter, dyr);
+            ok = mbar_wait(&s_m2, ph);
+            tc_fence_after();
+            {
+                float f[16], x[16], zz[16];
+                tmem_ld16(tF + my + 16 * quarter, f);
+                tmem_ld16(tV + my + 16 * quarter, x);
+                tmem_ld16(tZ + my + 16 * quarter, zz);
+                float2 b = make_float2(0.0f, 0.0f), z = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float2 y = mul2(splat2(down), make_float2(f[2 * i], f[2 * i + 1]));
+                    b = fma2(y, unpack2<T>(vr[i]), b);
+                    z = fma2(make_float2(zz[2 * i], zz[2 * i + 1]), unpack2<T>(dyr[i]), z);
+                    const float2 o = fma2(splat2(a.scale), make_float2(x[2 * i], x[2 * i + 1]), y);
+                    dv[i] = pack2<T>(o.x, o.y);
+                }
+                float sa = dec.up[tok] * (z.x + z.y), sb = b.x + b.y + col;
+                if (quarter <= run) sb -= s_row[quarter][tok];  // row_i, one row block each
+                if (at.pt > 0) {
+                    sa += s_a[quarter][tok];
+                    sb += s_b[quarter][tok];
+                }
+                s_a[quarter][tok] = sa;
+                s_b[quarter][tok] = sb;
+            }
+            ok = mbar_wait(&s_m3, ph) && ok;
+            tc_fence_after();
+            write_row(E, tok, quarter, dv);
+            tc_fence_before();
+            fence_proxy_async_smem();
+            failed = __syncthreads_or(!ok);  // C
+            if (failed) break;
+            if (at.last) {  // dq and dk of the group (or of this part of its heads)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const uint32_t from = k == 0 ? tQ : tK;
+                    float* part = (k == 0 ? w.dq_part : w.dk_part) + at.split * a.Bsz * a.L * a.G * a.N +
+                                  ((at.b * a.L + t0 + tok) * a.G + at.gq) * a.N;
+                    char* to = NB == 1 ? E + k * 16384 : E;  // NB == 2: E for dq, then for dk
+                    if (w.splits == 1 && (NB == 2 || k == 0)) __syncthreads();
+#pragma unroll
+                    for (int c = 0; c < NB; c++) {
+                        float x[16];
+                        const int n0 = 16 * NB * quarter + 16 * c;
+                        tmem_ld16(from + my + n0, x);
+                        if (w.splits == 1) {
+                            uint32_t r[8];
+#pragma unroll
+                            for (int i = 0; i < 8; i++) r[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+                            write_row(to + (n0 >> 6) * 16384, tok, (n0 >> 4) & 3, r);
+                        } else if (t0 + tok < a.L) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                if (n0 + i < a.N)
+                                    *reinterpret_cast<float4*>(part + n0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        }
+                    }
+                    if (w.splits == 1) {
+                        fence_proxy_async_smem();
+                        __syncthreads();
+                    }
+                }
+            }
+        }
     }
-    if (tid == 0) bulk_wait_all();
     tc_fence_before();
     __syncthreads();
     if (tid < 32) tmem_free(tm, 512);
@@ -488,7 +552,7 @@ template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t
     const cudaError_t e = cudaFuncSetAttribute(k_tc_bwd<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t items = w.a.Bsz * w.chunks * w.a.G * w.splits;
-    k_tc_bwd<T, NB><<<(unsigned)(items < kSms ? items : kSms), 256, smem, st>>>(w);
+    k_tc_bwd<T, NB><<<(unsigned)(items < kSms ? items : kSms), kThreads, smem, st>>>(w);
     return cudaGetLastError();
 }
 

@@ -33,11 +33,11 @@ template <typename T> constexpr int kParts = kF16<T> ? 2 : 3;
 // The chunk's decays, by runs of 32 tokens (one warp's): c_i = (the run's end) -
 // rel_i with rel a thread's own.  Shared: tail = e^{rel} (where wanted) and the
 // log2 decay of each run.
-// A warpgroup (token = tid % 128), x: the token's log2 decay.  Returns rel (at
+// A warpgroup (token = tid % 128), g: the token's log decay.  Returns rel (at
 // most 0 for decays).
-__device__ __forceinline__ float chunk_decays(float* tail, Two* total, float x) {
+__device__ __forceinline__ float chunk_decays(float* tail, Two* total, float g) {
     const int tok = threadIdx.x & (C - 1);
-    const float in[1] = {x};
+    const float in[1] = {clamp_g(g) * kLog2e};
     Two c[1];
     warp_cumsum<1>(in, c);
     const Two end = {__shfl_sync(kFull, c[0].h, 31), __shfl_sync(kFull, c[0].l, 31)};
@@ -52,9 +52,10 @@ __device__ __forceinline__ void run_ends(const Two* total, Two (&end)[4]) {
 #pragma unroll
     for (int i = 1; i < 4; i++) end[i] = two_add(end[i - 1], total[i]);
 }
+// The token's log decay as it is in memory: nothing waits for it until it is used.
 __device__ __forceinline__ float load_g(const Args& a, int64_t b, int64_t h, int64_t t0, int nv) {
     const int t = threadIdx.x & (C - 1);
-    return t < nv ? log_decay(a, b, t0 + t, h) * kLog2e : 0.0f;
+    return t < nv ? a.g[a.g_per_head ? h : (b * a.L + t0 + t) * a.H + h] : 0.0f;
 }
 
 // Barrier of one warpgroup (128 threads): id 1 or 2.
