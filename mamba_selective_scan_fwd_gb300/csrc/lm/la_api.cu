@@ -117,9 +117,9 @@ struct WalkTc {
     TcPlan plan;
     size_t state, decay;
 };
-WalkTc walktc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P) {
+WalkTc walktc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int64_t slots) {
     WalkTc w;
-    w.plan = tc_plan(Bsz * H * ceil_div(P, kTileP), L);
+    w.plan = tc_plan(Bsz * H * ceil_div(P, kTileP), L, slots);
     w.state = l.take((size_t)w.plan.cut * w.plan.K * N * kTileP * 4);
     w.decay = l.take((size_t)w.plan.cut * w.plan.K * 4);
     return w;
@@ -150,7 +150,7 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     const int rc = device_status_word(&w.status);
     if (rc != SS_OK) return rc;
     Layout l;
-    const WalkTc wl = walktc_layout(l, a.Bsz, a.L, a.H, a.N, a.P);
+    const WalkTc wl = walktc_layout(l, a.Bsz, a.L, a.H, a.N, a.P, 2 * kSms);
     w.a = a;
     w.plan = wl.plan;
     w.init = a.h0;
@@ -170,7 +170,7 @@ struct BwdTc {
 };
 BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     BwdTc b;
-    b.walk = walktc_layout(l, Bsz, L, H, N, P);
+    b.walk = walktc_layout(l, Bsz, L, H, N, P, kSms);
     b.chunks = ceil_div(L, kChunkTc);
     b.splits = tc_splits(Bsz * b.chunks * G, H / G);
     const size_t images = (size_t)Bsz * H * ceil_div(P, kTileP) * b.chunks * (N > 64 ? 2 : 1) * 16384;
@@ -288,7 +288,7 @@ size_t ss_la_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, i
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
     Layout l, t;
     walk32_layout(l, Bsz, L, H, N, P);
-    if (tc_sizes(L, N, P, dtype)) walktc_layout(t, Bsz, L, H, N, P);
+    if (tc_sizes(L, N, P, dtype)) walktc_layout(t, Bsz, L, H, N, P, 2 * kSms);
     return l.total > t.total ? l.total : t.total;  // either path may run: strides and pointers decide
 }
 

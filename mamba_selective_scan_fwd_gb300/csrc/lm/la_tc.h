@@ -24,12 +24,13 @@ struct TcPlan {
     int64_t blocks() const { return whole + cut * K; }
 };
 
-// Two blocks run on an SM: full rounds of whole units, and the last partial
-// round cut so that it fills the SMs, where that costs less than running it
-// uncut.  Costs in chunks' time: a round of blocks, half as much for the sum
-// pass, 3 for the two launches that cutting adds.
-inline TcPlan tc_plan(int64_t units, int64_t L) {
-    const int64_t chunks = ceil_div(L, kChunkTc), slots = 2 * kSms, rest = units % slots;
+// slots: blocks that run at once (two on an SM in the forward, one in the
+// state walk).  Full rounds of whole units, and the last partial round cut so
+// that it fills the SMs, where that costs less than running it uncut.  Costs in
+// chunks' time: a round of blocks, half as much for the sum pass, 3 for the two
+// launches that cutting adds.
+inline TcPlan tc_plan(int64_t units, int64_t L, int64_t slots) {
+    const int64_t chunks = ceil_div(L, kChunkTc), rest = units % slots;
     TcPlan best = {units, 0, 1, chunks * kChunkTc};
     if (rest == 0) return best;
     double least = (double)chunks;

@@ -58,7 +58,7 @@ __device__ __forceinline__ float load_g(const Args& a, int64_t b, int64_t h, int
     return t < nv ? a.g[a.g_per_head ? h : (b * a.L + t0 + t) * a.H + h] : 0.0f;
 }
 
-// Barrier of one warpgroup (128 threads): id 1 or 2.
+// Barrier of one warpgroup (128 threads): id 1, 2 or 3.
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Largest value of a warpgroup's threads (all get it); v >= 0.  Two barriers.
@@ -78,19 +78,20 @@ __device__ __forceinline__ float group_max(float v, uint32_t* red, int id) {
 template <typename T> __device__ __forceinline__ uint32_t split2(float2& f) {
     if (kF16<T>) {
         const uint32_t r = pack2<T>(f.x, f.y);
-        const float2 g = unpack2<T>(r);
-        f = make_float2(f.x - g.x, f.y - g.y);
+        f = fma2(unpack2<T>(r), splat2(-1.0f), f);
         return r;
     }
     const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y);
-    f = make_float2(f.x - __uint_as_float(x & 0xffff0000u), f.y - __uint_as_float(y & 0xffff0000u));
+    f = fma2(make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u)), splat2(-1.0f), f);
     return __byte_perm(x, y, 0x7632);
 }
 
-// Row `row` of a value tile, times w, as 16-bit parts (same layout).
-template <typename T> __device__ __forceinline__ void split_row(void* v, int row, float w, void* p0, void* p1, void* p2) {
+// 16-byte units u0 .. u1 - 1 of row `row` of a value tile, times w, as 16-bit
+// parts (same layout).
+template <typename T>
+__device__ __forceinline__ void split_row(void* v, int row, int u0, int u1, float w, void* p0, void* p1, void* p2) {
 #pragma unroll 2
-    for (int u = 0; u < 8; u++) {
+    for (int u = u0; u < u1; u++) {
         const uint4 in = *unit(v, row, u);
         const uint32_t x[4] = {in.x, in.y, in.z, in.w};
         uint32_t r[3][4];
@@ -111,10 +112,10 @@ template <typename T> __device__ __forceinline__ void split_row(void* v, int row
     }
 }
 
-template <typename T> __device__ __forceinline__ float row_max(void* v, int row) {
+template <typename T> __device__ __forceinline__ float row_max(void* v, int row, int half) {  // units 4 half .. + 3
     float m = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 8; u++) {
+    for (int u = 4 * half; u < 4 * half + 4; u++) {
         const uint4 in = *unit(v, row, u);
         const uint32_t x[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
@@ -251,8 +252,8 @@ template <typename T, int NB> __device__ __forceinline__ void put_state2(void* h
             float2 f = make_float2(X[8 * u + 2 * i], X[8 * u + 2 * i + 1]);
             if (kF16<T>) f = mul2(f, splat2(s));
             r[i] = pack2<T>(f.x, f.y);
-            const float2 g = unpack2<T>(r[i]);
-            q[i] = pack2<T>(f.x - g.x, f.y - g.y);
+            const float2 rest = fma2(unpack2<T>(r[i]), splat2(-1.0f), f);
+            q[i] = pack2<T>(rest.x, rest.y);
         }
         *unit(hi, n, u0 + u) = make_uint4(r[0], r[1], r[2], r[3]);
         *unit(lo, n, u0 + u) = make_uint4(q[0], q[1], q[2], q[3]);
@@ -369,10 +370,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             run_ends(s_total[0], end);
             const Two mine = end_of(end);
             float vs = 1.0f;
-            if (kF16<T>) vs = f16_scale(group_max(row_max<T>(V, tok), s_red, 1));
+            if (kF16<T>) vs = f16_scale(group_max(fmaxf(row_max<T>(V, tok, 0), row_max<T>(V, tok, 1)), s_red, 1));
             const float wt = ex2(two_diff(end[3], mine) + rel), cl = end[3].h + end[3].l;
             ok = mbar_wait(&s_mE, ph);  // q (and the last y's staging tile) make room for w v
-            split_row<T>(V, tok, wt * vs, W[0], W[1], W[2]);
+            split_row<T>(V, tok, 0, 8, wt * vs, W[0], W[1], W[2]);
             fence_proxy_async_smem();
             group_sync(1);
             if (tid == 0) {
@@ -536,121 +537,183 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
 // each chunk as operand tiles for the backward.
 //   forward   X <- e^{cl} X + k^T (e^{cl - c} v)
 //   reverse   X <- e^{cl} X + q^T (scale e^c dy), chunks last to first
+//
+// Two chunks are in work at a time, each part of the block on its own: 8 warps
+// make w v, 4 keep the state (add a chunk's product to it, write it out as an
+// image), one makes the weights w, one issues copies and products.
 template <int NB> struct StateSmem {
-    static constexpr int k = 0, v = k + NB * 16384, w = v + 16384, total = w + 3 * 16384;
+    static constexpr int k = 0, v = k + NB * 16384, w = v + 16384, stage = w + 3 * 16384, image = 2 * stage,
+                         total = image + 2 * NB * 8192;
 };
+constexpr int kSplit = 256, kStateThreads = kSplit + 128 + 64;
 
 template <typename T, int NB, bool REV, bool SUM>
-__global__ void __launch_bounds__(128, 2) k_tc_state(const __grid_constant__ TcWalkArgs w) {
+__global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = StateSmem<NB>;
-    __shared__ Two s_total[4];
-    __shared__ __align__(8) uint64_t s_ld, s_m;
-    __shared__ uint32_t s_tm, s_red[4];
+    __shared__ float s_weight[2][C], s_all[2], s_vs[2];  // w and e^{cl} of a stage's chunk
+    // of each of the two stages: copies landed; w made; w v made; product done; product read
+    __shared__ __align__(8) uint64_t s_ld[2], s_g[2], s_w[2], s_u[2], s_free[2];
+    __shared__ uint32_t s_tm, s_red[3][4], s_fail;
     const Args& a = w.a;
-    const int tid = threadIdx.x, warp = tid >> 5, tok = tid, run = warp;
+    const int tid = threadIdx.x;
     const Walk at(w, SUM, REV);
-    const int64_t b = at.b, h = at.h, hq = at.hq, p0 = at.p0, t_begin = at.t_begin, t_end = at.t_end;
+    const int64_t b = at.b, h = at.h, t_begin = at.t_begin, t_end = at.t_end;
     const int64_t len = row_length(a, b);
     const int chunks = (int)((t_end - t_begin + C - 1) / C);
-    char *K = sm + L::k, *V = sm + L::v;
-    void* const W[3] = {sm + L::w, sm + L::w + 16384, sm + L::w + 32768};
 
     if (tid == 0) {
-        mbar_init(&s_ld, 1);
-        mbar_init(&s_m, 1);
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            mbar_init(&s_ld[s], 1);
+            mbar_init(&s_g[s], 32);
+            mbar_init(&s_w[s], kSplit);
+            mbar_init(&s_u[s], 1);
+            mbar_init(&s_free[s], 128);
+        }
+        s_fail = 0;
         fence_proxy_async_smem();
     }
-    if (warp == 0) tmem_alloc(&s_tm, 256);
+    if (tid < 32) tmem_alloc(&s_tm, 512);
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tm;
     auto start_of = [&](int ch) { return t_begin + (int64_t)(REV ? chunks - 1 - ch : ch) * C; };
     auto valid = [&](int64_t t0) { return (int)max((int64_t)0, min((int64_t)C, len - t0)); };
-    auto load = [&](int64_t t0) {
-        mbar_expect_tx(&s_ld, (NB + 1) * 16384);
+
+    if (tid < kSplit) {  // ---------------- w v, half a row (four 16-byte units) a thread
+        const int tok = tid & (C - 1), half = tid >> 7;
+        for (int ch = 0; ch < chunks; ch++) {
+            const int s = ch & 1;
+            const uint32_t ph = (ch >> 1) & 1;
+            const int64_t t0 = start_of(ch);
+            char *K = sm + s * L::stage + L::k, *V = sm + s * L::stage + L::v, *W = sm + s * L::stage + L::w;
+            wait_or_fail(&s_g[s], ph, &s_fail);  // (made after the stage's last product was read)
+            wait_or_fail(&s_ld[s], ph, &s_fail);
+            if (tok >= valid(t0) && t0 + tok < a.L) {
 #pragma unroll
-        for (int n = 0; n < NB; n++)
-            tma_load_4d(K + n * 16384, REV ? &w.maps.q : &w.maps.k, n * 64, (int)hq, (int)t0, (int)b, &s_ld);
-        tma_load_4d(V, REV ? &w.maps.dy : &w.maps.v, (int)p0, (int)h, (int)t0, (int)b, &s_ld);
-    };
-    if (tid == 0) load(start_of(0));
-    float X[32 * NB];
-    load_state<NB>(SUM ? StateTile{nullptr, 0, 0, 0} : at.start(w), X);
-    float total = 0.0f, g = load_g(a, b, h, start_of(0), valid(start_of(0)));
-    bool ok = true;
-    int ch = 0;
-    for (; ch < chunks; ch++) {
-        const int64_t t0 = start_of(ch);
-        const int nv = valid(t0);
-        if (!SUM) {
-            float s = 1.0f;
-            if (kF16<T>) s = f16_scale(group_max(state_max<NB>(X), s_red, 1));
-            put_state2<T, NB>(W[0], W[1], s, X);
-            fence_proxy_async_smem();
-            __syncthreads();
-            if (tid == 0) {
-                const int64_t image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + t0 / C;
-                char* to = static_cast<char*>(w.images) + image * (2 * NB * 8192);
-                bulk_store(to, W[0], NB * 8192);
-                bulk_store(to + NB * 8192, W[1], NB * 8192);
-                bulk_commit();
-                if (kF16<T>) w.image_scale[image] = s;
-                bulk_wait_read();
+                for (int u = 4 * half; u < 4 * half + 4; u++) {
+#pragma unroll
+                    for (int n = 0; n < NB; n++) *unit(K + n * 16384, tok, u) = make_uint4(0, 0, 0, 0);
+                    *unit(V, tok, u) = make_uint4(0, 0, 0, 0);
+                }
             }
-        }
-        const float rel = chunk_decays(nullptr, s_total, g);
-        if (ch + 1 < chunks) g = load_g(a, b, h, start_of(ch + 1), valid(start_of(ch + 1)));
-        ok = mbar_wait(&s_ld, ch & 1);
-        if (ok && tok >= nv && t0 + tok < a.L) {
-            if (NB == 2) {
-                char* const t[3] = {K, V, K + 16384};
-                clear_row<3>(t, tok);
-            } else {
-                char* const t[2] = {K, V};
-                clear_row<2>(t, tok);
+            float wt = s_weight[s][tok];
+            if (kF16<T>) {
+                // one scale for the tile: the larger of both halves' largest values
+                const float m = group_max(row_max<T>(V, tok, half), s_red[half], 1 + half);
+                if (tok == 0) s_red[half][0] = __float_as_uint(m);
+                asm volatile("bar.sync 4, 256;" ::: "memory");
+                const float vs = f16_scale(fmaxf(__uint_as_float(s_red[0][0]), __uint_as_float(s_red[1][0])));
+                if (tid == 0) s_vs[s] = vs;
+                wt *= vs;
+                asm volatile("bar.sync 4, 256;" ::: "memory");
             }
+            split_row<T>(V, tok, 4 * half, 4 * half + 4, wt, W, W + 16384, W + 32768);
             fence_proxy_async_smem();
+            mbar_arrive(&s_w[s]);
         }
-        if (__syncthreads_or(!ok)) break;
-        float vs = 1.0f;
-        if (kF16<T>) vs = f16_scale(group_max(row_max<T>(V, tok), s_red, 1));
-        Two end[4];
-        run_ends(s_total, end);
-        const Two mine = run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3]));
-        const float cl = end[3].h + end[3].l;
-        split_row<T>(V, tok, vs * ex2(REV ? (mine.h - rel) + mine.l : two_diff(end[3], mine) + rel), W[0], W[1], W[2]);
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
+    } else if (tid < kSplit + 128) {  // ---------------- the state
+        float X[32 * NB];
+        load_state<NB>(SUM ? StateTile{nullptr, 0, 0, 0} : at.start(w), X);
+        char* image = sm + L::image;
+        const bool lead = tid == kSplit;
+        for (int ch = 0; ch < chunks; ch++) {
+            const int s = ch & 1;
+            const uint32_t ph = (ch >> 1) & 1;
+            if (!SUM) {
+                float sc = 1.0f;
+                if (kF16<T>) sc = f16_scale(group_max(state_max<NB>(X), s_red[2], 3));
+                if (lead) bulk_wait_read();  // the last image has left
+                group_sync(3);
+                put_state2<T, NB>(image, image + NB * 8192, sc, X);
+                fence_proxy_async_smem();
+                group_sync(3);
+                if (lead) {
+                    const int64_t at_image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + start_of(ch) / C;
+                    bulk_store(static_cast<char*>(w.images) + at_image * (2 * NB * 8192), image, 2 * NB * 8192);
+                    bulk_commit();
+                    if (kF16<T>) w.image_scale[at_image] = sc;
+                }
+            }
+            wait_or_fail(&s_u[s], ph, &s_fail);
             tc_fence_after();
-            mma_state_wide<T, NB>(tm, K, W[0]);
-            mma_commit(&s_m);
+            add_product<NB, kParts<T>>(tm + 256 * s, s_all[s], (REV ? a.scale : 1.0f) / (kF16<T> ? s_vs[s] : 1.0f), X);
+            tc_fence_before();
+            mbar_arrive(&s_free[s]);
         }
-        ok = mbar_wait(&s_m, ch & 1);
-        tc_fence_after();
-        if (tid == 0 && ok && ch + 1 < chunks) load(start_of(ch + 1));
-        add_product<NB, kParts<T>>(tm, ex2(cl), (REV ? a.scale : 1.0f) / vs, X);
-        total += cl;
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-    }
-    if (ch < chunks) {
-        if (tid == 0) {
+        if (SUM) {
+            save_state<NB>(at.segment(w), X);
+        } else if (w.last && at.ends(w, REV)) {
+            save_state<NB>(at.whole(w, w.last), X);
+        }
+        if (lead) bulk_wait_all();
+    } else if (tid < kSplit + 160) {  // ---------------- weights, tokens 4 lane .. 4 lane + 3
+        const int lane = tid & 31;
+        float g[4], total = 0.0f;
+        auto raw_g = [&](int ch) {
+            const int64_t t0 = start_of(ch);
+            const int nv = valid(t0);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                g[e] = 4 * lane + e < nv ? a.g[a.g_per_head ? h : (b * a.L + t0 + 4 * lane + e) * a.H + h] : 0.0f;
+        };
+        raw_g(0);
+        for (int ch = 0; ch < chunks; ch++) {
+            const int s = ch & 1;
+            float x[4];
+            Two c[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[e] = clamp_g(g[e]) * kLog2e;
+            if (ch + 1 < chunks) raw_g(ch + 1);
+            warp_cumsum<4>(x, c);
+            const Two cl = {__shfl_sync(kFull, c[3].h, 31), __shfl_sync(kFull, c[3].l, 31)};
+            total += cl.h + cl.l;
+            if (ch >= 2) wait_or_fail(&s_free[s], ((ch >> 1) & 1) ^ 1, &s_fail);  // the stage's last product is done and read
+#pragma unroll
+            for (int e = 0; e < 4; e++) s_weight[s][4 * lane + e] = ex2a(REV ? c[e].h + c[e].l : two_diff(cl, c[e]));
+            if (lane == 0) s_all[s] = ex2a(cl.h + cl.l);
+            mbar_arrive(&s_g[s]);
+        }
+        if (SUM && lane == 0) w.seg_decay[at.cut * w.plan.K + at.seg] = total / kLog2e;
+    } else if ((tid & 31) == 0) {  // ---------------- copies and products
+        auto load = [&](int ch) {
+            const int s = ch & 1, t0 = (int)start_of(ch);
+            char* to = sm + s * L::stage;
+            mbar_expect_tx(&s_ld[s], (NB + 1) * 16384);
+#pragma unroll
+            for (int n = 0; n < NB; n++)
+                tma_load_4d(to + L::k + n * 16384, REV ? &w.maps.q : &w.maps.k, n * 64, (int)at.hq, t0, (int)b, &s_ld[s]);
+            tma_load_4d(to + L::v, REV ? &w.maps.dy : &w.maps.v, (int)at.p0, (int)h, t0, (int)b, &s_ld[s]);
+        };
+        load(0);
+        if (chunks > 1) load(1);
+        int ch = 0;
+        for (; ch < chunks; ch++) {
+            const int s = ch & 1;
+            const uint32_t ph = (ch >> 1) & 1;
+            if (!wait_or_fail(&s_w[s], ph, &s_fail)) break;  // s_w also says that the stage's last product was read
+            tc_fence_after();
+            mma_state_wide<T, NB>(tm + 256 * s, sm + s * L::stage + L::k, sm + s * L::stage + L::w);
+            mma_commit(&s_u[s]);
+            if (ch > 0 && ch + 1 < chunks) {
+                if (!wait_or_fail(&s_u[s ^ 1], ((ch - 1) >> 1) & 1, &s_fail)) break;
+                load(ch + 1);
+            }
+        }
+        if (s_fail) {  // report, wait for what is in flight (within limits)
             atomicOr(w.status, kDevWaitTimeout);
-            mbar_wait(&s_ld, ch & 1);
-            mbar_wait(&s_ld, (ch + 1) & 1);
-            mbar_wait(&s_m, ch & 1);
+            for (int s = 0; s < 2; s++) {
+                mbar_wait(&s_ld[s], 0);
+                mbar_wait(&s_ld[s], 1);
+                mbar_wait(&s_u[s], 0);
+                mbar_wait(&s_u[s], 1);
+            }
         }
-    } else if (SUM) {
-        save_state<NB>(at.segment(w), X);
-        if (tid == 0) w.seg_decay[at.cut * w.plan.K + at.seg] = total / kLog2e;
-    } else if (w.last && at.ends(w, REV)) {
-        save_state<NB>(at.whole(w, w.last), X);
     }
-    if (tid == 0) bulk_wait_all();
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_free(tm, 256);
+    if (tid < 32) tmem_free(tm, 512);
 }
 
 // seg_state: end state of each segment walked from zero -> the state each
@@ -697,8 +760,8 @@ template <typename T, int NB> cudaError_t fwd_n(const TcWalkArgs& w, cudaStream_
 template <typename T, int NB> cudaError_t state_n(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st) {
     const unsigned grid = (unsigned)(sum ? w.plan.cut * (w.plan.K - 1) : w.plan.blocks());
     constexpr int smem = StateSmem<NB>::total;
-    if (reverse) return sum ? go(k_tc_state<T, NB, true, true>, 128, smem, grid, w, st) : go(k_tc_state<T, NB, true, false>, 128, smem, grid, w, st);
-    return sum ? go(k_tc_state<T, NB, false, true>, 128, smem, grid, w, st) : go(k_tc_state<T, NB, false, false>, 128, smem, grid, w, st);
+    if (reverse) return sum ? go(k_tc_state<T, NB, true, true>, kStateThreads, smem, grid, w, st) : go(k_tc_state<T, NB, true, false>, kStateThreads, smem, grid, w, st);
+    return sum ? go(k_tc_state<T, NB, false, true>, kStateThreads, smem, grid, w, st) : go(k_tc_state<T, NB, false, false>, kStateThreads, smem, grid, w, st);
 }
 
 }  // namespace

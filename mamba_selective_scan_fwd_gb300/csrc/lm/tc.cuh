@@ -85,6 +85,20 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                  : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Waits of a block whose parts run on their own: the first wait that runs out
+// sets *fail, and from then on no wait of the block waits, so that every part
+// runs to its end at once.
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t phase, volatile uint32_t* fail) {
+    if (*fail) return false;
+    if (mbar_wait(bar, phase)) return true;
+    *fail = 1;
+    return false;
+}
+
 // ---------------------------------------------------------------- copies
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
