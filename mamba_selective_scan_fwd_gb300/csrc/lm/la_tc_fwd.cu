@@ -58,7 +58,7 @@ __device__ __forceinline__ float load_g(const Args& a, int64_t b, int64_t h, int
     return t < nv ? a.g[a.g_per_head ? h : (b * a.L + t0 + t) * a.H + h] : 0.0f;
 }
 
-// Barrier of one warpgroup (128 threads): id 1, 2 or 3.
+// Barrier of one warpgroup (128 threads): id 1 or 2.
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Largest value of a warpgroup's threads (all get it); v >= 0.  Two barriers.
@@ -127,23 +127,27 @@ template <typename T> __device__ __forceinline__ float row_max(void* v, int row,
     return m;
 }
 
-// The state a thread of a warpgroup holds: NB == 2, row tid, 64 columns; NB ==
-// 1, row tid % 64, 32 columns (the product's 128 rows hold the 64 twice).
-template <int NB> struct StateOf {
-    static constexpr int W = 32 * NB;
+// The part of the state that one of TH threads (128 or 256, aligned in the block)
+// holds: a row, W adjacent columns.  NB == 1: the product's 128 rows hold the 64
+// twice, so that a thread's row is in its own lane.
+template <int NB, int TH> struct StateOf {
+    static constexpr int W = 64 * 64 * NB / TH;
     __device__ static int row() { return threadIdx.x & (64 * NB - 1); }
-    __device__ static int col() { return NB == 2 ? 0 : (int)(threadIdx.x & 64) / 2; }
+    __device__ static int col() { return (int)(threadIdx.x & (TH - 1)) / (64 * NB) * W; }
 };
+
+__device__ __forceinline__ void tmem_ldw(uint32_t addr, float (&x)[16]) { tmem_ld16(addr, x); }
+__device__ __forceinline__ void tmem_ldw(uint32_t addr, float (&x)[32]) { tmem_ld32(addr, x); }
 
 // A state tile in memory: rows of `stride` floats, `cols` of the 64 columns exist.
 struct StateTile {
     const float* p;  // null: zero
     int64_t rows, stride, cols;
 };
-template <int NB> __device__ __forceinline__ void load_state(const StateTile& s, float (&X)[32 * NB]) {
-    const int n = StateOf<NB>::row(), c0 = StateOf<NB>::col();
+template <int NB, int TH> __device__ __forceinline__ void load_state(const StateTile& s, float (&X)[StateOf<NB, TH>::W]) {
+    const int n = StateOf<NB, TH>::row(), c0 = StateOf<NB, TH>::col();
 #pragma unroll
-    for (int c = 0; c < 32 * NB; c += 4) {
+    for (int c = 0; c < StateOf<NB, TH>::W; c += 4) {
         float4 f = {0.0f, 0.0f, 0.0f, 0.0f};
         if (s.p && n < s.rows && c0 + c < s.cols) f = *reinterpret_cast<const float4*>(s.p + n * s.stride + c0 + c);
         X[c] = f.x;
@@ -152,10 +156,10 @@ template <int NB> __device__ __forceinline__ void load_state(const StateTile& s,
         X[c + 3] = f.w;
     }
 }
-template <int NB> __device__ __forceinline__ void save_state(const StateTile& s, const float (&X)[32 * NB]) {
-    const int n = StateOf<NB>::row(), c0 = StateOf<NB>::col();
+template <int NB, int TH> __device__ __forceinline__ void save_state(const StateTile& s, const float (&X)[StateOf<NB, TH>::W]) {
+    const int n = StateOf<NB, TH>::row(), c0 = StateOf<NB, TH>::col();
 #pragma unroll
-    for (int c = 0; c < 32 * NB; c += 4)
+    for (int c = 0; c < StateOf<NB, TH>::W; c += 4)
         if (n < s.rows && c0 + c < s.cols)
             *reinterpret_cast<float4*>(const_cast<float*>(s.p) + n * s.stride + c0 + c) =
                 make_float4(X[c], X[c + 1], X[c + 2], X[c + 3]);
@@ -200,63 +204,53 @@ struct Walk {
         return !is_cut || seg == (reverse ? 0 : w.plan.K - 1);
     }
 };
-template <int NB> __device__ __forceinline__ float state_max(const float (&X)[32 * NB]) {
+template <int W> __device__ __forceinline__ float state_max(const float (&X)[W]) {
     float m = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 32 * NB; c++) m = fmaxf(m, fabsf(X[c]));
+    for (int c = 0; c < W; c++) m = fmaxf(m, fabsf(X[c]));
     return m;
 }
 // X <- d X + u * (the sum of PARTS products, 64 columns apart in tensor memory)
-template <int NB, int PARTS> __device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float (&X)[32 * NB]) {
+template <int NB, int TH, int PARTS>
+__device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float (&X)[StateOf<NB, TH>::W]) {
+    constexpr int W = StateOf<NB, TH>::W, B = W < 32 ? W : 32;
 #pragma unroll
-    for (int c = 0; c < NB; c++) {
+    for (int c = 0; c < W; c += B) {
 #pragma unroll
         for (int p = 0; p < PARTS; p++) {
-            float f[32];
-            tmem_ld32(tm + ((threadIdx.x & 96) << 16) + StateOf<NB>::col() + 32 * c + 64 * p, f);
+            float f[B];
+            tmem_ldw(tm + ((threadIdx.x & 96) << 16) + StateOf<NB, TH>::col() + c + 64 * p, f);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const float2 x = make_float2(f[i], f[i + 1]);
-                float2 y = make_float2(X[32 * c + i], X[32 * c + i + 1]);
+            for (int i = 0; i < B; i += 2) {
+                float2 y = make_float2(X[c + i], X[c + i + 1]);
                 if (p == 0) y = mul2(splat2(d), y);
-                y = fma2(splat2(u), x, y);
-                X[32 * c + i] = y.x;
-                X[32 * c + i + 1] = y.y;
+                y = fma2(splat2(u), make_float2(f[i], f[i + 1]), y);
+                X[c + i] = y.x;
+                X[c + i + 1] = y.y;
             }
         }
     }
 }
-// 16-bit rows [n][p] of X * s: an operand tile
-template <typename T, int NB> __device__ __forceinline__ void put_state(void* to, float s, const float (&X)[32 * NB]) {
-    const int n = StateOf<NB>::row(), u0 = StateOf<NB>::col() / 8;
+// 16-bit rows [n][p] of X * s: an operand tile; LOW: and, in another, of what the
+// rounding left
+template <typename T, int NB, int TH, bool LOW>
+__device__ __forceinline__ void put_state(void* hi, void* lo, float s, const float (&X)[StateOf<NB, TH>::W]) {
+    const int n = StateOf<NB, TH>::row(), u0 = StateOf<NB, TH>::col() / 8;
 #pragma unroll
-    for (int u = 0; u < 4 * NB; u++) {
-        uint32_t r[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float2 f = make_float2(X[8 * u + 2 * i], X[8 * u + 2 * i + 1]);
-            if (kF16<T>) f = mul2(f, splat2(s));
-            r[i] = pack2<T>(f.x, f.y);
-        }
-        *unit(to, n, u0 + u) = make_uint4(r[0], r[1], r[2], r[3]);
-    }
-}
-// ... and of what the rounding left
-template <typename T, int NB> __device__ __forceinline__ void put_state2(void* hi, void* lo, float s, const float (&X)[32 * NB]) {
-    const int n = StateOf<NB>::row(), u0 = StateOf<NB>::col() / 8;
-#pragma unroll
-    for (int u = 0; u < 4 * NB; u++) {
+    for (int u = 0; u < StateOf<NB, TH>::W / 8; u++) {
         uint32_t r[4], q[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             float2 f = make_float2(X[8 * u + 2 * i], X[8 * u + 2 * i + 1]);
             if (kF16<T>) f = mul2(f, splat2(s));
             r[i] = pack2<T>(f.x, f.y);
-            const float2 rest = fma2(unpack2<T>(r[i]), splat2(-1.0f), f);
-            q[i] = pack2<T>(rest.x, rest.y);
+            if (LOW) {
+                const float2 rest = fma2(unpack2<T>(r[i]), splat2(-1.0f), f);
+                q[i] = pack2<T>(rest.x, rest.y);
+            }
         }
         *unit(hi, n, u0 + u) = make_uint4(r[0], r[1], r[2], r[3]);
-        *unit(lo, n, u0 + u) = make_uint4(q[0], q[1], q[2], q[3]);
+        if (LOW) *unit(lo, n, u0 + u) = make_uint4(q[0], q[1], q[2], q[3]);
     }
 }
 
@@ -352,16 +346,16 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
     };
     auto end_of = [&](const Two (&end)[4]) { return run == 0 ? end[0] : (run == 1 ? end[1] : (run == 2 ? end[2] : end[3])); };
     if (!out) {
-        float X[32 * NB];
-        load_state<NB>(at.start(w), X);
+        float X[StateOf<NB, 128>::W];
+        load_state<NB, 128>(at.start(w), X);
         for (; ch < chunks; ch++) {
             const uint32_t ph = ch & 1;
             float hs = 1.0f;  // scale of H as an operand
             if (kF16<T>) {
-                hs = f16_scale(group_max(state_max<NB>(X), s_red, 1));
+                hs = f16_scale(group_max(state_max(X), s_red, 1));
                 if (tid == 0) s_hs[ph] = hs;
             }
-            put_state<T, NB>(H, hs, X);
+            put_state<T, NB, 128, false>(H, nullptr, hs, X);
             const float rel = decays(nullptr, s_total[0], t_begin + (int64_t)ch * C);
             ok = ok && mbar_wait(&s_ld, ph);
             fence_proxy_async_smem();
@@ -384,10 +378,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             }
             ok = mbar_wait(&s_mU, ph) && ok;
             tc_fence_after();
-            add_product<NB, 1>(tU, ex2(cl), 1.0f / vs, X);
+            add_product<NB, 128, 1>(tU, ex2(cl), 1.0f / vs, X);
             tc_fence_before();
         }
-        if (ch == chunks && w.last && at.ends(w, false)) save_state<NB>(at.whole(w, w.last), X);
+        if (ch == chunks && w.last && at.ends(w, false)) save_state<NB, 128>(at.whole(w, w.last), X);
     } else {
         for (; ch < chunks; ch++) {
             const int64_t t0 = t_begin + (int64_t)ch * C;
@@ -538,23 +532,25 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
 //   forward   X <- e^{cl} X + k^T (e^{cl - c} v)
 //   reverse   X <- e^{cl} X + q^T (scale e^c dy), chunks last to first
 //
-// Two chunks are in work at a time, each part of the block on its own: 8 warps
-// make w v, 4 keep the state (add a chunk's product to it, write it out as an
+// Two chunks are in work at a time (and the copies of the next under way), each
+// part of the block on its own: 8 warps
+// make w v, 8 keep the state (add a chunk's product to it, write it out as an
 // image), one makes the weights w, one issues copies and products.
 template <int NB> struct StateSmem {
-    static constexpr int k = 0, v = k + NB * 16384, w = v + 16384, stage = w + 3 * 16384, image = 2 * stage,
-                         total = image + 2 * NB * 8192;
+    static constexpr int ring = NB == 1 ? 3 : 2;  // chunks whose k and v are here or on their way
+    static constexpr int k = 0, v = k + NB * 16384, stage = v + 16384, w = ring * stage, parts = 3 * 16384,
+                         image = w + 2 * parts, total = image + 2 * NB * 8192;
 };
-constexpr int kSplit = 256, kStateThreads = kSplit + 128 + 64;
+constexpr int kSplit = 256, kKeep = 256, kStateThreads = kSplit + kKeep + 64;
 
 template <typename T, int NB, bool REV, bool SUM>
 __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = StateSmem<NB>;
     __shared__ float s_weight[2][C], s_all[2], s_vs[2];  // w and e^{cl} of a stage's chunk
-    // of each of the two stages: copies landed; w made; w v made; product done; product read
-    __shared__ __align__(8) uint64_t s_ld[2], s_g[2], s_w[2], s_u[2], s_free[2];
-    __shared__ uint32_t s_tm, s_red[3][4], s_fail;
+    // copies landed (of a ring's place); w made; w v made; product done; product read (of a stage)
+    __shared__ __align__(8) uint64_t s_ld[L::ring], s_g[2], s_w[2], s_u[2], s_free[2];
+    __shared__ uint32_t s_tm, s_red[2][4], s_most[8], s_fail;
     const Args& a = w.a;
     const int tid = threadIdx.x;
     const Walk at(w, SUM, REV);
@@ -564,12 +560,13 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
 
     if (tid == 0) {
 #pragma unroll
+        for (int s = 0; s < L::ring; s++) mbar_init(&s_ld[s], 1);
+#pragma unroll
         for (int s = 0; s < 2; s++) {
-            mbar_init(&s_ld[s], 1);
             mbar_init(&s_g[s], 32);
             mbar_init(&s_w[s], kSplit);
             mbar_init(&s_u[s], 1);
-            mbar_init(&s_free[s], 128);
+            mbar_init(&s_free[s], kKeep);
         }
         s_fail = 0;
         fence_proxy_async_smem();
@@ -587,9 +584,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
             const int s = ch & 1;
             const uint32_t ph = (ch >> 1) & 1;
             const int64_t t0 = start_of(ch);
-            char *K = sm + s * L::stage + L::k, *V = sm + s * L::stage + L::v, *W = sm + s * L::stage + L::w;
+            char *K = sm + (ch % L::ring) * L::stage + L::k, *V = sm + (ch % L::ring) * L::stage + L::v;
+            char* W = sm + L::w + s * L::parts;
             wait_or_fail(&s_g[s], ph, &s_fail);  // (made after the stage's last product was read)
-            wait_or_fail(&s_ld[s], ph, &s_fail);
+            wait_or_fail(&s_ld[ch % L::ring], (ch / L::ring) & 1, &s_fail);
             if (tok >= valid(t0) && t0 + tok < a.L) {
 #pragma unroll
                 for (int u = 4 * half; u < 4 * half + 4; u++) {
@@ -613,22 +611,33 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
             fence_proxy_async_smem();
             mbar_arrive(&s_w[s]);
         }
-    } else if (tid < kSplit + 128) {  // ---------------- the state
-        float X[32 * NB];
-        load_state<NB>(SUM ? StateTile{nullptr, 0, 0, 0} : at.start(w), X);
+    } else if (tid < kSplit + kKeep) {  // ---------------- the state
+        float X[StateOf<NB, kKeep>::W];
+        load_state<NB, kKeep>(SUM ? StateTile{nullptr, 0, 0, 0} : at.start(w), X);
         char* image = sm + L::image;
+        auto keep_sync = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };
         const bool lead = tid == kSplit;
         for (int ch = 0; ch < chunks; ch++) {
             const int s = ch & 1;
             const uint32_t ph = (ch >> 1) & 1;
             if (!SUM) {
                 float sc = 1.0f;
-                if (kF16<T>) sc = f16_scale(group_max(state_max<NB>(X), s_red[2], 3));
+                if (kF16<T>) {
+                    uint32_t m;
+                    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(state_max(X))));
+                    if ((tid & 31) == 0) s_most[(tid >> 5) & 7] = m;
+                }
                 if (lead) bulk_wait_read();  // the last image has left
-                group_sync(3);
-                put_state2<T, NB>(image, image + NB * 8192, sc, X);
+                keep_sync();
+                if (kF16<T>) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) m = max(m, s_most[i]);
+                    sc = f16_scale(__uint_as_float(m));
+                }
+                put_state<T, NB, kKeep, true>(image, image + NB * 8192, sc, X);
                 fence_proxy_async_smem();
-                group_sync(3);
+                keep_sync();
                 if (lead) {
                     const int64_t at_image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + start_of(ch) / C;
                     bulk_store(static_cast<char*>(w.images) + at_image * (2 * NB * 8192), image, 2 * NB * 8192);
@@ -638,17 +647,17 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
             }
             wait_or_fail(&s_u[s], ph, &s_fail);
             tc_fence_after();
-            add_product<NB, kParts<T>>(tm + 256 * s, s_all[s], (REV ? a.scale : 1.0f) / (kF16<T> ? s_vs[s] : 1.0f), X);
+            add_product<NB, kKeep, kParts<T>>(tm + 256 * s, s_all[s], (REV ? a.scale : 1.0f) / (kF16<T> ? s_vs[s] : 1.0f), X);
             tc_fence_before();
             mbar_arrive(&s_free[s]);
         }
         if (SUM) {
-            save_state<NB>(at.segment(w), X);
+            save_state<NB, kKeep>(at.segment(w), X);
         } else if (w.last && at.ends(w, REV)) {
-            save_state<NB>(at.whole(w, w.last), X);
+            save_state<NB, kKeep>(at.whole(w, w.last), X);
         }
         if (lead) bulk_wait_all();
-    } else if (tid < kSplit + 160) {  // ---------------- weights, tokens 4 lane .. 4 lane + 3
+    } else if (tid < kSplit + kKeep + 32) {  // ---------------- weights, tokens 4 lane .. 4 lane + 3
         const int lane = tid & 31;
         float g[4], total = 0.0f;
         auto raw_g = [&](int ch) {
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
         if (SUM && lane == 0) w.seg_decay[at.cut * w.plan.K + at.seg] = total / kLog2e;
     } else if ((tid & 31) == 0) {  // ---------------- copies and products
         auto load = [&](int ch) {
-            const int s = ch & 1, t0 = (int)start_of(ch);
+            const int s = ch % L::ring, t0 = (int)start_of(ch);
             char* to = sm + s * L::stage;
             mbar_expect_tx(&s_ld[s], (NB + 1) * 16384);
 #pragma unroll
@@ -686,26 +695,23 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
                 tma_load_4d(to + L::k + n * 16384, REV ? &w.maps.q : &w.maps.k, n * 64, (int)at.hq, t0, (int)b, &s_ld[s]);
             tma_load_4d(to + L::v, REV ? &w.maps.dy : &w.maps.v, (int)at.p0, (int)h, t0, (int)b, &s_ld[s]);
         };
-        load(0);
-        if (chunks > 1) load(1);
-        int ch = 0;
-        for (; ch < chunks; ch++) {
-            const int s = ch & 1;
-            const uint32_t ph = (ch >> 1) & 1;
-            if (!wait_or_fail(&s_w[s], ph, &s_fail)) break;  // s_w also says that the stage's last product was read
+        for (int ch = 0; ch < L::ring - 1 && ch < chunks; ch++) load(ch);
+        for (int ch = 0; ch < chunks; ch++) {
+            const int s = ch & 1, ahead = ch + L::ring - 1;
+            if (ch > 0 && !wait_or_fail(&s_u[s ^ 1], ((ch - 1) >> 1) & 1, &s_fail)) break;
+            if (ahead < chunks) load(ahead);  // in the place of chunk ch - 1
+            if (!wait_or_fail(&s_w[s], (ch >> 1) & 1, &s_fail)) break;  // (also: the stage's last product was read)
             tc_fence_after();
-            mma_state_wide<T, NB>(tm + 256 * s, sm + s * L::stage + L::k, sm + s * L::stage + L::w);
+            mma_state_wide<T, NB>(tm + 256 * s, sm + (ch % L::ring) * L::stage + L::k, sm + L::w + s * L::parts);
             mma_commit(&s_u[s]);
-            if (ch > 0 && ch + 1 < chunks) {
-                if (!wait_or_fail(&s_u[s ^ 1], ((ch - 1) >> 1) & 1, &s_fail)) break;
-                load(ch + 1);
-            }
         }
         if (s_fail) {  // report, wait for what is in flight (within limits)
             atomicOr(w.status, kDevWaitTimeout);
-            for (int s = 0; s < 2; s++) {
+            for (int s = 0; s < L::ring; s++) {
                 mbar_wait(&s_ld[s], 0);
                 mbar_wait(&s_ld[s], 1);
+            }
+            for (int s = 0; s < 2; s++) {
                 mbar_wait(&s_u[s], 0);
                 mbar_wait(&s_u[s], 1);
             }
