@@ -21,12 +21,15 @@ template <> struct Vec<__half, 8> { using M = uint4; };
 template <> struct Vec<__nv_bfloat16, 8> { using M = uint4; };
 template <typename T> struct Vec<T, 1> { using M = T; };
 
-template <typename T, int E> __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[E]) {
+template <typename T, int E> __device__ __forceinline__ typename Vec<T, E>::M load(const void* p, int64_t i) {
+    return *reinterpret_cast<const typename Vec<T, E>::M*>(static_cast<const T*>(p) + i);
+}
+template <typename T, int E> __device__ __forceinline__ void widen(const typename Vec<T, E>::M& m, float (&f)[E]) {
     union {
         typename Vec<T, E>::M m;
         T t[E];
     } u;
-    u.m = *reinterpret_cast<const typename Vec<T, E>::M*>(static_cast<const T*>(p) + i);
+    u.m = m;
 #pragma unroll
     for (int e = 0; e < E; e++) f[e] = la::ldf(&u.t[e]);
 }
@@ -90,23 +93,42 @@ __global__ void __launch_bounds__(kThreads<LPG>) k_gnorm(GnormArgs a) {
             dw[j][e] = db[j][e] = 0.0f;
         }
     }
-    for (int64_t r0 = (int64_t)blockIdx.y * kRowsPerStep<LPG>; r0 < a.M; r0 += (int64_t)gridDim.y * kRowsPerStep<LPG>) {
-        const int64_t r = r0 + (LPG <= 32 ? warp : 0);
+    // the runs of one row, on their way while the row before is computed (one run
+    // a thread; threads with several have enough loads in flight)
+    using M = typename Vec<T, E>::M;
+    constexpr bool kAhead = VPT == 1;
+    M xn[VPT], zn[VPT], dn[VPT];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int j = 0; j < VPT; j++)
+            if (r < a.M && on[j]) {
+                const int64_t i = r * a.C + grp * gs + (int64_t)(l + j * LPG) * E;
+                xn[j] = load<T, E>(a.x, i);
+                if (gate) zn[j] = load<T, E>(a.z, i);
+                if (BWD) dn[j] = load<T, E>(a.dout, i);
+            }
+    };
+    const int64_t pace = (int64_t)gridDim.y * kRowsPerStep<LPG>, mine = LPG <= 32 ? warp : 0;
+    int64_t r0 = (int64_t)blockIdx.y * kRowsPerStep<LPG>;
+    if (kAhead) fetch(r0 + mine);
+    for (; r0 < a.M; r0 += pace) {
+        const int64_t r = r0 + mine;
         const bool row = r < a.M;
         const int64_t at = r * a.C + grp * gs;
         float x[VPT][E], z[VPT][E], d[VPT][E];
+        if (!kAhead) fetch(r);
 #pragma unroll
         for (int j = 0; j < VPT; j++) {
-            const int64_t i = at + (int64_t)(l + j * LPG) * E;
             if (row && on[j]) {
-                load<T, E>(a.x, i, x[j]);
-                if (gate) load<T, E>(a.z, i, z[j]);
-                if (BWD) load<T, E>(a.dout, i, d[j]);
+                widen<T, E>(xn[j], x[j]);
+                if (gate) widen<T, E>(zn[j], z[j]);
+                if (BWD) widen<T, E>(dn[j], d[j]);
             } else {
 #pragma unroll
                 for (int e = 0; e < E; e++) x[j][e] = z[j][e] = d[j][e] = 0.0f;
             }
         }
+        if (kAhead) fetch(r + pace);
         // u: what is normalised (x, or x silu(z))
         float u[VPT][E], sum = 0.0f;
 #pragma unroll

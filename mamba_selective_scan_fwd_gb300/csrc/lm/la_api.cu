@@ -132,8 +132,24 @@ cudaError_t tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st) {
     return e != cudaSuccess ? e : launch_tc_carry(w, reverse, st);
 }
 
+// The forward's plans and the workspace of the larger: strides and pointers
+// decide which path runs.
+struct FwdPlan {
+    Walk32 f32;
+    WalkTc tc;
+    size_t bytes;
+};
+FwdPlan fwd_plan(int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dtype) {
+    FwdPlan p = {};
+    Layout l, t;
+    p.f32 = walk32_layout(l, Bsz, L, H, N, P);
+    if (tc_sizes(L, N, P, dtype)) p.tc = walktc_layout(t, Bsz, L, H, N, P, 2 * kSms);
+    p.bytes = l.total > t.total ? l.total : t.total;
+    return p;
+}
+
 // Forward on the tensor cores; *ran tells whether the inputs allow it.
-int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, bool* ran) {
+int tc_forward(const Args& a, const WalkTc& wl, void* y, float* last, char* ws, cudaStream_t st, bool* ran) {
     *ran = false;
     if (!tc_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) ||
         !tc_input(a.v, a.L, a.Bsz))
@@ -149,8 +165,6 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
         return SS_OK;
     const int rc = device_status_word(&w.status);
     if (rc != SS_OK) return rc;
-    Layout l;
-    const WalkTc wl = walktc_layout(l, a.Bsz, a.L, a.H, a.N, a.P, 2 * kSms);
     w.a = a;
     w.plan = wl.plan;
     w.init = a.h0;
@@ -286,10 +300,7 @@ extern "C" {
 
 size_t ss_la_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
-    Layout l, t;
-    walk32_layout(l, Bsz, L, H, N, P);
-    if (tc_sizes(L, N, P, dtype)) walktc_layout(t, Bsz, L, H, N, P, 2 * kSms);
-    return l.total > t.total ? l.total : t.total;  // either path may run: strides and pointers decide
+    return fwd_plan(Bsz, L, H, N, P, dtype).bytes;
 }
 
 int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
@@ -303,7 +314,8 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
         return SS_ERR_UNSUPPORTED;
     if (empty(d->Bsz, d->L)) return pass_state(d->last_state, d->h0, d->Bsz, d->H, d->N, d->P, st);
     if (!d->q || !d->k || !d->v || !d->g || !d->y) return SS_ERR_INVALID_PROBLEM;
-    const size_t need = ss_la_fwd_workspace_bytes(d->Bsz, d->L, d->H, d->G, d->N, d->P, d->dtype);
+    const FwdPlan plan = fwd_plan(d->Bsz, d->L, d->H, d->N, d->P, d->dtype);
+    const size_t need = plan.bytes;
     if (d->workspace_bytes < need || (need > 0 && !d->workspace)) return SS_ERR_WORKSPACE_TOO_SMALL;
     Args a = {};
     a.q = {d->q, d->q_token, d->q_batch};
@@ -318,10 +330,9 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
     a.g_per_head = d->g_per_head ? 1 : 0;
     char* ws = static_cast<char*>(d->workspace);
     bool ran;
-    const int tc = tc_forward(a, d->y, d->last_state, ws, st, &ran);
+    const int tc = tc_forward(a, plan.tc, d->y, d->last_state, ws, st, &ran);
     if (ran || tc != SS_OK) return tc;
-    Layout l;
-    const Walk32 wl = walk32_layout(l, a.Bsz, a.L, a.H, a.N, a.P);
+    const Walk32& wl = plan.f32;
     WalkArgs w = {};
     w.a = a;
     w.plan = wl.plan;

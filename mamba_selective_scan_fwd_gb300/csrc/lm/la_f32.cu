@@ -543,7 +543,7 @@ template <typename T> cudaError_t walk_io(const WalkArgs& w, bool reverse, WalkM
 
 template <typename T, int NB> cudaError_t bwd_n(const BwdArgs& b, cudaStream_t st) {
     const int bytes = (int)sizeof(Smem32<NB>);
-    const cudaError_t e = cudaFuncSetAttribute(k_bwd32<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem<k_bwd32<T, NB>>(bytes);
     if (e != cudaSuccess) return e;
     k_bwd32<T, NB><<<(unsigned)(b.a.Bsz * b.chunks * b.a.G * b.splits), 256, bytes, st>>>(b);
     return cudaGetLastError();

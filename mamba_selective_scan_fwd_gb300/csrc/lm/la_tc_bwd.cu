@@ -549,7 +549,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 
 template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t st) {
     constexpr int smem = BwdSmem<NB>::total;
-    const cudaError_t e = cudaFuncSetAttribute(k_tc_bwd<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<k_tc_bwd<T, NB>>(smem);
     if (e != cudaSuccess) return e;
     const int64_t items = w.a.Bsz * w.chunks * w.a.G * w.splits;
     k_tc_bwd<T, NB><<<(unsigned)(items < kSms ? items : kSms), kThreads, smem, st>>>(w);

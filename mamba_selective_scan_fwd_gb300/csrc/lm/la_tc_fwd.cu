@@ -753,21 +753,23 @@ __global__ void __launch_bounds__(256) k_tc_carry(TcWalkArgs w, bool reverse) {
     }
 }
 
-template <typename K> cudaError_t go(K kernel, int threads, int smem, unsigned grid, const TcWalkArgs& w, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto Kernel> cudaError_t go(int threads, int smem, int64_t grid, const TcWalkArgs& w, cudaStream_t st) {
+    const cudaError_t e = allow_smem<Kernel>(smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, st>>>(w);
+    Kernel<<<(unsigned)grid, threads, smem, st>>>(w);
     return cudaGetLastError();
 }
 
 template <typename T, int NB> cudaError_t fwd_n(const TcWalkArgs& w, cudaStream_t st) {
-    return go(k_tc_fwd<T, NB>, 256, FwdSmem<NB>::total, (unsigned)w.plan.blocks(), w, st);
+    return go<k_tc_fwd<T, NB>>(256, FwdSmem<NB>::total, w.plan.blocks(), w, st);
+}
+template <typename T, int NB, bool REV> cudaError_t state_n(const TcWalkArgs& w, bool sum, cudaStream_t st) {
+    constexpr int smem = StateSmem<NB>::total;
+    return sum ? go<k_tc_state<T, NB, REV, true>>(kStateThreads, smem, w.plan.cut * (w.plan.K - 1), w, st)
+               : go<k_tc_state<T, NB, REV, false>>(kStateThreads, smem, w.plan.blocks(), w, st);
 }
 template <typename T, int NB> cudaError_t state_n(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st) {
-    const unsigned grid = (unsigned)(sum ? w.plan.cut * (w.plan.K - 1) : w.plan.blocks());
-    constexpr int smem = StateSmem<NB>::total;
-    if (reverse) return sum ? go(k_tc_state<T, NB, true, true>, kStateThreads, smem, grid, w, st) : go(k_tc_state<T, NB, true, false>, kStateThreads, smem, grid, w, st);
-    return sum ? go(k_tc_state<T, NB, false, true>, kStateThreads, smem, grid, w, st) : go(k_tc_state<T, NB, false, false>, kStateThreads, smem, grid, w, st);
+    return reverse ? state_n<T, NB, true>(w, sum, st) : state_n<T, NB, false>(w, sum, st);
 }
 
 }  // namespace

@@ -10,9 +10,9 @@ of q and k), g is f32 [Bsz, L, H], or [H] for one decay per head; states are f32
 from __future__ import annotations
 
 import ctypes
+import functools
 
-from .binding import (_I32, _I64, _P, _SZ, _check, _nbytes, _on_device, _p, _require, _state_arg, _workspace, dtype_id,
-                      lib, stream_handle)
+from .binding import _I32, _I64, _P, _SZ, _check, _on_device, _require, _workspace, dtype_id, lib
 
 GNORM_CENTER, GNORM_GATE_FIRST = 1, 2
 
@@ -43,63 +43,82 @@ class LaStepDesc(ctypes.Structure):
         ("scale", ctypes.c_float), ("dtype", _I32), ("g_per_head", _I32), ("reserved", _I32)]
 
 
+@functools.lru_cache(maxsize=256)
 def la_fwd_workspace_bytes(Bsz, L, H, G, N, P, dtype) -> int:
     return int(lib().ss_la_fwd_workspace_bytes(Bsz, L, H, G, N, P, dtype))
 
 
+@functools.lru_cache(maxsize=256)
 def la_bwd_workspace_bytes(Bsz, L, H, G, N, P, dtype) -> int:
     return int(lib().ss_la_bwd_workspace_bytes(Bsz, L, H, G, N, P, dtype))
 
 
-def _require_sliced(t, name, shape, dtype, device, inner):
-    """Like _require, but only the last ``inner`` dimensions must be contiguous: the
-    others may step over a wider tensor's other columns."""
+# The checks below answer the ordinary case with a few comparisons (a single-token call takes
+# as long to check as to run) and leave the wording of a refusal to _require.
+
+
+def _whole(t, name, shape, dtype, device):
+    if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.device == device):
+        _require(t, name, shape, dtype, device)
+
+
+def _optional(t, name, shape, dtype, device):
+    """The checked tensor's address.  The caller keeps the tensor: one that only the call holds must
+    not be freed, and its memory handed to an output, before the launch."""
+    if t is None:
+        return None
+    _whole(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _sliced(t, name, shape, dtype, device):
+    """Check a tensor whose last two dimensions are contiguous; the others may step over a wider
+    tensor's other columns.  Returns its strides."""
+    stride = t.stride()
+    if t.shape == shape and t.dtype is dtype and stride[-1] == 1 and stride[-2] == shape[-1] and t.device == device:
+        return stride
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
-    want = 1
-    for d in reversed(range(len(shape) - inner, len(shape))):
-        if shape[d] > 1 and t.stride(d) != want:
-            raise ValueError(f"{name}: the last {inner} dimensions must be contiguous")
-        want *= shape[d]
+    if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
+        raise ValueError(f"{name}: the last two dimensions must be contiguous")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return stride
 
 
-def _set(desc, tensors):
-    for name, t in tensors.items():
-        setattr(desc, name, None if t is None else t.data_ptr())
-
-
-def _set_strides(desc, tensors):
-    for name, t in tensors.items():
-        setattr(desc, f"{name}_batch", t.stride(0) if t.shape[0] > 1 else 0)
-        if t.dim() == 4:
-            setattr(desc, f"{name}_token", t.stride(1) if t.shape[1] > 1 else 0)
-
-
-def _la_prepare(q, k, v, g, lengths):
-    """Check the shared inputs of the forward and the backward; returns the sizes."""
+def _call(fn, t, *args):
+    """Run a library call on t's device and that device's current stream."""
     import torch
 
-    Bsz, L, H, P = v.shape
-    G, N = q.shape[2:]
-    dev, io = v.device, v.dtype
+    device = t.device
+    if device.index == torch._C._cuda_getDevice():
+        rc = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc:
+        _check(fn, rc)
+
+
+def _in_stream(stream, t, fn, *args):
+    """fn with ``stream`` as the current stream: what it allocates (workspaces, outputs) then belongs
+    to the stream that uses it, and is not handed out again while that still runs."""
+    import torch
+
+    with _on_device(t, stream), torch.cuda.stream(stream):
+        return fn(*args)
+
+
+def _heads(H, G):
     if G < 1 or H % G != 0:
         raise ValueError(f"{H} heads of v cannot share {G} heads of q and k evenly")
-    _require_sliced(q, "q", (Bsz, L, G, N), io, dev, 2)
-    _require_sliced(k, "k", (Bsz, L, G, N), io, dev, 2)
-    _require_sliced(v, "v", (Bsz, L, H, P), io, dev, 2)
-    _require(g, "g", (H,) if g.dim() == 1 else (Bsz, L, H), torch.float32, dev)
-    if lengths is not None:
-        _require(lengths, "lengths", (Bsz,), torch.int32, dev)
-    return Bsz, L, H, G, N, P
 
 
-def _set_sizes(d, sizes, scale, dtype, g):
-    d.Bsz, d.L, d.H, d.G, d.N, d.P = sizes
-    d.scale, d.dtype, d.g_per_head, d.reserved = float(scale), dtype, int(g.dim() == 1), 0
+def _gpu(t):
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be CUDA tensors, got {t.device}")
 
 
 def ss_la_fwd(q, k, v, g, scale=1.0, h0=None, lengths=None, y=None, last_state=None, return_last_state=True,
@@ -109,25 +128,36 @@ def ss_la_fwd(q, k, v, g, scale=1.0, h0=None, lengths=None, y=None, last_state=N
     Returns (y, last_state or None)."""
     import torch
 
-    sizes = _la_prepare(q, k, v, g, lengths)
-    Bsz, L, H, G, N, P = sizes
-    dev, dt = v.device, dtype_id(v)
-    _state_arg(h0, "h0", (Bsz, H, N, P), dev)
+    if stream is not None:
+        return _in_stream(stream, v, ss_la_fwd, q, k, v, g, scale, h0, lengths, y, last_state, return_last_state,
+                          workspace)
+    Bsz, L, H, P = v.shape
+    G, N = q.shape[2:]
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    _heads(H, G)
+    qs = _sliced(q, "q", (Bsz, L, G, N), io, dev)
+    ks = _sliced(k, "k", (Bsz, L, G, N), io, dev)
+    vs = _sliced(v, "v", (Bsz, L, H, P), io, dev)
+    per_head = g.dim() == 1
+    _whole(g, "g", (H,) if per_head else (Bsz, L, H), f32, dev)
+    state = (Bsz, H, N, P)
+    lengths_p = _optional(lengths, "lengths", (Bsz,), torch.int32, dev)
+    h0_p = _optional(h0, "h0", state, f32, dev)
+    _gpu(v)
     if y is None:
-        y = torch.empty((Bsz, L, H, P), dtype=v.dtype, device=dev)
-    _require(y, "y", (Bsz, L, H, P), v.dtype, dev)
+        y = torch.empty((Bsz, L, H, P), dtype=io, device=dev)
+    else:
+        _whole(y, "y", (Bsz, L, H, P), io, dev)
     if last_state is None and return_last_state:
-        last_state = torch.empty((Bsz, H, N, P), dtype=torch.float32, device=dev)
-    _state_arg(last_state, "last_state", (Bsz, H, N, P), dev)
-    with _on_device(v, stream):
-        workspace, wsb = _workspace(la_fwd_workspace_bytes(*sizes, dt), dev, workspace)
-        d = LaFwdDesc()
-        _set(d, dict(q=q, k=k, v=v, g=g, h0=h0, lengths=lengths, y=y, last_state=last_state, workspace=workspace))
-        _set_strides(d, dict(q=q, k=k, v=v))
-        _set_sizes(d, sizes, scale, dt, g)
-        d.workspace_bytes = wsb
-        rc = lib().ss_la_fwd(ctypes.byref(d), stream_handle(stream, dev))
-    _check("ss_la_fwd", rc)
+        last_state = torch.empty(state, dtype=f32, device=dev)
+    last = _optional(last_state, "last_state", state, f32, dev)
+    dt = dtype_id(v)
+    need = la_fwd_workspace_bytes(Bsz, L, H, G, N, P, dt)
+    workspace, wsb = _workspace(need, dev, workspace)
+    d = LaFwdDesc(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), h0_p, lengths_p, y.data_ptr(), last,
+                  None if workspace is None else workspace.data_ptr(), wsb, qs[1], qs[0], ks[1], ks[0], vs[1], vs[0],
+                  Bsz, L, H, G, N, P, scale, dt, per_head, 0)
+    _call("ss_la_fwd", v, ctypes.byref(d))
     return y, last_state
 
 
@@ -137,32 +167,42 @@ def ss_la_bwd(q, k, v, g, dy, scale=1.0, h0=None, dlast_state=None, lengths=None
     the heads that share them) and dv in the io type, dg (g's shape) and dh0 (None without h0) f32."""
     import torch
 
-    sizes = _la_prepare(q, k, v, g, lengths)
-    Bsz, L, H, G, N, P = sizes
-    dev, dt, f32 = v.device, dtype_id(v), torch.float32
-    _require_sliced(dy, "dy", (Bsz, L, H, P), v.dtype, dev, 2)
-    _state_arg(h0, "h0", (Bsz, H, N, P), dev)
-    _state_arg(dlast_state, "dlast_state", (Bsz, H, N, P), dev)
-    shapes = {"dq": ((Bsz, L, G, N), v.dtype), "dk": ((Bsz, L, G, N), v.dtype), "dv": ((Bsz, L, H, P), v.dtype),
-              "dg": (tuple(g.shape), f32), "dh0": ((Bsz, H, N, P), f32)}
+    if stream is not None:
+        return _in_stream(stream, v, ss_la_bwd, q, k, v, g, dy, scale, h0, dlast_state, lengths, out, workspace)
+    Bsz, L, H, P = v.shape
+    G, N = q.shape[2:]
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    _heads(H, G)
+    qs = _sliced(q, "q", (Bsz, L, G, N), io, dev)
+    ks = _sliced(k, "k", (Bsz, L, G, N), io, dev)
+    vs = _sliced(v, "v", (Bsz, L, H, P), io, dev)
+    ys = _sliced(dy, "dy", (Bsz, L, H, P), io, dev)
+    per_head = g.dim() == 1
+    _whole(g, "g", (H,) if per_head else (Bsz, L, H), f32, dev)
+    state = (Bsz, H, N, P)
+    lengths_p = _optional(lengths, "lengths", (Bsz,), torch.int32, dev)
+    h0_p = _optional(h0, "h0", state, f32, dev)
+    dlast_p = _optional(dlast_state, "dlast_state", state, f32, dev)
+    _gpu(v)
+    shapes = {"dq": ((Bsz, L, G, N), io), "dk": ((Bsz, L, G, N), io), "dv": ((Bsz, L, H, P), io),
+              "dg": (tuple(g.shape), f32), "dh0": (state, f32)}
     out = dict(out or {})
     for name, (shape, dtype) in shapes.items():
         if name == "dh0" and h0 is None:
             out[name] = None
-            continue
-        if out.get(name) is None:
+        elif out.get(name) is None:
             out[name] = torch.empty(shape, dtype=dtype, device=dev)
-        _require(out[name], name, shape, dtype, dev)
-    with _on_device(v, stream):
-        workspace, wsb = _workspace(la_bwd_workspace_bytes(*sizes, dt), dev, workspace)
-        d = LaBwdDesc()
-        _set(d, dict(q=q, k=k, v=v, g=g, h0=h0, lengths=lengths, dy=dy, dlast_state=dlast_state, workspace=workspace,
-                     **{n: out[n] for n in shapes}))
-        _set_strides(d, dict(q=q, k=k, v=v, dy=dy))
-        _set_sizes(d, sizes, scale, dt, g)
-        d.workspace_bytes = wsb
-        rc = lib().ss_la_bwd(ctypes.byref(d), stream_handle(stream, dev))
-    _check("ss_la_bwd", rc)
+        else:
+            _whole(out[name], name, shape, dtype, dev)
+    dt = dtype_id(v)
+    need = la_bwd_workspace_bytes(Bsz, L, H, G, N, P, dt)
+    workspace, wsb = _workspace(need, dev, workspace)
+    d = LaBwdDesc(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), h0_p, lengths_p, dy.data_ptr(), dlast_p,
+                  out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(), out["dg"].data_ptr(),
+                  None if out["dh0"] is None else out["dh0"].data_ptr(),
+                  None if workspace is None else workspace.data_ptr(), wsb, qs[1], qs[0], ks[1], ks[0], vs[1], vs[0],
+                  ys[1], ys[0], Bsz, L, H, G, N, P, scale, dt, per_head, 0)
+    _call("ss_la_bwd", v, ctypes.byref(d))
     return out
 
 
@@ -172,53 +212,48 @@ def ss_la_step(q, k, v, g, state, scale=1.0, slots=None, y=None, stream=None):
     padding row (y = 0); without it row b owns state b.  Returns y [Bsz, H, P]."""
     import torch
 
+    if stream is not None:
+        return _in_stream(stream, v, ss_la_step, q, k, v, g, state, scale, slots, y)
     Bsz, H, P = v.shape
     G, N = q.shape[1:]
-    dev, io = v.device, v.dtype
-    if G < 1 or H % G != 0:
-        raise ValueError(f"{H} heads of v cannot share {G} heads of q and k evenly")
-    _require_sliced(q, "q", (Bsz, G, N), io, dev, 2)
-    _require_sliced(k, "k", (Bsz, G, N), io, dev, 2)
-    _require_sliced(v, "v", (Bsz, H, P), io, dev, 2)
-    _require(g, "g", (H,) if g.dim() == 1 else (Bsz, H), torch.float32, dev)
-    _require(state, "state", (state.shape[0], H, N, P), torch.float32, dev)
-    if slots is not None:
-        _require(slots, "slots", (Bsz,), torch.int32, dev)
-    elif state.shape[0] < Bsz:
-        raise ValueError(f"state holds {state.shape[0]} states for {Bsz} rows")
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    _heads(H, G)
+    qs = _sliced(q, "q", (Bsz, G, N), io, dev)
+    ks = _sliced(k, "k", (Bsz, G, N), io, dev)
+    vs = _sliced(v, "v", (Bsz, H, P), io, dev)
+    per_head = g.dim() == 1
+    _whole(g, "g", (H,) if per_head else (Bsz, H), f32, dev)
+    pool = state.shape[0]
+    _whole(state, "state", (pool, H, N, P), f32, dev)
+    if slots is None and pool < Bsz:
+        raise ValueError(f"state holds {pool} states for {Bsz} rows")
+    slots_p = _optional(slots, "slots", (Bsz,), torch.int32, dev)
+    _gpu(v)
     if y is None:
         y = torch.empty((Bsz, H, P), dtype=io, device=dev)
-    _require(y, "y", (Bsz, H, P), io, dev)
-    with _on_device(v, stream):
-        d = LaStepDesc()
-        _set(d, dict(q=q, k=k, v=v, g=g, state=state, slots=slots, y=y))
-        _set_strides(d, dict(q=q, k=k, v=v))
-        d.Bsz, d.H, d.G, d.N, d.P, d.pool = Bsz, H, G, N, P, state.shape[0]
-        d.scale, d.dtype, d.g_per_head, d.reserved = float(scale), dtype_id(v), int(g.dim() == 1), 0
-        rc = lib().ss_la_step(ctypes.byref(d), stream_handle(stream, dev))
-    _check("ss_la_step", rc)
+    else:
+        _whole(y, "y", (Bsz, H, P), io, dev)
+    d = LaStepDesc(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(), slots_p, y.data_ptr(),
+                   qs[0], ks[0], vs[0], Bsz, H, G, N, P, pool, scale, dtype_id(v), per_head, 0)
+    _call("ss_la_step", v, ctypes.byref(d))
     return y
 
 
-def _gnorm_prepare(x, weight, bias, z, groups):
+def _gnorm_prepare(x, weight, bias, z, groups, center, gate_first):
+    """Check the shared inputs of both directions; returns M, C, flags and the inputs' pointers."""
     import torch
 
-    C = x.shape[-1]
+    C, dev, f32 = x.shape[-1], x.device, torch.float32
     if groups < 1 or C % groups != 0:
         raise ValueError(f"{C} channels cannot form {groups} groups")
-    _require(x, "x", x.shape, x.dtype, x.device)
-    if z is not None:
-        _require(z, "z", x.shape, x.dtype, x.device)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _require(t, name, (C,), torch.float32, x.device)
-    return x.numel() // C, C
-
-
-def _gnorm_flags(z, center, gate_first):
     if gate_first and z is None:
         raise ValueError("gate_first needs a gate z")
-    return (GNORM_CENTER if center else 0) | (GNORM_GATE_FIRST if gate_first else 0)
+    _whole(x, "x", x.shape, x.dtype, dev)
+    flags = (GNORM_CENTER if center else 0) | (GNORM_GATE_FIRST if gate_first else 0)
+    pointers = (_optional(weight, "weight", (C,), f32, dev), _optional(bias, "bias", (C,), f32, dev),
+                _optional(z, "z", x.shape, x.dtype, dev))
+    _gpu(x)
+    return x.numel() // C, C, flags, *pointers
 
 
 def ss_gnorm_fwd(x, weight=None, bias=None, z=None, groups=1, eps=1e-5, center=True, gate_first=False, out=None,
@@ -229,15 +264,14 @@ def ss_gnorm_fwd(x, weight=None, bias=None, z=None, groups=1, eps=1e-5, center=T
     Returns out (x's shape and dtype)."""
     import torch
 
-    M, C = _gnorm_prepare(x, weight, bias, z, groups)
-    flags = _gnorm_flags(z, center, gate_first)
+    if stream is not None:
+        return _in_stream(stream, x, ss_gnorm_fwd, x, weight, bias, z, groups, eps, center, gate_first, out)
+    M, C, flags, wp, bp, zp = _gnorm_prepare(x, weight, bias, z, groups, center, gate_first)
     if out is None:
         out = torch.empty_like(x)
-    _require(out, "out", x.shape, x.dtype, x.device)
-    with _on_device(x, stream):
-        rc = lib().ss_gnorm_fwd(_p(x), _p(weight), _p(bias), _p(z), _p(out), M, C, groups, float(eps), flags,
-                                dtype_id(x), stream_handle(stream, x.device))
-    _check("ss_gnorm_fwd", rc)
+    else:
+        _whole(out, "out", x.shape, x.dtype, x.device)
+    _call("ss_gnorm_fwd", x, x.data_ptr(), wp, bp, zp, out.data_ptr(), M, C, groups, eps, flags, dtype_id(x))
     return out
 
 
@@ -247,25 +281,25 @@ def ss_gnorm_bwd(x, weight, bias, dout, z=None, groups=1, eps=1e-5, center=True,
     (f32); dz, dweight and dbias are None when their input is."""
     import torch
 
-    M, C = _gnorm_prepare(x, weight, bias, z, groups)
-    flags = _gnorm_flags(z, center, gate_first)
-    _require(dout, "dout", x.shape, x.dtype, x.device)
+    if stream is not None:
+        return _in_stream(stream, x, ss_gnorm_bwd, x, weight, bias, dout, z, groups, eps, center, gate_first, out,
+                          workspace)
+    M, C, flags, wp, bp, zp = _gnorm_prepare(x, weight, bias, z, groups, center, gate_first)
+    _whole(dout, "dout", x.shape, x.dtype, x.device)
     shapes = {"dx": (x.shape, x.dtype), "dz": (x.shape, x.dtype), "dweight": ((C,), torch.float32),
               "dbias": ((C,), torch.float32)}
-    present = {"dz": z is not None, "dweight": weight is not None, "dbias": bias is not None}
-    res = dict(out or {})
+    present = {"dz": zp is not None, "dweight": wp is not None, "dbias": bp is not None}
+    out = dict(out or {})
     for name, (shape, dtype) in shapes.items():
         if not present.get(name, True):
-            res[name] = None
-            continue
-        if res.get(name) is None:
-            res[name] = torch.empty(shape, dtype=dtype, device=x.device)
-        _require(res[name], name, shape, dtype, x.device)
+            out[name] = None
+        elif out.get(name) is None:
+            out[name] = torch.empty(shape, dtype=dtype, device=x.device)
+        else:
+            _whole(out[name], name, shape, dtype, x.device)
     dt = dtype_id(x)
-    with _on_device(x, stream):
-        workspace, _ = _workspace(int(lib().ss_gnorm_bwd_workspace_bytes(M, C, groups, dt)), x.device, workspace)
-        rc = lib().ss_gnorm_bwd(_p(x), _p(weight), _p(bias), _p(z), _p(dout), _p(res["dx"]), _p(res["dz"]),
-                                _p(res["dweight"]), _p(res["dbias"]), M, C, groups, float(eps), flags, dt,
-                                _p(workspace), _nbytes(workspace), stream_handle(stream, x.device))
-    _check("ss_gnorm_bwd", rc)
-    return res
+    workspace, wsb = _workspace(int(lib().ss_gnorm_bwd_workspace_bytes(M, C, groups, dt)), x.device, workspace)
+    ptr = {name: None if out[name] is None else out[name].data_ptr() for name in shapes}
+    _call("ss_gnorm_bwd", x, x.data_ptr(), wp, bp, zp, dout.data_ptr(), ptr["dx"], ptr["dz"], ptr["dweight"],
+          ptr["dbias"], M, C, groups, eps, flags, dt, workspace.data_ptr(), wsb)
+    return out
