@@ -6,13 +6,13 @@
 // thread keeps its channels' weight and bias (and, in the backward, their
 // gradients' sums) while it walks over rows, so parameters are not re-read and
 // the parameter gradients need one small second pass.
+#include "../simd.cuh"
 #include "la_dev.cuh"
 #include "ss_la.h"
 
 namespace ss {
 namespace {
 
-using la::ex2;
 using la::kLog2e;
 
 template <typename T, int E> struct Vec;  // E values moved at once
@@ -43,40 +43,66 @@ template <typename T, int E> __device__ __forceinline__ void store(void* p, int6
     *reinterpret_cast<typename Vec<T, E>::M*>(static_cast<T*>(p) + i) = u.m;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcpa(1.0f + ex2a(-kLog2e * x)); }
+__device__ __forceinline__ float2 sigmoid(float2 x) {
+    const float2 e = mul2(x, splat2(-kLog2e));
+    const float2 d = add2(make_float2(ex2a(e.x), ex2a(e.y)), splat2(1.0f));
+    return make_float2(rcpa(d.x), rcpa(d.y));
+}
+// A run's values as pairs (runs of one value: the second of the pair is not used)
+template <int E> __device__ __forceinline__ float2 pair(const float (&x)[E], int e) {
+    return make_float2(x[e], E > 1 ? x[e + (E > 1)] : 0.0f);
+}
+template <int E> __device__ __forceinline__ void put(float (&x)[E], int e, float2 v) {
+    x[e] = v.x;
+    if (E > 1) x[e + (E > 1)] = v.y;
+}
 
-// Sum over the LPG threads of a group (all of them get it): lanes of a warp, or the block.
+// Sum over the threads of a group (all of them get it): LPG lanes of a warp, or
+// the whole block (LPG = 0).
 template <int LPG> __device__ __forceinline__ float group_sum(float v, float* red) {
-    constexpr int W = LPG < 32 ? LPG : 32;
+    constexpr int W = LPG > 0 ? LPG : 32;
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if (LPG > 32) {
+    if (LPG == 0) {
         __syncthreads();
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < LPG / 32; w++) v += red[w];
+        for (int w = 0; w < (int)blockDim.x / 32; w++) v += red[w];
     }
     return v;
 }
 
-// LPG threads hold one group, VPT runs of E values each.  LPG <= 32: a warp
-// covers 32 / LPG adjacent groups, a block's 8 warps take different rows.
-// LPG > 32: the block covers one group.  Rows advance by gridDim.y * (rows per step).
-template <int LPG> constexpr int kThreads = LPG <= 32 ? 256 : LPG;
-template <int LPG> constexpr int kRowsPerStep = LPG <= 32 ? 8 : 1;
+// A group is held by LPG lanes of a warp, VPT runs of E values each: a warp
+// covers 32 / LPG adjacent groups, the 8 warps of a block take different rows.
+// LPG = 0: the block covers one group of one row.  Rows advance by gridDim.y *
+// kRowsPerStep.
+template <int LPG> constexpr int kRowsPerStep = LPG > 0 ? 8 : 1;
+
+// Threads with one 16-byte run keep the rows to come on their way to shared
+// memory (their own slots of it: no barrier), as many as it takes to cover the
+// memory's latency; threads with several runs have enough loads in flight.
+template <int E, int VPT> constexpr bool kRing = E > 1 && VPT == 1;
+template <bool BWD> constexpr int kDepth = BWD ? 3 : 4;
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T, int E, int LPG, int VPT, bool BWD>
-__global__ void __launch_bounds__(kThreads<LPG>) k_gnorm(GnormArgs a) {
+__global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 1 ? 1 : (LPG > 0 ? (BWD ? 2 : 4) : (BWD ? 1 : 2))) k_gnorm(GnormArgs a) {
+    extern __shared__ __align__(16) uint4 ring[];  // [depth][x, z, dout][thread] (kRing)
     __shared__ float red[32];
-    __shared__ float cols[BWD && LPG <= 32 ? 8 : 1][BWD && LPG <= 32 ? 32 * E * VPT : 1];
+    __shared__ float cols[BWD && LPG > 0 ? 8 : 1][BWD && LPG > 0 ? 32 * E * VPT : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t gs = a.C / a.groups;
     const int nvec = (int)(gs / E);
-    const int64_t slot = LPG <= 32 ? (int64_t)blockIdx.x * 32 + lane : (int64_t)blockIdx.x * LPG + threadIdx.x;
-    const int64_t grp = slot / LPG;
-    const int l = (int)(slot % LPG);
+    const int64_t slot = (int64_t)blockIdx.x * 32 + lane;
+    const int lanes = LPG > 0 ? LPG : (int)blockDim.x;
+    const int64_t grp = LPG > 0 ? slot / lanes : (int64_t)blockIdx.x;
+    const int l = LPG > 0 ? (int)(slot % lanes) : (int)threadIdx.x;
     const bool center = a.flags & SS_GNORM_CENTER, first = a.flags & SS_GNORM_GATE_FIRST;
     const bool gate = a.z != nullptr;
     const float inv = 1.0f / (float)gs;
@@ -84,8 +110,8 @@ __global__ void __launch_bounds__(kThreads<LPG>) k_gnorm(GnormArgs a) {
     float w[VPT][E], bb[VPT][E], dw[VPT][E], db[VPT][E];
 #pragma unroll
     for (int j = 0; j < VPT; j++) {
-        on[j] = grp < a.groups && l + j * LPG < nvec;
-        const int64_t c = grp * gs + (int64_t)(l + j * LPG) * E;
+        on[j] = grp < a.groups && l + j * lanes < nvec;
+        const int64_t c = grp * gs + (int64_t)(l + j * lanes) * E;
 #pragma unroll
         for (int e = 0; e < E; e++) {
             w[j][e] = on[j] && a.weight ? a.weight[c + e] : 1.0f;
@@ -93,116 +119,141 @@ __global__ void __launch_bounds__(kThreads<LPG>) k_gnorm(GnormArgs a) {
             dw[j][e] = db[j][e] = 0.0f;
         }
     }
-    // the runs of one row, on their way while the row before is computed (one run
-    // a thread; threads with several have enough loads in flight)
-    using M = typename Vec<T, E>::M;
-    constexpr bool kAhead = VPT == 1;
-    M xn[VPT], zn[VPT], dn[VPT];
-    auto fetch = [&](int64_t r) {
-#pragma unroll
-        for (int j = 0; j < VPT; j++)
-            if (r < a.M && on[j]) {
-                const int64_t i = r * a.C + grp * gs + (int64_t)(l + j * LPG) * E;
-                xn[j] = load<T, E>(a.x, i);
-                if (gate) zn[j] = load<T, E>(a.z, i);
-                if (BWD) dn[j] = load<T, E>(a.dout, i);
-            }
-    };
-    const int64_t pace = (int64_t)gridDim.y * kRowsPerStep<LPG>, mine = LPG <= 32 ? warp : 0;
+    const int64_t pace = (int64_t)gridDim.y * kRowsPerStep<LPG>, mine = LPG > 0 ? warp : 0;
     int64_t r0 = (int64_t)blockIdx.y * kRowsPerStep<LPG>;
-    if (kAhead) fetch(r0 + mine);
+    constexpr int D = kDepth<BWD>, kIn = BWD ? 3 : 2;
+    auto at_ring = [&](int stage, int which) { return ring + (stage * kIn + which) * (int)blockDim.x + threadIdx.x; };
+    auto ahead = [&](int stage, int64_t r) {
+        if (r < a.M && on[0]) {
+            const int64_t i = r * a.C + grp * gs + (int64_t)l * E;
+            copy16(at_ring(stage, 0), static_cast<const T*>(a.x) + i);
+            if (gate) copy16(at_ring(stage, 1), static_cast<const T*>(a.z) + i);
+            if (BWD) copy16(at_ring(stage, 2), static_cast<const T*>(a.dout) + i);
+        }
+        copy_commit();
+    };
+    if constexpr (kRing<E, VPT>) {
+#pragma unroll
+        for (int i = 0; i < D - 1; i++) ahead(i, r0 + i * pace + mine);
+    }
+    int stage = 0;
     for (; r0 < a.M; r0 += pace) {
         const int64_t r = r0 + mine;
         const bool row = r < a.M;
         const int64_t at = r * a.C + grp * gs;
         float x[VPT][E], z[VPT][E], d[VPT][E];
-        if (!kAhead) fetch(r);
+        if constexpr (kRing<E, VPT>) {
+            ahead(stage == 0 ? D - 1 : stage - 1, r + (D - 1) * pace);
+            copy_wait<D - 1>();
+        }
 #pragma unroll
         for (int j = 0; j < VPT; j++) {
+            const int64_t i = at + (int64_t)(l + j * lanes) * E;
             if (row && on[j]) {
-                widen<T, E>(xn[j], x[j]);
-                if (gate) widen<T, E>(zn[j], z[j]);
-                if (BWD) widen<T, E>(dn[j], d[j]);
+                if constexpr (kRing<E, VPT>) {
+                    widen<T, E>(*at_ring(stage, 0), x[j]);
+                    if (gate) widen<T, E>(*at_ring(stage, 1), z[j]);
+                    if (BWD) widen<T, E>(*at_ring(stage, 2), d[j]);
+                } else {
+                    widen<T, E>(load<T, E>(a.x, i), x[j]);
+                    if (gate) widen<T, E>(load<T, E>(a.z, i), z[j]);
+                    if (BWD) widen<T, E>(load<T, E>(a.dout, i), d[j]);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < E; e++) x[j][e] = z[j][e] = d[j][e] = 0.0f;
             }
         }
-        if (kAhead) fetch(r + pace);
+        if constexpr (kRing<E, VPT>) stage = stage + 1 == D ? 0 : stage + 1;
         // u: what is normalised (x, or x silu(z))
-        float u[VPT][E], sum = 0.0f;
+        float u[VPT][E];
+        float2 sum = splat2(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; j++)
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                u[j][e] = gate && first ? x[j][e] * (z[j][e] * sigmoid(z[j][e])) : x[j][e];
-                sum += u[j][e];
+            for (int e = 0; e < E; e += 2) {
+                float2 v = pair(x[j], e);
+                if (gate && first) {
+                    const float2 zv = pair(z[j], e);
+                    v = mul2(v, mul2(zv, sigmoid(zv)));
+                }
+                sum = add2(sum, v);
+                put(u[j], e, v);
             }
-        const float mean = center ? group_sum<LPG>(sum, red) * inv : 0.0f;
-        float sq = 0.0f;
+        const float mean = center ? group_sum<LPG>(sum.x + sum.y, red) * inv : 0.0f;
+        float2 sq = splat2(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; j++)
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                u[j][e] -= mean;
-                sq += on[j] ? u[j][e] * u[j][e] : 0.0f;
+            for (int e = 0; e < E; e += 2) {
+                float2 v = add2(pair(u[j], e), splat2(-mean));
+                if (!on[j]) v = splat2(0.0f);
+                if (E == 1) v.y = 0.0f;
+                sq = fma2(v, v, sq);
+                put(u[j], e, v);
             }
-        const float rstd = rsqrtf(group_sum<LPG>(sq, red) * inv + a.eps);
+        const float rstd = rsqrtf(group_sum<LPG>(sq.x + sq.y, red) * inv + a.eps);
         if (!BWD) {
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
                 float o[E];
 #pragma unroll
-                for (int e = 0; e < E; e++) {
-                    const float n = fmaf(u[j][e] * rstd, w[j][e], bb[j][e]);
-                    o[e] = gate ? (first ? n : n * (z[j][e] * sigmoid(z[j][e]))) : n * sigmoid(n);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 n = fma2(mul2(pair(u[j], e), splat2(rstd)), pair(w[j], e), pair(bb[j], e));
+                    const float2 zv = gate ? pair(z[j], e) : n;
+                    put(o, e, gate && first ? n : mul2(n, gate ? mul2(zv, sigmoid(zv)) : sigmoid(zv)));
                 }
-                if (row && on[j]) store<T, E>(a.out, at + (int64_t)(l + j * LPG) * E, o);
+                if (row && on[j]) store<T, E>(a.out, at + (int64_t)(l + j * lanes) * E, o);
             }
         } else {
-            float s1 = 0.0f, s2 = 0.0f;  // sums of t and t * xhat, t the gradient of xhat
+            float2 s1 = splat2(0.0f), s2 = splat2(0.0f);  // sums of t and t * xhat, t the gradient of xhat
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
                 float o[E];
 #pragma unroll
-                for (int e = 0; e < E; e++) {
-                    const float xh = u[j][e] * rstd;
-                    const float n = fmaf(xh, w[j][e], bb[j][e]);
-                    float g = d[j][e];
-                    if (gate && !first) {
-                        const float sg = sigmoid(z[j][e]);
-                        o[e] = g * n * (sg * (1.0f + z[j][e] * (1.0f - sg)));
-                        g *= z[j][e] * sg;
-                    } else if (!gate) {
-                        const float sg = sigmoid(n);
-                        g *= sg * (1.0f + n * (1.0f - sg));
+                for (int e = 0; e < E; e += 2) {
+                    const float2 xh = mul2(pair(u[j], e), splat2(rstd)), wv = pair(w[j], e);
+                    const float2 n = fma2(xh, wv, pair(bb[j], e));
+                    float2 g = pair(d[j], e);
+                    if (!(gate && first)) {
+                        const float2 v = gate ? pair(z[j], e) : n, sg = sigmoid(v), f = mul2(v, sg);
+                        // silu'(v) = sg (1 + v (1 - sg)) = sg + f - f sg
+                        const float2 df = fma2(f, fma2(sg, splat2(-1.0f), splat2(1.0f)), sg);
+                        if (gate) {
+                            put(o, e, mul2(mul2(g, n), df));
+                            g = mul2(g, f);
+                        } else {
+                            g = mul2(g, df);
+                        }
                     }
-                    dw[j][e] = fmaf(g, xh, dw[j][e]);
-                    db[j][e] += g;
-                    const float t = g * w[j][e];
-                    s1 += t;
-                    s2 = fmaf(t, xh, s2);
-                    d[j][e] = t;
-                    u[j][e] = xh;
+                    put(dw[j], e, fma2(g, xh, pair(dw[j], e)));
+                    put(db[j], e, add2(g, pair(db[j], e)));
+                    const float2 t = mul2(g, wv);
+                    s1 = add2(s1, t);
+                    s2 = fma2(t, xh, s2);
+                    put(d[j], e, t);
+                    put(u[j], e, xh);
                 }
-                if (gate && !first && row && on[j]) store<T, E>(a.dz, at + (int64_t)(l + j * LPG) * E, o);
+                if (gate && !first && row && on[j]) store<T, E>(a.dz, at + (int64_t)(l + j * lanes) * E, o);
             }
-            s1 = center ? group_sum<LPG>(s1, red) * inv : 0.0f;
-            s2 = group_sum<LPG>(s2, red) * inv;
+            const float m1 = center ? group_sum<LPG>(E > 1 ? s1.x + s1.y : s1.x, red) * inv : 0.0f;
+            const float m2 = group_sum<LPG>(E > 1 ? s2.x + s2.y : s2.x, red) * inv;
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
                 float o[E], o2[E];
 #pragma unroll
-                for (int e = 0; e < E; e++) {
-                    const float du = rstd * (d[j][e] - s1 - u[j][e] * s2);
-                    o[e] = du;
+                for (int e = 0; e < E; e += 2) {
+                    float2 du = fma2(pair(u[j], e), splat2(-m2), add2(pair(d[j], e), splat2(-m1)));
+                    du = mul2(du, splat2(rstd));
                     if (gate && first) {
-                        const float sg = sigmoid(z[j][e]);
-                        o2[e] = du * x[j][e] * (sg * (1.0f + z[j][e] * (1.0f - sg)));
-                        o[e] = du * (z[j][e] * sg);
+                        const float2 v = pair(z[j], e), sg = sigmoid(v), f = mul2(v, sg);
+                        const float2 df = fma2(f, fma2(sg, splat2(-1.0f), splat2(1.0f)), sg);
+                        put(o2, e, mul2(mul2(du, pair(x[j], e)), df));
+                        du = mul2(du, f);
                     }
+                    put(o, e, du);
                 }
-                const int64_t i = at + (int64_t)(l + j * LPG) * E;
+                const int64_t i = at + (int64_t)(l + j * lanes) * E;
                 if (row && on[j]) {
                     store<T, E>(a.dx, i, o);
                     if (gate && first) store<T, E>(a.dz, i, o2);
@@ -215,7 +266,7 @@ __global__ void __launch_bounds__(kThreads<LPG>) k_gnorm(GnormArgs a) {
         float* part = a.part + (int64_t)blockIdx.y * 2 * a.C;
 #pragma unroll
         for (int pass = 0; pass < 2; pass++) {
-            if (LPG <= 32) {
+            if (LPG > 0) {
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < VPT; j++)
@@ -227,11 +278,11 @@ __global__ void __launch_bounds__(kThreads<LPG>) k_gnorm(GnormArgs a) {
 #pragma unroll
             for (int j = 0; j < VPT; j++)
                 if (on[j]) {
-                    const int64_t c = grp * gs + (int64_t)(l + j * LPG) * E;
+                    const int64_t c = grp * gs + (int64_t)(l + j * lanes) * E;
 #pragma unroll
                     for (int e = 0; e < E; e++) {
                         float v = pass ? db[j][e] : dw[j][e];
-                        if (LPG <= 32) {
+                        if (LPG > 0) {
                             v = 0.0f;
 #pragma unroll
                             for (int k = 0; k < 8; k++) v += cols[k][(j * E + e) * 32 + lane];
@@ -262,18 +313,24 @@ __global__ void __launch_bounds__(256) k_gnorm_params(const float* part, float* 
     }
 }
 
-// Row blocks of a launch: enough blocks for a few on every SM.
+// Row blocks of a launch, xblocks blocks wide, of which per_sm fit on an SM: one
+// round of blocks, each walking over its share of the rows.
 int64_t row_blocks(int64_t M, int64_t xblocks, int64_t rows, int64_t per_sm) {
-    const int64_t want = ceil_div(la::kSms * per_sm, xblocks), most = ceil_div(M, rows);
+    const int64_t want = la::kSms * per_sm / xblocks, most = ceil_div(M, rows);
     const int64_t y = want < most ? want : most;
     return y < 1 ? 1 : (y > 65535 ? 65535 : y);
 }
 
 template <typename T, int E, int LPG, int VPT, bool BWD> cudaError_t go(const GnormArgs& a, cudaStream_t st) {
-    const int64_t x = LPG <= 32 ? ceil_div(a.groups * LPG, 32) : a.groups;
+    const int64_t x = LPG > 0 ? ceil_div(a.groups * LPG, 32) : a.groups;
+    // the block that covers a group: whole warps, no more than its runs need
+    const int threads = LPG > 0 ? 256 : (int)(ceil_div(ceil_div(a.C / a.groups / E, VPT), 32) * 32);
     const int64_t y = BWD ? gnorm_bwd_blocks(a.M, a.C, a.groups)
-                          : row_blocks(a.M, x, kRowsPerStep<LPG>, LPG <= 32 ? 16 : 8);
-    k_gnorm<T, E, LPG, VPT, BWD><<<dim3((unsigned)x, (unsigned)y), kThreads<LPG>, 0, st>>>(a);
+                          : row_blocks(a.M, x, kRowsPerStep<LPG>, LPG > 0 ? 4 : ceil_div(1280, threads));
+    const int smem = kRing<E, VPT> ? kDepth<BWD> * (BWD ? 3 : 2) * threads * 16 : 0;
+    const cudaError_t e = la::allow_smem<k_gnorm<T, E, LPG, VPT, BWD>>(kRing<E, VPT> ? kDepth<BWD> * (BWD ? 3 : 2) * 640 * 16 : 0);
+    if (e != cudaSuccess) return e;
+    k_gnorm<T, E, LPG, VPT, BWD><<<dim3((unsigned)x, (unsigned)y), threads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -291,19 +348,16 @@ template <typename T, bool BWD> cudaError_t pick(const GnormArgs& a, cudaStream_
     const int64_t gs = a.C / a.groups;
     if (gs % E != 0 || !aligned(a)) {
         if (gs <= 256) return go<T, 1, 32, 8, BWD>(a, st);
-        if (gs <= 2048) return go<T, 1, 256, 8, BWD>(a, st);
-        return go<T, 1, 512, 16, BWD>(a, st);
+        if (gs <= 2048) return go<T, 1, 0, 4, BWD>(a, st);
+        return go<T, 1, 0, 16, BWD>(a, st);
     }
     const int64_t n = gs / E;
     if (n <= 4) return go<T, E, 4, 1, BWD>(a, st);
     if (n <= 8) return go<T, E, 8, 1, BWD>(a, st);
     if (n <= 16) return go<T, E, 16, 1, BWD>(a, st);
     if (n <= 32) return go<T, E, 32, 1, BWD>(a, st);
-    if (n <= 64) return go<T, E, 32, 2, BWD>(a, st);
-    if (n <= 256) return go<T, E, 256, 1, BWD>(a, st);
-    if (n <= 512) return go<T, E, 256, 2, BWD>(a, st);
-    if (n <= 1024) return go<T, E, 256, 4, BWD>(a, st);
-    return go<T, E, 512, 4, BWD>(a, st);
+    if (n <= 640) return go<T, E, 0, 1, BWD>(a, st);
+    return go<T, E, 0, 4, BWD>(a, st);
 }
 
 template <bool BWD> cudaError_t pick_io(const GnormArgs& a, cudaStream_t st) {
@@ -319,7 +373,7 @@ template <bool BWD> cudaError_t pick_io(const GnormArgs& a, cudaStream_t st) {
 int64_t gnorm_bwd_blocks(int64_t M, int64_t C, int64_t groups) {
     const int64_t gs = C / groups;
     const int64_t x = gs > 256 ? groups : ceil_div(C, 256);
-    return row_blocks(M, x, gs > 256 ? 1 : 8, 8);
+    return row_blocks(M, x, gs > 256 ? 1 : 8, gs > 256 ? ceil_div(5120, gs) : 2);
 }
 
 cudaError_t launch_gnorm_fwd(const GnormArgs& a, cudaStream_t st) { return pick_io<false>(a, st); }
