@@ -80,11 +80,11 @@ template <int LPG> __device__ __forceinline__ float group_sum(float v, float* re
 // kRowsPerStep.
 template <int LPG> constexpr int kRowsPerStep = LPG > 0 ? 8 : 1;
 
-// Threads with one 16-byte run keep the rows to come on their way to shared
+// Threads whose runs are of 16 bytes keep the rows to come on their way to shared
 // memory (their own slots of it: no barrier), as many as it takes to cover the
-// memory's latency; threads with several runs have enough loads in flight.
-template <int E, int VPT> constexpr bool kRing = E > 1 && VPT == 1;
-template <bool BWD> constexpr int kDepth = BWD ? 3 : 4;
+// memory's latency.
+template <int E> constexpr bool kRing = E > 1;
+template <int VPT, bool BWD> constexpr int kDepth = VPT > 1 ? 2 : (BWD ? 3 : 4);
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
@@ -93,7 +93,7 @@ template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.
 
 template <typename T, int E, int LPG, int VPT, bool BWD>
 __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 1 ? 1 : (LPG > 0 ? (BWD ? 2 : 4) : (BWD ? 1 : 2))) k_gnorm(GnormArgs a) {
-    extern __shared__ __align__(16) uint4 ring[];  // [depth][x, z, dout][thread] (kRing)
+    extern __shared__ __align__(16) uint4 ring[];  // [depth][x, z, dout][run][thread] (kRing)
     __shared__ float red[32];
     __shared__ float cols[BWD && LPG > 0 ? 8 : 1][BWD && LPG > 0 ? 32 * E * VPT : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -107,32 +107,41 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
     const bool gate = a.z != nullptr;
     const float inv = 1.0f / (float)gs;
     bool on[VPT];
-    float w[VPT][E], bb[VPT][E], dw[VPT][E], db[VPT][E];
-#pragma unroll
-    for (int j = 0; j < VPT; j++) {
-        on[j] = grp < a.groups && l + j * lanes < nvec;
+    // weight and bias: in registers with one run a thread, read again for each row (from the L1 cache) with several
+    float w[1][E], bb[1][E], dw[VPT][E], db[VPT][E];
+    auto params = [&](int j, float (&wj)[E], float (&bj)[E]) {
         const int64_t c = grp * gs + (int64_t)(l + j * lanes) * E;
 #pragma unroll
         for (int e = 0; e < E; e++) {
-            w[j][e] = on[j] && a.weight ? a.weight[c + e] : 1.0f;
-            bb[j][e] = on[j] && a.bias ? a.bias[c + e] : 0.0f;
-            dw[j][e] = db[j][e] = 0.0f;
+            wj[e] = on[j] && a.weight ? __ldg(a.weight + c + e) : 1.0f;
+            bj[e] = on[j] && a.bias ? __ldg(a.bias + c + e) : 0.0f;
         }
+    };
+#pragma unroll
+    for (int j = 0; j < VPT; j++) {
+        on[j] = grp < a.groups && l + j * lanes < nvec;
+#pragma unroll
+        for (int e = 0; e < E; e++) dw[j][e] = db[j][e] = 0.0f;
     }
+    if (VPT == 1) params(0, w[0], bb[0]);
     const int64_t pace = (int64_t)gridDim.y * kRowsPerStep<LPG>, mine = LPG > 0 ? warp : 0;
     int64_t r0 = (int64_t)blockIdx.y * kRowsPerStep<LPG>;
-    constexpr int D = kDepth<BWD>, kIn = BWD ? 3 : 2;
-    auto at_ring = [&](int stage, int which) { return ring + (stage * kIn + which) * (int)blockDim.x + threadIdx.x; };
+    constexpr int D = kDepth<VPT, BWD>, kIn = BWD ? 3 : 2;
+    auto at_ring = [&](int stage, int which, int j) {
+        return ring + ((stage * kIn + which) * VPT + j) * (int)blockDim.x + threadIdx.x;
+    };
     auto ahead = [&](int stage, int64_t r) {
-        if (r < a.M && on[0]) {
-            const int64_t i = r * a.C + grp * gs + (int64_t)l * E;
-            copy16(at_ring(stage, 0), static_cast<const T*>(a.x) + i);
-            if (gate) copy16(at_ring(stage, 1), static_cast<const T*>(a.z) + i);
-            if (BWD) copy16(at_ring(stage, 2), static_cast<const T*>(a.dout) + i);
-        }
+#pragma unroll
+        for (int j = 0; j < VPT; j++)
+            if (r < a.M && on[j]) {
+                const int64_t i = r * a.C + grp * gs + (int64_t)(l + j * lanes) * E;
+                copy16(at_ring(stage, 0, j), static_cast<const T*>(a.x) + i);
+                if (gate) copy16(at_ring(stage, 1, j), static_cast<const T*>(a.z) + i);
+                if (BWD) copy16(at_ring(stage, 2, j), static_cast<const T*>(a.dout) + i);
+            }
         copy_commit();
     };
-    if constexpr (kRing<E, VPT>) {
+    if constexpr (kRing<E>) {
 #pragma unroll
         for (int i = 0; i < D - 1; i++) ahead(i, r0 + i * pace + mine);
     }
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
         const bool row = r < a.M;
         const int64_t at = r * a.C + grp * gs;
         float x[VPT][E], z[VPT][E], d[VPT][E];
-        if constexpr (kRing<E, VPT>) {
+        if constexpr (kRing<E>) {
             ahead(stage == 0 ? D - 1 : stage - 1, r + (D - 1) * pace);
             copy_wait<D - 1>();
         }
@@ -150,10 +159,10 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
         for (int j = 0; j < VPT; j++) {
             const int64_t i = at + (int64_t)(l + j * lanes) * E;
             if (row && on[j]) {
-                if constexpr (kRing<E, VPT>) {
-                    widen<T, E>(*at_ring(stage, 0), x[j]);
-                    if (gate) widen<T, E>(*at_ring(stage, 1), z[j]);
-                    if (BWD) widen<T, E>(*at_ring(stage, 2), d[j]);
+                if constexpr (kRing<E>) {
+                    widen<T, E>(*at_ring(stage, 0, j), x[j]);
+                    if (gate) widen<T, E>(*at_ring(stage, 1, j), z[j]);
+                    if (BWD) widen<T, E>(*at_ring(stage, 2, j), d[j]);
                 } else {
                     widen<T, E>(load<T, E>(a.x, i), x[j]);
                     if (gate) widen<T, E>(load<T, E>(a.z, i), z[j]);
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
                 for (int e = 0; e < E; e++) x[j][e] = z[j][e] = d[j][e] = 0.0f;
             }
         }
-        if constexpr (kRing<E, VPT>) stage = stage + 1 == D ? 0 : stage + 1;
+        if constexpr (kRing<E>) stage = stage + 1 == D ? 0 : stage + 1;
         // u: what is normalised (x, or x silu(z))
         float u[VPT][E];
         float2 sum = splat2(0.0f);
@@ -197,9 +206,10 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
                 float o[E];
+                if (VPT > 1) params(j, w[0], bb[0]);
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
-                    const float2 n = fma2(mul2(pair(u[j], e), splat2(rstd)), pair(w[j], e), pair(bb[j], e));
+                    const float2 n = fma2(mul2(pair(u[j], e), splat2(rstd)), pair(w[0], e), pair(bb[0], e));
                     const float2 zv = gate ? pair(z[j], e) : n;
                     put(o, e, gate && first ? n : mul2(n, gate ? mul2(zv, sigmoid(zv)) : sigmoid(zv)));
                 }
@@ -210,10 +220,11 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
                 float o[E];
+                if (VPT > 1) params(j, w[0], bb[0]);
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
-                    const float2 xh = mul2(pair(u[j], e), splat2(rstd)), wv = pair(w[j], e);
-                    const float2 n = fma2(xh, wv, pair(bb[j], e));
+                    const float2 xh = mul2(pair(u[j], e), splat2(rstd)), wv = pair(w[0], e);
+                    const float2 n = fma2(xh, wv, pair(bb[0], e));
                     float2 g = pair(d[j], e);
                     if (!(gate && first)) {
                         const float2 v = gate ? pair(z[j], e) : n, sg = sigmoid(v), f = mul2(v, sg);
@@ -327,8 +338,9 @@ template <typename T, int E, int LPG, int VPT, bool BWD> cudaError_t go(const Gn
     const int threads = LPG > 0 ? 256 : (int)(ceil_div(ceil_div(a.C / a.groups / E, VPT), 32) * 32);
     const int64_t y = BWD ? gnorm_bwd_blocks(a.M, a.C, a.groups)
                           : row_blocks(a.M, x, kRowsPerStep<LPG>, LPG > 0 ? 4 : ceil_div(1280, threads));
-    const int smem = kRing<E, VPT> ? kDepth<BWD> * (BWD ? 3 : 2) * threads * 16 : 0;
-    const cudaError_t e = la::allow_smem<k_gnorm<T, E, LPG, VPT, BWD>>(kRing<E, VPT> ? kDepth<BWD> * (BWD ? 3 : 2) * 640 * 16 : 0);
+    constexpr int slot = kRing<E> ? kDepth<VPT, BWD> * (BWD ? 3 : 2) * VPT * 16 : 0;  // bytes a thread
+    const int smem = slot * threads;
+    const cudaError_t e = la::allow_smem<k_gnorm<T, E, LPG, VPT, BWD>>(slot * (LPG > 0 ? 256 : (VPT == 1 ? 640 : 512)));
     if (e != cudaSuccess) return e;
     k_gnorm<T, E, LPG, VPT, BWD><<<dim3((unsigned)x, (unsigned)y), threads, smem, st>>>(a);
     return cudaGetLastError();
@@ -356,6 +368,8 @@ template <typename T, bool BWD> cudaError_t pick(const GnormArgs& a, cudaStream_
     if (n <= 8) return go<T, E, 8, 1, BWD>(a, st);
     if (n <= 16) return go<T, E, 16, 1, BWD>(a, st);
     if (n <= 32) return go<T, E, 32, 1, BWD>(a, st);
+    if (n <= 64) return go<T, E, 32, 2, BWD>(a, st);
+    if (BWD && n <= 128) return go<T, E, 32, 4, BWD>(a, st);  // (forward: the block form is faster from here on)
     if (n <= 640) return go<T, E, 0, 1, BWD>(a, st);
     return go<T, E, 0, 4, BWD>(a, st);
 }
@@ -372,8 +386,8 @@ template <bool BWD> cudaError_t pick_io(const GnormArgs& a, cudaStream_t st) {
 // holds one partial sum per block): by the channels a block covers at most.
 int64_t gnorm_bwd_blocks(int64_t M, int64_t C, int64_t groups) {
     const int64_t gs = C / groups;
-    const int64_t x = gs > 256 ? groups : ceil_div(C, 256);
-    return row_blocks(M, x, gs > 256 ? 1 : 8, gs > 256 ? ceil_div(5120, gs) : 2);
+    if (gs > 1024) return row_blocks(M, groups, 1, ceil_div(5120, gs));
+    return row_blocks(M, gs > 256 ? groups : ceil_div(C, 256), 8, gs > 256 ? 1 : 2);
 }
 
 cudaError_t launch_gnorm_fwd(const GnormArgs& a, cudaStream_t st) { return pick_io<false>(a, st); }
