@@ -179,21 +179,26 @@ int tc_forward(const Args& a, const WalkTc& wl, void* y, float* last, char* ws, 
 struct BwdTc {
     WalkTc walk;
     int64_t chunks;
-    int splits;
-    size_t before, after, dq, dk, dg, rows;
+    int splits, dg_parts;
+    size_t before, after, before_scale, after_scale, dq, dk, dg, rows;
 };
-BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
+BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     BwdTc b;
     b.walk = walktc_layout(l, Bsz, L, H, N, P, kSms);
     b.chunks = ceil_div(L, kChunkTc);
-    b.splits = tc_splits(Bsz * b.chunks * G, H / G);
-    const size_t images = (size_t)Bsz * H * ceil_div(P, kTileP) * b.chunks * (N > 64 ? 2 : 1) * 16384;
+    const int64_t ptiles = ceil_div(P, kTileP), states = Bsz * H * ptiles * b.chunks;
+    const bool f16 = dtype == SS_F16;
+    b.splits = f16 ? (int)(H / G * ptiles) : tc_splits(Bsz * b.chunks * G, H / G);
+    b.dg_parts = f16 ? (int)ptiles : 1;
+    const size_t images = (size_t)states * (N > 64 ? 2 : 1) * 16384;
     b.before = l.take(images);
     b.after = l.take(images);
+    b.before_scale = l.take(f16 ? states * 4 : 0);
+    b.after_scale = l.take(f16 ? states * 4 : 0);
     const size_t part = b.splits > 1 ? (size_t)b.splits * Bsz * L * G * N * 4 : 0;
     b.dq = l.take(part);
     b.dk = l.take(part);
-    b.dg = l.take((size_t)Bsz * L * H * 4);
+    b.dg = l.take((size_t)b.dg_parts * Bsz * L * H * 4);
     b.rows = l.take((size_t)kDgParts * H * 4);
     return b;
 }
@@ -211,13 +216,10 @@ int bwd_sums(const ss_la_bwd_desc& d, int splits, const float* dq_part, const fl
     return SS_OK;
 }
 
-// Whether the backward of these sizes may run on the tensor cores.
-bool tc_bwd_sizes(int64_t L, int64_t N, int64_t P, int dtype) { return tc_sizes(L, N, P, dtype) && dtype == SS_BF16; }
-
 // Backward on the tensor cores; *ran tells whether the inputs allow it.
 int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* ran) {
     *ran = false;
-    if (!tc_bwd_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) ||
+    if (!tc_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) ||
         !tc_input(a.v, a.L, a.Bsz) || !tc_input(a.dy, a.L, a.Bsz))
         return SS_OK;
     const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
@@ -239,7 +241,7 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     char* ws = static_cast<char*>(d.workspace);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     Layout l;
-    const BwdTc bl = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
+    const BwdTc bl = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P, a.dtype);
     *ran = true;
     w.maps.q = b.maps.q;
     w.maps.k = b.maps.k;
@@ -252,21 +254,28 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     w.chunks = bl.chunks;
     w.init = a.h0;
     w.images = ws + bl.before;
+    w.image_scale = f32(bl.before_scale);
     if (tc_carry(w, false, st) != cudaSuccess || launch_tc_state(w, false, false, st) != cudaSuccess) return SS_ERR_CUDA;
     w.init = a.dlast;
     w.images = ws + bl.after;
+    w.image_scale = f32(bl.after_scale);
     w.last = d.dh0;
     if (tc_carry(w, true, st) != cudaSuccess || launch_tc_state(w, true, false, st) != cudaSuccess) return SS_ERR_CUDA;
     b.a = a;
     b.before = ws + bl.before;
     b.after = ws + bl.after;
+    b.before_scale = f32(bl.before_scale);
+    b.after_scale = f32(bl.after_scale);
     b.chunks = bl.chunks;
-    b.dg = a.g_per_head ? f32(bl.dg) : d.dg;
+    const bool own_dg = !a.g_per_head && bl.dg_parts == 1;
+    b.dg = own_dg ? d.dg : f32(bl.dg);
     b.dq_part = f32(bl.dq);
     b.dk_part = f32(bl.dk);
     b.splits = bl.splits;
     b.status = w.status;
     if (launch_tc_bwd(b, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (bl.dg_parts > 1 && launch_sum_parts(b.dg, a.g_per_head ? b.dg : d.dg, bl.dg_parts, a.Bsz * a.L * a.H, SS_F32, st) != cudaSuccess)
+        return SS_ERR_CUDA;
     return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
 }
 
@@ -348,7 +357,7 @@ size_t ss_la_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, i
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
     Layout l, t;
     bwd32_layout(l, Bsz, L, H, G, N, P);
-    if (tc_bwd_sizes(L, N, P, dtype)) bwdtc_layout(t, Bsz, L, H, G, N, P);
+    if (tc_sizes(L, N, P, dtype)) bwdtc_layout(t, Bsz, L, H, G, N, P, dtype);
     return l.total > t.total ? l.total : t.total;
 }
 

@@ -83,11 +83,12 @@ struct TcBwdMaps {
 struct TcBwdArgs {
     TcBwdMaps maps;
     Args a;
-    const void *before, *after;  // images of H and R (as TcWalkArgs::images)
+    const void *before, *after;               // images of H and R (as TcWalkArgs::images)
+    const float *before_scale, *after_scale;  // f16: their scales
     int64_t chunks;
-    float* dg;                 // [Bsz, L, H]
+    float* dg;                 // [Bsz, L, H]; f16: [value tiles, Bsz, L, H]
     float *dq_part, *dk_part;  // [splits, Bsz, L, G, N] f32 when splits > 1
-    int splits;
+    int splits;                // parts of a group's heads; f16: one per head and value tile
     int* status;
 };
 cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st);

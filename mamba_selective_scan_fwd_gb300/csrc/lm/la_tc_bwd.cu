@@ -1,6 +1,6 @@
 // Linear attention backward on the tensor cores: one chunk of one group of heads
 // at a time, from the states before (H) and the state adjoints after (R) every
-// chunk.  bf16 io.
+// chunk.  16-bit io.
 //
 // Per head (or 64 of its value channels), rows j, columns i >= j, m_ji = e^{c_i - c_j}:
 //   S^T = k q^T,  D^T = v dy^T,  P^T = m o S^T,  E^T = scale m o D^T,  W = E^T o S^T (i > j)
@@ -11,7 +11,15 @@
 // dq and dk stay in tensor memory over the heads; q and k are read once for all
 // of them.  Roundings to 16 bits: P, E, the scaled dy and v, and H and R as
 // operands of dq and dk (outputs of 16 bits); dg takes k R and q H with both
-// parts of R and H and everything else in f32.
+// parts of R and H and everything else in f32.  c_i - c_j inside a run of 32
+// tokens is a difference of f32 sums over the run: exact to f32 rounding of the
+// run's decay (a reset to -128 in the run leaves its other tokens 2^-17).
+//
+// f16's range needs scales, powers of two that keep every operand's largest value
+// near 2^13: P has one, E, the scaled dy and the scaled v share one, H and R come
+// with theirs.  dq and dk of different heads then cannot add up in tensor memory:
+// with f16 a block's work is one head's value tile, and dq, dk are added up in f32
+// by a kernel of their own.
 #include "../simd.cuh"
 #include "la_tc.h"
 #include "tc.cuh"
@@ -102,18 +110,18 @@ __device__ __forceinline__ void put_decays(Decays& d, const float (&g)[4], float
 }
 
 // Where a block is: items blockIdx.x, + gridDim.x, ...; in each the heads h_lo ..
-// h_hi - 1 of one group, their value tiles.
+// h_hi - 1 of one group, their value tiles (SINGLE: one head, one tile).
 struct Place {
     int64_t item;
-    int b, chunk, gq, split, h, h_lo, h_hi, pt;
+    int b, chunk, gq, split, h, h_lo, h_hi, pt, pt_lo, pt_hi;
     int first, last, more;  // of its item's heads and tiles; whether another place follows
 
-    __device__ void mark(const TcBwdArgs& w, int ptiles, int64_t items) {
-        first = h == h_lo && pt == 0;
-        last = h + 1 == h_hi && pt + 1 == ptiles;
+    __device__ void mark(const TcBwdArgs& w, int64_t items) {
+        first = h == h_lo && pt == pt_lo;
+        last = h + 1 == h_hi && pt + 1 == pt_hi;
         more = !last || item + gridDim.x < items;
     }
-    __device__ void begin(const TcBwdArgs& w) {
+    template <bool SINGLE> __device__ void begin(const TcBwdArgs& w, int ptiles) {
         const int rep = (int)(w.a.H / w.a.G);
         int64_t id = item;
         split = (int)(id % w.splits);
@@ -122,20 +130,29 @@ struct Place {
         id /= w.a.G;
         chunk = (int)(id % w.chunks);
         b = (int)(id / w.chunks);
-        h_lo = gq * rep + rep * split / w.splits;
-        h_hi = gq * rep + rep * (split + 1) / w.splits;
+        if (SINGLE) {
+            h_lo = gq * rep + split / ptiles;
+            h_hi = h_lo + 1;
+            pt_lo = split % ptiles;
+            pt_hi = pt_lo + 1;
+        } else {
+            h_lo = gq * rep + rep * split / w.splits;
+            h_hi = gq * rep + rep * (split + 1) / w.splits;
+            pt_lo = 0;
+            pt_hi = ptiles;
+        }
         h = h_lo;
-        pt = 0;
+        pt = pt_lo;
     }
-    __device__ void step(const TcBwdArgs& w, int ptiles, int64_t items) {  // if more
-        if (++pt == ptiles) {
-            pt = 0;
+    template <bool SINGLE> __device__ void step(const TcBwdArgs& w, int ptiles, int64_t items) {  // if more
+        if (++pt == pt_hi) {
+            pt = pt_lo;
             if (++h == h_hi) {
                 item += gridDim.x;
-                begin(w);
+                begin<SINGLE>(w, ptiles);
             }
         }
-        mark(w, ptiles, items);
+        mark(w, items);
     }
 };
 
@@ -152,6 +169,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     // copies: v, dy (and q, k); states.  Products: S, D; dv, k R, q H; dq, dk
     __shared__ __align__(8) uint64_t s_ld, s_st, s_m1, s_m2, s_m3;
     __shared__ uint32_t s_tm;
+    __shared__ uint32_t s_most[kF16<T> ? 4 : 1][16];
     __shared__ Place s_at[3];  // of iteration it at it % 3, the next one's too
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, quarter = tid >> 7;
@@ -169,8 +187,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
         fence_proxy_async_smem();
         Place p;
         p.item = blockIdx.x;
-        p.begin(w);
-        p.mark(w, ptiles, items);
+        p.begin<kF16<T>>(w, ptiles);
+        p.mark(w, items);
         s_at[0] = p;
     }
     if (tid < 32) tmem_alloc(&s_tm, 512);
@@ -183,6 +201,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     auto valid = [&](const Place& p) {
         return (int)max((int64_t)0, min((int64_t)C, row_length(a, p.b) - (int64_t)p.chunk * C));
     };
+    auto image_of = [&](const Place& p) { return ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk; };
     bool ok = true, more = true, failed = false;
     uint32_t it = 0;
 
@@ -200,7 +219,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             tma_load_4d(V, &w.maps.v, p.pt * PT, p.h, t0, p.b, &s_ld);
             tma_load_4d(DY, &w.maps.dy, p.pt * PT, p.h, t0, p.b, &s_ld);
             constexpr int bytes = 2 * NB * 8192;
-            const int64_t image = ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk;
+            const int64_t image = image_of(p);
             mbar_expect_tx(&s_st, 2 * bytes);
             bulk_load(H, static_cast<const char*>(w.before) + image * bytes, bytes, &s_st);
             bulk_load(R, static_cast<const char*>(w.after) + image * bytes, bytes, &s_st);
@@ -225,7 +244,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             Place next = at;
             more = at.more;
             if (more) {
-                next.step(w, ptiles, items);
+                next.step<kF16<T>>(w, ptiles, items);
                 if (lead) s_at[(it + 1) % 3] = next;
                 raw_g(next);
             }
@@ -289,7 +308,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 bulk_commit();
             }
             __syncwarp();
-            if (at.pt + 1 == ptiles) {  // dg of this head, tokens 4 lane .. 4 lane + 3
+            if (at.pt + 1 == at.pt_hi) {  // dg of this head (f16: its tile's part), tokens 4 lane .. 4 lane + 3
                 const int nv = valid(at);
                 float sum = 0.0f, av[4], bv[4];
 #pragma unroll
@@ -314,7 +333,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int64_t t = 4 * lane + e;
-                    if (t0 + t < a.L) w.dg[(at.b * a.L + t0 + t) * a.H + at.h] = t < nv ? suf + pre + sum : 0.0f;
+                    if (t0 + t < a.L) w.dg[((at.pt_lo * a.Bsz + at.b) * a.L + t0 + t) * a.H + at.h] = t < nv ? suf + pre + sum : 0.0f;
                     suf -= av[e];
                     pre += bv[e];
                 }
@@ -372,76 +391,125 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             const float down = dec.down[tok];
             uint32_t vr[8];
             read_row(V, tok, quarter, vr);
-            {
+            auto put_ds = [&](float f) {  // f dy
                 uint32_t x[8];
                 read_row(DY, tok, quarter, x);
-                const float up = dec.up[tok];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const float2 f = mul2(unpack2<T>(x[i]), splat2(up));
-                    x[i] = pack2<T>(f.x, f.y);
+                    const float2 y = mul2(unpack2<T>(x[i]), splat2(f));
+                    x[i] = pack2<T>(y.x, y.y);
                 }
                 write_row(DS, tok, quarter, x);
-            }
-            ok = mbar_wait(&s_m1, ph);
-            tc_fence_after();
-            {
+            };
+            auto put_v = [&](float f) {  // f v, in v's place
                 uint32_t x[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const float2 f = mul2(unpack2<T>(vr[i]), splat2(down));
-                    x[i] = pack2<T>(f.x, f.y);
+                    const float2 y = mul2(unpack2<T>(vr[i]), splat2(f));
+                    x[i] = pack2<T>(y.x, y.y);
                 }
                 write_row(V, tok, quarter, x);
-            }
-            // P, E and W by 32 x 32 blocks: rows of `run`, columns of `quarter`
+            };
+            if (!kF16<T>) put_ds(dec.up[tok]);
+            ok = mbar_wait(&s_m1, ph);
+            tc_fence_after();
+            if (!kF16<T>) put_v(down);
+            // P, E and W by 32 x 32 blocks: rows of `run`, columns of `quarter`.  W keeps its diagonal: it is in a
+            // row's sum and in a column's, which dg subtracts
             uint32_t pr[16], er[16];
-            float col = 0.0f;
+            float col = 0.0f, ih = 1.0f, ir = 1.0f, kap = 1.0f, ps = 1.0f;
             const int cb = quarter;
-            if (cb >= run) {
+            // the block: S, D from tensor memory; use(i, P, E, S) for its column pairs
+            auto block = [&](auto use) {
                 float s[32], d[32];
                 tmem_ld32(tS + my + 32 * cb, s);
                 tmem_ld32(tD + my + 32 * cb, d);
-                // W keeps its diagonal: it is in a row's sum and in a column's, which dg subtracts
+                const float2 f = splat2(cb > run ? dec.tail[tok] * (cb == run + 1 ? 1.0f : dec.skip[cb - 2 + (cb - run == 3 ? 1 : 0)])
+                                                 : -dec.c[tok]);
                 if (cb > run) {
-                    const float2 f = splat2(dec.tail[tok] * (cb == run + 1 ? 1.0f : dec.skip[cb - 2 + (cb - run == 3 ? 1 : 0)]));
                     const float2 fs = mul2(f, splat2(a.scale));
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float2 t = *reinterpret_cast<const float2*>(&dec.head[32 * cb + j]);
                         const float2 sv = make_float2(s[j], s[j + 1]);
-                        const float2 p = mul2(mul2(f, t), sv);
-                        const float2 e = mul2(mul2(fs, t), make_float2(d[j], d[j + 1]));
-                        const float2 x = mul2(e, sv);
-                        pr[j / 2] = pack2<T>(p.x, p.y);
-                        er[j / 2] = pack2<T>(e.x, e.y);
-                        s[j] = x.x;
-                        s[j + 1] = x.y;
+                        use(j, mul2(mul2(f, t), sv), mul2(mul2(fs, t), make_float2(d[j], d[j + 1])), sv);
                     }
                 } else {
-                    const float own = dec.c[tok];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float2 c = add2(*reinterpret_cast<const float2*>(&dec.c[32 * cb + j]), splat2(-own));
+                        const float2 c = add2(*reinterpret_cast<const float2*>(&dec.c[32 * cb + j]), f);
                         const float2 m = make_float2(j >= lane ? ex2a(c.x) : 0.0f, j + 1 >= lane ? ex2a(c.y) : 0.0f);
                         const float2 sv = make_float2(s[j], s[j + 1]);
-                        const float2 p = mul2(m, sv);
-                        const float2 e = mul2(mul2(m, splat2(a.scale)), make_float2(d[j], d[j + 1]));
-                        const float2 x = mul2(e, sv);
-                        pr[j / 2] = pack2<T>(p.x, p.y);
-                        er[j / 2] = pack2<T>(e.x, e.y);
-                        s[j] = x.x;
-                        s[j + 1] = x.y;
+                        use(j, mul2(m, sv), mul2(mul2(m, splat2(a.scale)), make_float2(d[j], d[j + 1])), sv);
                     }
                 }
-                float2 sum = make_float2(s[0], s[1]);
-#pragma unroll
-                for (int i = 2; i < 32; i += 2) sum = add2(sum, make_float2(s[i], s[i + 1]));
+            };
+            if (cb >= run) {
+                float wv[32];
+                float2 sum = splat2(0.0f), most = splat2(0.0f);
+                block([&](int j, float2 p, float2 e, float2 sv) {
+                    const float2 x = mul2(e, sv);
+                    sum = add2(sum, x);
+                    wv[j] = x.x;
+                    wv[j + 1] = x.y;
+                    if (kF16<T>) {
+                        most.x = fmaxf(most.x, fmaxf(fabsf(p.x), fabsf(p.y)));
+                        most.y = fmaxf(most.y, fmaxf(fabsf(e.x), fabsf(e.y)));
+                    } else {
+                        pr[j / 2] = pack2<T>(p.x, p.y);
+                        er[j / 2] = pack2<T>(e.x, e.y);
+                    }
+                });
                 col = sum.x + sum.y;
-                s_row[run][32 * cb + lane] = column_sums(s);
+                s_row[run][32 * cb + lane] = column_sums(wv);
+                if (kF16<T>) {
+                    ps = most.x;
+                    kap = most.y;
+                }
             } else {
+                if (kF16<T>) ps = kap = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; i++) pr[i] = er[i] = 0;
+            }
+            if constexpr (kF16<T>) {
+                // the scales: the block's largest P, E, scaled dy and scaled v
+                float md = 0.0f, mv = 0.0f;
+                uint32_t x[8];
+                read_row(DY, tok, quarter, x);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float2 y = unpack2<T>(x[i]), v = unpack2<T>(vr[i]);
+                    md = fmaxf(md, fmaxf(fabsf(y.x), fabsf(y.y)));
+                    mv = fmaxf(mv, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
+                const int64_t image = image_of(at);
+                ih = 1.0f / w.before_scale[image];
+                ir = 1.0f / w.after_scale[image];
+                const float most[4] = {ps, kap, md * fabsf(dec.up[tok]) * ih, mv * down * ir};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    uint32_t m;
+                    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(most[i])));
+                    if (lane == 0) s_most[i][tid >> 5] = m;
+                }
+                asm volatile("bar.sync 1, 512;" ::: "memory");
+                uint32_t mp = 0, mk = 0;
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    mp = max(mp, s_most[0][i]);
+                    mk = max(mk, max(s_most[1][i], max(s_most[2][i], s_most[3][i])));
+                }
+                ps = f16_scale(__uint_as_float(mp));
+                kap = f16_scale(__uint_as_float(mk));
+                put_ds(dec.up[tok] * ih * kap);
+                put_v(down * ir * kap);
+                if (cb >= run)
+                    block([&](int j, float2 p, float2 e, float2) {
+                        p = mul2(p, splat2(ps));
+                        e = mul2(e, splat2(kap));
+                        pr[j / 2] = pack2<T>(p.x, p.y);
+                        er[j / 2] = pack2<T>(e.x, e.y);
+                    });
             }
             // E: row j, columns 32 cb .. + 31 of two 64-column tiles
 #pragma unroll
@@ -458,7 +526,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             failed = __syncthreads_or(!ok);  // B
             if (failed) break;
             // <R, H> of this tile: rows n of both, high + low
-            if (at.pt == 0) through = 0.0f;
+            if (at.pt == at.pt_lo) through = 0.0f;
             if (tok < NP) {
                 uint32_t h0[8], h1[8], r0[8], r1[8];
                 read_row(H, tok, quarter, h0);
@@ -474,7 +542,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             float th = through;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) th += __shfl_xor_sync(kFull, th, o);
-            if (lane == 0) s_red[tid >> 5] = th * dec.all;
+            if (lane == 0) s_red[tid >> 5] = th * (dec.all * ih * ir);
             uint32_t dyr[8], dv[8];
             read_row(DY, tok, quarter, dyr);
             ok = mbar_wait(&s_m2, ph);
@@ -485,17 +553,18 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 tmem_ld16(tV + my + 16 * quarter, x);
                 tmem_ld16(tZ + my + 16 * quarter, zz);
                 float2 b = make_float2(0.0f, 0.0f), z = make_float2(0.0f, 0.0f);
+                const float fv = a.scale / ps, fr = down * ir;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const float2 y = mul2(splat2(down), make_float2(f[2 * i], f[2 * i + 1]));
+                    const float2 y = mul2(splat2(fr), make_float2(f[2 * i], f[2 * i + 1]));
                     b = fma2(y, unpack2<T>(vr[i]), b);
                     z = fma2(make_float2(zz[2 * i], zz[2 * i + 1]), unpack2<T>(dyr[i]), z);
-                    const float2 o = fma2(splat2(a.scale), make_float2(x[2 * i], x[2 * i + 1]), y);
+                    const float2 o = fma2(splat2(fv), make_float2(x[2 * i], x[2 * i + 1]), y);
                     dv[i] = pack2<T>(o.x, o.y);
                 }
-                float sa = dec.up[tok] * (z.x + z.y), sb = b.x + b.y + col;
+                float sa = dec.up[tok] * ih * (z.x + z.y), sb = b.x + b.y + col;
                 if (quarter <= run) sb -= s_row[quarter][tok];  // row_i, one row block each
-                if (at.pt > 0) {
+                if (at.pt > at.pt_lo) {
                     sa += s_a[quarter][tok];
                     sb += s_b[quarter][tok];
                 }
@@ -522,6 +591,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                         float x[16];
                         const int n0 = 16 * NB * quarter + 16 * c;
                         tmem_ld16(from + my + n0, x);
+                        if (kF16<T>)
+#pragma unroll
+                            for (int i = 0; i < 16; i++) x[i] *= 1.0f / kap;
                         if (w.splits == 1) {
                             uint32_t r[8];
 #pragma unroll
@@ -559,6 +631,7 @@ template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t
 }  // namespace
 
 cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st) {
+    if (w.a.dtype == 1) return w.a.N > 64 ? bwd_n<__half, 2>(w, st) : bwd_n<__half, 1>(w, st);
     return w.a.N > 64 ? bwd_n<__nv_bfloat16, 2>(w, st) : bwd_n<__nv_bfloat16, 1>(w, st);
 }
 

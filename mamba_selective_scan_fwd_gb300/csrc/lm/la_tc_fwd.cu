@@ -25,8 +25,6 @@ namespace {
 constexpr int C = kChunkTc;
 constexpr int PT = kTileP;
 
-template <typename T> constexpr bool kF16 = false;
-template <> constexpr bool kF16<__half> = true;
 // 16-bit parts of w v: 3 x 8 bits (bf16), 2 x 11 (f16)
 template <typename T> constexpr int kParts = kF16<T> ? 2 : 3;
 

@@ -141,6 +141,9 @@ template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
     return __half22float2(*reinterpret_cast<__half2*>(&x));
 }
 
+template <typename T> constexpr bool kF16 = false;
+template <> constexpr bool kF16<__half> = true;
+
 // 16-byte unit c of row r of a swizzled tile
 __device__ __forceinline__ uint4* unit(void* tile, int r, int c) {
     return reinterpret_cast<uint4*>(static_cast<char*>(tile) + r * 128 + ((c ^ (r & 7)) << 4));
