@@ -104,7 +104,9 @@ struct BwdArgs {
 cudaError_t launch_walk32(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st);
 cudaError_t launch_carry(const CarryArgs& c, cudaStream_t st);
 cudaError_t launch_bwd32(const BwdArgs& b, cudaStream_t st);
-cudaError_t launch_sum_parts(const float* part, void* out, int splits, int64_t n, int dtype, cudaStream_t st);
+// out[i] = sum of the splits' part[., i] (n each), of one pair of arrays or (out2 given) of two
+cudaError_t launch_sum_parts(const float* part, void* out, const float* part2, void* out2, int splits, int64_t n, int dtype,
+                             cudaStream_t st);
 // dg [rows, H] summed over rows into out [H]; part holds kDgParts * H floats
 constexpr int kDgParts = 64;
 cudaError_t launch_sum_rows(const float* dg, float* part, float* out, int64_t rows, int64_t H, cudaStream_t st);

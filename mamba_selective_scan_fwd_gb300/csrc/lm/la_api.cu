@@ -117,19 +117,19 @@ struct WalkTc {
     TcPlan plan;
     size_t state, decay;
 };
-WalkTc walktc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int64_t slots) {
+WalkTc walktc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dirs, int64_t slots) {
     WalkTc w;
-    w.plan = tc_plan(Bsz * H * ceil_div(P, kTileP), L, slots);
+    w.plan = tc_plan(dirs * Bsz * H * ceil_div(P, kTileP), L, slots);
     w.state = l.take((size_t)w.plan.cut * w.plan.K * N * kTileP * 4);
     w.decay = l.take((size_t)w.plan.cut * w.plan.K * 4);
     return w;
 }
 
 // The sum pass of a walk cut in time, and the states its segments start from.
-cudaError_t tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st) {
+cudaError_t tc_carry(const TcWalkArgs& w, cudaStream_t st) {
     if (w.plan.cut == 0) return cudaSuccess;
-    const cudaError_t e = launch_tc_state(w, reverse, true, st);
-    return e != cudaSuccess ? e : launch_tc_carry(w, reverse, st);
+    const cudaError_t e = launch_tc_state(w, true, st);
+    return e != cudaSuccess ? e : launch_tc_carry(w, st);
 }
 
 // The forward's plans and the workspace of the larger: strides and pointers
@@ -143,7 +143,7 @@ FwdPlan fwd_plan(int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dt
     FwdPlan p = {};
     Layout l, t;
     p.f32 = walk32_layout(l, Bsz, L, H, N, P);
-    if (tc_sizes(L, N, P, dtype)) p.tc = walktc_layout(t, Bsz, L, H, N, P, 2 * kSms);
+    if (tc_sizes(L, N, P, dtype)) p.tc = walktc_layout(t, Bsz, L, H, N, P, 1, 2 * kSms);
     p.bytes = l.total > t.total ? l.total : t.total;
     return p;
 }
@@ -167,12 +167,12 @@ int tc_forward(const Args& a, const WalkTc& wl, void* y, float* last, char* ws, 
     if (rc != SS_OK) return rc;
     w.a = a;
     w.plan = wl.plan;
-    w.init = a.h0;
+    w.dirs = 1;
+    w.dir[0] = {a.h0, last, nullptr, nullptr};
     w.seg_state = reinterpret_cast<float*>(ws + wl.state);
     w.seg_decay = reinterpret_cast<float*>(ws + wl.decay);
-    w.last = last;
     *ran = true;
-    if (tc_carry(w, false, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (tc_carry(w, st) != cudaSuccess) return SS_ERR_CUDA;
     return launch_tc_fwd(w, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -184,7 +184,7 @@ struct BwdTc {
 };
 BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     BwdTc b;
-    b.walk = walktc_layout(l, Bsz, L, H, N, P, kSms);
+    b.walk = walktc_layout(l, Bsz, L, H, N, P, 2, kSms);
     b.chunks = ceil_div(L, kChunkTc);
     const int64_t ptiles = ceil_div(P, kTileP), states = Bsz * H * ptiles * b.chunks;
     const bool f16 = dtype == SS_F16;
@@ -208,9 +208,7 @@ int bwd_sums(const ss_la_bwd_desc& d, int splits, const float* dq_part, const fl
              cudaStream_t st) {
     if (splits > 1) {
         const int64_t n = d.Bsz * d.L * d.G * d.N;
-        if (launch_sum_parts(dq_part, d.dq, splits, n, d.dtype, st) != cudaSuccess ||
-            launch_sum_parts(dk_part, d.dk, splits, n, d.dtype, st) != cudaSuccess)
-            return SS_ERR_CUDA;
+        if (launch_sum_parts(dq_part, d.dq, dk_part, d.dk, splits, n, d.dtype, st) != cudaSuccess) return SS_ERR_CUDA;
     }
     if (d.g_per_head && launch_sum_rows(dg, rows, d.dg, d.Bsz * d.L, d.H, st) != cudaSuccess) return SS_ERR_CUDA;
     return SS_OK;
@@ -252,15 +250,10 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     w.seg_state = f32(bl.walk.state);
     w.seg_decay = f32(bl.walk.decay);
     w.chunks = bl.chunks;
-    w.init = a.h0;
-    w.images = ws + bl.before;
-    w.image_scale = f32(bl.before_scale);
-    if (tc_carry(w, false, st) != cudaSuccess || launch_tc_state(w, false, false, st) != cudaSuccess) return SS_ERR_CUDA;
-    w.init = a.dlast;
-    w.images = ws + bl.after;
-    w.image_scale = f32(bl.after_scale);
-    w.last = d.dh0;
-    if (tc_carry(w, true, st) != cudaSuccess || launch_tc_state(w, true, false, st) != cudaSuccess) return SS_ERR_CUDA;
+    w.dirs = 2;
+    w.dir[0] = {a.h0, nullptr, ws + bl.before, f32(bl.before_scale)};
+    w.dir[1] = {a.dlast, d.dh0, ws + bl.after, f32(bl.after_scale)};
+    if (tc_carry(w, st) != cudaSuccess || launch_tc_state(w, false, st) != cudaSuccess) return SS_ERR_CUDA;
     b.a = a;
     b.before = ws + bl.before;
     b.after = ws + bl.after;
@@ -274,7 +267,7 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     b.splits = bl.splits;
     b.status = w.status;
     if (launch_tc_bwd(b, st) != cudaSuccess) return SS_ERR_CUDA;
-    if (bl.dg_parts > 1 && launch_sum_parts(b.dg, a.g_per_head ? b.dg : d.dg, bl.dg_parts, a.Bsz * a.L * a.H, SS_F32, st) != cudaSuccess)
+    if (bl.dg_parts > 1 && launch_sum_parts(b.dg, a.g_per_head ? b.dg : d.dg, nullptr, nullptr, bl.dg_parts, a.Bsz * a.L * a.H, SS_F32, st) != cudaSuccess)
         return SS_ERR_CUDA;
     return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
 }

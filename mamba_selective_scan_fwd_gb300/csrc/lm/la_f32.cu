@@ -493,12 +493,31 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(256) k_sum_parts(const float* part, T* out, int splits, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// Four values a thread (n is a multiple of 4, VEC) or one; parts in a fixed order.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_sum_parts(const float* part, T* out, const float* part2, T* out2, int splits, int64_t n) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * (VEC ? 4 : 1);
     if (i >= n) return;
-    float s = 0.0f;
-    for (int k = 0; k < splits; k++) s += part[k * n + i];
-    st(out + i, s);
+    if (blockIdx.y) {
+        part = part2;
+        out = out2;
+    }
+    if (VEC) {
+        float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int k = 0; k < splits; k++) {
+            const float4 x = *reinterpret_cast<const float4*>(part + k * n + i);
+            s = {s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w};
+        }
+        st(out + i, s.x);
+        st(out + i + 1, s.y);
+        st(out + i + 2, s.z);
+        st(out + i + 3, s.w);
+    } else {
+        float s = 0.0f;
+        for (int k = 0; k < splits; k++) s += part[k * n + i];
+        st(out + i, s);
+    }
 }
 
 // part[slice, h] = sum of the slice's rows (32 heads x 8 rows at a time)
@@ -582,12 +601,20 @@ cudaError_t launch_bwd32(const BwdArgs& b, cudaStream_t st) {
     return bwd_io<__nv_bfloat16>(b, st);
 }
 
-cudaError_t launch_sum_parts(const float* part, void* out, int splits, int64_t n, int dtype, cudaStream_t st) {
-    const unsigned grid = (unsigned)ceil_div(n, 256);
-    if (dtype == 0) k_sum_parts<float><<<grid, 256, 0, st>>>(part, static_cast<float*>(out), splits, n);
-    else if (dtype == 1) k_sum_parts<__half><<<grid, 256, 0, st>>>(part, static_cast<__half*>(out), splits, n);
-    else k_sum_parts<__nv_bfloat16><<<grid, 256, 0, st>>>(part, static_cast<__nv_bfloat16*>(out), splits, n);
+template <typename T>
+cudaError_t sum_parts(const float* part, void* out, const float* part2, void* out2, int splits, int64_t n, cudaStream_t st) {
+    const bool vec = n % 4 == 0;
+    const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256), out2 ? 2 : 1);
+    T *o = static_cast<T*>(out), *o2 = static_cast<T*>(out2);
+    if (vec) k_sum_parts<T, true><<<grid, 256, 0, st>>>(part, o, part2, o2, splits, n);
+    else k_sum_parts<T, false><<<grid, 256, 0, st>>>(part, o, part2, o2, splits, n);
     return cudaGetLastError();
+}
+cudaError_t launch_sum_parts(const float* part, void* out, const float* part2, void* out2, int splits, int64_t n, int dtype,
+                             cudaStream_t st) {
+    if (dtype == 0) return sum_parts<float>(part, out, part2, out2, splits, n, st);
+    if (dtype == 1) return sum_parts<__half>(part, out, part2, out2, splits, n, st);
+    return sum_parts<__nv_bfloat16>(part, out, part2, out2, splits, n, st);
 }
 
 cudaError_t launch_sum_rows(const float* dg, float* part, float* out, int64_t rows, int64_t H, cudaStream_t st) {

@@ -15,8 +15,8 @@ struct TcMaps {
     CUtensorMap q, k, v, dy, y;
 };
 
-// How a walk over units (batch row, head, 64 value channels; in this order, the
-// last fastest) is cut: the first `whole` units are one block each, the other
+// How a walk over units (direction, batch row, head, 64 value channels; in this
+// order, the last fastest) is cut: the first `whole` units are one block each, the other
 // `cut` units K segments of seg tokens.  A cut unit's segments but the last are
 // walked twice: a sum pass gives the state each segment starts from.
 struct TcPlan {
@@ -46,16 +46,24 @@ inline TcPlan tc_plan(int64_t units, int64_t L, int64_t slots) {
     return best;
 }
 
+// What a walk starts from and leaves, one for each direction.
+struct TcDir {
+    const float* init;   // state before its first token, or null
+    float* last;         // state after its last token, or null
+    void* images;        // [Bsz, H, ptiles, chunks] of (high, low) operand tiles of the state before each chunk
+    float* image_scale;  // f16: the power of two each image was multiplied by
+};
+
+// A walk in one direction (dirs = 1: forward), or the backward's two at once:
+// units 0 .. and, from the middle of all units on, their reverse.
 struct TcWalkArgs {
     TcMaps maps;
     Args a;
     TcPlan plan;
-    const float* init;
+    TcDir dir[2];
+    int dirs;
     float* seg_state;  // [cut, K, N, 64]: end states of the segments, then (after the carry) their start states
     float* seg_decay;  // [cut, K]
-    float* last;
-    void* images;        // [Bsz, H, ptiles, chunks] of (high, low) operand tiles of the state before each chunk
-    float* image_scale;  // f16: the power of two each image was multiplied by
     int64_t chunks;
     int* status;
 };
@@ -94,8 +102,8 @@ struct TcBwdArgs {
 cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st);
 
 cudaError_t launch_tc_fwd(const TcWalkArgs& w, cudaStream_t st);
-cudaError_t launch_tc_state(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st);
-cudaError_t launch_tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st);
+cudaError_t launch_tc_state(const TcWalkArgs& w, bool sum, cudaStream_t st);
+cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st);
 
 }  // namespace la
 

@@ -163,43 +163,49 @@ template <int NB, int TH> __device__ __forceinline__ void save_state(const State
                 make_float4(X[c], X[c + 1], X[c + 2], X[c + 3]);
 }
 
-// The walk a block takes, from its index.
+// A unit's place, and the walk a block takes, from its index.
 struct Walk {
     int64_t b, h, hq, pt, p0, cut, seg, t_begin, t_end;
-    bool is_cut;
+    bool is_cut, reverse;
 
-    __device__ Walk(const TcWalkArgs& w, bool sum, bool reverse) {
+    __device__ void place(const TcWalkArgs& w, int64_t unit) {
         const Args& a = w.a;
-        const int64_t ptiles = (a.P + PT - 1) / PT;
+        const int64_t ptiles = (a.P + PT - 1) / PT, units = a.Bsz * a.H * ptiles;
+        reverse = unit >= units;
+        if (reverse) unit -= units;
+        pt = unit % ptiles;
+        p0 = pt * PT;
+        h = unit / ptiles % a.H;
+        b = unit / ptiles / a.H;
+        hq = h / (a.H / a.G);
+    }
+    __device__ Walk() {}
+    __device__ Walk(const TcWalkArgs& w, bool sum) {
         int64_t id = blockIdx.x, unit = id;
         is_cut = sum || id >= w.plan.whole;
         cut = seg = 0;
         if (is_cut) {
             if (!sum) id -= w.plan.whole;
             cut = id % w.plan.cut;
-            seg = id / w.plan.cut + (sum && reverse ? 1 : 0);  // the segment walked last needs no sum
+            seg = id / w.plan.cut;
             unit = w.plan.whole + cut;
         }
-        pt = unit % ptiles;
-        p0 = pt * PT;
-        h = unit / ptiles % a.H;
-        b = unit / ptiles / a.H;
-        hq = h / (a.H / a.G);
+        place(w, unit);
+        if (sum && reverse) seg += 1;  // the segment walked last needs no sum
         t_begin = is_cut ? seg * w.plan.seg : 0;
-        t_end = is_cut ? min(a.L, t_begin + w.plan.seg) : a.L;
+        t_end = is_cut ? min(w.a.L, t_begin + w.plan.seg) : w.a.L;
     }
-    __device__ StateTile start(const TcWalkArgs& w) const {
-        if (is_cut) return segment(w);
-        return whole(w, w.init);
-    }
+    __device__ const TcDir& dir(const TcWalkArgs& w) const { return w.dir[reverse]; }
+    __device__ StateTile start(const TcWalkArgs& w) const { return is_cut ? segment(w) : whole(w, dir(w).init); }
     __device__ StateTile segment(const TcWalkArgs& w) const {
         return {w.seg_state + (cut * w.plan.K + seg) * w.a.N * PT, w.a.N, PT, PT};
     }
     __device__ StateTile whole(const TcWalkArgs& w, const float* p) const {
         return {p ? p + (b * w.a.H + h) * w.a.N * w.a.P + p0 : nullptr, w.a.N, w.a.P, w.a.P - p0};
     }
-    __device__ bool ends(const TcWalkArgs& w, bool reverse) const {  // whether its last state is the walk's
-        return !is_cut || seg == (reverse ? 0 : w.plan.K - 1);
+    // where its last state goes, if that is the whole walk's
+    __device__ float* last(const TcWalkArgs& w) const {
+        return !is_cut || seg == (reverse ? 0 : w.plan.K - 1) ? dir(w).last : nullptr;
     }
 };
 template <int W> __device__ __forceinline__ float state_max(const float (&X)[W]) {
@@ -298,7 +304,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5;
     const bool out = tid >= C;  // output half, else state half
-    const Walk at(w, false, false);
+    const Walk at(w, false);
     const int64_t b = at.b, h = at.h, hq = at.hq, p0 = at.p0, t_begin = at.t_begin, t_end = at.t_end;
     const int64_t len = row_length(a, b);
     const int chunks = (int)((t_end - t_begin + C - 1) / C);
@@ -379,7 +385,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             add_product<NB, 128, 1>(tU, ex2(cl), 1.0f / vs, X);
             tc_fence_before();
         }
-        if (ch == chunks && w.last && at.ends(w, false)) save_state<NB, 128>(at.whole(w, w.last), X);
+        if (ch == chunks && at.last(w)) save_state<NB, 128>(at.whole(w, at.last(w)), X);
     } else {
         for (; ch < chunks; ch++) {
             const int64_t t0 = t_begin + (int64_t)ch * C;
@@ -541,7 +547,7 @@ template <int NB> struct StateSmem {
 };
 constexpr int kSplit = 256, kKeep = 256, kStateThreads = kSplit + kKeep + 64;
 
-template <typename T, int NB, bool REV, bool SUM>
+template <typename T, int NB, bool SUM>
 __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = StateSmem<NB>;
@@ -551,7 +557,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
     __shared__ uint32_t s_tm, s_red[2][4], s_most[8], s_fail;
     const Args& a = w.a;
     const int tid = threadIdx.x;
-    const Walk at(w, SUM, REV);
+    const Walk at(w, SUM);
+    const bool REV = at.reverse;
     const int64_t b = at.b, h = at.h, t_begin = at.t_begin, t_end = at.t_end;
     const int64_t len = row_length(a, b);
     const int chunks = (int)((t_end - t_begin + C - 1) / C);
@@ -638,9 +645,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
                 keep_sync();
                 if (lead) {
                     const int64_t at_image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + start_of(ch) / C;
-                    bulk_store(static_cast<char*>(w.images) + at_image * (2 * NB * 8192), image, 2 * NB * 8192);
+                    bulk_store(static_cast<char*>(at.dir(w).images) + at_image * (2 * NB * 8192), image, 2 * NB * 8192);
                     bulk_commit();
-                    if (kF16<T>) w.image_scale[at_image] = sc;
+                    if (kF16<T>) at.dir(w).image_scale[at_image] = sc;
                 }
             }
             wait_or_fail(&s_u[s], ph, &s_fail);
@@ -651,8 +658,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
         }
         if (SUM) {
             save_state<NB, kKeep>(at.segment(w), X);
-        } else if (w.last && at.ends(w, REV)) {
-            save_state<NB, kKeep>(at.whole(w, w.last), X);
+        } else if (at.last(w)) {
+            save_state<NB, kKeep>(at.whole(w, at.last(w)), X);
         }
         if (lead) bulk_wait_all();
     } else if (tid < kSplit + kKeep + 32) {  // ---------------- weights, tokens 4 lane .. 4 lane + 3
@@ -723,14 +730,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
 // seg_state: end state of each segment walked from zero -> the state each
 // segment starts from.  One thread per state element; eight segments' states are
 // on their way before the first is folded in.
-__global__ void __launch_bounds__(256) k_tc_carry(TcWalkArgs w, bool reverse) {
+__global__ void __launch_bounds__(256) k_tc_carry(const __grid_constant__ TcWalkArgs w) {
     constexpr int U = 8;
-    const Args& a = w.a;
-    const int64_t K = w.plan.K, tile = a.N * PT, x = (int64_t)blockIdx.x * 256 + threadIdx.x, cut = blockIdx.y;
+    const int64_t K = w.plan.K, tile = w.a.N * PT, x = (int64_t)blockIdx.x * 256 + threadIdx.x, cut = blockIdx.y;
     if (x >= tile) return;
-    const int64_t ptiles = (a.P + PT - 1) / PT, unit = w.plan.whole + cut;
-    const int64_t n = x / PT, p = unit % ptiles * PT + x % PT;
-    float S = w.init && p < a.P ? w.init[(unit / ptiles * a.N + n) * a.P + p] : 0.0f;
+    Walk at;
+    at.place(w, w.plan.whole + cut);
+    const bool reverse = at.reverse;
+    const StateTile from = at.whole(w, at.dir(w).init);
+    float S = from.p && x % PT < from.cols ? from.p[x / PT * from.stride + x % PT] : 0.0f;
     for (int64_t i0 = 0; i0 < K; i0 += U) {
         float own[U], d[U];
 #pragma unroll
@@ -761,13 +769,10 @@ template <auto Kernel> cudaError_t go(int threads, int smem, int64_t grid, const
 template <typename T, int NB> cudaError_t fwd_n(const TcWalkArgs& w, cudaStream_t st) {
     return go<k_tc_fwd<T, NB>>(256, FwdSmem<NB>::total, w.plan.blocks(), w, st);
 }
-template <typename T, int NB, bool REV> cudaError_t state_n(const TcWalkArgs& w, bool sum, cudaStream_t st) {
+template <typename T, int NB> cudaError_t state_n(const TcWalkArgs& w, bool sum, cudaStream_t st) {
     constexpr int smem = StateSmem<NB>::total;
-    return sum ? go<k_tc_state<T, NB, REV, true>>(kStateThreads, smem, w.plan.cut * (w.plan.K - 1), w, st)
-               : go<k_tc_state<T, NB, REV, false>>(kStateThreads, smem, w.plan.blocks(), w, st);
-}
-template <typename T, int NB> cudaError_t state_n(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st) {
-    return reverse ? state_n<T, NB, true>(w, sum, st) : state_n<T, NB, false>(w, sum, st);
+    return sum ? go<k_tc_state<T, NB, true>>(kStateThreads, smem, w.plan.cut * (w.plan.K - 1), w, st)
+               : go<k_tc_state<T, NB, false>>(kStateThreads, smem, w.plan.blocks(), w, st);
 }
 
 }  // namespace
@@ -778,16 +783,16 @@ cudaError_t launch_tc_fwd(const TcWalkArgs& w, cudaStream_t st) {
     return wide ? fwd_n<__nv_bfloat16, 2>(w, st) : fwd_n<__nv_bfloat16, 1>(w, st);
 }
 
-cudaError_t launch_tc_carry(const TcWalkArgs& w, bool reverse, cudaStream_t st) {
+cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st) {
     // cut < 2 * kSms blocks in y
-    k_tc_carry<<<dim3((unsigned)ceil_div(w.a.N * PT, 256), (unsigned)w.plan.cut), 256, 0, st>>>(w, reverse);
+    k_tc_carry<<<dim3((unsigned)ceil_div(w.a.N * PT, 256), (unsigned)w.plan.cut), 256, 0, st>>>(w);
     return cudaGetLastError();
 }
 
-cudaError_t launch_tc_state(const TcWalkArgs& w, bool reverse, bool sum, cudaStream_t st) {
+cudaError_t launch_tc_state(const TcWalkArgs& w, bool sum, cudaStream_t st) {
     const bool wide = w.a.N > 64;
-    if (w.a.dtype == 1) return wide ? state_n<__half, 2>(w, reverse, sum, st) : state_n<__half, 1>(w, reverse, sum, st);
-    return wide ? state_n<__nv_bfloat16, 2>(w, reverse, sum, st) : state_n<__nv_bfloat16, 1>(w, reverse, sum, st);
+    if (w.a.dtype == 1) return wide ? state_n<__half, 2>(w, sum, st) : state_n<__half, 1>(w, sum, st);
+    return wide ? state_n<__nv_bfloat16, 2>(w, sum, st) : state_n<__nv_bfloat16, 1>(w, sum, st);
 }
 
 }  // namespace la
