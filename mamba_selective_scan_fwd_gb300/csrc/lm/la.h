@@ -52,42 +52,49 @@ constexpr int kWalkP = 32;    // value channels per block of the token walk
 constexpr int kWalkT = 16;    // tokens staged at a time
 constexpr int kChunk32 = 64;  // tokens per chunk of the FP32 backward
 
-// The token walk: every (batch row, head, tile of value channels) is cut into
-// K segments of seg tokens (a multiple of a chunk).
+// The token walk: every unit (direction, batch row, head, tile of value
+// channels) is cut into K segments of seg tokens (a multiple of a chunk).
 struct WalkPlan {
     int64_t K, seg;
 };
+// About four blocks run on an SM.  The K with the fewest rounds of blocks times
+// tokens a block; cutting costs a sum pass (0.6 of a walk) and two launches
+// (about 60 tokens' time).
 inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t chunk) {
-    // enough blocks for four on every SM, segments of at least four chunks
-    int64_t K = (4 * kSms + units - 1) / (units > 0 ? units : 1);
-    const int64_t most = L / (4 * chunk);
-    if (K > most) K = most;
-    if (K < 1) K = 1;
-    int64_t seg = ceil_div(ceil_div(L, K), chunk) * chunk;
-    return {ceil_div(L, seg), seg};
+    const int64_t chunks = ceil_div(L, chunk), slots = 4 * kSms;
+    WalkPlan best = {1, chunks * chunk};
+    double least = (double)ceil_div(units, slots) * L;
+    for (int64_t K = 2; K <= 64 && K <= chunks; K++) {
+        const int64_t per = ceil_div(chunks, K);
+        if (ceil_div(chunks, per) != K) continue;
+        const double cost = (ceil_div(units * K, slots) + 0.6 * ceil_div(units * (K - 1), slots)) * (double)(per * chunk) + 60;
+        if (cost < 0.95 * least) {
+            least = cost;
+            best = {K, per * chunk};
+        }
+    }
+    return best;
 }
 
 enum WalkMode { kWalkSum = 0, kWalkY = 1, kWalkStates = 2 };
 
+// What a walk starts from and leaves, one for each direction.
+struct WalkDir {
+    const float* init;   // state before the walk's first token, or null
+    float* last;         // state after its last token, or null
+    float* chunk_state;  // kWalkStates: [Bsz, H, chunks, N, P] state before each chunk (in walking order)
+};
+
+// dirs = 1: forward; 2: the forward's and the reverse walk in one launch.
 struct WalkArgs {
     Args a;
     WalkPlan plan;
-    const float* init;   // state before the walk's first token, or null
-    float* seg_state;    // [Bsz, H, K, N, P]: end states of the segments, then (after the carry) their start states
-    float* seg_decay;    // [Bsz, H, K]
-    void* y;             // kWalkY
-    float* last;         // state after the walk's last token, or null
-    float* chunk_state;  // kWalkStates: [Bsz, H, chunks, N, P] state before each chunk (in walking order)
+    WalkDir dir[2];
+    int dirs;
+    float* seg_state;  // [dirs, Bsz, H, K, N, P]: end states of the segments, then (after the carry) their start states
+    float* seg_decay;  // [dirs, Bsz, H, K]
+    void* y;           // kWalkY
     int64_t chunks;
-};
-
-// Adds the incoming states up along the segments of a walk.
-struct CarryArgs {
-    float* seg_state;
-    const float* seg_decay;
-    const float* init;
-    int64_t BH, K, NP;
-    int reverse;
 };
 
 struct BwdArgs {
@@ -101,8 +108,8 @@ struct BwdArgs {
     int splits;           // parts the heads of one group are divided into
 };
 
-cudaError_t launch_walk32(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st);
-cudaError_t launch_carry(const CarryArgs& c, cudaStream_t st);
+cudaError_t launch_walk32(const WalkArgs& w, WalkMode mode, cudaStream_t st);
+cudaError_t launch_carry32(const WalkArgs& w, cudaStream_t st);
 cudaError_t launch_bwd32(const BwdArgs& b, cudaStream_t st);
 // out[i] = sum of the splits' part[., i] (n each), of one pair of arrays or (out2 given) of two
 cudaError_t launch_sum_parts(const float* part, void* out, const float* part2, void* out2, int splits, int64_t n, int dtype,

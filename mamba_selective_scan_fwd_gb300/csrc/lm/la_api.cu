@@ -43,13 +43,13 @@ struct Walk32 {
     WalkPlan plan;
     size_t state, decay;
 };
-Walk32 walk32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P) {
+Walk32 walk32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dirs) {
     Walk32 w;
-    w.plan = walk_plan(Bsz * H * ceil_div(P, kWalkP), L, kChunk32);
+    w.plan = walk_plan(dirs * Bsz * H * ceil_div(P, kWalkP), L, kChunk32);
     w.state = w.decay = 0;
     if (w.plan.K > 1) {
-        w.state = l.take((size_t)Bsz * H * w.plan.K * N * P * 4);
-        w.decay = l.take((size_t)Bsz * H * w.plan.K * 4);
+        w.state = l.take((size_t)dirs * Bsz * H * w.plan.K * N * P * 4);
+        w.decay = l.take((size_t)dirs * Bsz * H * w.plan.K * 4);
     }
     return w;
 }
@@ -70,7 +70,7 @@ int head_splits(int64_t blocks, int64_t rep) {
 }
 Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     Bwd32 b;
-    b.walk = walk32_layout(l, Bsz, L, H, N, P);
+    b.walk = walk32_layout(l, Bsz, L, H, N, P, 2);
     b.chunks = ceil_div(L, kChunk32);
     b.splits = head_splits(Bsz * b.chunks * G, H / G);
     const size_t states = (size_t)Bsz * H * b.chunks * N * P * 4;
@@ -142,7 +142,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dtype) {
     FwdPlan p = {};
     Layout l, t;
-    p.f32 = walk32_layout(l, Bsz, L, H, N, P);
+    p.f32 = walk32_layout(l, Bsz, L, H, N, P, 1);
     if (tc_sizes(L, N, P, dtype)) p.tc = walktc_layout(t, Bsz, L, H, N, P, 1, 2 * kSms);
     p.bytes = l.total > t.total ? l.total : t.total;
     return p;
@@ -284,14 +284,13 @@ int pass_state(float* to, const float* from, int64_t Bsz, int64_t H, int64_t N, 
 }
 
 // A walk over all segments: sums of the segments, their carries, then the walk itself.
-cudaError_t run_walk32(WalkArgs w, bool reverse, WalkMode mode, cudaStream_t st) {
+cudaError_t run_walk32(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
     if (w.plan.K > 1) {
-        cudaError_t e = launch_walk32(w, reverse, kWalkSum, st);
-        if (e != cudaSuccess) return e;
-        e = launch_carry({w.seg_state, w.seg_decay, w.init, w.a.Bsz * w.a.H, w.plan.K, w.a.N * w.a.P, reverse ? 1 : 0}, st);
+        cudaError_t e = launch_walk32(w, kWalkSum, st);
+        if (e == cudaSuccess) e = launch_carry32(w, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_walk32(w, reverse, mode, st);
+    return launch_walk32(w, mode, st);
 }
 
 bool strides_ok(int64_t token, int64_t batch) { return token >= 0 && batch >= 0 && token <= (1ll << 40) && batch <= (1ll << 48); }
@@ -338,12 +337,12 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
     WalkArgs w = {};
     w.a = a;
     w.plan = wl.plan;
-    w.init = a.h0;
+    w.dirs = 1;
+    w.dir[0] = {a.h0, d->last_state, nullptr};
     w.seg_state = reinterpret_cast<float*>(ws + wl.state);
     w.seg_decay = reinterpret_cast<float*>(ws + wl.decay);
     w.y = d->y;
-    w.last = d->last_state;
-    return run_walk32(w, false, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+    return run_walk32(w, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 size_t ss_la_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
@@ -402,13 +401,10 @@ int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
     w.seg_state = f32(bl.walk.state);
     w.seg_decay = f32(bl.walk.decay);
     w.chunks = bl.chunks;
-    w.init = a.h0;
-    w.chunk_state = f32(bl.before);
-    if (run_walk32(w, false, kWalkStates, st) != cudaSuccess) return SS_ERR_CUDA;
-    w.init = a.dlast;
-    w.chunk_state = f32(bl.after);
-    w.last = d->dh0;
-    if (run_walk32(w, true, kWalkStates, st) != cudaSuccess) return SS_ERR_CUDA;
+    w.dirs = 2;
+    w.dir[0] = {a.h0, nullptr, f32(bl.before)};
+    w.dir[1] = {a.dlast, d->dh0, f32(bl.after)};
+    if (run_walk32(w, kWalkStates, st) != cudaSuccess) return SS_ERR_CUDA;
     BwdArgs b = {};
     b.a = a;
     b.before = f32(bl.before);

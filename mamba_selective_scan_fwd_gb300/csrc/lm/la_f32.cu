@@ -8,6 +8,7 @@
 // decay enters as S + (e^g - 1) S: a rounded e^g near 1 would be off by the same
 // 2^-25 at every token and add up over a long memory.  The
 // backward works on chunks of 64 tokens from the states at their borders.
+#include "../simd.cuh"
 #include "la_dev.cuh"
 
 namespace ss {
@@ -15,19 +16,21 @@ namespace la {
 namespace {
 
 // One block: kWalkP value channels of one head, one segment of tokens.  Lane =
-// value channel, warp = NR of the padded N state rows.
+// value channel, warp = NR of the padded N state rows, in pairs.
 //   forward   S <- e^g S + k v^T, y = scale q S
 //   reverse   X <- e^g (X + scale q dy^T), tokens last to first (X before the
 //             update is the adjoint of the state after the token)
-template <typename T, int NR, bool REV, int MODE>
+// The next kWalkT tokens are loaded into registers while these are computed.
+template <typename T, int NR, int MODE>
 __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
-    constexpr int NP = NR * 8;
-    constexpr int TT = kWalkT;
+    constexpr int NP = NR * 8, TT = kWalkT;
+    constexpr bool Y = MODE == kWalkY;
+    constexpr int EK = TT * NP / 256, EV = TT * kWalkP / 256;  // values a thread loads
     __shared__ __align__(16) float s_k[TT][NP];
-    __shared__ __align__(16) float s_q[MODE == kWalkY ? TT : 1][NP];
+    __shared__ __align__(16) float s_q[Y ? TT : 1][NP];
     __shared__ float s_v[TT][kWalkP];
     __shared__ float s_a[TT], s_g[TT];
-    __shared__ float s_y[MODE == kWalkY ? 8 : 1][TT][kWalkP];
+    __shared__ float s_y[Y ? 8 : 1][TT][kWalkP];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t ptiles = (a.P + kWalkP - 1) / kWalkP;
@@ -38,95 +41,117 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
     id /= a.H;
     const int64_t segs = MODE == kWalkSum ? w.plan.K - 1 : w.plan.K;
     int64_t seg = id % segs;
-    const int64_t b = id / segs;
-    if (MODE == kWalkSum && REV) seg += 1;  // the segment walked last needs no sum
-    const int64_t hq = h / (a.H / a.G);
+    id /= segs;
+    const int64_t b = id % a.Bsz;
+    const bool rev = id / a.Bsz != 0;
+    if (MODE == kWalkSum && rev) seg += 1;  // the segment walked last needs no sum
+    const int64_t hq = h / (a.H / a.G), bh = b * a.H + h, at = ((rev ? a.Bsz * a.H : 0) + bh) * w.plan.K + seg;
     const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
     const int64_t len = row_length(a, b);
     const int64_t p = p0 + lane;
     const int n0 = warp * NR;
     const int64_t NPel = a.N * a.P;
-    const In& kin = REV ? a.q : a.k;
-    const In& vin = REV ? a.dy : a.v;
+    const In& kin = rev ? a.q : a.k;
+    const In& vin = rev ? a.dy : a.v;
     const T* kp = static_cast<const T*>(kin.p) + b * kin.batch + hq * a.N;
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
     const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P;
-    const float kscale = REV ? a.scale : 1.0f;
+    const float kscale = rev ? a.scale : 1.0f;
+    const WalkDir& dir = w.dir[rev];
 
-    float S[NR];
+    float2 S[NR / 2];
     const float* init = nullptr;
     if (MODE != kWalkSum) {
-        if (w.plan.K > 1) init = w.seg_state + ((b * a.H + h) * w.plan.K + seg) * NPel;
-        else if (w.init) init = w.init + (b * a.H + h) * NPel;
+        if (w.plan.K > 1) init = w.seg_state + at * NPel;
+        else if (dir.init) init = dir.init + bh * NPel;
     }
+    auto from = [&](int n) { return init && n < a.N && p < a.P ? init[n * a.P + p] : 0.0f; };
 #pragma unroll
-    for (int r = 0; r < NR; r++) S[r] = (init && n0 + r < a.N && p < a.P) ? init[(n0 + r) * a.P + p] : 0.0f;
+    for (int r = 0; r < NR / 2; r++) S[r] = make_float2(from(n0 + 2 * r), from(n0 + 2 * r + 1));
     auto put = [&](float* dst) {
 #pragma unroll
-        for (int r = 0; r < NR; r++)
-            if (n0 + r < a.N && p < a.P) dst[(n0 + r) * a.P + p] = S[r];
+        for (int r = 0; r < NR / 2; r++) {
+            if (n0 + 2 * r < a.N && p < a.P) dst[(n0 + 2 * r) * a.P + p] = S[r].x;
+            if (n0 + 2 * r + 1 < a.N && p < a.P) dst[(n0 + 2 * r + 1) * a.P + p] = S[r].y;
+        }
     };
 
-    float total = 0.0f;  // thread 0 of a sum pass: the segment's log decay
     const int64_t tiles = (t_end - t_begin + TT - 1) / TT;
+    auto start_of = [&](int64_t i) { return t_begin + (rev ? tiles - 1 - i : i) * TT; };
+    auto valid = [&](int64_t t0) { return (int)max((int64_t)0, min((int64_t)TT, min(len, t_end) - t0)); };  // tokens that count
+    float rk[EK], rq[Y ? EK : 1], rv[EV], rg = 0.0f;
+    auto fetch = [&](int64_t i) {
+        const int64_t t0 = start_of(i);
+        const int nv = valid(t0);
+#pragma unroll
+        for (int e = 0; e < EK; e++) {
+            const int t = (tid + 256 * e) / NP, n = (tid + 256 * e) % NP;
+            rk[e] = (t < nv && n < a.N) ? kscale * ldf(kp + (t0 + t) * kin.token + n) : 0.0f;
+            if (Y) rq[e] = (t < nv && n < a.N) ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < EV; e++) {
+            const int t = (tid + 256 * e) / kWalkP, c = (tid + 256 * e) % kWalkP;
+            rv[e] = (t < nv && p0 + c < a.P) ? ldf(vp + (t0 + t) * vin.token + p0 + c) : 0.0f;
+        }
+        if (tid < TT) rg = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
+    };
+    fetch(0);
+    float total = 0.0f;  // thread 0 of a sum pass: the segment's log decay
     for (int64_t i = 0; i < tiles; i++) {
-        const int64_t t0 = t_begin + (REV ? tiles - 1 - i : i) * TT;
+        const int64_t t0 = start_of(i);
         if (MODE == kWalkStates) {
             const int64_t c = t0 / kChunk32;
-            const bool first = REV ? (t0 + TT >= t_end || (t0 + TT) % kChunk32 == 0) : t0 % kChunk32 == 0;
-            if (first) put(w.chunk_state + ((b * a.H + h) * w.chunks + c) * NPel);
+            const bool first = rev ? (t0 + TT >= t_end || (t0 + TT) % kChunk32 == 0) : t0 % kChunk32 == 0;
+            if (first) put(dir.chunk_state + (bh * w.chunks + c) * NPel);
         }
+        const int nv = valid(t0);
         __syncthreads();
-        const int nv = (int)max((int64_t)0, min((int64_t)TT, min(len, t_end) - t0));  // tokens that count
-        for (int e = tid; e < TT * NP; e += 256) {
-            const int t = e / NP, n = e % NP;
-            s_k[t][n] = (t < nv && n < a.N) ? kscale * ldf(kp + (t0 + t) * kin.token + n) : 0.0f;
-            if (MODE == kWalkY) s_q[t][n] = (t < nv && n < a.N) ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < EK; e++) {
+            (&s_k[0][0])[tid + 256 * e] = rk[e];
+            if (Y) (&s_q[0][0])[tid + 256 * e] = rq[e];
         }
-        for (int e = tid; e < TT * kWalkP; e += 256) {
-            const int t = e / kWalkP, c = e % kWalkP;
-            s_v[t][c] = (t < nv && p0 + c < a.P) ? ldf(vp + (t0 + t) * vin.token + p0 + c) : 0.0f;
-        }
+#pragma unroll
+        for (int e = 0; e < EV; e++) (&s_v[0][0])[tid + 256 * e] = rv[e];
         if (tid < TT) {
-            const float g = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
-            s_g[tid] = g;
-            s_a[tid] = expm1f(g);
+            s_g[tid] = rg;
+            s_a[tid] = expm1f(rg);
         }
         __syncthreads();
+        if (i + 1 < tiles) fetch(i + 1);
         if (MODE == kWalkSum && tid == 0)
             for (int t = 0; t < nv; t++) total += s_g[t];
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < nv; j++) {
-            const int t = REV ? nv - 1 - j : j;
-            const float av = s_a[t], v = s_v[t][lane];
-            float acc = 0.0f;
+            const int t = rev ? nv - 1 - j : j;
+            const float2 av = splat2(s_a[t]), v = splat2(s_v[t][lane]);
+            float2 acc[2] = {splat2(0.0f), splat2(0.0f)};
 #pragma unroll
-            for (int r = 0; r < NR; r += 4) {
-                const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + r]);
-                if (REV) {
-                    const float x0 = fmaf(kk.x, v, S[r]), x1 = fmaf(kk.y, v, S[r + 1]);
-                    const float x2 = fmaf(kk.z, v, S[r + 2]), x3 = fmaf(kk.w, v, S[r + 3]);
-                    S[r] = fmaf(av, x0, x0);
-                    S[r + 1] = fmaf(av, x1, x1);
-                    S[r + 2] = fmaf(av, x2, x2);
-                    S[r + 3] = fmaf(av, x3, x3);
+            for (int r = 0; r < NR / 2; r += 2) {
+                const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
+                const float2 k0 = make_float2(kk.x, kk.y), k1 = make_float2(kk.z, kk.w);
+                if (rev) {
+                    S[r] = fma2(k0, v, S[r]);
+                    S[r + 1] = fma2(k1, v, S[r + 1]);
+                    S[r] = fma2(av, S[r], S[r]);
+                    S[r + 1] = fma2(av, S[r + 1], S[r + 1]);
                 } else {
-                    S[r] = fmaf(kk.x, v, fmaf(av, S[r], S[r]));
-                    S[r + 1] = fmaf(kk.y, v, fmaf(av, S[r + 1], S[r + 1]));
-                    S[r + 2] = fmaf(kk.z, v, fmaf(av, S[r + 2], S[r + 2]));
-                    S[r + 3] = fmaf(kk.w, v, fmaf(av, S[r + 3], S[r + 3]));
+                    S[r] = fma2(k0, v, fma2(av, S[r], S[r]));
+                    S[r + 1] = fma2(k1, v, fma2(av, S[r + 1], S[r + 1]));
                 }
-                if (MODE == kWalkY) {
-                    const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + r]);
-                    acc = fmaf(qq.x, S[r], acc);
-                    acc = fmaf(qq.y, S[r + 1], acc);
-                    acc = fmaf(qq.z, S[r + 2], acc);
-                    acc = fmaf(qq.w, S[r + 3], acc);
+                if (Y) {
+                    const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
+                    acc[0] = fma2(make_float2(qq.x, qq.y), S[r], acc[0]);
+                    acc[1] = fma2(make_float2(qq.z, qq.w), S[r + 1], acc[1]);
                 }
             }
-            if (MODE == kWalkY) s_y[warp][t][lane] = acc;
+            if (Y) {
+                const float2 s = add2(acc[0], acc[1]);
+                s_y[warp][t][lane] = s.x + s.y;
+            }
         }
-        if (MODE == kWalkY) {
+        if (Y) {
             __syncthreads();
             T* yp = static_cast<T*>(w.y) + (b * a.L * a.H + h) * a.P;
             for (int e = tid; e < TT * kWalkP; e += 256) {
@@ -143,36 +168,39 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
         }
     }
     if (MODE == kWalkSum) {
-        put(w.seg_state + ((b * a.H + h) * w.plan.K + seg) * NPel);
-        if (tid == 0 && p0 == 0) w.seg_decay[(b * a.H + h) * w.plan.K + seg] = total;
-    } else if (w.last && seg == (REV ? 0 : w.plan.K - 1)) {
-        put(w.last + (b * a.H + h) * NPel);
+        put(w.seg_state + at * NPel);
+        if (tid == 0 && p0 == 0) w.seg_decay[at] = total;
+    } else if (dir.last && seg == (rev ? 0 : w.plan.K - 1)) {
+        put(dir.last + bh * NPel);
     }
 }
 
 // seg_state: end state of each segment walked from zero -> the state each
 // segment starts from.  One thread per state element; eight segments' states are
 // on their way before the first is folded in (one memory wait per eight).
-__global__ void __launch_bounds__(256) k_carry(CarryArgs c) {
+__global__ void __launch_bounds__(256) k_carry32(WalkArgs w, int64_t first) {
     constexpr int U = 8;
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y;
-    if (x >= c.NP) return;
-    float S = c.init ? c.init[bh * c.NP + x] : 0.0f;
-    for (int64_t i0 = 0; i0 < c.K; i0 += U) {
+    const int64_t K = w.plan.K, BH = w.a.Bsz * w.a.H, NP = w.a.N * w.a.P;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, unit = first + blockIdx.y;
+    if (x >= NP) return;
+    const bool rev = unit >= BH;
+    const float* init = w.dir[rev].init;
+    float S = init ? init[(unit - (rev ? BH : 0)) * NP + x] : 0.0f;
+    for (int64_t i0 = 0; i0 < K; i0 += U) {
         float own[U], d[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int64_t i = i0 + u, s = bh * c.K + (c.reverse ? c.K - 1 - i : i);
+            const int64_t i = i0 + u, s = unit * K + (rev ? K - 1 - i : i);
             own[u] = d[u] = 0.0f;
-            if (i + 1 < c.K) {  // the segment walked last has no sum
-                own[u] = c.seg_state[s * c.NP + x];
-                d[u] = expf(c.seg_decay[s]);
+            if (i + 1 < K) {  // the segment walked last has no sum
+                own[u] = w.seg_state[s * NP + x];
+                d[u] = expf(w.seg_decay[s]);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int64_t i = i0 + u, s = bh * c.K + (c.reverse ? c.K - 1 - i : i);
-            if (i < c.K) c.seg_state[s * c.NP + x] = S;
+            const int64_t i = i0 + u, s = unit * K + (rev ? K - 1 - i : i);
+            if (i < K) w.seg_state[s * NP + x] = S;
             S = fmaf(d[u], S, own[u]);
         }
     }
@@ -540,24 +568,20 @@ __global__ void __launch_bounds__(256) k_sum_rows(const float* x, float* part, i
     }
 }
 
-template <typename T, int NR, bool REV> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+template <typename T, int NR> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
     const Args& a = w.a;
     const int64_t segs = mode == kWalkSum ? w.plan.K - 1 : w.plan.K;
-    const unsigned grid = (unsigned)(ceil_div(a.P, kWalkP) * a.H * a.Bsz * segs);
-    if (mode == kWalkSum) k_walk32<T, NR, REV, kWalkSum><<<grid, 256, 0, st>>>(w);
-    else if (mode == kWalkStates) k_walk32<T, NR, REV, kWalkStates><<<grid, 256, 0, st>>>(w);
-    else if constexpr (!REV) k_walk32<T, NR, REV, kWalkY><<<grid, 256, 0, st>>>(w);
+    const unsigned grid = (unsigned)(ceil_div(a.P, kWalkP) * a.H * a.Bsz * w.dirs * segs);
+    if (mode == kWalkSum) k_walk32<T, NR, kWalkSum><<<grid, 256, 0, st>>>(w);
+    else if (mode == kWalkStates) k_walk32<T, NR, kWalkStates><<<grid, 256, 0, st>>>(w);
+    else k_walk32<T, NR, kWalkY><<<grid, 256, 0, st>>>(w);
     return cudaGetLastError();
 }
 
-template <typename T, bool REV> cudaError_t walk_n(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
-    if (w.a.N <= 32) return walk_mode<T, 4, REV>(w, mode, st);
-    if (w.a.N <= 64) return walk_mode<T, 8, REV>(w, mode, st);
-    return walk_mode<T, 16, REV>(w, mode, st);
-}
-
-template <typename T> cudaError_t walk_io(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st) {
-    return reverse ? walk_n<T, true>(w, mode, st) : walk_n<T, false>(w, mode, st);
+template <typename T> cudaError_t walk_io(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+    if (w.a.N <= 32) return walk_mode<T, 4>(w, mode, st);
+    if (w.a.N <= 64) return walk_mode<T, 8>(w, mode, st);
+    return walk_mode<T, 16>(w, mode, st);
 }
 
 template <typename T, int NB> cudaError_t bwd_n(const BwdArgs& b, cudaStream_t st) {
@@ -576,21 +600,18 @@ template <typename T> cudaError_t bwd_io(const BwdArgs& b, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_walk32(const WalkArgs& w, bool reverse, WalkMode mode, cudaStream_t st) {
-    if (w.a.dtype == 0) return walk_io<float>(w, reverse, mode, st);
-    if (w.a.dtype == 1) return walk_io<__half>(w, reverse, mode, st);
-    return walk_io<__nv_bfloat16>(w, reverse, mode, st);
+cudaError_t launch_walk32(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+    if (w.a.dtype == 0) return walk_io<float>(w, mode, st);
+    if (w.a.dtype == 1) return walk_io<__half>(w, mode, st);
+    return walk_io<__nv_bfloat16>(w, mode, st);
 }
 
-cudaError_t launch_carry(const CarryArgs& c, cudaStream_t st) {
-    // grid.y: at most 2^16 - 1 (batch row, head) pairs a launch
-    for (int64_t at = 0; at < c.BH; at += 65535) {
-        CarryArgs part = c;
-        part.BH = c.BH - at < 65535 ? c.BH - at : 65535;
-        part.seg_state += at * c.K * c.NP;
-        part.seg_decay += at * c.K;
-        if (part.init) part.init += at * c.NP;
-        k_carry<<<dim3((unsigned)ceil_div(c.NP, 256), (unsigned)part.BH), 256, 0, st>>>(part);
+cudaError_t launch_carry32(const WalkArgs& w, cudaStream_t st) {
+    // grid.y: at most 2^16 - 1 (direction, batch row, head) units a launch
+    const int64_t units = w.dirs * w.a.Bsz * w.a.H;
+    for (int64_t at = 0; at < units; at += 65535) {
+        const int64_t n = units - at < 65535 ? units - at : 65535;
+        k_carry32<<<dim3((unsigned)ceil_div(w.a.N * w.a.P, 256), (unsigned)n), 256, 0, st>>>(w, at);
     }
     return cudaGetLastError();
 }
