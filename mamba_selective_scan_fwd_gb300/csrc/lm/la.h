@@ -48,8 +48,8 @@ constexpr int kSms = 152;
 constexpr int kMaxN = 128;
 
 // ---------------------------------------------------------------- FP32 path
-constexpr int kWalkP = 32;    // value channels per block of the token walk
-constexpr int kWalkT = 16;    // tokens staged at a time
+constexpr int kWalkP = 64;    // value channels per block of the token walk
+constexpr int kWalkT = 16;    // tokens staged at a time (at most)
 constexpr int kChunk32 = 64;  // tokens per chunk of the FP32 backward
 
 // The token walk: every unit (direction, batch row, head, tile of value
@@ -57,11 +57,11 @@ constexpr int kChunk32 = 64;  // tokens per chunk of the FP32 backward
 struct WalkPlan {
     int64_t K, seg;
 };
-// About four blocks run on an SM.  The K with the fewest rounds of blocks times
+// Three blocks run on an SM.  The K with the fewest rounds of blocks times
 // tokens a block; cutting costs a sum pass (0.6 of a walk) and two launches
 // (about 60 tokens' time).
 inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t chunk) {
-    const int64_t chunks = ceil_div(L, chunk), slots = 4 * kSms;
+    const int64_t chunks = ceil_div(L, chunk), slots = 3 * kSms;
     WalkPlan best = {1, chunks * chunk};
     double least = (double)ceil_div(units, slots) * L;
     for (int64_t K = 2; K <= 64 && K <= chunks; K++) {

@@ -15,22 +15,24 @@ namespace ss {
 namespace la {
 namespace {
 
-// One block: kWalkP value channels of one head, one segment of tokens.  Lane =
-// value channel, warp = NR of the padded N state rows, in pairs.
+// One block: kWalkP value channels of one head, one segment of tokens.  Lane = two
+// value channels 32 apart, warp = NR of the padded N state rows, in pairs.  The
+// rows' k and q are broadcasts from shared memory, which is what bounds it: two
+// channels a lane halve them.
 //   forward   S <- e^g S + k v^T, y = scale q S
 //   reverse   X <- e^g (X + scale q dy^T), tokens last to first (X before the
 //             update is the adjoint of the state after the token)
-// The next kWalkT tokens are loaded into registers while these are computed.
+// The next TT tokens are loaded into registers while these are computed.
 template <typename T, int NR, int MODE>
-__global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
-    constexpr int NP = NR * 8, TT = kWalkT;
+__global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
     constexpr bool Y = MODE == kWalkY;
+    constexpr int NP = NR * 8, TT = Y && NR == 16 ? kWalkT / 2 : kWalkT;
     constexpr int EK = TT * NP / 256, EV = TT * kWalkP / 256;  // values a thread loads
     __shared__ __align__(16) float s_k[TT][NP];
     __shared__ __align__(16) float s_q[Y ? TT : 1][NP];
     __shared__ float s_v[TT][kWalkP];
     __shared__ float s_a[TT], s_g[TT];
-    __shared__ float s_y[Y ? 8 : 1][TT][kWalkP];
+    __shared__ float s_y[Y ? 8 : 1][Y ? TT : 1][kWalkP];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t ptiles = (a.P + kWalkP - 1) / kWalkP;
@@ -48,7 +50,6 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
     const int64_t hq = h / (a.H / a.G), bh = b * a.H + h, at = ((rev ? a.Bsz * a.H : 0) + bh) * w.plan.K + seg;
     const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
     const int64_t len = row_length(a, b);
-    const int64_t p = p0 + lane;
     const int n0 = warp * NR;
     const int64_t NPel = a.N * a.P;
     const In& kin = rev ? a.q : a.k;
@@ -59,20 +60,28 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
     const float kscale = rev ? a.scale : 1.0f;
     const WalkDir& dir = w.dir[rev];
 
-    float2 S[NR / 2];
+    float2 S[2][NR / 2];  // [channel][pair of rows]
     const float* init = nullptr;
     if (MODE != kWalkSum) {
         if (w.plan.K > 1) init = w.seg_state + at * NPel;
         else if (dir.init) init = dir.init + bh * NPel;
     }
-    auto from = [&](int n) { return init && n < a.N && p < a.P ? init[n * a.P + p] : 0.0f; };
 #pragma unroll
-    for (int r = 0; r < NR / 2; r++) S[r] = make_float2(from(n0 + 2 * r), from(n0 + 2 * r + 1));
+    for (int c = 0; c < 2; c++) {
+        const int64_t p = p0 + lane + 32 * c;
+        auto from = [&](int n) { return init && n < a.N && p < a.P ? init[n * a.P + p] : 0.0f; };
+#pragma unroll
+        for (int r = 0; r < NR / 2; r++) S[c][r] = make_float2(from(n0 + 2 * r), from(n0 + 2 * r + 1));
+    }
     auto put = [&](float* dst) {
 #pragma unroll
-        for (int r = 0; r < NR / 2; r++) {
-            if (n0 + 2 * r < a.N && p < a.P) dst[(n0 + 2 * r) * a.P + p] = S[r].x;
-            if (n0 + 2 * r + 1 < a.N && p < a.P) dst[(n0 + 2 * r + 1) * a.P + p] = S[r].y;
+        for (int c = 0; c < 2; c++) {
+            const int64_t p = p0 + lane + 32 * c;
+#pragma unroll
+            for (int r = 0; r < NR / 2; r++) {
+                if (n0 + 2 * r < a.N && p < a.P) dst[(n0 + 2 * r) * a.P + p] = S[c][r].x;
+                if (n0 + 2 * r + 1 < a.N && p < a.P) dst[(n0 + 2 * r + 1) * a.P + p] = S[c][r].y;
+            }
         }
     };
 
@@ -122,34 +131,41 @@ __global__ void __launch_bounds__(256) k_walk32(WalkArgs w) {
         if (i + 1 < tiles) fetch(i + 1);
         if (MODE == kWalkSum && tid == 0)
             for (int t = 0; t < nv; t++) total += s_g[t];
-#pragma unroll 4
+#pragma unroll 2
         for (int j = 0; j < nv; j++) {
             const int t = rev ? nv - 1 - j : j;
-            const float2 av = splat2(s_a[t]), v = splat2(s_v[t][lane]);
-            float2 acc[2] = {splat2(0.0f), splat2(0.0f)};
+            const float2 av = splat2(s_a[t]), v[2] = {splat2(s_v[t][lane]), splat2(s_v[t][lane + 32])};
+            float2 acc[2][2] = {{splat2(0.0f), splat2(0.0f)}, {splat2(0.0f), splat2(0.0f)}};
 #pragma unroll
             for (int r = 0; r < NR / 2; r += 2) {
                 const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
-                const float2 k0 = make_float2(kk.x, kk.y), k1 = make_float2(kk.z, kk.w);
-                if (rev) {
-                    S[r] = fma2(k0, v, S[r]);
-                    S[r + 1] = fma2(k1, v, S[r + 1]);
-                    S[r] = fma2(av, S[r], S[r]);
-                    S[r + 1] = fma2(av, S[r + 1], S[r + 1]);
-                } else {
-                    S[r] = fma2(k0, v, fma2(av, S[r], S[r]));
-                    S[r + 1] = fma2(k1, v, fma2(av, S[r + 1], S[r + 1]));
-                }
+                const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
+                float2 qr[2];
                 if (Y) {
                     const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
-                    acc[0] = fma2(make_float2(qq.x, qq.y), S[r], acc[0]);
-                    acc[1] = fma2(make_float2(qq.z, qq.w), S[r + 1], acc[1]);
+                    qr[0] = make_float2(qq.x, qq.y);
+                    qr[1] = make_float2(qq.z, qq.w);
                 }
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        float2& x = S[c][r + u];
+                        if (rev) {
+                            x = fma2(kr[u], v[c], x);
+                            x = fma2(av, x, x);
+                        } else {
+                            x = fma2(kr[u], v[c], fma2(av, x, x));
+                        }
+                        if (Y) acc[c][u] = fma2(qr[u], x, acc[c][u]);
+                    }
             }
-            if (Y) {
-                const float2 s = add2(acc[0], acc[1]);
-                s_y[warp][t][lane] = s.x + s.y;
-            }
+            if (Y)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const float2 s = add2(acc[c][0], acc[c][1]);
+                    s_y[warp][t][lane + 32 * c] = s.x + s.y;
+                }
         }
         if (Y) {
             __syncthreads();
