@@ -8,6 +8,8 @@
 // decay enters as S + (e^g - 1) S: a rounded e^g near 1 would be off by the same
 // 2^-25 at every token and add up over a long memory.  The
 // backward works on chunks of 64 tokens from the states at their borders.
+#include <type_traits>
+
 #include "../simd.cuh"
 #include "la_dev.cuh"
 
@@ -131,42 +133,48 @@ __global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
         if (i + 1 < tiles) fetch(i + 1);
         if (MODE == kWalkSum && tid == 0)
             for (int t = 0; t < nv; t++) total += s_g[t];
+        // the direction as a constant: a test in the innermost loop doubled its instructions
+        auto tokens = [&](auto direction) {
+            constexpr bool R = decltype(direction)::value;
 #pragma unroll 2
-        for (int j = 0; j < nv; j++) {
-            const int t = rev ? nv - 1 - j : j;
-            const float2 av = splat2(s_a[t]), v[2] = {splat2(s_v[t][lane]), splat2(s_v[t][lane + 32])};
-            float2 acc[2][2] = {{splat2(0.0f), splat2(0.0f)}, {splat2(0.0f), splat2(0.0f)}};
+            for (int j = 0; j < nv; j++) {
+                const int t = R ? nv - 1 - j : j;
+                const float2 av = splat2(s_a[t]), v[2] = {splat2(s_v[t][lane]), splat2(s_v[t][lane + 32])};
+                float2 acc[2][2] = {{splat2(0.0f), splat2(0.0f)}, {splat2(0.0f), splat2(0.0f)}};
 #pragma unroll
-            for (int r = 0; r < NR / 2; r += 2) {
-                const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
-                const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
-                float2 qr[2];
-                if (Y) {
-                    const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
-                    qr[0] = make_float2(qq.x, qq.y);
-                    qr[1] = make_float2(qq.z, qq.w);
-                }
+                for (int r = 0; r < NR / 2; r += 2) {
+                    const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
+                    const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
+                    float2 qr[2];
+                    if (Y) {
+                        const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
+                        qr[0] = make_float2(qq.x, qq.y);
+                        qr[1] = make_float2(qq.z, qq.w);
+                    }
 #pragma unroll
-                for (int c = 0; c < 2; c++)
+                    for (int c = 0; c < 2; c++)
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        float2& x = S[c][r + u];
-                        if (rev) {
-                            x = fma2(kr[u], v[c], x);
-                            x = fma2(av, x, x);
-                        } else {
-                            x = fma2(kr[u], v[c], fma2(av, x, x));
+                        for (int u = 0; u < 2; u++) {
+                            float2& x = S[c][r + u];
+                            if (R) {
+                                x = fma2(kr[u], v[c], x);
+                                x = fma2(av, x, x);
+                            } else {
+                                x = fma2(kr[u], v[c], fma2(av, x, x));
+                            }
+                            if (Y) acc[c][u] = fma2(qr[u], x, acc[c][u]);
                         }
-                        if (Y) acc[c][u] = fma2(qr[u], x, acc[c][u]);
+                }
+                if (Y)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        const float2 s = add2(acc[c][0], acc[c][1]);
+                        s_y[warp][t][lane + 32 * c] = s.x + s.y;
                     }
             }
-            if (Y)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    const float2 s = add2(acc[c][0], acc[c][1]);
-                    s_y[warp][t][lane + 32 * c] = s.x + s.y;
-                }
-        }
+        };
+        if (!Y && rev) tokens(std::true_type{});
+        else tokens(std::false_type{});
         if (Y) {
             __syncthreads();
             T* yp = static_cast<T*>(w.y) + (b * a.L * a.H + h) * a.P;
