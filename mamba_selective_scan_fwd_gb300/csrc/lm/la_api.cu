@@ -91,13 +91,18 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 
 // [Bsz, L, heads, width] as a map {width, heads, L, Bsz}, boxes of 64 columns
 // by 128 tokens in the 128-byte swizzle; what lies outside reads as zero.
+// (f32: boxes of 32 columns)
 bool tc_map(EncodeTiledFn encode, CUtensorMap* m, const In& x, int64_t heads, int64_t width, int64_t L, int64_t Bsz, int dtype) {
+    const cuuint64_t esz = dtype == SS_F32 ? 4 : 2;
     const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)Bsz};
     // the stride of a dimension of one is never used, but has to be valid
     const int64_t token = L > 1 ? x.token : heads * width, batch = Bsz > 1 ? x.batch : heads * width;
-    const cuuint64_t strides[3] = {(cuuint64_t)(width * 2), (cuuint64_t)(token * 2), (cuuint64_t)(batch * 2)};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)kChunkTc, 1}, step[4] = {1, 1, 1, 1};
-    return encode(m, dtype == SS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+    const cuuint64_t strides[3] = {width * esz, token * esz, batch * esz};
+    const cuuint32_t box[4] = {(cuuint32_t)(128 / esz), 1, (cuuint32_t)kChunkTc, 1}, step[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = dtype == SS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == SS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode(m, type, 4,
                   const_cast<void*>(x.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -224,22 +229,25 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     if (!encode) return SS_OK;
     TcWalkArgs w = {};
     TcBwdArgs b = {};
-    const In dq = {d.dq, a.G * a.N, a.L * a.G * a.N}, dk = {d.dk, a.G * a.N, a.L * a.G * a.N},
+    char* ws = static_cast<char*>(d.workspace);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    Layout l;
+    const BwdTc bl = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P, a.dtype);
+    const bool parts = bl.splits > 1;
+    const int64_t qk_rows = parts ? bl.splits * a.Bsz : a.Bsz;
+    const int qk_type = parts ? SS_F32 : a.dtype;
+    const In dq = {parts ? ws + bl.dq : d.dq, a.G * a.N, a.L * a.G * a.N}, dk = {parts ? ws + bl.dk : d.dk, a.G * a.N, a.L * a.G * a.N},
              dv = {d.dv, a.H * a.P, a.L * a.H * a.P};
     if (!tc_map(encode, &b.maps.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &b.maps.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &b.maps.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &b.maps.dy, a.dy, a.H, a.P, a.L, a.Bsz, a.dtype) ||
-        !tc_map(encode, &b.maps.dq, dq, a.G, a.N, a.L, a.Bsz, a.dtype) ||
-        !tc_map(encode, &b.maps.dk, dk, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.dq, dq, a.G, a.N, a.L, qk_rows, qk_type) ||
+        !tc_map(encode, &b.maps.dk, dk, a.G, a.N, a.L, qk_rows, qk_type) ||
         !tc_map(encode, &b.maps.dv, dv, a.H, a.P, a.L, a.Bsz, a.dtype))
         return SS_OK;
     const int rc = device_status_word(&w.status);
     if (rc != SS_OK) return rc;
-    char* ws = static_cast<char*>(d.workspace);
-    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    Layout l;
-    const BwdTc bl = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P, a.dtype);
     *ran = true;
     w.maps.q = b.maps.q;
     w.maps.k = b.maps.k;
@@ -262,14 +270,12 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     b.chunks = bl.chunks;
     const bool own_dg = !a.g_per_head && bl.dg_parts == 1;
     b.dg = own_dg ? d.dg : f32(bl.dg);
-    b.dq_part = f32(bl.dq);
-    b.dk_part = f32(bl.dk);
     b.splits = bl.splits;
     b.status = w.status;
     if (launch_tc_bwd(b, st) != cudaSuccess) return SS_ERR_CUDA;
     if (bl.dg_parts > 1 && launch_sum_parts(b.dg, a.g_per_head ? b.dg : d.dg, nullptr, nullptr, bl.dg_parts, a.Bsz * a.L * a.H, SS_F32, st) != cudaSuccess)
         return SS_ERR_CUDA;
-    return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
+    return bwd_sums(d, b.splits, f32(bl.dq), f32(bl.dk), b.dg, f32(bl.rows), st);
 }
 
 bool empty(int64_t Bsz, int64_t L) { return Bsz == 0 || L == 0; }

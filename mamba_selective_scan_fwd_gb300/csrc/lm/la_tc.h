@@ -84,6 +84,8 @@ inline int tc_splits(int64_t items, int64_t rep) {
     return best;
 }
 
+// dq, dk: the outputs, or (splits > 1) the f32 parts [splits, Bsz, L, G, N] in boxes
+// of 32 columns.
 struct TcBwdMaps {
     CUtensorMap q, k, v, dy, dq, dk, dv;
 };
@@ -95,8 +97,7 @@ struct TcBwdArgs {
     const float *before_scale, *after_scale;  // f16: their scales
     int64_t chunks;
     float* dg;                 // [Bsz, L, H]; f16: [value tiles, Bsz, L, H]
-    float *dq_part, *dk_part;  // [splits, Bsz, L, G, N] f32 when splits > 1
-    int splits;                // parts of a group's heads; f16: one per head and value tile
+    int splits;  // parts of a group's heads; f16: one per head and value tile
     int* status;
 };
 cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st);

@@ -31,9 +31,12 @@ namespace {
 constexpr int C = kChunkTc;
 constexpr int PT = kTileP;
 
+// x: two places of 32 KB that take turns: v and dy of an iteration, and the low
+// parts of its H and R; what is free once k R and q H are done takes the next v
+// and dy, what is free once dq and dk are done the next low parts.
 template <int NB> struct BwdSmem {
-    static constexpr int q = 0, k = q + NB * 16384, v = k + NB * 16384, dy = v + 16384, h = dy + 16384,
-                         r = h + 2 * NB * 8192, e = r + 2 * NB * 8192, ds = e + 32768, total = ds + 16384;
+    static constexpr int q = 0, k = q + NB * 16384, x = k + NB * 16384, h = x + 65536, r = h + NB * 8192, e = r + NB * 8192,
+                         ds = e + 32768, total = ds + 16384;
 };
 
 // Sum over the lanes of x[i] for every i: lane i gets the sum of x[i].
@@ -156,9 +159,15 @@ struct Place {
     }
 };
 
-// 16 compute warps (thread: row tok of every tile, a quarter of its columns)
-// and a warp that issues the copies and products and adds up dg.
-constexpr int kCompute = 512, kThreads = kCompute + 32;
+// 16 compute warps (thread: row tok of every tile, a quarter of its columns), a
+// warp that issues copies and products, and one that makes the decays of the next
+// iteration, adds up dg of the last one and sends out what is staged in E.
+// Within an iteration (one head's value tile) the products of dq and dk run while
+// the compute warps end it and the next one begins.
+constexpr int kCompute = 512, kIssue = kCompute, kHelp = kCompute + 32, kThreads = kCompute + 64;
+
+// Barrier of the compute warps and the issuing warp.
+__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 2, 544;" ::: "memory"); }
 
 template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_tc_bwd(const __grid_constant__ TcBwdArgs w) {
     extern __shared__ __align__(1024) char sm[];
@@ -166,30 +175,29 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     constexpr int NP = NB * 64;
     __shared__ Decays s_decays[2];  // of iteration it at it & 1
     __shared__ float s_row[4][C], s_a[4][C], s_b[4][C], s_red[16];
-    // copies: v, dy (and q, k); states.  Products: S, D; dv, k R, q H; dq, dk
-    __shared__ __align__(8) uint64_t s_ld, s_st, s_m1, s_m2, s_m3;
-    __shared__ uint32_t s_tm;
+    // copies: v, dy; q, k; states.  Products: S, D; dv, k R, q H; dq, dk.
+    __shared__ __align__(8) uint64_t s_ld, s_kq, s_st, s_m1, s_m2, s_m3;
+    // decays made; the states' low parts and dy read; iteration over; its dg made; E staged; E sent
+    __shared__ __align__(8) uint64_t s_dec, s_rh, s_epi, s_dg, s_stage, s_sent;
+    __shared__ uint32_t s_tm, s_fail;
     __shared__ uint32_t s_most[kF16<T> ? 4 : 1][16];
     __shared__ Place s_at[3];  // of iteration it at it % 3, the next one's too
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, quarter = tid >> 7;
-    char *Q = sm + L::q, *K = sm + L::k, *V = sm + L::v, *DY = sm + L::dy, *H = sm + L::h, *R = sm + L::r, *E = sm + L::e,
-         *DS = sm + L::ds;
+    char *Q = sm + L::q, *K = sm + L::k, *H = sm + L::h, *R = sm + L::r, *E = sm + L::e, *DS = sm + L::ds;
     const int ptiles = (int)((a.P + PT - 1) / PT);
     const int64_t items = a.Bsz * w.chunks * a.G * w.splits;
 
     if (tid == 0) {
-        mbar_init(&s_ld, 1);
-        mbar_init(&s_st, 1);
-        mbar_init(&s_m1, 1);
-        mbar_init(&s_m2, 1);
-        mbar_init(&s_m3, 1);
+        uint64_t* one[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_m3, &s_sent};
+        for (uint64_t* b : one) mbar_init(b, 1);
+        mbar_init(&s_dec, 32);
+        mbar_init(&s_dg, 32);
+        mbar_init(&s_rh, kCompute);
+        mbar_init(&s_epi, kCompute);
+        mbar_init(&s_stage, kCompute);
+        s_fail = 0;
         fence_proxy_async_smem();
-        Place p;
-        p.item = blockIdx.x;
-        p.begin<kF16<T>>(w, ptiles);
-        p.mark(w, items);
-        s_at[0] = p;
     }
     if (tid < 32) tmem_alloc(&s_tm, 512);
     __syncthreads();
@@ -198,37 +206,55 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     // S^T, then P^T and q H in its place; D^T, then dv and k R; dq; dk
     const uint32_t tS = tm, tP = tm, tZ = tm + 64, tD = tm + 128, tV = tm + 128, tF = tm + 192, tQ = tm + 256,
                    tK = tm + 256 + NP;
+    auto wait = [&](uint64_t& bar, uint32_t phase) { return wait_or_fail(&bar, phase & 1, &s_fail); };
     auto valid = [&](const Place& p) {
         return (int)max((int64_t)0, min((int64_t)C, row_length(a, p.b) - (int64_t)p.chunk * C));
     };
     auto image_of = [&](const Place& p) { return ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk; };
-    bool ok = true, more = true, failed = false;
-    uint32_t it = 0;
+    // rounds through E at an item's end (dv has one at every iteration's): bf16 tiles of dq and dk, or f32 tiles
+    const int qk_rounds = w.splits == 1 ? NB : 2 * NB;
+    Place at;  // issuing and helping warp
+    if (tid >= kCompute) {
+        at.item = blockIdx.x;
+        at.begin<kF16<T>>(w, ptiles);
+        at.mark(w, items);
+    }
 
-    if (tid >= kCompute) {  // ---------------- the issuing warp
-        auto load = [&](const Place& p) {
-            const int t0 = p.chunk * C;
-            const bool first = p.first;
-            mbar_expect_tx(&s_ld, (first ? 2 * NB + 2 : 2) * 16384);
-            if (first)
-#pragma unroll
-                for (int n = 0; n < NB; n++) {
-                    tma_load_4d(K + n * 16384, &w.maps.k, n * 64, p.gq, t0, p.b, &s_ld);
-                    tma_load_4d(Q + n * 16384, &w.maps.q, n * 64, p.gq, t0, p.b, &s_ld);
-                }
-            tma_load_4d(V, &w.maps.v, p.pt * PT, p.h, t0, p.b, &s_ld);
-            tma_load_4d(DY, &w.maps.dy, p.pt * PT, p.h, t0, p.b, &s_ld);
-            constexpr int bytes = 2 * NB * 8192;
-            const int64_t image = image_of(p);
-            mbar_expect_tx(&s_st, 2 * bytes);
-            bulk_load(H, static_cast<const char*>(w.before) + image * bytes, bytes, &s_st);
-            bulk_load(R, static_cast<const char*>(w.after) + image * bytes, bytes, &s_st);
-        };
+    if (tid >= kHelp) {  // ---------------- the helping warp
         const bool lead = lane == 0;
-        Place at = s_at[0];
-        if (lead) load(at);
-        float g[4];
-        auto raw_g = [&](const Place& p) {
+        auto put_dg = [&](const Place& at) {  // of its head (f16: its tile's part), tokens 4 lane .. 4 lane + 3
+            if (at.pt + 1 < at.pt_hi) return;
+            const int64_t t0 = (int64_t)at.chunk * C;
+            const int nv = valid(at);
+            float sum = 0.0f, av[4], bv[4];
+#pragma unroll
+            for (int u = 0; u < 16; u++) sum += s_red[u];
+            float A = 0.0f, B = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int t = 4 * lane + e;
+                av[e] = (s_a[0][t] + s_a[1][t]) + (s_a[2][t] + s_a[3][t]);
+                bv[e] = (s_b[0][t] + s_b[1][t]) + (s_b[2][t] + s_b[3][t]);
+                A += av[e];
+                B += bv[e];
+            }
+            float suf = A, pre = B;  // inclusive over lanes, from the right and from the left
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_down_sync(kFull, suf, o), y = __shfl_up_sync(kFull, pre, o);
+                if (lane + o < 32) suf += x;
+                if (lane >= o) pre += y;
+            }
+            pre -= B;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int64_t t = 4 * lane + e;
+                if (t0 + t < a.L) w.dg[((at.pt_lo * a.Bsz + at.b) * a.L + t0 + t) * a.H + at.h] = t < nv ? suf + pre + sum : 0.0f;
+                suf -= av[e];
+                pre += bv[e];
+            }
+        };
+        auto raw_g = [&](const Place& p, float (&g)[4]) {
             const int nv = valid(p);
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -236,22 +262,96 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 g[e] = t < nv ? a.g[a.g_per_head ? (int64_t)p.h : ((p.b * a.L + (int64_t)p.chunk * C + t) * a.H + p.h)] : 0.0f;
             }
         };
-        raw_g(at);
-        put_decays(s_decays[0], g, a.scale);
-        for (; more; it++) {
-            const uint32_t ph = it & 1;
-            const bool first = at.first, last = at.last;
-            Place next = at;
-            more = at.more;
-            if (more) {
-                next.step<kF16<T>>(w, ptiles, items);
-                if (lead) s_at[(it + 1) % 3] = next;
-                raw_g(next);
-            }
-            ok = mbar_wait(&s_ld, ph);
-            failed = __syncthreads_or(!ok);  // A
-            if (failed) break;
+        uint32_t round = 0;
+        auto send = [&](auto store) {  // what the compute warps staged in E
+            wait(s_stage, round++);
             if (lead) {
+                if (!s_fail) store();
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(&s_sent);
+            }
+            __syncwarp();
+        };
+        float g[4];
+        raw_g(at, g);
+        if (lead) s_at[0] = at;
+        put_decays(s_decays[0], g, a.scale);
+        mbar_arrive(&s_dec);
+        for (uint32_t it = 0;; it++) {
+            Place next = at;
+            if (at.more) {
+                next.step<kF16<T>>(w, ptiles, items);
+                raw_g(next, g);
+                // (the last iteration is over: nothing reads that place and those decays any more)
+                if (lead) s_at[(it + 1) % 3] = next;
+                put_decays(s_decays[(it + 1) & 1], g, a.scale);
+                mbar_arrive(&s_dec);
+            }
+            wait(s_epi, it);
+            put_dg(at);
+            mbar_arrive(&s_dg);
+            send([&] { tma_store_4d(&w.maps.dv, E, at.pt * PT, at.h, at.chunk * C, at.b); });
+            if (at.last)
+                for (int k = 0; k < qk_rounds; k++)
+                    send([&] {
+                        const int t0 = at.chunk * C;
+                        if (w.splits == 1) {  // NB == 1: dq and dk; NB == 2: both halves of one of them
+                            tma_store_4d(NB == 1 || k == 0 ? &w.maps.dq : &w.maps.dk, E, 0, at.gq, t0, at.b);
+                            if (NB == 1) tma_store_4d(&w.maps.dk, E + 16384, 0, at.gq, t0, at.b);
+                            else tma_store_4d(k == 0 ? &w.maps.dq : &w.maps.dk, E + 16384, 64, at.gq, t0, at.b);
+                        } else {  // 64 columns of dq or dk, 32 a tile
+                            const CUtensorMap* map = k < NB ? &w.maps.dq : &w.maps.dk;
+                            const int n = (k % NB) * 64, row = at.split * (int)a.Bsz + at.b;
+                            tma_store_4d(map, E, n, at.gq, t0, row);
+                            tma_store_4d(map, E + 16384, n + 32, at.gq, t0, row);
+                        }
+                    });
+            if (!at.more) break;
+            at = next;
+        }
+        if (lead) bulk_wait_all();
+    } else if (tid >= kIssue) {  // ---------------- the issuing warp
+        const bool lead = lane == 0;
+        auto load_kq = [&](const Place& p) {
+            mbar_expect_tx(&s_kq, 2 * NB * 16384);
+#pragma unroll
+            for (int n = 0; n < NB; n++) {
+                tma_load_4d(K + n * 16384, &w.maps.k, n * 64, p.gq, p.chunk * C, p.b, &s_kq);
+                tma_load_4d(Q + n * 16384, &w.maps.q, n * 64, p.gq, p.chunk * C, p.b, &s_kq);
+            }
+        };
+        auto load_v = [&](const Place& p, uint32_t it) {
+            char* to = sm + L::x + (it & 1) * 32768;
+            mbar_expect_tx(&s_ld, 32768);
+            tma_load_4d(to, &w.maps.v, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
+            tma_load_4d(to + 16384, &w.maps.dy, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
+        };
+        auto load_states = [&](const Place& p, uint32_t it) {
+            constexpr int half = NB * 8192;
+            char* low = sm + L::x + ((it & 1) ^ 1) * 32768;
+            const char *hs = static_cast<const char*>(w.before) + image_of(p) * 2 * half,
+                       *rs = static_cast<const char*>(w.after) + image_of(p) * 2 * half;
+            mbar_expect_tx(&s_st, 4 * half);
+            bulk_load(H, hs, half, &s_st);
+            bulk_load(R, rs, half, &s_st);
+            bulk_load(low, hs + half, half, &s_st);
+            bulk_load(low + 16384, rs + half, half, &s_st);
+        };
+        if (lead) {
+            load_kq(at);
+            load_v(at, 0);
+            load_states(at, 0);
+        }
+        uint32_t kq = 0, it = 0;
+        for (;; it++) {
+            const uint32_t ph = it & 1;
+            char *V = sm + L::x + ph * 32768, *DY = V + 16384, *HL = sm + L::x + (ph ^ 1) * 32768, *RL = HL + 16384;
+            const bool first = at.first;
+            wait(s_ld, it);
+            if (first) wait(s_kq, kq++);
+            work_sync();  // A: tiles ready, the last iteration's accumulators read
+            if (lead && !s_fail) {
                 tc_fence_after();
                 constexpr uint32_t d = mma_desc<T>(128, 128, false, false);
 #pragma unroll
@@ -262,16 +362,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 #pragma unroll
                 for (int s = 0; s < 4; s++)
                     mma(tD, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(DY) + s * 32), d, s > 0);
-                bulk_wait_read();  // the last dv (dq, dk) has left E
                 mma_commit(&s_m1);
             }
             __syncwarp();
-            if (more) put_decays(s_decays[ph ^ 1], g, a.scale);
-            ok = mbar_wait(&s_st, ph);
-            __syncthreads();                 // S and D have been read
-            failed = __syncthreads_or(!ok);  // B
-            if (failed) break;
-            if (lead) {
+            if (it > 0 && wait(s_m3, it - 1) && lead) load_states(at, it);
+            work_sync();  // S and D have been read
+            wait(s_st, it);
+            work_sync();  // B: P, E and the scaled tiles are there
+            if (lead && !s_fail) {
                 tc_fence_after();
                 constexpr uint32_t dV = mma_desc<T>(128, PT, false, true), dQ = mma_desc<T>(128, NP, true, true),
                                    dQs = mma_desc<T>(128, NP, false, false), dK = mma_desc<T>(128, NP, false, true);
@@ -280,9 +378,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 #pragma unroll
                 for (int s = 0; s < 8 * NB; s++) {  // k R and q H, high and low parts
                     const int n = s % (4 * NB);
-                    const uint32_t o = (n >> 2) * 16384 + (n & 3) * 32, st = (s / (4 * NB)) * NB * 8192 + n * 2048;
-                    mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(R) + st), dV, s > 0);
-                    mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(H) + st), dV, s > 0);
+                    const uint32_t o = (n >> 2) * 16384 + (n & 3) * 32;
+                    mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(s < 4 * NB ? R : RL) + n * 2048), dV, s > 0);
+                    mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(s < 4 * NB ? H : HL) + n * 2048), dV, s > 0);
                 }
                 mma_commit(&s_m2);
 #pragma unroll
@@ -299,80 +397,73 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 }
                 mma_commit(&s_m3);
             }
-            failed = __syncthreads_or(0);  // C
-            if (failed) break;
-            const int64_t t0 = (int64_t)at.chunk * C;
-            if (lead) {
-                if (more) load(next);
-                tma_store_4d(&w.maps.dv, E, at.pt * PT, at.h, (int)t0, at.b);
-                bulk_commit();
-            }
             __syncwarp();
-            if (at.pt + 1 == at.pt_hi) {  // dg of this head (f16: its tile's part), tokens 4 lane .. 4 lane + 3
-                const int nv = valid(at);
-                float sum = 0.0f, av[4], bv[4];
-#pragma unroll
-                for (int u = 0; u < 16; u++) sum += s_red[u];
-                float A = 0.0f, B = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int t = 4 * lane + e;
-                    av[e] = (s_a[0][t] + s_a[1][t]) + (s_a[2][t] + s_a[3][t]);
-                    bv[e] = (s_b[0][t] + s_b[1][t]) + (s_b[2][t] + s_b[3][t]);
-                    A += av[e];
-                    B += bv[e];
-                }
-                float suf = A, pre = B;  // inclusive over lanes, from the right and from the left
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float x = __shfl_down_sync(kFull, suf, o), y = __shfl_up_sync(kFull, pre, o);
-                    if (lane + o < 32) suf += x;
-                    if (lane >= o) pre += y;
-                }
-                pre -= B;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int64_t t = 4 * lane + e;
-                    if (t0 + t < a.L) w.dg[((at.pt_lo * a.Bsz + at.b) * a.L + t0 + t) * a.H + at.h] = t < nv ? suf + pre + sum : 0.0f;
-                    suf -= av[e];
-                    pre += bv[e];
-                }
-            }
-            if (last && w.splits == 1) {  // dq and dk: see the compute warps
-                for (int k = 0; k < 2; k++) {
-                    if (NB == 2 || k == 0) {
-                        if (lead) bulk_wait_read();
-                        __syncthreads();  // E is free
-                    }
-                    __syncthreads();  // the tile is written
-                    if (lead) {
-                        char* from = NB == 1 ? E + k * 16384 : E;
-                        for (int n = 0; n < NB; n++)
-                            tma_store_4d(k == 0 ? &w.maps.dq : &w.maps.dk, from + n * 16384, n * 64, at.gq, (int)t0, at.b);
-                        bulk_commit();
-                    }
-                }
-            }
-            at = next;
+            if (!at.more) break;
+            at.step<kF16<T>>(w, ptiles, items);
+            wait(s_rh, it);
+            if (wait(s_m2, it) && lead) load_v(at, it + 1);
+            if (at.first && wait(s_m3, it) && lead) load_kq(at);
         }
-        if (failed && lead) {  // a wait ran out: report, wait for what is in flight (within limits)
+        wait(s_m3, it);
+        if (s_fail && lead) {  // a wait ran out: report, wait for what is in flight (within limits)
             atomicOr(w.status, kDevWaitTimeout);
-            mbar_wait(&s_ld, it & 1);
-            mbar_wait(&s_st, it & 1);
-            mbar_wait(&s_m1, it & 1);
-            mbar_wait(&s_m3, it & 1);
+            uint64_t* all[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_m3};
+            for (uint64_t* b : all) {
+                mbar_wait(b, 0);
+                mbar_wait(b, 1);
+            }
         }
-        if (lead) bulk_wait_all();
     } else {  // ---------------- the compute warps
-        float through = 0.0f;
-        for (; more; it++) {
+        uint32_t round = 0;
+        auto stage = [&](auto fill) {  // a round through E: what was there has been sent
+            if (round > 0) wait(s_sent, round - 1);
+            round++;
+            fill();
+            fence_proxy_async_smem();
+            mbar_arrive(&s_stage);
+        };
+        // what an iteration leaves: dv; after an item's last one, dq and dk of the group (or of a part of its heads)
+        auto put_out = [&](const Place& at, const uint32_t (&dv)[8], float kap) {
+            stage([&] { write_row(E, tok, quarter, dv); });
+            if (!at.last) return;
+            for (int k = 0; k < qk_rounds; k++)
+                stage([&] {
+                    if (w.splits == 1) {
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {  // 16 columns of a tile each: NB == 1: of dq, dk; NB == 2: of two tiles
+                            const uint32_t from = NB == 1 ? (c == 0 ? tQ : tK) : (k == 0 ? tQ : tK) + 64 * c;
+                            float x[16];
+                            uint32_t r[8];
+                            tmem_ld16(from + my + 16 * quarter, x);
+#pragma unroll
+                            for (int i = 0; i < 8; i++) r[i] = kF16<T> ? pack2<T>(x[2 * i] / kap, x[2 * i + 1] / kap) : pack2<T>(x[2 * i], x[2 * i + 1]);
+                            write_row(E + c * 16384, tok, quarter, r);
+                        }
+                    } else {
+                        float x[16];
+                        tmem_ld16((k < NB ? tQ : tK) + 64 * (k % NB) + my + 16 * quarter, x);
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            float4 f = make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+                            if (kF16<T>) f = make_float4(f.x / kap, f.y / kap, f.z / kap, f.w / kap);
+                            *reinterpret_cast<float4*>(unit(E + (quarter >> 1) * 16384, tok, (quarter & 1) * 4 + u)) = f;
+                        }
+                    }
+                });
+            tc_fence_before();
+        };
+        float through = 0.0f, kap_last = 1.0f;
+        uint32_t dv[8], kq = 0, it = 0;
+        for (;; it++) {
             const uint32_t ph = it & 1;
+            char *V = sm + L::x + ph * 32768, *DY = V + 16384, *HL = sm + L::x + (ph ^ 1) * 32768, *RL = HL + 16384;
+            wait(s_dec, it);
             const Place& at = s_at[it % 3];
             const Decays& dec = s_decays[ph];
             const int64_t t0 = (int64_t)at.chunk * C;
-            more = at.more;
             const int nv = valid(at);
-            ok = mbar_wait(&s_ld, ph);
+            bool ok = wait(s_ld, it);
+            if (at.first) ok = wait(s_kq, kq++) && ok;
             if (ok && tok >= nv && t0 + tok < a.L) {  // tokens beyond the row's length
                 const uint32_t zero[8] = {};
                 write_row(V, tok, quarter, zero);
@@ -383,11 +474,15 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                         write_row(Q + n * 16384, tok, quarter, zero);
                         write_row(K + n * 16384, tok, quarter, zero);
                     }
+                fence_proxy_async_smem();
             }
             tc_fence_before();
-            fence_proxy_async_smem();
-            failed = __syncthreads_or(!ok);  // A
-            if (failed) break;
+            work_sync();  // A
+            if (it > 0) {  // the last products have read E, the scaled dy and v
+                wait(s_m3, it - 1);
+                tc_fence_after();
+                put_out(s_at[(it + 2) % 3], dv, kap_last);
+            }
             const float down = dec.down[tok];
             uint32_t vr[8];
             read_row(V, tok, quarter, vr);
@@ -411,7 +506,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 write_row(V, tok, quarter, x);
             };
             if (!kF16<T>) put_ds(dec.up[tok]);
-            ok = mbar_wait(&s_m1, ph);
+            wait(s_m1, it);
             tc_fence_after();
             if (!kF16<T>) put_v(down);
             // P, E and W by 32 x 32 blocks: rows of `run`, columns of `quarter`.  W keeps its diagonal: it is in a
@@ -511,28 +606,29 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                         er[j / 2] = pack2<T>(e.x, e.y);
                     });
             }
+            if (round > 0) wait(s_sent, round - 1);
             // E: row j, columns 32 cb .. + 31 of two 64-column tiles
 #pragma unroll
             for (int u = 0; u < 4; u++)
                 *unit(E + (cb >> 1) * 16384, tok, (cb & 1) * 4 + u) = make_uint4(er[4 * u], er[4 * u + 1], er[4 * u + 2], er[4 * u + 3]);
             tc_fence_before();
-            __syncthreads();  // S and D have been read
+            work_sync();  // S and D have been read
             tc_fence_after();
             tmem_st16(tP + my + 16 * cb, pr);
             tmem_wait_st();
             tc_fence_before();
             fence_proxy_async_smem();
-            ok = mbar_wait(&s_st, ph) && ok;
-            failed = __syncthreads_or(!ok);  // B
-            if (failed) break;
+            wait(s_st, it);
+            if (it > 0) wait(s_dg, it - 1);  // what dg reads may be written again
+            work_sync();                     // B
             // <R, H> of this tile: rows n of both, high + low
             if (at.pt == at.pt_lo) through = 0.0f;
             if (tok < NP) {
                 uint32_t h0[8], h1[8], r0[8], r1[8];
                 read_row(H, tok, quarter, h0);
-                read_row(H + NB * 8192, tok, quarter, h1);
+                read_row(HL, tok, quarter, h1);
                 read_row(R, tok, quarter, r0);
-                read_row(R + NB * 8192, tok, quarter, r1);
+                read_row(RL, tok, quarter, r1);
                 float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int i = 0; i < 8; i++)
@@ -543,9 +639,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) th += __shfl_xor_sync(kFull, th, o);
             if (lane == 0) s_red[tid >> 5] = th * (dec.all * ih * ir);
-            uint32_t dyr[8], dv[8];
+            uint32_t dyr[8];
             read_row(DY, tok, quarter, dyr);
-            ok = mbar_wait(&s_m2, ph);
+            mbar_arrive(&s_rh);
+            wait(s_m2, it);
             tc_fence_after();
             {
                 float f[16], x[16], zz[16];
@@ -571,48 +668,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 s_a[quarter][tok] = sa;
                 s_b[quarter][tok] = sb;
             }
-            ok = mbar_wait(&s_m3, ph) && ok;
-            tc_fence_after();
-            write_row(E, tok, quarter, dv);
-            tc_fence_before();
-            fence_proxy_async_smem();
-            failed = __syncthreads_or(!ok);  // C
-            if (failed) break;
-            if (at.last) {  // dq and dk of the group (or of this part of its heads)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const uint32_t from = k == 0 ? tQ : tK;
-                    float* part = (k == 0 ? w.dq_part : w.dk_part) + at.split * a.Bsz * a.L * a.G * a.N +
-                                  ((at.b * a.L + t0 + tok) * a.G + at.gq) * a.N;
-                    char* to = NB == 1 ? E + k * 16384 : E;  // NB == 2: E for dq, then for dk
-                    if (w.splits == 1 && (NB == 2 || k == 0)) __syncthreads();
-#pragma unroll
-                    for (int c = 0; c < NB; c++) {
-                        float x[16];
-                        const int n0 = 16 * NB * quarter + 16 * c;
-                        tmem_ld16(from + my + n0, x);
-                        if (kF16<T>)
-#pragma unroll
-                            for (int i = 0; i < 16; i++) x[i] *= 1.0f / kap;
-                        if (w.splits == 1) {
-                            uint32_t r[8];
-#pragma unroll
-                            for (int i = 0; i < 8; i++) r[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
-                            write_row(to + (n0 >> 6) * 16384, tok, (n0 >> 4) & 3, r);
-                        } else if (t0 + tok < a.L) {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4)
-                                if (n0 + i < a.N)
-                                    *reinterpret_cast<float4*>(part + n0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                        }
-                    }
-                    if (w.splits == 1) {
-                        fence_proxy_async_smem();
-                        __syncthreads();
-                    }
-                }
-            }
+            kap_last = kap;
+            const bool more = at.more;
+            mbar_arrive(&s_epi);
+            if (!more) break;
         }
+        wait(s_m3, it);
+        tc_fence_after();
+        put_out(s_at[it % 3], dv, kap_last);
     }
     tc_fence_before();
     __syncthreads();
