@@ -160,11 +160,12 @@ struct Place {
 };
 
 // 16 compute warps (thread: row tok of every tile, a quarter of its columns), a
-// warp that issues copies and products, and one that makes the decays of the next
-// iteration, adds up dg of the last one and sends out what is staged in E.
+// warp that issues the products, one that issues the copies (the products' issue
+// waits for the tensor cores), and one that makes the decays of the next iteration,
+// adds up dg of the last one and sends out what is staged in E.
 // Within an iteration (one head's value tile) the products of dq and dk run while
 // the compute warps end it and the next one begins.
-constexpr int kCompute = 512, kIssue = kCompute, kHelp = kCompute + 32, kThreads = kCompute + 64;
+constexpr int kCompute = 512, kIssue = kCompute, kLoad = kCompute + 32, kHelp = kCompute + 64, kThreads = kCompute + 96;
 
 // Barrier of the compute warps and the issuing warp.
 __device__ __forceinline__ void work_sync() { asm volatile("bar.sync 2, 544;" ::: "memory"); }
@@ -213,7 +214,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     auto image_of = [&](const Place& p) { return ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk; };
     // rounds through E at an item's end (dv has one at every iteration's): bf16 tiles of dq and dk, or f32 tiles
     const int qk_rounds = w.splits == 1 ? NB : 2 * NB;
-    Place at;  // issuing and helping warp
+    Place at;  // the other warps
     if (tid >= kCompute) {
         at.item = blockIdx.x;
         at.begin<kF16<T>>(w, ptiles);
@@ -311,38 +312,55 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             at = next;
         }
         if (lead) bulk_wait_all();
-    } else if (tid >= kIssue) {  // ---------------- the issuing warp
-        const bool lead = lane == 0;
-        auto load_kq = [&](const Place& p) {
-            mbar_expect_tx(&s_kq, 2 * NB * 16384);
+    } else if (tid >= kLoad) {  // ---------------- the loading warp
+        if (lane == 0) {
+            auto load_kq = [&](const Place& p) {
+                mbar_expect_tx(&s_kq, 2 * NB * 16384);
 #pragma unroll
-            for (int n = 0; n < NB; n++) {
-                tma_load_4d(K + n * 16384, &w.maps.k, n * 64, p.gq, p.chunk * C, p.b, &s_kq);
-                tma_load_4d(Q + n * 16384, &w.maps.q, n * 64, p.gq, p.chunk * C, p.b, &s_kq);
-            }
-        };
-        auto load_v = [&](const Place& p, uint32_t it) {
-            char* to = sm + L::x + (it & 1) * 32768;
-            mbar_expect_tx(&s_ld, 32768);
-            tma_load_4d(to, &w.maps.v, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
-            tma_load_4d(to + 16384, &w.maps.dy, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
-        };
-        auto load_states = [&](const Place& p, uint32_t it) {
-            constexpr int half = NB * 8192;
-            char* low = sm + L::x + ((it & 1) ^ 1) * 32768;
-            const char *hs = static_cast<const char*>(w.before) + image_of(p) * 2 * half,
-                       *rs = static_cast<const char*>(w.after) + image_of(p) * 2 * half;
-            mbar_expect_tx(&s_st, 4 * half);
-            bulk_load(H, hs, half, &s_st);
-            bulk_load(R, rs, half, &s_st);
-            bulk_load(low, hs + half, half, &s_st);
-            bulk_load(low + 16384, rs + half, half, &s_st);
-        };
-        if (lead) {
+                for (int n = 0; n < NB; n++) {
+                    tma_load_4d(K + n * 16384, &w.maps.k, n * 64, p.gq, p.chunk * C, p.b, &s_kq);
+                    tma_load_4d(Q + n * 16384, &w.maps.q, n * 64, p.gq, p.chunk * C, p.b, &s_kq);
+                }
+            };
+            auto load_v = [&](const Place& p, uint32_t it) {
+                char* to = sm + L::x + (it & 1) * 32768;
+                mbar_expect_tx(&s_ld, 32768);
+                tma_load_4d(to, &w.maps.v, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
+                tma_load_4d(to + 16384, &w.maps.dy, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
+            };
+            auto load_states = [&](const Place& p, uint32_t it) {
+                constexpr int half = NB * 8192;
+                char* low = sm + L::x + ((it & 1) ^ 1) * 32768;
+                const char *hs = static_cast<const char*>(w.before) + image_of(p) * 2 * half,
+                           *rs = static_cast<const char*>(w.after) + image_of(p) * 2 * half;
+                mbar_expect_tx(&s_st, 4 * half);
+                bulk_load(H, hs, half, &s_st);
+                bulk_load(R, rs, half, &s_st);
+                bulk_load(low, hs + half, half, &s_st);
+                bulk_load(low + 16384, rs + half, half, &s_st);
+            };
             load_kq(at);
             load_v(at, 0);
             load_states(at, 0);
+            auto prefetch = [&](const Place& p) {
+                tma_prefetch_4d(&w.maps.v, p.pt * PT, p.h, p.chunk * C, p.b);
+                tma_prefetch_4d(&w.maps.dy, p.pt * PT, p.h, p.chunk * C, p.b);
+                bulk_prefetch(static_cast<const char*>(w.before) + image_of(p) * NB * 16384, NB * 16384);
+                bulk_prefetch(static_cast<const char*>(w.after) + image_of(p) * NB * 16384, NB * 16384);
+            };
+            for (uint32_t it = 0; at.more; it++) {
+                at.step<kF16<T>>(w, ptiles, items);
+                prefetch(at);
+                wait(s_rh, it);
+                if (wait(s_m2, it)) load_v(at, it + 1);
+                if (wait(s_m3, it)) {
+                    if (at.first) load_kq(at);
+                    load_states(at, it + 1);
+                }
+            }
         }
+    } else if (tid >= kIssue) {  // ---------------- the issuing warp
+        const bool lead = lane == 0;
         uint32_t kq = 0, it = 0;
         for (;; it++) {
             const uint32_t ph = it & 1;
@@ -365,7 +383,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 mma_commit(&s_m1);
             }
             __syncwarp();
-            if (it > 0 && wait(s_m3, it - 1) && lead) load_states(at, it);
             work_sync();  // S and D have been read
             wait(s_st, it);
             work_sync();  // B: P, E and the scaled tiles are there
@@ -400,9 +417,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             __syncwarp();
             if (!at.more) break;
             at.step<kF16<T>>(w, ptiles, items);
-            wait(s_rh, it);
-            if (wait(s_m2, it) && lead) load_v(at, it + 1);
-            if (at.first && wait(s_m3, it) && lead) load_kq(at);
         }
         wait(s_m3, it);
         if (s_fail && lead) {  // a wait ran out: report, wait for what is in flight (within limits)

@@ -336,6 +336,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
         }
         tma_load_4d(V, &w.maps.v, (int)p0, (int)h, (int)t0, (int)b, &s_ld);
     };
+    auto prefetch = [&](int64_t t0) {
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            tma_prefetch_4d(&w.maps.k, n * 64, (int)hq, (int)t0, (int)b);
+            tma_prefetch_4d(&w.maps.q, n * 64, (int)hq, (int)t0, (int)b);
+        }
+        tma_prefetch_4d(&w.maps.v, (int)p0, (int)h, (int)t0, (int)b);
+    };
     auto valid = [&](int64_t t0) { return (int)max((int64_t)0, min((int64_t)C, len - t0)); };
     if (tid == C) load(t_begin);
 
@@ -370,7 +378,24 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             float vs = 1.0f;
             if (kF16<T>) vs = f16_scale(group_max(fmaxf(row_max<T>(V, tok, 0), row_max<T>(V, tok, 1)), s_red, 1));
             const float wt = ex2(two_diff(end[3], mine) + rel), cl = end[3].h + end[3].l;
-            ok = mbar_wait(&s_mE, ph);  // q (and the last y's staging tile) make room for w v
+            if (tid == 0) {  // (this half waits for both; the other's P must not)
+                tc_fence_after();
+                constexpr uint32_t dS = mma_desc<T>(128, 128, false, false), dE = mma_desc<T>(128, PT, false, true);
+#pragma unroll
+                for (int s = 0; s < 4 * NB; s++) {
+                    const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
+                    mma(tS, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(K) + at), dS, s > 0);
+                }
+                mma_commit(&s_mS);
+#pragma unroll
+                for (int s = 0; s < 4 * NB; s++) {
+                    const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
+                    mma(tE, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(H) + s * 2048), dE, s > 0);
+                }
+                mma_commit(&s_mE);
+            }
+            __syncwarp();
+            ok = mbar_wait(&s_mE, ph);  // q makes room for w v
             split_row<T>(V, tok, 0, 8, wt * vs, W[0], W[1], W[2]);
             fence_proxy_async_smem();
             group_sync(1);
@@ -402,27 +427,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
                 }
             }
             fence_proxy_async_smem();
+            if (tid == C) {
+                bulk_wait_read();  // the last y has left its staging tile, which a part of w v takes
+                if (ch + 1 < chunks) prefetch(t0 + C);
+            }
             if (__syncthreads_or(!ok)) break;
             Two end[4];
             run_ends(s_total[1], end);
             const Two mine = end_of(end);
-            if (tid == C) {
-                tc_fence_after();
-                constexpr uint32_t dS = mma_desc<T>(128, 128, false, false), dE = mma_desc<T>(128, PT, false, true);
-#pragma unroll
-                for (int s = 0; s < 4 * NB; s++) {
-                    const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
-                    mma(tS, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(K) + at), dS, s > 0);
-                }
-                mma_commit(&s_mS);
-#pragma unroll
-                for (int s = 0; s < 4 * NB; s++) {
-                    const uint32_t at = (s >> 2) * 16384 + (s & 3) * 32;
-                    mma(tE, smem_desc(smem_addr(Q) + at), smem_desc(smem_addr(H) + s * 2048), dE, s > 0);
-                }
-                bulk_wait_read();  // the last y has left its staging tile
-                mma_commit(&s_mE);
-            }
             const float ci = (mine.h - rel) + mine.l;
             ok = mbar_wait(&s_mS, ph);
             tc_fence_after();
