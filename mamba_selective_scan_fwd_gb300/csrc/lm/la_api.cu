@@ -195,7 +195,7 @@ BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     const bool f16 = dtype == SS_F16;
     b.splits = f16 ? (int)(H / G * ptiles) : tc_splits(Bsz * b.chunks * G, H / G);
     b.dg_parts = f16 ? (int)ptiles : 1;
-    const size_t images = (size_t)states * (N > 64 ? 2 : 1) * 16384;
+    const size_t images = (size_t)states * image_bytes(f16, N);
     b.before = l.take(images);
     b.after = l.take(images);
     b.before_scale = l.take(f16 ? states * 4 : 0);

@@ -46,11 +46,22 @@ inline TcPlan tc_plan(int64_t units, int64_t L, int64_t slots) {
     return best;
 }
 
+// An image of a state (N x 64, f32) for the backward: operand tiles of 64 * nb
+// rows whose sum it is to 22 bits (f16: 2 parts of 11), 24 (bf16, N <= 64: 3 parts
+// of 8) or 16 (bf16, N > 64: a third part finds no room in shared memory; dg is
+// then good to 3e-6).
+template <bool F16, int NB> constexpr int kImageParts = !F16 && NB == 1 ? 3 : 2;
+inline int64_t image_bytes(bool f16, int64_t N) {
+    const int parts = N > 64 ? (f16 ? kImageParts<true, 2> : kImageParts<false, 2>)
+                             : (f16 ? kImageParts<true, 1> : kImageParts<false, 1>);
+    return (int64_t)parts * (N > 64 ? 2 : 1) * 8192;
+}
+
 // What a walk starts from and leaves, one for each direction.
 struct TcDir {
     const float* init;   // state before its first token, or null
     float* last;         // state after its last token, or null
-    void* images;        // [Bsz, H, ptiles, chunks] of (high, low) operand tiles of the state before each chunk
+    void* images;        // [Bsz, H, ptiles, chunks] images of the state before each chunk
     float* image_scale;  // f16: the power of two each image was multiplied by
 };
 

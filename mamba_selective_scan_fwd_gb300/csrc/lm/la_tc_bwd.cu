@@ -9,9 +9,9 @@
 //   dg_t = sum_{i >= t} a_i + sum_{j < t} (b_j + col_j - row_j) + e^{cl} <R, H>
 //     a_i = scale e^{c_i} dy_i . (q_i H),  b_j = e^{cl - c_j} v_j . (k_j R),  col_j, row_i: sums of W over i, j
 // dq and dk stay in tensor memory over the heads; q and k are read once for all
-// of them.  Roundings to 16 bits: P, E, the scaled dy and v, and H and R as
-// operands of dq and dk (outputs of 16 bits); dg takes k R and q H with both
-// parts of R and H and everything else in f32.  c_i - c_j inside a run of 32
+// of them.  Roundings to 16 bits: P, E and the scaled dy and v (one rounding of
+// each term of a 16-bit output); H and R enter in parts (kImageParts), and dg
+// takes everything else in f32.  c_i - c_j inside a run of 32
 // tokens is a difference of f32 sums over the run: exact to f32 rounding of the
 // run's decay (a reset to -128 in the run leaves its other tokens 2^-17).
 //
@@ -173,7 +173,7 @@ __device__ __forceinline__ void work_sync() { asm volatile("bar.sync 2, 544;" ::
 template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_tc_bwd(const __grid_constant__ TcBwdArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = BwdSmem<NB>;
-    constexpr int NP = NB * 64;
+    constexpr int NP = NB * 64, kImage = kImageParts<kF16<T>, NB>;
     __shared__ Decays s_decays[2];  // of iteration it at it & 1
     __shared__ float s_row[4][C], s_a[4][C], s_b[4][C], s_red[16];
     // copies: v, dy; q, k; states.  Products: S, D; dv, k R, q H; dq, dk.
@@ -328,16 +328,16 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 tma_load_4d(to, &w.maps.v, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
                 tma_load_4d(to + 16384, &w.maps.dy, p.pt * PT, p.h, p.chunk * C, p.b, &s_ld);
             };
+            constexpr int part = NB * 8192, low = (kImage - 1) * part;
             auto load_states = [&](const Place& p, uint32_t it) {
-                constexpr int half = NB * 8192;
-                char* low = sm + L::x + ((it & 1) ^ 1) * 32768;
-                const char *hs = static_cast<const char*>(w.before) + image_of(p) * 2 * half,
-                           *rs = static_cast<const char*>(w.after) + image_of(p) * 2 * half;
-                mbar_expect_tx(&s_st, 4 * half);
-                bulk_load(H, hs, half, &s_st);
-                bulk_load(R, rs, half, &s_st);
-                bulk_load(low, hs + half, half, &s_st);
-                bulk_load(low + 16384, rs + half, half, &s_st);
+                char* to = sm + L::x + ((it & 1) ^ 1) * 32768;
+                const char *hs = static_cast<const char*>(w.before) + image_of(p) * kImage * part,
+                           *rs = static_cast<const char*>(w.after) + image_of(p) * kImage * part;
+                mbar_expect_tx(&s_st, 2 * kImage * part);
+                bulk_load(H, hs, part, &s_st);
+                bulk_load(R, rs, part, &s_st);
+                bulk_load(to, hs + part, low, &s_st);
+                bulk_load(to + 16384, rs + part, low, &s_st);
             };
             load_kq(at);
             load_v(at, 0);
@@ -345,8 +345,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             auto prefetch = [&](const Place& p) {
                 tma_prefetch_4d(&w.maps.v, p.pt * PT, p.h, p.chunk * C, p.b);
                 tma_prefetch_4d(&w.maps.dy, p.pt * PT, p.h, p.chunk * C, p.b);
-                bulk_prefetch(static_cast<const char*>(w.before) + image_of(p) * NB * 16384, NB * 16384);
-                bulk_prefetch(static_cast<const char*>(w.after) + image_of(p) * NB * 16384, NB * 16384);
+                bulk_prefetch(static_cast<const char*>(w.before) + image_of(p) * kImage * part, kImage * part);
+                bulk_prefetch(static_cast<const char*>(w.after) + image_of(p) * kImage * part, kImage * part);
             };
             for (uint32_t it = 0; at.more; it++) {
                 at.step<kF16<T>>(w, ptiles, items);
@@ -393,19 +393,23 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 #pragma unroll
                 for (int s = 0; s < C / 16; s++) mma_ts(tV, tP + 8 * s, smem_desc(smem_addr(DY) + s * 2048), dV, s > 0);
 #pragma unroll
-                for (int s = 0; s < 8 * NB; s++) {  // k R and q H, high and low parts
-                    const int n = s % (4 * NB);
+                for (int s = 0; s < 4 * NB * kImage; s++) {  // k R and q H, all parts
+                    const int n = s % (4 * NB), low = (s / (4 * NB) - 1) * NB * 8192;
                     const uint32_t o = (n >> 2) * 16384 + (n & 3) * 32;
-                    mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(s < 4 * NB ? R : RL) + n * 2048), dV, s > 0);
-                    mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(s < 4 * NB ? H : HL) + n * 2048), dV, s > 0);
+                    mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(low < 0 ? R : RL + low) + n * 2048), dV, s > 0);
+                    mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(low < 0 ? H : HL + low) + n * 2048), dV, s > 0);
+                }
+#pragma unroll
+                for (int s = 0; s < PT / 16; s++) {  // the second parts in dq and dk: one rounding less (of dy and v only)
+                    mma(tQ, smem_desc(smem_addr(DS) + s * 32), smem_desc(smem_addr(HL) + s * 32), dQs, !first || s > 0);
+                    mma(tK, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(RL) + s * 32), dQs, !first || s > 0);
                 }
                 mma_commit(&s_m2);
 #pragma unroll
                 for (int s = 0; s < C / 16; s++) {
-                    mma(tQ, smem_desc(smem_addr(E) + s * 2048, 16384), smem_desc(smem_addr(K) + s * 2048, 16384), dQ,
-                        !first || s > 0);
+                    mma(tQ, smem_desc(smem_addr(E) + s * 2048, 16384), smem_desc(smem_addr(K) + s * 2048, 16384), dQ, true);
                     mma(tK, smem_desc(smem_addr(E) + (s >> 2) * 16384 + (s & 3) * 32), smem_desc(smem_addr(Q) + s * 2048, 16384),
-                        dK, !first || s > 0);
+                        dK, true);
                 }
 #pragma unroll
                 for (int s = 0; s < PT / 16; s++) {
@@ -635,18 +639,23 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             wait(s_st, it);
             if (it > 0) wait(s_dg, it - 1);  // what dg reads may be written again
             work_sync();                     // B
-            // <R, H> of this tile: rows n of both, high + low
+            // <R, H> of this tile: rows n of both
             if (at.pt == at.pt_lo) through = 0.0f;
             if (tok < NP) {
-                uint32_t h0[8], h1[8], r0[8], r1[8];
-                read_row(H, tok, quarter, h0);
-                read_row(HL, tok, quarter, h1);
-                read_row(R, tok, quarter, r0);
-                read_row(RL, tok, quarter, r1);
-                float2 acc = make_float2(0.0f, 0.0f);
+                uint32_t h[8], r[8];
+                float2 hv[8], rv[8], acc = splat2(0.0f);
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    acc = fma2(add2(unpack2<T>(h0[i]), unpack2<T>(h1[i])), add2(unpack2<T>(r0[i]), unpack2<T>(r1[i])), acc);
+                for (int p = 0; p < kImage; p++) {
+                    read_row(p == 0 ? H : HL + (p - 1) * NB * 8192, tok, quarter, h);
+                    read_row(p == 0 ? R : RL + (p - 1) * NB * 8192, tok, quarter, r);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        hv[i] = p == 0 ? unpack2<T>(h[i]) : add2(hv[i], unpack2<T>(h[i]));
+                        rv[i] = p == 0 ? unpack2<T>(r[i]) : add2(rv[i], unpack2<T>(r[i]));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) acc = fma2(hv[i], rv[i], acc);
                 through += acc.x + acc.y;
             }
             float th = through;

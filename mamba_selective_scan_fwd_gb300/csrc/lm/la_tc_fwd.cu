@@ -235,26 +235,26 @@ __device__ __forceinline__ void add_product(uint32_t tm, float d, float u, float
         }
     }
 }
-// 16-bit rows [n][p] of X * s: an operand tile; LOW: and, in another, of what the
-// rounding left
-template <typename T, int NB, int TH, bool LOW>
-__device__ __forceinline__ void put_state(void* hi, void* lo, float s, const float (&X)[StateOf<NB, TH>::W]) {
+// 16-bit rows [n][p] of X * s: an operand tile, and PARTS - 1 more, one after the
+// other, of what the rounding left
+template <typename T, int NB, int TH, int PARTS>
+__device__ __forceinline__ void put_state(char* to, float s, const float (&X)[StateOf<NB, TH>::W]) {
     const int n = StateOf<NB, TH>::row(), u0 = StateOf<NB, TH>::col() / 8;
 #pragma unroll
     for (int u = 0; u < StateOf<NB, TH>::W / 8; u++) {
-        uint32_t r[4], q[4];
+        uint32_t r[PARTS][4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             float2 f = make_float2(X[8 * u + 2 * i], X[8 * u + 2 * i + 1]);
             if (kF16<T>) f = mul2(f, splat2(s));
-            r[i] = pack2<T>(f.x, f.y);
-            if (LOW) {
-                const float2 rest = fma2(unpack2<T>(r[i]), splat2(-1.0f), f);
-                q[i] = pack2<T>(rest.x, rest.y);
+#pragma unroll
+            for (int p = 0; p < PARTS; p++) {
+                r[p][i] = pack2<T>(f.x, f.y);
+                if (p + 1 < PARTS) f = fma2(unpack2<T>(r[p][i]), splat2(-1.0f), f);
             }
         }
-        *unit(hi, n, u0 + u) = make_uint4(r[0], r[1], r[2], r[3]);
-        if (LOW) *unit(lo, n, u0 + u) = make_uint4(q[0], q[1], q[2], q[3]);
+#pragma unroll
+        for (int p = 0; p < PARTS; p++) *unit(to + p * NB * 8192, n, u0 + u) = make_uint4(r[p][0], r[p][1], r[p][2], r[p][3]);
     }
 }
 
@@ -367,7 +367,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
                 hs = f16_scale(group_max(state_max(X), s_red, 1));
                 if (tid == 0) s_hs[ph] = hs;
             }
-            put_state<T, NB, 128, false>(H, nullptr, hs, X);
+            put_state<T, NB, 128, 1>(H, hs, X);
             const float rel = decays(nullptr, s_total[0], t_begin + (int64_t)ch * C);
             ok = ok && mbar_wait(&s_ld, ph);
             fence_proxy_async_smem();
@@ -552,17 +552,18 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
 // part of the block on its own: 8 warps
 // make w v, 8 keep the state (add a chunk's product to it, write it out as an
 // image), one makes the weights w, one issues copies and products.
-template <int NB> struct StateSmem {
+template <int NB, int PARTS> struct StateSmem {
     static constexpr int ring = NB == 1 ? 3 : 2;  // chunks whose k and v are here or on their way
     static constexpr int k = 0, v = k + NB * 16384, stage = v + 16384, w = ring * stage, parts = 3 * 16384,
-                         image = w + 2 * parts, total = image + 2 * NB * 8192;
+                         image = w + 2 * parts, total = image + PARTS * NB * 8192;
 };
 constexpr int kSplit = 256, kKeep = 256, kStateThreads = kSplit + kKeep + 64;
 
 template <typename T, int NB, bool SUM>
 __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
-    using L = StateSmem<NB>;
+    constexpr int kImage = kImageParts<kF16<T>, NB>;
+    using L = StateSmem<NB, kImage>;
     __shared__ float s_weight[2][C], s_all[2], s_vs[2];  // w and e^{cl} of a stage's chunk
     // copies landed (of a ring's place); w made; w v made; product done; product read (of a stage)
     __shared__ __align__(8) uint64_t s_ld[L::ring], s_g[2], s_w[2], s_u[2], s_free[2];
@@ -652,12 +653,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
                     for (int i = 0; i < 8; i++) m = max(m, s_most[i]);
                     sc = f16_scale(__uint_as_float(m));
                 }
-                put_state<T, NB, kKeep, true>(image, image + NB * 8192, sc, X);
+                put_state<T, NB, kKeep, kImage>(image, sc, X);
                 fence_proxy_async_smem();
                 keep_sync();
                 if (lead) {
                     const int64_t at_image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + start_of(ch) / C;
-                    bulk_store(static_cast<char*>(at.dir(w).images) + at_image * (2 * NB * 8192), image, 2 * NB * 8192);
+                    bulk_store(static_cast<char*>(at.dir(w).images) + at_image * (kImage * NB * 8192), image, kImage * NB * 8192);
                     bulk_commit();
                     if (kF16<T>) at.dir(w).image_scale[at_image] = sc;
                 }
@@ -782,7 +783,7 @@ template <typename T, int NB> cudaError_t fwd_n(const TcWalkArgs& w, cudaStream_
     return go<k_tc_fwd<T, NB>>(256, FwdSmem<NB>::total, w.plan.blocks(), w, st);
 }
 template <typename T, int NB> cudaError_t state_n(const TcWalkArgs& w, bool sum, cudaStream_t st) {
-    constexpr int smem = StateSmem<NB>::total;
+    constexpr int smem = StateSmem<NB, kImageParts<kF16<T>, NB>>::total;
     return sum ? go<k_tc_state<T, NB, true>>(kStateThreads, smem, w.plan.cut * (w.plan.K - 1), w, st)
                : go<k_tc_state<T, NB, false>>(kStateThreads, smem, w.plan.blocks(), w, st);
 }
