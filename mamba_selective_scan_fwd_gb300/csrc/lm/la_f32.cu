@@ -4,10 +4,14 @@
 //
 // The walk (forward, and the states the backward needs) is the recurrence
 // itself, token by token with the state in registers: 3 N P operations per
-// token and head, fewer than any chunked form takes without matrix units.  The
-// decay enters as S + (e^g - 1) S: a rounded e^g near 1 would be off by the same
-// 2^-25 at every token and add up over a long memory.  The
-// backward works on chunks of 64 tokens from the states at their borders.
+// token and head, fewer than any chunked form takes without matrix units.  In a
+// tile of at most 16 tokens whose decay is e^-4 or weaker (kSlowTile) the state at
+// its start stays as it is and what the tile adds is summed apart, in units of the
+// decay since the start: the same operations, and the state is rounded once a tile
+// instead of twice a token, which a long memory adds up (2 x 3294 tokens, f32:
+// 1.4e-6 -> 2e-7 of f64).  Under a stronger decay the tokens enter one by one, with
+// the decay as S + (e^g - 1) S: a rounded e^g would be off by the same 2^-25 at
+// every token.  The backward works on chunks of 64 tokens from the states at their borders.
 #include <type_traits>
 
 #include "../simd.cuh"
@@ -16,6 +20,8 @@
 namespace ss {
 namespace la {
 namespace {
+
+constexpr float kSlowTile = -4.0f;  // keeps e^-c below 55: no range is lost
 
 // One block: kWalkP value channels of one head, one segment of tokens.  Lane = two
 // value channels 32 apart, warp = NR of the padded N state rows, in pairs.  The
@@ -26,14 +32,14 @@ namespace {
 //             update is the adjoint of the state after the token)
 // The next TT tokens are loaded into registers while these are computed.
 template <typename T, int NR, int MODE>
-__global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
+__global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
     constexpr bool Y = MODE == kWalkY;
     constexpr int NP = NR * 8, TT = Y && NR == 16 ? kWalkT / 2 : kWalkT;
     constexpr int EK = TT * NP / 256, EV = TT * kWalkP / 256;  // values a thread loads
     __shared__ __align__(16) float s_k[TT][NP];
     __shared__ __align__(16) float s_q[Y ? TT : 1][NP];
     __shared__ float s_v[TT][kWalkP];
-    __shared__ float s_a[TT], s_g[TT];
+    __shared__ float s_a[TT], s_down[TT], s_up[Y ? TT : 1], s_all;
     __shared__ float s_y[Y ? 8 : 1][Y ? TT : 1][kWalkP];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -108,7 +114,7 @@ __global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
         if (tid < TT) rg = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
     };
     fetch(0);
-    float total = 0.0f;  // thread 0 of a sum pass: the segment's log decay
+    float total = 0.0f;  // the segment's log decay
     for (int64_t i = 0; i < tiles; i++) {
         const int64_t t0 = start_of(i);
         if (MODE == kWalkStates) {
@@ -125,14 +131,25 @@ __global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
         }
 #pragma unroll
         for (int e = 0; e < EV; e++) (&s_v[0][0])[tid + 256 * e] = rv[e];
-        if (tid < TT) {
-            s_g[tid] = rg;
-            s_a[tid] = expm1f(rg);
+        if (warp == 0) {  // the tile's decays in the walk's direction
+            const int t = rev ? TT - 1 - lane : lane;
+            const float g[1] = {__shfl_sync(kFull, rg, t & (TT - 1))};
+            const float x[1] = {lane < TT ? g[0] : 0.0f};
+            Two c[1];
+            warp_cumsum<1>(x, c);
+            if (lane == 31) s_all = c[0].h + c[0].l;
+            const Two before = {__shfl_up_sync(kFull, c[0].h, 1), __shfl_up_sync(kFull, c[0].l, 1)};
+            if (rev) c[0] = lane ? before : Two{0.0f, 0.0f};
+            if (lane < TT) {
+                s_a[t] = expm1f(x[0]);
+                s_down[t] = expf(-c[0].h) * (1.0f - c[0].l);
+                if (Y) s_up[t] = expf(c[0].h) * (1.0f + c[0].l);
+            }
         }
         __syncthreads();
         if (i + 1 < tiles) fetch(i + 1);
-        if (MODE == kWalkSum && tid == 0)
-            for (int t = 0; t < nv; t++) total += s_g[t];
+        const float all = s_all;
+        total += all;
         // the direction as a constant: a test in the innermost loop doubled its instructions
         auto tokens = [&](auto direction) {
             constexpr bool R = decltype(direction)::value;
@@ -173,8 +190,57 @@ __global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
                     }
             }
         };
-        if (!Y && rev) tokens(std::true_type{});
-        else tokens(std::false_type{});
+        const bool slow = all >= kSlowTile;  // (NaN: no)
+        if (slow) {
+            // S = S0 + L in units of 2^c: S0 stays, L takes what the tile adds
+            float2 A[2][NR / 2];
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int r = 0; r < NR / 2; r++) A[c][r] = splat2(0.0f);
+#pragma unroll 2
+            for (int j = 0; j < nv; j++) {
+                const int t = !Y && rev ? nv - 1 - j : j;
+                const float down = s_down[t];
+                const float2 v[2] = {splat2(s_v[t][lane] * down), splat2(s_v[t][lane + 32] * down)};
+                float2 acc[2][2] = {{splat2(0.0f), splat2(0.0f)}, {splat2(0.0f), splat2(0.0f)}};
+#pragma unroll
+                for (int r = 0; r < NR / 2; r += 2) {
+                    const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
+                    const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
+#pragma unroll
+                    for (int c = 0; c < 2; c++)
+#pragma unroll
+                        for (int u = 0; u < 2; u++) A[c][r + u] = fma2(kr[u], v[c], A[c][r + u]);
+                    if (Y) {
+                        const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
+                        const float2 qr[2] = {make_float2(qq.x, qq.y), make_float2(qq.z, qq.w)};
+#pragma unroll
+                        for (int c = 0; c < 2; c++)
+#pragma unroll
+                            for (int u = 0; u < 2; u++) acc[c][u] = fma2(qr[u], add2(S[c][r + u], A[c][r + u]), acc[c][u]);
+                    }
+                }
+                if (Y)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        const float2 s = add2(acc[c][0], acc[c][1]);
+                        s_y[warp][t][lane + 32 * c] = s.x + s.y;
+                    }
+            }
+            const float2 keep = splat2(expm1f(all));
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int r = 0; r < NR / 2; r++) {
+                    const float2 x = add2(S[c][r], A[c][r]);
+                    S[c][r] = fma2(keep, x, x);
+                }
+        } else if (!Y && rev) {
+            tokens(std::true_type{});
+        } else {
+            tokens(std::false_type{});
+        }
         if (Y) {
             __syncthreads();
             T* yp = static_cast<T*>(w.y) + (b * a.L * a.H + h) * a.P;
@@ -186,7 +252,7 @@ __global__ void __launch_bounds__(256, 3) k_walk32(WalkArgs w) {
 #pragma unroll
                         for (int u = 0; u < 8; u++) y += s_y[u][t][c];
                     }
-                    st(yp + (t0 + t) * a.H * a.P + p0 + c, a.scale * y);
+                    st(yp + (t0 + t) * a.H * a.P + p0 + c, a.scale * (slow ? s_up[t] * y : y));
                 }
             }
         }
