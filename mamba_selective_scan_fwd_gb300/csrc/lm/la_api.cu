@@ -183,7 +183,7 @@ int tc_forward(const Args& a, const WalkTc& wl, void* y, float* last, char* ws, 
 
 struct BwdTc {
     WalkTc walk;
-    int64_t chunks;
+    int64_t chunks, part_rows;
     int splits, dg_parts;
     size_t before, after, before_scale, after_scale, dq, dk, dg, rows;
 };
@@ -193,14 +193,15 @@ BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     b.chunks = ceil_div(L, kChunkTc);
     const int64_t ptiles = ceil_div(P, kTileP), states = Bsz * H * ptiles * b.chunks;
     const bool f16 = dtype == SS_F16;
-    b.splits = f16 ? (int)(H / G * ptiles) : tc_splits(Bsz * b.chunks * G, H / G);
+    b.splits = f16 ? (int)(H / G * ptiles) : 1;
     b.dg_parts = f16 ? (int)ptiles : 1;
     const size_t images = (size_t)states * image_bytes(f16, N);
     b.before = l.take(images);
     b.after = l.take(images);
     b.before_scale = l.take(f16 ? states * 4 : 0);
     b.after_scale = l.take(f16 ? states * 4 : 0);
-    const size_t part = b.splits > 1 ? (size_t)b.splits * Bsz * L * G * N * 4 : 0;
+    b.part_rows = f16 ? (b.splits > 1 ? b.splits * Bsz : 0) : (H > G ? 2 * tc_bwd_blocks(Bsz * b.chunks * H) : 0);
+    const size_t part = (size_t)b.part_rows * (f16 ? L * G : kChunkTc) * N * 4;
     b.dq = l.take(part);
     b.dk = l.take(part);
     b.dg = l.take((size_t)b.dg_parts * Bsz * L * H * 4);
@@ -233,17 +234,20 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     Layout l;
     const BwdTc bl = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P, a.dtype);
-    const bool parts = bl.splits > 1;
-    const int64_t qk_rows = parts ? bl.splits * a.Bsz : a.Bsz;
-    const int qk_type = parts ? SS_F32 : a.dtype;
-    const In dq = {parts ? ws + bl.dq : d.dq, a.G * a.N, a.L * a.G * a.N}, dk = {parts ? ws + bl.dk : d.dk, a.G * a.N, a.L * a.G * a.N},
+    const bool f16 = a.dtype == SS_F16;
+    const int64_t part_heads = f16 ? a.G : 1, part_len = f16 ? a.L : kChunkTc;
+    auto part = [&](size_t at) { return In{ws + at, part_heads * a.N, part_len * part_heads * a.N}; };
+    const In dq = {d.dq, a.G * a.N, a.L * a.G * a.N}, dk = {d.dk, a.G * a.N, a.L * a.G * a.N},
              dv = {d.dv, a.H * a.P, a.L * a.H * a.P};
     if (!tc_map(encode, &b.maps.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &b.maps.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &b.maps.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &b.maps.dy, a.dy, a.H, a.P, a.L, a.Bsz, a.dtype) ||
-        !tc_map(encode, &b.maps.dq, dq, a.G, a.N, a.L, qk_rows, qk_type) ||
-        !tc_map(encode, &b.maps.dk, dk, a.G, a.N, a.L, qk_rows, qk_type) ||
+        !tc_map(encode, &b.maps.dq, dq, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &b.maps.dk, dk, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        (bl.part_rows > 0 &&
+         (!tc_map(encode, &b.maps.dq_part, part(bl.dq), part_heads, a.N, part_len, bl.part_rows, SS_F32) ||
+          !tc_map(encode, &b.maps.dk_part, part(bl.dk), part_heads, a.N, part_len, bl.part_rows, SS_F32))) ||
         !tc_map(encode, &b.maps.dv, dv, a.H, a.P, a.L, a.Bsz, a.dtype))
         return SS_OK;
     const int rc = device_status_word(&w.status);
@@ -271,11 +275,15 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     const bool own_dg = !a.g_per_head && bl.dg_parts == 1;
     b.dg = own_dg ? d.dg : f32(bl.dg);
     b.splits = bl.splits;
+    b.dq = d.dq;
+    b.dk = d.dk;
+    b.dq_part = f32(bl.dq);
+    b.dk_part = f32(bl.dk);
     b.status = w.status;
     if (launch_tc_bwd(b, st) != cudaSuccess) return SS_ERR_CUDA;
     if (bl.dg_parts > 1 && launch_sum_parts(b.dg, a.g_per_head ? b.dg : d.dg, nullptr, nullptr, bl.dg_parts, a.Bsz * a.L * a.H, SS_F32, st) != cudaSuccess)
         return SS_ERR_CUDA;
-    return bwd_sums(d, b.splits, f32(bl.dq), f32(bl.dk), b.dg, f32(bl.rows), st);
+    return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
 }
 
 bool empty(int64_t Bsz, int64_t L) { return Bsz == 0 || L == 0; }

@@ -79,26 +79,17 @@ struct TcWalkArgs {
     int* status;
 };
 
-// Parts the heads of a group are divided into in the backward, which runs one
-// block per SM: the fewest rounds of blocks times heads per block (each part
-// beyond the first costs an f32 copy of dq and dk, about a tenth of a head).
-inline int tc_splits(int64_t items, int64_t rep) {
-    int best = 1;
-    double least = 1e30;
-    for (int s = 1; s <= rep && s <= 64; s++) {
-        const double cost = (double)ceil_div(items * s, kSms) * ceil_div(rep, s) + (s > 1 ? 0.5 + 0.1 * s : 0.0);
-        if (cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
-}
+// The backward runs one block per SM.  bf16: the heads of all (batch row, chunk,
+// group) in a row, in equal runs: dq and dk of a group that one block holds whole are
+// outputs of that block, of one that is cut they are f32 parts (at most two a block:
+// of the group its run begins in and of the one it ends in) that a second kernel
+// adds up.
+inline int64_t tc_bwd_blocks(int64_t heads) { return heads < kSms ? heads : kSms; }
 
-// dq, dk: the outputs, or (splits > 1) the f32 parts [splits, Bsz, L, G, N] in boxes
-// of 32 columns.
+// dq, dk: the outputs; parts: f32, in boxes of 32 columns (bf16: [2 blocks, 128, N];
+// f16: [splits, Bsz, L, G, N], with splits > 1)
 struct TcBwdMaps {
-    CUtensorMap q, k, v, dy, dq, dk, dv;
+    CUtensorMap q, k, v, dy, dq, dk, dv, dq_part, dk_part;
 };
 
 struct TcBwdArgs {
@@ -108,7 +99,9 @@ struct TcBwdArgs {
     const float *before_scale, *after_scale;  // f16: their scales
     int64_t chunks;
     float* dg;                 // [Bsz, L, H]; f16: [value tiles, Bsz, L, H]
-    int splits;  // parts of a group's heads; f16: one per head and value tile
+    int splits;  // f16: parts of a group's dq and dk, one per head and value tile; bf16: 1
+    void *dq, *dk;
+    const float *dq_part, *dk_part;
     int* status;
 };
 cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st);

@@ -18,8 +18,8 @@
 // f16's range needs scales, powers of two that keep every operand's largest value
 // near 2^13: P has one, E, the scaled dy and the scaled v share one, H and R come
 // with theirs.  dq and dk of different heads then cannot add up in tensor memory:
-// with f16 a block's work is one head's value tile, and dq, dk are added up in f32
-// by a kernel of their own.
+// with f16 a block's work is one head's value tile, and all dq, dk are added up in
+// f32 by a kernel of their own.
 #include "../simd.cuh"
 #include "la_tc.h"
 #include "tc.cuh"
@@ -112,50 +112,60 @@ __device__ __forceinline__ void put_decays(Decays& d, const float (&g)[4], float
     }
 }
 
-// Where a block is: items blockIdx.x, + gridDim.x, ...; in each the heads h_lo ..
-// h_hi - 1 of one group, their value tiles (SINGLE: one head, one tile).
+// Where a block is.  SINGLE: items blockIdx.x, + gridDim.x, ... of one head's value
+// tile each.  Else a run of heads (item: the first of them in their group), with the
+// value tiles of each.
 struct Place {
-    int64_t item;
-    int b, chunk, gq, split, h, h_lo, h_hi, pt, pt_lo, pt_hi;
+    int64_t item, end;
+    int b, chunk, gq, part, h, h_lo, h_hi, pt, pt_lo, pt_hi;  // part: its row of dq's and dk's parts, -1: the outputs
     int first, last, more;  // of its item's heads and tiles; whether another place follows
 
-    __device__ void mark(const TcBwdArgs& w, int64_t items) {
+    template <bool SINGLE> __device__ void mark() {
         first = h == h_lo && pt == pt_lo;
         last = h + 1 == h_hi && pt + 1 == pt_hi;
-        more = !last || item + gridDim.x < items;
+        more = !last || item + (SINGLE ? (int64_t)gridDim.x : (int64_t)(h_hi - h_lo)) < end;
     }
     template <bool SINGLE> __device__ void begin(const TcBwdArgs& w, int ptiles) {
-        const int rep = (int)(w.a.H / w.a.G);
-        int64_t id = item;
-        split = (int)(id % w.splits);
-        id /= w.splits;
+        const int rep = (int)(w.a.H / w.a.G), per = SINGLE ? w.splits : rep;
+        const int at = (int)(item % per);
+        int64_t id = item / per;
+        const int64_t left = end - id * per;  // of the run, from the group's first head on
         gq = (int)(id % w.a.G);
         id /= w.a.G;
         chunk = (int)(id % w.chunks);
         b = (int)(id / w.chunks);
         if (SINGLE) {
-            h_lo = gq * rep + split / ptiles;
+            h_lo = gq * rep + at / ptiles;
             h_hi = h_lo + 1;
-            pt_lo = split % ptiles;
+            pt_lo = at % ptiles;
             pt_hi = pt_lo + 1;
+            part = w.splits == 1 ? -1 : at * (int)w.a.Bsz + b;
         } else {
-            h_lo = gq * rep + rep * split / w.splits;
-            h_hi = gq * rep + rep * (split + 1) / w.splits;
+            h_lo = gq * rep + at;
+            h_hi = gq * rep + (int)min((int64_t)rep, left);
             pt_lo = 0;
             pt_hi = ptiles;
+            part = h_hi - h_lo == rep ? -1 : 2 * (int)blockIdx.x + (at == 0);
         }
         h = h_lo;
         pt = pt_lo;
     }
-    template <bool SINGLE> __device__ void step(const TcBwdArgs& w, int ptiles, int64_t items) {  // if more
+    template <bool SINGLE> __device__ void start(const TcBwdArgs& w, int ptiles) {
+        const int64_t all = w.a.Bsz * w.chunks * w.a.G * (SINGLE ? w.splits : (int)(w.a.H / w.a.G));
+        item = SINGLE ? (int64_t)blockIdx.x : all * blockIdx.x / gridDim.x;
+        end = SINGLE ? all : all * (blockIdx.x + 1) / gridDim.x;
+        begin<SINGLE>(w, ptiles);
+        mark<SINGLE>();
+    }
+    template <bool SINGLE> __device__ void step(const TcBwdArgs& w, int ptiles) {  // if more
         if (++pt == pt_hi) {
             pt = pt_lo;
             if (++h == h_hi) {
-                item += gridDim.x;
+                item += SINGLE ? (int64_t)gridDim.x : (int64_t)(h_hi - h_lo);
                 begin<SINGLE>(w, ptiles);
             }
         }
-        mark(w, items);
+        mark<SINGLE>();
     }
 };
 
@@ -187,7 +197,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5, quarter = tid >> 7;
     char *Q = sm + L::q, *K = sm + L::k, *H = sm + L::h, *R = sm + L::r, *E = sm + L::e, *DS = sm + L::ds;
     const int ptiles = (int)((a.P + PT - 1) / PT);
-    const int64_t items = a.Bsz * w.chunks * a.G * w.splits;
 
     if (tid == 0) {
         uint64_t* one[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_m3, &s_sent};
@@ -213,13 +222,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     };
     auto image_of = [&](const Place& p) { return ((p.b * a.H + p.h) * ptiles + p.pt) * w.chunks + p.chunk; };
     // rounds through E at an item's end (dv has one at every iteration's): bf16 tiles of dq and dk, or f32 tiles
-    const int qk_rounds = w.splits == 1 ? NB : 2 * NB;
+    auto qk_rounds = [](const Place& p) { return p.part < 0 ? NB : 2 * NB; };
     Place at;  // the other warps
-    if (tid >= kCompute) {
-        at.item = blockIdx.x;
-        at.begin<kF16<T>>(w, ptiles);
-        at.mark(w, items);
-    }
+    if (tid >= kCompute) at.start<kF16<T>>(w, ptiles);
 
     if (tid >= kHelp) {  // ---------------- the helping warp
         const bool lead = lane == 0;
@@ -282,7 +287,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
         for (uint32_t it = 0;; it++) {
             Place next = at;
             if (at.more) {
-                next.step<kF16<T>>(w, ptiles, items);
+                next.step<kF16<T>>(w, ptiles);
                 raw_g(next, g);
                 // (the last iteration is over: nothing reads that place and those decays any more)
                 if (lead) s_at[(it + 1) % 3] = next;
@@ -294,18 +299,18 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             mbar_arrive(&s_dg);
             send([&] { tma_store_4d(&w.maps.dv, E, at.pt * PT, at.h, at.chunk * C, at.b); });
             if (at.last)
-                for (int k = 0; k < qk_rounds; k++)
+                for (int k = 0; k < qk_rounds(at); k++)
                     send([&] {
                         const int t0 = at.chunk * C;
-                        if (w.splits == 1) {  // NB == 1: dq and dk; NB == 2: both halves of one of them
+                        if (at.part < 0) {  // NB == 1: dq and dk; NB == 2: both halves of one of them
                             tma_store_4d(NB == 1 || k == 0 ? &w.maps.dq : &w.maps.dk, E, 0, at.gq, t0, at.b);
                             if (NB == 1) tma_store_4d(&w.maps.dk, E + 16384, 0, at.gq, t0, at.b);
                             else tma_store_4d(k == 0 ? &w.maps.dq : &w.maps.dk, E + 16384, 64, at.gq, t0, at.b);
                         } else {  // 64 columns of dq or dk, 32 a tile
-                            const CUtensorMap* map = k < NB ? &w.maps.dq : &w.maps.dk;
-                            const int n = (k % NB) * 64, row = at.split * (int)a.Bsz + at.b;
-                            tma_store_4d(map, E, n, at.gq, t0, row);
-                            tma_store_4d(map, E + 16384, n + 32, at.gq, t0, row);
+                            const CUtensorMap* map = k < NB ? &w.maps.dq_part : &w.maps.dk_part;
+                            const int n = (k % NB) * 64, g = kF16<T> ? at.gq : 0, t = kF16<T> ? t0 : 0;
+                            tma_store_4d(map, E, n, g, t, at.part);
+                            tma_store_4d(map, E + 16384, n + 32, g, t, at.part);
                         }
                     });
             if (!at.more) break;
@@ -349,7 +354,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 bulk_prefetch(static_cast<const char*>(w.after) + image_of(p) * kImage * part, kImage * part);
             };
             for (uint32_t it = 0; at.more; it++) {
-                at.step<kF16<T>>(w, ptiles, items);
+                at.step<kF16<T>>(w, ptiles);
                 prefetch(at);
                 wait(s_rh, it);
                 if (wait(s_m2, it)) load_v(at, it + 1);
@@ -420,7 +425,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             }
             __syncwarp();
             if (!at.more) break;
-            at.step<kF16<T>>(w, ptiles, items);
+            at.step<kF16<T>>(w, ptiles);
         }
         wait(s_m3, it);
         if (s_fail && lead) {  // a wait ran out: report, wait for what is in flight (within limits)
@@ -444,9 +449,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
         auto put_out = [&](const Place& at, const uint32_t (&dv)[8], float kap) {
             stage([&] { write_row(E, tok, quarter, dv); });
             if (!at.last) return;
-            for (int k = 0; k < qk_rounds; k++)
+            for (int k = 0; k < qk_rounds(at); k++)
                 stage([&] {
-                    if (w.splits == 1) {
+                    if (at.part < 0) {
 #pragma unroll
                         for (int c = 0; c < 2; c++) {  // 16 columns of a tile each: NB == 1: of dq, dk; NB == 2: of two tiles
                             const uint32_t from = NB == 1 ? (c == 0 ? tQ : tK) : (k == 0 ? tQ : tK) + 64 * c;
@@ -705,12 +710,42 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     if (tid < 32) tmem_free(tm, 512);
 }
 
+// dq and dk of the groups that the blocks' runs cut: sums of their parts in the
+// runs' order.  Block x of `runs` - 1: the group that run x cuts and holds the start of.
+__global__ void __launch_bounds__(256) k_tc_join(const __grid_constant__ TcBwdArgs w, int runs) {
+    const Args& a = w.a;
+    const int64_t rep = a.H / a.G, all = a.Bsz * w.chunks * a.H;
+    auto begin = [&](int64_t x) { return all * x / runs; };
+    int64_t x = blockIdx.x;
+    int64_t id = begin(x + 1) / rep;
+    const int64_t first = id * rep, end = first + rep;
+    if (begin(x + 1) == first || begin(x) > first) return;
+    const int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, t = e / a.N, n = e % a.N;
+    const int64_t gq = id % a.G;
+    id /= a.G;
+    const int64_t at = (id % w.chunks) * C + t, b = id / w.chunks;
+    if (t >= C || at >= a.L) return;
+    const float* part = blockIdx.z ? w.dk_part : w.dq_part;
+    const int64_t size = C * a.N;
+    float4 s = *reinterpret_cast<const float4*>(part + (2 * x + 1) * size + e);
+    while (begin(++x) < end) {
+        const float4 y = *reinterpret_cast<const float4*>(part + 2 * x * size + e);
+        s = {s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w};
+    }
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.z ? w.dk : w.dq) + ((b * a.L + at) * a.G + gq) * a.N + n;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2<__nv_bfloat16>(s.x, s.y), pack2<__nv_bfloat16>(s.z, s.w));
+}
+
 template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t st) {
     constexpr int smem = BwdSmem<NB>::total;
-    const cudaError_t e = allow_smem<k_tc_bwd<T, NB>>(smem);
+    cudaError_t e = allow_smem<k_tc_bwd<T, NB>>(smem);
     if (e != cudaSuccess) return e;
-    const int64_t items = w.a.Bsz * w.chunks * w.a.G * w.splits;
-    k_tc_bwd<T, NB><<<(unsigned)(items < kSms ? items : kSms), kThreads, smem, st>>>(w);
+    const int64_t rep = w.a.H / w.a.G, all = w.a.Bsz * w.chunks * w.a.G * (kF16<T> ? w.splits : rep), blocks = tc_bwd_blocks(all);
+    k_tc_bwd<T, NB><<<(unsigned)blocks, kThreads, smem, st>>>(w);
+    e = cudaGetLastError();
+    // (equal runs of whole groups leave nothing to join)
+    if (kF16<T> || e != cudaSuccess || (all % blocks == 0 && all / blocks % rep == 0)) return e;
+    k_tc_join<<<dim3((unsigned)blocks - 1, (unsigned)ceil_div(C * w.a.N, 1024), 2), 256, 0, st>>>(w, (int)blocks);
     return cudaGetLastError();
 }
 
