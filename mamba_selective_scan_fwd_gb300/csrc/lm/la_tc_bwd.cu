@@ -728,9 +728,13 @@ __global__ void __launch_bounds__(256) k_tc_join(const __grid_constant__ TcBwdAr
     const float* part = blockIdx.z ? w.dk_part : w.dq_part;
     const int64_t size = C * a.N;
     float4 s = *reinterpret_cast<const float4*>(part + (2 * x + 1) * size + e);
-    while (begin(++x) < end) {
-        const float4 y = *reinterpret_cast<const float4*>(part + 2 * x * size + e);
-        s = {s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w};
+    for (x++; begin(x) < end; x += 4) {  // four parts on their way at a time
+        float4 y[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            y[u] = u == 0 || begin(x + u) < end ? *reinterpret_cast<const float4*>(part + 2 * (x + u) * size + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int u = 0; u < 4; u++) s = {s.x + y[u].x, s.y + y[u].y, s.z + y[u].z, s.w + y[u].w};
     }
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.z ? w.dk : w.dq) + ((b * a.L + at) * a.G + gq) * a.N + n;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2<__nv_bfloat16>(s.x, s.y), pack2<__nv_bfloat16>(s.z, s.w));
