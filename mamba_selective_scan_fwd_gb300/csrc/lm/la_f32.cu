@@ -310,8 +310,20 @@ template <int NB> struct Smem32 {
     float a[kChunk32], b[kChunk32], col[8][kChunk32], red[8];
 };
 
-// Thread (ty, tx) of 16 x 16 holds rows ty + 16 r and columns tx + 16 s of
-// every product.  With c_i the cumulative log decay inside the chunk, cl its
+__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void fma4(float (&acc)[4], float x, float4 z) {
+    acc[0] = fmaf(x, z.x, acc[0]);
+    acc[1] = fmaf(x, z.y, acc[1]);
+    acc[2] = fmaf(x, z.z, acc[2]);
+    acc[3] = fmaf(x, z.w, acc[3]);
+}
+__device__ __forceinline__ float dot4(float4 x, float4 z, float acc) {
+    return fmaf(x.w, z.w, fmaf(x.z, z.z, fmaf(x.y, z.y, fmaf(x.x, z.x, acc))));
+}
+
+// Thread (ty, tx) of 16 x 16 holds four rows and some columns of every product:
+// rows and columns 16 apart where a product runs over the rows' own columns,
+// adjacent ones where that makes a shared-memory read of 16 bytes.  With c_i the cumulative log decay inside the chunk, cl its
 // end, H the state before and R the adjoint after the chunk (all per head):
 //   m_ij = scale e^{c_i - c_j} (j <= i),  E = m o (dy v^T),  S = m o (q k^T),  W = E o (q k^T)
 //   dq = E k + scale e^{c} (dy H^T),  dk = E^T q + e^{cl - c} (v R^T),  dv = S^T dy + e^{cl - c} (k R)
@@ -374,15 +386,17 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             __syncthreads();
             const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + t0 * a.v.token + h * a.P + p0;
             const T* yp = static_cast<const T*>(a.dy.p) + b * a.dy.batch + t0 * a.dy.token + h * a.P + p0;
-            for (int e = tid; e < C * kPT; e += 256) {
-                const int t = e / kPT, p = e % kPT;
+#pragma unroll
+            for (int u = 0; u < C * kPT / 256; u++) {
+                const int e = tid + 256 * u, t = e / kPT, p = e % kPT;
                 const bool on = t < nv && p0 + p < a.P;
                 s.v[t][p] = on ? ldf(vp + t * a.v.token + p) : 0.0f;
                 s.dy[t][p] = on ? ldf(yp + t * a.dy.token + p) : 0.0f;
             }
             const int64_t at = ((b * a.H + h) * w.chunks + chunk) * a.N * a.P + p0;
-            for (int e = tid; e < NP * kPT; e += 256) {
-                const int n = e / kPT, p = e % kPT;
+#pragma unroll
+            for (int u = 0; u < NP * kPT / 256; u++) {
+                const int e = tid + 256 * u, n = e / kPT, p = e % kPT;
                 const bool on = n < a.N && p0 + p < a.P;
                 const float hv = on ? w.before[at + n * a.P + p] : 0.0f, rv = on ? w.after[at + n * a.P + p] : 0.0f;
                 s.H[n][p] = hv;
@@ -451,34 +465,35 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             }
             __syncthreads();
             const Two cl = s.c[C - 1];
-            {  // dv, and b from its inter-chunk part
+            {  // dv, and b from its inter-chunk part: rows 4 ty + r, columns 4 tx + c
                 float in[4][4] = {}, ac[4][4] = {};
+#pragma unroll 4
                 for (int i = 0; i < C; i++) {
-                    float x[4], z[4];
+                    const float4 x = at4(&s.S[i][4 * ty]), z = at4(&s.dy[i][4 * tx]);
+                    const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = s.S[i][ty + 16 * r], z[r] = s.dy[i][tx + 16 * r];
-#pragma unroll
-                    for (int r = 0; r < 4; r++)
-#pragma unroll
-                        for (int c = 0; c < 4; c++) ac[r][c] = fmaf(x[r], z[c], ac[r][c]);
+                    for (int r = 0; r < 4; r++) fma4(ac[r], xs[r], z);
                 }
-                for (int n = 0; n < NP; n++) {
-                    float x[4], z[4];
+                for (int n = 0; n < NP; n += 4) {
+                    float4 x[4], z[4];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = s.k[ty + 16 * r][n], z[r] = s.R[n][tx + 16 * r];
+                    for (int r = 0; r < 4; r++) x[r] = at4(&s.k[4 * ty + r][n]), z[r] = at4(&s.R[n + r][4 * tx]);
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-#pragma unroll
-                        for (int c = 0; c < 4; c++) in[r][c] = fmaf(x[r], z[c], in[r][c]);
+                    for (int r = 0; r < 4; r++) {
+                        fma4(in[r], x[r].x, z[0]);
+                        fma4(in[r], x[r].y, z[1]);
+                        fma4(in[r], x[r].z, z[2]);
+                        fma4(in[r], x[r].w, z[3]);
+                    }
                 }
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const int j = ty + 16 * r;
+                    const int j = 4 * ty + r;
                     const float d = ex2(two_diff(cl, s.c[j]));
                     float bj = 0.0f;
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
-                        const int p = tx + 16 * c;
+                        const int p = 4 * tx + c;
                         const float x = d * in[r][c];
                         bj = fmaf(s.v[j][p], x, bj);
                         if (j < nt && p0 + p < a.P)
@@ -490,33 +505,34 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                     if (tx == 0) s.b[j] += bj;
                 }
             }
-            {  // dq, and a from its inter-chunk part
-                for (int j = 0; j < C; j++) {
-                    float x[4];
+            {  // dq, and a from its inter-chunk part: rows 4 ty + r, columns tx + 16 n
+                for (int j = 0; j < C; j += 4) {
+                    float4 x[4];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = s.E[ty + 16 * r][j];
+                    for (int r = 0; r < 4; r++) x[r] = at4(&s.E[4 * ty + r][j]);
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
-                        const float z = s.k[j][tx + 16 * n];
+                        const int m = tx + 16 * n;
+                        const float4 z = make_float4(s.k[j][m], s.k[j + 1][m], s.k[j + 2][m], s.k[j + 3][m]);
 #pragma unroll
-                        for (int r = 0; r < 4; r++) dq[r][n] = fmaf(x[r], z, dq[r][n]);
+                        for (int r = 0; r < 4; r++) dq[r][n] = dot4(x[r], z, dq[r][n]);
                     }
                 }
                 float in[4][NB] = {};
-                for (int p = 0; p < kPT; p++) {
-                    float x[4];
+                for (int p = 0; p < kPT; p += 4) {
+                    float4 x[4];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = s.dy[ty + 16 * r][p];
+                    for (int r = 0; r < 4; r++) x[r] = at4(&s.dy[4 * ty + r][p]);
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
-                        const float z = s.H[tx + 16 * n][p];
+                        const float4 z = at4(&s.H[tx + 16 * n][p]);
 #pragma unroll
-                        for (int r = 0; r < 4; r++) in[r][n] = fmaf(x[r], z, in[r][n]);
+                        for (int r = 0; r < 4; r++) in[r][n] = dot4(x[r], z, in[r][n]);
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const int i = ty + 16 * r;
+                    const int i = 4 * ty + r;
                     const float d = a.scale * ex2(s.c[i].h + s.c[i].l);
                     float ai = 0.0f;
 #pragma unroll
@@ -530,33 +546,34 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                     if (tx == 0) s.a[i] += ai;
                 }
             }
-            {  // dk
+            {  // dk, like dq
+#pragma unroll 4
                 for (int i = 0; i < C; i++) {
-                    float x[4];
-#pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = s.E[i][ty + 16 * r];
+                    const float4 x = at4(&s.E[i][4 * ty]);
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
                         const float z = s.q[i][tx + 16 * n];
-#pragma unroll
-                        for (int r = 0; r < 4; r++) dk[r][n] = fmaf(x[r], z, dk[r][n]);
+                        dk[0][n] = fmaf(x.x, z, dk[0][n]);
+                        dk[1][n] = fmaf(x.y, z, dk[1][n]);
+                        dk[2][n] = fmaf(x.z, z, dk[2][n]);
+                        dk[3][n] = fmaf(x.w, z, dk[3][n]);
                     }
                 }
                 float in[4][NB] = {};
-                for (int p = 0; p < kPT; p++) {
-                    float x[4];
+                for (int p = 0; p < kPT; p += 4) {
+                    float4 x[4];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = s.v[ty + 16 * r][p];
+                    for (int r = 0; r < 4; r++) x[r] = at4(&s.v[4 * ty + r][p]);
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
-                        const float z = s.R[tx + 16 * n][p];
+                        const float4 z = at4(&s.R[tx + 16 * n][p]);
 #pragma unroll
-                        for (int r = 0; r < 4; r++) in[r][n] = fmaf(x[r], z, in[r][n]);
+                        for (int r = 0; r < 4; r++) in[r][n] = dot4(x[r], z, in[r][n]);
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const float d = ex2(two_diff(cl, s.c[ty + 16 * r]));
+                    const float d = ex2(two_diff(cl, s.c[4 * ty + r]));
 #pragma unroll
                     for (int n = 0; n < NB; n++) dk[r][n] = fmaf(d, in[r][n], dk[r][n]);
                 }
@@ -591,7 +608,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
     }
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-        const int t = ty + 16 * r;
+        const int t = 4 * ty + r;
         if (t >= nt) continue;
 #pragma unroll
         for (int n = 0; n < NB; n++) {

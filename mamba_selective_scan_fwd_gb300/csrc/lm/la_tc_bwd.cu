@@ -713,30 +713,40 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 // dq and dk of the groups that the blocks' runs cut: sums of their parts in the
 // runs' order.  Block x of `runs` - 1: the group that run x cuts and holds the start of.
 __global__ void __launch_bounds__(256) k_tc_join(const __grid_constant__ TcBwdArgs w, int runs) {
+    __shared__ int s_parts, s_t0;  // parts after the first (-1: nothing to do); the chunk's first token
+    __shared__ int64_t s_out;      // its place in dq and dk
     const Args& a = w.a;
-    const int64_t rep = a.H / a.G, all = a.Bsz * w.chunks * a.H;
-    auto begin = [&](int64_t x) { return all * x / runs; };
-    int64_t x = blockIdx.x;
-    int64_t id = begin(x + 1) / rep;
-    const int64_t first = id * rep, end = first + rep;
-    if (begin(x + 1) == first || begin(x) > first) return;
-    const int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, t = e / a.N, n = e % a.N;
-    const int64_t gq = id % a.G;
-    id /= a.G;
-    const int64_t at = (id % w.chunks) * C + t, b = id / w.chunks;
-    if (t >= C || at >= a.L) return;
-    const float* part = blockIdx.z ? w.dk_part : w.dq_part;
-    const int64_t size = C * a.N;
-    float4 s = *reinterpret_cast<const float4*>(part + (2 * x + 1) * size + e);
-    for (x++; begin(x) < end; x += 4) {  // four parts on their way at a time
+    if (threadIdx.x == 0) {
+        const int64_t rep = a.H / a.G, all = a.Bsz * w.chunks * a.H;
+        auto begin = [&](int64_t x) { return all * x / runs; };
+        int64_t x = blockIdx.x, id = begin(x + 1) / rep;
+        const int64_t first = id * rep, end = first + rep;
+        int parts = -1;
+        if (begin(x + 1) > first && begin(x) <= first) {
+            parts = 0;
+            while (begin(++x) < end) parts++;
+        }
+        s_parts = parts;
+        const int64_t gq = id % a.G, b = id / a.G / w.chunks;
+        s_t0 = (int)(id / a.G % w.chunks) * C;
+        s_out = ((b * a.L + s_t0) * a.G + gq) * a.N;
+    }
+    __syncthreads();
+    const int parts = s_parts, N = (int)a.N;
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4, t = e / N;
+    if (parts < 0 || t >= C || s_t0 + t >= a.L) return;
+    const int64_t size = C * N;
+    const float* part = (blockIdx.z ? w.dk_part : w.dq_part) + 2 * (int64_t)blockIdx.x * size + e;
+    float4 s = *reinterpret_cast<const float4*>(part + size);
+    for (int u0 = 1; u0 <= parts; u0 += 4) {  // four parts on their way at a time
         float4 y[4];
 #pragma unroll
         for (int u = 0; u < 4; u++)
-            y[u] = u == 0 || begin(x + u) < end ? *reinterpret_cast<const float4*>(part + 2 * (x + u) * size + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            y[u] = u0 + u <= parts ? *reinterpret_cast<const float4*>(part + 2 * (u0 + u) * size) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int u = 0; u < 4; u++) s = {s.x + y[u].x, s.y + y[u].y, s.z + y[u].z, s.w + y[u].w};
     }
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.z ? w.dk : w.dq) + ((b * a.L + at) * a.G + gq) * a.N + n;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.z ? w.dk : w.dq) + s_out + (int64_t)t * a.G * N + e % N;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2<__nv_bfloat16>(s.x, s.y), pack2<__nv_bfloat16>(s.z, s.w));
 }
 
