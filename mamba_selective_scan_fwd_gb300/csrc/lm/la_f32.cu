@@ -311,14 +311,15 @@ template <int NB> struct Smem32 {
 };
 
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ void fma4(float (&acc)[4], float x, float4 z) {
-    acc[0] = fmaf(x, z.x, acc[0]);
-    acc[1] = fmaf(x, z.y, acc[1]);
-    acc[2] = fmaf(x, z.z, acc[2]);
-    acc[3] = fmaf(x, z.w, acc[3]);
+// acc (4 adjacent values) += x z
+__device__ __forceinline__ void fma4(float2 (&acc)[2], float x, float4 z) {
+    acc[0] = fma2(splat2(x), make_float2(z.x, z.y), acc[0]);
+    acc[1] = fma2(splat2(x), make_float2(z.z, z.w), acc[1]);
 }
-__device__ __forceinline__ float dot4(float4 x, float4 z, float acc) {
-    return fmaf(x.w, z.w, fmaf(x.z, z.z, fmaf(x.y, z.y, fmaf(x.x, z.x, acc))));
+// acc (two halves of a sum) += x . z
+__device__ __forceinline__ void dot4(float2& acc, float4 x, float4 z) {
+    acc = fma2(make_float2(x.x, x.y), make_float2(z.x, z.y), acc);
+    acc = fma2(make_float2(x.z, x.w), make_float2(z.z, z.w), acc);
 }
 
 // Thread (ty, tx) of 16 x 16 holds four rows and some columns of every product:
@@ -353,17 +354,15 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
 
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + t0 * a.q.token + gq * a.N;
     const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + t0 * a.k.token + gq * a.N;
-    for (int e = tid; e < C * NP; e += 256) {
-        const int t = e / NP, n = e % NP;
+#pragma unroll 8
+    for (int u = 0; u < C * NP / 256; u++) {
+        const int e = tid + 256 * u, t = e / NP, n = e % NP;
         const bool on = t < nv && n < a.N;
         s.q[t][n] = on ? ldf(qp + t * a.q.token + n) : 0.0f;
         s.k[t][n] = on ? ldf(kp + t * a.k.token + n) : 0.0f;
     }
-    float dq[4][NB], dk[4][NB];
-#pragma unroll
-    for (int r = 0; r < 4; r++)
-#pragma unroll
-        for (int n = 0; n < NB; n++) dq[r][n] = dk[r][n] = 0.0f;
+    float dq[4][NB] = {};
+    float2 dk[2][NB] = {};  // pairs of rows
 
     for (int64_t h = h_lo; h < h_hi; h++) {
         __syncthreads();
@@ -405,31 +404,25 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             }
             __syncthreads();
             {  // scores
-                float qk[4][4] = {}, yv[4][4] = {};
-                for (int n = 0; n < NP; n += 4) {
-                    float4 x[4], z[4];
+                float qk[4][4], yv[4][4];
+                auto scores = [&](float (&out)[4][4], const auto& left, const auto& right, int n) {  // rows . rows, of n values
+                    float2 acc[4][4] = {};
+                    for (int e = 0; e < n; e += 4) {
+                        float4 x[4], z[4];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = *reinterpret_cast<const float4*>(&s.q[ty + 16 * r][n]);
+                        for (int r = 0; r < 4; r++) x[r] = at4(&left[ty + 16 * r][e]), z[r] = at4(&right[tx + 16 * r][e]);
 #pragma unroll
-                    for (int r = 0; r < 4; r++) z[r] = *reinterpret_cast<const float4*>(&s.k[tx + 16 * r][n]);
+                        for (int r = 0; r < 4; r++)
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-#pragma unroll
-                        for (int c = 0; c < 4; c++)
-                            qk[r][c] += x[r].x * z[c].x + x[r].y * z[c].y + x[r].z * z[c].z + x[r].w * z[c].w;
-                }
-                for (int p = 0; p < kPT; p += 4) {
-                    float4 x[4], z[4];
-#pragma unroll
-                    for (int r = 0; r < 4; r++) x[r] = *reinterpret_cast<const float4*>(&s.dy[ty + 16 * r][p]);
-#pragma unroll
-                    for (int r = 0; r < 4; r++) z[r] = *reinterpret_cast<const float4*>(&s.v[tx + 16 * r][p]);
+                            for (int c = 0; c < 4; c++) dot4(acc[r][c], x[r], z[c]);
+                    }
 #pragma unroll
                     for (int r = 0; r < 4; r++)
 #pragma unroll
-                        for (int c = 0; c < 4; c++)
-                            yv[r][c] += x[r].x * z[c].x + x[r].y * z[c].y + x[r].z * z[c].z + x[r].w * z[c].w;
-                }
+                        for (int c = 0; c < 4; c++) out[r][c] = acc[r][c].x + acc[r][c].y;
+                };
+                scores(qk, s.q, s.k, NP);
+                scores(yv, s.dy, s.v, kPT);
                 float col[4] = {};
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
@@ -466,7 +459,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             __syncthreads();
             const Two cl = s.c[C - 1];
             {  // dv, and b from its inter-chunk part: rows 4 ty + r, columns 4 tx + c
-                float in[4][4] = {}, ac[4][4] = {};
+                float2 in[4][2] = {}, ac[4][2] = {};
 #pragma unroll 4
                 for (int i = 0; i < C; i++) {
                     const float4 x = at4(&s.S[i][4 * ty]), z = at4(&s.dy[i][4 * tx]);
@@ -494,11 +487,11 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         const int p = 4 * tx + c;
-                        const float x = d * in[r][c];
+                        const float x = d * (c & 1 ? in[r][c / 2].y : in[r][c / 2].x);
                         bj = fmaf(s.v[j][p], x, bj);
                         if (j < nt && p0 + p < a.P)
                             st(static_cast<T*>(w.dv) + ((b * a.L + t0 + j) * a.H + h) * a.P + p0 + p,
-                               j < nv ? ac[r][c] + x : 0.0f);
+                               j < nv ? (c & 1 ? ac[r][c / 2].y : ac[r][c / 2].x) + x : 0.0f);
                     }
 #pragma unroll
                     for (int o = 8; o > 0; o >>= 1) bj += __shfl_xor_sync(kFull, bj, o);
@@ -506,6 +499,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                 }
             }
             {  // dq, and a from its inter-chunk part: rows 4 ty + r, columns tx + 16 n
+                float2 ac[4][NB] = {}, in[4][NB] = {};
                 for (int j = 0; j < C; j += 4) {
                     float4 x[4];
 #pragma unroll
@@ -515,10 +509,9 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                         const int m = tx + 16 * n;
                         const float4 z = make_float4(s.k[j][m], s.k[j + 1][m], s.k[j + 2][m], s.k[j + 3][m]);
 #pragma unroll
-                        for (int r = 0; r < 4; r++) dq[r][n] = dot4(x[r], z, dq[r][n]);
+                        for (int r = 0; r < 4; r++) dot4(ac[r][n], x[r], z);
                     }
                 }
-                float in[4][NB] = {};
                 for (int p = 0; p < kPT; p += 4) {
                     float4 x[4];
 #pragma unroll
@@ -527,7 +520,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                     for (int n = 0; n < NB; n++) {
                         const float4 z = at4(&s.H[tx + 16 * n][p]);
 #pragma unroll
-                        for (int r = 0; r < 4; r++) in[r][n] = dot4(x[r], z, in[r][n]);
+                        for (int r = 0; r < 4; r++) dot4(in[r][n], x[r], z);
                     }
                 }
 #pragma unroll
@@ -537,9 +530,9 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                     float ai = 0.0f;
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
-                        const float x = d * in[r][n];
+                        const float x = d * (in[r][n].x + in[r][n].y);
                         ai = fmaf(s.q[i][tx + 16 * n], x, ai);
-                        dq[r][n] += x;
+                        dq[r][n] += ac[r][n].x + ac[r][n].y + x;
                     }
 #pragma unroll
                     for (int o = 8; o > 0; o >>= 1) ai += __shfl_xor_sync(kFull, ai, o);
@@ -553,13 +546,11 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
                         const float z = s.q[i][tx + 16 * n];
-                        dk[0][n] = fmaf(x.x, z, dk[0][n]);
-                        dk[1][n] = fmaf(x.y, z, dk[1][n]);
-                        dk[2][n] = fmaf(x.z, z, dk[2][n]);
-                        dk[3][n] = fmaf(x.w, z, dk[3][n]);
+                        dk[0][n] = fma2(make_float2(x.x, x.y), splat2(z), dk[0][n]);
+                        dk[1][n] = fma2(make_float2(x.z, x.w), splat2(z), dk[1][n]);
                     }
                 }
-                float in[4][NB] = {};
+                float2 in[4][NB] = {};
                 for (int p = 0; p < kPT; p += 4) {
                     float4 x[4];
 #pragma unroll
@@ -568,14 +559,15 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
                     for (int n = 0; n < NB; n++) {
                         const float4 z = at4(&s.R[tx + 16 * n][p]);
 #pragma unroll
-                        for (int r = 0; r < 4; r++) in[r][n] = dot4(x[r], z, in[r][n]);
+                        for (int r = 0; r < 4; r++) dot4(in[r][n], x[r], z);
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const float d = ex2(two_diff(cl, s.c[4 * ty + r]));
+                for (int r = 0; r < 4; r += 2) {
+                    const float2 d = make_float2(ex2(two_diff(cl, s.c[4 * ty + r])), ex2(two_diff(cl, s.c[4 * ty + r + 1])));
 #pragma unroll
-                    for (int n = 0; n < NB; n++) dk[r][n] = fmaf(d, in[r][n], dk[r][n]);
+                    for (int n = 0; n < NB; n++)
+                        dk[r / 2][n] = fma2(d, make_float2(in[r][n].x + in[r][n].y, in[r + 1][n].x + in[r + 1][n].y), dk[r / 2][n]);
                 }
             }
         }
@@ -615,7 +607,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             const int c = tx + 16 * n;
             if (c >= a.N) continue;
             const int64_t at = ((b * a.L + t0 + t) * a.G + gq) * a.N + c;
-            const float x = t < nv ? dq[r][n] : 0.0f, z = t < nv ? dk[r][n] : 0.0f;
+            const float x = t < nv ? dq[r][n] : 0.0f, z = t < nv ? (r & 1 ? dk[r / 2][n].y : dk[r / 2][n].x) : 0.0f;
             if (w.splits > 1) {
                 const int64_t part = split * a.Bsz * a.L * a.G * a.N + at;
                 w.dq_part[part] = x;
