@@ -53,7 +53,8 @@ constexpr int kWalkT = 16;    // tokens staged at a time (at most)
 constexpr int kChunk32 = 64;  // tokens per chunk of the FP32 backward
 
 // The token walk: every unit (direction, batch row, head, tile of value
-// channels) is cut into K segments of seg tokens (a multiple of a chunk).
+// channels) is cut into K segments of seg tokens (a multiple of a chunk; the
+// backward's are one chunk each: their start states are what it reads).
 struct WalkPlan {
     int64_t K, seg;
 };
@@ -76,16 +77,16 @@ inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t chunk) {
     return best;
 }
 
-enum WalkMode { kWalkSum = 0, kWalkY = 1, kWalkStates = 2 };
+enum WalkMode { kWalkSum = 0, kWalkY = 1 };
 
 // What a walk starts from and leaves, one for each direction.
 struct WalkDir {
     const float* init;   // state before the walk's first token, or null
     float* last;         // state after its last token, or null
-    float* chunk_state;  // kWalkStates: [Bsz, H, chunks, N, P] state before each chunk (in walking order)
 };
 
-// dirs = 1: forward; 2: the forward's and the reverse walk in one launch.
+// dirs = 1: the forward, whose sum pass leaves out the segment walked last; 2: the
+// backward's states in both directions, from sums of all segments.
 struct WalkArgs {
     Args a;
     WalkPlan plan;
@@ -94,7 +95,6 @@ struct WalkArgs {
     float* seg_state;  // [dirs, Bsz, H, K, N, P]: end states of the segments, then (after the carry) their start states
     float* seg_decay;  // [dirs, Bsz, H, K]
     void* y;           // kWalkY
-    int64_t chunks;
 };
 
 struct BwdArgs {

@@ -45,9 +45,10 @@ struct Walk32 {
 };
 Walk32 walk32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dirs) {
     Walk32 w;
-    w.plan = walk_plan(dirs * Bsz * H * ceil_div(P, kWalkP), L, kChunk32);
+    if (dirs == 1) w.plan = walk_plan(Bsz * H * ceil_div(P, kWalkP), L, kChunk32);
+    else w.plan = {ceil_div(L, kChunk32), kChunk32};
     w.state = w.decay = 0;
-    if (w.plan.K > 1) {
+    if (dirs == 2 || w.plan.K > 1) {
         w.state = l.take((size_t)dirs * Bsz * H * w.plan.K * N * P * 4);
         w.decay = l.take((size_t)dirs * Bsz * H * w.plan.K * 4);
     }
@@ -58,7 +59,7 @@ struct Bwd32 {
     Walk32 walk;
     int64_t chunks;
     int splits;
-    size_t before, after, dq, dk, dg, rows;
+    size_t dq, dk, dg, rows;
 };
 // Parts the heads of a group are divided into, so that the chunk kernel has
 // about two blocks per SM; each part beyond the first costs one more f32 copy
@@ -73,9 +74,6 @@ Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     b.walk = walk32_layout(l, Bsz, L, H, N, P, 2);
     b.chunks = ceil_div(L, kChunk32);
     b.splits = head_splits(Bsz * b.chunks * G, H / G);
-    const size_t states = (size_t)Bsz * H * b.chunks * N * P * 4;
-    b.before = l.take(states);
-    b.after = l.take(states);
     const size_t part = b.splits > 1 ? (size_t)b.splits * Bsz * L * G * N * 4 : 0;
     b.dq = l.take(part);
     b.dk = l.take(part);
@@ -297,14 +295,10 @@ int pass_state(float* to, const float* from, int64_t Bsz, int64_t H, int64_t N, 
     return e == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
-// A walk over all segments: sums of the segments, their carries, then the walk itself.
-cudaError_t run_walk32(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
-    if (w.plan.K > 1) {
-        cudaError_t e = launch_walk32(w, kWalkSum, st);
-        if (e == cudaSuccess) e = launch_carry32(w, st);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_walk32(w, mode, st);
+// The segments' sums and their carries.
+cudaError_t start_states32(const WalkArgs& w, cudaStream_t st) {
+    const cudaError_t e = launch_walk32(w, kWalkSum, st);
+    return e != cudaSuccess ? e : launch_carry32(w, st);
 }
 
 bool strides_ok(int64_t token, int64_t batch) { return token >= 0 && batch >= 0 && token <= (1ll << 40) && batch <= (1ll << 48); }
@@ -352,11 +346,12 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
     w.a = a;
     w.plan = wl.plan;
     w.dirs = 1;
-    w.dir[0] = {a.h0, d->last_state, nullptr};
+    w.dir[0] = {a.h0, d->last_state};
     w.seg_state = reinterpret_cast<float*>(ws + wl.state);
     w.seg_decay = reinterpret_cast<float*>(ws + wl.decay);
     w.y = d->y;
-    return run_walk32(w, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+    if (w.plan.K > 1 && start_states32(w, st) != cudaSuccess) return SS_ERR_CUDA;
+    return launch_walk32(w, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 size_t ss_la_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
@@ -414,15 +409,14 @@ int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
     w.plan = bl.walk.plan;
     w.seg_state = f32(bl.walk.state);
     w.seg_decay = f32(bl.walk.decay);
-    w.chunks = bl.chunks;
     w.dirs = 2;
-    w.dir[0] = {a.h0, nullptr, f32(bl.before)};
-    w.dir[1] = {a.dlast, d->dh0, f32(bl.after)};
-    if (run_walk32(w, kWalkStates, st) != cudaSuccess) return SS_ERR_CUDA;
+    w.dir[0] = {a.h0, nullptr};
+    w.dir[1] = {a.dlast, d->dh0};
+    if (start_states32(w, st) != cudaSuccess) return SS_ERR_CUDA;
     BwdArgs b = {};
     b.a = a;
-    b.before = f32(bl.before);
-    b.after = f32(bl.after);
+    b.before = w.seg_state;
+    b.after = w.seg_state + a.Bsz * a.H * bl.chunks * a.N * a.P;
     b.chunks = bl.chunks;
     b.dq = d->dq; b.dk = d->dk; b.dv = d->dv;
     b.dg = a.g_per_head ? f32(bl.dg) : d->dg;

@@ -49,12 +49,10 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
     id /= ptiles;
     const int64_t h = id % a.H;
     id /= a.H;
-    const int64_t segs = MODE == kWalkSum ? w.plan.K - 1 : w.plan.K;
-    int64_t seg = id % segs;
+    const int64_t segs = !Y && w.dirs == 1 ? w.plan.K - 1 : w.plan.K, seg = id % segs;
     id /= segs;
     const int64_t b = id % a.Bsz;
-    const bool rev = id / a.Bsz != 0;
-    if (MODE == kWalkSum && rev) seg += 1;  // the segment walked last needs no sum
+    const bool rev = !Y && id / a.Bsz != 0;
     const int64_t hq = h / (a.H / a.G), bh = b * a.H + h, at = ((rev ? a.Bsz * a.H : 0) + bh) * w.plan.K + seg;
     const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
     const int64_t len = row_length(a, b);
@@ -70,7 +68,7 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
 
     float2 S[2][NR / 2];  // [channel][pair of rows]
     const float* init = nullptr;
-    if (MODE != kWalkSum) {
+    if (Y) {
         if (w.plan.K > 1) init = w.seg_state + at * NPel;
         else if (dir.init) init = dir.init + bh * NPel;
     }
@@ -117,11 +115,6 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
     float total = 0.0f;  // the segment's log decay
     for (int64_t i = 0; i < tiles; i++) {
         const int64_t t0 = start_of(i);
-        if (MODE == kWalkStates) {
-            const int64_t c = t0 / kChunk32;
-            const bool first = rev ? (t0 + TT >= t_end || (t0 + TT) % kChunk32 == 0) : t0 % kChunk32 == 0;
-            if (first) put(dir.chunk_state + (bh * w.chunks + c) * NPel);
-        }
         const int nv = valid(t0);
         __syncthreads();
 #pragma unroll
@@ -257,10 +250,10 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
             }
         }
     }
-    if (MODE == kWalkSum) {
+    if (!Y) {
         put(w.seg_state + at * NPel);
         if (tid == 0 && p0 == 0) w.seg_decay[at] = total;
-    } else if (dir.last && seg == (rev ? 0 : w.plan.K - 1)) {
+    } else if (dir.last && seg == w.plan.K - 1) {
         put(dir.last + bh * NPel);
     }
 }
@@ -276,13 +269,14 @@ __global__ void __launch_bounds__(256) k_carry32(WalkArgs w, int64_t first) {
     const bool rev = unit >= BH;
     const float* init = w.dir[rev].init;
     float S = init ? init[(unit - (rev ? BH : 0)) * NP + x] : 0.0f;
+    const int64_t sums = w.dirs == 1 ? K - 1 : K;
     for (int64_t i0 = 0; i0 < K; i0 += U) {
         float own[U], d[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int64_t i = i0 + u, s = unit * K + (rev ? K - 1 - i : i);
             own[u] = d[u] = 0.0f;
-            if (i + 1 < K) {  // the segment walked last has no sum
+            if (i < sums) {
                 own[u] = w.seg_state[s * NP + x];
                 d[u] = expf(w.seg_decay[s]);
             }
@@ -291,9 +285,11 @@ __global__ void __launch_bounds__(256) k_carry32(WalkArgs w, int64_t first) {
         for (int u = 0; u < U; u++) {
             const int64_t i = i0 + u, s = unit * K + (rev ? K - 1 - i : i);
             if (i < K) w.seg_state[s * NP + x] = S;
-            S = fmaf(d[u], S, own[u]);
+            if (i < sums) S = fmaf(d[u], S, own[u]);
         }
     }
+    float* last = w.dir[rev].last;
+    if (w.dirs == 2 && last) last[(unit - (rev ? BH : 0)) * NP + x] = S;
 }
 
 // ---------------------------------------------------------------- backward, one chunk of one group of heads
@@ -669,10 +665,9 @@ __global__ void __launch_bounds__(256) k_sum_rows(const float* x, float* part, i
 
 template <typename T, int NR> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
     const Args& a = w.a;
-    const int64_t segs = mode == kWalkSum ? w.plan.K - 1 : w.plan.K;
+    const int64_t segs = mode == kWalkSum && w.dirs == 1 ? w.plan.K - 1 : w.plan.K;
     const unsigned grid = (unsigned)(ceil_div(a.P, kWalkP) * a.H * a.Bsz * w.dirs * segs);
     if (mode == kWalkSum) k_walk32<T, NR, kWalkSum><<<grid, 256, 0, st>>>(w);
-    else if (mode == kWalkStates) k_walk32<T, NR, kWalkStates><<<grid, 256, 0, st>>>(w);
     else k_walk32<T, NR, kWalkY><<<grid, 256, 0, st>>>(w);
     return cudaGetLastError();
 }
