@@ -77,8 +77,6 @@ inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t chunk) {
     return best;
 }
 
-enum WalkMode { kWalkSum = 0, kWalkY = 1 };
-
 // What a walk starts from and leaves, one for each direction.
 struct WalkDir {
     const float* init;   // state before the walk's first token, or null
@@ -94,7 +92,8 @@ struct WalkArgs {
     int dirs;
     float* seg_state;  // [dirs, Bsz, H, K, N, P]: end states of the segments, then (after the carry) their start states
     float* seg_decay;  // [dirs, Bsz, H, K]
-    void* y;           // kWalkY
+    void* y;
+    bool vec;          // runs of four values are whole and aligned
 };
 
 struct BwdArgs {
@@ -108,7 +107,7 @@ struct BwdArgs {
     int splits;           // parts the heads of one group are divided into
 };
 
-cudaError_t launch_walk32(const WalkArgs& w, WalkMode mode, cudaStream_t st);
+cudaError_t launch_walk32(const WalkArgs& w, bool sum, cudaStream_t st);  // sum: the segments' end states; else y
 cudaError_t launch_carry32(const WalkArgs& w, cudaStream_t st);
 cudaError_t launch_bwd32(const BwdArgs& b, cudaStream_t st);
 // out[i] = sum of the splits' part[., i] (n each), of one pair of arrays or (out2 given) of two

@@ -297,7 +297,7 @@ int pass_state(float* to, const float* from, int64_t Bsz, int64_t H, int64_t N, 
 
 // The segments' sums and their carries.
 cudaError_t start_states32(const WalkArgs& w, cudaStream_t st) {
-    const cudaError_t e = launch_walk32(w, kWalkSum, st);
+    const cudaError_t e = launch_walk32(w, true, st);
     return e != cudaSuccess ? e : launch_carry32(w, st);
 }
 
@@ -351,7 +351,7 @@ int ss_la_fwd(const ss_la_fwd_desc* d, void* stream) {
     w.seg_decay = reinterpret_cast<float*>(ws + wl.decay);
     w.y = d->y;
     if (w.plan.K > 1 && start_states32(w, st) != cudaSuccess) return SS_ERR_CUDA;
-    return launch_walk32(w, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+    return launch_walk32(w, false, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 size_t ss_la_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {

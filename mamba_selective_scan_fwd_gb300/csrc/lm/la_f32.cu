@@ -23,24 +23,152 @@ namespace {
 
 constexpr float kSlowTile = -4.0f;  // keeps e^-c below 55: no range is lost
 
-// One block: kWalkP value channels of one head, one segment of tokens.  Lane = two
+__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// Four adjacent values, of which `left` exist; vec: they exist together and are aligned.
+template <typename T> __device__ __forceinline__ float4 fetch4(const T* p, int64_t left, bool vec) {
+    float x[4] = {};
+    if (vec) {
+        if (left > 0) {
+            if constexpr (sizeof(T) == 4) return at4(p);
+            union {
+                uint2 m;
+                T t[4];
+            } u;
+            u.m = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[e] = ldf(&u.t[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = e < left ? ldf(p + e) : 0.0f;
+    }
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// End states of the segments, each walked from zero.  One block: kWalkP value
+// channels of one head, one segment, in tiles of TT tokens:
+//   forward   X <- e^{cl} X + k^T (e^{cl - c} v)
+//   reverse   X <- e^{cl} X + q^T (scale e^c dy), tiles last to first
+// with c the cumulative log decay in the tile and cl its end.  Thread (ty, tx) of
+// 16 x 16: RN rows and four columns of X, read 16 bytes of k and v a token.
+template <typename T, int RN>
+__global__ void __launch_bounds__(256, RN == 8 ? 2 : 3) k_sum32(WalkArgs w) {
+    constexpr int NP = RN * 16, TT = RN == 8 ? 16 : 32;
+    constexpr int EK = TT * NP / 1024 < 1 ? 1 : TT * NP / 1024, EV = TT * kWalkP / 1024;  // runs of 4 values a thread loads
+    __shared__ __align__(16) float s_k[2][TT][NP], s_v[2][TT][kWalkP];
+    __shared__ float2 s_w[2][TT];  // (a token's weight, twice)
+    __shared__ float s_all[2];
+    const Args& a = w.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid & 15, ty = tid >> 4;
+    const int64_t ptiles = (a.P + kWalkP - 1) / kWalkP, segs = w.dirs == 1 ? w.plan.K - 1 : w.plan.K;
+    int64_t id = blockIdx.x;
+    const int64_t p0 = (id % ptiles) * kWalkP;
+    id /= ptiles;
+    const int64_t h = id % a.H;
+    id /= a.H;
+    const int64_t seg = id % segs;
+    id /= segs;
+    const int64_t b = id % a.Bsz;
+    const bool rev = id / a.Bsz != 0;
+    const int64_t hq = h / (a.H / a.G), at = ((rev ? a.Bsz * a.H : 0) + b * a.H + h) * w.plan.K + seg;
+    const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg), len = row_length(a, b);
+    const In &kin = rev ? a.q : a.k, &vin = rev ? a.dy : a.v;
+    const T* kp = static_cast<const T*>(kin.p) + b * kin.batch + hq * a.N;
+    const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P + p0;
+    const int tiles = (int)((t_end - t_begin + TT - 1) / TT), N = (int)a.N, pleft = (int)(a.P - p0);
+
+    float4 rk[EK], rv[EV];
+    float rg = 0.0f;
+    auto fetch = [&](int i) {
+        const int64_t t0 = t_begin + (int64_t)(rev ? tiles - 1 - i : i) * TT;
+        const int nv = (int)max((int64_t)0, min((int64_t)TT, min(len, t_end) - t0));
+        const T *k0 = kp + t0 * kin.token, *v0 = vp + t0 * vin.token;
+#pragma unroll
+        for (int e = 0; e < EK; e++) {
+            const int x = tid + 256 * e, t = x / (NP / 4), n = x % (NP / 4) * 4;
+            rk[e] = fetch4(k0 + t * kin.token + n, t < nv ? N - n : 0, w.vec);
+        }
+#pragma unroll
+        for (int e = 0; e < EV; e++) {
+            const int x = tid + 256 * e, t = x / (kWalkP / 4), c = x % (kWalkP / 4) * 4;
+            rv[e] = fetch4(v0 + t * vin.token + c, t < nv ? pleft - c : 0, w.vec);
+        }
+        if (warp == 0) rg = lane < nv ? log_decay(a, b, t0 + lane, h) : 0.0f;
+    };
+    fetch(0);
+    float2 S[RN / 2][4] = {};  // pairs of rows
+    float total = 0.0f;
+    for (int i = 0; i < tiles; i++) {
+        const int s = i & 1;
+#pragma unroll
+        for (int e = 0; e < EK; e++)
+            if (TT * NP >= 1024 || tid < TT * NP / 4) reinterpret_cast<float4*>(s_k[s])[tid + 256 * e] = rk[e];
+#pragma unroll
+        for (int e = 0; e < EV; e++) reinterpret_cast<float4*>(s_v[s])[tid + 256 * e] = rv[e];
+        if (warp == 0) {
+            const float x[1] = {rg};
+            Two c[1];
+            warp_cumsum<1>(x, c);
+            const Two cl = {__shfl_sync(kFull, c[0].h, 31), __shfl_sync(kFull, c[0].l, 31)};
+            if (lane < TT) s_w[s][lane] = splat2(rev ? a.scale * expf(c[0].h) * (1.0f + c[0].l) : expf(two_diff(cl, c[0])));
+            if (lane == 0) s_all[s] = cl.h + cl.l;
+        }
+        __syncthreads();
+        if (i + 1 < tiles) fetch(i + 1);
+        float2 X[RN / 2][4] = {};
+#pragma unroll 8
+        for (int t = 0; t < TT; t++) {
+            const float4 v = at4(&s_v[s][t][4 * tx]);
+            const float2 wt = s_w[s][t], vs[4] = {splat2(v.x), splat2(v.y), splat2(v.z), splat2(v.w)};
+#pragma unroll
+            for (int r = 0; r < RN / 2; r++) {
+                const float2 k = mul2(wt, *reinterpret_cast<const float2*>(&s_k[s][t][RN * ty + 2 * r]));
+#pragma unroll
+                for (int c = 0; c < 4; c++) X[r][c] = fma2(k, vs[c], X[r][c]);
+            }
+        }
+        // (e^cl - 1: a rounded e^cl would be off the same way at every tile)
+        const float all = s_all[s];
+        const float2 less = splat2(expm1f(all));
+        total += all;
+#pragma unroll
+        for (int r = 0; r < RN / 2; r++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) S[r][c] = add2(fma2(less, S[r][c], S[r][c]), X[r][c]);
+    }
+    float* to = w.seg_state + at * a.N * a.P + p0 + 4 * tx;
+#pragma unroll
+    for (int r = 0; r < RN; r++) {
+        const int n = RN * ty + r;
+        if (n >= N) continue;
+        const float4 x = r & 1 ? make_float4(S[r / 2][0].y, S[r / 2][1].y, S[r / 2][2].y, S[r / 2][3].y)
+                               : make_float4(S[r / 2][0].x, S[r / 2][1].x, S[r / 2][2].x, S[r / 2][3].x);
+        float* row = to + n * a.P;
+        if (w.vec) {
+            if (4 * tx < pleft) *reinterpret_cast<float4*>(row) = x;
+        } else {
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                if (4 * tx + c < pleft) row[c] = y[c];
+        }
+    }
+    if (tid == 0 && p0 == 0) w.seg_decay[at] = total;
+}
+
+// y.  One block: kWalkP value channels of one head, one segment of tokens.  Lane = two
 // value channels 32 apart, warp = NR of the padded N state rows, in pairs.  The
 // rows' k and q are broadcasts from shared memory, which is what bounds it: two
 // channels a lane halve them.
-//   forward   S <- e^g S + k v^T, y = scale q S
-//   reverse   X <- e^g (X + scale q dy^T), tokens last to first (X before the
-//             update is the adjoint of the state after the token)
 // The next TT tokens are loaded into registers while these are computed.
-template <typename T, int NR, int MODE>
+template <typename T, int NR>
 __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
-    constexpr bool Y = MODE == kWalkY;
-    constexpr int NP = NR * 8, TT = Y && NR == 16 ? kWalkT / 2 : kWalkT;
-    constexpr int EK = TT * NP / 256, EV = TT * kWalkP / 256;  // values a thread loads
-    __shared__ __align__(16) float s_k[TT][NP];
-    __shared__ __align__(16) float s_q[Y ? TT : 1][NP];
-    __shared__ float s_v[TT][kWalkP];
-    __shared__ float s_a[TT], s_down[TT], s_up[Y ? TT : 1], s_all;
-    __shared__ float s_y[Y ? 8 : 1][Y ? TT : 1][kWalkP];
+    constexpr int NP = NR * 8, TT = NR == 16 ? kWalkT / 2 : kWalkT;
+    constexpr int EK = TT * NP / 1024 < 1 ? 1 : TT * NP / 1024, EV = TT * kWalkP / 1024 < 1 ? 1 : TT * kWalkP / 1024;  // runs of 4 values a thread loads
+    __shared__ __align__(16) float s_k[TT][NP], s_q[TT][NP], s_v[TT][kWalkP];
+    __shared__ float s_a[TT], s_down[TT], s_up[TT], s_all;
+    __shared__ float s_y[8][TT][kWalkP];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t ptiles = (a.P + kWalkP - 1) / kWalkP;
@@ -49,29 +177,19 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
     id /= ptiles;
     const int64_t h = id % a.H;
     id /= a.H;
-    const int64_t segs = !Y && w.dirs == 1 ? w.plan.K - 1 : w.plan.K, seg = id % segs;
-    id /= segs;
-    const int64_t b = id % a.Bsz;
-    const bool rev = !Y && id / a.Bsz != 0;
-    const int64_t hq = h / (a.H / a.G), bh = b * a.H + h, at = ((rev ? a.Bsz * a.H : 0) + bh) * w.plan.K + seg;
+    const int64_t seg = id % w.plan.K, b = id / w.plan.K;
+    const int64_t hq = h / (a.H / a.G), bh = b * a.H + h;
     const int64_t t_begin = seg * w.plan.seg, t_end = min(a.L, t_begin + w.plan.seg);
     const int64_t len = row_length(a, b);
-    const int n0 = warp * NR;
+    const int n0 = warp * NR, N = (int)a.N, pleft = (int)(a.P - p0);
     const int64_t NPel = a.N * a.P;
-    const In& kin = rev ? a.q : a.k;
-    const In& vin = rev ? a.dy : a.v;
-    const T* kp = static_cast<const T*>(kin.p) + b * kin.batch + hq * a.N;
+    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hq * a.N;
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
-    const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P;
-    const float kscale = rev ? a.scale : 1.0f;
-    const WalkDir& dir = w.dir[rev];
+    const T* vp = static_cast<const T*>(a.v.p) + b * a.v.batch + h * a.P + p0;
+    const WalkDir& dir = w.dir[0];
 
     float2 S[2][NR / 2];  // [channel][pair of rows]
-    const float* init = nullptr;
-    if (Y) {
-        if (w.plan.K > 1) init = w.seg_state + at * NPel;
-        else if (dir.init) init = dir.init + bh * NPel;
-    }
+    const float* init = w.plan.K > 1 ? w.seg_state + (bh * w.plan.K + seg) * NPel : (dir.init ? dir.init + bh * NPel : nullptr);
 #pragma unroll
     for (int c = 0; c < 2; c++) {
         const int64_t p = p0 + lane + 32 * c;
@@ -79,7 +197,118 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
 #pragma unroll
         for (int r = 0; r < NR / 2; r++) S[c][r] = make_float2(from(n0 + 2 * r), from(n0 + 2 * r + 1));
     }
-    auto put = [&](float* dst) {
+
+    const int64_t tiles = (t_end - t_begin + TT - 1) / TT;
+    auto valid = [&](int64_t t0) { return (int)max((int64_t)0, min((int64_t)TT, min(len, t_end) - t0)); };  // tokens that count
+    float4 rk[EK], rq[EK], rv[EV];
+    float rg = 0.0f;
+    auto fetch = [&](int64_t i) {
+        const int64_t t0 = t_begin + i * TT;
+        const int nv = valid(t0);
+        const T *k0 = kp + t0 * a.k.token, *q0 = qp + t0 * a.q.token, *v0 = vp + t0 * a.v.token;
+#pragma unroll
+        for (int e = 0; e < EK; e++) {
+            const int x = tid + 256 * e, t = x / (NP / 4), n = x % (NP / 4) * 4, left = t < nv ? N - n : 0;
+            rk[e] = fetch4(k0 + t * a.k.token + n, left, w.vec);
+            rq[e] = fetch4(q0 + t * a.q.token + n, left, w.vec);
+        }
+#pragma unroll
+        for (int e = 0; e < EV; e++) {
+            const int x = tid + 256 * e, t = x / (kWalkP / 4), c = x % (kWalkP / 4) * 4;
+            rv[e] = fetch4(v0 + t * a.v.token + c, t < nv ? pleft - c : 0, w.vec);
+        }
+        if (tid < TT) rg = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
+    };
+    fetch(0);
+    for (int64_t i = 0; i < tiles; i++) {
+        const int64_t t0 = t_begin + i * TT;
+        const int nv = valid(t0);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EK; e++)
+            if (TT * NP >= 1024 || tid < TT * NP / 4) {
+                reinterpret_cast<float4*>(s_k)[tid + 256 * e] = rk[e];
+                reinterpret_cast<float4*>(s_q)[tid + 256 * e] = rq[e];
+            }
+#pragma unroll
+        for (int e = 0; e < EV; e++)
+            if (TT * kWalkP >= 1024 || tid < TT * kWalkP / 4) reinterpret_cast<float4*>(s_v)[tid + 256 * e] = rv[e];
+        if (warp == 0) {  // the tile's decays
+            const float x[1] = {lane < TT ? rg : 0.0f};
+            Two c[1];
+            warp_cumsum<1>(x, c);
+            if (lane == 31) s_all = c[0].h + c[0].l;
+            if (lane < TT) {
+                s_a[lane] = expm1f(x[0]);
+                s_down[lane] = expf(-c[0].h) * (1.0f - c[0].l);
+                s_up[lane] = expf(c[0].h) * (1.0f + c[0].l);
+            }
+        }
+        __syncthreads();
+        if (i + 1 < tiles) fetch(i + 1);
+        const float all = s_all;
+        const bool slow = all >= kSlowTile;  // (NaN: no)
+        // SLOW: S = S0 + A in units of e^c: S0 stays, A takes what the tile adds
+        auto tokens = [&](auto which) {
+            constexpr bool SLOW = decltype(which)::value;
+            float2 A[2][NR / 2] = {};
+#pragma unroll 2
+            for (int t = 0; t < nv; t++) {
+                const float d = SLOW ? s_down[t] : 1.0f;
+                const float2 av = splat2(s_a[t]), v[2] = {splat2(s_v[t][lane] * d), splat2(s_v[t][lane + 32] * d)};
+                float2 acc[2][2] = {};
+#pragma unroll
+                for (int r = 0; r < NR / 2; r += 2) {
+                    const float4 kk = at4(&s_k[t][n0 + 2 * r]), qq = at4(&s_q[t][n0 + 2 * r]);
+                    const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
+                    const float2 qr[2] = {make_float2(qq.x, qq.y), make_float2(qq.z, qq.w)};
+#pragma unroll
+                    for (int c = 0; c < 2; c++)
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            float2 &x = S[c][r + u], &y = A[c][r + u];
+                            if (SLOW) y = fma2(kr[u], v[c], y);
+                            else x = fma2(kr[u], v[c], fma2(av, x, x));
+                            acc[c][u] = fma2(qr[u], SLOW ? add2(x, y) : x, acc[c][u]);
+                        }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const float2 s = add2(acc[c][0], acc[c][1]);
+                    s_y[warp][t][lane + 32 * c] = s.x + s.y;
+                }
+            }
+            if (SLOW) {
+                const float2 less = splat2(expm1f(all));
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+#pragma unroll
+                    for (int r = 0; r < NR / 2; r++) {
+                        const float2 x = add2(S[c][r], A[c][r]);
+                        S[c][r] = fma2(less, x, x);
+                    }
+            }
+        };
+        if (slow) tokens(std::true_type{});
+        else tokens(std::false_type{});
+        __syncthreads();
+        T* yp = static_cast<T*>(w.y) + ((b * a.L + t0) * a.H + h) * a.P + p0;
+        const int nt = (int)min((int64_t)TT, t_end - t0);
+#pragma unroll
+        for (int u = 0; u < TT * kWalkP / 256; u++) {
+            const int e = tid + 256 * u, t = e / kWalkP, c = e % kWalkP;
+            if (t < nt && c < pleft) {
+                float y = 0.0f;
+                if (t < nv) {
+#pragma unroll
+                    for (int o = 0; o < 8; o++) y += s_y[o][t][c];
+                }
+                st(yp + t * a.H * a.P + c, a.scale * (slow ? s_up[t] * y : y));
+            }
+        }
+    }
+    if (dir.last && seg == w.plan.K - 1) {
+        float* dst = dir.last + bh * NPel;
 #pragma unroll
         for (int c = 0; c < 2; c++) {
             const int64_t p = p0 + lane + 32 * c;
@@ -89,172 +318,6 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
                 if (n0 + 2 * r + 1 < a.N && p < a.P) dst[(n0 + 2 * r + 1) * a.P + p] = S[c][r].y;
             }
         }
-    };
-
-    const int64_t tiles = (t_end - t_begin + TT - 1) / TT;
-    auto start_of = [&](int64_t i) { return t_begin + (rev ? tiles - 1 - i : i) * TT; };
-    auto valid = [&](int64_t t0) { return (int)max((int64_t)0, min((int64_t)TT, min(len, t_end) - t0)); };  // tokens that count
-    float rk[EK], rq[Y ? EK : 1], rv[EV], rg = 0.0f;
-    auto fetch = [&](int64_t i) {
-        const int64_t t0 = start_of(i);
-        const int nv = valid(t0);
-#pragma unroll
-        for (int e = 0; e < EK; e++) {
-            const int t = (tid + 256 * e) / NP, n = (tid + 256 * e) % NP;
-            rk[e] = (t < nv && n < a.N) ? kscale * ldf(kp + (t0 + t) * kin.token + n) : 0.0f;
-            if (Y) rq[e] = (t < nv && n < a.N) ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < EV; e++) {
-            const int t = (tid + 256 * e) / kWalkP, c = (tid + 256 * e) % kWalkP;
-            rv[e] = (t < nv && p0 + c < a.P) ? ldf(vp + (t0 + t) * vin.token + p0 + c) : 0.0f;
-        }
-        if (tid < TT) rg = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
-    };
-    fetch(0);
-    float total = 0.0f;  // the segment's log decay
-    for (int64_t i = 0; i < tiles; i++) {
-        const int64_t t0 = start_of(i);
-        const int nv = valid(t0);
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < EK; e++) {
-            (&s_k[0][0])[tid + 256 * e] = rk[e];
-            if (Y) (&s_q[0][0])[tid + 256 * e] = rq[e];
-        }
-#pragma unroll
-        for (int e = 0; e < EV; e++) (&s_v[0][0])[tid + 256 * e] = rv[e];
-        if (warp == 0) {  // the tile's decays in the walk's direction
-            const int t = rev ? TT - 1 - lane : lane;
-            const float g[1] = {__shfl_sync(kFull, rg, t & (TT - 1))};
-            const float x[1] = {lane < TT ? g[0] : 0.0f};
-            Two c[1];
-            warp_cumsum<1>(x, c);
-            if (lane == 31) s_all = c[0].h + c[0].l;
-            const Two before = {__shfl_up_sync(kFull, c[0].h, 1), __shfl_up_sync(kFull, c[0].l, 1)};
-            if (rev) c[0] = lane ? before : Two{0.0f, 0.0f};
-            if (lane < TT) {
-                s_a[t] = expm1f(x[0]);
-                s_down[t] = expf(-c[0].h) * (1.0f - c[0].l);
-                if (Y) s_up[t] = expf(c[0].h) * (1.0f + c[0].l);
-            }
-        }
-        __syncthreads();
-        if (i + 1 < tiles) fetch(i + 1);
-        const float all = s_all;
-        total += all;
-        // the direction as a constant: a test in the innermost loop doubled its instructions
-        auto tokens = [&](auto direction) {
-            constexpr bool R = decltype(direction)::value;
-#pragma unroll 2
-            for (int j = 0; j < nv; j++) {
-                const int t = R ? nv - 1 - j : j;
-                const float2 av = splat2(s_a[t]), v[2] = {splat2(s_v[t][lane]), splat2(s_v[t][lane + 32])};
-                float2 acc[2][2] = {{splat2(0.0f), splat2(0.0f)}, {splat2(0.0f), splat2(0.0f)}};
-#pragma unroll
-                for (int r = 0; r < NR / 2; r += 2) {
-                    const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
-                    const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
-                    float2 qr[2];
-                    if (Y) {
-                        const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
-                        qr[0] = make_float2(qq.x, qq.y);
-                        qr[1] = make_float2(qq.z, qq.w);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; c++)
-#pragma unroll
-                        for (int u = 0; u < 2; u++) {
-                            float2& x = S[c][r + u];
-                            if (R) {
-                                x = fma2(kr[u], v[c], x);
-                                x = fma2(av, x, x);
-                            } else {
-                                x = fma2(kr[u], v[c], fma2(av, x, x));
-                            }
-                            if (Y) acc[c][u] = fma2(qr[u], x, acc[c][u]);
-                        }
-                }
-                if (Y)
-#pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        const float2 s = add2(acc[c][0], acc[c][1]);
-                        s_y[warp][t][lane + 32 * c] = s.x + s.y;
-                    }
-            }
-        };
-        const bool slow = all >= kSlowTile;  // (NaN: no)
-        if (slow) {
-            // S = S0 + L in units of 2^c: S0 stays, L takes what the tile adds
-            float2 A[2][NR / 2];
-#pragma unroll
-            for (int c = 0; c < 2; c++)
-#pragma unroll
-                for (int r = 0; r < NR / 2; r++) A[c][r] = splat2(0.0f);
-#pragma unroll 2
-            for (int j = 0; j < nv; j++) {
-                const int t = !Y && rev ? nv - 1 - j : j;
-                const float down = s_down[t];
-                const float2 v[2] = {splat2(s_v[t][lane] * down), splat2(s_v[t][lane + 32] * down)};
-                float2 acc[2][2] = {{splat2(0.0f), splat2(0.0f)}, {splat2(0.0f), splat2(0.0f)}};
-#pragma unroll
-                for (int r = 0; r < NR / 2; r += 2) {
-                    const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][n0 + 2 * r]);
-                    const float2 kr[2] = {make_float2(kk.x, kk.y), make_float2(kk.z, kk.w)};
-#pragma unroll
-                    for (int c = 0; c < 2; c++)
-#pragma unroll
-                        for (int u = 0; u < 2; u++) A[c][r + u] = fma2(kr[u], v[c], A[c][r + u]);
-                    if (Y) {
-                        const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][n0 + 2 * r]);
-                        const float2 qr[2] = {make_float2(qq.x, qq.y), make_float2(qq.z, qq.w)};
-#pragma unroll
-                        for (int c = 0; c < 2; c++)
-#pragma unroll
-                            for (int u = 0; u < 2; u++) acc[c][u] = fma2(qr[u], add2(S[c][r + u], A[c][r + u]), acc[c][u]);
-                    }
-                }
-                if (Y)
-#pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        const float2 s = add2(acc[c][0], acc[c][1]);
-                        s_y[warp][t][lane + 32 * c] = s.x + s.y;
-                    }
-            }
-            const float2 keep = splat2(expm1f(all));
-#pragma unroll
-            for (int c = 0; c < 2; c++)
-#pragma unroll
-                for (int r = 0; r < NR / 2; r++) {
-                    const float2 x = add2(S[c][r], A[c][r]);
-                    S[c][r] = fma2(keep, x, x);
-                }
-        } else if (!Y && rev) {
-            tokens(std::true_type{});
-        } else {
-            tokens(std::false_type{});
-        }
-        if (Y) {
-            __syncthreads();
-            T* yp = static_cast<T*>(w.y) + (b * a.L * a.H + h) * a.P;
-            for (int e = tid; e < TT * kWalkP; e += 256) {
-                const int t = e / kWalkP, c = e % kWalkP;
-                if (t0 + t < t_end && p0 + c < a.P) {
-                    float y = 0.0f;
-                    if (t < nv) {
-#pragma unroll
-                        for (int u = 0; u < 8; u++) y += s_y[u][t][c];
-                    }
-                    st(yp + (t0 + t) * a.H * a.P + p0 + c, a.scale * (slow ? s_up[t] * y : y));
-                }
-            }
-        }
-    }
-    if (!Y) {
-        put(w.seg_state + at * NPel);
-        if (tid == 0 && p0 == 0) w.seg_decay[at] = total;
-    } else if (dir.last && seg == w.plan.K - 1) {
-        put(dir.last + bh * NPel);
     }
 }
 
@@ -306,7 +369,6 @@ template <int NB> struct Smem32 {
     float a[kChunk32], b[kChunk32], col[8][kChunk32], red[8];
 };
 
-__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 // acc (4 adjacent values) += x z
 __device__ __forceinline__ void fma4(float2 (&acc)[2], float x, float4 z) {
     acc[0] = fma2(splat2(x), make_float2(z.x, z.y), acc[0]);
@@ -345,6 +407,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
     const int64_t len = row_length(a, b);
     const int nt = (int)min((int64_t)C, a.L - t0);
     const int nv = (int)max((int64_t)0, min((int64_t)nt, len - t0));
+    const int nc = (nv + 3) & ~3;  // sums over tokens end here: what follows is zero
     const int64_t rep = a.H / a.G;
     const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
 
@@ -457,7 +520,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             {  // dv, and b from its inter-chunk part: rows 4 ty + r, columns 4 tx + c
                 float2 in[4][2] = {}, ac[4][2] = {};
 #pragma unroll 4
-                for (int i = 0; i < C; i++) {
+                for (int i = 0; i < nc; i++) {
                     const float4 x = at4(&s.S[i][4 * ty]), z = at4(&s.dy[i][4 * tx]);
                     const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -496,7 +559,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             }
             {  // dq, and a from its inter-chunk part: rows 4 ty + r, columns tx + 16 n
                 float2 ac[4][NB] = {}, in[4][NB] = {};
-                for (int j = 0; j < C; j += 4) {
+                for (int j = 0; j < nc; j += 4) {
                     float4 x[4];
 #pragma unroll
                     for (int r = 0; r < 4; r++) x[r] = at4(&s.E[4 * ty + r][j]);
@@ -537,7 +600,7 @@ __global__ void __launch_bounds__(256) k_bwd32(BwdArgs w) {
             }
             {  // dk, like dq
 #pragma unroll 4
-                for (int i = 0; i < C; i++) {
+                for (int i = 0; i < nc; i++) {
                     const float4 x = at4(&s.E[i][4 * ty]);
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
@@ -663,19 +726,19 @@ __global__ void __launch_bounds__(256) k_sum_rows(const float* x, float* part, i
     }
 }
 
-template <typename T, int NR> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+template <typename T, int NR> cudaError_t walk_mode(const WalkArgs& w, bool sum, cudaStream_t st) {
     const Args& a = w.a;
-    const int64_t segs = mode == kWalkSum && w.dirs == 1 ? w.plan.K - 1 : w.plan.K;
+    const int64_t segs = sum && w.dirs == 1 ? w.plan.K - 1 : w.plan.K;
     const unsigned grid = (unsigned)(ceil_div(a.P, kWalkP) * a.H * a.Bsz * w.dirs * segs);
-    if (mode == kWalkSum) k_walk32<T, NR, kWalkSum><<<grid, 256, 0, st>>>(w);
-    else k_walk32<T, NR, kWalkY><<<grid, 256, 0, st>>>(w);
+    if (sum) k_sum32<T, NR / 2><<<grid, 256, 0, st>>>(w);
+    else k_walk32<T, NR><<<grid, 256, 0, st>>>(w);
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t walk_io(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
-    if (w.a.N <= 32) return walk_mode<T, 4>(w, mode, st);
-    if (w.a.N <= 64) return walk_mode<T, 8>(w, mode, st);
-    return walk_mode<T, 16>(w, mode, st);
+template <typename T> cudaError_t walk_io(const WalkArgs& w, bool sum, cudaStream_t st) {
+    if (w.a.N <= 32) return walk_mode<T, 4>(w, sum, st);
+    if (w.a.N <= 64) return walk_mode<T, 8>(w, sum, st);
+    return walk_mode<T, 16>(w, sum, st);
 }
 
 template <typename T, int NB> cudaError_t bwd_n(const BwdArgs& b, cudaStream_t st) {
@@ -694,10 +757,21 @@ template <typename T> cudaError_t bwd_io(const BwdArgs& b, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_walk32(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
-    if (w.a.dtype == 0) return walk_io<float>(w, mode, st);
-    if (w.a.dtype == 1) return walk_io<__half>(w, mode, st);
-    return walk_io<__nv_bfloat16>(w, mode, st);
+// Whether every run of four values of q, k, v, dy and the states is whole and aligned.
+static bool fours(const WalkArgs& w) {
+    const Args& a = w.a;
+    const uintptr_t bytes = a.dtype == 0 ? 16 : 8;
+    for (const In* x : {&a.q, &a.k, &a.v, &a.dy})
+        if (reinterpret_cast<uintptr_t>(x->p) % bytes != 0 || x->token % 4 != 0 || x->batch % 4 != 0) return false;
+    return a.N % 4 == 0 && a.P % 4 == 0;
+}
+
+cudaError_t launch_walk32(const WalkArgs& args, bool sum, cudaStream_t st) {
+    WalkArgs w = args;
+    w.vec = fours(w);
+    if (w.a.dtype == 0) return walk_io<float>(w, sum, st);
+    if (w.a.dtype == 1) return walk_io<__half>(w, sum, st);
+    return walk_io<__nv_bfloat16>(w, sum, st);
 }
 
 cudaError_t launch_carry32(const WalkArgs& w, cudaStream_t st) {
