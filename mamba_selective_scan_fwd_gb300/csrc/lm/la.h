@@ -53,25 +53,28 @@ constexpr int kWalkT = 16;    // tokens staged at a time (at most)
 constexpr int kChunk32 = 64;  // tokens per chunk of the FP32 backward
 
 // The token walk: every unit (direction, batch row, head, tile of value
-// channels) is cut into K segments of seg tokens (a multiple of a chunk; the
-// backward's are one chunk each: their start states are what it reads).
+// channels) is cut into K segments of seg tokens (the backward's are one chunk
+// each: their start states are what it reads).
 struct WalkPlan {
     int64_t K, seg;
 };
-// Three blocks run on an SM.  The K with the fewest rounds of blocks times
-// tokens a block; cutting costs a sum pass (0.6 of a walk) and two launches
-// (about 60 tokens' time).
-inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t chunk) {
-    const int64_t chunks = ceil_div(L, chunk), slots = 3 * kSms;
-    WalkPlan best = {1, chunks * chunk};
-    double least = (double)ceil_div(units, slots) * L;
-    for (int64_t K = 2; K <= 64 && K <= chunks; K++) {
-        const int64_t per = ceil_div(chunks, K);
-        if (ceil_div(chunks, per) != K) continue;
-        const double cost = (ceil_div(units * K, slots) + 0.6 * ceil_div(units * (K - 1), slots)) * (double)(per * chunk) + 60;
+// The K with the fewest tokens an SM walks: its blocks share it (fewer than the two or
+// three that fit take as long as those), and a block's start and end are as long as 32
+// tokens.  Cutting costs a sum pass (0.4 of a walk), two launches (as long as 160
+// tokens) and the traffic of the segments' states (a token for 12 of them).
+inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t N) {
+    const int64_t tiles = ceil_div(L, kWalkT);
+    const int64_t fit = N > 64 ? 2 : 3;
+    auto load = [&](int64_t blocks) { const int64_t n = ceil_div(blocks, kSms); return n < fit ? fit : n; };
+    WalkPlan best = {1, tiles * kWalkT};
+    double least = (double)load(units) * (L + 32);
+    for (int64_t K = 2; K <= 64 && K <= tiles; K++) {
+        const int64_t per = ceil_div(tiles, K);
+        if (ceil_div(tiles, per) != K) continue;
+        const double cost = (load(units * K) + 0.4 * load(units * (K - 1))) * (double)(per * kWalkT + 32) + 160 + units * K / 12;
         if (cost < 0.95 * least) {
             least = cost;
-            best = {K, per * chunk};
+            best = {K, per * kWalkT};
         }
     }
     return best;

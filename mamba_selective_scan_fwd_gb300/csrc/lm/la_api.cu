@@ -45,7 +45,7 @@ struct Walk32 {
 };
 Walk32 walk32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dirs) {
     Walk32 w;
-    if (dirs == 1) w.plan = walk_plan(Bsz * H * ceil_div(P, kWalkP), L, kChunk32);
+    if (dirs == 1) w.plan = walk_plan(Bsz * H * ceil_div(P, kWalkP), L, N);
     else w.plan = {ceil_div(L, kChunk32), kChunk32};
     w.state = w.decay = 0;
     if (dirs == 2 || w.plan.K > 1) {
