@@ -297,7 +297,7 @@ def _workspace(nbytes, device, workspace):
     import torch
 
     if workspace is None and nbytes > 0:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return workspace, size
 

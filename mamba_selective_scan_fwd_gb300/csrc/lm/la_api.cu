@@ -208,13 +208,17 @@ BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
 }
 
 // What follows the chunk kernels of both paths: the parts' sums.
-int bwd_sums(const ss_la_bwd_desc& d, int splits, const float* dq_part, const float* dk_part, const float* dg, float* rows,
+int bwd_sums(const ss_la_bwd_desc& d, int splits, const float* dq_part, const float* dk_part, const float* dg, int dg_parts, float* rows,
              cudaStream_t st) {
     if (splits > 1) {
         const int64_t n = d.Bsz * d.L * d.G * d.N;
         if (launch_sum_parts(dq_part, d.dq, dk_part, d.dk, splits, n, d.dtype, st) != cudaSuccess) return SS_ERR_CUDA;
     }
-    if (d.g_per_head && launch_sum_rows(dg, rows, d.dg, d.Bsz * d.L, d.H, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (d.g_per_head) {
+        if (launch_sum_rows(dg, rows, d.dg, dg_parts * d.Bsz * d.L, d.H, st) != cudaSuccess) return SS_ERR_CUDA;
+    } else if (dg_parts > 1) {
+        if (launch_sum_parts(dg, d.dg, nullptr, nullptr, dg_parts, d.Bsz * d.L * d.H, SS_F32, st) != cudaSuccess) return SS_ERR_CUDA;
+    }
     return SS_OK;
 }
 
@@ -279,9 +283,7 @@ int tc_backward(const Args& a, const ss_la_bwd_desc& d, cudaStream_t st, bool* r
     b.dk_part = f32(bl.dk);
     b.status = w.status;
     if (launch_tc_bwd(b, st) != cudaSuccess) return SS_ERR_CUDA;
-    if (bl.dg_parts > 1 && launch_sum_parts(b.dg, a.g_per_head ? b.dg : d.dg, nullptr, nullptr, bl.dg_parts, a.Bsz * a.L * a.H, SS_F32, st) != cudaSuccess)
-        return SS_ERR_CUDA;
-    return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
+    return bwd_sums(d, b.splits, b.dq_part, b.dk_part, b.dg, bl.dg_parts, f32(bl.rows), st);
 }
 
 bool empty(int64_t Bsz, int64_t L) { return Bsz == 0 || L == 0; }
@@ -424,7 +426,7 @@ int ss_la_bwd(const ss_la_bwd_desc* d, void* stream) {
     b.dk_part = f32(bl.dk);
     b.splits = bl.splits;
     if (launch_bwd32(b, st) != cudaSuccess) return SS_ERR_CUDA;
-    return bwd_sums(*d, b.splits, b.dq_part, b.dk_part, b.dg, f32(bl.rows), st);
+    return bwd_sums(*d, b.splits, b.dq_part, b.dk_part, b.dg, 1, f32(bl.rows), st);
 }
 
 int ss_la_step(const ss_la_step_desc* d, void* stream) {

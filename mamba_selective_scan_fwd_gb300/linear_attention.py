@@ -111,6 +111,13 @@ def _in_stream(stream, t, fn, *args):
         return fn(*args)
 
 
+def _new(a, b, c, d, dtype, device):
+    """An uninitialised contiguous tensor [a, b, c, d] (torch.empty takes twice as long)."""
+    import torch
+
+    return torch.empty_strided((a, b, c, d), (b * c * d, c * d, d, 1), dtype=dtype, device=device)
+
+
 def _heads(H, G):
     if G < 1 or H % G != 0:
         raise ValueError(f"{H} heads of v cannot share {G} heads of q and k evenly")
@@ -145,11 +152,11 @@ def ss_la_fwd(q, k, v, g, scale=1.0, h0=None, lengths=None, y=None, last_state=N
     h0_p = _optional(h0, "h0", state, f32, dev)
     _gpu(v)
     if y is None:
-        y = torch.empty((Bsz, L, H, P), dtype=io, device=dev)
+        y = _new(Bsz, L, H, P, io, dev)
     else:
         _whole(y, "y", (Bsz, L, H, P), io, dev)
     if last_state is None and return_last_state:
-        last_state = torch.empty(state, dtype=f32, device=dev)
+        last_state = _new(Bsz, H, N, P, f32, dev)
     last = _optional(last_state, "last_state", state, f32, dev)
     dt = dtype_id(v)
     need = la_fwd_workspace_bytes(Bsz, L, H, G, N, P, dt)
@@ -184,16 +191,20 @@ def ss_la_bwd(q, k, v, g, dy, scale=1.0, h0=None, dlast_state=None, lengths=None
     h0_p = _optional(h0, "h0", state, f32, dev)
     dlast_p = _optional(dlast_state, "dlast_state", state, f32, dev)
     _gpu(v)
-    shapes = {"dq": ((Bsz, L, G, N), io), "dk": ((Bsz, L, G, N), io), "dv": ((Bsz, L, H, P), io),
-              "dg": (tuple(g.shape), f32), "dh0": (state, f32)}
-    out = dict(out or {})
-    for name, (shape, dtype) in shapes.items():
-        if name == "dh0" and h0 is None:
-            out[name] = None
-        elif out.get(name) is None:
-            out[name] = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _whole(out[name], name, shape, dtype, dev)
+    if out:
+        shapes = {"dq": ((Bsz, L, G, N), io), "dk": ((Bsz, L, G, N), io), "dv": ((Bsz, L, H, P), io),
+                  "dg": (tuple(g.shape), f32), "dh0": (state, f32)}
+        out = dict(out)
+        for name, (shape, dtype) in shapes.items():
+            if name == "dh0" and h0 is None:
+                out[name] = None
+            elif out.get(name) is None:
+                out[name] = torch.empty(shape, dtype=dtype, device=dev)
+            else:
+                _whole(out[name], name, shape, dtype, dev)
+    else:
+        out = {"dq": _new(Bsz, L, G, N, io, dev), "dk": _new(Bsz, L, G, N, io, dev), "dv": _new(Bsz, L, H, P, io, dev),
+               "dg": torch.empty_like(g), "dh0": None if h0 is None else torch.empty_like(h0)}
     dt = dtype_id(v)
     need = la_bwd_workspace_bytes(Bsz, L, H, G, N, P, dt)
     workspace, wsb = _workspace(need, dev, workspace)
@@ -230,7 +241,7 @@ def ss_la_step(q, k, v, g, state, scale=1.0, slots=None, y=None, stream=None):
     slots_p = _optional(slots, "slots", (Bsz,), torch.int32, dev)
     _gpu(v)
     if y is None:
-        y = torch.empty((Bsz, H, P), dtype=io, device=dev)
+        y = torch.empty_strided((Bsz, H, P), (H * P, P, 1), dtype=io, device=dev)
     else:
         _whole(y, "y", (Bsz, H, P), io, dev)
     d = LaStepDesc(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(), slots_p, y.data_ptr(),
