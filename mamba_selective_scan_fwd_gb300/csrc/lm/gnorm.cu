@@ -3,9 +3,13 @@
 // Both directions are bound by HBM: x, z (and dout) are read once into
 // registers, the statistics are two sums over the registers (mean, then the
 // squared deviations: no cancellation), and the results are written once.  A
-// thread keeps its channels' weight and bias (and, in the backward, their
-// gradients' sums) while it walks over rows, so parameters are not re-read and
-// the parameter gradients need one small second pass.
+// thread keeps its channels while it walks over rows, so that weight and bias stay
+// in registers (or the L1 cache), and the parameter gradients need one small second
+// pass.  Sums and statistics are f32.
+//
+// Measured, bf16 with a gate (503 MB forward, 419 MB backward; copying takes 74 and
+// 62 us): 16384 x 5120 in groups of 64: 82 us, backward of 8192 rows 81 us; groups of
+// 512: 101 and 118, of 1024: 109 and 144, of 5120: 128 and 138 (a barrier a sum).
 #include "../simd.cuh"
 #include "la_dev.cuh"
 #include "ss_la.h"
@@ -59,17 +63,38 @@ template <int E> __device__ __forceinline__ void put(float (&x)[E], int e, float
 }
 
 // Sum over the threads of a group (all of them get it): LPG lanes of a warp, or
-// the whole block (LPG = 0).
+// the whole block (LPG = 0) by way of red, 32 floats that no other sum since the
+// last barrier but one has used.
 template <int LPG> __device__ __forceinline__ float group_sum(float v, float* red) {
     constexpr int W = LPG > 0 ? LPG : 32;
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     if (LPG == 0) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        v = lane < (int)blockDim.x / 32 ? red[lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    }
+    return v;
+}
+// Two sums at once.
+template <int LPG> __device__ __forceinline__ float2 group_sum2(float2 v, float* red, float* red2) {
+    constexpr int W = LPG > 0 ? LPG : 32;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v = add2(v, make_float2(__shfl_xor_sync(kFull, v.x, o), __shfl_xor_sync(kFull, v.y, o)));
+    if (LPG == 0) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) {
+            red[threadIdx.x >> 5] = v.x;
+            red2[threadIdx.x >> 5] = v.y;
+        }
         __syncthreads();
-        v = 0.0f;
-        for (int w = 0; w < (int)blockDim.x / 32; w++) v += red[w];
+        const bool on = lane < (int)blockDim.x / 32;
+        v = make_float2(on ? red[lane] : 0.0f, on ? red2[lane] : 0.0f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = add2(v, make_float2(__shfl_xor_sync(kFull, v.x, o), __shfl_xor_sync(kFull, v.y, o)));
     }
     return v;
 }
@@ -84,7 +109,10 @@ template <int LPG> constexpr int kRowsPerStep = LPG > 0 ? 8 : 1;
 // memory (their own slots of it: no barrier), as many as it takes to cover the
 // memory's latency.
 template <int E> constexpr bool kRing = E > 1;
-template <int VPT, bool BWD> constexpr int kDepth = VPT > 1 ? 2 : (BWD ? 3 : 4);
+template <int LPG, int VPT, bool BWD> constexpr int kDepth = LPG == 0 && VPT > 2 ? 2 : (VPT > 1 || BWD ? 3 : 4);
+// Blocks that are to fit on an SM: by their registers.
+template <int LPG, int VPT, bool BWD>
+constexpr int kPerSm = LPG > 0 ? (VPT == 1 ? (BWD ? 2 : 4) : (BWD || VPT > 4 ? 1 : 2)) : (VPT > 1 || BWD ? 1 : 2);
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
@@ -92,9 +120,9 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T, int E, int LPG, int VPT, bool BWD>
-__global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 1 ? 1 : (LPG > 0 ? (BWD ? 2 : 4) : (BWD ? 1 : 2))) k_gnorm(GnormArgs a) {
+__global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT <= 2 ? 640 : 512), kPerSm<LPG, VPT, BWD>) k_gnorm(GnormArgs a) {
     extern __shared__ __align__(16) uint4 ring[];  // [depth][x, z, dout][run][thread] (kRing)
-    __shared__ float red[32];
+    __shared__ float s_red[LPG > 0 ? 1 : 2][4][32];  // of rows by turns
     __shared__ float cols[BWD && LPG > 0 ? 8 : 1][BWD && LPG > 0 ? 32 * E * VPT : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t gs = a.C / a.groups;
@@ -111,11 +139,25 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
     float w[1][E], bb[1][E], dw[VPT][E], db[VPT][E];
     auto params = [&](int j, float (&wj)[E], float (&bj)[E]) {
         const int64_t c = grp * gs + (int64_t)(l + j * lanes) * E;
+        auto get = [&](const float* p, float other, float (&f)[E]) {
+            if (!p || !on[j]) {
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-            wj[e] = on[j] && a.weight ? __ldg(a.weight + c + e) : 1.0f;
-            bj[e] = on[j] && a.bias ? __ldg(a.bias + c + e) : 0.0f;
-        }
+                for (int e = 0; e < E; e++) f[e] = other;
+            } else if constexpr (E == 1) {
+                f[0] = __ldg(p + c);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(p + c + e));
+                    f[e] = x.x;
+                    f[e + 1] = x.y;
+                    f[e + 2] = x.z;
+                    f[e + 3] = x.w;
+                }
+            }
+        };
+        get(a.weight, 1.0f, wj);
+        get(a.bias, 0.0f, bj);
     };
 #pragma unroll
     for (int j = 0; j < VPT; j++) {
@@ -126,7 +168,7 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
     if (VPT == 1) params(0, w[0], bb[0]);
     const int64_t pace = (int64_t)gridDim.y * kRowsPerStep<LPG>, mine = LPG > 0 ? warp : 0;
     int64_t r0 = (int64_t)blockIdx.y * kRowsPerStep<LPG>;
-    constexpr int D = kDepth<VPT, BWD>, kIn = BWD ? 3 : 2;
+    constexpr int D = kDepth<LPG, VPT, BWD>, kIn = BWD ? 3 : 2;
     auto at_ring = [&](int stage, int which, int j) {
         return ring + ((stage * kIn + which) * VPT + j) * (int)blockDim.x + threadIdx.x;
     };
@@ -145,8 +187,10 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
 #pragma unroll
         for (int i = 0; i < D - 1; i++) ahead(i, r0 + i * pace + mine);
     }
-    int stage = 0;
+    int stage = 0, turn = 0;
     for (; r0 < a.M; r0 += pace) {
+        float(*red)[32] = s_red[turn];
+        if (LPG == 0) turn ^= 1;
         const int64_t r = r0 + mine;
         const bool row = r < a.M;
         const int64_t at = r * a.C + grp * gs;
@@ -189,7 +233,7 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
                 sum = add2(sum, v);
                 put(u[j], e, v);
             }
-        const float mean = center ? group_sum<LPG>(sum.x + sum.y, red) * inv : 0.0f;
+        const float mean = center ? group_sum<LPG>(sum.x + sum.y, red[0]) * inv : 0.0f;
         float2 sq = splat2(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; j++)
@@ -201,7 +245,7 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
                 sq = fma2(v, v, sq);
                 put(u[j], e, v);
             }
-        const float rstd = rsqrtf(group_sum<LPG>(sq.x + sq.y, red) * inv + a.eps);
+        const float rstd = rsqrtf(group_sum<LPG>(sq.x + sq.y, red[1]) * inv + a.eps);
         if (!BWD) {
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
@@ -247,8 +291,8 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT == 1 ? 640 : 512), VPT > 
                 }
                 if (gate && !first && row && on[j]) store<T, E>(a.dz, at + (int64_t)(l + j * lanes) * E, o);
             }
-            const float m1 = center ? group_sum<LPG>(E > 1 ? s1.x + s1.y : s1.x, red) * inv : 0.0f;
-            const float m2 = group_sum<LPG>(E > 1 ? s2.x + s2.y : s2.x, red) * inv;
+            const float2 m = group_sum2<LPG>(E > 1 ? make_float2(s1.x + s1.y, s2.x + s2.y) : make_float2(s1.x, s2.x), red[2], red[3]);
+            const float m1 = center ? m.x * inv : 0.0f, m2 = m.y * inv;
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
                 float o[E], o2[E];
@@ -337,24 +381,26 @@ template <typename T, int E, int LPG, int VPT, bool BWD> cudaError_t go(const Gn
     // the block that covers a group: whole warps, no more than its runs need
     const int threads = LPG > 0 ? 256 : (int)(ceil_div(ceil_div(a.C / a.groups / E, VPT), 32) * 32);
     const int64_t y = BWD ? gnorm_bwd_blocks(a.M, a.C, a.groups)
-                          : row_blocks(a.M, x, kRowsPerStep<LPG>, LPG > 0 ? 4 : ceil_div(1280, threads));
-    constexpr int slot = kRing<E> ? kDepth<VPT, BWD> * (BWD ? 3 : 2) * VPT * 16 : 0;  // bytes a thread
+                          : row_blocks(a.M, x, kRowsPerStep<LPG>, LPG > 0 ? kPerSm<LPG, VPT, BWD> : ceil_div(1280, threads));
+    constexpr int slot = kRing<E> ? kDepth<LPG, VPT, BWD> * (BWD ? 3 : 2) * VPT * 16 : 0;  // bytes a thread
     const int smem = slot * threads;
-    const cudaError_t e = la::allow_smem<k_gnorm<T, E, LPG, VPT, BWD>>(slot * (LPG > 0 ? 256 : (VPT == 1 ? 640 : 512)));
+    const cudaError_t e = la::allow_smem<k_gnorm<T, E, LPG, VPT, BWD>>(slot * (LPG > 0 ? 256 : (VPT <= 2 ? 640 : 512)));
     if (e != cudaSuccess) return e;
     k_gnorm<T, E, LPG, VPT, BWD><<<dim3((unsigned)x, (unsigned)y), threads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 bool aligned(const GnormArgs& a) {
-    const void* p[] = {a.x, a.z, a.dout, a.out, a.dx, a.dz};
+    const void* p[] = {a.x, a.z, a.dout, a.out, a.dx, a.dz, a.weight, a.bias};
     for (const void* q : p)
         if (reinterpret_cast<uintptr_t>(q) & 15u) return false;
     return true;
 }
 
-// The threads that hold a group, by the number of 16-byte runs in it; groups
-// that are no whole number of runs move value by value.
+// The threads that hold a group, by the number of 16-byte runs in it: part of a warp, a
+// warp with up to four runs a lane (groups of 1024: 109 and 144 us, with a block each
+// 119 and 361), then a block.  Groups that are no whole number of runs, and unaligned
+// tensors, move value by value (groups of 64 would take 909 and 1281 us that way).
 template <typename T, bool BWD> cudaError_t pick(const GnormArgs& a, cudaStream_t st) {
     constexpr int E = 16 / (int)sizeof(T);
     const int64_t gs = a.C / a.groups;
@@ -369,8 +415,9 @@ template <typename T, bool BWD> cudaError_t pick(const GnormArgs& a, cudaStream_
     if (n <= 16) return go<T, E, 16, 1, BWD>(a, st);
     if (n <= 32) return go<T, E, 32, 1, BWD>(a, st);
     if (n <= 64) return go<T, E, 32, 2, BWD>(a, st);
-    if (BWD && n <= 128) return go<T, E, 32, 4, BWD>(a, st);  // (forward: the block form is faster from here on)
+    if (n <= 128) return go<T, E, 32, 4, BWD>(a, st);
     if (n <= 640) return go<T, E, 0, 1, BWD>(a, st);
+    if (n <= 1280) return go<T, E, 0, 2, BWD>(a, st);
     return go<T, E, 0, 4, BWD>(a, st);
 }
 
