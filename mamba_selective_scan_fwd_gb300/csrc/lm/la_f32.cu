@@ -2,16 +2,22 @@
 // strides.  f32 inputs run here, and 16-bit inputs that the tensor-core path's
 // 16-byte rules exclude.
 //
-// The walk (forward, and the states the backward needs) is the recurrence
-// itself, token by token with the state in registers: 3 N P operations per
-// token and head, fewer than any chunked form takes without matrix units.  In a
+// The forward's walk is the recurrence itself, token by token with the state in
+// registers: 3 N P operations per token and head, fewer than any chunked form takes
+// without matrix units.  In a
 // tile of at most 16 tokens whose decay is e^-4 or weaker (kSlowTile) the state at
 // its start stays as it is and what the tile adds is summed apart, in units of the
 // decay since the start: the same operations, and the state is rounded once a tile
 // instead of twice a token, which a long memory adds up (2 x 3294 tokens, f32:
 // 1.4e-6 -> 2e-7 of f64).  Under a stronger decay the tokens enter one by one, with
 // the decay as S + (e^g - 1) S: a rounded e^g would be off by the same 2^-25 at
-// every token.  The backward works on chunks of 64 tokens from the states at their borders.
+// every token.  The backward works on chunks of 64 tokens from the states at their
+// borders, which are the carried sums of the chunks.
+//
+// Measured, f32: 2 x 1000 tokens, 24 heads, N = P = 64: sums 20 us, carries 6, walk 47
+// (57 % of the issue slots, shared memory 41 %; without the slow-decay form 5 us less);
+// uncut 204.  Backward of 777 tokens, 16 heads, N 32, P 64: sums 11 us, carries 6, chunks
+// 32, parts 4.
 #include <type_traits>
 
 #include "../simd.cuh"
@@ -382,7 +388,9 @@ __device__ __forceinline__ void dot4(float2& acc, float4 x, float4 z) {
 
 // Thread (ty, tx) of 16 x 16 holds four rows and some columns of every product:
 // rows and columns 16 apart where a product runs over the rows' own columns,
-// adjacent ones where that makes a shared-memory read of 16 bytes.  With c_i the cumulative log decay inside the chunk, cl its
+// adjacent ones where that makes a shared-memory read of 16 bytes.  Bound by the
+// latencies of one block's steps: 208 blocks on 152 SMs at 777 tokens x 16 heads, a
+// third of the issue slots used.  With c_i the cumulative log decay inside the chunk, cl its
 // end, H the state before and R the adjoint after the chunk (all per head):
 //   m_ij = scale e^{c_i - c_j} (j <= i),  E = m o (dy v^T),  S = m o (q k^T),  W = E o (q k^T)
 //   dq = E k + scale e^{c} (dy H^T),  dk = E^T q + e^{cl - c} (v R^T),  dv = S^T dy + e^{cl - c} (k R)

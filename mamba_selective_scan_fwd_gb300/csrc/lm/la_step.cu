@@ -4,6 +4,8 @@
 // element that is read and written once (8 bytes), so the kernel is bound by
 // HBM.  A block takes all N rows of LPR * VEC value channels of one (row, head)
 // and has every load of its state in flight before it touches q and k.
+// Measured: 256 rows x 80 heads of 128 x 64: 195 us, 6.9 TB/s (copying takes 198); one
+// row of 24 heads: 2.9 us on the GPU, 15 from Python.
 #include "la_dev.cuh"
 
 namespace ss {

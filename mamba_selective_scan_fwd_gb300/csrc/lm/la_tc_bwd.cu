@@ -20,6 +20,13 @@
 // with theirs.  dq and dk of different heads then cannot add up in tensor memory:
 // with f16 a block's work is one head's value tile, and all dq, dk are added up in
 // f32 by a kernel of their own.
+//
+// Measured, bf16, 2 x 4096 tokens, 80 heads that share q and k, N 128, P 64: 236 us
+// (DRAM 32 %, tensor cores 32 %, issue 33 %), 34 heads a block of 12 thousand cycles
+// each: P, E and W 3000 (the block rows of the first 32 tokens have four times the
+// last ones' work, and a warp reaches only its own rows of tensor memory), dv, k R and
+// q H 3000, S and D 1000, their reading and the barriers between them the rest.  One
+// block is all that an SM's tensor and shared memory hold at N = 128.
 #include "../simd.cuh"
 #include "la_tc.h"
 #include "tc.cuh"
@@ -712,6 +719,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
 
 // dq and dk of the groups that the blocks' runs cut: sums of their parts in the
 // runs' order.  Block x of `runs` - 1: the group that run x cuts and holds the start of.
+// Bound by memory (13 us for 28 MB of parts, most of them in the L2 cache).
 __global__ void __launch_bounds__(256) k_tc_join(const __grid_constant__ TcBwdArgs w, int runs) {
     __shared__ int s_parts, s_t0;  // parts after the first (-1: nothing to do); the chunk's first token
     __shared__ int64_t s_out;      // its place in dq and dk
