@@ -561,9 +561,11 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
 // part of the block on its own: 8 warps make w v, 8 keep the state (add a chunk's
 // product to it, write it out as an image), one makes the weights w, one issues copies
 // and products.
-// Measured, bf16, 2 x 4096 tokens, 80 heads, N 128, P 64, both directions: 117 us (183 MB
-// read, 278 written and 84 more kept in the L2 cache: half of DRAM's rate); a chunk takes
-// 3250 cycles, of which the shared memory's traffic (256 KB) alone 2000.
+// Measured, bf16, 2 x 4096 tokens, 80 heads, N 128, P 64, both directions: 115 us (183 MB
+// read, 278 written and 84 more kept in the L2 cache: half of DRAM's rate; 117 us without
+// the prefetch, 132 with the image stored from registers); a chunk takes 3200 cycles, of
+// which the shared memory's traffic (256 KB) alone 2000, and no part of its chain left
+// out takes more than 15 us off.
 template <int NB, int PARTS> struct StateSmem {
     static constexpr int ring = NB == 1 ? 3 : 2;  // chunks whose k and v are here or on their way
     static constexpr int k = 0, v = k + NB * 16384, stage = v + 16384, w = ring * stage, parts = 3 * 16384,
@@ -725,11 +727,20 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
                 tma_load_4d(to + L::k + n * 16384, REV ? &w.maps.q : &w.maps.k, n * 64, (int)at.hq, t0, (int)b, &s_ld[s]);
             tma_load_4d(to + L::v, REV ? &w.maps.dy : &w.maps.v, (int)at.p0, (int)h, t0, (int)b, &s_ld[s]);
         };
+        auto prefetch = [&](int ch) {  // the chunk after those on their way, into the L2 cache
+            const int t0 = (int)start_of(ch);
+#pragma unroll
+            for (int n = 0; n < NB; n++)
+                tma_prefetch_4d(REV ? &w.maps.q : &w.maps.k, n * 64, (int)at.hq, t0, (int)b);
+            tma_prefetch_4d(REV ? &w.maps.dy : &w.maps.v, (int)at.p0, (int)h, t0, (int)b);
+        };
         for (int ch = 0; ch < L::ring - 1 && ch < chunks; ch++) load(ch);
+        if (L::ring - 1 < chunks) prefetch(L::ring - 1);
         for (int ch = 0; ch < chunks; ch++) {
             const int s = ch & 1, ahead = ch + L::ring - 1;
             if (ch > 0 && !wait_or_fail(&s_u[s ^ 1], ((ch - 1) >> 1) & 1, &s_fail)) break;
             if (ahead < chunks) load(ahead);  // in the place of chunk ch - 1
+            if (ahead + 1 < chunks) prefetch(ahead + 1);
             if (!wait_or_fail(&s_w[s], (ch >> 1) & 1, &s_fail)) break;  // (also: the stage's last product was read)
             tc_fence_after();
             mma_state_wide<T, NB>(tm + 256 * s, sm + (ch % L::ring) * L::stage + L::k, sm + L::w + s * L::parts);
