@@ -193,8 +193,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     constexpr int NP = NB * 64, kImage = kImageParts<kF16<T>, NB>;
     __shared__ Decays s_decays[2];  // of iteration it at it & 1
     __shared__ float s_row[4][C], s_a[4][C], s_b[4][C], s_red[16];
-    // copies: v, dy; q, k; states.  Products: S, D; dv, k R, q H; dq, dk.
-    __shared__ __align__(8) uint64_t s_ld, s_kq, s_st, s_m1, s_m2, s_m3;
+    // copies: v, dy; q, k; states.  Products: S, D; dv, k R, q H; those of the low parts; dq, dk.
+    __shared__ __align__(8) uint64_t s_ld, s_kq, s_st, s_m1, s_m2, s_low, s_m3;
     // decays made; the states' low parts and dy read; iteration over; its dg made; E staged; E sent
     __shared__ __align__(8) uint64_t s_dec, s_rh, s_epi, s_dg, s_stage, s_sent;
     __shared__ uint32_t s_tm, s_fail;
@@ -206,7 +206,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
     const int ptiles = (int)((a.P + PT - 1) / PT);
 
     if (tid == 0) {
-        uint64_t* one[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_m3, &s_sent};
+        uint64_t* one[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_low, &s_m3, &s_sent};
         for (uint64_t* b : one) mbar_init(b, 1);
         mbar_init(&s_dec, 32);
         mbar_init(&s_dg, 32);
@@ -364,7 +364,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 at.step<kF16<T>>(w, ptiles);
                 prefetch(at);
                 wait(s_rh, it);
-                if (wait(s_m2, it)) load_v(at, it + 1);
+                if (wait(s_low, it)) load_v(at, it + 1);
                 if (wait(s_m3, it)) {
                     if (at.first) load_kq(at);
                     load_states(at, it + 1);
@@ -411,12 +411,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                     mma(tF, smem_desc(smem_addr(K) + o), smem_desc(smem_addr(low < 0 ? R : RL + low) + n * 2048), dV, s > 0);
                     mma(tZ, smem_desc(smem_addr(Q) + o), smem_desc(smem_addr(low < 0 ? H : HL + low) + n * 2048), dV, s > 0);
                 }
+                mma_commit(&s_m2);
 #pragma unroll
                 for (int s = 0; s < PT / 16; s++) {  // the second parts in dq and dk: one rounding less (of dy and v only)
                     mma(tQ, smem_desc(smem_addr(DS) + s * 32), smem_desc(smem_addr(HL) + s * 32), dQs, !first || s > 0);
                     mma(tK, smem_desc(smem_addr(V) + s * 32), smem_desc(smem_addr(RL) + s * 32), dQs, !first || s > 0);
                 }
-                mma_commit(&s_m2);
+                mma_commit(&s_low);
 #pragma unroll
                 for (int s = 0; s < C / 16; s++) {
                     mma(tQ, smem_desc(smem_addr(E) + s * 2048, 16384), smem_desc(smem_addr(K) + s * 2048, 16384), dQ, true);
@@ -437,7 +438,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
         wait(s_m3, it);
         if (s_fail && lead) {  // a wait ran out: report, wait for what is in flight (within limits)
             atomicOr(w.status, kDevWaitTimeout);
-            uint64_t* all[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_m3};
+            uint64_t* all[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_low, &s_m3};
             for (uint64_t* b : all) {
                 mbar_wait(b, 0);
                 mbar_wait(b, 1);
