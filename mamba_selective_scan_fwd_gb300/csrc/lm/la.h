@@ -68,7 +68,7 @@ inline WalkPlan walk_plan(int64_t units, int64_t L, int64_t N) {
     auto load = [&](int64_t blocks) { const int64_t n = ceil_div(blocks, kSms); return n < fit ? fit : n; };
     WalkPlan best = {1, tiles * kWalkT};
     double least = (double)load(units) * (L + 32);
-    for (int64_t K = 2; K <= 64 && K <= tiles; K++) {
+    for (int64_t K = 2; K <= 512 && K <= tiles; K += K < 64 ? 1 : 16) {
         const int64_t per = ceil_div(tiles, K);
         if (ceil_div(tiles, per) != K) continue;
         const double cost = (load(units * K) + 0.4 * load(units * (K - 1))) * (double)(per * kWalkT + 32) + 160 + units * K / 12;

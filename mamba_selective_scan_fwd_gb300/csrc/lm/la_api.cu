@@ -24,7 +24,7 @@ int check_sizes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t
     // products stay inside int64, grids inside 2^31 - 1 blocks
     if (Bsz > (1 << 20) || L > (1ll << 31) || H > (1 << 16) || P > (1 << 16)) return SS_ERR_UNSUPPORTED;
     if (Bsz * H * ceil_div(P, 16) > (1ll << 24) || Bsz * L > (1ll << 36)) return SS_ERR_UNSUPPORTED;
-    if (Bsz * ceil_div(L, kChunk32) * H > (1ll << 30)) return SS_ERR_UNSUPPORTED;
+    if (2 * Bsz * ceil_div(L, kChunk32) * H * ceil_div(P, kWalkP) >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
     return SS_OK;
 }
 

@@ -328,10 +328,10 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
 }
 
 // seg_state: end state of each segment walked from zero -> the state each
-// segment starts from.  One thread per state element; eight segments' states are
-// on their way before the first is folded in (one memory wait per eight).
+// segment starts from.  One thread per state element; 16 segments' states are on
+// their way before the first is folded in (one memory wait per 16).
 __global__ void __launch_bounds__(256) k_carry32(WalkArgs w, int64_t first) {
-    constexpr int U = 8;
+    constexpr int U = 16;
     const int64_t K = w.plan.K, BH = w.a.Bsz * w.a.H, NP = w.a.N * w.a.P;
     const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, unit = first + blockIdx.y;
     if (x >= NP) return;
