@@ -21,11 +21,12 @@
 // with f16 a block's work is one head's value tile, and all dq, dk are added up in
 // f32 by a kernel of their own.
 //
-// Measured, bf16, 2 x 4096 tokens, 80 heads that share q and k, N 128, P 64: 236 us
-// (DRAM 32 %, tensor cores 32 %, issue 33 %), 34 heads a block of 12 thousand cycles
+// Measured, bf16, 2 x 4096 tokens, 80 heads that share q and k, N 128, P 64: 229 us
+// (DRAM 33 %, tensor cores 33 %, issue 34 %), 34 heads a block of 12 thousand cycles
 // each: P, E and W 3000 (the block rows of the first 32 tokens have four times the
 // last ones' work, and a warp reaches only its own rows of tensor memory), dv, k R and
-// q H 3000, S and D 1000, their reading and the barriers between them the rest.  One
+// q H 2500, S and D 1000, their reading and the barriers between them the rest.  (With
+// the low parts' products of dq and dk before those, 240 us.)  One
 // block is all that an SM's tensor and shared memory hold at N = 128.
 #include "../simd.cuh"
 #include "la_tc.h"
