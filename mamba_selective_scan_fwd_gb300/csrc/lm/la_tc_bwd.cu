@@ -767,8 +767,8 @@ template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t
     const int64_t rep = w.a.H / w.a.G, all = w.a.Bsz * w.chunks * w.a.G * (kF16<T> ? w.splits : rep), blocks = tc_bwd_blocks(all);
     k_tc_bwd<T, NB><<<(unsigned)blocks, kThreads, smem, st>>>(w);
     e = cudaGetLastError();
-    // (equal runs of whole groups leave nothing to join)
-    if (kF16<T> || e != cudaSuccess || (all % blocks == 0 && all / blocks % rep == 0)) return e;
+    // (groups of one head, and equal runs of whole groups, leave nothing to join)
+    if (kF16<T> || e != cudaSuccess || rep == 1 || (all % blocks == 0 && all / blocks % rep == 0)) return e;
     k_tc_join<<<dim3((unsigned)blocks - 1, (unsigned)ceil_div(C * w.a.N, 1024), 2), 256, 0, st>>>(w, (int)blocks);
     return cudaGetLastError();
 }
