@@ -26,9 +26,11 @@
  * 0..L are clamped): later tokens are not read as numbers (they may hold NaN),
  * give y = 0 and zero gradients, and leave the state alone.
  *
- * g is a log decay.  exp(g) = 0 (g = -inf or below -128) resets the state;
- * NaN and positive g propagate as in IEEE arithmetic.  A chunk's scores are
- * matrix products, so a non-finite q, k or v may reach any y of its chunk.
+ * g is a log decay.  exp(g) = 0 (g = -inf or below -128) resets the state.
+ * Positive g lets it grow, in every type: the result is finite wherever it can be
+ * represented, as long as no run of tokens inside 128 adds up to more than 60.
+ * A chunk's scores are matrix products and its decays are taken from the ends of
+ * runs of 32 tokens, so a non-finite q, k, v or g may reach any y of its chunk.
  *
  * Types.  io is f32, f16 or bf16 (`dtype`, as in ss.h).  States, decays, sums
  * and dg, dh0 are f32.  dq, dk, dv have the io type: they feed the

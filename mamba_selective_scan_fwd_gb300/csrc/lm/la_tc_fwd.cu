@@ -38,18 +38,26 @@ constexpr int PT = kTileP;
 template <typename T> constexpr int kParts = kF16<T> ? 2 : 3;
 
 // The chunk's decays, by runs of 32 tokens (one warp's): c_i = (the run's end) -
-// rel_i with rel a thread's own.  Shared: tail = e^{rel} (where wanted) and the
-// log2 decay of each run.
+// rel_i with rel a thread's own.  Shared: tail = e^{rel}, its largest value in each
+// run (each where wanted) and the log2 decay of each run.
 // A warpgroup (token = tid % 128), g: the token's log decay.  Returns rel (at
 // most 0 for decays).
-__device__ __forceinline__ float chunk_decays(float* tail, Two* total, float g) {
+__device__ __forceinline__ float chunk_decays(float* tail, float* top, Two* total, float g) {
     const int tok = threadIdx.x & (C - 1);
     const float in[1] = {clamp_g(g) * kLog2e};
     Two c[1];
     warp_cumsum<1>(in, c);
     const Two end = {__shfl_sync(kFull, c[0].h, 31), __shfl_sync(kFull, c[0].l, 31)};
     const float rel = two_diff(end, c[0]);
-    if (tail) tail[tok] = ex2(rel);
+    if (tail) {
+        const float t = ex2(rel);
+        tail[tok] = t;
+        if (top) {
+            uint32_t m;
+            asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(t)));
+            if ((tok & 31) == 0) top[tok >> 5] = __uint_as_float(m);
+        }
+    }
     if ((tok & 31) == 31) total[tok >> 5] = end;
     return rel;
 }
@@ -304,7 +312,7 @@ template <int NB> struct FwdSmem {
 template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = FwdSmem<NB>;
-    __shared__ float s_tail[C];
+    __shared__ float s_tail[C], s_top[4];
     __shared__ Two s_total[2][4];
     // copies landed; S; q H; P v; k^T (w v)
     __shared__ __align__(8) uint64_t s_ld, s_mS, s_mE, s_mO, s_mU;
@@ -361,7 +369,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
     int ch = 0;
     // both halves: chunk ch's decays (into end, rel), then its tiles
     auto decays = [&](float* tail, Two* total, int64_t t0) {
-        const float rel = chunk_decays(tail, total, g);
+        const float rel = chunk_decays(tail, kF16<T> ? s_top : nullptr, total, g);
         if (ch + 1 < chunks) g = load_g(a, b, h, t0 + C, valid(t0 + C));
         return rel;
     };
@@ -384,8 +392,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             Two end[4];
             run_ends(s_total[0], end);
             const Two mine = end_of(end);
-            float vs = 1.0f;
-            if (kF16<T>) vs = f16_scale(group_max(fmaxf(row_max<T>(V, tok, 0), row_max<T>(V, tok, 1)), s_red, 1));
             const float wt = ex2(two_diff(end[3], mine) + rel), cl = end[3].h + end[3].l;
             if (tid == 0) {  // (this half waits for both; the other's P must not)
                 tc_fence_after();
@@ -404,6 +410,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
                 mma_commit(&s_mE);
             }
             __syncwarp();
+            float vs = 1.0f;
+            if (kF16<T>) vs = f16_scale(group_max(wt * fmaxf(row_max<T>(V, tok, 0), row_max<T>(V, tok, 1)), s_red, 1));
             ok = mbar_wait(&s_mE, ph);  // q makes room for w v
             split_row<T>(V, tok, 0, 8, wt * vs, W[0], W[1], W[2]);
             fence_proxy_async_smem();
@@ -445,6 +453,19 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             run_ends(s_total[1], end);
             const Two mine = end_of(end);
             const float ci = (mine.h - rel) + mine.l;
+            float lift = 1.0f;  // largest e^{c_i - c_j} of the token's row (1 for decays)
+            if (kF16<T>) {
+                float top = rel;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float x = __shfl_up_sync(kFull, top, o);
+                    if (lane >= o) top = fmaxf(top, x);
+                }
+                lift = ex2(top - rel);
+#pragma unroll
+                for (int cb = 0; cb < 3; cb++)
+                    if (cb < run) lift = fmaxf(lift, ex2(two_diff(mine, end[cb]) - rel) * s_top[cb]);
+            }
             ok = mbar_wait(&s_mS, ph);
             tc_fence_after();
             // P, by runs of 32 columns: left of the diagonal e^{c_i - c_j} = e^{c_i - c_e} e^{c_e - c_j} with e
@@ -459,7 +480,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
                     for (int j = 0; j < 32; j++)
                         if (32 * cb + j <= tok) m = fmaxf(m, fabsf(s[j]));
                 }
-                ps = f16_scale(m);
+                ps = f16_scale(m * lift);
             }
             for (int cb = 0; cb < 4; cb++) {
                 uint32_t r[16];
@@ -630,8 +651,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
             }
             float wt = s_weight[s][tok];
             if (kF16<T>) {
-                // one scale for the tile: the larger of both halves' largest values
-                const float m = group_max(row_max<T>(V, tok, half), s_red[half], 1 + half);
+                // one scale for the tile: the larger of both halves' largest w v
+                const float m = group_max(wt * row_max<T>(V, tok, half), s_red[half], 1 + half);
                 if (tok == 0) s_red[half][0] = __float_as_uint(m);
                 asm volatile("bar.sync 4, 256;" ::: "memory");
                 const float vs = f16_scale(fmaxf(__uint_as_float(s_red[0][0]), __uint_as_float(s_red[1][0])));

@@ -162,7 +162,8 @@ __device__ __forceinline__ uint4* unit(void* tile, int r, int c) {
 
 // A power of two 2^e that takes `most` (>= 0) into [2^13, 2^14): f16 operands
 // are scaled by it, so that neither their range nor their small values cost
-// precision.  1 for 0, NaN and infinity.
+// precision.  `most` bounds the operand as it will be, decays and weights in it:
+// positive log decays make those larger than 1.  1 for 0, NaN and infinity.
 __device__ __forceinline__ float f16_scale(float most) {
     const int e = (int)(__float_as_uint(most) >> 23) - 127;
     if (most == 0.0f || e >= 128) return 1.0f;
