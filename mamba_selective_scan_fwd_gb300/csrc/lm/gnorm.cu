@@ -245,7 +245,9 @@ __global__ void __launch_bounds__(LPG > 0 ? 256 : (VPT <= 2 ? 640 : 512), kPerSm
                 sq = fma2(v, v, sq);
                 put(u[j], e, v);
             }
-        const float rstd = rsqrtf(group_sum<LPG>(sq.x + sq.y, red[1]) * inv + a.eps);
+        const float var = group_sum<LPG>(sq.x + sq.y, red[1]) * inv;
+        // (a warp beyond the last row: with eps = 0 its 0 * inf would reach the parameters' sums)
+        const float rstd = !BWD || LPG == 0 || row ? rsqrtf(var + a.eps) : 0.0f;
         if (!BWD) {
 #pragma unroll
             for (int j = 0; j < VPT; j++) {
