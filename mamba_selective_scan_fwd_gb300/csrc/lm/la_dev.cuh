@@ -34,6 +34,21 @@ __device__ __forceinline__ float log_decay(const Args& a, int64_t b, int64_t t, 
     return clamp_g(a.g_per_head ? a.g[h] : a.g[(b * a.L + t) * a.H + h]);
 }
 
+// A decay e^g of an f32 state: S + (e^g - 1) S where it is weak (a rounded e^g near 1
+// would be off the same way at every step, which a long memory adds up), e^g S below
+// one half (e^g - 1 is next to -1 there, and what is left of S would carry its
+// rounding: 2e-5 of it at g = -8, all of it at -18).
+constexpr float kWeakG = -0.6931472f;
+struct Decay {
+    float by;
+    bool weak;
+};
+__device__ __forceinline__ Decay decay_of(float g) {
+    const bool weak = g >= kWeakG;  // (NaN: no)
+    return {weak ? expm1f(g) : expf(g), weak};
+}
+__device__ __forceinline__ float decayed(Decay d, float x) { return d.weak ? fmaf(d.by, x, x) : d.by * x; }
+
 // Cumulative log decays are kept as the unevaluated sum of two floats (Knuth's
 // two-sum): e^{c_i - c_j} of neighbouring tokens then stays exact to f32
 // rounding however far c has fallen since the chunk's start (a reset in the

@@ -9,9 +9,8 @@
 // its start stays as it is and what the tile adds is summed apart, in units of the
 // decay since the start: the same operations, and the state is rounded once a tile
 // instead of twice a token, which a long memory adds up (2 x 3294 tokens, f32:
-// 1.4e-6 -> 2e-7 of f64).  Under a stronger decay the tokens enter one by one, with
-// the decay as S + (e^g - 1) S: a rounded e^g would be off by the same 2^-25 at
-// every token.  The backward works on chunks of 64 tokens from the states at their
+// 1.4e-6 -> 2e-7 of f64).  Under a stronger decay the tokens enter one by one (their
+// decays: Decay in la_dev.cuh).  The backward works on chunks of 64 tokens from the states at their
 // borders, which are the carried sums of the chunks.
 //
 // Measured, f32: 2 x 1000 tokens, 24 heads, N = P = 64: sums 20 us, carries 6, walk 47
@@ -50,6 +49,10 @@ template <typename T> __device__ __forceinline__ float4 fetch4(const T* p, int64
         for (int e = 0; e < 4; e++) x[e] = e < left ? ldf(p + e) : 0.0f;
     }
     return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ float2 decayed2(Decay d, float2 x) {
+    return d.weak ? fma2(splat2(d.by), x, x) : mul2(splat2(d.by), x);
 }
 
 // End states of the segments, each walked from zero.  One block: kWalkP value
@@ -134,14 +137,13 @@ __global__ void __launch_bounds__(256, RN == 8 ? 2 : 3) k_sum32(WalkArgs w) {
                 for (int c = 0; c < 4; c++) X[r][c] = fma2(k, vs[c], X[r][c]);
             }
         }
-        // (e^cl - 1: a rounded e^cl would be off the same way at every tile)
         const float all = s_all[s];
-        const float2 less = splat2(expm1f(all));
+        const Decay d = decay_of(all);
         total += all;
 #pragma unroll
         for (int r = 0; r < RN / 2; r++)
 #pragma unroll
-            for (int c = 0; c < 4; c++) S[r][c] = add2(fma2(less, S[r][c], S[r][c]), X[r][c]);
+            for (int c = 0; c < 4; c++) S[r][c] = add2(decayed2(d, S[r][c]), X[r][c]);
     }
     float* to = w.seg_state + at * a.N * a.P + p0 + 4 * tx;
 #pragma unroll
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
     constexpr int EK = TT * NP / 1024 < 1 ? 1 : TT * NP / 1024, EV = TT * kWalkP / 1024 < 1 ? 1 : TT * kWalkP / 1024;  // runs of 4 values a thread loads
     __shared__ __align__(16) float s_k[TT][NP], s_q[TT][NP], s_v[TT][kWalkP];
     __shared__ float s_a[TT], s_down[TT], s_up[TT], s_all;
+    __shared__ uint32_t s_weak;  // bit t: token t's decay is weak
     __shared__ float s_y[8][TT][kWalkP];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -244,8 +247,11 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
             Two c[1];
             warp_cumsum<1>(x, c);
             if (lane == 31) s_all = c[0].h + c[0].l;
+            const Decay d = decay_of(x[0]);
+            const uint32_t weak = __ballot_sync(kFull, d.weak);
+            if (lane == 0) s_weak = weak;
             if (lane < TT) {
-                s_a[lane] = expm1f(x[0]);
+                s_a[lane] = d.by;
                 s_down[lane] = expf(-c[0].h) * (1.0f - c[0].l);
                 s_up[lane] = expf(c[0].h) * (1.0f + c[0].l);
             }
@@ -254,12 +260,13 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
         if (i + 1 < tiles) fetch(i + 1);
         const float all = s_all;
         const bool slow = all >= kSlowTile;  // (NaN: no)
+        const uint32_t weak = s_weak;
         // SLOW: S = S0 + A in units of e^c: S0 stays, A takes what the tile adds
         auto tokens = [&](auto which) {
             constexpr bool SLOW = decltype(which)::value;
             float2 A[2][NR / 2] = {};
-#pragma unroll 2
-            for (int t = 0; t < nv; t++) {
+            auto token = [&](int t, auto how) {
+                constexpr bool WEAK = decltype(how)::value;
                 const float d = SLOW ? s_down[t] : 1.0f;
                 const float2 av = splat2(s_a[t]), v[2] = {splat2(s_v[t][lane] * d), splat2(s_v[t][lane + 32] * d)};
                 float2 acc[2][2] = {};
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
                         for (int u = 0; u < 2; u++) {
                             float2 &x = S[c][r + u], &y = A[c][r + u];
                             if (SLOW) y = fma2(kr[u], v[c], y);
-                            else x = fma2(kr[u], v[c], fma2(av, x, x));
+                            else x = fma2(kr[u], v[c], WEAK ? fma2(av, x, x) : mul2(av, x));
                             acc[c][u] = fma2(qr[u], SLOW ? add2(x, y) : x, acc[c][u]);
                         }
                 }
@@ -283,16 +290,18 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
                     const float2 s = add2(acc[c][0], acc[c][1]);
                     s_y[warp][t][lane + 32 * c] = s.x + s.y;
                 }
+            };
+#pragma unroll 2
+            for (int t = 0; t < nv; t++) {
+                if (SLOW || (weak >> t & 1)) token(t, std::true_type{});
+                else token(t, std::false_type{});
             }
             if (SLOW) {
-                const float2 less = splat2(expm1f(all));
+                const Decay d = decay_of(all);
 #pragma unroll
                 for (int c = 0; c < 2; c++)
 #pragma unroll
-                    for (int r = 0; r < NR / 2; r++) {
-                        const float2 x = add2(S[c][r], A[c][r]);
-                        S[c][r] = fma2(less, x, x);
-                    }
+                    for (int r = 0; r < NR / 2; r++) S[c][r] = decayed2(d, add2(S[c][r], A[c][r]));
             }
         };
         if (slow) tokens(std::true_type{});

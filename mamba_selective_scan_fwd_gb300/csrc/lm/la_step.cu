@@ -54,8 +54,7 @@ template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128) k
         v[e] = mine ? ldf(static_cast<const T*>(s.v) + b * s.v_batch + h * s.P + p + e) : 0.0f;
         acc[e] = 0.0f;
     }
-    // e^g - 1: a rounded e^g near 1 would be off the same way at every token of a long answer
-    const float a = expm1f(clamp_g(s.g_per_head ? s.g[h] : s.g[b * s.H + h]));
+    const Decay a = decay_of(clamp_g(s.g_per_head ? s.g[h] : s.g[b * s.H + h]));
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NI; i++) {
@@ -64,7 +63,7 @@ template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128) k
             const float kn = s_k[n], qn = s_q[n];
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                x[i].f[e] = fmaf(kn, v[e], fmaf(a, x[i].f[e], x[i].f[e]));
+                x[i].f[e] = fmaf(kn, v[e], decayed(a, x[i].f[e]));
                 acc[e] = fmaf(qn, x[i].f[e], acc[e]);
             }
             *reinterpret_cast<FV*>(at + (int64_t)n * s.P) = x[i].v;
