@@ -5,7 +5,7 @@
 // The forward's walk is the recurrence itself, token by token with the state in
 // registers: 3 N P operations per token and head, fewer than any chunked form takes
 // without matrix units.  In a
-// tile of at most 16 tokens whose decay is e^-4 or weaker (kSlowTile) the state at
+// tile of at most 16 tokens whose decay stays at e^-4 or weaker (kSlowTile) the state at
 // its start stays as it is and what the tile adds is summed apart, in units of the
 // decay since the start: the same operations, and the state is rounded once a tile
 // instead of twice a token, which a long memory adds up (2 x 3294 tokens, f32:
@@ -26,7 +26,7 @@ namespace ss {
 namespace la {
 namespace {
 
-constexpr float kSlowTile = -4.0f;  // keeps e^-c below 55: no range is lost
+constexpr float kSlowTile = -4.0f;  // every c of the tile between it and its opposite: e^-c stays between 1 / 55 and 55
 
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
     __shared__ __align__(16) float s_k[TT][NP], s_q[TT][NP], s_v[TT][kWalkP];
     __shared__ float s_a[TT], s_down[TT], s_up[TT], s_all;
     __shared__ uint32_t s_weak;  // bit t: token t's decay is weak
+    __shared__ bool s_slow;
     __shared__ float s_y[8][TT][kWalkP];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -246,7 +247,11 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
             const float x[1] = {lane < TT ? rg : 0.0f};
             Two c[1];
             warp_cumsum<1>(x, c);
-            if (lane == 31) s_all = c[0].h + c[0].l;
+            const bool slow = __all_sync(kFull, c[0].h >= kSlowTile && c[0].h <= -kSlowTile);  // (NaN: no)
+            if (lane == 31) {
+                s_all = c[0].h + c[0].l;
+                s_slow = slow;
+            }
             const Decay d = decay_of(x[0]);
             const uint32_t weak = __ballot_sync(kFull, d.weak);
             if (lane == 0) s_weak = weak;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(256, NR == 16 ? 2 : 3) k_walk32(WalkArgs w) {
         __syncthreads();
         if (i + 1 < tiles) fetch(i + 1);
         const float all = s_all;
-        const bool slow = all >= kSlowTile;  // (NaN: no)
+        const bool slow = s_slow;
         const uint32_t weak = s_weak;
         // SLOW: S = S0 + A in units of e^c: S0 stays, A takes what the tile adds
         auto tokens = [&](auto which) {
