@@ -277,8 +277,19 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             }
         };
         uint32_t round = 0;
-        auto send = [&](auto store) {  // what the compute warps staged in E
+        // sends what the compute warps staged in E (one tile or two), zeros past the row's length: zero rows times a
+        // state or an operand that is not finite are not zero
+        int lo, hi;  // the chunk's tokens past the length
+        auto send = [&](int tiles, auto store) {
             wait(s_stage, round++);
+            if (lo < hi) {
+                for (int k = 0; k < tiles; k++)
+#pragma unroll 4
+                    for (int i = lo * 8 + lane; i < hi * 8; i += 32)
+                        *reinterpret_cast<uint4*>(E + k * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
             if (lead) {
                 if (!s_fail) store();
                 bulk_commit();
@@ -302,13 +313,15 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                 put_decays(s_decays[(it + 1) & 1], g, a.scale);
                 mbar_arrive(&s_dec);
             }
+            lo = valid(at);
+            hi = (int)min((int64_t)C, a.L - (int64_t)at.chunk * C);
             wait(s_epi, it);
             put_dg(at);
             mbar_arrive(&s_dg);
-            send([&] { tma_store_4d(&w.maps.dv, E, at.pt * PT, at.h, at.chunk * C, at.b); });
+            send(1, [&] { tma_store_4d(&w.maps.dv, E, at.pt * PT, at.h, at.chunk * C, at.b); });
             if (at.last)
                 for (int k = 0; k < qk_rounds(at); k++)
-                    send([&] {
+                    send(2, [&] {
                         const int t0 = at.chunk * C;
                         if (at.part < 0) {  // NB == 1: dq and dk; NB == 2: both halves of one of them
                             tma_store_4d(NB == 1 || k == 0 ? &w.maps.dq : &w.maps.dk, E, 0, at.gq, t0, at.b);

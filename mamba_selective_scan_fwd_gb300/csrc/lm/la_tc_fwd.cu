@@ -525,6 +525,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             }
             ok = mbar_wait(&s_mE, ph) && ok;
             tc_fence_after();
+            // past the row's length: zero rows times a state or a v that is not finite are not zero
+            const bool counts = tok < valid(t0);
             const float fe = a.scale * (kF16<T> ? ex2(ci) / s_hs[ph] : ex2(ci)), fi = kF16<T> ? a.scale / ps : a.scale;
             ok = mbar_wait(&s_mO, ph) && ok;
             ok = mbar_wait(&s_mU, ph) && ok;  // w v has left the staging tile, k and v are done with
@@ -543,7 +545,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
                         const int c = 8 * u + 2 * i;
                         const float2 x = fma2(splat2(fi), make_float2(o[c], o[c + 1]),
                                               mul2(splat2(fe), make_float2(e[c], e[c + 1])));
-                        r[i] = pack2<T>(x.x, x.y);
+                        r[i] = counts ? pack2<T>(x.x, x.y) : 0;
                     }
                     *unit(Y, tok, 4 * half + u) = make_uint4(r[0], r[1], r[2], r[3]);
                 }
