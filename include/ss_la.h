@@ -122,6 +122,15 @@ typedef struct {
 int ss_la_step(const ss_la_step_desc *desc, void *stream);
 
 /*
+ * Runs one block on `stream` one part of which waits, for limit_ns nanoseconds
+ * (0 .. 2e9; else SS_ERR_INVALID_PROBLEM), on a barrier nothing completes while
+ * the others are over, and which ends as the tensor-core kernels above do: the
+ * wait is reported in the status word that ss_device_status reads.  For testing
+ * that path without any failure of the GPU.
+ */
+int ss_la_selftest_wait_timeout(int64_t limit_ns, void *stream);
+
+/*
  * Group norm over groups of C / groups adjacent channels of each token, with
  * an activation:
  *   norm(a)  = (a - mean(a)) / sqrt(var(a) + eps) * weight + bias   per group; without SS_GNORM_CENTER

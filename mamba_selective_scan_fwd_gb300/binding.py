@@ -30,6 +30,7 @@ EXPORTS = ["ss_fwd", "ss_bwd", "ss_fwd_workspace_bytes", "ss_bwd_workspace_bytes
            "ss_set_copies_only", "ss_staging_uses_tma", "ss_measure_ex2_rate",
            "ss_measure_fma_rate",
            "ss_la_fwd_workspace_bytes", "ss_la_fwd", "ss_la_bwd_workspace_bytes", "ss_la_bwd", "ss_la_step",
+           "ss_la_selftest_wait_timeout",
            "ss_gnorm_fwd", "ss_gnorm_bwd_workspace_bytes", "ss_gnorm_bwd"]
 ABI_VERSION = 7
 
@@ -127,6 +128,8 @@ def lib() -> ctypes.CDLL:
     for fn in ("ss_la_fwd", "ss_la_bwd", "ss_la_step"):
         getattr(L, fn).restype = ctypes.c_int
         getattr(L, fn).argtypes = [_P, _P]
+    L.ss_la_selftest_wait_timeout.restype = ctypes.c_int
+    L.ss_la_selftest_wait_timeout.argtypes = [_I64, _P]
     L.ss_gnorm_fwd.restype = ctypes.c_int
     L.ss_gnorm_fwd.argtypes = [_P] * 5 + [_I64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, _P]
     L.ss_gnorm_bwd_workspace_bytes.restype = _SZ

@@ -445,6 +445,14 @@ int ss_la_step(const ss_la_step_desc* d, void* stream) {
     return launch_step(s, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
+int ss_la_selftest_wait_timeout(int64_t limit_ns, void* stream) {
+    if (limit_ns < 0 || limit_ns > (int64_t)kWaitLimitNs) return SS_ERR_INVALID_PROBLEM;
+    int* status = nullptr;
+    const int rc = device_status_word(&status);
+    if (rc != SS_OK) return rc;
+    return launch_late_timeout(status, (uint64_t)limit_ns, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
 namespace {
 int check_gnorm(int64_t M, int64_t C, int64_t groups, float eps, int flags, int dtype, bool z) {
     if (M < 0 || C < 1 || groups < 1 || C % groups != 0 || !(eps >= 0.0f)) return SS_ERR_INVALID_PROBLEM;

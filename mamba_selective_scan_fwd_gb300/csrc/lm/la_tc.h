@@ -111,6 +111,7 @@ cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st);
 cudaError_t launch_tc_fwd(const TcWalkArgs& w, cudaStream_t st);
 cudaError_t launch_tc_state(const TcWalkArgs& w, bool sum, cudaStream_t st);
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st);
+cudaError_t launch_late_timeout(int* status, uint64_t limit_ns, cudaStream_t st);  // a wait that runs out, reported
 
 }  // namespace la
 

@@ -450,14 +450,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
             at.step<kF16<T>>(w, ptiles);
         }
         wait(s_m3, it);
-        if (s_fail && lead) {  // a wait ran out: report, wait for what is in flight (within limits)
-            atomicOr(w.status, kDevWaitTimeout);
-            uint64_t* all[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_low, &s_m3};
-            for (uint64_t* b : all) {
-                mbar_wait(b, 0);
-                mbar_wait(b, 1);
-            }
-        }
     } else {  // ---------------- the compute warps
         uint32_t round = 0;
         auto stage = [&](auto fill) {  // a round through E: what was there has been sent
@@ -727,9 +719,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
         tc_fence_after();
         put_out(s_at[it % 3], dv, kap_last);
     }
-    tc_fence_before();
-    __syncthreads();
-    if (tid < 32) tmem_free(tm, 512);
+    uint64_t* const bars[] = {&s_ld, &s_kq, &s_st, &s_m1, &s_m2, &s_low, &s_m3};
+    end_block(&s_fail, w.status, bars, tm, 512);
 }
 
 // dq and dk of the groups that the blocks' runs cut: sums of their parts in the
@@ -773,6 +764,24 @@ __global__ void __launch_bounds__(256) k_tc_join(const __grid_constant__ TcBwdAr
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2<__nv_bfloat16>(s.x, s.y), pack2<__nv_bfloat16>(s.z, s.w));
 }
 
+// A block one part of which is long over when another's wait, on a barrier that nothing
+// completes, runs out.
+__global__ void __launch_bounds__(64, 1) k_late_timeout(int* status, uint64_t limit_ns) {
+    __shared__ __align__(8) uint64_t s_bar;
+    __shared__ uint32_t s_tm, s_fail;
+    if (threadIdx.x == 0) {
+        mbar_init(&s_bar, 1);
+        s_fail = 0;
+        fence_proxy_async_smem();
+    }
+    if (threadIdx.x < 32) tmem_alloc(&s_tm, 32);
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x >= 32) wait_or_fail(&s_bar, 0, &s_fail, limit_ns);
+    uint64_t* const bars[] = {&s_bar};
+    end_block(&s_fail, status, bars, s_tm, 32);
+}
+
 template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t st) {
     constexpr int smem = BwdSmem<NB>::total;
     cudaError_t e = allow_smem<k_tc_bwd<T, NB>>(smem);
@@ -787,6 +796,11 @@ template <typename T, int NB> cudaError_t bwd_n(const TcBwdArgs& w, cudaStream_t
 }
 
 }  // namespace
+
+cudaError_t launch_late_timeout(int* status, uint64_t limit_ns, cudaStream_t st) {
+    k_late_timeout<<<1, 64, 0, st>>>(status, limit_ns);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_tc_bwd(const TcBwdArgs& w, cudaStream_t st) {
     if (w.a.dtype == 1) return w.a.N > 64 ? bwd_n<__half, 2>(w, st) : bwd_n<__half, 1>(w, st);

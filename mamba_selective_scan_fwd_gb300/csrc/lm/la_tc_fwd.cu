@@ -316,7 +316,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
     __shared__ Two s_total[2][4];
     // copies landed; S; q H; P v; k^T (w v)
     __shared__ __align__(8) uint64_t s_ld, s_mS, s_mE, s_mO, s_mU;
-    __shared__ uint32_t s_tm, s_red[4];
+    __shared__ uint32_t s_tm, s_red[4], s_fail;
     __shared__ float s_hs[2];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, tok = tid & (C - 1), run = tok >> 5;
@@ -334,6 +334,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
         mbar_init(&s_mE, 1);
         mbar_init(&s_mO, 1);
         mbar_init(&s_mU, 1);
+        s_fail = 0;
         fence_proxy_async_smem();
     }
     if (tid < 32) tmem_alloc(&s_tm, 256);
@@ -559,19 +560,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(256, 2) k_tc_fwd
             }
         }
     }
-    if (ch < chunks) {  // a wait ran out: report, wait for what is in flight (within limits), leave
-        if (tid == C) {
-            atomicOr(w.status, kDevWaitTimeout);
-            mbar_wait(&s_ld, ch & 1);
-            mbar_wait(&s_ld, (ch + 1) & 1);
-            mbar_wait(&s_mE, (ch + 1) & 1);
-            mbar_wait(&s_mO, (ch + 1) & 1);
-            mbar_wait(&s_mU, (ch + 1) & 1);
-        }
-    }
+    if (!ok) s_fail = 1;  // a wait ran out, in the last chunk or (everybody left the loop then) before
     if (tid == C) bulk_wait_all();
-    __syncthreads();
-    if (tid < 32) tmem_free(tm, 256);
+    uint64_t* const bars[] = {&s_ld, &s_mS, &s_mE, &s_mO, &s_mU};
+    end_block(&s_fail, w.status, bars, tm, 256);
 }
 
 // ---------------------------------------------------------------- states
@@ -769,21 +761,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
             mma_state_wide<T, NB>(tm + 256 * s, sm + (ch % L::ring) * L::stage + L::k, sm + L::w + s * L::parts);
             mma_commit(&s_u[s]);
         }
-        if (s_fail) {  // report, wait for what is in flight (within limits)
-            atomicOr(w.status, kDevWaitTimeout);
-            for (int s = 0; s < L::ring; s++) {
-                mbar_wait(&s_ld[s], 0);
-                mbar_wait(&s_ld[s], 1);
-            }
-            for (int s = 0; s < 2; s++) {
-                mbar_wait(&s_u[s], 0);
-                mbar_wait(&s_u[s], 1);
-            }
-        }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (tid < 32) tmem_free(tm, 512);
+    uint64_t* const bars[] = {&s_ld[0], &s_ld[1], &s_ld[L::ring - 1], &s_u[0], &s_u[1]};
+    end_block(&s_fail, w.status, bars, tm, 512);
 }
 
 // seg_state: end state of each segment walked from zero -> the state each

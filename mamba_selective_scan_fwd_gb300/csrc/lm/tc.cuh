@@ -92,11 +92,36 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // Waits of a block whose parts run on their own: the first wait that runs out
 // sets *fail, and from then on no wait of the block waits, so that every part
 // runs to its end at once.
-__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t phase, volatile uint32_t* fail) {
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t phase, volatile uint32_t* fail,
+                                             uint64_t limit_ns = kWaitLimitNs) {
     if (*fail) return false;
-    if (mbar_wait(bar, phase)) return true;
+    if (mbar_wait(bar, phase, limit_ns)) return true;
     *fail = 1;
     return false;
+}
+
+// The block's end, all its threads: a wait that ran out in any part (a part that ended
+// before it cannot tell) is noted in the status word, what may still be in flight on
+// the barriers `bars` of copies and products is waited for (one of a barrier's two
+// phases is over already, the other gets kDrainLimitNs), and tensor memory is freed.
+constexpr uint64_t kDrainLimitNs = 100000000ull;
+template <int N>
+__device__ __forceinline__ void end_block(volatile uint32_t* fail, int* status, uint64_t* const (&bars)[N], uint32_t tm, uint32_t cols) {
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        if (*fail) {
+            if (threadIdx.x == 0) {
+                atomicOr(status, kDevWaitTimeout);
+                for (int i = 0; i < N; i++) {
+                    mbar_wait(bars[i], 0, kDrainLimitNs);
+                    mbar_wait(bars[i], 1, kDrainLimitNs);
+                }
+            }
+        }
+        __syncwarp();
+        tmem_free(tm, cols);
+    }
 }
 
 // ---------------------------------------------------------------- copies

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from .binding import _I32, _I64, _P, _SZ, _check, _on_device, _require, _workspace, dtype_id, lib
+from .binding import _I32, _I64, _P, _SZ, _check, _on_device, _require, _workspace, dtype_id, lib, stream_handle
 
 GNORM_CENTER, GNORM_GATE_FIRST = 1, 2
 
@@ -248,6 +248,12 @@ def ss_la_step(q, k, v, g, state, scale=1.0, slots=None, y=None, stream=None):
                    qs[0], ks[0], vs[0], Bsz, H, G, N, P, pool, scale, dtype_id(v), per_head, 0)
     _call("ss_la_step", v, ctypes.byref(d))
     return y
+
+
+def la_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
+    """Launch one block, built like the tensor-core kernels', one part of which waits limit_ns for
+    nothing after the others are over; it records the failure in the device status word."""
+    _check("ss_la_selftest_wait_timeout", lib().ss_la_selftest_wait_timeout(int(limit_ns), stream_handle(stream)))
 
 
 def _gnorm_prepare(x, weight, bias, z, groups, center, gate_first):
