@@ -131,8 +131,8 @@ int ss_la_step(const ss_la_step_desc *desc, void *stream);
 int ss_la_selftest_wait_timeout(int64_t limit_ns, void *stream);
 
 /*
- * Group norm over groups of C / groups adjacent channels of each token, with
- * an activation:
+ * Group norm over groups of C / groups adjacent channels of each token (at most
+ * 8192, else SS_ERR_UNSUPPORTED), with an activation:
  *   norm(a)  = (a - mean(a)) / sqrt(var(a) + eps) * weight + bias   per group; without SS_GNORM_CENTER
  *              a / sqrt(mean(a^2) + eps) * weight + bias
  *   z given, SS_GNORM_GATE_FIRST not set: out = norm(x) * silu(z)

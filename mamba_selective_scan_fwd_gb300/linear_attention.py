@@ -260,8 +260,8 @@ def _gnorm_prepare(x, weight, bias, z, groups, center, gate_first):
     """Check the shared inputs of both directions; returns M, C, flags and the inputs' pointers."""
     import torch
 
-    C, dev, f32 = x.shape[-1], x.device, torch.float32
-    if groups < 1 or C % groups != 0:
+    C, dev, f32 = x.shape[-1] if x.dim() else 0, x.device, torch.float32
+    if groups < 1 or C < 1 or C % groups != 0:
         raise ValueError(f"{C} channels cannot form {groups} groups")
     if gate_first and z is None:
         raise ValueError("gate_first needs a gate z")
@@ -275,8 +275,8 @@ def _gnorm_prepare(x, weight, bias, z, groups, center, gate_first):
 
 def ss_gnorm_fwd(x, weight=None, bias=None, z=None, groups=1, eps=1e-5, center=True, gate_first=False, out=None,
                  stream=None):
-    """Group norm of each token's channels (the last dimension, ``groups`` runs of adjacent
-    channels), then an activation: norm(x) * silu(z); norm(x * silu(z)) with ``gate_first``;
+    """Group norm of each token's channels (the last dimension, ``groups`` runs of at most 8192
+    adjacent channels), then an activation: norm(x) * silu(z); norm(x * silu(z)) with ``gate_first``;
     silu(norm(x)) without z.  ``center=False`` divides by the root mean square instead.
     Returns out (x's shape and dtype)."""
     import torch
@@ -318,5 +318,5 @@ def ss_gnorm_bwd(x, weight, bias, dout, z=None, groups=1, eps=1e-5, center=True,
     workspace, wsb = _workspace(int(lib().ss_gnorm_bwd_workspace_bytes(M, C, groups, dt)), x.device, workspace)
     ptr = {name: None if out[name] is None else out[name].data_ptr() for name in shapes}
     _call("ss_gnorm_bwd", x, x.data_ptr(), wp, bp, zp, dout.data_ptr(), ptr["dx"], ptr["dz"], ptr["dweight"],
-          ptr["dbias"], M, C, groups, eps, flags, dt, workspace.data_ptr(), wsb)
+          ptr["dbias"], M, C, groups, eps, flags, dt, None if workspace is None else workspace.data_ptr(), wsb)
     return out
