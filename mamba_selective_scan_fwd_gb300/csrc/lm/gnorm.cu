@@ -419,8 +419,10 @@ template <typename T, bool BWD> cudaError_t pick(const GnormArgs& a, cudaStream_
     if (n <= 64) return go<T, E, 32, 2, BWD>(a, st);
     if (n <= 128) return go<T, E, 32, 4, BWD>(a, st);
     if (n <= 640) return go<T, E, 0, 1, BWD>(a, st);
-    if (n <= 1280) return go<T, E, 0, 2, BWD>(a, st);
-    return go<T, E, 0, 4, BWD>(a, st);
+    // (8192 channels are at most 1024 runs of 16-bit values, 2048 of f32)
+    if constexpr (E == 4)
+        if (n > 1280) return go<T, E, 0, 4, BWD>(a, st);
+    return go<T, E, 0, 2, BWD>(a, st);
 }
 
 template <bool BWD> cudaError_t pick_io(const GnormArgs& a, cudaStream_t st) {
