@@ -276,15 +276,17 @@ __device__ __forceinline__ void put_state(char* to, float s, const float (&X)[St
 }
 
 // k^T (w v): rows n (both halves of the 128 rows the same 64 when NB == 1), columns
-// p.  Its parts added up in 64 columns of tensor memory (w: one tile per part) ...
+// p.  Its parts added up in 64 columns of tensor memory (w: one tile per part), the
+// smallest first: each step's rounding goes with what has been added so far, and the
+// last state is off by 1.5e-7 instead of 1.4e-6 (bf16, 1000 tokens) ...
 template <typename T, int NB> __device__ __forceinline__ void mma_state(uint32_t tm, const void* k, const void* const (&w)[3]) {
     constexpr uint32_t desc = mma_desc<T>(128, PT, true, true);
     const uint32_t ka = smem_addr(k);
 #pragma unroll
-    for (int p = 0; p < kParts<T>; p++)
+    for (int p = kParts<T> - 1; p >= 0; p--)
 #pragma unroll
         for (int s = 0; s < C / 16; s++)
-            mma(tm, smem_desc(ka + s * 2048, NB == 2 ? 16384 : 0), smem_desc(smem_addr(w[p]) + s * 2048), desc, p + s > 0);
+            mma(tm, smem_desc(ka + s * 2048, NB == 2 ? 16384 : 0), smem_desc(smem_addr(w[p]) + s * 2048), desc, p < kParts<T> - 1 || s > 0);
 }
 // ... or side by side (w: the parts' tiles one after the other), which reads k once
 template <typename T, int NB> __device__ __forceinline__ void mma_state_wide(uint32_t tm, const void* k, const void* w) {
