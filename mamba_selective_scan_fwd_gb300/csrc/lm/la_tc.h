@@ -64,7 +64,7 @@ struct TcDir {
     const float* init;   // state before its first token, or null
     float* last;         // state after its last token, or null
     void* images;        // [Bsz, H, ptiles, chunks] images of the state before each chunk
-    float* image_scale;  // f16: the power of two each image was multiplied by
+    float* image_scale;  // f16: the power of two each image was multiplied by (infinite: the state is zero)
 };
 
 // A walk in one direction (dirs = 1: forward), or the backward's two at once:

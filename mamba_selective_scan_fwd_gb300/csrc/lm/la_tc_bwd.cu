@@ -17,7 +17,8 @@
 //
 // f16's range needs scales, powers of two that keep every operand's largest value
 // near 2^13: P has one, E, the scaled dy and the scaled v share one, H and R come
-// with theirs.  dq and dk of different heads then cannot add up in tensor memory:
+// with theirs (a zero H or R makes the dy or v that multiplies it zero, so that E alone
+// sets the scale).  dq and dk of different heads then cannot add up in tensor memory:
 // with f16 a block's work is one head's value tile, and all dq, dk are added up in
 // f32 by a kernel of their own.
 //

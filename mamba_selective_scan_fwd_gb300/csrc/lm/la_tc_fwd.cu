@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
             const uint32_t ph = (ch >> 1) & 1;
             if (!SUM) {
                 float sc = 1.0f;
+                bool none = false;
                 if (kF16<T>) {
                     uint32_t m;
                     asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(state_max(X))));
@@ -683,6 +684,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < 8; i++) m = max(m, s_most[i]);
                     sc = f16_scale(__uint_as_float(m));
+                    none = m == 0;
                 }
                 put_state<T, NB, kKeep, kImage>(image, sc, X);
                 fence_proxy_async_smem();
@@ -691,7 +693,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_tc_state(const __grid_cons
                     const int64_t at_image = ((b * a.H + h) * ((a.P + PT - 1) / PT) + at.pt) * w.chunks + start_of(ch) / C;
                     bulk_store(static_cast<char*>(at.dir(w).images) + at_image * (kImage * NB * 8192), image, kImage * NB * 8192);
                     bulk_commit();
-                    if (kF16<T>) at.dir(w).image_scale[at_image] = sc;
+                    // (a state of zeros gets an infinite scale: what multiplies it then counts for nothing)
+                    if (kF16<T>) at.dir(w).image_scale[at_image] = none ? __uint_as_float(0x7f800000u) : sc;
                 }
             }
             wait_or_fail(&s_u[s], ph, &s_fail);

@@ -55,3 +55,13 @@ def test_every_other_token_resets(io):
     x["g"][0, ::2, :] = -np.inf
     check_fwd(x, io)
     check_bwd(x, io)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [64, 128])
+def test_growth_near_the_documented_limit(N, io):
+    """128 tokens that add up to 57, of 60 that a chunk takes; the scale brings e^57 back into f16's range."""
+    x = ref.la_inputs(1, 128, 2, 1, N, 64, seed=61)
+    x["g"][:] = 0.45
+    check_fwd(x, io, scale=1e-24)
+    check_bwd(x, io, scale=1e-24)
