@@ -47,7 +47,7 @@ __device__ __forceinline__ Decay decay_of(float g) {
     const bool weak = g >= kWeakG;  // (NaN: no)
     return {weak ? expm1f(g) : expf(g), weak};
 }
-__device__ __forceinline__ float decayed(Decay d, float x) { return d.weak ? fmaf(d.by, x, x) : d.by * x; }
+__device__ __forceinline__ float decayed(Decay d, float x) { return fmaf(d.by, x, d.weak ? x : 0.0f); }
 
 // Cumulative log decays are kept as the unevaluated sum of two floats (Knuth's
 // two-sum): e^{c_i - c_j} of neighbouring tokens then stays exact to f32

@@ -16,7 +16,8 @@ template <int VEC> struct F;
 template <> struct F<4> { using T = float4; };
 template <> struct F<1> { using T = float; };
 
-template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128) k_step(StepArgs s) {
+// (wide tiles: five blocks an SM, at 96 registers; the narrow ones of small calls are left alone)
+template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128, LPR == 16 ? 5 : 0) k_step(StepArgs s) {
     constexpr int RP = 128 / LPR;  // state rows the block touches at once
     constexpr int NI = kMaxN / RP;
     constexpr int PT = LPR * VEC;
