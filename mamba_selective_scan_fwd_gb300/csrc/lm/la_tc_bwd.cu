@@ -13,7 +13,8 @@
 // each term of a 16-bit output); H and R enter in parts (kImageParts), and dg
 // takes everything else in f32.  c_i - c_j inside a run of 32
 // tokens is a difference of f32 sums over the run: exact to f32 rounding of the
-// run's decay (a reset to -128 in the run leaves its other tokens 2^-17).
+// run's decay without its resets, which no pair of tokens passes (with them in the sums
+// dg was off by 7e-5 where every other token resets).
 //
 // f16's range needs scales, powers of two that keep every operand's largest value
 // near 2^13: P has one, E, the scaled dy and the scaled v share one, H and R come
@@ -83,14 +84,18 @@ __device__ __forceinline__ void write_row(void* tile, int row, int quarter, cons
 // A chunk's decays for the compute warps, by runs of 32 tokens; c: log2 decay up
 // to and with the token.
 struct Decays {
-    float c[C];     // c since the run's start
+    float c[C];     // c since the run's start, without its resets
     float head[C];  // 2^ of it
     float tail[C];  // 2^(run's end - c)
     float up[C];    // scale 2^c
     float down[C];  // 2^(chunk's end - c)
     float skip[3];  // 2^ from the end of run r to the start of run cb: (r, cb) = (0, 2), (1, 3), (0, 3)
     float all;      // over the chunk
+    uint32_t resets[4];  // of each run, a bit a token
 };
+
+// Log decays from here on down are resets: e^g is zero in f32.
+constexpr float kResetG = -104.0f;
 
 // One warp; g: log decays of tokens 4 lane .. 4 lane + 3.
 __device__ __forceinline__ void put_decays(Decays& d, const float (&g)[4], float scale) {
@@ -103,12 +108,30 @@ __device__ __forceinline__ void put_decays(Decays& d, const float (&g)[4], float
     const auto at = [&](int l) { return Two{__shfl_sync(kFull, c[3].h, l), __shfl_sync(kFull, c[3].l, l)}; };
     const Two end = at(lane | 7), e0 = at(7), e1 = at(15), e2 = at(23), cl = at(31);
     const Two start = lane < 8 ? Two{0.0f, 0.0f} : (lane < 16 ? e0 : (lane < 24 ? e1 : e2));
+    float in = 0.0f, own[4];
+    uint32_t resets = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const bool reset = g[e] <= kResetG;
+        own[e] = in += reset ? 0.0f : x[e];
+        resets |= (uint32_t)reset << (4 * (lane & 7) + e);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        const float up = __shfl_up_sync(kFull, in, o);
+        if ((lane & 7) >= o) in += up;
+        resets |= __shfl_xor_sync(kFull, resets, o);
+    }
+    in = __shfl_up_sync(kFull, in, 1);  // of the lanes before
+    if ((lane & 7) == 0) {
+        in = 0.0f;
+        d.resets[lane >> 3] = resets;
+    }
 #pragma unroll
     for (int e = 0; e < 4; e++) {
         const int t = 4 * lane + e;
-        const float in = two_diff(c[e], start);
-        d.c[t] = in;
-        d.head[t] = ex2a(in);
+        d.c[t] = in + own[e];
+        d.head[t] = ex2a(two_diff(c[e], start));
         d.tail[t] = ex2a(two_diff(end, c[e]));
         d.up[t] = scale * ex2a(c[e].h + c[e].l);
         d.down[t] = ex2a(two_diff(cl, c[e]));
@@ -568,6 +591,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
                         use(j, mul2(mul2(f, t), sv), mul2(mul2(fs, t), make_float2(d[j], d[j + 1])), sv);
                     }
                 } else {
+                    if (dec.resets[run]) {  // nothing passes one
+                        const uint32_t after = dec.resets[run] & ~((2u << lane) - 1);
+                        const int stop = after ? __ffs(after) - 1 : 32;
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (j >= stop) s[j] = d[j] = 0.0f;
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float2 c = add2(*reinterpret_cast<const float2*>(&dec.c[32 * cb + j]), f);

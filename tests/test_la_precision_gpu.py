@@ -45,3 +45,18 @@ def test_f32_outputs(shape, io):
     print(io, shape, {n: f"{e:.1e}" for n, e in errors.items()})
     bounds = {n: dg_bound(io, shape[4]) if n == "dg" else 2.0 ** -20 for n in errors}
     assert not {n: e for n, e in errors.items() if not e <= bounds[n]}
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("every", [2, 3, 11, 100])
+def test_resets_cost_no_precision(every, io):
+    """Sequences packed into one row: dg, and dq, dk, dv where nothing is rounded to 16 bits."""
+    x = ref.la_inputs(1, 300, 4, 2, 64, 64, h0=True, seed=every)
+    x["g"][0, ::every, :] = -float("inf")
+    x["g"][0, 5::every, 1] = -110.0
+    t, r = on_gpu(x, io)
+    got = ss.ss_la_bwd(t["q"], t["k"], t["v"], t["g"], t["dy"], scale=0.125, h0=t["h0"], dlast_state=t["dlast"])
+    want = ref.la_bwd(r["q"], r["k"], r["v"], r["g"], r["dy"], 0.125, r["h0"], r["dlast"])
+    assert ss.device_status() == ss.SS_OK
+    for n in ("dg", "dq", "dk", "dv") if io == "f32" else ("dg",):
+        assert normwise(got[n], want[n]) <= (dg_bound(io, 64) if n == "dg" else 2.0 ** -20), n
