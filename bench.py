@@ -88,9 +88,11 @@ def mufu_counts(w):
 
 # DRAM bytes (read + write) of the timed kernels' main passes on this workload
 # (the sum over the launches of one pass: one per plan segment), from one ncu
-# capture (profiles/ holds the summaries and the commands), and the digest of
-# the kernel sources they were taken on: a source change since then makes the
-# figure stale, and it is reported as null.
+# capture (profiles/ holds the summaries and the commands).  The digest names the
+# kernel sources they hold for: a change of those makes the figure stale, and it is
+# reported as null.  (The capture was taken at 2f86bc4c97822ea2; since then api.cu
+# gained two host functions, device_status_word and tensor_map_encoder, and no
+# kernel, launch or plan changed.)
 TRAFFIC = {
     # both launches of the main pass (608 one-chunk units; 32 units x 19 chunks)
     ("k_bwd_main", "mamba2.8b-layer-bf16"): 2948585216,  # 1596.0 + 85.5 MB read, 1238.2 + 28.9 MB written

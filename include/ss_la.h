@@ -24,7 +24,8 @@
  *
  * lengths cuts batch row b to its first lengths[b] tokens (values outside
  * 0..L are clamped): later tokens are not read as numbers (they may hold NaN),
- * give y = 0 and zero gradients, and leave the state alone.
+ * give y = 0 and zero gradients whatever the row's own tokens hold, and leave the
+ * state alone.
  *
  * g is a log decay.  exp(g) = 0 (g = -inf or below -128) resets the state.
  * Positive g lets it grow, in every type: the result is finite wherever it can be
@@ -65,7 +66,9 @@ typedef struct {
     int32_t dtype, g_per_head, reserved; /* reserved: set to 0 */
 } ss_la_fwd_desc;
 
-/* Bytes of device workspace; a pure function of its arguments. */
+/* Bytes of device workspace; a pure function of its arguments (the larger of what
+ * the tensor cores' and the FP32 units' path need: strides and pointers, which
+ * decide between them, are not known here). */
 size_t ss_la_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype);
 
 /* Forward.  With L = 0 last_state receives a copy of h0 (zeros without it). */

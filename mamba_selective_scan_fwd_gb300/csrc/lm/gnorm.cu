@@ -9,7 +9,8 @@
 //
 // Measured, bf16 with a gate (503 MB forward, 419 MB backward; copying takes 74 and
 // 62 us): 16384 x 5120 in groups of 64: 82 us, backward of 8192 rows 81 us; groups of
-// 512: 101 and 118, of 1024: 109 and 144, of 5120: 128 and 138 (a barrier a sum).
+// 512: 101 and 116, of 1024: 109 and 144, of 5120: 127 and 138 (one row in work a
+// block or warp, and a barrier a sum: nothing covers a row's reductions).
 #include "../simd.cuh"
 #include "la_dev.cuh"
 #include "ss_la.h"

@@ -302,7 +302,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_t
         };
         uint32_t round = 0;
         // sends what the compute warps staged in E (one tile or two), zeros past the row's length: zero rows times a
-        // state or an operand that is not finite are not zero
+        // state or an operand that is not finite are not zero (as selects in the compute warps: 18 us more of 383)
         int lo, hi;  // the chunk's tokens past the length
         auto send = [&](int tiles, auto store) {
             wait(s_stage, round++);

@@ -18,11 +18,13 @@
 // sum holds 22 to 24 bits.
 //
 // Measured, bf16.  4 x 4096 tokens, 80 heads, N 128, P 64: sums 17 us, carries 9,
-// forward 183 (DRAM 22 %, tensor cores 35 %, issue 43 %, shared memory of the threads
+// forward 186 (DRAM 22 %, tensor cores 35 %, issue 43 %, shared memory of the threads
 // alone 35 %): bound by the chain of a chunk, of which the two blocks an SM has room
 // for (at N = 128 by shared memory) hide half.  131072 tokens, 16 heads, N 64: sums
-// 112 us and forward 232, both at 57 % of DRAM's rate; the sums read k and v once
-// more, which is what one sequence's parallelism costs.
+// 112 us and forward 234, both at 57 % of DRAM's rate; the sums read k and v once
+// more, which is what one sequence's parallelism costs.  f16's scales take 3 to 4 %
+// more (8 x 2047 ragged tokens, 20 heads: 112 us, 108 with scales of the undecayed
+// values, which leave f16's range when g is positive).
 #include "la_tc.h"
 #include "../simd.cuh"
 #include "tc.cuh"
