@@ -136,6 +136,15 @@ def lib() -> ctypes.CDLL:
     L.ss_gnorm_bwd_workspace_bytes.argtypes = [_I64] * 3 + [ctypes.c_int]
     L.ss_gnorm_bwd.restype = ctypes.c_int
     L.ss_gnorm_bwd.argtypes = [_P] * 9 + [_I64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, _P, _SZ, _P]
+    # include/ss_gdr.h (the descriptors are defined in delta_rule.py)
+    for fn in ("ss_gdr_fwd_workspace_bytes", "ss_gdr_bwd_workspace_bytes"):
+        getattr(L, fn).restype = _SZ
+        getattr(L, fn).argtypes = [_I64] * 6 + [ctypes.c_int]
+    L.ss_qknorm_bwd_workspace_bytes.restype = _SZ
+    L.ss_qknorm_bwd_workspace_bytes.argtypes = [_I64] * 5 + [ctypes.c_int]
+    for fn in ("ss_gdr_fwd", "ss_gdr_bwd", "ss_gdr_step", "ss_qknorm_fwd", "ss_qknorm_bwd"):
+        getattr(L, fn).restype = ctypes.c_int
+        getattr(L, fn).argtypes = [_P, _P]
     _lib = L
     return L
 

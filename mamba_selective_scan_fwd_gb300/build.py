@@ -24,9 +24,10 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 SOURCES = ["api.cu", "dispatch.cu", "fwd_f32.cu", "fwd_bf16.cu", "fwd_f16.cu", "bwd_f32.cu",
            "bwd_bf16.cu", "bwd_f16.cu", "decode.cu", "fwd_noalloc.cu", "probe.cu"]
-# linear attention and its output norm (include/ss_la.h): kernels of their own, in
-# a folder of their own, outside source_digest() (which identifies the scan's kernels)
-LM_SOURCES = ["lm/la_api.cu", "lm/la_f32.cu", "lm/la_tc_fwd.cu", "lm/la_tc_bwd.cu", "lm/la_step.cu", "lm/gnorm.cu"]
+# linear attention and its output norm (include/ss_la.h), the gated delta rule and the norm
+# of q and k (include/ss_gdr.h): kernels of their own, in a folder of their own, outside source_digest() (which identifies the scan's kernels)
+LM_SOURCES = ["lm/la_api.cu", "lm/la_f32.cu", "lm/la_tc_fwd.cu", "lm/la_tc_bwd.cu", "lm/la_step.cu", "lm/gnorm.cu",
+              "lm/gdr_api.cu", "lm/gdr_f32.cu", "lm/gdr_step.cu", "lm/qknorm.cu"]
 
 
 def nvcc() -> str:

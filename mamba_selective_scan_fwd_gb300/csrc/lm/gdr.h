@@ -1,0 +1,93 @@
+// Gated delta rule and q / k norm: arguments, plans and launches shared by the C
+// ABI (gdr_api.cu) and the kernels.
+#pragma once
+
+#include "la.h"
+
+namespace ss {
+namespace gdr {
+
+using la::In;
+using la::kMaxN;
+using la::kSms;
+
+struct Args {
+    In q, k, v, dy;          // dy: backward only
+    const float *g, *beta;   // [Bsz, L, H]; g may be null (no decay)
+    const float* h0;         // initial state, or null
+    const float* dlast;      // gradient of the last state, or null (backward)
+    const int32_t* lengths;  // [Bsz] or null
+    int64_t Bsz, L, H, G, N, P;
+    float scale;
+    int dtype;
+};
+
+constexpr int kChunk = 64;  // tokens whose pairs the backward forms (and the tensor cores' chunk)
+
+// ---------------------------------------------------------------- FP32 path
+constexpr int kWalkT = 16;  // tokens staged at a time
+// lanes that share a value channel's N states, 16 each, and value channels per block
+inline int walk_lanes(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
+inline int64_t walk_cols(int64_t N) { return 256 / walk_lanes(N); }
+
+enum WalkMode { kWalkY, kWalkKeep, kWalkBack };
+struct WalkArgs {
+    Args a;
+    const float* init;  // state (kWalkBack: adjoint) the walk starts from, or null
+    float* last;        // where its last one goes, or null
+    void* y;            // kWalkY: y; kWalkBack: dv
+    float* rows;        // kWalkKeep: v - e^g S^T k (u / beta); kWalkBack: x; f32 [Bsz, L, H, P]
+    float* states;      // kWalkKeep: before each chunk; kWalkBack: adjoint after it; f32 [Bsz, H, chunks, N, P]
+    int64_t chunks;
+    bool vec;           // runs of four values are whole and aligned
+};
+
+struct ChunkArgs {
+    Args a;
+    const float *miss, *x;         // the walks' rows
+    const float *before, *after;   // the walks' states
+    int64_t chunks;
+    void *dq, *dk;                 // io, when one head of v uses each head of q and k
+    float *dq_part, *dk_part;      // else f32 [H / G, Bsz, L, G, N]
+    float *dg, *dbeta;             // dg: may be null
+};
+
+cudaError_t launch_walk(const WalkArgs& w, WalkMode mode, cudaStream_t st);
+cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st);
+
+struct StepArgs {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    float* state;
+    const int32_t* slots;
+    void* y;
+    int64_t q_batch, k_batch, v_batch;
+    int64_t Bsz, H, G, N, P, pool;
+    float scale;
+    int dtype;
+};
+cudaError_t launch_step(const StepArgs& s, cudaStream_t st);
+
+// ---------------------------------------------------------------- q / k norm
+struct NormSide {  // q or k
+    In x, d;                 // d: gradient of the output (backward)
+    const float* weight;     // or null
+    void* out;               // forward: the output; backward: the gradient of x
+    float* dweight;          // backward, or null
+    int64_t heads;
+};
+struct NormArgs {
+    NormSide side[2];
+    const int32_t* positions;
+    const float* freqs;
+    float* part;             // backward: [blocks of q, then of k][N] partial sums of the weights' gradients
+    int64_t Bsz, L, N, pairs;
+    float eps;
+    int flags, dtype;
+};
+// Blocks of each side; a pure function of its arguments.
+int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N);
+cudaError_t launch_qknorm(const NormArgs& a, bool backward, cudaStream_t st);
+
+}  // namespace gdr
+}  // namespace ss

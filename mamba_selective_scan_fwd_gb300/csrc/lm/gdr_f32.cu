@@ -1,0 +1,549 @@
+// Gated delta rule on the FP32 units: every io type, any N <= 128, P and strides.
+// f32 inputs run here, and 16-bit inputs that the tensor-core path's rules exclude.
+//
+// Forward: the recurrence itself, token by token.  The columns of the state (value
+// channels) are independent, so a column's N values lie in the registers of N / 16
+// lanes and every token costs two sums over those lanes (S^T k, and S^T q off the
+// chain).  Backward: with x_t = R_t^T k_t, R_t the adjoint of S_t,
+//   R_t = (adjoint left by t + 1) + scale q_t dy_t^T,   adjoint left = e^{g_t} (R_t - beta_t k_t x_t^T)
+// a second walk of the same form from the last token gives x and the adjoints R at
+// the chunks' ends, the forward's walk the misses w_t = v_t - e^{g_t} S^T k_t
+// (u = beta w) and the states H at their starts.  With u and x known everything else
+// is products inside a chunk of 64 tokens (c_i: cumulative log decay, cl: its end):
+//   E_ij = scale e^{c_i - c_j} dy_i . u_j (j <= i),   F_ij = -beta_i e^{c_i - c_j} x_i . u_j (j < i)
+//   dq_i = scale e^{c_i} H dy_i + sum_j E_ij k_j
+//   dk_i = -beta_i e^{c_i} H x_i + sum_j F_ij k_j + e^{cl - c_i} R u_i + sum_j (E_ji q_j + F_ji k_j)
+//   dv_i = beta_i x_i,   dbeta_i = x_i . w_i
+//   dg_t = every path that crosses token t, by its two ends: sum_{i >= t} a_i + sum_{j < t} b_j
+//          + sum_{j < t <= i} (E_ij q_i . k_j + F_ij k_i . k_j) + e^{cl} <R, H>
+// a_i, b_j: the parts of q_i . dq_i + k_i . dk_i that come from H, of k_j . dk_j that go to R.
+#include "../simd.cuh"
+#include "gdr_dev.cuh"
+
+namespace ss {
+namespace gdr {
+namespace {
+
+using la::Decay;
+using la::Two;
+using la::two_diff;
+
+__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// Four adjacent values, of which `left` exist; vec: they exist together and are aligned.
+template <typename T> __device__ __forceinline__ float4 fetch4(const T* p, int64_t left, bool vec) {
+    float x[4] = {};
+    if (vec) {
+        if (left > 0) {
+            if constexpr (sizeof(T) == 4) return at4(p);
+            union {
+                uint2 m;
+                T t[4];
+            } u;
+            u.m = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[e] = ldf(&u.t[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = e < left ? ldf(p + e) : 0.0f;
+    }
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+template <int LN> __device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+    for (int o = LN / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float2 decayed2(Decay d, float2 x) {
+    return d.weak ? fma2(splat2(d.by), x, x) : mul2(splat2(d.by), x);
+}
+
+// One block: 256 / LN value channels of one head.  Lane (cg, ln): two adjacent
+// channels, the states n = 4 (ln + LN j) + e, j, e < 4, in pairs of e (runs of four
+// so that the lanes' reads of k and q are 16 bytes side by side).
+template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(128) k_walk(WalkArgs w) {
+    constexpr int NP = 16 * LN, PT = 256 / LN, TT = kWalkT;
+    constexpr int EK = NP * TT / 512 < 1 ? 1 : NP * TT / 512, EV = PT * TT / 512 < 1 ? 1 : PT * TT / 512;
+    __shared__ __align__(16) float s_k[TT][NP], s_q[TT][NP], s_v[TT][PT], s_o[TT][PT];
+    __shared__ float s_a[TT], s_beta[TT];
+    __shared__ uint32_t s_weak;
+    const Args& a = w.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane % LN, cg = lane / LN;
+    const int64_t ptiles = (a.P + PT - 1) / PT;
+    int64_t id = blockIdx.x;
+    const int64_t p0 = (id % ptiles) * PT;
+    id /= ptiles;
+    const int64_t h = id % a.H, b = id / a.H, hq = h / (a.H / a.G), bh = b * a.H + h;
+    const int N = (int)a.N, pleft = (int)min((int64_t)PT, a.P - p0);
+    const int col = (warp * (32 / LN) + cg) * 2;  // of the block's channels
+    const int64_t len = row_length(a, b), NPel = a.N * a.P;
+    const In& vin = MODE == kWalkBack ? a.dy : a.v;
+    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hq * a.N;
+    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
+    const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P + p0;
+
+    float2 S[2][8];  // [channel][2 j + e / 2]
+    auto state = [&](float* p, bool put) {  // p: the head's N x P
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int n = 4 * (ln + LN * (i / 2)) + 2 * (i & 1);
+                const bool ok = p && col + c < pleft;
+                float* q = p + n * a.P + p0 + col + c;
+                if (put) {
+                    if (ok && n < N) q[0] = S[c][i].x;
+                    if (ok && n + 1 < N) q[a.P] = S[c][i].y;
+                } else {
+                    S[c][i].x = ok && n < N ? q[0] : 0.0f;
+                    S[c][i].y = ok && n + 1 < N ? q[a.P] : 0.0f;
+                }
+            }
+    };
+    state(w.init ? const_cast<float*>(w.init) + bh * NPel : nullptr, false);
+
+    const int64_t tiles = (len + TT - 1) / TT;
+    auto start = [&](int64_t i) { return (MODE == kWalkBack ? tiles - 1 - i : i) * TT; };
+    float4 rk[EK], rq[EK], rv[EV];
+    float rg = 0.0f, rb = 0.0f;
+    auto fetch = [&](int64_t i) {
+        const int64_t t0 = start(i);
+        const int nv = (int)min((int64_t)TT, len - t0);
+#pragma unroll
+        for (int e = 0; e < EK; e++) {
+            const int x = tid + 128 * e, t = x / (NP / 4), n = x % (NP / 4) * 4, left = t < nv ? N - n : 0;
+            rk[e] = fetch4(kp + (t0 + t) * a.k.token + n, left, w.vec);
+            if (MODE != kWalkKeep) rq[e] = fetch4(qp + (t0 + t) * a.q.token + n, left, w.vec);
+        }
+#pragma unroll
+        for (int e = 0; e < EV; e++) {
+            const int x = tid + 128 * e, t = x / (PT / 4), c = x % (PT / 4) * 4;
+            rv[e] = fetch4(vp + (t0 + t) * vin.token + c, t < nv ? pleft - c : 0, w.vec);
+        }
+        if (tid < TT) {
+            rg = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
+            rb = tid < nv ? a.beta[(b * a.L + t0 + tid) * a.H + h] : 0.0f;
+        }
+    };
+    if (tiles > 0) fetch(0);
+    for (int64_t i = 0; i < tiles; i++) {
+        const int64_t t0 = start(i);
+        const int nv = (int)min((int64_t)TT, len - t0);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EK; e++)
+            if (tid + 128 * e < TT * NP / 4) {
+                reinterpret_cast<float4*>(s_k)[tid + 128 * e] = rk[e];
+                if (MODE != kWalkKeep) {
+                    const float f = MODE == kWalkBack ? a.scale : 1.0f;
+                    reinterpret_cast<float4*>(s_q)[tid + 128 * e] = make_float4(f * rq[e].x, f * rq[e].y, f * rq[e].z, f * rq[e].w);
+                }
+            }
+#pragma unroll
+        for (int e = 0; e < EV; e++)
+            if (tid + 128 * e < TT * PT / 4) reinterpret_cast<float4*>(s_v)[tid + 128 * e] = rv[e];
+        if (warp == 0) {
+            const Decay d = la::decay_of(lane < TT ? rg : 0.0f);
+            const uint32_t weak = __ballot_sync(kFull, d.weak);
+            if (lane < TT) {
+                s_a[lane] = d.by;
+                s_beta[lane] = rb;
+            }
+            if (lane == 0) s_weak = weak;
+        }
+        __syncthreads();
+        if (i + 1 < tiles) fetch(i + 1);
+        // the state before a chunk's first token, the adjoint after its last one
+        if (MODE == kWalkKeep ? t0 % kChunk == 0 : MODE == kWalkBack && (i == 0 || (t0 + TT) % kChunk == 0))
+            state(w.states + (bh * w.chunks + t0 / kChunk) * NPel, true);
+        const uint32_t weak = s_weak;
+#pragma unroll 1
+        for (int u = 0; u < nv; u++) {
+            const int t = MODE == kWalkBack ? nv - 1 - u : u;
+            const Decay d = {s_a[t], (weak >> t & 1) != 0};
+            const float beta = s_beta[t];
+            const float2 v = *reinterpret_cast<const float2*>(&s_v[t][col]);
+            float2 k[8], q[8];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float4 kk = at4(&s_k[t][4 * (ln + LN * j)]);
+                k[2 * j] = make_float2(kk.x, kk.y);
+                k[2 * j + 1] = make_float2(kk.z, kk.w);
+                if (MODE != kWalkKeep) {
+                    const float4 qq = at4(&s_q[t][4 * (ln + LN * j)]);
+                    q[2 * j] = make_float2(qq.x, qq.y);
+                    q[2 * j + 1] = make_float2(qq.z, qq.w);
+                }
+            }
+            float out[2];
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const float vc = c ? v.y : v.x;
+                float2 acc[2] = {};
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    S[c][j] = MODE == kWalkBack ? fma2(q[j], splat2(vc), S[c][j]) : decayed2(d, S[c][j]);
+                    acc[j & 1] = fma2(k[j], S[c][j], acc[j & 1]);
+                }
+                acc[0] = add2(acc[0], acc[1]);
+                const float dot = lane_sum<LN>(acc[0].x + acc[0].y);
+                const float miss = vc - dot;
+                out[c] = MODE == kWalkBack ? dot : miss;
+                const float2 by = splat2(MODE == kWalkBack ? -beta * dot : beta * miss);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    S[c][j] = fma2(k[j], by, S[c][j]);
+                    if (MODE == kWalkBack) S[c][j] = decayed2(d, S[c][j]);
+                }
+                if (MODE == kWalkY) {
+                    float2 y[2] = {};
+#pragma unroll
+                    for (int j = 0; j < 8; j++) y[j & 1] = fma2(q[j], S[c][j], y[j & 1]);
+                    y[0] = add2(y[0], y[1]);
+                    out[c] = a.scale * lane_sum<LN>(y[0].x + y[0].y);
+                }
+            }
+            if (ln == 0) *reinterpret_cast<float2*>(&s_o[t][col]) = make_float2(out[0], out[1]);
+        }
+        __syncthreads();
+        const int64_t row0 = ((b * a.L + t0) * a.H + h) * a.P + p0;
+#pragma unroll
+        for (int u = 0; u < TT * PT / 128; u++) {
+            const int e = tid + 128 * u, t = e / PT, c = e % PT;
+            if (t < nv && c < pleft) {
+                const int64_t at = row0 + t * a.H * a.P + c;
+                const float x = s_o[t][c];
+                if (MODE != kWalkY) w.rows[at] = x;
+                if (MODE != kWalkKeep) st(static_cast<T*>(w.y) + at, MODE == kWalkBack ? s_beta[t] * x : x);
+            }
+        }
+    }
+    if (MODE != kWalkKeep)  // rows that do not count
+        for (int64_t t = len + tid / 32; t < a.L; t += 4)
+            for (int c = lane; c < pleft; c += 32) st(static_cast<T*>(w.y) + ((b * a.L + t) * a.H + h) * a.P + p0 + c, 0.0f);
+    if (w.last) state(w.last + bh * NPel, true);
+}
+
+// ---------------------------------------------------------------- one chunk of one head
+constexpr int C = kChunk;
+constexpr int kPT = 64;  // value channels per pass
+constexpr int kLdP = kPT + 4;
+
+template <int NB> struct ChunkSmem {
+    static constexpr int NP = NB * 16, LD = NP + 4;
+    float q[C][LD], k[C][LD];
+    float u[C][kLdP], dy[C][kLdP], x[C][kLdP];  // after the last pass: E in dy, F in x
+    float H[NP][kLdP], R[NP][kLdP];
+    Two c[C];
+    float beta[C], a[C], b[C], db[C], col[8][C], red[8];
+};
+
+// Thread (ty, tx) of 16 x 16: rows 4 ty + r and columns tx + 16 n of the products with
+// H, R, q, k; rows ty + 16 r and columns tx + 16 c of the 64 x 64 scores.
+template <typename T, int NB> __global__ void __launch_bounds__(256) k_chunk(ChunkArgs w) {
+    extern __shared__ __align__(16) char raw[];
+    using Sm = ChunkSmem<NB>;
+    Sm& s = *reinterpret_cast<Sm*>(raw);
+    constexpr int NP = Sm::NP;
+    const Args& a = w.a;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
+    int64_t id = blockIdx.x;
+    const int64_t h = id % a.H;
+    id /= a.H;
+    const int64_t chunk = id % w.chunks, b = id / w.chunks, rep = a.H / a.G, hq = h / rep;
+    const int64_t t0 = chunk * C, len = row_length(a, b);
+    const int nt = (int)min((int64_t)C, a.L - t0);
+    const int nv = (int)max((int64_t)0, min((int64_t)nt, len - t0));
+
+    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + t0 * a.q.token + hq * a.N;
+    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + t0 * a.k.token + hq * a.N;
+#pragma unroll 8
+    for (int u = 0; u < C * NP / 256; u++) {
+        const int e = tid + 256 * u, t = e / NP, n = e % NP;
+        const bool on = t < nv && n < a.N;
+        s.q[t][n] = on ? ldf(qp + t * a.q.token + n) : 0.0f;
+        s.k[t][n] = on ? ldf(kp + t * a.k.token + n) : 0.0f;
+    }
+    if (warp == 0) {
+        float g[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const int t = lane * 2 + e;
+            g[e] = t < nv ? log_decay(a, b, t0 + t, h) * la::kLog2e : 0.0f;
+            s.beta[t] = t < nv ? a.beta[(b * a.L + t0 + t) * a.H + h] : 0.0f;
+        }
+        Two c[2];
+        la::warp_cumsum<2>(g, c);
+        s.c[lane * 2] = c[0];
+        s.c[lane * 2 + 1] = c[1];
+    } else if (tid >= 64 && tid < 64 + C) {
+        s.a[tid - 64] = s.b[tid - 64] = s.db[tid - 64] = 0.0f;
+    }
+    float through = 0.0f;
+    float eu[4][4] = {}, fu[4][4] = {};                // dy . u, x . u
+    float hd[4][NB] = {}, hx[4][NB] = {}, ru[4][NB] = {};  // H dy, H x, R u
+    for (int64_t p0 = 0; p0 < a.P; p0 += kPT) {
+        __syncthreads();
+        const T* yp = static_cast<const T*>(a.dy.p) + b * a.dy.batch + t0 * a.dy.token + h * a.P + p0;
+        const int64_t row0 = ((b * a.L + t0) * a.H + h) * a.P + p0;
+#pragma unroll 2
+        for (int u = 0; u < C / 8; u++) {
+            const int t = warp + 8 * u;
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int p = lane + 32 * e;
+                const bool on = t < nv && p0 + p < a.P;
+                const float m = on ? w.miss[row0 + t * a.H * a.P + p] : 0.0f, x = on ? w.x[row0 + t * a.H * a.P + p] : 0.0f;
+                s.u[t][p] = s.beta[t] * m;
+                s.x[t][p] = x;
+                s.dy[t][p] = on ? ldf(yp + t * a.dy.token + p) : 0.0f;
+                sum = fmaf(m, x, sum);
+            }
+            sum = lane_sum<32>(sum);
+            if (lane == 0) s.db[t] += sum;
+        }
+        const int64_t at = ((b * a.H + h) * w.chunks + chunk) * a.N * a.P + p0;
+#pragma unroll 8
+        for (int u = 0; u < NP * kPT / 256; u++) {
+            const int e = tid + 256 * u, n = e / kPT, p = e % kPT;
+            const bool on = nv > 0 && n < a.N && p0 + p < a.P;
+            const float hv = on ? w.before[at + n * a.P + p] : 0.0f, rv = on ? w.after[at + n * a.P + p] : 0.0f;
+            s.H[n][p] = hv;
+            s.R[n][p] = rv;
+            through = fmaf(hv, rv, through);
+        }
+        __syncthreads();
+        for (int p = 0; p < kPT; p += 4) {
+            float4 yv[4], xv[4], uv[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) yv[r] = at4(&s.dy[ty + 16 * r][p]), xv[r] = at4(&s.x[ty + 16 * r][p]), uv[r] = at4(&s.u[tx + 16 * r][p]);
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    eu[r][c] = fmaf(yv[r].x, uv[c].x, fmaf(yv[r].y, uv[c].y, fmaf(yv[r].z, uv[c].z, fmaf(yv[r].w, uv[c].w, eu[r][c]))));
+                    fu[r][c] = fmaf(xv[r].x, uv[c].x, fmaf(xv[r].y, uv[c].y, fmaf(xv[r].z, uv[c].z, fmaf(xv[r].w, uv[c].w, fu[r][c]))));
+                }
+        }
+        for (int p = 0; p < kPT; p += 4) {
+            float4 yv[4], xv[4], uv[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) yv[r] = at4(&s.dy[4 * ty + r][p]), xv[r] = at4(&s.x[4 * ty + r][p]), uv[r] = at4(&s.u[4 * ty + r][p]);
+#pragma unroll
+            for (int n = 0; n < NB; n++) {
+                const float4 hv = at4(&s.H[tx + 16 * n][p]), rv = at4(&s.R[tx + 16 * n][p]);
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    hd[r][n] = fmaf(yv[r].x, hv.x, fmaf(yv[r].y, hv.y, fmaf(yv[r].z, hv.z, fmaf(yv[r].w, hv.w, hd[r][n]))));
+                    hx[r][n] = fmaf(xv[r].x, hv.x, fmaf(xv[r].y, hv.y, fmaf(xv[r].z, hv.z, fmaf(xv[r].w, hv.w, hx[r][n]))));
+                    ru[r][n] = fmaf(uv[r].x, rv.x, fmaf(uv[r].y, rv.y, fmaf(uv[r].z, rv.z, fmaf(uv[r].w, rv.w, ru[r][n]))));
+                }
+            }
+        }
+    }
+    float qk[4][4] = {}, kk[4][4] = {};
+    for (int n = 0; n < NP; n += 4) {
+        float4 qv[4], ki[4], kj[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++) qv[r] = at4(&s.q[ty + 16 * r][n]), ki[r] = at4(&s.k[ty + 16 * r][n]), kj[r] = at4(&s.k[tx + 16 * r][n]);
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                qk[r][c] = fmaf(qv[r].x, kj[c].x, fmaf(qv[r].y, kj[c].y, fmaf(qv[r].z, kj[c].z, fmaf(qv[r].w, kj[c].w, qk[r][c]))));
+                kk[r][c] = fmaf(ki[r].x, kj[c].x, fmaf(ki[r].y, kj[c].y, fmaf(ki[r].z, kj[c].z, fmaf(ki[r].w, kj[c].w, kk[r][c]))));
+            }
+    }
+    __syncthreads();  // the last pass's tiles are read
+    {
+        float col[4] = {};
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int i = ty + 16 * r;
+            float row = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const int j = tx + 16 * c;
+                const float m = j <= i ? la::ex2(two_diff(s.c[i], s.c[j])) : 0.0f;
+                const float e = a.scale * m * eu[r][c], f = j < i ? -s.beta[i] * m * fu[r][c] : 0.0f;
+                s.dy[i][j] = e;
+                s.x[i][j] = f;
+                const float x = j < i ? fmaf(e, qk[r][c], f * kk[r][c]) : 0.0f;
+                row += x;
+                col[c] += x;
+            }
+            row = lane_sum<16>(row);
+            if (tx == 0) s.b[i] -= row;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            col[c] += __shfl_xor_sync(kFull, col[c], 16);
+            if (lane < 16) s.col[warp][tx + 16 * c] = col[c];
+        }
+    }
+    __syncthreads();
+    if (tid < C) {
+        float x = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; u++) x += s.col[u][tid];
+        s.b[tid] += x;
+    }
+    __syncthreads();
+    const Two cl = s.c[C - 1];
+    float dq[4][NB], dk[4][NB];
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        const int i = 4 * ty + r;
+        const float up = la::ex2(s.c[i].h + s.c[i].l), down = la::ex2(two_diff(cl, s.c[i])), beta = s.beta[i];
+        float ai = 0.0f, bi = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const int m = tx + 16 * n;
+            dq[r][n] = a.scale * up * hd[r][n];
+            const float in = -beta * up * hx[r][n], to = down * ru[r][n];
+            dk[r][n] = in + to;
+            ai = fmaf(s.q[i][m], dq[r][n], fmaf(s.k[i][m], in, ai));
+            bi = fmaf(s.k[i][m], to, bi);
+        }
+        ai = lane_sum<16>(ai);
+        bi = lane_sum<16>(bi);
+        if (tx == 0) {
+            s.a[i] = ai;
+            s.b[i] += bi;
+        }
+    }
+    for (int j = 0; j < C; j += 4) {  // E k, F k: rows i of E, F
+        float4 e[4], f[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++) e[r] = at4(&s.dy[4 * ty + r][j]), f[r] = at4(&s.x[4 * ty + r][j]);
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const int m = tx + 16 * n;
+            const float k0 = s.k[j][m], k1 = s.k[j + 1][m], k2 = s.k[j + 2][m], k3 = s.k[j + 3][m];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                dq[r][n] = fmaf(e[r].x, k0, fmaf(e[r].y, k1, fmaf(e[r].z, k2, fmaf(e[r].w, k3, dq[r][n]))));
+                dk[r][n] = fmaf(f[r].x, k0, fmaf(f[r].y, k1, fmaf(f[r].z, k2, fmaf(f[r].w, k3, dk[r][n]))));
+            }
+        }
+    }
+#pragma unroll 2
+    for (int i = 0; i < C; i++) {  // E^T q, F^T k: columns
+        const float4 e = at4(&s.dy[i][4 * ty]), f = at4(&s.x[i][4 * ty]);
+        const float es[4] = {e.x, e.y, e.z, e.w}, fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const float q = s.q[i][tx + 16 * n], k = s.k[i][tx + 16 * n];
+#pragma unroll
+            for (int r = 0; r < 4; r++) dk[r][n] = fmaf(es[r], q, fmaf(fs[r], k, dk[r][n]));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        const int t = 4 * ty + r;
+        if (t >= nt) continue;
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const int c = tx + 16 * n;
+            if (c >= a.N) continue;
+            const int64_t at = ((b * a.L + t0 + t) * a.G + hq) * a.N + c;
+            const float x = t < nv ? dq[r][n] : 0.0f, z = t < nv ? dk[r][n] : 0.0f;
+            if (rep > 1) {
+                const int64_t part = (h % rep) * a.Bsz * a.L * a.G * a.N + at;
+                w.dq_part[part] = x;
+                w.dk_part[part] = z;
+            } else {
+                st(static_cast<T*>(w.dq) + at, x);
+                st(static_cast<T*>(w.dk) + at, z);
+            }
+        }
+    }
+    through = lane_sum<32>(through);
+    if (lane == 0) s.red[warp] = through;
+    __syncthreads();
+    if (warp == 0) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; u++) sum += s.red[u];
+        sum *= la::ex2(cl.h + cl.l);
+        const int t = 2 * lane;
+        const float a0 = s.a[t], a1 = s.a[t + 1], b0 = s.b[t], b1 = s.b[t + 1];
+        float A = a0 + a1, B = b0 + b1;  // suffix of a, prefix of b over lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_down_sync(kFull, A, o), y = __shfl_up_sync(kFull, B, o);
+            if (lane + o < 32) A += x;
+            if (lane >= o) B += y;
+        }
+        const float Bx = __shfl_up_sync(kFull, B, 1), Ax = __shfl_down_sync(kFull, A, 1);
+        const float pre = lane > 0 ? Bx : 0.0f, suf = lane < 31 ? Ax : 0.0f;
+        const float g[2] = {(a0 + a1 + suf) + pre + sum, (a1 + suf) + (pre + b0) + sum};
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+            if (t + e < nt) {
+                const int64_t at = (b * a.L + t0 + t + e) * a.H + h;
+                if (w.dg) w.dg[at] = t + e < nv ? g[e] : 0.0f;
+                w.dbeta[at] = t + e < nv ? s.db[t + e] : 0.0f;
+            }
+    }
+}
+
+template <typename T, int LN> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+    const unsigned grid = (unsigned)(ceil_div(w.a.P, 256 / LN) * w.a.H * w.a.Bsz);
+    if (mode == kWalkY) k_walk<T, LN, kWalkY><<<grid, 128, 0, st>>>(w);
+    else if (mode == kWalkKeep) k_walk<T, LN, kWalkKeep><<<grid, 128, 0, st>>>(w);
+    else k_walk<T, LN, kWalkBack><<<grid, 128, 0, st>>>(w);
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t walk_io(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+    switch (walk_lanes(w.a.N)) {
+        case 1: return walk_mode<T, 1>(w, mode, st);
+        case 2: return walk_mode<T, 2>(w, mode, st);
+        case 4: return walk_mode<T, 4>(w, mode, st);
+        default: return walk_mode<T, 8>(w, mode, st);
+    }
+}
+
+template <typename T, int NB> cudaError_t chunk_n(const ChunkArgs& c, cudaStream_t st) {
+    const int bytes = (int)sizeof(ChunkSmem<NB>);
+    const cudaError_t e = la::allow_smem<k_chunk<T, NB>>(bytes);
+    if (e != cudaSuccess) return e;
+    k_chunk<T, NB><<<(unsigned)(c.a.Bsz * c.chunks * c.a.H), 256, bytes, st>>>(c);
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t chunk_io(const ChunkArgs& c, cudaStream_t st) {
+    if (c.a.N <= 32) return chunk_n<T, 2>(c, st);
+    if (c.a.N <= 64) return chunk_n<T, 4>(c, st);
+    return chunk_n<T, 8>(c, st);
+}
+
+// Whether every run of four values of q, k, v, dy is whole and aligned.
+bool fours(const Args& a) {
+    const uintptr_t bytes = a.dtype == 0 ? 16 : 8;
+    for (const In* x : {&a.q, &a.k, &a.v, &a.dy})
+        if (reinterpret_cast<uintptr_t>(x->p) % bytes != 0 || x->token % 4 != 0 || x->batch % 4 != 0) return false;
+    return a.N % 4 == 0 && a.P % 4 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_walk(const WalkArgs& args, WalkMode mode, cudaStream_t st) {
+    WalkArgs w = args;
+    w.vec = fours(w.a);
+    if (w.a.dtype == 0) return walk_io<float>(w, mode, st);
+    if (w.a.dtype == 1) return walk_io<__half>(w, mode, st);
+    return walk_io<__nv_bfloat16>(w, mode, st);
+}
+
+cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st) {
+    if (c.a.dtype == 0) return chunk_io<float>(c, st);
+    if (c.a.dtype == 1) return chunk_io<__half>(c, st);
+    return chunk_io<__nv_bfloat16>(c, st);
+}
+
+}  // namespace gdr
+}  // namespace ss
