@@ -31,7 +31,9 @@ EXPORTS = ["ss_fwd", "ss_bwd", "ss_fwd_workspace_bytes", "ss_bwd_workspace_bytes
            "ss_measure_fma_rate",
            "ss_la_fwd_workspace_bytes", "ss_la_fwd", "ss_la_bwd_workspace_bytes", "ss_la_bwd", "ss_la_step",
            "ss_la_selftest_wait_timeout",
-           "ss_gnorm_fwd", "ss_gnorm_bwd_workspace_bytes", "ss_gnorm_bwd"]
+           "ss_gnorm_fwd", "ss_gnorm_bwd_workspace_bytes", "ss_gnorm_bwd",
+           "ss_gdr_fwd_workspace_bytes", "ss_gdr_fwd", "ss_gdr_bwd_workspace_bytes", "ss_gdr_bwd", "ss_gdr_step",
+           "ss_qknorm_fwd", "ss_qknorm_bwd_workspace_bytes", "ss_qknorm_bwd"]
 ABI_VERSION = 7
 
 # Size of the library-owned scratch behind ss_fwd_noalloc (SS_FWD_NOALLOC_MAX_SCRATCH_BYTES).
