@@ -1,6 +1,9 @@
 // C ABI of the gated delta rule and the q / k norm (include/ss_gdr.h).  Everything is
 // checked before the first CUDA call; on error nothing is written.
+#include <cuda.h>
+
 #include "gdr.h"
+#include "gdr_tc.h"
 #include "ss_gdr.h"
 
 using namespace ss;
@@ -53,6 +56,117 @@ Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     return b;
 }
 
+// ---------------------------------------------------------------- tensor-core path
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// [Bsz, L, heads, width] of 16-bit values as a map {width, heads, L, Bsz}, boxes of 64 columns
+// by 64 tokens in the 128-byte swizzle; what lies outside reads as zero.
+bool tc_map(EncodeTiledFn encode, CUtensorMap* m, const In& x, int64_t heads, int64_t width, int64_t L, int64_t Bsz, int dtype) {
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)Bsz};
+    // the stride of a dimension of one is never used, but has to be valid
+    const int64_t token = L > 1 ? x.token : heads * width, batch = Bsz > 1 ? x.batch : heads * width;
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)token * 2, (cuuint64_t)batch * 2};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)kChunk, 1}, step[4] = {1, 1, 1, 1};
+    return encode(m, dtype == SS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x.p),
+                  dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether these sizes may run on the tensor cores (their inputs too, if tc_input says so).
+bool tc_sizes(int64_t L, int64_t N, int64_t P, int dtype) { return dtype != SS_F32 && N % 8 == 0 && P % 8 == 0 && L < (1ll << 31); }
+
+// TMA's rules on an input: 16-byte units everywhere.
+bool tc_input(const In& x, int64_t L, int64_t Bsz) {
+    if (misaligned16(x.p)) return false;
+    if (L > 1 && (x.token % 8 != 0 || x.token < 8 || x.token >= (1ll << 38))) return false;
+    return Bsz <= 1 || (x.batch % 8 == 0 && x.batch >= 8 && x.batch < (1ll << 38));
+}
+
+// Segments that the walks over time are cut into: where there are fewer (batch row, head, value
+// tile) units than SMs, or a last round of them leaves SMs idle.  Costs in chunks walked by one
+// block: the walk itself, the segments' two sums before it, two a segment for the carry, four for
+// the launches.
+TcPlan tc_plan(int64_t heads, int64_t ptiles, int64_t chunks) {
+    auto rounds = [](int64_t blocks) { return ceil_div(blocks, kSms); };
+    TcPlan best = {1, chunks};
+    double least = (double)(rounds(heads * ptiles) * chunks);
+    for (int64_t K = 2; K <= 128 && 2 * K <= chunks; K++) {
+        const int64_t per = ceil_div(chunks, K);
+        if (ceil_div(chunks, per) != K) continue;
+        const double cost = (double)((rounds(heads * ptiles * K) + rounds(heads * (ptiles + 1) * (K - 1))) * per + 2 * K + 4);
+        if (cost < 0.95 * least) {
+            least = cost;
+            best = {K, per};
+        }
+    }
+    return best;
+}
+
+struct FwdTc {
+    TcPlan plan;
+    int64_t chunks;
+    size_t images, state, phi;
+};
+FwdTc fwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dtype) {
+    FwdTc f;
+    f.chunks = ceil_div(L, kChunk);
+    f.plan = tc_plan(Bsz * H, ceil_div(P, kTileP), f.chunks);
+    f.images = l.take((size_t)Bsz * H * f.chunks * image_bytes(fwd_parts(dtype)));
+    const bool cut = f.plan.K > 1;
+    f.state = l.take(cut ? (size_t)Bsz * H * f.plan.K * N * P * 4 : 0);
+    f.phi = l.take(cut ? (size_t)Bsz * H * f.plan.K * N * N * 4 : 0);
+    return f;
+}
+
+// Blocks a group's heads are divided into by the first kernel: until there are two for each place on
+// the SMs.
+int prep_splits(int64_t blocks, int64_t rep) {
+    int64_t s = ceil_div(4 * kSms, blocks);
+    if (s > rep) s = rep;
+    return (int)(s < 1 ? 1 : s);
+}
+
+// Forward on the tensor cores; *ran tells whether the inputs allow it.
+int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, bool* ran) {
+    *ran = false;
+    if (!tc_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) || !tc_input(a.v, a.L, a.Bsz))
+        return SS_OK;
+    const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!encode) return SS_OK;
+    Layout l;
+    const FwdTc f = fwdtc_layout(l, a.Bsz, a.L, a.H, a.N, a.P, a.dtype);
+    TcWalkArgs w = {};
+    const In yo = {y, a.H * a.P, a.L * a.H * a.P};
+    if (!tc_map(encode, &w.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) || !tc_map(encode, &w.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &w.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) || !tc_map(encode, &w.y, yo, a.H, a.P, a.L, a.Bsz, a.dtype))
+        return SS_OK;
+    const int rc = device_status_word(&w.status);
+    if (rc != SS_OK) return rc;
+    *ran = true;
+    PrepArgs p = {};
+    p.q = w.q;
+    p.k = w.k;
+    p.a = a;
+    p.chunks = f.chunks;
+    p.splits = prep_splits(a.Bsz * f.chunks * a.G, a.H / a.G);
+    p.images = ws + f.images;
+    p.status = w.status;
+    w.a = a;
+    w.plan = f.plan;
+    w.chunks = f.chunks;
+    w.images = p.images;
+    w.init = a.h0;
+    w.last = last;
+    w.seg_state = reinterpret_cast<float*>(ws + f.state);
+    w.seg_phi = reinterpret_cast<float*>(ws + f.phi);
+    w.yp = y;
+    if (launch_prep(p, fwd_parts(a.dtype), st) != cudaSuccess) return SS_ERR_CUDA;
+    if (w.plan.K > 1 && (launch_tc_walk(w, kTcSum, st) != cudaSuccess || launch_tc_carry(w, st) != cudaSuccess)) return SS_ERR_CUDA;
+    return launch_tc_walk(w, kTcY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
 // The state that no token changes: a copy of the incoming one, or zeros.
 int pass_state(float* to, const float* from, int64_t Bsz, int64_t H, int64_t N, int64_t P, cudaStream_t st) {
     const size_t bytes = (size_t)Bsz * H * N * P * 4;
@@ -103,8 +217,10 @@ template <typename D> NormArgs norm_args(const D& d) {
 extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
-    if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
-    return 0;
+    if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L) || !tc_sizes(L, N, P, dtype)) return 0;
+    Layout l;
+    fwdtc_layout(l, Bsz, L, H, N, P, dtype);
+    return l.total;
 }
 
 int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
@@ -121,6 +237,9 @@ int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
     const size_t need = ss_gdr_fwd_workspace_bytes(d->Bsz, d->L, d->H, d->G, d->N, d->P, d->dtype);
     if (d->workspace_bytes < need || (need > 0 && !d->workspace)) return SS_ERR_WORKSPACE_TOO_SMALL;
     const Args a = args_of(*d);
+    bool ran;
+    const int tc = tc_forward(a, d->y, d->last_state, static_cast<char*>(d->workspace), st, &ran);
+    if (ran || tc != SS_OK) return tc;
     WalkArgs w = {};
     w.a = a;
     w.init = a.h0;
