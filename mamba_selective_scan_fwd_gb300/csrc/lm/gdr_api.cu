@@ -107,12 +107,13 @@ TcPlan tc_plan(int64_t heads, int64_t ptiles, int64_t chunks) {
 struct FwdTc {
     TcPlan plan;
     int64_t chunks;
-    size_t images, state, phi;
+    size_t keys, images, state, phi;
 };
-FwdTc fwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P, int dtype) {
+FwdTc fwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     FwdTc f;
     f.chunks = ceil_div(L, kChunk);
     f.plan = tc_plan(Bsz * H, ceil_div(P, kTileP), f.chunks);
+    f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
     f.images = l.take((size_t)Bsz * H * f.chunks * image_bytes(fwd_parts(dtype)));
     const bool cut = f.plan.K > 1;
     f.state = l.take(cut ? (size_t)Bsz * H * f.plan.K * N * P * 4 : 0);
@@ -136,26 +137,26 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (!encode) return SS_OK;
     Layout l;
-    const FwdTc f = fwdtc_layout(l, a.Bsz, a.L, a.H, a.N, a.P, a.dtype);
+    const FwdTc f = fwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P, a.dtype);
     TcWalkArgs w = {};
+    PrepArgs p = {};
     const In yo = {y, a.H * a.P, a.L * a.H * a.P};
-    if (!tc_map(encode, &w.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) || !tc_map(encode, &w.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+    if (!tc_map(encode, &p.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) || !tc_map(encode, &p.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
         !tc_map(encode, &w.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) || !tc_map(encode, &w.y, yo, a.H, a.P, a.L, a.Bsz, a.dtype))
         return SS_OK;
     const int rc = device_status_word(&w.status);
     if (rc != SS_OK) return rc;
     *ran = true;
-    PrepArgs p = {};
-    p.q = w.q;
-    p.k = w.k;
     p.a = a;
     p.chunks = f.chunks;
     p.splits = prep_splits(a.Bsz * f.chunks * a.G, a.H / a.G);
+    p.keys = ws + f.keys;
     p.images = ws + f.images;
     p.status = w.status;
     w.a = a;
     w.plan = f.plan;
     w.chunks = f.chunks;
+    w.keys = p.keys;
     w.images = p.images;
     w.init = a.h0;
     w.last = last;
@@ -219,7 +220,7 @@ extern "C" {
 size_t ss_gdr_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L) || !tc_sizes(L, N, P, dtype)) return 0;
     Layout l;
-    fwdtc_layout(l, Bsz, L, H, N, P, dtype);
+    fwdtc_layout(l, Bsz, L, H, G, N, P, dtype);
     return l.total;
 }
 

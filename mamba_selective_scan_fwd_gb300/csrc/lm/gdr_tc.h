@@ -17,19 +17,29 @@ namespace gdr {
 constexpr int kTileP = 128;  // value channels per block: the lanes of tensor memory
 constexpr int kTileBytes = 8192;  // 64 rows of 64 16-bit values
 
-// An image: tiles of 64 x 64 (128-byte rows, swizzled as TMA would): M in two bf16 parts,
-// P in `parts` bf16 parts, then the chunk's factors.
+// All operands that the kernels make are f16: two parts of one, scaled by a power of two, hold
+// 22 bits (bf16's two hold 16).  So q and k become f16 once, scaled alike: every bf16 value
+// within 2^27 of its tile's largest stays exact.  Tiles are 64 rows of 64 values in 128-byte rows,
+// swizzled as TMA would.
+//
+// Keys: per (batch row, chunk, head of q and k), for each 64 columns a tile of K and one of Q,
+// rows past the row's length zero.
+constexpr int key_bytes(int64_t N) { return (N > 64 ? 4 : 2) * kTileBytes; }
+// Image: per (batch row, head, chunk) tiles of M in two parts and of P in `parts`, then the
+// chunk's factors.
 struct ImageHead {
     float up[kChunk];    // e^{c_t}
     float down[kChunk];  // e^{cl - c_t}
     float beta[kChunk];
+    float beta_up[kChunk];  // beta_t e^{c_t}
     float by;            // the chunk's decay as la::Decay
     int32_t weak;
-    float pad[62];
+    float inv_k, inv_q, inv_m, inv_p;  // what undoes the scales of K, Q, M and P
+    float pad[58];
 };
-static_assert(sizeof(ImageHead) == 1024, "bulk copies are multiples of 16 bytes");
+static_assert(sizeof(ImageHead) == 1280, "bulk copies are multiples of 16 bytes");
 __host__ __device__ constexpr int image_bytes(int parts) { return (2 + parts) * kTileBytes + (int)sizeof(ImageHead); }
-// parts of P: y is good to the io type's half step with one in bf16, with two in f16
+// parts of P: y is good to the io type's half step with one for bf16, with two for f16
 constexpr int fwd_parts(int dtype) { return dtype == 1 ? 2 : 1; }
 
 struct PrepArgs {
@@ -37,6 +47,7 @@ struct PrepArgs {
     Args a;
     int64_t chunks;
     int splits;        // blocks the heads of a group are divided into
+    char* keys;        // [Bsz, chunks, G]
     char* images;      // [Bsz, H, chunks]
     int* status;
 };
@@ -50,19 +61,27 @@ struct TcPlan {
 };
 
 struct TcWalkArgs {
-    CUtensorMap q, k, v, y;
+    CUtensorMap v, y;
     Args a;
     TcPlan plan;
     int64_t chunks;
-    const char* images;
+    const char *keys, *images;
     const float* init;  // h0, or null (plan.K == 1)
     float* last;        // or null
     float* seg_state;   // [Bsz, H, K, N, P]: E of each segment, then (after the carry) the states they start from
     float* seg_phi;     // [Bsz, H, K, N, N]
     void* yp;           // y again, for rows that no copy writes
+    char *states, *us;  // kTcKeep: images [Bsz, H, value tiles, chunks]
+    float *state_inv, *u_inv;  // what undoes each image's scale
     int* status;
 };
-enum TcWalkMode { kTcY, kTcSum };
+// f16 images in two parts, one scale each: the state transposed, [part][64 columns n][128 rows p][64], and U, [part][64
+// columns p][64 rows t][64].
+__host__ __device__ constexpr int state_bytes(int nb) { return 2 * nb * 2 * kTileBytes; }
+constexpr int kRowsBytes = 4 * kTileBytes;
+// kTcY: y and the last state.  kTcSum: what each segment does to a state.  kTcKeep: for the backward, the
+// state before each chunk and U, as operand images.
+enum TcWalkMode { kTcY, kTcSum, kTcKeep };
 cudaError_t launch_tc_walk(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st);
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st);
 

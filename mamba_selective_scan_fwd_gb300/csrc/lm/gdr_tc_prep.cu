@@ -24,26 +24,38 @@ using bf16 = __nv_bfloat16;
 
 constexpr int C = kChunk;
 constexpr int LDA = C + 4;
+constexpr int kHeads = 8;  // heads whose decays are made at a time: one a warp
 
+// K and Q as they come; then the image as it goes
 template <int NB, int PARTS> struct PrepSmem {
-    static constexpr int kq = 0, image = NB * 16384, a = image + image_bytes(PARTS), m = a + C * LDA * 4, total = m + C * LDA * 4;
+    static constexpr int kq = 0, image = 0, first = NB * 16384 > image_bytes(PARTS) ? NB * 16384 : image_bytes(PARTS), a = first,
+                         m = a + C * LDA * 4, total = m + C * LDA * 4;
 };
 
-// 16 values as two bf16 parts, in units u0, u0 + 1 of a row of two tiles
-__device__ __forceinline__ void put_parts(char* hi, char* lo, int row, int u0, const float (&x)[16]) {
+// 16 values times s as one or two f16 parts, in units u0, u0 + 1 of a row of two tiles
+__device__ __forceinline__ void put_parts(char* hi, char* lo, int row, int u0, const float* x, float s) {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         uint32_t h[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float2 f = make_float2(x[8 * u + 2 * i], x[8 * u + 2 * i + 1]);
-            h[i] = pack2<bf16>(f.x, f.y);
-            const float2 r = unpack2<bf16>(h[i]);
-            l[i] = pack2<bf16>(f.x - r.x, f.y - r.y);
+            float2 f = mul2(make_float2(x[8 * u + 2 * i], x[8 * u + 2 * i + 1]), splat2(s));
+            h[i] = pack2<__half>(f.x, f.y);
+            f = fma2(unpack2<__half>(h[i]), splat2(-1.0f), f);
+            l[i] = pack2<__half>(f.x, f.y);
         }
         *unit(hi, row, u0 + u) = make_uint4(h[0], h[1], h[2], h[3]);
         if (lo) *unit(lo, row, u0 + u) = make_uint4(l[0], l[1], l[2], l[3]);
     }
+}
+
+__device__ __forceinline__ float warp_max(float v) {  // v >= 0
+    uint32_t m;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
+    return __uint_as_float(m);
+}
+__device__ __forceinline__ float max8(const float* x) {
+    return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 }
 
 // M = (I + A)^{-1} of a unit lower triangular I + A, 64 x 64, all 256 threads; M's upper
@@ -100,14 +112,17 @@ __device__ __forceinline__ void invert(const float* A, float* M) {
 }
 
 template <typename T, int NB, int PARTS>
-__global__ void __launch_bounds__(256, 2) k_prep(const __grid_constant__ PrepArgs w) {
+__global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = PrepSmem<NB, PARTS>;
     __shared__ __align__(8) uint64_t s_ld, s_mma;
     __shared__ uint32_t s_tm, s_fail;
-    __shared__ Two s_c[C];
+    __shared__ Two s_c[kHeads][C];
+    __shared__ __align__(16) float s_tail[kHeads][C];  // e^{c_e - c_t}, e the end of the token's run of 16
+    __shared__ float s_beta[kHeads][C], s_max[2][8];
+    __shared__ la::Decay s_by[kHeads];
     const Args& a = w.a;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t id = blockIdx.x;
     const int64_t split = id % w.splits;
     id /= w.splits;
@@ -124,113 +139,192 @@ __global__ void __launch_bounds__(256, 2) k_prep(const __grid_constant__ PrepArg
         mbar_init(&s_mma, 1);
         s_fail = 0;
         fence_proxy_async_smem();
-    }
-    if (tid < 32) la::tmem_alloc(&s_tm, 64);
-    __syncthreads();
-    la::tc_fence_after();
-    const uint32_t tm = s_tm, my = (uint32_t)(tid & 96) << 16;
-    if (tid == 0) {
         mbar_expect_tx(&s_ld, NB * 16384);
 #pragma unroll
         for (int n = 0; n < NB; n++) {
             la::tma_load_4d(KQ + n * 16384, &w.k, n * 64, (int)gq, (int)t0, (int)b, &s_ld);
-            la::tma_load_4d(KQ + n * 16384 + 8192, &w.q, n * 64, (int)gq, (int)t0, (int)b, &s_ld);
-        }
-        if (la::wait_or_fail(&s_ld, 0, &s_fail)) {
-            constexpr uint32_t d = la::mma_desc<T>(128, 64, false, false);
-            const uint32_t at = smem_addr(KQ);
-#pragma unroll
-            for (int s = 0; s < 4 * NB; s++) {
-                const uint32_t x = at + (s >> 2) * 16384 + (s & 3) * 32;
-                la::mma(tm, la::smem_desc(x), la::smem_desc(x), d, s > 0);
-            }
-            la::mma_commit(&s_mma);
+            la::tma_load_4d(KQ + n * 16384 + kTileBytes, &w.q, n * 64, (int)gq, (int)t0, (int)b, &s_ld);
         }
     }
+    if (warp == 1) la::tmem_alloc(&s_tm, 64);
+    const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
+    auto decays = [&](int64_t h) {  // this warp's head
+        float x[2], e[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int t = 2 * lane + i;
+            x[i] = t < nv ? log_decay(a, b, t0 + t, h) * la::kLog2e : 0.0f;
+            s_beta[warp][t] = t < nv ? a.beta[(b * a.L + t0 + t) * a.H + h] : 0.0f;
+        }
+        Two c[2];
+        la::warp_cumsum<2>(x, c);
+        const Two end = {__shfl_sync(kFull, c[1].h, lane | 7), __shfl_sync(kFull, c[1].l, lane | 7)};
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            s_c[warp][2 * lane + i] = c[i];
+            e[i] = la::ex2(two_diff(end, c[i]));
+            s_tail[warp][2 * lane + i] = e[i];
+        }
+        // the chunk's decay, in natural units from the same sum (rounded once more: 2^-24 of cl)
+        if (lane == 31) s_by[warp] = la::decay_of((c[1].h + c[1].l) * kLn2);
+    };
+    if (h_lo + warp < h_hi) decays(h_lo + warp);
+    __syncthreads();
+    la::tc_fence_after();
+    const uint32_t tm = s_tm, my = (uint32_t)(tid & 96) << 16;
+    bool ok = la::wait_or_fail(&s_ld, 0, &s_fail);
+    if (tid == 0 && ok) {
+        constexpr uint32_t d = la::mma_desc<T>(128, 64, false, false);
+        const uint32_t at = smem_addr(KQ);
+#pragma unroll
+        for (int s = 0; s < 4 * NB; s++) {
+            const uint32_t x = at + (s >> 2) * 16384 + (s & 3) * 32;
+            la::mma(tm, la::smem_desc(x), la::smem_desc(x), d, s > 0);
+        }
+        la::mma_commit(&s_mma);
+    }
     __syncwarp();
-    bool ok = true;
-    for (int64_t h = gq * rep + rep * split / w.splits; h < gq * rep + rep * (split + 1) / w.splits; h++) {
-        if (tid < 32) {
-            float g[2], x[2];
+    // K (threads 0 .. 127) and Q as f16: unit u of row r of each tile; 64 x 8 NB units each
+    float scale_k, scale_q;
+    {
+        const int mine = tid & 127, side = tid >> 7;
+        float most = 0.0f;
+        uint4 x[4 * NB];
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int t = 2 * lane + e;
-                g[e] = t < nv ? log_decay(a, b, t0 + t, h) : 0.0f;
-                x[e] = g[e] * la::kLog2e;
-            }
-            Two c[2], n[2];
-            la::warp_cumsum<2>(x, c);
-            la::warp_cumsum<2>(g, n);
-            const Two cl = {__shfl_sync(kFull, c[1].h, 31), __shfl_sync(kFull, c[1].l, 31)};
-            if (lane == 31) {
-                const la::Decay d = la::decay_of(n[1].h + n[1].l);
-                head->by = d.by;
-                head->weak = d.weak;
-            }
+        for (int i = 0; i < 4 * NB; i++) {
+            const int row = (mine + 128 * i) >> 3 & 63;
+            x[i] = *reinterpret_cast<const uint4*>(KQ + (i >> 2) * 16384 + side * kTileBytes + ((mine + 128 * i) & 511) * 16);
+            if (row >= nv) x[i] = make_uint4(0, 0, 0, 0);
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int t = 2 * lane + e;
-                s_c[t] = c[e];
-                head->up[t] = la::ex2(c[e].h + c[e].l);
-                head->down[t] = la::ex2(two_diff(cl, c[e]));
-                head->beta[t] = t < nv ? a.beta[(b * a.L + t0 + t) * a.H + h] : 0.0f;
+            for (int e = 0; e < 4; e++) {
+                const float2 f = unpack2<T>(v[e]);
+                most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
         }
-        ok = ok && la::wait_or_fail(&s_mma, 0, &s_fail);
-        if (__syncthreads_or(!ok)) break;
-        la::tc_fence_after();
-        {  // thread: row i of K K^T (warps 0, 1 of a warpgroup) or Q K^T, 32 columns
+        most = warp_max(most);
+        if (lane == 0) s_max[0][warp] = most;
+        __syncthreads();
+        scale_k = la::f16_scale(fmaxf(fmaxf(s_max[0][0], s_max[0][1]), fmaxf(s_max[0][2], s_max[0][3])));
+        scale_q = la::f16_scale(fmaxf(fmaxf(s_max[0][4], s_max[0][5]), fmaxf(s_max[0][6], s_max[0][7])));
+        const float2 s = splat2(side ? scale_q : scale_k);
+        char* to = w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384);
+        if (split == 0)
+#pragma unroll
+            for (int i = 0; i < 4 * NB; i++) {
+                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t r[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float2 f = mul2(unpack2<T>(v[e]), s);
+                    r[e] = pack2<__half>(f.x, f.y);
+                }
+                *reinterpret_cast<uint4*>(to + (i >> 2) * 16384 + side * kTileBytes + ((mine + 128 * i) & 511) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+    }
+    ok = la::wait_or_fail(&s_mma, 0, &s_fail) && ok;
+    la::tc_fence_after();
+    for (int64_t h0 = h_lo; h0 < h_hi; h0 += kHeads) {
+        if (h0 > h_lo) {
+            __syncthreads();
+            if (h0 + warp < h_hi) decays(h0 + warp);
+        }
+        for (int64_t h = h0; h < min(h_hi, h0 + kHeads); h++) {
+            const int hl = (int)(h - h0);
+            if (__syncthreads_or(!ok)) break;  // (and: the last head's image has left, s_max is free)
+            // thread: row i of K K^T (warps 0, 1 of a warpgroup) or Q K^T, columns j0 .. j0 + 31: two runs of 16.  A run
+            // left of the row's own takes e^{c_i - c_e} e^{c_e - c_j} with e its end, the row's own an exponential each.
             const bool is_q = tid & 64;
-            const int i = tid & 63, j0 = (tid >> 7) * 32;
+            const int i = tid & 63, j0 = (tid >> 7) * 32, last = is_q ? i : i - 1;
             float s[32];
             la::tmem_ld32(tm + my + j0, s);
-            const Two ci = s_c[i];
-            const float f = is_q ? 1.0f : head->beta[i];
-            const bool own = i < nv;
-            const int last = is_q ? i : i - 1;
+            const Two ci = s_c[hl][i];
+            const float f = i >= nv ? 0.0f : is_q ? 1.0f : s_beta[hl][i];
 #pragma unroll
-            for (int j = 0; j < 32; j++) {
-                const int col = j0 + j;
-                s[j] = own && col <= last ? f * s[j] * la::ex2(two_diff(ci, s_c[col])) : 0.0f;
-            }
-            if (is_q) {
-                char* hi = I + 2 * kTileBytes;
+            for (int r = 0; r < 2; r++) {
+                const int c0 = j0 + 16 * r;
+                if (c0 + 16 <= (i & ~15)) {
+                    const float by = f * la::ex2(two_diff(ci, s_c[hl][c0 + 15]));
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    float x[16];
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(&s_tail[hl][c0 + j]);
+                        s[16 * r + j] *= by * t.x;
+                        s[16 * r + j + 1] *= by * t.y;
+                        s[16 * r + j + 2] *= by * t.z;
+                        s[16 * r + j + 3] *= by * t.w;
+                    }
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 16; e++) x[e] = s[16 * u + e];
-                    put_parts(hi, PARTS > 1 ? hi + kTileBytes : nullptr, i, j0 / 8 + 2 * u, x);
+                    for (int j = 0; j < 16; j++) {
+                        const float e = c0 + j <= last ? la::ex2(two_diff(ci, s_c[hl][c0 + j])) : 0.0f;
+                        s[16 * r + j] = c0 + j <= last ? f * e * s[16 * r + j] : 0.0f;
+                    }
                 }
+                if (i >= nv)  // (whatever the row holds)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) s[16 * r + j] = 0.0f;
+            }
+            float most = 0.0f;
+            if (is_q) {
+#pragma unroll
+                for (int j = 0; j < 32; j++) most = fmaxf(most, fabsf(s[j]));
+                most = warp_max(most);
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)
                     *reinterpret_cast<float4*>(A + i * LDA + j0 + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
             }
-        }
-        __syncthreads();
-        invert(A, M);
-        {
-            const int i = tid >> 2, j0 = (tid & 3) * 16;
-            float x[16];
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(M + i * LDA + j0 + e);
-                x[e] = j0 + e <= i ? v.x : 0.0f;
-                x[e + 1] = j0 + e + 1 <= i ? v.y : 0.0f;
-                x[e + 2] = j0 + e + 2 <= i ? v.z : 0.0f;
-                x[e + 3] = j0 + e + 3 <= i ? v.w : 0.0f;
+            if (lane == 0) s_max[0][warp] = most;
+            if (tid < C) {
+                const Two c = s_c[hl][tid], cl = s_c[hl][C - 1];
+                const float up = la::ex2(c.h + c.l);
+                head->up[tid] = up;
+                head->beta_up[tid] = s_beta[hl][tid] * up;
+                head->down[tid] = la::ex2(two_diff(cl, c));
+                head->beta[tid] = s_beta[hl][tid];
             }
-            put_parts(I, I + kTileBytes, i, j0 / 8, x);
+            __syncthreads();
+            const float scale_p = la::f16_scale(fmaxf(fmaxf(s_max[0][2], s_max[0][3]), fmaxf(s_max[0][6], s_max[0][7])));
+            if (is_q) {
+                char* hi = I + 2 * kTileBytes;
+                put_parts(hi, PARTS > 1 ? hi + kTileBytes : nullptr, i, j0 / 8, s, scale_p);
+                put_parts(hi, PARTS > 1 ? hi + kTileBytes : nullptr, i, j0 / 8 + 2, s + 16, scale_p);
+            }
+            invert(A, M);
+            {
+                const int i = tid >> 2, j0 = (tid & 3) * 16;
+                float x[16], most = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(M + i * LDA + j0 + e);
+                    x[e] = j0 + e <= i ? v.x : 0.0f;
+                    x[e + 1] = j0 + e + 1 <= i ? v.y : 0.0f;
+                    x[e + 2] = j0 + e + 2 <= i ? v.z : 0.0f;
+                    x[e + 3] = j0 + e + 3 <= i ? v.w : 0.0f;
+                    most = fmaxf(most, fmaxf(fmaxf(fabsf(x[e]), fabsf(x[e + 1])), fmaxf(fabsf(x[e + 2]), fabsf(x[e + 3]))));
+                }
+                most = warp_max(most);
+                if (lane == 0) s_max[1][warp] = most;
+                __syncthreads();
+                const float scale_m = la::f16_scale(max8(s_max[1]));
+                put_parts(I, I + kTileBytes, i, j0 / 8, x, scale_m);
+                if (tid == 0) {
+                    head->by = s_by[hl].by;
+                    head->weak = s_by[hl].weak;
+                    head->inv_k = 1.0f / scale_k;
+                    head->inv_q = 1.0f / scale_q;
+                    head->inv_m = 1.0f / scale_m;
+                    head->inv_p = 1.0f / scale_p;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (tid == 0) {
+                la::bulk_store(w.images + ((b * a.H + h) * w.chunks + chunk) * image_bytes(PARTS), I, image_bytes(PARTS));
+                la::bulk_commit();
+                if (h + 1 < h_hi) la::bulk_wait_read();
+            }
         }
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            la::bulk_store(w.images + ((b * a.H + h) * w.chunks + chunk) * image_bytes(PARTS), I, image_bytes(PARTS));
-            la::bulk_commit();
-            la::bulk_wait_read();
-        }
-        __syncthreads();
     }
     if (tid == 0) la::bulk_wait_all();
     uint64_t* const bars[2] = {&s_ld, &s_mma};

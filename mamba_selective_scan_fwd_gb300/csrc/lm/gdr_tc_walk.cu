@@ -4,18 +4,18 @@
 // with the state transposed: the value channels are the 128 lanes of tensor memory, so that
 // a thread owns a channel (half of its N states, half of a chunk's tokens) and every
 // left operand is written by the thread that will read the product's row:
-//   D1 = S^T K^T             [128 x 64]   S in two 16-bit parts, from tensor memory
-//   X = beta (V^T - e^c D1)               two bf16 parts
-//   D2 = X M^T = U^T         [128 x 64]   lo hi + hi lo + hi hi
-//   D3 = (e^{cl - c} U)^T K  [128 x N]    two 16-bit parts;  S <- e^{cl} S + D3, f32 in registers
+//   D1 = S^T [K; Q]^T        [128 x 128]  S in two f16 parts, from tensor memory
+//   X = beta (V^T - e^c D1)               two parts
+//   D2 = X M^T = U^T         [128 x 2 x 64]  hi [hi; lo] + lo hi
+//   D3 = (e^{cl - c} U)^T K  [128 x N]    two parts;  S <- e^{cl} S + D3, f32 in registers
 //   y = scale (e^c S^T Q^T + U^T P^T)     off the chain: a third warpgroup writes it
-// A loading warp copies a chunk's tiles one chunk ahead and issues all products.  Chain of a
-// chunk: three products and three passes through the registers.
+// One thread copies a chunk's tiles one chunk ahead and issues all products.  The chain of a
+// chunk is three products and three passes through the registers, and bounds the walk.
 //
-// Roundings: two 16-bit parts of S, X, M and e U hold 16 bits (f16: 22) of each, which leaves
-// the f32 state good to a few 1e-6; P and U enter y's product with one bf16 part each (f16 io:
-// two), one rounding each of terms of a 16-bit y.  f16's S and e U are scaled by a power of two
-// per channel, taken from their largest value.
+// Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken
+// from the channel's largest value, which its two threads exchange; the f32 state stays good to
+// a few 1e-7.  P and U enter y's product with one part each for bf16 io (2^-12 of a y that is
+// rounded to 2^-9), with two for f16.
 #include "gdr_tc.h"
 #include "../simd.cuh"
 #include "tc.cuh"
@@ -30,19 +30,21 @@ using la::pack2;
 using la::unit;
 using la::unpack2;
 using la::wait_or_fail;
-using bf16 = __nv_bfloat16;
 
 constexpr int C = kChunk;
 constexpr int kStateThreads = 256, kThreads = 256 + 128 + 32;
 
-// columns of tensor memory: D1 then D2; S^T Q^T; D3; U^T P^T; parts of S, then of e U; parts of X, then of U
+// columns of tensor memory: S^T K^T; S^T Q^T; X M^T in two halves, then D3; U^T P^T; parts of S, then of
+// e U; parts of X, then of U
 constexpr uint32_t kD1 = 0, kQ = 64, kD3 = 128, kY = 256, kS = 320, kX = 448;
 
-template <typename T> constexpr int kPParts = kF16<T> ? 2 : 1;
+template <typename T> constexpr int kPParts = kF16<T> ? 2 : 1;  // of P and U in y's product
 
-template <typename T, int NB> struct Stage {
-    static constexpr int k = 0, q = k + NB * kTileBytes, v = q + NB * kTileBytes, image = v + 2 * kTileBytes,
-                         head = image + (2 + kPParts<T>) * kTileBytes, bytes = head + 1024;
+// A stage of shared memory: tiles of K and Q by turns (not Q: kTcSum, kTcKeep), V, the image
+template <int NB, int PP, bool Q> struct Stage {
+    static constexpr int block = (Q ? 2 : 1) * kTileBytes;  // K (and Q) of 64 columns
+    static constexpr int v = NB * block, image = v + 2 * kTileBytes, head = image + (2 + (Q ? PP : 0)) * kTileBytes,
+                         bytes = head + 2048;
 };
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {  // a warp's
@@ -52,46 +54,71 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {  // a warp's
 }
 __device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// 32 values as two 16-bit parts: 16 columns of tensor memory each
-template <typename T> __device__ __forceinline__ void put2(uint32_t hi, uint32_t lo, const float (&x)[32], float s) {
+// 32 values times s as two f16 parts: 16 columns of tensor memory each
+__device__ __forceinline__ void put2(uint32_t hi, uint32_t lo, const float* x, float s) {
     uint32_t r[16], q[16];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
-        float2 f = make_float2(x[2 * i], x[2 * i + 1]);
-        if (kF16<T>) f = mul2(f, splat2(s));
-        r[i] = pack2<T>(f.x, f.y);
-        f = fma2(unpack2<T>(r[i]), splat2(-1.0f), f);
-        q[i] = pack2<T>(f.x, f.y);
+        float2 f = mul2(make_float2(x[2 * i], x[2 * i + 1]), splat2(s));
+        r[i] = pack2<__half>(f.x, f.y);
+        f = fma2(unpack2<__half>(r[i]), splat2(-1.0f), f);
+        q[i] = pack2<__half>(f.x, f.y);
     }
     la::tmem_st16(hi, r);
     la::tmem_st16(lo, q);
 }
-template <typename T> __device__ __forceinline__ void put1(uint32_t to, const float (&x)[32]) {
+__device__ __forceinline__ void put1(uint32_t to, const float* x, float s) {
     uint32_t r[16];
 #pragma unroll
-    for (int i = 0; i < 16; i++) r[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 16; i++) r[i] = pack2<__half>(s * x[2 * i], s * x[2 * i + 1]);
     la::tmem_st16(to, r);
 }
+template <int N> __device__ __forceinline__ float max_abs(const float* x) {
+    float m[4] = {};
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+#pragma unroll
+        for (int e = 0; e < 4; e++) m[e] = fmaxf(m[e], fabsf(x[i + e]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// The power of two for a row whose largest value is `most`; of a row of zeros it is the largest there is, so
+// that it never decides a scale common to more rows.
+__device__ __forceinline__ float scale_of(float most) { return most == 0.0f ? 8.507059173023462e37f : la::f16_scale(most); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
+    const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&z);
+}
+// Smallest of a warpgroup's positive values (all get it).  Two barriers.
+__device__ __forceinline__ float group_min(float v, uint32_t* red, int id) {
+    uint32_t m;
+    asm volatile("redux.sync.min.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
+    if ((threadIdx.x & 31) == 0) red[(threadIdx.x >> 5) & 3] = m;
+    named_sync(id, 128);
+    m = min(min(red[0], red[1]), min(red[2], red[3]));
+    named_sync(id, 128);
+    return __uint_as_float(m);
+}
 
-// SUM: no y.  blockIdx.y of SUM: 0 walks from zero (E), 1 from the identity without v (Phi).
-template <typename T, int NB, bool SUM>
+// blockIdx.y of kTcSum: 0 walks from zero (E), 1 from the identity without v (Phi).
+template <typename T, int NB, TcWalkMode MODE>
 __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ TcWalkArgs w) {
     extern __shared__ __align__(1024) char sm[];
-    using L = Stage<T, NB>;
-    constexpr int W = 32 * NB;  // states of a thread
-    constexpr int PP = kPParts<T>;
-    __shared__ __align__(8) uint64_t s_full[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_y, s_done;
-    __shared__ uint32_t s_tm, s_fail;
-    __shared__ float s_max[2][2][128], s_ss[2][128];
+    constexpr bool SUM = MODE == kTcSum, OUT = MODE == kTcY, KEEP = MODE == kTcKeep;
+    // (the backward's images hold P in two parts)
+    constexpr int W = 32 * NB, PP = kPParts<T>, IP = KEEP ? 2 : PP;
+    using L = Stage<NB, PP, OUT>;
+    // landed; S; D1; X; D2; U; D3; U^T P^T; read by the third warpgroup: early, late
+    __shared__ __align__(8) uint64_t s_full[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_y, s_early, s_late;
+    __shared__ uint32_t s_tm, s_fail, s_red[4];
+    __shared__ float s_max[3][2][128], s_um[2][128], s_ss[2][128], s_us[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pl = tid & 127;
     const bool phi = SUM && blockIdx.y == 1;
-    const int64_t width = phi ? a.N : a.P, ptiles = (width + kTileP - 1) / kTileP;
+    const int64_t width = phi ? a.N : a.P, ptiles = (a.P + kTileP - 1) / kTileP;
     int64_t id = blockIdx.x;
-    // phi has fewer tiles of columns than v may have: the blocks beyond do nothing
-    const int64_t p0 = id % ((a.P + kTileP - 1) / kTileP) * kTileP;
-    id /= (a.P + kTileP - 1) / kTileP;
-    if (phi && p0 >= ptiles * kTileP) return;
+    const int64_t pt = id % ptiles, p0 = pt * kTileP;
+    id /= ptiles;
+    if (phi && pt > 0) return;  // N <= 128 columns
     const int64_t bh = id % (a.Bsz * a.H), seg = id / (a.Bsz * a.H);
     const int64_t b = bh / a.H, h = bh % a.H, hq = h / (a.H / a.G);
     const int64_t len = row_length(a, b);
@@ -101,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     if (tid == 0) {
         for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_y}) mbar_init(bar, 1);
         for (uint64_t* bar : {&s_s, &s_x, &s_u}) mbar_init(bar, kStateThreads / 32);
-        mbar_init(&s_done, 4);
+        for (uint64_t* bar : {&s_early, &s_late}) mbar_init(bar, 4);
         s_fail = 0;
         fence_proxy_async_smem();
     }
@@ -109,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     __syncthreads();
     la::tc_fence_after();
     const uint32_t tm = s_tm, my = (uint32_t)((warp & 3) * 32) << 16;
-    char* Y = sm + 2 * L::bytes;  // staging of y: two tiles of [token][64 channels]
+    char* staging = sm + 2 * L::bytes;
     auto valid = [&](int ch) { return (int)min((int64_t)C, len - (t_begin + (int64_t)ch * C)); };
 
     if (warp < kStateThreads / 32) {
@@ -127,120 +154,134 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             for (int n = 0; n < W; n++) S[n] = from && mine && half * W + n < a.N ? from[(half * W + n) * a.P + p] : 0.0f;
         }
         // (a wait that ran out ends no loop here: the others wait at its barriers)
-        // f16: the power of two of this channel's row, from both halves' largest values
+        // The power of two of this channel's row, from its two threads' largest values (`which` alternates between a
+        // chunk's three exchanges, so that none overwrites what the other thread has not read).
         auto row_scale = [&](float most, int which) {
             s_max[which][half][pl] = most;
-            named_sync(1, kStateThreads);
-            return la::f16_scale(fmaxf(s_max[which][0][pl], s_max[which][1][pl]));
+            named_sync(1 + (warp & 3), 64);
+            return scale_of(fmaxf(most, s_max[which][half ^ 1][pl]));
         };
         bool ok = true;
+        float most = max_abs<W>(S);
         for (int ch = 0; ch < chunks; ch++) {
             const uint32_t ph = ch & 1;
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const int nv = valid(ch);
-            float ss = 1.0f;
-            if (kF16<T>) {
-                float m = 0.0f;
-#pragma unroll
-                for (int n = 0; n < W; n++) m = fmaxf(m, fabsf(S[n]));
-                ss = row_scale(m, 0);
-                if (half == 0) s_ss[ph][pl] = ss;  // y's product has it too
-            }
+            const float ss = row_scale(most, 0);
+            if (!SUM && half == 0) s_ss[ph][pl] = ss;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
-                float x[32];
-#pragma unroll
-                for (int n = 0; n < 32; n++) x[n] = S[32 * c + n];
                 const uint32_t to = tm + my + kS + half * (W / 2) + 16 * c;
-                put2<T>(to, to + 32 * NB, x, ss);
+                put2(to, to + 32 * NB, S + 32 * c, ss);
             }
             la::tmem_wait_st();
-            ok = ok && wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
-            if (nv < C && ok) {  // keys past the row's length: zero, whatever they hold
-                const int row = tid & 63;
-                if (row >= nv && (tid >> 6) < NB)
-#pragma unroll
-                    for (int u = 0; u < 8; u++) *unit(at + L::k + (tid >> 6) * kTileBytes, row, u) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
             arrive(&s_s);
-            float vv[32];
-            {
-                const char* tile = at + L::v + (pl >> 6) * kTileBytes;
-                const int c = (pl & 63) >> 3, e = (pl & 7) * 2;
+            ok = ok && wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
+            const float inv1 = -head->inv_k / ss;
+            float x[32];
+            if (phi) {
 #pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    const int t = 32 * half + j;
-                    vv[j] = phi ? 0.0f : ldf(reinterpret_cast<const T*>(tile + t * 128 + ((c ^ (t & 7)) << 4) + e));
+                for (int j = 0; j < 32; j++) x[j] = 0.0f;
+            } else {
+                const char* tile = at + L::v + (pl >> 6) * kTileBytes + (pl & 7) * 2;
+                const int c = (pl & 63) >> 3;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 be = *reinterpret_cast<const float4*>(&head->beta[32 * half + j]);
+                    const float bs[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int t = 32 * half + j + e;
+                        x[j + e] = bs[e] * ldf(reinterpret_cast<const T*>(tile + t * 128 + ((c ^ (t & 7)) << 4)));
+                    }
                 }
             }
             ok = ok && wait_or_fail(&s_d1, ph, &s_fail);
             la::tc_fence_after();
             float d[32];
             la::tmem_ld32(tm + my + kD1 + 32 * half, d);
-            const float inv = kF16<T> ? 1.0f / ss : 1.0f;
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-                const float4 up = *reinterpret_cast<const float4*>(&head->up[32 * half + j]);
-                const float4 be = *reinterpret_cast<const float4*>(&head->beta[32 * half + j]);
-                const float us[4] = {up.x, up.y, up.z, up.w}, bs[4] = {be.x, be.y, be.z, be.w};
-#pragma unroll
-                for (int e = 0; e < 4; e++) d[j + e] = bs[e] * fmaf(-(kF16<T> ? us[e] * inv : us[e]), d[j + e], vv[j + e]);
+                const float4 f = *reinterpret_cast<const float4*>(&head->beta_up[32 * half + j]);
+                const float2 y = fma2(mul2(splat2(inv1), make_float2(f.x, f.y)), make_float2(d[j], d[j + 1]), make_float2(x[j], x[j + 1]));
+                const float2 z = fma2(mul2(splat2(inv1), make_float2(f.z, f.w)), make_float2(d[j + 2], d[j + 3]), make_float2(x[j + 2], x[j + 3]));
+                x[j] = y.x;
+                x[j + 1] = y.y;
+                x[j + 2] = z.x;
+                x[j + 3] = z.y;
             }
             if (nv < C) {
 #pragma unroll
                 for (int j = 0; j < 32; j++)
-                    if (32 * half + j >= nv) d[j] = 0.0f;
+                    if (32 * half + j >= nv) x[j] = 0.0f;
             }
+            const float xs = row_scale(max_abs<32>(x), 1);
+            // U of the chunk before has left its columns
+            if (KEEP && ch > 0) ok = ok && wait_or_fail(&s_late, ph ^ 1, &s_fail);
             {
                 const uint32_t to = tm + my + kX + 16 * half;
-                put2<bf16>(to, to + 32, d, 1.0f);
+                put2(to, to + 32, x, xs);
             }
             la::tmem_wait_st();
             arrive(&s_x);
+            const float inv2 = head->inv_m / xs;
             ok = ok && wait_or_fail(&s_d2, ph, &s_fail);
             la::tc_fence_after();
-            la::tmem_ld32(tm + my + kD1 + 32 * half, d);
-            if (!SUM) {
-                const uint32_t to = tm + my + kX + 16 * half;
-                if (PP > 1) put2<bf16>(to, to + 32, d, 1.0f);
-                else put1<bf16>(to, d);
+            la::tmem_ld32(tm + my + kD3 + 64 + 32 * half, x);
+            la::tmem_ld32(tm + my + kD3 + 32 * half, d);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float2 f = mul2(splat2(inv2), add2(make_float2(d[j], d[j + 1]), make_float2(x[j], x[j + 1])));
+                x[j] = f.x;
+                x[j + 1] = f.y;
             }
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&head->down[32 * half + j]);
-                d[j] *= f.x;
-                d[j + 1] *= f.y;
-                d[j + 2] *= f.z;
-                d[j + 3] *= f.w;
+                d[j] = x[j] * f.x;
+                d[j + 1] = x[j + 1] * f.y;
+                d[j + 2] = x[j + 2] * f.z;
+                d[j + 3] = x[j + 3] * f.w;
             }
-            float us = 1.0f;
-            if (kF16<T>) {
-                float m = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 32; j++) m = fmaxf(m, fabsf(d[j]));
-                us = row_scale(m, 1);
+            if (!SUM) s_um[half][pl] = max_abs<32>(x);
+            const float us = row_scale(max_abs<32>(d), 2);
+            if (!SUM) {
+                const float uy = scale_of(fmaxf(s_um[0][pl], s_um[1][pl]));
+                if (half == 0) s_us[ph][pl] = uy;
+                const uint32_t to = tm + my + kX + 16 * half;
+                if (KEEP || PP > 1) put2(to, to + 32, x, uy);
+                else put1(to, x, uy);
             }
+            // the parts of S have been copied
+            if (KEEP) ok = ok && wait_or_fail(&s_early, ph, &s_fail);
             {
                 const uint32_t to = tm + my + kS + 16 * half;
-                put2<T>(to, to + 32, d, us);
+                put2(to, to + 32, d, us);
             }
             la::tmem_wait_st();
-            const la::Decay by = {head->by, head->weak != 0};
+            const float by = head->by, keep = head->weak ? 1.0f : 0.0f, inv3 = head->inv_k / us;
             arrive(&s_u);
             ok = ok && wait_or_fail(&s_d3, ph, &s_fail);
             la::tc_fence_after();
-            const float uinv = kF16<T> ? 1.0f / us : 1.0f;
+            float m[2] = {};
 #pragma unroll
             for (int c = 0; c < NB; c++) {
                 la::tmem_ld32(tm + my + kD3 + half * W + 32 * c, d);
 #pragma unroll
-                for (int n = 0; n < 32; n++) S[32 * c + n] = fmaf(uinv, d[n], la::decayed(by, S[32 * c + n]));
+                for (int n = 0; n < 32; n += 2) {
+                    const float2 o = make_float2(S[32 * c + n], S[32 * c + n + 1]);
+                    // S + (e^cl - 1) S for a weak decay, e^cl S else (la::Decay)
+                    const float2 f = fma2(splat2(inv3), make_float2(d[n], d[n + 1]), fma2(splat2(by), o, mul2(splat2(keep), o)));
+                    S[32 * c + n] = f.x;
+                    S[32 * c + n + 1] = f.y;
+                    m[0] = fmaxf(m[0], fabsf(f.x));
+                    m[1] = fmaxf(m[1], fabsf(f.y));
+                }
             }
-            if (!ok) break;
+            most = fmaxf(m[0], m[1]);
         }
-        if (mine && !s_fail) {
+        if (mine && ok) {
             float* to = nullptr;
             if (phi) to = w.seg_phi + (bh * w.plan.K + seg) * a.N * a.N;
             else if (SUM) to = w.seg_state + (bh * w.plan.K + seg) * a.N * a.P;
@@ -251,102 +292,168 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     if (half * W + n < a.N) to[(half * W + n) * width + p] = S[n];
         }
     } else if (warp < kStateThreads / 32 + 4) {
-        if (!SUM) {
+        const bool first = tid == kStateThreads;
+        if (OUT) {
             T* yp = static_cast<T*>(w.yp) + (b * a.L * a.H + h) * a.P;
             const bool wide = p0 + 64 < a.P;
             for (int ch = 0; ch < chunks; ch++) {
                 const uint32_t ph = ch & 1;
                 const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + ph * L::bytes + L::head);
                 const int nv = valid(ch);
-                if (tid == kStateThreads) la::bulk_wait_read();
-                named_sync(2, 128);  // the staging tiles are free
                 wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
+                wait_or_fail(&s_d1, ph, &s_fail);
+                la::tc_fence_after();
+                float q[64];
+                {
+                    const float inv = a.scale * head->inv_q / s_ss[ph][pl];
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        float x[32];
+                        la::tmem_ld32(tm + my + kQ + 32 * hf, x);
+#pragma unroll
+                        for (int j = 0; j < 32; j++) q[32 * hf + j] = inv * head->up[32 * hf + j] * x[j];
+                    }
+                }
+                arrive(&s_early);
+                if (first) la::bulk_wait_read();
+                named_sync(5, 128);  // the staging tiles are free
                 wait_or_fail(&s_y, ph, &s_fail);
                 la::tc_fence_after();
-                const float inv = kF16<T> ? a.scale / s_ss[ph][pl] : a.scale;
-                char* tile = Y + (pl >> 6) * kTileBytes;
-                const int cu = (pl & 63) >> 3, eb = (pl & 7) * 2;
+                const float inv = a.scale * head->inv_p / s_us[ph][pl];
+                char* tile = staging + (pl >> 6) * kTileBytes + (pl & 7) * 2;
+                const int cu = (pl & 63) >> 3;
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    float q[32], y[32];
-                    la::tmem_ld32(tm + my + kQ + 32 * hf, q);
+                    float y[32];
                     la::tmem_ld32(tm + my + kY + 32 * hf, y);
 #pragma unroll
                     for (int j = 0; j < 32; j++) {
                         const int t = 32 * hf + j;
-                        const float x = fmaf(inv * head->up[t], q[j], a.scale * y[j]);
-                        st(reinterpret_cast<T*>(tile + t * 128 + ((cu ^ (t & 7)) << 4) + eb), t < nv ? x : 0.0f);
+                        const float x = fmaf(inv, y[j], q[t]);
+                        st(reinterpret_cast<T*>(tile + t * 128 + ((cu ^ (t & 7)) << 4)), t < nv ? x : 0.0f);
                     }
                 }
-                arrive(&s_done);
+                arrive(&s_late);
                 fence_proxy_async_smem();
-                named_sync(2, 128);
-                if (tid == kStateThreads) {
+                named_sync(5, 128);
+                if (first) {
                     const int64_t t0 = t_begin + (int64_t)ch * C;
-                    la::tma_store_4d(&w.y, Y, (int)p0, (int)h, (int)t0, (int)b);
-                    if (wide) la::tma_store_4d(&w.y, Y + kTileBytes, (int)p0 + 64, (int)h, (int)t0, (int)b);
+                    la::tma_store_4d(&w.y, staging, (int)p0, (int)h, (int)t0, (int)b);
+                    if (wide) la::tma_store_4d(&w.y, staging + kTileBytes, (int)p0 + 64, (int)h, (int)t0, (int)b);
                     la::bulk_commit();
                 }
             }
-            if (tid == kStateThreads) la::bulk_wait_all();
             // tokens of chunks beyond the row's length
             for (int64_t t = t_begin + (int64_t)chunks * C + (warp & 3); t < t_end; t += 4)
                 for (int64_t p = p0 + lane * 8; p < min(a.P, p0 + kTileP); p += 256)
                     *reinterpret_cast<uint4*>(yp + t * a.H * a.P + p) = make_uint4(0, 0, 0, 0);
         }
+        if (KEEP) {
+            for (int ch = 0; ch < chunks; ch++) {
+                const uint32_t ph = ch & 1;
+                const int64_t image = (bh * ptiles + pt) * w.chunks + c_begin + ch;
+                wait_or_fail(&s_s, ph, &s_fail);
+                la::tc_fence_after();
+                // the parts of S under one scale: what the largest channel's is
+                float own = s_ss[ph][pl], all = group_min(own, s_red, 5);
+                uint32_t f = pack2<__half>(all / own, all / own);
+#pragma unroll
+                for (int c = 0; c < 2 * NB; c++) {  // 32 columns: 64 states of one part
+                    float x[32];
+                    la::tmem_ld32(tm + my + kS + 32 * c, x);
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        *unit(staging + c * 2 * kTileBytes, pl, u) =
+                            make_uint4(hmul2(__float_as_uint(x[4 * u]), f), hmul2(__float_as_uint(x[4 * u + 1]), f),
+                                       hmul2(__float_as_uint(x[4 * u + 2]), f), hmul2(__float_as_uint(x[4 * u + 3]), f));
+                }
+                arrive(&s_early);
+                fence_proxy_async_smem();
+                named_sync(5, 128);
+                if (first) {
+                    la::bulk_store(w.states + image * state_bytes(NB), staging, state_bytes(NB));
+                    la::bulk_commit();
+                    w.state_inv[image] = 1.0f / all;
+                }
+                wait_or_fail(&s_u, ph, &s_fail);
+                la::tc_fence_after();
+                own = s_us[ph][pl], all = group_min(own, s_red, 5);
+                f = pack2<__half>(all / own, all / own);
+                char* to = staging + state_bytes(NB) + (pl >> 6) * kTileBytes + (pl & 7) * 2;
+                const int cu = (pl & 63) >> 3;
+#pragma unroll
+                for (int part = 0; part < 2; part++) {
+                    float x[32];
+                    la::tmem_ld32(tm + my + kX + 32 * part, x);
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        const uint32_t r = hmul2(__float_as_uint(x[j]), f);
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int t = 2 * j + e;
+                            *reinterpret_cast<uint16_t*>(to + part * 2 * kTileBytes + t * 128 + ((cu ^ (t & 7)) << 4)) = (uint16_t)(e ? r >> 16 : r);
+                        }
+                    }
+                }
+                arrive(&s_late);
+                fence_proxy_async_smem();
+                named_sync(5, 128);
+                if (first) {
+                    la::bulk_store(w.us + image * kRowsBytes, staging + state_bytes(NB), kRowsBytes);
+                    la::bulk_commit();
+                    w.u_inv[image] = 1.0f / all;
+                    la::bulk_wait_read();
+                }
+                named_sync(5, 128);
+            }
+        }
+        if (first) la::bulk_wait_all();
     } else if (lane == 0) {
+        const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
+        const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(IP);
         auto load = [&](int ch) {
             char* at = sm + (ch & 1) * L::bytes;
             uint64_t* bar = &s_full[ch & 1];
             const int t0 = (int)(t_begin + (int64_t)ch * C);
-            mbar_expect_tx(bar, ((SUM ? 1 : 2) * NB + (phi ? 0 : 2)) * kTileBytes + image_bytes(PP));
+            mbar_expect_tx(bar, (OUT ? 2 : 1) * NB * kTileBytes + (phi ? 0 : 2 * kTileBytes) + (2 + (OUT ? PP : 0)) * kTileBytes +
+                                    (int)sizeof(ImageHead));
+            const char* kq = keys + ch * a.G * (NB * 2 * kTileBytes);
 #pragma unroll
-            for (int n = 0; n < NB; n++) {
-                la::tma_load_4d(at + L::k + n * kTileBytes, &w.k, n * 64, (int)hq, t0, (int)b, bar);
-                if (!SUM) la::tma_load_4d(at + L::q + n * kTileBytes, &w.q, n * 64, (int)hq, t0, (int)b, bar);
-            }
+            for (int n = 0; n < NB; n++) bulk_load(at + n * L::block, kq + n * 2 * kTileBytes, L::block, bar);
             if (!phi) {
                 la::tma_load_4d(at + L::v, &w.v, (int)p0, (int)h, t0, (int)b, bar);
                 la::tma_load_4d(at + L::v + kTileBytes, &w.v, (int)p0 + 64, (int)h, t0, (int)b, bar);
             }
-            bulk_load(at + L::image, w.images + (bh * w.chunks + c_begin + ch) * image_bytes(PP), image_bytes(PP), bar);
+            const char* im = images + (int64_t)ch * image_bytes(IP);
+            bulk_load(at + L::image, im, (2 + (OUT ? PP : 0)) * kTileBytes, bar);
+            bulk_load(at + L::head, im + (2 + IP) * kTileBytes, (int)sizeof(ImageHead), bar);
         };
         if (chunks > 0) load(0);
         if (chunks > 1) load(1);
         for (int ch = 0; ch < chunks; ch++) {
             const uint32_t ph = ch & 1;
-            const uint32_t at = smem_addr(sm + ph * L::bytes), K = at + L::k, Q = at + L::q, M = at + L::image,
-                           P = M + 2 * kTileBytes;
-            constexpr uint32_t dK = la::mma_desc<T>(128, C, false, false), dM = la::mma_desc<bf16>(128, C, false, false),
-                               dU = la::mma_desc<T>(128, 64 * NB, false, true);
+            const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
+            constexpr int N1 = OUT ? 2 * C : C;  // K, or K and Q
+            constexpr uint32_t d1 = la::mma_desc<__half>(128, N1, false, false), d2 = la::mma_desc<__half>(128, 2 * C, false, false),
+                               dP = la::mma_desc<__half>(128, C, false, false), d3 = la::mma_desc<__half>(128, 64 * NB, false, true);
             if (!wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail) || !wait_or_fail(&s_s, ph, &s_fail)) break;
+            if (OUT && ch > 0 && !wait_or_fail(&s_early, ph ^ 1, &s_fail)) break;  // Q's product of the chunk before is read
             la::tc_fence_after();
-            auto with_state = [&](uint32_t to, uint32_t tile, int parts) {
-                for (int part = parts - 1; part >= 0; part--)
 #pragma unroll
-                    for (int s = 0; s < 4 * NB; s++)
-                        la::mma_ts(tm + to, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(tile + (s >> 2) * kTileBytes + (s & 3) * 32), dK,
-                                   part < parts - 1 || s > 0);
-            };
-            with_state(kD1, K, 2);
+            for (int part = 1; part >= 0; part--)
+#pragma unroll
+                for (int s = 0; s < 4 * NB; s++)
+                    la::mma_ts(tm + kD1, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(at + (s >> 2) * L::block + (s & 3) * 32), d1, part < 1 || s > 0);
             la::mma_commit(&s_d1);
-            if (!SUM) {
-                // y of the chunk before is out of tensor memory, and with it all products of that chunk are done
-                if (ch > 0 && !wait_or_fail(&s_done, ph ^ 1, &s_fail)) break;
-                with_state(kQ, Q, PP);
-            }
+            // all that the chunk before read from its stage is read (its products: the wait for y's, or for S)
+            if (OUT && ch > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail)) break;
             if (ch > 0 && ch + 1 < chunks) load(ch + 1);
             if (!wait_or_fail(&s_x, ph, &s_fail)) break;
             la::tc_fence_after();
-            auto parts_by = [&](uint32_t to, uint32_t left, uint32_t tile, bool wide) {  // 64 tokens; lo hi + hi lo + hi hi
 #pragma unroll
-                for (int o = wide ? 0 : 2; o < 3; o++)
+            for (int s = 0; s < 4; s++) la::mma_ts(tm + kD3, tm + kX + 8 * s, la::smem_desc(M + s * 32), d2, s > 0);  // hi [hi; lo]
 #pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        la::mma_ts(tm + to, tm + left + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(tile + (o == 1 ? kTileBytes : 0) + s * 32), dM,
-                                   o > (wide ? 0 : 2) || s > 0);
-            };
-            parts_by(kD1, kX, M, true);
+            for (int s = 0; s < 4; s++) la::mma_ts(tm + kD3 + 64, tm + kX + 32 + 8 * s, la::smem_desc(M + s * 32), dP, true);  // lo hi
             la::mma_commit(&s_d2);
             if (!wait_or_fail(&s_u, ph, &s_fail)) break;
             la::tc_fence_after();
@@ -354,10 +461,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             for (int part = 1; part >= 0; part--)
 #pragma unroll
                 for (int s = 0; s < 4; s++)
-                    la::mma_ts(tm + kD3, tm + kS + part * 32 + 8 * s, la::smem_desc(K + s * 2048, kTileBytes), dU, part < 1 || s > 0);
+                    la::mma_ts(tm + kD3, tm + kS + part * 32 + 8 * s, la::smem_desc(at + s * 2048, L::block), d3, part < 1 || s > 0);
             la::mma_commit(&s_d3);
-            if (!SUM) {
-                parts_by(kY, kX, P, PP > 1);
+            if (OUT) {
+#pragma unroll
+                for (int o = PP > 1 ? 0 : 2; o < 3; o++)  // lo hi, hi lo, hi hi
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+                        la::mma_ts(tm + kY, tm + kX + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(P + (o == 1 ? kTileBytes : 0) + s * 32), dP,
+                                   o > (PP > 1 ? 0 : 2) || s > 0);
                 la::mma_commit(&s_y);
             }
         }
@@ -415,24 +527,27 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
     }
 }
 
-template <typename T, int NB, bool SUM> cudaError_t walk_go(const TcWalkArgs& w, cudaStream_t st) {
-    constexpr int bytes = 2 * Stage<T, NB>::bytes + (SUM ? 0 : 2 * kTileBytes);
-    const cudaError_t e = la::allow_smem<k_walk<T, NB, SUM>>(bytes);
+template <typename T, int NB, TcWalkMode MODE> cudaError_t walk_go(const TcWalkArgs& w, cudaStream_t st) {
+    constexpr int bytes = 2 * Stage<NB, kPParts<T>, MODE == kTcY>::bytes +
+                          (MODE == kTcY ? 2 * kTileBytes : MODE == kTcKeep ? state_bytes(NB) + kRowsBytes : 0);
+    const cudaError_t e = la::allow_smem<k_walk<T, NB, MODE>>(bytes);
     if (e != cudaSuccess) return e;
-    const int64_t segs = SUM ? w.plan.K - 1 : w.plan.K;
-    const dim3 grid((unsigned)(ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H * segs), SUM ? 2 : 1);
-    k_walk<T, NB, SUM><<<grid, kThreads, bytes, st>>>(w);
+    const int64_t segs = MODE == kTcSum ? w.plan.K - 1 : w.plan.K;
+    const dim3 grid((unsigned)(ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H * segs), MODE == kTcSum ? 2 : 1);
+    k_walk<T, NB, MODE><<<grid, kThreads, bytes, st>>>(w);
     return cudaGetLastError();
 }
 template <typename T, int NB> cudaError_t walk_mode(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st) {
-    return mode == kTcSum ? walk_go<T, NB, true>(w, st) : walk_go<T, NB, false>(w, st);
+    if (mode == kTcSum) return walk_go<T, NB, kTcSum>(w, st);
+    if (mode == kTcKeep) return walk_go<T, NB, kTcKeep>(w, st);
+    return walk_go<T, NB, kTcY>(w, st);
 }
 
 }  // namespace
 
 cudaError_t launch_tc_walk(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st) {
     if (w.a.dtype == 1) return w.a.N <= 64 ? walk_mode<__half, 1>(w, mode, st) : walk_mode<__half, 2>(w, mode, st);
-    return w.a.N <= 64 ? walk_mode<bf16, 1>(w, mode, st) : walk_mode<bf16, 2>(w, mode, st);
+    return w.a.N <= 64 ? walk_mode<__nv_bfloat16, 1>(w, mode, st) : walk_mode<__nv_bfloat16, 2>(w, mode, st);
 }
 
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st) {
