@@ -35,7 +35,8 @@ struct ImageHead {
     float by;            // the chunk's decay as la::Decay
     int32_t weak;
     float inv_k, inv_q, inv_m, inv_p;  // what undoes the scales of K, Q, M and P
-    float pad[58];
+    float most_bu;       // largest |beta_up|
+    float pad[57];
 };
 static_assert(sizeof(ImageHead) == 1280, "bulk copies are multiples of 16 bytes");
 __host__ __device__ constexpr int image_bytes(int parts) { return (2 + parts) * kTileBytes + (int)sizeof(ImageHead); }

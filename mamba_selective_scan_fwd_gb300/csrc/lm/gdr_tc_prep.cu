@@ -3,9 +3,9 @@
 //
 // One block: one chunk of the heads that share a head of q and k.  [K; Q] K^T is one
 // product of 128 rows.  Per head A = beta e^{c_i - c_j} k_i . k_j below the diagonal;
-// M = (I + A)^{-1} by blocks of 16: the diagonal ones by forward substitution (a thread a
-// column), the others by distance from the diagonal, M_IJ = -M_II sum_K A_IK M_KJ, all in
-// f32 (substitution, not a series in A: A's powers may be large where M is not).
+// M = (I + A)^{-1} in f32 by forward substitution, in blocks (not by a series in A, whose
+// powers may be large where M is not).  One head at a time in a block of four warps: a block's
+// steps wait for one another, and four blocks on an SM cover that.
 #include "gdr_tc.h"
 #include "../simd.cuh"
 #include "tc.cuh"
@@ -24,12 +24,12 @@ using bf16 = __nv_bfloat16;
 
 constexpr int C = kChunk;
 constexpr int LDA = C + 4;
-constexpr int kHeads = 8;  // heads whose decays are made at a time: one a warp
+constexpr int kThreads = 128, kHeads = 4;  // heads whose decays are made at a time: one a warp
 
 // K and Q as they come; then the image as it goes
 template <int NB, int PARTS> struct PrepSmem {
     static constexpr int kq = 0, image = 0, first = NB * 16384 > image_bytes(PARTS) ? NB * 16384 : image_bytes(PARTS), a = first,
-                         m = a + C * LDA * 4, total = m + C * LDA * 4;
+                         total = a + C * LDA * 4;
 };
 
 // 16 values times s as one or two f16 parts, in units u0, u0 + 1 of a row of two tiles
@@ -54,15 +54,36 @@ __device__ __forceinline__ float warp_max(float v) {  // v >= 0
     asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
     return __uint_as_float(m);
 }
-__device__ __forceinline__ float max8(const float* x) {
-    return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+__device__ __forceinline__ float max4(const float* x) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }
+
+// One warp: the products of rows i, i + 8 of `left` with columns c .. c + 3 of `right`, n terms (a multiple of 4).
+__device__ __forceinline__ void product16(const float* left, const float* right, int n, float4 (&out)[2]) {
+    const int i = (threadIdx.x & 31) >> 2, c = (threadIdx.x & 3) * 4;
+    out[0] = out[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < n; k += 4) {
+        const float4 l0 = *reinterpret_cast<const float4*>(left + i * LDA + k), l1 = *reinterpret_cast<const float4*>(left + (i + 8) * LDA + k);
+        const float a0[4] = {l0.x, l0.y, l0.z, l0.w}, a1[4] = {l1.x, l1.y, l1.z, l1.w};
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const float4 r = *reinterpret_cast<const float4*>(right + (k + u) * LDA + c);
+            out[0] = make_float4(fmaf(a0[u], r.x, out[0].x), fmaf(a0[u], r.y, out[0].y), fmaf(a0[u], r.z, out[0].z), fmaf(a0[u], r.w, out[0].w));
+            out[1] = make_float4(fmaf(a1[u], r.x, out[1].x), fmaf(a1[u], r.y, out[1].y), fmaf(a1[u], r.z, out[1].z), fmaf(a1[u], r.w, out[1].w));
+        }
+    }
+}
+__device__ __forceinline__ void put16(float* to, const float4 (&x)[2], float sign) {
+    const int i = (threadIdx.x & 31) >> 2, c = (threadIdx.x & 3) * 4;
+#pragma unroll
+    for (int r = 0; r < 2; r++)
+        *reinterpret_cast<float4*>(to + (i + 8 * r) * LDA + c) = make_float4(sign * x[r].x, sign * x[r].y, sign * x[r].z, sign * x[r].w);
 }
 
-// M = (I + A)^{-1} of a unit lower triangular I + A, 64 x 64, all 256 threads; M's upper
-// blocks hold intermediate products and are not cleared.
-__device__ __forceinline__ void invert(const float* A, float* M) {
-    const int tid = threadIdx.x;
-    if (tid < C) {  // diagonal blocks: thread = column
+// A (64 x 64, below the diagonal; zeros elsewhere) becomes M = (I + A)^{-1} in place, four warps: blocks of 16 by
+// forward substitution (a thread a column), then [[a, 0], [A, b]]: -b A a, of 16 and of 32.
+__device__ __forceinline__ void invert(float* A) {
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid < C) {
         const int d = tid & ~15, j = tid & 15;
         float x[16];
 #pragma unroll
@@ -78,49 +99,46 @@ __device__ __forceinline__ void invert(const float* A, float* M) {
             }
             x[i] = s0 + s1;
         }
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; i++) M[(d + i) * LDA + d + j] = x[i];
+        for (int i = 0; i < 16; i++) A[(d + i) * LDA + d + j] = x[i];
+        __syncwarp();
+        float4 t[2];  // warp w: the block below the diagonal's, between its two
+        float *a = A + 32 * warp * (LDA + 1), *below = a + 16 * LDA;
+        product16(below, a, 16, t);
+        __syncwarp();
+        put16(below, t, 1.0f);
+        __syncwarp();
+        product16(below + 16, below, 16, t);
+        __syncwarp();
+        put16(below, t, -1.0f);
     }
     __syncthreads();
-    const int e = tid & 63, i = e >> 2, c = (e & 3) * 4;
-#pragma unroll
-    for (int dist = 1; dist < 4; dist++) {
-        const int I = 16 * (dist + (tid >> 6)), J = I - 16 * dist;
-        const bool on = (tid >> 6) < 4 - dist;
-        auto product = [&](const float* left, const float* right, int n) {  // row i of left, columns c .. c + 3 of right
-            float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-            for (int k = 0; k < n; k += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(left + i * LDA + k);
-                const float ls[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const float4 r = *reinterpret_cast<const float4*>(right + (k + u) * LDA + c);
-                    s = make_float4(fmaf(ls[u], r.x, s.x), fmaf(ls[u], r.y, s.y), fmaf(ls[u], r.z, s.z), fmaf(ls[u], r.w, s.w));
-                }
-            }
-            return s;
-        };
-        if (on) *reinterpret_cast<float4*>(M + (J + i) * LDA + I + c) = product(A + I * LDA + J, M + J * LDA + J, 16 * dist);
-        __syncthreads();
-        if (on) {
-            const float4 s = product(M + I * LDA + I, M + J * LDA + I, 16);
-            *reinterpret_cast<float4*>(M + (I + i) * LDA + J + c) = make_float4(-s.x, -s.y, -s.z, -s.w);
-        }
-        __syncthreads();
-    }
+    const int r = 16 * (warp >> 1), c = 16 * (warp & 1);  // warp: a block of the lower left 32 x 32
+    float* quarter = A + 32 * LDA;
+    float4 t[2];
+    product16(quarter + r * LDA + c, A + c * LDA + c, 32 - c, t);  // (a is zero above its blocks' diagonal)
+    __syncthreads();
+    put16(quarter + r * LDA + c, t, 1.0f);
+    __syncthreads();
+    product16(quarter + r * LDA + 32, quarter + c, 16 + r, t);
+    __syncthreads();
+    put16(quarter + r * LDA + c, t, -1.0f);
+    __syncthreads();
 }
 
 template <typename T, int NB, int PARTS>
-__global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArgs w) {
+__global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ PrepArgs w) {
     extern __shared__ __align__(1024) char sm[];
     using L = PrepSmem<NB, PARTS>;
     __shared__ __align__(8) uint64_t s_ld, s_mma;
     __shared__ uint32_t s_tm, s_fail;
     __shared__ Two s_c[kHeads][C];
     __shared__ __align__(16) float s_tail[kHeads][C];  // e^{c_e - c_t}, e the end of the token's run of 16
-    __shared__ float s_beta[kHeads][C], s_max[2][8];
+    __shared__ float s_beta[kHeads][C], s_max[2][4];
     __shared__ la::Decay s_by[kHeads];
+    __shared__ float s_bu[kHeads];
+    __shared__ bool s_flat[kHeads];  // no run of 16 leaves 2^-64 .. 2^64
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t id = blockIdx.x;
@@ -132,7 +150,7 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
     const int nv = (int)max((int64_t)0, min((int64_t)C, row_length(a, b) - t0));
     if (nv == 0) return;  // no walk gets here
     char *KQ = sm + L::kq, *I = sm + L::image;
-    float *A = reinterpret_cast<float*>(sm + L::a), *M = reinterpret_cast<float*>(sm + L::m);
+    float* A = reinterpret_cast<float*>(sm + L::a);
     ImageHead* head = reinterpret_cast<ImageHead*>(I + (2 + PARTS) * kTileBytes);
     if (tid == 0) {
         mbar_init(&s_ld, 1);
@@ -149,7 +167,7 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
     if (warp == 1) la::tmem_alloc(&s_tm, 64);
     const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
     auto decays = [&](int64_t h) {  // this warp's head
-        float x[2], e[2];
+        float x[2];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const int t = 2 * lane + i;
@@ -159,11 +177,21 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
         Two c[2];
         la::warp_cumsum<2>(x, c);
         const Two end = {__shfl_sync(kFull, c[1].h, lane | 7), __shfl_sync(kFull, c[1].l, lane | 7)};
+        bool flat = true;
+        float bu = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             s_c[warp][2 * lane + i] = c[i];
-            e[i] = la::ex2(two_diff(end, c[i]));
-            s_tail[warp][2 * lane + i] = e[i];
+            const float rel = two_diff(end, c[i]);
+            flat = flat && fabsf(rel) <= 64.0f;  // (NaN: no)
+            s_tail[warp][2 * lane + i] = ex2a(rel);
+            bu = fmaxf(bu, fabsf(s_beta[warp][2 * lane + i] * ex2a(c[i].h)));
+        }
+        flat = __all_sync(kFull, flat);
+        bu = warp_max(bu);
+        if (lane == 0) {
+            s_flat[warp] = flat;
+            s_bu[warp] = bu;
         }
         // the chunk's decay, in natural units from the same sum (rounded once more: 2^-24 of cl)
         if (lane == 31) s_by[warp] = la::decay_of((c[1].h + c[1].l) * kLn2);
@@ -184,17 +212,18 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
         la::mma_commit(&s_mma);
     }
     __syncwarp();
-    // K (threads 0 .. 127) and Q as f16: unit u of row r of each tile; 64 x 8 NB units each
+    // K and Q as f16: unit tid + 128 i of the 512 of each tile
     float scale_k, scale_q;
-    {
-        const int mine = tid & 127, side = tid >> 7;
+    char* keys = w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384);
+#pragma unroll
+    for (int side = 0; side < 2; side++) {
         float most = 0.0f;
         uint4 x[4 * NB];
 #pragma unroll
         for (int i = 0; i < 4 * NB; i++) {
-            const int row = (mine + 128 * i) >> 3 & 63;
-            x[i] = *reinterpret_cast<const uint4*>(KQ + (i >> 2) * 16384 + side * kTileBytes + ((mine + 128 * i) & 511) * 16);
-            if (row >= nv) x[i] = make_uint4(0, 0, 0, 0);
+            const int at = tid + 128 * (i & 3);
+            x[i] = *reinterpret_cast<const uint4*>(KQ + (i >> 2) * 16384 + side * kTileBytes + at * 16);
+            if (at >> 3 >= nv) x[i] = make_uint4(0, 0, 0, 0);
             const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -203,12 +232,11 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
             }
         }
         most = warp_max(most);
-        if (lane == 0) s_max[0][warp] = most;
+        if (lane == 0) s_max[side][warp] = most;
         __syncthreads();
-        scale_k = la::f16_scale(fmaxf(fmaxf(s_max[0][0], s_max[0][1]), fmaxf(s_max[0][2], s_max[0][3])));
-        scale_q = la::f16_scale(fmaxf(fmaxf(s_max[0][4], s_max[0][5]), fmaxf(s_max[0][6], s_max[0][7])));
-        const float2 s = splat2(side ? scale_q : scale_k);
-        char* to = w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384);
+        const float scale = la::f16_scale(max4(s_max[side]));
+        if (side) scale_q = scale;
+        else scale_k = scale;
         if (split == 0)
 #pragma unroll
             for (int i = 0; i < 4 * NB; i++) {
@@ -216,10 +244,10 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
                 uint32_t r[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const float2 f = mul2(unpack2<T>(v[e]), s);
+                    const float2 f = mul2(unpack2<T>(v[e]), splat2(scale));
                     r[e] = pack2<__half>(f.x, f.y);
                 }
-                *reinterpret_cast<uint4*>(to + (i >> 2) * 16384 + side * kTileBytes + ((mine + 128 * i) & 511) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4*>(keys + (i >> 2) * 16384 + side * kTileBytes + (tid + 128 * (i & 3)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
             }
     }
     ok = la::wait_or_fail(&s_mma, 0, &s_fail) && ok;
@@ -232,84 +260,89 @@ __global__ void __launch_bounds__(256, 3) k_prep(const __grid_constant__ PrepArg
         for (int64_t h = h0; h < min(h_hi, h0 + kHeads); h++) {
             const int hl = (int)(h - h0);
             if (__syncthreads_or(!ok)) break;  // (and: the last head's image has left, s_max is free)
-            // thread: row i of K K^T (warps 0, 1 of a warpgroup) or Q K^T, columns j0 .. j0 + 31: two runs of 16.  A run
-            // left of the row's own takes e^{c_i - c_e} e^{c_e - c_j} with e its end, the row's own an exponential each.
-            const bool is_q = tid & 64;
-            const int i = tid & 63, j0 = (tid >> 7) * 32, last = is_q ? i : i - 1;
-            float s[32];
-            la::tmem_ld32(tm + my + j0, s);
+            // thread: row i of K K^T (warps 0, 1) or Q K^T.  A run of 16 columns takes e^{c_i - c_e} e^{c_e - c_j} with e
+            // its end; the row's own, where that could leave f32's range, an exponential each.
+            const bool is_q = tid >= C;
+            const int i = tid & 63, last = is_q ? i : i - 1;
+            float s[C];
+            la::tmem_ld32(tm + my, *reinterpret_cast<float(*)[32]>(s));
+            la::tmem_ld32(tm + my + 32, *reinterpret_cast<float(*)[32]>(s + 32));
             const Two ci = s_c[hl][i];
-            const float f = i >= nv ? 0.0f : is_q ? 1.0f : s_beta[hl][i];
+            const float f = is_q ? 1.0f : s_beta[hl][i];
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const int c0 = j0 + 16 * r;
-                if (c0 + 16 <= (i & ~15)) {
-                    const float by = f * la::ex2(two_diff(ci, s_c[hl][c0 + 15]));
+            for (int c0 = 0; c0 < C; c0 += 16) {
+                if (c0 <= (i | 15) && (s_flat[hl] || c0 + 16 <= (i & ~15))) {
+                    const float by = f * ex2a(two_diff(ci, s_c[hl][c0 + 15]));
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(&s_tail[hl][c0 + j]);
-                        s[16 * r + j] *= by * t.x;
-                        s[16 * r + j + 1] *= by * t.y;
-                        s[16 * r + j + 2] *= by * t.z;
-                        s[16 * r + j + 3] *= by * t.w;
+                    for (int j = c0; j < c0 + 16; j += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(&s_tail[hl][j]);
+                        const float2 x = mul2(make_float2(s[j], s[j + 1]), mul2(splat2(by), make_float2(t.x, t.y)));
+                        const float2 y = mul2(make_float2(s[j + 2], s[j + 3]), mul2(splat2(by), make_float2(t.z, t.w)));
+                        s[j] = j <= last ? x.x : 0.0f;
+                        s[j + 1] = j + 1 <= last ? x.y : 0.0f;
+                        s[j + 2] = j + 2 <= last ? y.x : 0.0f;
+                        s[j + 3] = j + 3 <= last ? y.y : 0.0f;
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        const float e = c0 + j <= last ? la::ex2(two_diff(ci, s_c[hl][c0 + j])) : 0.0f;
-                        s[16 * r + j] = c0 + j <= last ? f * e * s[16 * r + j] : 0.0f;
+                    for (int j = c0; j < c0 + 16; j++) {
+                        float x = 0.0f;
+                        if (j <= last) x = f * ex2a(two_diff(ci, s_c[hl][j])) * s[j];
+                        s[j] = x;
                     }
                 }
-                if (i >= nv)  // (whatever the row holds)
-#pragma unroll
-                    for (int j = 0; j < 16; j++) s[16 * r + j] = 0.0f;
             }
+            if (i >= nv)  // (whatever the row holds)
+#pragma unroll
+                for (int j = 0; j < C; j++) s[j] = 0.0f;
             float most = 0.0f;
             if (is_q) {
 #pragma unroll
-                for (int j = 0; j < 32; j++) most = fmaxf(most, fabsf(s[j]));
+                for (int j = 0; j < C; j++) most = fmaxf(most, fabsf(s[j]));
                 most = warp_max(most);
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4*>(A + i * LDA + j0 + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+                for (int j = 0; j < C; j += 4)
+                    *reinterpret_cast<float4*>(A + i * LDA + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
             }
             if (lane == 0) s_max[0][warp] = most;
             if (tid < C) {
                 const Two c = s_c[hl][tid], cl = s_c[hl][C - 1];
-                const float up = la::ex2(c.h + c.l);
+                const float up = ex2a(c.h + c.l);
                 head->up[tid] = up;
                 head->beta_up[tid] = s_beta[hl][tid] * up;
-                head->down[tid] = la::ex2(two_diff(cl, c));
+                head->down[tid] = ex2a(two_diff(cl, c));
                 head->beta[tid] = s_beta[hl][tid];
             }
             __syncthreads();
-            const float scale_p = la::f16_scale(fmaxf(fmaxf(s_max[0][2], s_max[0][3]), fmaxf(s_max[0][6], s_max[0][7])));
+            const float scale_p = la::f16_scale(fmaxf(s_max[0][2], s_max[0][3]));
             if (is_q) {
                 char* hi = I + 2 * kTileBytes;
-                put_parts(hi, PARTS > 1 ? hi + kTileBytes : nullptr, i, j0 / 8, s, scale_p);
-                put_parts(hi, PARTS > 1 ? hi + kTileBytes : nullptr, i, j0 / 8 + 2, s + 16, scale_p);
-            }
-            invert(A, M);
-            {
-                const int i = tid >> 2, j0 = (tid & 3) * 16;
-                float x[16], most = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(M + i * LDA + j0 + e);
-                    x[e] = j0 + e <= i ? v.x : 0.0f;
-                    x[e + 1] = j0 + e + 1 <= i ? v.y : 0.0f;
-                    x[e + 2] = j0 + e + 2 <= i ? v.z : 0.0f;
-                    x[e + 3] = j0 + e + 3 <= i ? v.w : 0.0f;
-                    most = fmaxf(most, fmaxf(fmaxf(fabsf(x[e]), fabsf(x[e + 1])), fmaxf(fabsf(x[e + 2]), fabsf(x[e + 3]))));
+                for (int u = 0; u < 4; u++) put_parts(hi, PARTS > 1 ? hi + kTileBytes : nullptr, i, 2 * u, s + 16 * u, scale_p);
+            }
+            invert(A);
+            {
+                const int i = tid >> 1, j0 = (tid & 1) * 32;
+                float x[32], most = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(A + i * LDA + j0 + e);
+                    x[e] = v.x;
+                    x[e + 1] = v.y;
+                    x[e + 2] = v.z;
+                    x[e + 3] = v.w;
+                    most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
                 }
                 most = warp_max(most);
                 if (lane == 0) s_max[1][warp] = most;
                 __syncthreads();
-                const float scale_m = la::f16_scale(max8(s_max[1]));
+                const float scale_m = la::f16_scale(max4(s_max[1]));
                 put_parts(I, I + kTileBytes, i, j0 / 8, x, scale_m);
+                put_parts(I, I + kTileBytes, i, j0 / 8 + 2, x + 16, scale_m);
                 if (tid == 0) {
                     head->by = s_by[hl].by;
+                    head->most_bu = s_bu[hl];
                     head->weak = s_by[hl].weak;
                     head->inv_k = 1.0f / scale_k;
                     head->inv_q = 1.0f / scale_q;
@@ -335,7 +368,7 @@ template <typename T, int NB, int PARTS> cudaError_t prep_go(const PrepArgs& w, 
     constexpr int bytes = PrepSmem<NB, PARTS>::total;
     const cudaError_t e = la::allow_smem<k_prep<T, NB, PARTS>>(bytes);
     if (e != cudaSuccess) return e;
-    k_prep<T, NB, PARTS><<<(unsigned)(w.a.Bsz * w.chunks * w.a.G * w.splits), 256, bytes, st>>>(w);
+    k_prep<T, NB, PARTS><<<(unsigned)(w.a.Bsz * w.chunks * w.a.G * w.splits), kThreads, bytes, st>>>(w);
     return cudaGetLastError();
 }
 template <typename T, int NB> cudaError_t prep_parts(const PrepArgs& w, int parts, cudaStream_t st) {

@@ -4,7 +4,7 @@
 // with the state transposed: the value channels are the 128 lanes of tensor memory, so that
 // a thread owns a channel (half of its N states, half of a chunk's tokens) and every
 // left operand is written by the thread that will read the product's row:
-//   D1 = S^T [K; Q]^T        [128 x 128]  S in two f16 parts, from tensor memory
+//   D1 = S^T K^T             [128 x 64]   S in two f16 parts, from tensor memory
 //   X = beta (V^T - e^c D1)               two parts
 //   D2 = X M^T = U^T         [128 x 2 x 64]  hi [hi; lo] + lo hi
 //   D3 = (e^{cl - c} U)^T K  [128 x N]    two parts;  S <- e^{cl} S + D3, f32 in registers
@@ -32,7 +32,10 @@ using la::unpack2;
 using la::wait_or_fail;
 
 constexpr int C = kChunk;
-constexpr int kStateThreads = 256, kThreads = 256 + 128 + 32;
+constexpr int kStateThreads = 256, kThreads = 512;  // state; output; loads and products (one thread of the last 128)
+// Registers a thread: 128 at launch; the state's threads take what the others leave (2 x 168 + 112 + 56 of 4 x 128).
+template <int N> __device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // columns of tensor memory: S^T K^T; S^T Q^T; X M^T in two halves, then D3; U^T P^T; parts of S, then of
 // e U; parts of X, then of U
@@ -107,10 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     // (the backward's images hold P in two parts)
     constexpr int W = 32 * NB, PP = kPParts<T>, IP = KEEP ? 2 : PP;
     using L = Stage<NB, PP, OUT>;
-    // landed; S; D1; X; D2; U; D3; U^T P^T; read by the third warpgroup: early, late
-    __shared__ __align__(8) uint64_t s_full[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_y, s_early, s_late;
+    // landed; stage free; S; D1; X; D2; U; D3; S^T Q^T; U^T P^T; read by the third warpgroup: early, late
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_q, s_uy, s_y, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
-    __shared__ float s_max[3][2][128], s_um[2][128], s_ss[2][128], s_us[2][128];
+    __shared__ float s_most[2][2][128], s_ud[2][128], s_ss[2][128], s_us[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pl = tid & 127;
     const bool phi = SUM && blockIdx.y == 1;
@@ -126,9 +129,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     const int chunks = (int)max((int64_t)0, (min(len, t_end) - t_begin + C - 1) / C);
 
     if (tid == 0) {
-        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_y}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&s_s, &s_x, &s_u}) mbar_init(bar, kStateThreads / 32);
+        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_q, &s_y}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_s, &s_x, &s_u, &s_uy}) mbar_init(bar, kStateThreads / 32);
         for (uint64_t* bar : {&s_early, &s_late}) mbar_init(bar, 4);
+        for (uint64_t* bar : {&s_free[0], &s_free[1]}) mbar_init(bar, OUT ? 4 : kStateThreads / 32);
         s_fail = 0;
         fence_proxy_async_smem();
     }
@@ -140,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     auto valid = [&](int ch) { return (int)min((int64_t)C, len - (t_begin + (int64_t)ch * C)); };
 
     if (warp < kStateThreads / 32) {
+        take_regs<168>();
         const int half = tid >> 7;
         const int64_t p = p0 + pl;
         const bool mine = p < width;
@@ -154,21 +159,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             for (int n = 0; n < W; n++) S[n] = from && mine && half * W + n < a.N ? from[(half * W + n) * a.P + p] : 0.0f;
         }
         // (a wait that ran out ends no loop here: the others wait at its barriers)
-        // The power of two of this channel's row, from its two threads' largest values (`which` alternates between a
-        // chunk's three exchanges, so that none overwrites what the other thread has not read).
-        auto row_scale = [&](float most, int which) {
-            s_max[which][half][pl] = most;
-            named_sync(1 + (warp & 3), 64);
-            return scale_of(fmaxf(most, s_max[which][half ^ 1][pl]));
-        };
+        // Scales come from bounds that are known before they are needed: the largest values of S and beta V, which
+        // the channel's two threads exchange while a product runs, |k| <= 2^14 inv_k and |M| <= 2^14 inv_m.  Only e U's is
+        // its own largest value: under strong decays that is what is left of the state.
+        auto pair_sync = [&] { named_sync(1 + (warp & 3), 64); };
+        auto max_over = [&](const float (&m)[2][128]) { return fmaxf(m[0][pl], m[1][pl]); };
         bool ok = true;
-        float most = max_abs<W>(S);
+        s_most[0][half][pl] = max_abs<W>(S);
+        pair_sync();
+        float bound = max_over(s_most[0]);  // of |S|
+        pair_sync();
         for (int ch = 0; ch < chunks; ch++) {
             const uint32_t ph = ch & 1;
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const int nv = valid(ch);
-            const float ss = row_scale(most, 0);
+            const float ss = scale_of(bound);
             if (!SUM && half == 0) s_ss[ph][pl] = ss;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
@@ -197,6 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     }
                 }
             }
+            s_most[0][half][pl] = max_abs<W>(S);
+            s_most[1][half][pl] = max_abs<32>(x);
+            pair_sync();
+            const float k_most = 16384.0f * head->inv_k, s_most_ = max_over(s_most[0]);
+            const float x_bound = fmaf(head->most_bu * (64 * NB) * k_most, s_most_, max_over(s_most[1])), xs = scale_of(x_bound);
             ok = ok && wait_or_fail(&s_d1, ph, &s_fail);
             la::tc_fence_after();
             float d[32];
@@ -216,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                 for (int j = 0; j < 32; j++)
                     if (32 * half + j >= nv) x[j] = 0.0f;
             }
-            const float xs = row_scale(max_abs<32>(x), 1);
             // U of the chunk before has left its columns
             if (KEEP && ch > 0) ok = ok && wait_or_fail(&s_late, ph ^ 1, &s_fail);
             {
@@ -239,20 +249,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&head->down[32 * half + j]);
-                d[j] = x[j] * f.x;
-                d[j + 1] = x[j + 1] * f.y;
-                d[j + 2] = x[j + 2] * f.z;
-                d[j + 3] = x[j + 3] * f.w;
+                const float2 y = mul2(make_float2(x[j], x[j + 1]), make_float2(f.x, f.y)), z = mul2(make_float2(x[j + 2], x[j + 3]), make_float2(f.z, f.w));
+                d[j] = y.x;
+                d[j + 1] = y.y;
+                d[j + 2] = z.x;
+                d[j + 3] = z.y;
             }
-            if (!SUM) s_um[half][pl] = max_abs<32>(x);
-            const float us = row_scale(max_abs<32>(d), 2);
-            if (!SUM) {
-                const float uy = scale_of(fmaxf(s_um[0][pl], s_um[1][pl]));
-                if (half == 0) s_us[ph][pl] = uy;
-                const uint32_t to = tm + my + kX + 16 * half;
-                if (KEEP || PP > 1) put2(to, to + 32, x, uy);
-                else put1(to, x, uy);
-            }
+            s_ud[half][pl] = max_abs<32>(d);
+            pair_sync();
+            const float ud_most = max_over(s_ud), us = scale_of(ud_most);
             // the parts of S have been copied
             if (KEEP) ok = ok && wait_or_fail(&s_early, ph, &s_fail);
             {
@@ -261,10 +266,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             }
             la::tmem_wait_st();
             const float by = head->by, keep = head->weak ? 1.0f : 0.0f, inv3 = head->inv_k / us;
+            bound = fmaf(64.0f * k_most, ud_most, s_most_ * (keep + fabsf(by)));
             arrive(&s_u);
+            if (!SUM) {
+                const float uy = scale_of(64.0f * 16384.0f * head->inv_m * x_bound);
+                if (half == 0) s_us[ph][pl] = uy;
+                const uint32_t to = tm + my + kX + 16 * half;
+                if (KEEP || PP > 1) put2(to, to + 32, x, uy);
+                else put1(to, x, uy);
+                la::tmem_wait_st();
+                arrive(&s_uy);
+            }
             ok = ok && wait_or_fail(&s_d3, ph, &s_fail);
             la::tc_fence_after();
-            float m[2] = {};
+            if (!OUT) arrive(&s_free[ph]);
 #pragma unroll
             for (int c = 0; c < NB; c++) {
                 la::tmem_ld32(tm + my + kD3 + half * W + 32 * c, d);
@@ -275,16 +290,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     const float2 f = fma2(splat2(inv3), make_float2(d[n], d[n + 1]), fma2(splat2(by), o, mul2(splat2(keep), o)));
                     S[32 * c + n] = f.x;
                     S[32 * c + n + 1] = f.y;
-                    m[0] = fmaxf(m[0], fabsf(f.x));
-                    m[1] = fmaxf(m[1], fabsf(f.y));
                 }
             }
-            most = fmaxf(m[0], m[1]);
         }
         if (mine && ok) {
             float* to = nullptr;
-            if (phi) to = w.seg_phi + (bh * w.plan.K + seg) * a.N * a.N;
-            else if (SUM) to = w.seg_state + (bh * w.plan.K + seg) * a.N * a.P;
+            if (phi) {  // transposed: column p in a row
+                float* col = w.seg_phi + (bh * w.plan.K + seg) * a.N * a.N + p * a.N;
+#pragma unroll
+                for (int n = 0; n < W; n += 4)
+                    if (half * W + n < a.N) *reinterpret_cast<float4*>(col + half * W + n) = make_float4(S[n], S[n + 1], S[n + 2], S[n + 3]);
+            } else if (SUM) to = w.seg_state + (bh * w.plan.K + seg) * a.N * a.P;
             else if (seg == w.plan.K - 1 && w.last) to = w.last + bh * a.N * a.P;
             if (to)
 #pragma unroll
@@ -292,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     if (half * W + n < a.N) to[(half * W + n) * width + p] = S[n];
         }
     } else if (warp < kStateThreads / 32 + 4) {
+        leave_regs<112>();
         const bool first = tid == kStateThreads;
         if (OUT) {
             T* yp = static_cast<T*>(w.yp) + (b * a.L * a.H + h) * a.P;
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                 const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + ph * L::bytes + L::head);
                 const int nv = valid(ch);
                 wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
-                wait_or_fail(&s_d1, ph, &s_fail);
+                wait_or_fail(&s_q, ph, &s_fail);
                 la::tc_fence_after();
                 float q[64];
                 {
@@ -334,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     }
                 }
                 arrive(&s_late);
+                arrive(&s_free[ph]);
                 fence_proxy_async_smem();
                 named_sync(5, 128);
                 if (first) {
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     la::bulk_commit();
                     w.state_inv[image] = 1.0f / all;
                 }
-                wait_or_fail(&s_u, ph, &s_fail);
+                wait_or_fail(&s_uy, ph, &s_fail);
                 la::tc_fence_after();
                 own = s_us[ph][pl], all = group_min(own, s_red, 5);
                 f = pack2<__half>(all / own, all / own);
@@ -408,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             }
         }
         if (first) la::bulk_wait_all();
-    } else if (lane == 0) {
+    } else {
+        leave_regs<56>();
+        if (tid == kThreads - 96) {  // loads
         const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
         const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(IP);
         auto load = [&](int ch) {
@@ -428,26 +448,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             bulk_load(at + L::image, im, (2 + (OUT ? PP : 0)) * kTileBytes, bar);
             bulk_load(at + L::head, im + (2 + IP) * kTileBytes, (int)sizeof(ImageHead), bar);
         };
-        if (chunks > 0) load(0);
-        if (chunks > 1) load(1);
+        for (int ch = 0; ch < chunks; ch++) {
+            if (ch > 1 && !wait_or_fail(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
+            load(ch);
+        }
+        } else if (tid == kThreads - 128) {  // products
         for (int ch = 0; ch < chunks; ch++) {
             const uint32_t ph = ch & 1;
             const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
-            constexpr int N1 = OUT ? 2 * C : C;  // K, or K and Q
-            constexpr uint32_t d1 = la::mma_desc<__half>(128, N1, false, false), d2 = la::mma_desc<__half>(128, 2 * C, false, false),
+            constexpr uint32_t d2 = la::mma_desc<__half>(128, 2 * C, false, false),
                                dP = la::mma_desc<__half>(128, C, false, false), d3 = la::mma_desc<__half>(128, 64 * NB, false, true);
             if (!wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail) || !wait_or_fail(&s_s, ph, &s_fail)) break;
-            if (OUT && ch > 0 && !wait_or_fail(&s_early, ph ^ 1, &s_fail)) break;  // Q's product of the chunk before is read
             la::tc_fence_after();
+            auto with_state = [&](uint32_t to, uint32_t tile, int parts) {
+                for (int part = parts - 1; part >= 0; part--)
 #pragma unroll
-            for (int part = 1; part >= 0; part--)
-#pragma unroll
-                for (int s = 0; s < 4 * NB; s++)
-                    la::mma_ts(tm + kD1, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(at + (s >> 2) * L::block + (s & 3) * 32), d1, part < 1 || s > 0);
+                    for (int s = 0; s < 4 * NB; s++)
+                        la::mma_ts(tm + to, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(tile + (s >> 2) * L::block + (s & 3) * 32), dP,
+                                   part < parts - 1 || s > 0);
+            };
+            with_state(kD1, at, 2);
             la::mma_commit(&s_d1);
-            // all that the chunk before read from its stage is read (its products: the wait for y's, or for S)
-            if (OUT && ch > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail)) break;
-            if (ch > 0 && ch + 1 < chunks) load(ch + 1);
+            if (OUT) {  // Q's product of the chunk before is read
+                if (ch > 0 && !wait_or_fail(&s_early, ph ^ 1, &s_fail)) break;
+                with_state(kQ, at + kTileBytes, PP);
+                la::mma_commit(&s_q);
+            }
             if (!wait_or_fail(&s_x, ph, &s_fail)) break;
             la::tc_fence_after();
 #pragma unroll
@@ -464,6 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                     la::mma_ts(tm + kD3, tm + kS + part * 32 + 8 * s, la::smem_desc(at + s * 2048, L::block), d3, part < 1 || s > 0);
             la::mma_commit(&s_d3);
             if (OUT) {
+                if (!wait_or_fail(&s_uy, ph, &s_fail) || (ch > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail))) break;
+                la::tc_fence_after();
 #pragma unroll
                 for (int o = PP > 1 ? 0 : 2; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
@@ -473,57 +501,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                 la::mma_commit(&s_y);
             }
         }
+        }
     }
     __syncwarp();
-    uint64_t* const bars[6] = {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_y};
+    uint64_t* const bars[7] = {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_q, &s_y};
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
 
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
-// from.  A block: 16 columns of one head's state, kept in shared memory.
+// from.  A block: 8 columns of one head's state, in shared memory, thread = row and four of them; the next Phi
+// (transposed) is on its way while one is used.  65536 tokens x 8 heads, 19 segments: PLACEHOLDER us.
+constexpr int kCarryCols = 8;
 __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
-    constexpr int NC = 16;
-    __shared__ float s[2][la::kMaxN][NC];
+    extern __shared__ __align__(16) float phi[];  // [2][N][N]
+    __shared__ __align__(16) float s[2][la::kMaxN][kCarryCols];
+    __shared__ __align__(8) uint64_t s_full[2];
+    __shared__ uint32_t s_fail;
     const Args& a = w.a;
-    const int tid = threadIdx.x, N = (int)a.N;
-    const int64_t ptiles = (a.P + NC - 1) / NC, p0 = blockIdx.x % ptiles * NC, bh = blockIdx.x / ptiles;
-    const int c = tid % NC, r = tid / NC;
-    const bool mine = p0 + c < a.P;
-    float own[la::kMaxN / 16];
-#pragma unroll
-    for (int u = 0; u < la::kMaxN / 16; u++) {
-        const int n = r + 16 * u;
-        s[0][n][c] = mine && n < N && w.init ? w.init[(bh * N + n) * a.P + p0 + c] : 0.0f;
+    const int tid = threadIdx.x, N = (int)a.N, n = tid >> 1, c = (tid & 1) * 4;
+    const int64_t ptiles = (a.P + kCarryCols - 1) / kCarryCols, p0 = blockIdx.x % ptiles * kCarryCols, bh = blockIdx.x / ptiles;
+    const int K = (int)w.plan.K;
+    if (tid == 0) {
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        s_fail = 0;
+        fence_proxy_async_smem();
     }
-    for (int64_t k = 0; k < w.plan.K; k++) {
-        float* at = w.seg_state + (bh * w.plan.K + k) * N * a.P + p0 + c;
-        const float* phi = w.seg_phi + (bh * w.plan.K + k) * N * N;
-        float(*now)[NC] = s[k & 1], (*next)[NC] = s[~k & 1];
-#pragma unroll
-        for (int u = 0; u < la::kMaxN / 16; u++) {
-            const int n = r + 16 * u;
-            own[u] = mine && n < N && k + 1 < w.plan.K ? at[n * a.P] : 0.0f;
+    auto load = [&](int k) {
+        mbar_expect_tx(&s_full[k & 1], N * N * 4);
+        bulk_load(phi + (k & 1) * N * N, w.seg_phi + (bh * K + k) * N * N, N * N * 4, &s_full[k & 1]);
+    };
+    const bool mine = n < N;  // (P is a multiple of 8)
+    float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (mine && w.init) x = *reinterpret_cast<const float4*>(w.init + (bh * N + n) * a.P + p0 + c);
+    __syncthreads();
+    if (tid == 0) load(0);
+    for (int k = 0; k < K; k++) {
+        float4* at = reinterpret_cast<float4*>(w.seg_state + ((bh * K + k) * N + n) * a.P + p0 + c);
+        float4 e = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (mine) {
+            if (k + 1 < K) e = *at;
+            *reinterpret_cast<float4*>(&s[k & 1][n][c]) = x;
+            *at = x;
         }
-        __syncthreads();
+        if (k + 1 == K) break;
+        __syncthreads();  // (the Phi before is used)
+        if (tid == 0 && k + 2 < K) load(k + 1);
+        wait_or_fail(&s_full[k & 1], (k >> 1) & 1, &s_fail);
+        const float* f = phi + (k & 1) * N * N + n;
+        float4 y[2] = {e, {0.0f, 0.0f, 0.0f, 0.0f}};
+        if (mine)
+#pragma unroll 8
+            for (int m = 0; m < N; m += 2)
 #pragma unroll
-        for (int u = 0; u < la::kMaxN / 16; u++) {
-            const int n = r + 16 * u;
-            if (mine && n < N) at[n * a.P] = now[n][c];
-        }
-        if (k + 1 == w.plan.K) break;
-#pragma unroll 2
-        for (int m = 0; m < N; m += 4) {
-            const float x[4] = {now[m][c], now[m + 1][c], now[m + 2][c], now[m + 3][c]};
-#pragma unroll
-            for (int u = 0; u < la::kMaxN / 16; u++) {
-                const int n = r + 16 * u;
-                if (n >= N) continue;
-                const float4 f = *reinterpret_cast<const float4*>(phi + n * N + m);
-                own[u] = fmaf(f.x, x[0], fmaf(f.y, x[1], fmaf(f.z, x[2], fmaf(f.w, x[3], own[u]))));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < la::kMaxN / 16; u++) next[r + 16 * u][c] = own[u];
+                for (int u = 0; u < 2; u++) {
+                    const float p = f[(m + u) * N];
+                    const float4 z = *reinterpret_cast<const float4*>(&s[k & 1][m + u][c]);
+                    y[u] = make_float4(fmaf(p, z.x, y[u].x), fmaf(p, z.y, y[u].y), fmaf(p, z.z, y[u].z), fmaf(p, z.w, y[u].w));
+                }
+        x = make_float4(y[0].x + y[1].x, y[0].y + y[1].y, y[0].z + y[1].z, y[0].w + y[1].w);
+    }
+    __syncthreads();
+    if (tid == 0 && s_fail) {
+        atomicOr(w.status, kDevWaitTimeout);
+        for (int i = 0; i < 2; i++)
+            for (uint32_t ph = 0; ph < 2; ph++) mbar_wait(&s_full[i], ph, la::kDrainLimitNs);
     }
 }
 
@@ -551,7 +593,10 @@ cudaError_t launch_tc_walk(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st
 }
 
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st) {
-    k_carry<<<(unsigned)(ceil_div(w.a.P, 16) * w.a.Bsz * w.a.H), 256, 0, st>>>(w);
+    const int bytes = 2 * (int)(w.a.N * w.a.N) * 4;
+    const cudaError_t e = la::allow_smem<k_carry>(2 * la::kMaxN * la::kMaxN * 4);
+    if (e != cudaSuccess) return e;
+    k_carry<<<(unsigned)(ceil_div(w.a.P, kCarryCols) * w.a.Bsz * w.a.H), 256, bytes, st>>>(w);
     return cudaGetLastError();
 }
 
