@@ -37,8 +37,8 @@ constexpr int kStateThreads = 256, kThreads = 512;  // state; output; loads and 
 template <int N> __device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// columns of tensor memory: S^T K^T; S^T Q^T; X M^T in two halves, then D3; U^T P^T; parts of S, then of
-// e U; parts of X, then of U
+// columns of tensor memory: S^T K^T, then parts of U; S^T Q^T; X M^T in two halves, then D3; U^T P^T; parts of S;
+// parts of X, then of e U
 constexpr uint32_t kD1 = 0, kQ = 64, kD3 = 128, kY = 256, kS = 320, kX = 448;
 
 template <typename T> constexpr int kPParts = kF16<T> ? 2 : 1;  // of P and U in y's product
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     // (the backward's images hold P in two parts)
     constexpr int W = 32 * NB, PP = kPParts<T>, IP = KEEP ? 2 : PP;
     using L = Stage<NB, PP, OUT>;
-    // landed; stage free; S; D1; X; D2; U; D3; S^T Q^T; U^T P^T; read by the third warpgroup: early, late
-    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_q, s_uy, s_y, s_early, s_late;
+    // landed; stage free; S (each half); D1; X; D2; U; D3; S^T Q^T; U^T P^T; read by the third warpgroup: early, late
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s[2], s_d1, s_x, s_d2, s_u, s_d3[2], s_q, s_uy, s_y, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
     __shared__ float s_most[2][2][128], s_ud[2][128], s_ss[2][128], s_us[2][128];
     const Args& a = w.a;
@@ -129,9 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     const int chunks = (int)max((int64_t)0, (min(len, t_end) - t_begin + C - 1) / C);
 
     if (tid == 0) {
-        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_q, &s_y}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&s_s, &s_x, &s_u, &s_uy}) mbar_init(bar, kStateThreads / 32);
-        for (uint64_t* bar : {&s_early, &s_late}) mbar_init(bar, 4);
+        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3[0], &s_d3[1], &s_q, &s_y}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_x, &s_u, &s_uy}) mbar_init(bar, kStateThreads / 32);
+        for (uint64_t* bar : {&s_s[0], &s_s[1], &s_early, &s_late}) mbar_init(bar, 4);
         for (uint64_t* bar : {&s_free[0], &s_free[1]}) mbar_init(bar, OUT ? 4 : kStateThreads / 32);
         s_fail = 0;
         fence_proxy_async_smem();
@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const int nv = valid(ch);
             const float ss = scale_of(bound);
+            if (KEEP && ch > 0) ok = ok && wait_or_fail(&s_early, ph ^ 1, &s_fail);  // the last parts have been copied
             if (!SUM && half == 0) s_ss[ph][pl] = ss;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                 put2(to, to + 32 * NB, S + 32 * c, ss);
             }
             la::tmem_wait_st();
-            arrive(&s_s);
+            arrive(&s_s[half]);
             ok = ok && wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
             const float inv1 = -head->inv_k / ss;
             float x[32];
@@ -227,8 +228,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                 for (int j = 0; j < 32; j++)
                     if (32 * half + j >= nv) x[j] = 0.0f;
             }
-            // U of the chunk before has left its columns
-            if (KEEP && ch > 0) ok = ok && wait_or_fail(&s_late, ph ^ 1, &s_fail);
             {
                 const uint32_t to = tm + my + kX + 16 * half;
                 put2(to, to + 32, x, xs);
@@ -258,10 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             s_ud[half][pl] = max_abs<32>(d);
             pair_sync();
             const float ud_most = max_over(s_ud), us = scale_of(ud_most);
-            // the parts of S have been copied
-            if (KEEP) ok = ok && wait_or_fail(&s_early, ph, &s_fail);
             {
-                const uint32_t to = tm + my + kS + 16 * half;
+                const uint32_t to = tm + my + kX + 16 * half;
                 put2(to, to + 32, d, us);
             }
             la::tmem_wait_st();
@@ -271,13 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             if (!SUM) {
                 const float uy = scale_of(64.0f * 16384.0f * head->inv_m * x_bound);
                 if (half == 0) s_us[ph][pl] = uy;
-                const uint32_t to = tm + my + kX + 16 * half;
+                const uint32_t to = tm + my + kD1 + 16 * half;
                 if (KEEP || PP > 1) put2(to, to + 32, x, uy);
                 else put1(to, x, uy);
                 la::tmem_wait_st();
                 arrive(&s_uy);
             }
-            ok = ok && wait_or_fail(&s_d3, ph, &s_fail);
+            ok = ok && wait_or_fail(&s_d3[half], ph, &s_fail);
             la::tc_fence_after();
             if (!OUT) arrive(&s_free[ph]);
 #pragma unroll
@@ -370,7 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             for (int ch = 0; ch < chunks; ch++) {
                 const uint32_t ph = ch & 1;
                 const int64_t image = (bh * ptiles + pt) * w.chunks + c_begin + ch;
-                wait_or_fail(&s_s, ph, &s_fail);
+                wait_or_fail(&s_s[0], ph, &s_fail);
+                wait_or_fail(&s_s[1], ph, &s_fail);
                 la::tc_fence_after();
                 // the parts of S under one scale: what the largest channel's is
                 float own = s_ss[ph][pl], all = group_min(own, s_red, 5);
@@ -402,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
 #pragma unroll
                 for (int part = 0; part < 2; part++) {
                     float x[32];
-                    la::tmem_ld32(tm + my + kX + 32 * part, x);
+                    la::tmem_ld32(tm + my + kD1 + 32 * part, x);
 #pragma unroll
                     for (int j = 0; j < 32; j++) {
                         const uint32_t r = hmul2(__float_as_uint(x[j]), f);
@@ -457,21 +455,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             const uint32_t ph = ch & 1;
             const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
             constexpr uint32_t d2 = la::mma_desc<__half>(128, 2 * C, false, false),
-                               dP = la::mma_desc<__half>(128, C, false, false), d3 = la::mma_desc<__half>(128, 64 * NB, false, true);
-            if (!wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail) || !wait_or_fail(&s_s, ph, &s_fail)) break;
-            la::tc_fence_after();
-            auto with_state = [&](uint32_t to, uint32_t tile, int parts) {
+                               dP = la::mma_desc<__half>(128, C, false, false), d3 = la::mma_desc<__half>(128, 64, false, true);
+            if (!wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail)) break;
+            // terms of half the states: the halves arrive one after the other, as D3's did
+            auto with_state = [&](uint32_t to, uint32_t tile, int parts, int half) {
                 for (int part = parts - 1; part >= 0; part--)
 #pragma unroll
-                    for (int s = 0; s < 4 * NB; s++)
+                    for (int i = 0; i < 2 * NB; i++) {
+                        const int s = half * 2 * NB + i;
                         la::mma_ts(tm + to, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(tile + (s >> 2) * L::block + (s & 3) * 32), dP,
-                                   part < parts - 1 || s > 0);
+                                   half > 0 || part < parts - 1 || i > 0);
+                    }
             };
-            with_state(kD1, at, 2);
+            // U of the chunk before has left its columns
+            if (!SUM && ch > 0 && !wait_or_fail(OUT ? &s_y : &s_late, ph ^ 1, &s_fail)) break;
+            if (!wait_or_fail(&s_s[0], ph, &s_fail)) break;
+            la::tc_fence_after();
+            with_state(kD1, at, 2, 0);
+            if (!wait_or_fail(&s_s[1], ph, &s_fail)) break;
+            la::tc_fence_after();
+            with_state(kD1, at, 2, 1);
             la::mma_commit(&s_d1);
             if (OUT) {  // Q's product of the chunk before is read
                 if (ch > 0 && !wait_or_fail(&s_early, ph ^ 1, &s_fail)) break;
-                with_state(kQ, at + kTileBytes, PP);
+                with_state(kQ, at + kTileBytes, PP, 0);
+                with_state(kQ, at + kTileBytes, PP, 1);
                 la::mma_commit(&s_q);
             }
             if (!wait_or_fail(&s_x, ph, &s_fail)) break;
@@ -484,11 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
             if (!wait_or_fail(&s_u, ph, &s_fail)) break;
             la::tc_fence_after();
 #pragma unroll
-            for (int part = 1; part >= 0; part--)
+            for (int n = 0; n < NB; n++) {
 #pragma unroll
-                for (int s = 0; s < 4; s++)
-                    la::mma_ts(tm + kD3, tm + kS + part * 32 + 8 * s, la::smem_desc(at + s * 2048, L::block), d3, part < 1 || s > 0);
-            la::mma_commit(&s_d3);
+                for (int part = 1; part >= 0; part--)
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+                        la::mma_ts(tm + kD3 + 64 * n, tm + kX + part * 32 + 8 * s, la::smem_desc(at + n * L::block + s * 2048), d3, part < 1 || s > 0);
+                la::mma_commit(&s_d3[n]);
+            }
+            if (NB == 1) la::mma_commit(&s_d3[1]);
             if (OUT) {
                 if (!wait_or_fail(&s_uy, ph, &s_fail) || (ch > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail))) break;
                 la::tc_fence_after();
@@ -496,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
                 for (int o = PP > 1 ? 0 : 2; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
                     for (int s = 0; s < 4; s++)
-                        la::mma_ts(tm + kY, tm + kX + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(P + (o == 1 ? kTileBytes : 0) + s * 32), dP,
+                        la::mma_ts(tm + kY, tm + kD1 + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(P + (o == 1 ? kTileBytes : 0) + s * 32), dP,
                                    o > (PP > 1 ? 0 : 2) || s > 0);
                 la::mma_commit(&s_y);
             }
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
         }
     }
     __syncwarp();
-    uint64_t* const bars[7] = {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_q, &s_y};
+    uint64_t* const bars[8] = {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3[0], &s_d3[1], &s_q, &s_y};
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
 
