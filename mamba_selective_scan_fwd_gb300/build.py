@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "dispatch.cu", "fwd_f32.cu", "fwd_bf16.cu", "fwd_f16.cu", "
 # of q and k (include/ss_gdr.h): kernels of their own, in a folder of their own, outside source_digest() (which identifies the scan's kernels)
 LM_SOURCES = ["lm/la_api.cu", "lm/la_f32.cu", "lm/la_tc_fwd.cu", "lm/la_tc_bwd.cu", "lm/la_step.cu", "lm/gnorm.cu",
               "lm/gdr_api.cu", "lm/gdr_f32.cu", "lm/gdr_step.cu", "lm/qknorm.cu",
-              "lm/gdr_tc_prep.cu", "lm/gdr_tc_walk.cu"]
+              "lm/gdr_tc_prep.cu", "lm/gdr_tc_walk.cu", "lm/gdr_tc_chunk.cu"]
 
 
 def nvcc() -> str:

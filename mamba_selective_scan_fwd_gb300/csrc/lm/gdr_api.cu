@@ -168,6 +168,102 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     return launch_tc_walk(w, kTcY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
+struct BwdTc {
+    int64_t chunks;
+    int splits;
+    size_t keys, images, before, after, us, xs, before_inv, after_inv, u_inv, x_inv, dq, dk;
+};
+BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
+    BwdTc f;
+    f.chunks = ceil_div(L, kChunk);
+    f.splits = prep_splits(Bsz * f.chunks * G, H / G);
+    const size_t heads = (size_t)Bsz * H * f.chunks, tiles = heads * ceil_div(P, kTileP);
+    f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
+    f.images = l.take(heads * image_bytes(2));
+    f.before = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
+    f.after = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
+    f.us = l.take(tiles * kRowsBytes);
+    f.xs = l.take(tiles * kRowsBytes);
+    for (size_t* x : {&f.before_inv, &f.after_inv, &f.u_inv, &f.x_inv}) *x = l.take(tiles * 4);
+    const size_t part = f.splits > 1 ? (size_t)f.splits * Bsz * L * G * N * 4 : 0;
+    f.dq = l.take(part);
+    f.dk = l.take(part);
+    return f;
+}
+
+// Backward on the tensor cores; *ran tells whether the inputs allow it.
+int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* ran) {
+    *ran = false;
+    if (!tc_sizes(a.L, a.N, a.P, a.dtype) || !tc_input(a.q, a.L, a.Bsz) || !tc_input(a.k, a.L, a.Bsz) || !tc_input(a.v, a.L, a.Bsz) ||
+        !tc_input(a.dy, a.L, a.Bsz))
+        return SS_OK;
+    const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!encode) return SS_OK;
+    Layout l;
+    const BwdTc f = bwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
+    char* ws = static_cast<char*>(d.workspace);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    PrepArgs p = {};
+    TcWalkArgs w = {};
+    TcBackArgs r = {};
+    TcChunkArgs c = {};
+    if (!tc_map(encode, &p.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) || !tc_map(encode, &p.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
+        !tc_map(encode, &w.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) || !tc_map(encode, &r.dy, a.dy, a.H, a.P, a.L, a.Bsz, a.dtype))
+        return SS_OK;
+    const int rc = device_status_word(&w.status);
+    if (rc != SS_OK) return rc;
+    *ran = true;
+    p.a = a;
+    p.chunks = f.chunks;
+    p.splits = f.splits;
+    p.keys = ws + f.keys;
+    p.images = ws + f.images;
+    p.status = w.status;
+    w.a = a;
+    w.plan = {1, f.chunks};
+    w.chunks = f.chunks;
+    w.keys = p.keys;
+    w.images = p.images;
+    w.init = a.h0;
+    w.states = ws + f.before;
+    w.us = ws + f.us;
+    w.state_inv = f32(f.before_inv);
+    w.u_inv = f32(f.u_inv);
+    r.init = a.dlast;
+    r.last = d.dh0;
+    r.states = ws + f.after;
+    r.xs = ws + f.xs;
+    r.state_inv = f32(f.after_inv);
+    r.x_inv = f32(f.x_inv);
+    c.dy = r.dy;
+    c.a = a;
+    c.chunks = f.chunks;
+    c.splits = f.splits;
+    c.keys = p.keys;
+    c.images = p.images;
+    c.before = w.states;
+    c.after = r.states;
+    c.us = w.us;
+    c.xs = r.xs;
+    c.before_inv = w.state_inv;
+    c.after_inv = r.state_inv;
+    c.u_inv = w.u_inv;
+    c.x_inv = r.x_inv;
+    c.dq = d.dq;
+    c.dk = d.dk;
+    c.dv = d.dv;
+    c.dq_part = f32(f.dq);
+    c.dk_part = f32(f.dk);
+    c.dg = d.dg;
+    c.dbeta = d.dbeta;
+    c.status = w.status;
+    if (launch_prep(p, 2, st) != cudaSuccess || launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (f.splits > 1 &&
+        la::launch_sum_parts(c.dq_part, d.dq, c.dk_part, d.dk, f.splits, a.Bsz * a.L * a.G * a.N, a.dtype, st) != cudaSuccess)
+        return SS_ERR_CUDA;
+    return SS_OK;
+}
+
 // The state that no token changes: a copy of the incoming one, or zeros.
 int pass_state(float* to, const float* from, int64_t Bsz, int64_t H, int64_t N, int64_t P, cudaStream_t st) {
     const size_t bytes = (size_t)Bsz * H * N * P * 4;
@@ -251,9 +347,10 @@ int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
 
 size_t ss_gdr_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
-    Layout l;
+    Layout l, t;
     bwd32_layout(l, Bsz, L, H, G, N, P);
-    return l.total;
+    if (tc_sizes(L, N, P, dtype)) bwdtc_layout(t, Bsz, L, H, G, N, P);
+    return l.total > t.total ? l.total : t.total;
 }
 
 int ss_gdr_bwd(const ss_gdr_bwd_desc* d, void* stream) {
@@ -276,6 +373,9 @@ int ss_gdr_bwd(const ss_gdr_bwd_desc* d, void* stream) {
     Args a = args_of(*d);
     a.dy = {d->dy, d->dy_token, d->dy_batch};
     a.dlast = d->dlast_state;
+    bool ran;
+    const int tc = tc_backward(a, *d, st, &ran);
+    if (ran || tc != SS_OK) return tc;
     char* ws = static_cast<char*>(d->workspace);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     Layout l;

@@ -35,8 +35,8 @@ struct ImageHead {
     float by;            // the chunk's decay as la::Decay
     int32_t weak;
     float inv_k, inv_q, inv_m, inv_p;  // what undoes the scales of K, Q, M and P
-    float most_bu;       // largest |beta_up|
-    float pad[57];
+    float most_bu, most_down;  // largest |beta_up|, largest down
+    float pad[56];
 };
 static_assert(sizeof(ImageHead) == 1280, "bulk copies are multiples of 16 bytes");
 __host__ __device__ constexpr int image_bytes(int parts) { return (2 + parts) * kTileBytes + (int)sizeof(ImageHead); }
@@ -76,6 +76,28 @@ struct TcWalkArgs {
     float *state_inv, *u_inv;  // what undoes each image's scale
     int* status;
 };
+// The backward's walk over the chunks from the last: x and, as images like the forward's, the state's
+// adjoint after each chunk and X.
+struct TcBackArgs {
+    CUtensorMap dy;
+    const float* init;  // gradient of the last state, or null
+    float* last;        // dh0, or null
+    char *states, *xs;
+    float *state_inv, *x_inv;
+};
+// What is left of the backward, one chunk at a time.
+struct TcChunkArgs {
+    CUtensorMap dy;
+    Args a;
+    int64_t chunks;
+    int splits;         // parts a group's heads are divided into
+    const char *keys, *images, *before, *after, *us, *xs;
+    const float *before_inv, *after_inv, *u_inv, *x_inv;
+    void *dq, *dk, *dv;
+    float *dq_part, *dk_part;  // [splits, Bsz, L, G, N], with splits > 1
+    float *dg, *dbeta;
+    int* status;
+};
 // f16 images in two parts, one scale each: the state transposed, [part][64 columns n][128 rows p][64], and U, [part][64
 // columns p][64 rows t][64].
 __host__ __device__ constexpr int state_bytes(int nb) { return 2 * nb * 2 * kTileBytes; }
@@ -85,6 +107,8 @@ constexpr int kRowsBytes = 4 * kTileBytes;
 enum TcWalkMode { kTcY, kTcSum, kTcKeep };
 cudaError_t launch_tc_walk(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st);
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st);
+cudaError_t launch_tc_walks(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st);  // kTcKeep and the backward's, at once
+cudaError_t launch_tc_chunks(const TcChunkArgs& c, cudaStream_t st);
 
 }  // namespace gdr
 

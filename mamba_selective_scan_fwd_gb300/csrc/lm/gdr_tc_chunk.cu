@@ -1,0 +1,521 @@
+// Gated delta rule's backward on the tensor cores: one chunk of the heads that share a head
+// of q and k, from the walks' images of H (state before the chunk), R (adjoint after it), U and X.
+//
+// Rows 0 .. 63 of every product belong to the tokens' keys, 64 .. 127 to their queries:
+//   [K; Q] K^T                       kk, qk
+//   [X; dY] U^T                      F = -beta e^{c_i - c_j} x_i . u_j (j < i),  E = scale e^{c_i - c_j} dy_i . u_j (j <= i)
+//   [X; dY] H^T                      -beta e^c of it: k's share by H; scale e^c of it: q's
+//   U R^T                            e^{cl - c} of it: k's share by R
+//   [F; E] K,  [F; E]^T [K; Q]       the pairs' shares
+// dq and dk stay in registers over the heads.  dv = beta x;  dbeta_i = x_i . v_i - e^{c_i} k_i . H x_i - sum_j e^{c_i - c_j}
+// (k_i . k_j) (x_i . u_j);  dg is made of every path's two ends (gdr_f32.cu has the formula).
+//
+// Roundings: E and F enter dq's and dk's products as one f16 (2^-12 of terms of a 16-bit output).
+// H, R, U and X come in two f16 parts (22 bits), and dg and dbeta take all else in f32.
+#include "gdr_tc.h"
+#include "../simd.cuh"
+#include "tc.cuh"
+#include "gdr_dev.cuh"
+
+namespace ss {
+namespace gdr {
+namespace {
+
+using la::pack2;
+using la::Two;
+using la::two_diff;
+using la::unit;
+using la::unpack2;
+using la::wait_or_fail;
+
+constexpr int C = kChunk;
+constexpr int kThreads = 256;
+
+template <int NB> struct ChunkSmem {
+    // K and Q by turns; [X; dY] in high and low parts, two blocks of 64 columns each; U, high and low by turns; H or R,
+    // for each 64 states high and low; [F; E]
+    static constexpr int keys = 0, z = NB * 16384, zl = z + 32768, u = zl + 32768, s = u + 32768, ef = s + NB * 32768, head = ef + 16384,
+                         total = head + 2048;
+};
+constexpr uint32_t cE = 0, cQK = 64, cT = 0, cZ = 128, cR = 256, cK = 384;
+
+__device__ __forceinline__ float warp_max(float v) {
+    uint32_t m;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
+    return __uint_as_float(m);
+}
+template <int W> __device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+// Sum over the lanes of x[i] for every i: lane i gets the sum of x[i].
+__device__ __forceinline__ float column_sums(float (&x)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; i++) {
+            const float keep = up ? x[i + o] : x[i], send = up ? x[i] : x[i + o];
+            x[i] = keep + __shfl_xor_sync(kFull, send, o);
+        }
+    }
+    return x[0];
+}
+// eight f16 values . eight f32 values
+__device__ __forceinline__ float dot8(uint4 k, const float* x, float sum) {
+    const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float2 f = unpack2<__half>(v[e]);
+        sum = fmaf(f.x, x[2 * e], fmaf(f.y, x[2 * e + 1], sum));
+    }
+    return sum;
+}
+
+template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_chunk(const __grid_constant__ TcChunkArgs w) {
+    extern __shared__ __align__(1024) char sm[];
+    using L = ChunkSmem<NB>;
+    constexpr int W = 32 * NB;  // states of a thread
+    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_c1, s_c2[2], s_c3, s_c4;
+    __shared__ uint32_t s_tm, s_fail;
+    __shared__ Two s_c[C];
+    __shared__ __align__(16) float s_tail[C];
+    __shared__ bool s_flat;
+    __shared__ float s_max[2][8], s_row[2][128], s_col[8][32], s_dot[3][2][128], s_a[C], s_b[C], s_db[C], s_thr[8];
+    const Args& a = w.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = tid & 127, half = tid >> 7;
+    int64_t id = blockIdx.x;
+    const int64_t split = id % w.splits;
+    id /= w.splits;
+    const int64_t gq = id % a.G;
+    id /= a.G;
+    const int64_t chunk = id % w.chunks, b = id / w.chunks, t0 = chunk * C, rep = a.H / a.G;
+    const int nt = (int)min((int64_t)C, a.L - t0);
+    const int nv = (int)max((int64_t)0, min((int64_t)nt, row_length(a, b) - t0));
+    const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
+    const int64_t ptiles = (a.P + kTileP - 1) / kTileP;
+    const bool q_side = r >= C;
+    const int tok = r & (C - 1);
+    const int n0 = half * W;  // this thread's states
+    float acc[W];
+#pragma unroll
+    for (int n = 0; n < W; n++) acc[n] = 0.0f;
+    auto put_out = [&] {  // dq's or dk's row
+        if (tok >= nt) return;
+        const int64_t at = ((b * a.L + t0 + tok) * a.G + gq) * a.N + n0;
+        const bool on = tok < nv;
+#pragma unroll
+        for (int n = 0; n < W; n += 8) {
+            if (n0 + n >= a.N) break;
+            if (w.splits > 1) {
+                float* to = (q_side ? w.dq_part : w.dk_part) + split * a.Bsz * a.L * a.G * a.N + at + n;
+#pragma unroll
+                for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<float4*>(to + e) = on ? make_float4(acc[n + e], acc[n + e + 1], acc[n + e + 2], acc[n + e + 3]) : make_float4(0, 0, 0, 0);
+            } else {
+                T* to = static_cast<T*>(q_side ? w.dq : w.dk) + at + n;
+                uint32_t x[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) x[e] = on ? pack2<T>(acc[n + 2 * e], acc[n + 2 * e + 1]) : 0;
+                *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        }
+    };
+    auto put_dv = [&](int64_t h, int64_t p0, int row, int u, uint4 x) {
+        if (row < nt && p0 + 8 * u < a.P)
+            *reinterpret_cast<uint4*>(static_cast<T*>(w.dv) + ((b * a.L + t0 + row) * a.H + h) * a.P + p0 + 8 * u) = x;
+    };
+    if (nv == 0) {
+        put_out();
+        for (int64_t h = h_lo; h < h_hi; h++) {
+            for (int64_t p0 = 0; p0 < a.P; p0 += kTileP)
+                for (int i = tid; i < C * 16; i += kThreads) put_dv(h, p0, i >> 4, i & 15, make_uint4(0, 0, 0, 0));
+            if (tid < nt) {
+                const int64_t at = (b * a.L + t0 + tid) * a.H + h;
+                if (w.dg) w.dg[at] = 0.0f;
+                w.dbeta[at] = 0.0f;
+            }
+        }
+        return;
+    }
+    char *KQ = sm + L::keys, *Z = sm + L::z, *Zl = sm + L::zl, *U = sm + L::u, *S = sm + L::s, *EF = sm + L::ef;
+    const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + L::head);
+    if (tid == 0) {
+        for (uint64_t* bar : {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4}) mbar_init(bar, 1);
+        s_fail = 0;
+        fence_proxy_async_smem();
+    }
+    if (warp == 0) la::tmem_alloc(&s_tm, 512);
+    for (int i = tid; i < 2 * C * 8; i += kThreads)  // dY has no low part
+        *reinterpret_cast<uint4*>(Zl + (i >> 9) * 16384 + kTileBytes + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    la::tc_fence_after();
+    const uint32_t tm = s_tm, my = (uint32_t)(tid & 96) << 16;
+    const int items = (int)((h_hi - h_lo) * ptiles);
+    auto image_of = [&](int item) { return ((b * a.H + h_lo + item / ptiles) * ptiles + item % ptiles) * w.chunks + chunk; };
+    auto load_states = [&](const char* images, int64_t im, int n) {  // 64 of the states, two parts
+        mbar_expect_tx(&s_h[n], 4 * kTileBytes);
+#pragma unroll
+        for (int part = 0; part < 2; part++)
+            bulk_load(S + n * 32768 + part * 16384, images + im * state_bytes(NB) + (part * NB + n) * 16384, 16384, &s_h[n]);
+    };
+    auto load = [&](int item) {
+        const int64_t h = h_lo + item / ptiles, p0 = item % ptiles * kTileP, im = image_of(item);
+        mbar_expect_tx(&s_in, 10 * kTileBytes + (int)sizeof(ImageHead));
+        bulk_load(sm + L::head, w.images + ((b * a.H + h) * w.chunks + chunk) * image_bytes(2) + 4 * kTileBytes, (int)sizeof(ImageHead), &s_in);
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            la::tma_load_4d(Z + p * 16384 + kTileBytes, &w.dy, (int)p0 + 64 * p, (int)h, (int)t0, (int)b, &s_in);
+            bulk_load(Z + p * 16384, w.xs + im * kRowsBytes + p * kTileBytes, kTileBytes, &s_in);
+            bulk_load(Zl + p * 16384, w.xs + im * kRowsBytes + (2 + p) * kTileBytes, kTileBytes, &s_in);
+            bulk_load(U + p * 16384, w.us + im * kRowsBytes + p * kTileBytes, kTileBytes, &s_in);
+            bulk_load(U + p * 16384 + kTileBytes, w.us + im * kRowsBytes + (2 + p) * kTileBytes, kTileBytes, &s_in);
+        }
+        for (int n = 0; n < NB; n++) load_states(w.before, im, n);
+    };
+    if (tid == 0) {
+        mbar_expect_tx(&s_key, NB * 16384);
+        bulk_load(KQ, w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384), NB * 16384, &s_key);
+        load(0);
+    }
+    __syncwarp();
+    bool ok = true;
+    for (int item = 0; item < items; item++) {
+        const uint32_t ph = item & 1;
+        const int64_t h = h_lo + item / ptiles, pt = item % ptiles, p0 = pt * kTileP, im = image_of(item);
+        const float x_inv = w.x_inv[im], u_inv = w.u_inv[im], before_inv = w.before_inv[im], after_inv = w.after_inv[im];
+        if (pt == 0) {
+            if (warp == 0) {
+                bool flat;
+                chunk_decays(a, b, t0, h, nv, s_c, s_tail, flat);
+                if (lane == 0) s_flat = flat;
+            }
+            if (tid >= 64 && tid < 64 + C) s_a[tid - 64] = s_b[tid - 64] = s_db[tid - 64] = 0.0f;
+            if (tid >= 128 && tid < 136) s_thr[tid - 128] = 0.0f;
+        }
+        ok = wait_or_fail(&s_in, ph, &s_fail) && ok;
+        // dY as f16: four units a thread of rows 64 .. 127 of Z's two blocks
+        float dy_scale = 1.0f;
+        {
+            uint4 x[4];
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int at = tid + 256 * (i & 1);
+                x[i] = *reinterpret_cast<const uint4*>(Z + (i >> 1) * 16384 + kTileBytes + at * 16);
+                if (at >> 3 >= nv) x[i] = make_uint4(0, 0, 0, 0);
+                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float2 f = unpack2<T>(v[e]);
+                    most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            most = warp_max(most);
+            if (lane == 0) s_max[0][warp] = most;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[0][i]);
+            dy_scale = la::f16_scale(most);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float2 f = mul2(unpack2<T>(v[e]), splat2(dy_scale));
+                    y[e] = pack2<__half>(f.x, f.y);
+                }
+                *reinterpret_cast<uint4*>(Z + (i >> 1) * 16384 + kTileBytes + (tid + 256 * (i & 1)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        constexpr uint32_t kk = la::mma_desc<__half>(128, C, false, false), kr = la::mma_desc<__half>(128, C, false, true),
+                           rr = la::mma_desc<__half>(128, C, true, true);
+        const uint32_t keys_at = smem_addr(KQ), z_at = smem_addr(Z), zl_at = smem_addr(Zl), u_at = smem_addr(U), s_at = smem_addr(S), ef_at = smem_addr(EF);
+        if (tid == 0) {
+            wait_or_fail(&s_key, 0, &s_fail);
+            la::tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 4 * NB; s++) {
+                const uint32_t x = keys_at + (s >> 2) * 16384 + (s & 3) * 32;
+                la::mma(tm + cQK, la::smem_desc(x), la::smem_desc(x), kk, s > 0);
+            }
+#pragma unroll
+            for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
+#pragma unroll
+                for (int s = 0; s < 8; s++) {
+                    const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
+                    la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + x), la::smem_desc(u_at + (o == 1 ? kTileBytes : 0) + x), kk, o > 0 || s > 0);
+                }
+            la::mma_commit(&s_c1);
+            for (int n = 0; n < NB; n++) {
+                wait_or_fail(&s_h[n], 0, &s_fail);
+#pragma unroll
+                for (int o = 0; o < 3; o++)
+#pragma unroll
+                    for (int s = 0; s < 8; s++) {
+                        const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
+                        la::mma(tm + cZ + 64 * n, la::smem_desc((o == 0 ? zl_at : z_at) + x), la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr,
+                                o > 0 || s > 0);
+                    }
+                la::mma_commit(&s_c2[n]);
+            }
+        }
+        __syncwarp();
+        // dv, and x . v: 16 threads a row, two passes of columns' blocks
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int at = tid + 256 * i, row = at >> 4, u = at & 15;
+            const uint4 hi = *unit(Z + (u >> 3) * 16384, row, u & 7), lo = *unit(Zl + (u >> 3) * 16384, row, u & 7);
+            uint4 vv = make_uint4(0, 0, 0, 0);
+            if (row < nv && p0 + 8 * u < a.P)
+                vv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + row) * a.v.token + h * a.P + p0 + 8 * u);
+            const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {vv.x, vv.y, vv.z, vv.w};
+            const float beta = head->beta[row];
+            uint32_t out[4];
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float2 f = mul2(splat2(x_inv), add2(unpack2<__half>(x[e]), unpack2<__half>(y[e]))), g = unpack2<T>(v[e]);
+                sum = fmaf(f.x, g.x, fmaf(f.y, g.y, sum));
+                out[e] = row < nv ? pack2<T>(beta * f.x, beta * f.y) : 0;
+            }
+            put_dv(h, p0, row, u, make_uint4(out[0], out[1], out[2], out[3]));
+            sum = lane_sum<16>(sum);
+            if ((lane & 15) == 0) s_db[row] += sum;
+        }
+        ok = wait_or_fail(&s_c1, ph, &s_fail) && ok;
+        la::tc_fence_after();
+        const float inv_k = head->inv_k, inv_q = head->inv_q, beta = head->beta[tok], rho = q_side ? inv_q / inv_k : 1.0f;
+        float ef_scale;
+        {
+            float e[32], k[32];
+            la::tmem_ld32(tm + my + cE + 32 * half, e);
+            la::tmem_ld32(tm + my + cQK + 32 * half, k);
+            const Two ci = s_c[tok];
+            const float f = u_inv * (q_side ? a.scale / dy_scale : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
+            const int last = q_side ? tok : tok - 1;
+#pragma unroll
+            for (int c0 = 0; c0 < 32; c0 += 16) {
+                const int col0 = 32 * half + c0;
+                if (col0 <= (tok | 15) && (s_flat || col0 + 16 <= (tok & ~15))) {
+                    const float by = f * ex2a(two_diff(ci, s_c[col0 + 15]));
+#pragma unroll
+                    for (int j = 0; j < 16; j++) e[c0 + j] = col0 + j <= last ? e[c0 + j] * (by * s_tail[col0 + j]) : 0.0f;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        float x = 0.0f;
+                        if (col0 + j <= last) x = f * ex2a(two_diff(ci, s_c[col0 + j])) * e[c0 + j];
+                        e[c0 + j] = x;
+                    }
+                }
+            }
+            // of a key's row: e^{c_i - c_j} x_i . u_j so far
+            float row = 0.0f, most = 0.0f;
+            const float sign = q_side ? 1.0f : -beta;
+#pragma unroll
+            for (int j = 0; j < 32; j++) {
+                k[j] = 32 * half + j < tok ? kf * k[j] * e[j] : 0.0f;
+                row += k[j];
+                e[j] *= sign;
+                k[j] *= sign;
+                most = fmaxf(most, fabsf(e[j]));
+            }
+            s_row[half][r] = row;  // (without the sign: dbeta takes a key's as it is)
+            s_col[warp][lane] = column_sums(k);
+            most = warp_max(rho * most);
+            if (lane == 0) s_max[1][warp] = most;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[1][i]);
+            ef_scale = la::f16_scale(most) * rho;
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) x[i] = pack2<__half>(ef_scale * e[8 * u + 2 * i], ef_scale * e[8 * u + 2 * i + 1]);
+                *unit(EF, r, 4 * half + u) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        }
+        if (tid < C) {
+            const float rows_k = s_row[0][tid] + s_row[1][tid], rows_q = s_row[0][64 + tid] + s_row[1][64 + tid];
+            float col = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) col += s_col[(tid >> 5) * 4 + i][tid & 31];
+            s_b[tid] += col - (rows_q - head->beta[tid] * rows_k);
+            s_db[tid] -= rows_k;
+        }
+        la::tc_fence_before();
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            la::tc_fence_after();
+            for (int n = 0; n < NB; n++) {
+#pragma unroll
+                for (int s = 0; s < 4; s++)
+                    la::mma(tm + cK + 64 * n, la::smem_desc(ef_at + s * 32), la::smem_desc(keys_at + n * 16384 + s * 2048), kr, s > 0);
+#pragma unroll
+                for (int s = 0; s < 8; s++)
+                    la::mma(tm + cT + 64 * n, la::smem_desc(ef_at + s * 2048, 0), la::smem_desc(keys_at + n * 16384 + s * 2048), rr, s > 0);
+            }
+            la::mma_commit(&s_c4);
+        }
+        __syncwarp();
+        // H's products; its tiles go to registers (for <R, H>) and make room for R's
+        uint4 hs[NB][8];
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            ok = wait_or_fail(&s_h[n], 0, &s_fail) && ok;
+            if (w.dg)
+#pragma unroll
+                for (int i = 0; i < 8; i++) hs[n][i] = *reinterpret_cast<const uint4*>(S + n * 32768 + (tid + 256 * i) * 16);
+            ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
+        }
+        la::tc_fence_after();
+        __syncthreads();
+        if (tid == 0)
+            for (int n = 0; n < NB; n++) load_states(w.after, im, n);
+        __syncwarp();
+        const float up = head->up[tok], down = head->down[tok];
+        {
+            const float f = before_inv * (q_side ? a.scale * up / dy_scale : -beta * up * x_inv);
+            float dot = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NB; c++) {
+                float z[32];
+                la::tmem_ld32(tm + my + cZ + n0 + 32 * c, z);
+#pragma unroll
+                for (int u = 0; u < 4; u++) dot = dot8(*unit(KQ + ((n0 + 32 * c) >> 6) * 16384, r, ((n0 + 32 * c) & 63) / 8 + u), z + 8 * u, dot);
+#pragma unroll
+                for (int n = 0; n < 32; n++) acc[32 * c + n] = fmaf(f, z[n], acc[32 * c + n]);
+            }
+            s_dot[0][half][r] = (q_side ? inv_q * f : inv_k * f) * dot;                        // a
+            if (!q_side) s_dot[1][half][r] = -inv_k * before_inv * up * x_inv * dot;           // dbeta's share
+        }
+        if (tid == 0) {
+            for (int n = 0; n < NB; n++) {
+                wait_or_fail(&s_h[n], 1, &s_fail);
+                la::tc_fence_after();
+                // rows 64 .. 127 of what starts at U's low part are other tiles: those lanes are not read
+#pragma unroll
+                for (int o = 0; o < 3; o++)
+#pragma unroll
+                    for (int s = 0; s < 8; s++)
+                        la::mma(tm + cR + 64 * n, la::smem_desc(u_at + (o == 0 ? kTileBytes : 0) + (s >> 2) * 16384 + (s & 3) * 32),
+                                la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr, o > 0 || s > 0);
+            }
+            la::mma_commit(&s_c3);
+        }
+        __syncwarp();
+        if (w.dg) {
+            float through = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NB; n++) {
+                ok = wait_or_fail(&s_h[n], 1, &s_fail) && ok;
+                // units tid + 256 i: the high part for i < 4, the low part of the same values 1024 units on
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint4 rh = *reinterpret_cast<const uint4*>(S + n * 32768 + (tid + 256 * i) * 16),
+                                rl = *reinterpret_cast<const uint4*>(S + n * 32768 + 16384 + (tid + 256 * i) * 16);
+                    const uint32_t x[4] = {hs[n][i].x, hs[n][i].y, hs[n][i].z, hs[n][i].w}, y[4] = {hs[n][i + 4].x, hs[n][i + 4].y, hs[n][i + 4].z, hs[n][i + 4].w};
+                    const uint32_t p[4] = {rh.x, rh.y, rh.z, rh.w}, q[4] = {rl.x, rl.y, rl.z, rl.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float2 f = add2(unpack2<__half>(x[e]), unpack2<__half>(y[e])), g = add2(unpack2<__half>(p[e]), unpack2<__half>(q[e]));
+                        through = fmaf(f.x, g.x, fmaf(f.y, g.y, through));
+                    }
+                }
+            }
+            through = lane_sum<32>(through);
+            if (lane == 0) s_thr[warp] += through * (before_inv * after_inv);
+        }
+        ok = wait_or_fail(&s_c3, ph, &s_fail) && ok;
+        ok = wait_or_fail(&s_c4, ph, &s_fail) && ok;
+        la::tc_fence_after();
+        {
+            const float fk = inv_k / ef_scale, fr = down * u_inv * after_inv, ft = fk;  // (a key's row: rho is 1)
+            float dot = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NB; c++) {
+                float z[32];
+                la::tmem_ld32(tm + my + cK + n0 + 32 * c, z);
+#pragma unroll
+                for (int n = 0; n < 32; n++) acc[32 * c + n] = fmaf(fk, z[n], acc[32 * c + n]);
+                la::tmem_ld32(tm + my + cR + n0 + 32 * c, z);
+                if (!q_side) {
+#pragma unroll
+                    for (int u = 0; u < 4; u++) dot = dot8(*unit(KQ + ((n0 + 32 * c) >> 6) * 16384, r, ((n0 + 32 * c) & 63) / 8 + u), z + 8 * u, dot);
+#pragma unroll
+                    for (int n = 0; n < 32; n++) acc[32 * c + n] = fmaf(fr, z[n], acc[32 * c + n]);
+                }
+                la::tmem_ld32(tm + my + cT + n0 + 32 * c, z);
+                if (!q_side)
+#pragma unroll
+                    for (int n = 0; n < 32; n++) acc[32 * c + n] = fmaf(ft, z[n], acc[32 * c + n]);
+            }
+            if (!q_side) s_dot[2][half][r] = inv_k * fr * dot;  // b
+        }
+        la::tc_fence_before();
+        __syncthreads();  // all of the item's tiles and products are read
+        if (tid == 0 && item + 1 < items) load(item + 1);
+        if (tid < C) {
+            s_a[tid] += (s_dot[0][0][tid] + s_dot[0][1][tid]) + (s_dot[0][0][64 + tid] + s_dot[0][1][64 + tid]);
+            s_b[tid] += s_dot[2][0][tid] + s_dot[2][1][tid];
+            s_db[tid] += s_dot[1][0][tid] + s_dot[1][1][tid];
+        }
+        __syncthreads();
+        if (pt == ptiles - 1 && warp == 0) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; u++) sum += s_thr[u];
+            const Two cl = s_c[C - 1];
+            sum *= la::ex2(cl.h + cl.l);
+            const int t = 2 * lane;
+            const float a0 = s_a[t], a1 = s_a[t + 1], b0 = s_b[t], b1 = s_b[t + 1];
+            float A = a0 + a1, B = b0 + b1;  // suffix of a, prefix of b over lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_down_sync(kFull, A, o), y = __shfl_up_sync(kFull, B, o);
+                if (lane + o < 32) A += x;
+                if (lane >= o) B += y;
+            }
+            const float Bx = __shfl_up_sync(kFull, B, 1), Ax = __shfl_down_sync(kFull, A, 1);
+            const float pre = lane > 0 ? Bx : 0.0f, suf = lane < 31 ? Ax : 0.0f;
+            const float g[2] = {(a0 + a1 + suf) + pre + sum, (a1 + suf) + (pre + b0) + sum};
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                if (t + e < nt) {
+                    const int64_t at = (b * a.L + t0 + t + e) * a.H + h;
+                    if (w.dg) w.dg[at] = t + e < nv ? g[e] : 0.0f;
+                    w.dbeta[at] = t + e < nv ? s_db[t + e] : 0.0f;
+                }
+        }
+        __syncthreads();
+    }
+    if (ok) put_out();
+    uint64_t* const bars[9] = {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4};
+    la::end_block(&s_fail, w.status, bars, tm, 512);
+}
+
+template <typename T, int NB> cudaError_t chunks_go(const TcChunkArgs& c, cudaStream_t st) {
+    constexpr int bytes = ChunkSmem<NB>::total;
+    const cudaError_t e = la::allow_smem<k_chunk<T, NB>>(bytes);
+    if (e != cudaSuccess) return e;
+    k_chunk<T, NB><<<(unsigned)(c.a.Bsz * c.chunks * c.a.G * c.splits), kThreads, bytes, st>>>(c);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tc_chunks(const TcChunkArgs& c, cudaStream_t st) {
+    if (c.a.dtype == 1) return c.a.N <= 64 ? chunks_go<__half, 1>(c, st) : chunks_go<__half, 2>(c, st);
+    return c.a.N <= 64 ? chunks_go<__nv_bfloat16, 1>(c, st) : chunks_go<__nv_bfloat16, 2>(c, st);
+}
+
+}  // namespace gdr
+}  // namespace ss

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     __shared__ __align__(16) float s_tail[kHeads][C];  // e^{c_e - c_t}, e the end of the token's run of 16
     __shared__ float s_beta[kHeads][C], s_max[2][4];
     __shared__ la::Decay s_by[kHeads];
-    __shared__ float s_bu[kHeads];
+    __shared__ float s_bu[kHeads], s_down[kHeads];
     __shared__ bool s_flat[kHeads];  // no run of 16 leaves 2^-64 .. 2^64
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -167,31 +167,24 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     if (warp == 1) la::tmem_alloc(&s_tm, 64);
     const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
     auto decays = [&](int64_t h) {  // this warp's head
-        float x[2];
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int t = 2 * lane + i;
-            x[i] = t < nv ? log_decay(a, b, t0 + t, h) * la::kLog2e : 0.0f;
-            s_beta[warp][t] = t < nv ? a.beta[(b * a.L + t0 + t) * a.H + h] : 0.0f;
-        }
-        Two c[2];
-        la::warp_cumsum<2>(x, c);
-        const Two end = {__shfl_sync(kFull, c[1].h, lane | 7), __shfl_sync(kFull, c[1].l, lane | 7)};
-        bool flat = true;
+        bool flat;
+        const Pair p = chunk_decays(a, b, t0, h, nv, s_c[warp], s_tail[warp], flat);
+        const Two(&c)[2] = p.c;
         float bu = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            s_c[warp][2 * lane + i] = c[i];
-            const float rel = two_diff(end, c[i]);
-            flat = flat && fabsf(rel) <= 64.0f;  // (NaN: no)
-            s_tail[warp][2 * lane + i] = ex2a(rel);
-            bu = fmaxf(bu, fabsf(s_beta[warp][2 * lane + i] * ex2a(c[i].h)));
+            const int t = 2 * lane + i;
+            const float beta = t < nv ? a.beta[(b * a.L + t0 + t) * a.H + h] : 0.0f;
+            s_beta[warp][t] = beta;
+            bu = fmaxf(bu, fabsf(beta * ex2a(c[i].h)));
         }
-        flat = __all_sync(kFull, flat);
         bu = warp_max(bu);
+        const Two cl = {__shfl_sync(kFull, c[1].h, 31), __shfl_sync(kFull, c[1].l, 31)};
+        const float down = warp_max(fmaxf(ex2a(two_diff(cl, c[0])), ex2a(two_diff(cl, c[1]))));
         if (lane == 0) {
             s_flat[warp] = flat;
             s_bu[warp] = bu;
+            s_down[warp] = down;
         }
         // the chunk's decay, in natural units from the same sum (rounded once more: 2^-24 of cl)
         if (lane == 31) s_by[warp] = la::decay_of((c[1].h + c[1].l) * kLn2);
@@ -343,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 if (tid == 0) {
                     head->by = s_by[hl].by;
                     head->most_bu = s_bu[hl];
+                    head->most_down = s_down[hl];
                     head->weak = s_by[hl].weak;
                     head->inv_k = 1.0f / scale_k;
                     head->inv_q = 1.0f / scale_q;

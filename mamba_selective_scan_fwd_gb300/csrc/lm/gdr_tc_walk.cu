@@ -103,9 +103,7 @@ __device__ __forceinline__ float group_min(float v, uint32_t* red, int id) {
 }
 
 // blockIdx.y of kTcSum: 0 walks from zero (E), 1 from the identity without v (Phi).
-template <typename T, int NB, TcWalkMode MODE>
-__global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ TcWalkArgs w) {
-    extern __shared__ __align__(1024) char sm[];
+template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void walk(const TcWalkArgs& w, char* sm) {
     constexpr bool SUM = MODE == kTcSum, OUT = MODE == kTcY, KEEP = MODE == kTcKeep;
     // (the backward's images hold P in two parts)
     constexpr int W = 32 * NB, PP = kPParts<T>, IP = KEEP ? 2 : PP;
@@ -520,6 +518,376 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
 
+template <typename T, int NB, TcWalkMode MODE>
+__global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ TcWalkArgs w) {
+    extern __shared__ __align__(1024) char sm[];
+    walk<T, NB, MODE>(w, sm);
+}
+
+// ---------------------------------------------------------------- the backward's walk
+// From the last chunk, with R the adjoint of the state after the chunk, transposed like S:
+//   D0 = dY^T P              D1 = R^T K^T          dU = scale D0 + e^{cl - c} D1      (the adjoint of U)
+//   D2 = dU M = X^T          (the adjoint of beta (v - ..), transposed)
+//   Dq = (scale e^c dY)^T Q  D3 = (-beta e^c X)^T K     R <- e^{cl} R + Dq + D3
+// D0 and Dq do not wait for R: the third warpgroup makes their left operands (dY is exact in one f16
+// part under its channel's scale), and copies the parts of R and X that the chunk kernel reads.
+template <int NB> struct BackStage {
+    static constexpr int block = 2 * kTileBytes, dy = NB * block, image = dy + 2 * kTileBytes, head = image + 4 * kTileBytes,
+                         bytes = head + 2048;
+};
+// columns: D1, then parts of X; D0, then D2; Dq, then D3; parts of R; dY, then parts of dU, then of -beta e^c X; parts
+// of scale e^c dY
+constexpr uint32_t bD1 = 0, bD0 = 64, bD3 = 128, bR = 256, bX = 384, bDq = 448;
+
+template <typename T, int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w, const CUtensorMap* dy_map, const TcBackArgs& r, int64_t id, char* sm) {
+    constexpr int W = 32 * NB;
+    using L = BackStage<NB>;
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r[2], s_d1, s_dq, s_x, s_d2, s_u, s_d3[2], s_dy, s_dyq, s_xi, s_early, s_late;
+    __shared__ uint32_t s_tm, s_fail, s_red[4];
+    __shared__ float s_most[2][128], s_ud[2][128], s_rs[2][128], s_xsc[2][128], s_dys[2][128], s_dqs[2][128];
+    const Args& a = w.a;
+    const int tid = threadIdx.x, warp = tid >> 5, pl = tid & 127;
+    const int64_t ptiles = (a.P + kTileP - 1) / kTileP, pt = id % ptiles, p0 = pt * kTileP, bh = id / ptiles;
+    const int64_t b = bh / a.H, h = bh % a.H, hq = h / (a.H / a.G), len = row_length(a, b);
+    const int chunks = (int)((len + C - 1) / C);
+    if (tid == 0) {
+        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3[0], &s_d3[1]}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_x, &s_u, &s_xi}) mbar_init(bar, kStateThreads / 32);
+        for (uint64_t* bar : {&s_r[0], &s_r[1], &s_dy, &s_dyq, &s_early, &s_late}) mbar_init(bar, 4);
+        for (uint64_t* bar : {&s_free[0], &s_free[1]}) mbar_init(bar, kStateThreads / 32 + 4);
+        s_fail = 0;
+        fence_proxy_async_smem();
+    }
+    if (warp == 0) la::tmem_alloc(&s_tm, 512);
+    __syncthreads();
+    la::tc_fence_after();
+    const uint32_t tm = s_tm, my = (uint32_t)((warp & 3) * 32) << 16;
+    char* staging = sm + 2 * L::bytes;
+    auto chunk_of = [&](int i) { return chunks - 1 - i; };
+
+    if (warp < kStateThreads / 32) {
+        take_regs<168>();
+        const int half = tid >> 7;
+        const int64_t p = p0 + pl;
+        const bool mine = p < a.P;
+        float R[W];
+        const float* from = r.init ? r.init + bh * a.N * a.P : nullptr;
+#pragma unroll
+        for (int n = 0; n < W; n++) R[n] = from && mine && half * W + n < a.N ? from[(half * W + n) * a.P + p] : 0.0f;
+        auto pair_sync = [&] { named_sync(1 + (warp & 3), 64); };
+        auto max_over = [&](const float (&m)[2][128]) { return fmaxf(m[0][pl], m[1][pl]); };
+        bool ok = true;
+        s_most[half][pl] = max_abs<W>(R);
+        pair_sync();
+        float bound = max_over(s_most);
+        pair_sync();
+        for (int i = 0; i < chunks; i++) {
+            const uint32_t ph = i & 1;
+            char* at = sm + ph * L::bytes;
+            const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
+            const float rs = scale_of(bound);
+            if (i > 0) ok = ok && wait_or_fail(&s_early, ph ^ 1, &s_fail);
+            if (half == 0) s_rs[ph][pl] = rs;
+#pragma unroll
+            for (int c = 0; c < NB; c++) {
+                const uint32_t to = tm + my + bR + half * (W / 2) + 16 * c;
+                put2(to, to + 32 * NB, R + 32 * c, rs);
+            }
+            la::tmem_wait_st();
+            arrive(&s_r[half]);
+            s_most[half][pl] = max_abs<W>(R);
+            pair_sync();
+            const float r_most = max_over(s_most);
+            ok = ok && wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail);
+            const float k_most = 16384.0f * head->inv_k, inv1 = head->inv_k / rs;
+            ok = ok && wait_or_fail(&s_d1, ph, &s_fail);  // D0 and D1
+            la::tc_fence_after();
+            const float dys = s_dys[ph][pl], inv0 = a.scale * head->inv_p / dys;
+            float x[32], d[32];
+            la::tmem_ld32(tm + my + bD1 + 32 * half, x);
+            la::tmem_ld32(tm + my + bD0 + 32 * half, d);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&head->down[32 * half + j]);
+                const float2 y = fma2(mul2(splat2(inv1), make_float2(f.x, f.y)), make_float2(x[j], x[j + 1]), mul2(splat2(inv0), make_float2(d[j], d[j + 1])));
+                const float2 z = fma2(mul2(splat2(inv1), make_float2(f.z, f.w)), make_float2(x[j + 2], x[j + 3]), mul2(splat2(inv0), make_float2(d[j + 2], d[j + 3])));
+                x[j] = y.x;
+                x[j + 1] = y.y;
+                x[j + 2] = z.x;
+                x[j + 3] = z.y;
+            }
+            const float x_bound = fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * 16384.0f * head->inv_p * (16384.0f / dys)),
+                        xs = scale_of(x_bound);
+            {
+                const uint32_t to = tm + my + bX + 16 * half;
+                put2(to, to + 32, x, xs);
+            }
+            la::tmem_wait_st();
+            arrive(&s_x);
+            // Dq, while D2 is on its way
+            ok = ok && wait_or_fail(&s_dq, ph, &s_fail);
+            la::tc_fence_after();
+            const float by = head->by, keep = head->weak ? 1.0f : 0.0f, dqs = s_dqs[ph][pl], invq = head->inv_q / dqs;
+#pragma unroll
+            for (int c = 0; c < NB; c++) {
+                la::tmem_ld32(tm + my + bD3 + half * W + 32 * c, d);
+#pragma unroll
+                for (int n = 0; n < 32; n += 2) {
+                    const float2 o = make_float2(R[32 * c + n], R[32 * c + n + 1]);
+                    const float2 f = fma2(splat2(invq), make_float2(d[n], d[n + 1]), fma2(splat2(by), o, mul2(splat2(keep), o)));
+                    R[32 * c + n] = f.x;
+                    R[32 * c + n + 1] = f.y;
+                }
+            }
+            const float inv2 = head->inv_m / xs;
+            ok = ok && wait_or_fail(&s_d2, ph, &s_fail);
+            la::tc_fence_after();
+            la::tmem_ld32(tm + my + bD0 + 32 * half, x);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&head->beta_up[32 * half + j]);
+                const float2 y = mul2(splat2(inv2), make_float2(x[j], x[j + 1])), z = mul2(splat2(inv2), make_float2(x[j + 2], x[j + 3]));
+                x[j] = y.x;
+                x[j + 1] = y.y;
+                x[j + 2] = z.x;
+                x[j + 3] = z.y;
+                d[j] = -f.x * y.x;
+                d[j + 1] = -f.y * y.y;
+                d[j + 2] = -f.z * z.x;
+                d[j + 3] = -f.w * z.y;
+            }
+            s_ud[half][pl] = max_abs<32>(d);
+            pair_sync();
+            const float ud_most = max_over(s_ud), us = scale_of(ud_most), inv3 = head->inv_k / us;
+            {
+                const uint32_t to = tm + my + bX + 16 * half;
+                put2(to, to + 32, d, us);
+            }
+            la::tmem_wait_st();
+            bound = fmaf(64.0f * k_most, ud_most, fmaf(64.0f * 16384.0f * head->inv_q, 16384.0f / dqs, r_most * (keep + fabsf(by))));
+            arrive(&s_u);
+            {
+                const float xi = scale_of(64.0f * 16384.0f * head->inv_m * x_bound);
+                if (half == 0) s_xsc[ph][pl] = xi;
+                const uint32_t to = tm + my + bD1 + 16 * half;
+                put2(to, to + 32, x, xi);
+                la::tmem_wait_st();
+                arrive(&s_xi);
+            }
+            ok = ok && wait_or_fail(&s_d3[half], ph, &s_fail);
+            la::tc_fence_after();
+            arrive(&s_free[ph]);
+#pragma unroll
+            for (int c = 0; c < NB; c++) {
+                la::tmem_ld32(tm + my + bD3 + half * W + 32 * c, d);
+#pragma unroll
+                for (int n = 0; n < 32; n += 2) {
+                    const float2 f = fma2(splat2(inv3), make_float2(d[n], d[n + 1]), make_float2(R[32 * c + n], R[32 * c + n + 1]));
+                    R[32 * c + n] = f.x;
+                    R[32 * c + n + 1] = f.y;
+                }
+            }
+        }
+        if (mine && ok && r.last) {
+            float* to = r.last + bh * a.N * a.P;
+#pragma unroll
+            for (int n = 0; n < W; n++)
+                if (half * W + n < a.N) to[(half * W + n) * a.P + p] = R[n];
+        }
+    } else if (warp < kStateThreads / 32 + 4) {
+        leave_regs<112>();
+        const bool first = tid == kStateThreads;
+        for (int i = 0; i < chunks; i++) {
+            const uint32_t ph = i & 1;
+            const int ch = chunk_of(i), nv = (int)min((int64_t)C, len - (int64_t)ch * C);
+            const int64_t image = (bh * ptiles + pt) * w.chunks + ch;
+            char* at = sm + ph * L::bytes;
+            const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
+            wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail);
+            float y[64];
+            {
+                const char* tile = at + L::dy + (pl >> 6) * kTileBytes + (pl & 7) * 2;
+                const int c = (pl & 63) >> 3;
+#pragma unroll
+                for (int t = 0; t < 64; t++) {
+                    const float v = ldf(reinterpret_cast<const T*>(tile + t * 128 + ((c ^ (t & 7)) << 4)));
+                    y[t] = t < nv ? v : 0.0f;
+                }
+            }
+            float sc = scale_of(max_abs<64>(y));
+            s_dys[ph][pl] = sc;
+            if (i > 0) {  // what the last products read makes room
+                wait_or_fail(&s_d3[0], ph ^ 1, &s_fail);
+                wait_or_fail(&s_d3[1], ph ^ 1, &s_fail);
+                la::tc_fence_after();
+            }
+            put1(tm + my + bX, y, sc);
+            put1(tm + my + bX + 16, y + 32, sc);
+            la::tmem_wait_st();
+            arrive(&s_dy);
+#pragma unroll
+            for (int t = 0; t < 64; t += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&head->up[t]);
+                y[t] *= a.scale * f.x;
+                y[t + 1] *= a.scale * f.y;
+                y[t + 2] *= a.scale * f.z;
+                y[t + 3] *= a.scale * f.w;
+            }
+            arrive(&s_free[ph]);
+            sc = scale_of(max_abs<64>(y));
+            s_dqs[ph][pl] = sc;
+            put2(tm + my + bDq, tm + my + bDq + 32, y, sc);
+            put2(tm + my + bDq + 16, tm + my + bDq + 48, y + 32, sc);
+            la::tmem_wait_st();
+            arrive(&s_dyq);
+            // the parts of R under one scale
+            wait_or_fail(&s_r[0], ph, &s_fail);
+            wait_or_fail(&s_r[1], ph, &s_fail);
+            la::tc_fence_after();
+            float own = s_rs[ph][pl], all = group_min(own, s_red, 5);
+            uint32_t f = pack2<__half>(all / own, all / own);
+#pragma unroll
+            for (int part = 0; part < 2; part++) {
+                if (first) la::bulk_wait_read();
+                named_sync(5, 128);  // the staging tiles are free
+#pragma unroll
+                for (int n = 0; n < NB; n++) {
+                    float x[32];
+                    la::tmem_ld32(tm + my + bR + 32 * (part * NB + n), x);
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        *unit(staging + n * 2 * kTileBytes, pl, u) =
+                            make_uint4(hmul2(__float_as_uint(x[4 * u]), f), hmul2(__float_as_uint(x[4 * u + 1]), f),
+                                       hmul2(__float_as_uint(x[4 * u + 2]), f), hmul2(__float_as_uint(x[4 * u + 3]), f));
+                }
+                if (part == 1) arrive(&s_early);
+                fence_proxy_async_smem();
+                named_sync(5, 128);
+                if (first) {
+                    la::bulk_store(r.states + image * state_bytes(NB) + part * NB * 2 * kTileBytes, staging, NB * 2 * kTileBytes);
+                    la::bulk_commit();
+                }
+            }
+            if (first) r.state_inv[image] = 1.0f / all;
+            wait_or_fail(&s_xi, ph, &s_fail);
+            la::tc_fence_after();
+            own = s_xsc[ph][pl], all = group_min(own, s_red, 5);
+            f = pack2<__half>(all / own, all / own);
+            char* to = staging + NB * 2 * kTileBytes + (pl >> 6) * kTileBytes + (pl & 7) * 2;
+            const int cu = (pl & 63) >> 3;
+#pragma unroll
+            for (int part = 0; part < 2; part++) {
+                if (part == 1) {
+                    if (first) la::bulk_wait_read();
+                    named_sync(5, 128);
+                }
+                float x[32];
+                la::tmem_ld32(tm + my + bD1 + 32 * part, x);
+                if (part == 1) arrive(&s_late);
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    const uint32_t v = hmul2(__float_as_uint(x[j]), f);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int t = 2 * j + e;
+                        *reinterpret_cast<uint16_t*>(to + t * 128 + ((cu ^ (t & 7)) << 4)) = (uint16_t)(e ? v >> 16 : v);
+                    }
+                }
+                fence_proxy_async_smem();
+                named_sync(5, 128);
+                if (first) {
+                    la::bulk_store(r.xs + image * kRowsBytes + part * 2 * kTileBytes, staging + NB * 2 * kTileBytes, 2 * kTileBytes);
+                    la::bulk_commit();
+                }
+            }
+            if (first) r.x_inv[image] = 1.0f / all;
+        }
+        if (first) la::bulk_wait_all();
+    } else {
+        leave_regs<56>();
+        if (tid == kThreads - 96) {  // loads
+            for (int i = 0; i < chunks; i++) {
+                if (i > 1 && !wait_or_fail(&s_free[i & 1], ((i >> 1) + 1) & 1, &s_fail)) break;
+                char* at = sm + (i & 1) * L::bytes;
+                uint64_t* bar = &s_full[i & 1];
+                const int ch = chunk_of(i), t0 = ch * C;
+                mbar_expect_tx(bar, NB * L::block + 6 * kTileBytes + (int)sizeof(ImageHead));
+                bulk_load(at, w.keys + ((b * w.chunks + ch) * a.G + hq) * (NB * 2 * kTileBytes), NB * L::block, bar);
+                la::tma_load_4d(at + L::dy, dy_map, (int)p0, (int)h, t0, (int)b, bar);
+                la::tma_load_4d(at + L::dy + kTileBytes, dy_map, (int)p0 + 64, (int)h, t0, (int)b, bar);
+                bulk_load(at + L::image, w.images + (bh * w.chunks + ch) * image_bytes(2), 4 * kTileBytes + (int)sizeof(ImageHead), bar);
+            }
+        } else if (tid == kThreads - 128) {  // products
+            for (int i = 0; i < chunks; i++) {
+                const uint32_t ph = i & 1;
+                const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
+                constexpr uint32_t dK = la::mma_desc<__half>(128, C, false, false), dR = la::mma_desc<__half>(128, C, false, true);
+                if (!wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail) || !wait_or_fail(&s_dy, ph, &s_fail)) break;
+                la::tc_fence_after();
+#pragma unroll
+                for (int part = 1; part >= 0; part--)
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+                        la::mma_ts(tm + bD0, tm + bX + 8 * s, la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
+                if (i > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    if (!wait_or_fail(&s_r[half], ph, &s_fail)) break;
+                    la::tc_fence_after();
+#pragma unroll
+                    for (int part = 1; part >= 0; part--)
+#pragma unroll
+                        for (int e = 0; e < 2 * NB; e++) {
+                            const int s = half * 2 * NB + e;
+                            la::mma_ts(tm + bD1, tm + bR + part * 32 * NB + 8 * s, la::smem_desc(at + (s >> 2) * L::block + (s & 3) * 32), dK,
+                                       half > 0 || part < 1 || e > 0);
+                        }
+                }
+                la::mma_commit(&s_d1);
+                if (!wait_or_fail(&s_dyq, ph, &s_fail)) break;
+                la::tc_fence_after();
+                auto update = [&](uint32_t left, uint32_t keys, int n) {  // 64 of the states, two parts
+#pragma unroll
+                    for (int part = 1; part >= 0; part--)
+#pragma unroll
+                        for (int s = 0; s < 4; s++)
+                            la::mma_ts(tm + bD3 + 64 * n, tm + left + part * 32 + 8 * s, la::smem_desc(keys + n * L::block + s * 2048), dR, part < 1 || s > 0);
+                };
+#pragma unroll
+                for (int n = 0; n < NB; n++) update(bDq, at + kTileBytes, n);
+                la::mma_commit(&s_dq);
+                if (!wait_or_fail(&s_x, ph, &s_fail)) break;
+                la::tc_fence_after();
+#pragma unroll
+                for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+                        la::mma_ts(tm + bD0, tm + bX + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(M + (o == 1 ? kTileBytes : 0) + s * 2048), dR, o > 0 || s > 0);
+                la::mma_commit(&s_d2);
+                if (!wait_or_fail(&s_u, ph, &s_fail)) break;
+                la::tc_fence_after();
+#pragma unroll
+                for (int n = 0; n < NB; n++) {
+                    update(bX, at, n);
+                    la::mma_commit(&s_d3[n]);
+                }
+                if (NB == 1) la::mma_commit(&s_d3[1]);
+            }
+        }
+    }
+    __syncwarp();
+    uint64_t* const bars[7] = {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3[0], &s_d3[1]};
+    la::end_block(&s_fail, w.status, bars, tm, 512);
+}
+
+// Both of the backward's walks: neither needs the other, and together they fill more SMs.
+template <typename T, int NB>
+__global__ void __launch_bounds__(kThreads, 1) k_walks(const __grid_constant__ TcWalkArgs w, const __grid_constant__ TcBackArgs r, int forward) {
+    extern __shared__ __align__(1024) char sm[];
+    if ((int)blockIdx.x < forward) walk<T, NB, kTcKeep>(w, sm);
+    else walk_back<T, NB>(w, &r.dy, r, blockIdx.x - forward, sm);
+}
+
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
 // from.  A block: 8 columns of one head's state, in shared memory, thread = row and four of them; the next Phi
 // (transposed) is on its way while one is used.  65536 tokens x 8 heads, 19 segments: PLACEHOLDER us.
@@ -583,7 +951,7 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
 
 template <typename T, int NB, TcWalkMode MODE> cudaError_t walk_go(const TcWalkArgs& w, cudaStream_t st) {
     constexpr int bytes = 2 * Stage<NB, kPParts<T>, MODE == kTcY>::bytes +
-                          (MODE == kTcY ? 2 * kTileBytes : MODE == kTcKeep ? state_bytes(NB) + kRowsBytes : 0);
+                          (MODE == kTcY ? 2 * kTileBytes : 0);
     const cudaError_t e = la::allow_smem<k_walk<T, NB, MODE>>(bytes);
     if (e != cudaSuccess) return e;
     const int64_t segs = MODE == kTcSum ? w.plan.K - 1 : w.plan.K;
@@ -591,9 +959,17 @@ template <typename T, int NB, TcWalkMode MODE> cudaError_t walk_go(const TcWalkA
     k_walk<T, NB, MODE><<<grid, kThreads, bytes, st>>>(w);
     return cudaGetLastError();
 }
+template <typename T, int NB> cudaError_t walks_go(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
+    constexpr int keep = 2 * Stage<NB, kPParts<T>, false>::bytes + state_bytes(NB) + kRowsBytes,
+                  back = 2 * BackStage<NB>::bytes + NB * 2 * kTileBytes + 2 * kTileBytes, bytes = keep > back ? keep : back;
+    const cudaError_t e = la::allow_smem<k_walks<T, NB>>(bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t units = ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H;
+    k_walks<T, NB><<<(unsigned)(2 * units), kThreads, bytes, st>>>(w, r, (int)units);
+    return cudaGetLastError();
+}
 template <typename T, int NB> cudaError_t walk_mode(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st) {
     if (mode == kTcSum) return walk_go<T, NB, kTcSum>(w, st);
-    if (mode == kTcKeep) return walk_go<T, NB, kTcKeep>(w, st);
     return walk_go<T, NB, kTcY>(w, st);
 }
 
@@ -602,6 +978,11 @@ template <typename T, int NB> cudaError_t walk_mode(const TcWalkArgs& w, TcWalkM
 cudaError_t launch_tc_walk(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st) {
     if (w.a.dtype == 1) return w.a.N <= 64 ? walk_mode<__half, 1>(w, mode, st) : walk_mode<__half, 2>(w, mode, st);
     return w.a.N <= 64 ? walk_mode<__nv_bfloat16, 1>(w, mode, st) : walk_mode<__nv_bfloat16, 2>(w, mode, st);
+}
+
+cudaError_t launch_tc_walks(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
+    if (w.a.dtype == 1) return w.a.N <= 64 ? walks_go<__half, 1>(w, r, st) : walks_go<__half, 2>(w, r, st);
+    return w.a.N <= 64 ? walks_go<__nv_bfloat16, 1>(w, r, st) : walks_go<__nv_bfloat16, 2>(w, r, st);
 }
 
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st) {
