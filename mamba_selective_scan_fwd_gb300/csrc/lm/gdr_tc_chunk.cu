@@ -10,7 +10,7 @@
 // dq and dk stay in registers over the heads.  dv = beta x;  dbeta_i = x_i . v_i - e^{c_i} k_i . H x_i - sum_j e^{c_i - c_j}
 // (k_i . k_j) (x_i . u_j);  dg is made of every path's two ends (gdr_f32.cu has the formula).
 //
-// Roundings: E and F enter dq's and dk's products as one f16 (2^-12 of terms of a 16-bit output).
+// Roundings: E and F enter dq's and dk's products as one f16 (2^-12 of terms of a bf16 output; f16 io: in two parts).
 // H, R, U and X come in two f16 parts (22 bits), and dg and dbeta take all else in f32.
 #include "gdr_tc.h"
 #include "../simd.cuh"
@@ -78,6 +78,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     extern __shared__ __align__(1024) char sm[];
     using L = ChunkSmem<NB>;
     constexpr int W = 32 * NB;  // states of a thread
+    constexpr int EP = la::kF16<T> ? 2 : 1;  // parts of E and F in dq's and dk's products
     __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_c1, s_c2[2], s_c3, s_c4;
     __shared__ uint32_t s_tm, s_fail;
     __shared__ Two s_c[C];
@@ -334,12 +335,21 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
 #pragma unroll
             for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[1][i]);
             ef_scale = la::f16_scale(most) * rho;
+            if (EP > 1) {  // the low part takes Z's, which H's product is done with
+                for (int n = 0; n < NB; n++) ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
+            }
 #pragma unroll
             for (int u = 0; u < 4; u++) {
-                uint32_t x[4];
+                uint32_t x[4], y[4];
 #pragma unroll
-                for (int i = 0; i < 4; i++) x[i] = pack2<__half>(ef_scale * e[8 * u + 2 * i], ef_scale * e[8 * u + 2 * i + 1]);
+                for (int i = 0; i < 4; i++) {
+                    float2 f = mul2(splat2(ef_scale), make_float2(e[8 * u + 2 * i], e[8 * u + 2 * i + 1]));
+                    x[i] = pack2<__half>(f.x, f.y);
+                    f = fma2(unpack2<__half>(x[i]), splat2(-1.0f), f);
+                    y[i] = pack2<__half>(f.x, f.y);
+                }
                 *unit(EF, r, 4 * half + u) = make_uint4(x[0], x[1], x[2], x[3]);
+                if (EP > 1) *unit(Zl, r, 4 * half + u) = make_uint4(y[0], y[1], y[2], y[3]);
             }
         }
         if (tid < C) {
@@ -355,14 +365,16 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         __syncthreads();
         if (tid == 0) {
             la::tc_fence_after();
-            for (int n = 0; n < NB; n++) {
+            for (int n = 0; n < NB; n++)
+                for (int part = EP - 1; part >= 0; part--) {
+                    const uint32_t left = part ? zl_at : ef_at;
 #pragma unroll
-                for (int s = 0; s < 4; s++)
-                    la::mma(tm + cK + 64 * n, la::smem_desc(ef_at + s * 32), la::smem_desc(keys_at + n * 16384 + s * 2048), kr, s > 0);
+                    for (int s = 0; s < 4; s++)
+                        la::mma(tm + cK + 64 * n, la::smem_desc(left + s * 32), la::smem_desc(keys_at + n * 16384 + s * 2048), kr, part < EP - 1 || s > 0);
 #pragma unroll
-                for (int s = 0; s < 8; s++)
-                    la::mma(tm + cT + 64 * n, la::smem_desc(ef_at + s * 2048, 0), la::smem_desc(keys_at + n * 16384 + s * 2048), rr, s > 0);
-            }
+                    for (int s = 0; s < 8; s++)
+                        la::mma(tm + cT + 64 * n, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + n * 16384 + s * 2048), rr, part < EP - 1 || s > 0);
+                }
             la::mma_commit(&s_c4);
         }
         __syncwarp();
@@ -462,6 +474,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         }
         la::tc_fence_before();
         __syncthreads();  // all of the item's tiles and products are read
+        if (EP > 1)  // dY has no low part
+            for (int i = tid; i < C * 8; i += kThreads) *reinterpret_cast<uint4*>(Zl + kTileBytes + i * 16) = make_uint4(0, 0, 0, 0);
         if (tid == 0 && item + 1 < items) load(item + 1);
         if (tid < C) {
             s_a[tid] += (s_dot[0][0][tid] + s_dot[0][1][tid]) + (s_dot[0][0][64 + tid] + s_dot[0][1][64 + tid]);
