@@ -26,9 +26,8 @@ constexpr int kChunk = 64;  // tokens whose pairs the backward forms (and the te
 
 // ---------------------------------------------------------------- FP32 path
 constexpr int kWalkT = 16;  // tokens staged at a time
-// lanes that share a value channel's N states, 16 each, and value channels per block
+// lanes that share a value channel's N states, 16 each
 inline int walk_lanes(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
-inline int64_t walk_cols(int64_t N) { return 256 / walk_lanes(N); }
 
 enum WalkMode { kWalkY, kWalkKeep, kWalkBack };
 struct WalkArgs {
@@ -52,7 +51,8 @@ struct ChunkArgs {
     float *dg, *dbeta;             // dg: may be null
 };
 
-cudaError_t launch_walk(const WalkArgs& w, WalkMode mode, cudaStream_t st);
+cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st);                          // kWalkY
+cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st);  // the backward's two, at once
 cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st);
 
 struct StepArgs {

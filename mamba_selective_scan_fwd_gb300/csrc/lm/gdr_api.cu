@@ -342,7 +342,7 @@ int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
     w.init = a.h0;
     w.last = d->last_state;
     w.y = d->y;
-    return launch_walk(w, kWalkY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+    return launch_walk(w, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 size_t ss_gdr_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
@@ -380,19 +380,18 @@ int ss_gdr_bwd(const ss_gdr_bwd_desc* d, void* stream) {
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     Layout l;
     const Bwd32 bl = bwd32_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
-    WalkArgs w = {};
-    w.a = a;
-    w.chunks = bl.chunks;
-    w.init = a.h0;
-    w.rows = f32(bl.miss);
-    w.states = f32(bl.before);
-    if (launch_walk(w, kWalkKeep, st) != cudaSuccess) return SS_ERR_CUDA;
-    w.init = a.dlast;
-    w.last = d->dh0;
-    w.y = d->dv;
-    w.rows = f32(bl.x);
-    w.states = f32(bl.after);
-    if (launch_walk(w, kWalkBack, st) != cudaSuccess) return SS_ERR_CUDA;
+    WalkArgs keep = {}, back = {};
+    keep.a = back.a = a;
+    keep.chunks = back.chunks = bl.chunks;
+    keep.init = a.h0;
+    keep.rows = f32(bl.miss);
+    keep.states = f32(bl.before);
+    back.init = a.dlast;
+    back.last = d->dh0;
+    back.y = d->dv;
+    back.rows = f32(bl.x);
+    back.states = f32(bl.after);
+    if (launch_walks(keep, back, st) != cudaSuccess) return SS_ERR_CUDA;
     ChunkArgs c = {};
     c.a = a;
     c.miss = f32(bl.miss);

@@ -57,51 +57,46 @@ template <int LN> __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float2 decayed2(Decay d, float2 x) {
-    return d.weak ? fma2(splat2(d.by), x, x) : mul2(splat2(d.by), x);
-}
-
-// One block: 256 / LN value channels of one head.  Lane (cg, ln): two adjacent
-// channels, the states n = 4 (ln + LN j) + e, j, e < 4, in pairs of e (runs of four
-// so that the lanes' reads of k and q are 16 bytes side by side).
-template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(128) k_walk(WalkArgs w) {
-    constexpr int NP = 16 * LN, PT = 256 / LN, TT = kWalkT;
+// One block: 128 / LN value channels of one head, one a lane and LN lanes a channel; lane ln of a
+// channel holds the states n = 4 (ln + LN j) + e, j, e < 4, in pairs of e (runs of four so that the
+// lanes' reads of k and q are 16 bytes side by side).  The forward takes S^T k and S^T q in one pass
+// over the old state, y = S^T q + (q . k) u: one exchange of sums a token on the chain.  A token's k and
+// q are read while the one before is worked on.
+template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void walk(const WalkArgs& w, int64_t id) {
+    constexpr int NP = 16 * LN, PT = 128 / LN, TT = kWalkT;
     constexpr int EK = NP * TT / 512 < 1 ? 1 : NP * TT / 512, EV = PT * TT / 512 < 1 ? 1 : PT * TT / 512;
     __shared__ __align__(16) float s_k[TT][NP], s_q[TT][NP], s_v[TT][PT], s_o[TT][PT];
     __shared__ float s_a[TT], s_beta[TT];
     __shared__ uint32_t s_weak;
     const Args& a = w.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane % LN, cg = lane / LN;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane % LN;
     const int64_t ptiles = (a.P + PT - 1) / PT;
-    int64_t id = blockIdx.x;
     const int64_t p0 = (id % ptiles) * PT;
     id /= ptiles;
     const int64_t h = id % a.H, b = id / a.H, hq = h / (a.H / a.G), bh = b * a.H + h;
     const int N = (int)a.N, pleft = (int)min((int64_t)PT, a.P - p0);
-    const int col = (warp * (32 / LN) + cg) * 2;  // of the block's channels
+    const int col = tid / LN;  // of the block's channels
     const int64_t len = row_length(a, b), NPel = a.N * a.P;
     const In& vin = MODE == kWalkBack ? a.dy : a.v;
     const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hq * a.N;
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
     const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P + p0;
 
-    float2 S[2][8];  // [channel][2 j + e / 2]
+    float2 S[8];  // [2 j + e / 2]
     auto state = [&](float* p, bool put) {  // p: the head's N x P
 #pragma unroll
-        for (int c = 0; c < 2; c++)
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int n = 4 * (ln + LN * (i / 2)) + 2 * (i & 1);
-                const bool ok = p && col + c < pleft;
-                float* q = p + n * a.P + p0 + col + c;
-                if (put) {
-                    if (ok && n < N) q[0] = S[c][i].x;
-                    if (ok && n + 1 < N) q[a.P] = S[c][i].y;
-                } else {
-                    S[c][i].x = ok && n < N ? q[0] : 0.0f;
-                    S[c][i].y = ok && n + 1 < N ? q[a.P] : 0.0f;
-                }
+        for (int i = 0; i < 8; i++) {
+            const int n = 4 * (ln + LN * (i / 2)) + 2 * (i & 1);
+            const bool ok = p && col < pleft;
+            float* q = p + n * a.P + p0 + col;
+            if (put) {
+                if (ok && n < N) q[0] = S[i].x;
+                if (ok && n + 1 < N) q[a.P] = S[i].y;
+            } else {
+                S[i].x = ok && n < N ? q[0] : 0.0f;
+                S[i].y = ok && n + 1 < N ? q[a.P] : 0.0f;
             }
+        }
     };
     state(w.init ? const_cast<float*>(w.init) + bh * NPel : nullptr, false);
 
@@ -128,6 +123,33 @@ template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(1
             rb = tid < nv ? a.beta[(b * a.L + t0 + tid) * a.H + h] : 0.0f;
         }
     };
+    struct Token {
+        float2 k[8], q[8];
+        float a, beta, v;
+    };
+    auto read = [&](int t, Token& x) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float4 kk = at4(&s_k[t][4 * (ln + LN * j)]);
+            x.k[2 * j] = make_float2(kk.x, kk.y);
+            x.k[2 * j + 1] = make_float2(kk.z, kk.w);
+            if (MODE != kWalkKeep) {
+                const float4 qq = at4(&s_q[t][4 * (ln + LN * j)]);
+                x.q[2 * j] = make_float2(qq.x, qq.y);
+                x.q[2 * j + 1] = make_float2(qq.z, qq.w);
+            }
+        }
+        x.a = s_a[t];
+        x.beta = s_beta[t];
+        x.v = s_v[t][col];
+    };
+    auto dot = [&](const float2 (&x)[8], const float2 (&y)[8]) {
+        float2 s[2] = {};
+#pragma unroll
+        for (int j = 0; j < 8; j++) s[j & 1] = fma2(x[j], y[j], s[j & 1]);
+        s[0] = add2(s[0], s[1]);
+        return s[0].x + s[0].y;
+    };
     if (tiles > 0) fetch(0);
     for (int64_t i = 0; i < tiles; i++) {
         const int64_t t0 = start(i);
@@ -138,7 +160,7 @@ template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(1
             if (tid + 128 * e < TT * NP / 4) {
                 reinterpret_cast<float4*>(s_k)[tid + 128 * e] = rk[e];
                 if (MODE != kWalkKeep) {
-                    const float f = MODE == kWalkBack ? a.scale : 1.0f;
+                    const float f = a.scale;
                     reinterpret_cast<float4*>(s_q)[tid + 128 * e] = make_float4(f * rq[e].x, f * rq[e].y, f * rq[e].z, f * rq[e].w);
                 }
             }
@@ -160,53 +182,62 @@ template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(1
         if (MODE == kWalkKeep ? t0 % kChunk == 0 : MODE == kWalkBack && (i == 0 || (t0 + TT) % kChunk == 0))
             state(w.states + (bh * w.chunks + t0 / kChunk) * NPel, true);
         const uint32_t weak = s_weak;
-#pragma unroll 1
-        for (int u = 0; u < nv; u++) {
-            const int t = MODE == kWalkBack ? nv - 1 - u : u;
-            const Decay d = {s_a[t], (weak >> t & 1) != 0};
-            const float beta = s_beta[t];
-            const float2 v = *reinterpret_cast<const float2*>(&s_v[t][col]);
-            float2 k[8], q[8];
+        auto token = [&](int t, const Token& x) {
+            const Decay d = {x.a, (weak >> t & 1) != 0};
+            float out;
+            if (MODE == kWalkBack) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float4 kk = at4(&s_k[t][4 * (ln + LN * j)]);
-                k[2 * j] = make_float2(kk.x, kk.y);
-                k[2 * j + 1] = make_float2(kk.z, kk.w);
-                if (MODE != kWalkKeep) {
-                    const float4 qq = at4(&s_q[t][4 * (ln + LN * j)]);
-                    q[2 * j] = make_float2(qq.x, qq.y);
-                    q[2 * j + 1] = make_float2(qq.z, qq.w);
+                for (int j = 0; j < 8; j++) S[j] = fma2(x.q[j], splat2(x.v), S[j]);
+                out = lane_sum<LN>(dot(x.k, S));
+                const float2 by = splat2(-x.beta * out);
+#pragma unroll
+                for (int j = 0; j < 8; j++) S[j] = fma2(x.k[j], by, S[j]);
+                if (d.weak) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) S[j] = fma2(splat2(d.by), S[j], S[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) S[j] = mul2(splat2(d.by), S[j]);
                 }
-            }
-            float out[2];
+            } else {
+                if (d.weak) {
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                const float vc = c ? v.y : v.x;
-                float2 acc[2] = {};
+                    for (int j = 0; j < 8; j++) S[j] = fma2(splat2(d.by), S[j], S[j]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    S[c][j] = MODE == kWalkBack ? fma2(q[j], splat2(vc), S[c][j]) : decayed2(d, S[c][j]);
-                    acc[j & 1] = fma2(k[j], S[c][j], acc[j & 1]);
+                    for (int j = 0; j < 8; j++) S[j] = mul2(splat2(d.by), S[j]);
                 }
-                acc[0] = add2(acc[0], acc[1]);
-                const float dot = lane_sum<LN>(acc[0].x + acc[0].y);
-                const float miss = vc - dot;
-                out[c] = MODE == kWalkBack ? dot : miss;
-                const float2 by = splat2(MODE == kWalkBack ? -beta * dot : beta * miss);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    S[c][j] = fma2(k[j], by, S[c][j]);
-                    if (MODE == kWalkBack) S[c][j] = decayed2(d, S[c][j]);
-                }
+                float ks = dot(x.k, S), qs = 0.0f, qk = 0.0f;
                 if (MODE == kWalkY) {
-                    float2 y[2] = {};
-#pragma unroll
-                    for (int j = 0; j < 8; j++) y[j & 1] = fma2(q[j], S[c][j], y[j & 1]);
-                    y[0] = add2(y[0], y[1]);
-                    out[c] = a.scale * lane_sum<LN>(y[0].x + y[0].y);
+                    qs = dot(x.q, S);
+                    qk = dot(x.q, x.k);
                 }
+#pragma unroll
+                for (int o = LN / 2; o > 0; o >>= 1) {
+                    ks += __shfl_xor_sync(kFull, ks, o);
+                    if (MODE == kWalkY) {
+                        qs += __shfl_xor_sync(kFull, qs, o);
+                        qk += __shfl_xor_sync(kFull, qk, o);
+                    }
+                }
+                const float miss = x.v - ks, u = x.beta * miss;
+#pragma unroll
+                for (int j = 0; j < 8; j++) S[j] = fma2(x.k[j], splat2(u), S[j]);
+                out = MODE == kWalkY ? fmaf(qk, u, qs) : miss;
             }
-            if (ln == 0) *reinterpret_cast<float2*>(&s_o[t][col]) = make_float2(out[0], out[1]);
+            if (ln == 0) s_o[t][col] = out;
+        };
+        auto at = [&](int u) { return MODE == kWalkBack ? nv - 1 - u : u; };
+        Token x[2];
+        read(at(0), x[0]);
+#pragma unroll 1
+        for (int u = 0; u < nv; u += 2) {
+            if (u + 1 < nv) read(at(u + 1), x[1]);
+            token(at(u), x[0]);
+            if (u + 1 < nv) {
+                if (u + 2 < nv) read(at(u + 2), x[0]);
+                token(at(u + 1), x[1]);
+            }
         }
         __syncthreads();
         const int64_t row0 = ((b * a.L + t0) * a.H + h) * a.P + p0;
@@ -214,10 +245,10 @@ template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(1
         for (int u = 0; u < TT * PT / 128; u++) {
             const int e = tid + 128 * u, t = e / PT, c = e % PT;
             if (t < nv && c < pleft) {
-                const int64_t at = row0 + t * a.H * a.P + c;
-                const float x = s_o[t][c];
-                if (MODE != kWalkY) w.rows[at] = x;
-                if (MODE != kWalkKeep) st(static_cast<T*>(w.y) + at, MODE == kWalkBack ? s_beta[t] * x : x);
+                const int64_t to = row0 + t * a.H * a.P + c;
+                const float y = s_o[t][c];
+                if (MODE != kWalkY) w.rows[to] = y;
+                if (MODE != kWalkKeep) st(static_cast<T*>(w.y) + to, MODE == kWalkBack ? s_beta[t] * y : y);
             }
         }
     }
@@ -225,6 +256,11 @@ template <typename T, int LN, WalkMode MODE> __global__ void __launch_bounds__(1
         for (int64_t t = len + tid / 32; t < a.L; t += 4)
             for (int c = lane; c < pleft; c += 32) st(static_cast<T*>(w.y) + ((b * a.L + t) * a.H + h) * a.P + p0 + c, 0.0f);
     if (w.last) state(w.last + bh * NPel, true);
+}
+template <typename T, int LN> __global__ void __launch_bounds__(128) k_walk(WalkArgs w) { walk<T, LN, kWalkY>(w, blockIdx.x); }
+template <typename T, int LN> __global__ void __launch_bounds__(128) k_walks(WalkArgs keep, WalkArgs back) {
+    if (blockIdx.y == 0) walk<T, LN, kWalkKeep>(keep, blockIdx.x);
+    else walk<T, LN, kWalkBack>(back, blockIdx.x);
 }
 
 // ---------------------------------------------------------------- one chunk of one head
@@ -492,19 +528,18 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) k_chunk(Chu
     }
 }
 
-template <typename T, int LN> cudaError_t walk_mode(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
-    const unsigned grid = (unsigned)(ceil_div(w.a.P, 256 / LN) * w.a.H * w.a.Bsz);
-    if (mode == kWalkY) k_walk<T, LN, kWalkY><<<grid, 128, 0, st>>>(w);
-    else if (mode == kWalkKeep) k_walk<T, LN, kWalkKeep><<<grid, 128, 0, st>>>(w);
-    else k_walk<T, LN, kWalkBack><<<grid, 128, 0, st>>>(w);
+template <typename T, int LN> cudaError_t walk_go(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
+    const unsigned grid = (unsigned)(ceil_div(w.a.P, 128 / LN) * w.a.H * w.a.Bsz);
+    if (back) k_walks<T, LN><<<dim3(grid, 2), 128, 0, st>>>(w, *back);
+    else k_walk<T, LN><<<grid, 128, 0, st>>>(w);
     return cudaGetLastError();
 }
-template <typename T> cudaError_t walk_io(const WalkArgs& w, WalkMode mode, cudaStream_t st) {
+template <typename T> cudaError_t walk_io(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
     switch (walk_lanes(w.a.N)) {
-        case 1: return walk_mode<T, 1>(w, mode, st);
-        case 2: return walk_mode<T, 2>(w, mode, st);
-        case 4: return walk_mode<T, 4>(w, mode, st);
-        default: return walk_mode<T, 8>(w, mode, st);
+        case 1: return walk_go<T, 1>(w, back, st);
+        case 2: return walk_go<T, 2>(w, back, st);
+        case 4: return walk_go<T, 4>(w, back, st);
+        default: return walk_go<T, 8>(w, back, st);
     }
 }
 
@@ -531,13 +566,20 @@ bool fours(const Args& a) {
 
 }  // namespace
 
-cudaError_t launch_walk(const WalkArgs& args, WalkMode mode, cudaStream_t st) {
-    WalkArgs w = args;
+static cudaError_t go(WalkArgs w, const WalkArgs* back, cudaStream_t st) {
     w.vec = fours(w.a);
-    if (w.a.dtype == 0) return walk_io<float>(w, mode, st);
-    if (w.a.dtype == 1) return walk_io<__half>(w, mode, st);
-    return walk_io<__nv_bfloat16>(w, mode, st);
+    WalkArgs r;
+    if (back) {
+        r = *back;
+        r.vec = w.vec;
+        back = &r;
+    }
+    if (w.a.dtype == 0) return walk_io<float>(w, back, st);
+    if (w.a.dtype == 1) return walk_io<__half>(w, back, st);
+    return walk_io<__nv_bfloat16>(w, back, st);
 }
+cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st) { return go(w, nullptr, st); }
+cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st) { return go(keep, &back, st); }
 
 cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st) {
     if (c.a.dtype == 0) return chunk_io<float>(c, st);
