@@ -26,19 +26,32 @@ constexpr int kChunk = 64;  // tokens whose pairs the backward forms (and the te
 
 // ---------------------------------------------------------------- FP32 path
 constexpr int kWalkT = 16;  // tokens staged at a time
+constexpr int kFour = 4;    // tokens whose products with the state are formed together
 // lanes that share a value channel's N states, 16 each
 inline int walk_lanes(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
+
+// What 16 tokens' products need that does not depend on the state, with c_t the log decay from the start of a
+// token's four through it and cl its end.
+struct Pairs {
+    float kk[kWalkT][kFour], qk[kWalkT][kFour];  // e^{c_t - c_j} (k_t . k_j), (q_t . k_j), j of the token's four
+    float up[kWalkT], down[kWalkT], beta[kWalkT];  // e^{c_t}, e^{cl - c_t}
+    float by[kFour];                               // each four's decay as la::Decay
+    int32_t weak[kFour];
+    float pad[8];
+};
+static_assert(sizeof(Pairs) == 768, "whole 16-byte units");
 
 enum WalkMode { kWalkY, kWalkKeep, kWalkBack };
 struct WalkArgs {
     Args a;
+    const Pairs* pairs; // [Bsz, H, tiles of 16 tokens]
     const float* init;  // state (kWalkBack: adjoint) the walk starts from, or null
     float* last;        // where its last one goes, or null
     void* y;            // kWalkY: y; kWalkBack: dv
     float* rows;        // kWalkKeep: v - e^g S^T k (u / beta); kWalkBack: x; f32 [Bsz, L, H, P]
     float* states;      // kWalkKeep: before each chunk; kWalkBack: adjoint after it; f32 [Bsz, H, chunks, N, P]
     int64_t chunks;
-    bool vec;           // runs of four values are whole and aligned
+    bool vec;           // f32, and runs of four values are whole and aligned: asynchronous copies
 };
 
 struct ChunkArgs {
@@ -51,6 +64,7 @@ struct ChunkArgs {
     float *dg, *dbeta;             // dg: may be null
 };
 
+cudaError_t launch_pairs(const Args& a, Pairs* pairs, cudaStream_t st);
 cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st);                          // kWalkY
 cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st);  // the backward's two, at once
 cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st);

@@ -20,7 +20,7 @@ int check_sizes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t
     // products stay inside int64, grids inside 2^31 - 1 blocks
     if (Bsz > (1 << 20) || L > (1ll << 31) || H > (1 << 16) || P > (1 << 16)) return SS_ERR_UNSUPPORTED;
     if (Bsz * H * ceil_div(P, 16) > (1ll << 24) || Bsz * L > (1ll << 36)) return SS_ERR_UNSUPPORTED;
-    if (Bsz * H * ceil_div(P, 16) * ceil_div(L, kChunk) >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
+    if (Bsz * H * ceil_div(P, 8) * ceil_div(L, kWalkT) >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
     return SS_OK;
 }
 
@@ -37,15 +37,18 @@ struct Layout {
     }
 };
 
+size_t pairs_bytes(int64_t Bsz, int64_t L, int64_t H) { return (size_t)Bsz * H * ceil_div(L, kWalkT) * sizeof(Pairs); }
+
 // The FP32 backward's workspace.
 struct Bwd32 {
     int64_t chunks;
-    size_t miss, x, before, after, dq, dk;
+    size_t pairs, miss, x, before, after, dq, dk;
 };
 Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     Bwd32 b;
     b.chunks = ceil_div(L, kChunk);
     const size_t rows = (size_t)Bsz * L * H * P * 4, states = (size_t)Bsz * H * b.chunks * N * P * 4;
+    b.pairs = l.take(pairs_bytes(Bsz, L, H));
     b.miss = l.take(rows);
     b.x = l.take(rows);
     b.before = l.take(states);
@@ -314,10 +317,12 @@ template <typename D> NormArgs norm_args(const D& d) {
 extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
-    if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L) || !tc_sizes(L, N, P, dtype)) return 0;
-    Layout l;
-    fwdtc_layout(l, Bsz, L, H, G, N, P, dtype);
-    return l.total;
+    if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
+    // the larger of what the two paths need: strides and pointers, which decide between them, are not known here
+    Layout l, t;
+    l.take(pairs_bytes(Bsz, L, H));
+    if (tc_sizes(L, N, P, dtype)) fwdtc_layout(t, Bsz, L, H, G, N, P, dtype);
+    return l.total > t.total ? l.total : t.total;
 }
 
 int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
@@ -339,9 +344,11 @@ int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
     if (ran || tc != SS_OK) return tc;
     WalkArgs w = {};
     w.a = a;
+    w.pairs = static_cast<const Pairs*>(d->workspace);
     w.init = a.h0;
     w.last = d->last_state;
     w.y = d->y;
+    if (launch_pairs(a, static_cast<Pairs*>(d->workspace), st) != cudaSuccess) return SS_ERR_CUDA;
     return launch_walk(w, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -383,6 +390,8 @@ int ss_gdr_bwd(const ss_gdr_bwd_desc* d, void* stream) {
     WalkArgs keep = {}, back = {};
     keep.a = back.a = a;
     keep.chunks = back.chunks = bl.chunks;
+    Pairs* pairs = reinterpret_cast<Pairs*>(ws + bl.pairs);
+    keep.pairs = back.pairs = pairs;
     keep.init = a.h0;
     keep.rows = f32(bl.miss);
     keep.states = f32(bl.before);
@@ -391,7 +400,7 @@ int ss_gdr_bwd(const ss_gdr_bwd_desc* d, void* stream) {
     back.y = d->dv;
     back.rows = f32(bl.x);
     back.states = f32(bl.after);
-    if (launch_walks(keep, back, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_pairs(a, pairs, st) != cudaSuccess || launch_walks(keep, back, st) != cudaSuccess) return SS_ERR_CUDA;
     ChunkArgs c = {};
     c.a = a;
     c.miss = f32(bl.miss);

@@ -1,10 +1,9 @@
 // Gated delta rule on the FP32 units: every io type, any N <= 128, P and strides.
 // f32 inputs run here, and 16-bit inputs that the tensor-core path's rules exclude.
 //
-// Forward: the recurrence itself, token by token.  The columns of the state (value
+// Forward: the recurrence itself, four tokens at a time.  The columns of the state (value
 // channels) are independent, so a column's N values lie in the registers of N / 16
-// lanes and every token costs two sums over those lanes (S^T k, and S^T q off the
-// chain).  Backward: with x_t = R_t^T k_t, R_t the adjoint of S_t,
+// lanes.  Backward: with x_t = R_t^T k_t, R_t the adjoint of S_t,
 //   R_t = (adjoint left by t + 1) + scale q_t dy_t^T,   adjoint left = e^{g_t} (R_t - beta_t k_t x_t^T)
 // a second walk of the same form from the last token gives x and the adjoints R at
 // the chunks' ends, the forward's walk the misses w_t = v_t - e^{g_t} S^T k_t
@@ -30,26 +29,12 @@ using la::two_diff;
 
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// Four adjacent values, of which `left` exist; vec: they exist together and are aligned.
-template <typename T> __device__ __forceinline__ float4 fetch4(const T* p, int64_t left, bool vec) {
-    float x[4] = {};
-    if (vec) {
-        if (left > 0) {
-            if constexpr (sizeof(T) == 4) return at4(p);
-            union {
-                uint2 m;
-                T t[4];
-            } u;
-            u.m = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-            for (int e = 0; e < 4; e++) x[e] = ldf(&u.t[e]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; e++) x[e] = e < left ? ldf(p + e) : 0.0f;
-    }
-    return make_float4(x[0], x[1], x[2], x[3]);
+// 16 bytes on their way to shared memory, or zeros
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 template <int LN> __device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
@@ -57,19 +42,89 @@ template <int LN> __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
-// One block: 128 / LN value channels of one head, one a lane and LN lanes a channel; lane ln of a
+// One block: 16 tokens of one head, thread (token t, j of its four, which product).
+template <typename T> __global__ void __launch_bounds__(128) k_pairs(Args a, Pairs* pairs, int64_t tiles) {
+    constexpr int TT = kWalkT, LD = la::kMaxN + 4;
+    __shared__ __align__(16) float s_k[TT][LD], s_q[TT][LD];
+    __shared__ float s_g[TT];
+    const int tid = threadIdx.x, lane = tid & 31, N = (int)a.N, NP = (N + 3) & ~3;
+    int64_t id = blockIdx.x;
+    const int64_t tile = id % tiles;
+    id /= tiles;
+    const int64_t h = id % a.H, b = id / a.H, hq = h / (a.H / a.G), t0 = tile * TT;
+    const int nv = (int)max((int64_t)0, min((int64_t)TT, row_length(a, b) - t0));
+    if (nv == 0) return;
+    const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + t0 * a.k.token + hq * a.N;
+    const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + t0 * a.q.token + hq * a.N;
+    Pairs* to = pairs + blockIdx.x;
+#pragma unroll 4
+    for (int i = tid; i < TT * la::kMaxN; i += 128) {
+        const int t = i / la::kMaxN, n = i % la::kMaxN;
+        if (n >= NP) continue;
+        const bool on = t < nv && n < N;
+        s_k[t][n] = on ? ldf(kp + t * a.k.token + n) : 0.0f;
+        s_q[t][n] = on ? a.scale * ldf(qp + t * a.q.token + n) : 0.0f;
+    }
+    if (tid < 32) {  // decays inside a four: sums of at most four numbers
+        const float g = lane < nv ? log_decay(a, b, t0 + lane, h) : 0.0f;
+        const int f = lane & 3;
+        float up = g, down = 0.0f;
+#pragma unroll
+        for (int o = 1; o < 4; o++) {
+            const float before = __shfl_up_sync(kFull, g, o), after = __shfl_down_sync(kFull, g, o);
+            if (o <= f) up += before;
+            if (o <= 3 - f) down += after;
+        }
+        if (lane < TT) {
+            s_g[lane] = g;
+            to->up[lane] = expf(up);
+            to->down[lane] = expf(down);
+            to->beta[lane] = lane < nv ? a.beta[(b * a.L + t0 + lane) * a.H + h] : 0.0f;
+            if (f == 3) {
+                const Decay d = la::decay_of(up);
+                to->by[lane >> 2] = d.by;
+                to->weak[lane >> 2] = d.weak;
+            }
+        }
+    }
+    __syncthreads();
+    const int t = tid >> 3, j = tid >> 1 & 3, o = t & ~3, f = t & 3;
+    const bool is_q = tid & 1;
+    const float *x = is_q ? s_q[t] : s_k[t], *y = s_k[o + j];
+    float s[4] = {};
+#pragma unroll 4
+    for (int n = 0; n < NP; n += 4) {
+        const float4 u = at4(x + n), v = at4(y + n);
+        s[0] = fmaf(u.x, v.x, s[0]);
+        s[1] = fmaf(u.y, v.y, s[1]);
+        s[2] = fmaf(u.z, v.z, s[2]);
+        s[3] = fmaf(u.w, v.w, s[3]);
+    }
+    float c = 0.0f;
+#pragma unroll
+    for (int e = 1; e < 4; e++)
+        if (e > j && e <= f) c += s_g[o + e];
+    (is_q ? to->qk : to->kk)[t][j] = j <= f ? expf(c) * ((s[0] + s[1]) + (s[2] + s[3])) : 0.0f;
+}
+
+// One block: 64 / LN value channels of one head, one a lane and LN lanes a channel; lane ln of a
 // channel holds the states n = 4 (ln + LN j) + e, j, e < 4, in pairs of e (runs of four so that the
-// lanes' reads of k and q are 16 bytes side by side).  The forward takes S^T k and S^T q in one pass
-// over the old state, y = S^T q + (q . k) u: one exchange of sums a token on the chain.  A token's k and
-// q are read while the one before is worked on.
+// lanes' reads of k and q are 16 bytes side by side; those reads, four cycles of shared memory each, are
+// what bounds an SM's blocks, so blocks are small and spread).  Tokens go by fours, whose products with the
+// old state do not wait for one another:
+//   miss_t = v_t - e^{c_t} S^T k_t - sum_{j < t} e^{c_t - c_j} (k_t . k_j) u_j,   u_t = beta_t miss_t
+//   y_t = e^{c_t} S^T q_t + sum_{j <= t} e^{c_t - c_j} (q_t . k_j) u_j,   S <- e^{cl} S + sum_j e^{cl - c_j} k_j u_j^T
+// so that a chain of sums over the lanes is paid once for four tokens.  The backward's walk is the same from
+// the other end.  2 x 1000 tokens, 24 heads, N = P = 64: PLACEHOLDER us (token by token 228).
 template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void walk(const WalkArgs& w, int64_t id) {
-    constexpr int NP = 16 * LN, PT = 128 / LN, TT = kWalkT;
-    constexpr int EK = NP * TT / 512 < 1 ? 1 : NP * TT / 512, EV = PT * TT / 512 < 1 ? 1 : PT * TT / 512;
-    __shared__ __align__(16) float s_k[TT][NP], s_q[TT][NP], s_v[TT][PT], s_o[TT][PT];
-    __shared__ float s_a[TT], s_beta[TT];
-    __shared__ uint32_t s_weak;
+    constexpr int NT = 64, NP = 16 * LN, PT = NT / LN, TT = kWalkT;
+    struct Stage {
+        float k[TT][NP], q[MODE == kWalkKeep ? 1 : TT][NP], v[TT][PT];
+        Pairs p;
+    };
+    __shared__ __align__(16) Stage s_stage[2];
     const Args& a = w.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane % LN;
+    const int tid = threadIdx.x, lane = tid & 31, ln = lane % LN;
     const int64_t ptiles = (a.P + PT - 1) / PT;
     const int64_t p0 = (id % ptiles) * PT;
     id /= ptiles;
@@ -81,6 +136,7 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
     const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hq * a.N;
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
     const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P + p0;
+    const int64_t all_tiles = (a.L + TT - 1) / TT;
 
     float2 S[8];  // [2 j + e / 2]
     auto state = [&](float* p, bool put) {  // p: the head's N x P
@@ -102,51 +158,56 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
 
     const int64_t tiles = (len + TT - 1) / TT;
     auto start = [&](int64_t i) { return (MODE == kWalkBack ? tiles - 1 - i : i) * TT; };
-    float4 rk[EK], rq[EK], rv[EV];
-    float rg = 0.0f, rb = 0.0f;
     auto fetch = [&](int64_t i) {
+        Stage& s = s_stage[i & 1];
         const int64_t t0 = start(i);
         const int nv = (int)min((int64_t)TT, len - t0);
+        const char* pairs = reinterpret_cast<const char*>(w.pairs + bh * all_tiles + t0 / TT);
+        if (tid < (int)sizeof(Pairs) / 16) copy16(reinterpret_cast<char*>(&s.p) + 16 * tid, pairs + 16 * tid, true);
+        if (w.vec) {
 #pragma unroll
-        for (int e = 0; e < EK; e++) {
-            const int x = tid + 128 * e, t = x / (NP / 4), n = x % (NP / 4) * 4, left = t < nv ? N - n : 0;
-            rk[e] = fetch4(kp + (t0 + t) * a.k.token + n, left, w.vec);
-            if (MODE != kWalkKeep) rq[e] = fetch4(qp + (t0 + t) * a.q.token + n, left, w.vec);
-        }
+            for (int e = 0; e < TT * NP / 4 / NT; e++) {
+                const int x = tid + NT * e, t = x / (NP / 4), n = x % (NP / 4) * 4;
+                const bool on = t < nv && n < N;
+                const int64_t tt = on ? t0 + t : 0;
+                copy16(&s.k[t][n], kp + tt * a.k.token + (on ? n : 0), on);
+                if (MODE != kWalkKeep) copy16(&s.q[t][n], qp + tt * a.q.token + (on ? n : 0), on);
+            }
 #pragma unroll
-        for (int e = 0; e < EV; e++) {
-            const int x = tid + 128 * e, t = x / (PT / 4), c = x % (PT / 4) * 4;
-            rv[e] = fetch4(vp + (t0 + t) * vin.token + c, t < nv ? pleft - c : 0, w.vec);
-        }
-        if (tid < TT) {
-            rg = tid < nv ? log_decay(a, b, t0 + tid, h) : 0.0f;
-            rb = tid < nv ? a.beta[(b * a.L + t0 + tid) * a.H + h] : 0.0f;
-        }
-    };
-    struct Token {
-        float2 k[8], q[8];
-        float a, beta, v;
-    };
-    auto read = [&](int t, Token& x) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float4 kk = at4(&s_k[t][4 * (ln + LN * j)]);
-            x.k[2 * j] = make_float2(kk.x, kk.y);
-            x.k[2 * j + 1] = make_float2(kk.z, kk.w);
-            if (MODE != kWalkKeep) {
-                const float4 qq = at4(&s_q[t][4 * (ln + LN * j)]);
-                x.q[2 * j] = make_float2(qq.x, qq.y);
-                x.q[2 * j + 1] = make_float2(qq.z, qq.w);
+            for (int e = 0; e < (TT * PT / 4 + NT - 1) / NT; e++) {
+                const int x = tid + NT * e, t = x / (PT / 4), c = x % (PT / 4) * 4;
+                if (t >= TT) break;
+                const bool on = t < nv && c < pleft;
+                copy16(&s.v[t][c], vp + (on ? t0 + t : 0) * vin.token + (on ? c : 0), on);
+            }
+        } else {
+#pragma unroll 4
+            for (int x = tid; x < TT * NP; x += NT) {
+                const int t = x / NP, n = x % NP;
+                const bool on = t < nv && n < N;
+                s.k[t][n] = on ? ldf(kp + (t0 + t) * a.k.token + n) : 0.0f;
+                if (MODE != kWalkKeep) s.q[t][n] = on ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
+            }
+#pragma unroll 4
+            for (int x = tid; x < TT * PT; x += NT) {
+                const int t = x / PT, c = x % PT;
+                s.v[t][c] = t < nv && c < pleft ? ldf(vp + (t0 + t) * vin.token + c) : 0.0f;
             }
         }
-        x.a = s_a[t];
-        x.beta = s_beta[t];
-        x.v = s_v[t][col];
+        copy_commit();
     };
-    auto dot = [&](const float2 (&x)[8], const float2 (&y)[8]) {
+    auto read = [&](const float* from, float2 (&x)[8]) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float4 v = at4(from + 4 * (ln + LN * j));
+            x[2 * j] = make_float2(v.x, v.y);
+            x[2 * j + 1] = make_float2(v.z, v.w);
+        }
+    };
+    auto dot = [&](const float2 (&x)[8]) {
         float2 s[2] = {};
 #pragma unroll
-        for (int j = 0; j < 8; j++) s[j & 1] = fma2(x[j], y[j], s[j & 1]);
+        for (int j = 0; j < 8; j++) s[j & 1] = fma2(x[j], S[j], s[j & 1]);
         s[0] = add2(s[0], s[1]);
         return s[0].x + s[0].y;
     };
@@ -154,111 +215,126 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
     for (int64_t i = 0; i < tiles; i++) {
         const int64_t t0 = start(i);
         const int nv = (int)min((int64_t)TT, len - t0);
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < EK; e++)
-            if (tid + 128 * e < TT * NP / 4) {
-                reinterpret_cast<float4*>(s_k)[tid + 128 * e] = rk[e];
-                if (MODE != kWalkKeep) {
-                    const float f = a.scale;
-                    reinterpret_cast<float4*>(s_q)[tid + 128 * e] = make_float4(f * rq[e].x, f * rq[e].y, f * rq[e].z, f * rq[e].w);
-                }
-            }
-#pragma unroll
-        for (int e = 0; e < EV; e++)
-            if (tid + 128 * e < TT * PT / 4) reinterpret_cast<float4*>(s_v)[tid + 128 * e] = rv[e];
-        if (warp == 0) {
-            const Decay d = la::decay_of(lane < TT ? rg : 0.0f);
-            const uint32_t weak = __ballot_sync(kFull, d.weak);
-            if (lane < TT) {
-                s_a[lane] = d.by;
-                s_beta[lane] = rb;
-            }
-            if (lane == 0) s_weak = weak;
-        }
-        __syncthreads();
+        const Stage& s = s_stage[i & 1];
+        copy_wait();
+        __syncthreads();  // (and: the stage before is read)
         if (i + 1 < tiles) fetch(i + 1);
         // the state before a chunk's first token, the adjoint after its last one
         if (MODE == kWalkKeep ? t0 % kChunk == 0 : MODE == kWalkBack && (i == 0 || (t0 + TT) % kChunk == 0))
             state(w.states + (bh * w.chunks + t0 / kChunk) * NPel, true);
-        const uint32_t weak = s_weak;
-        auto token = [&](int t, const Token& x) {
-            const Decay d = {x.a, (weak >> t & 1) != 0};
-            float out;
+        const int fours = (nv + 3) >> 2;
+        const int64_t row0 = ((b * a.L + t0) * a.H + h) * a.P + p0 + col;
+#pragma unroll 1
+        for (int u = 0; u < fours; u++) {
+            const int o = kFour * (MODE == kWalkBack ? fours - 1 - u : u);
+            float2 k[kFour][8];
+            float ks[kFour], qs[kFour];
+#pragma unroll
+            for (int t = 0; t < kFour; t++) {
+                read(s.k[o + t], k[t]);
+                ks[t] = dot(k[t]);
+            }
+            if (MODE == kWalkY)
+#pragma unroll
+                for (int t = 0; t < kFour; t++) {
+                    float2 q[8];
+                    read(s.q[o + t], q);
+                    qs[t] = dot(q);
+                }
+#pragma unroll
+            for (int r = LN / 2; r > 0; r >>= 1)
+#pragma unroll
+                for (int t = 0; t < kFour; t++) {
+                    ks[t] += __shfl_xor_sync(kFull, ks[t], r);
+                    if (MODE == kWalkY) qs[t] += __shfl_xor_sync(kFull, qs[t], r);
+                }
+            float v[kFour], x[kFour], kk[kFour][kFour], qk[kFour][kFour], up[kFour], down[kFour], beta[kFour];
+            auto row = [](float (&to)[kFour], const float* from) {
+                const float4 f = at4(from);
+                to[0] = f.x;
+                to[1] = f.y;
+                to[2] = f.z;
+                to[3] = f.w;
+            };
+#pragma unroll
+            for (int t = 0; t < kFour; t++) {
+                v[t] = s.v[o + t][col];
+                if (t > 0) row(kk[t], s.p.kk[o + t]);
+                if (MODE != kWalkKeep) row(qk[t], s.p.qk[o + t]);
+            }
+            row(up, &s.p.up[o]);
+            row(down, &s.p.down[o]);
+            row(beta, &s.p.beta[o]);
+            const float by = s.p.by[o >> 2];
+            const bool weak = s.p.weak[o >> 2];
             if (MODE == kWalkBack) {
 #pragma unroll
-                for (int j = 0; j < 8; j++) S[j] = fma2(x.q[j], splat2(x.v), S[j]);
-                out = lane_sum<LN>(dot(x.k, S));
-                const float2 by = splat2(-x.beta * out);
+                for (int t = kFour - 1; t >= 0; t--) {
+                    float z = down[t] * ks[t];
 #pragma unroll
-                for (int j = 0; j < 8; j++) S[j] = fma2(x.k[j], by, S[j]);
-                if (d.weak) {
+                    for (int e = t; e < kFour; e++) z = fmaf(qk[e][t], v[e], z);
 #pragma unroll
-                    for (int j = 0; j < 8; j++) S[j] = fma2(splat2(d.by), S[j], S[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j++) S[j] = mul2(splat2(d.by), S[j]);
+                    for (int e = kFour - 1; e > t; e--) z = fmaf(-beta[e] * kk[e][t], x[e], z);
+                    x[t] = z;
                 }
             } else {
-                if (d.weak) {
+                float us[kFour];
 #pragma unroll
-                    for (int j = 0; j < 8; j++) S[j] = fma2(splat2(d.by), S[j], S[j]);
-                } else {
+                for (int t = 0; t < kFour; t++) {
+                    float z = fmaf(-up[t], ks[t], v[t]);
 #pragma unroll
-                    for (int j = 0; j < 8; j++) S[j] = mul2(splat2(d.by), S[j]);
-                }
-                float ks = dot(x.k, S), qs = 0.0f, qk = 0.0f;
-                if (MODE == kWalkY) {
-                    qs = dot(x.q, S);
-                    qk = dot(x.q, x.k);
+                    for (int e = 0; e < t; e++) z = fmaf(-kk[t][e], us[e], z);
+                    x[t] = z;
+                    us[t] = beta[t] * z;
                 }
 #pragma unroll
-                for (int o = LN / 2; o > 0; o >>= 1) {
-                    ks += __shfl_xor_sync(kFull, ks, o);
-                    if (MODE == kWalkY) {
-                        qs += __shfl_xor_sync(kFull, qs, o);
-                        qk += __shfl_xor_sync(kFull, qk, o);
+                for (int t = 0; t < kFour; t++) ks[t] = down[t] * us[t];  // what enters the state
+                if (MODE == kWalkY)
+#pragma unroll
+                    for (int t = 0; t < kFour; t++) {
+                        float z = a.scale * up[t] * qs[t];
+#pragma unroll
+                        for (int e = 0; e <= t; e++) z = fmaf(qk[t][e], us[e], z);
+                        x[t] = z;
                     }
+            }
+            if (weak) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) S[j] = fma2(splat2(by), S[j], S[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) S[j] = mul2(splat2(by), S[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < kFour; t++) {
+                const float2 f = splat2(MODE == kWalkBack ? -up[t] * beta[t] * x[t] : ks[t]);
+#pragma unroll
+                for (int j = 0; j < 8; j++) S[j] = fma2(k[t][j], f, S[j]);
+                if (MODE == kWalkBack) {
+                    float2 q[8];
+                    read(s.q[o + t], q);
+                    const float2 y = splat2(a.scale * up[t] * v[t]);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) S[j] = fma2(q[j], y, S[j]);
                 }
-                const float miss = x.v - ks, u = x.beta * miss;
+            }
+            if (ln == 0 && col < pleft)
 #pragma unroll
-                for (int j = 0; j < 8; j++) S[j] = fma2(x.k[j], splat2(u), S[j]);
-                out = MODE == kWalkY ? fmaf(qk, u, qs) : miss;
-            }
-            if (ln == 0) s_o[t][col] = out;
-        };
-        auto at = [&](int u) { return MODE == kWalkBack ? nv - 1 - u : u; };
-        Token x[2];
-        read(at(0), x[0]);
-#pragma unroll 1
-        for (int u = 0; u < nv; u += 2) {
-            if (u + 1 < nv) read(at(u + 1), x[1]);
-            token(at(u), x[0]);
-            if (u + 1 < nv) {
-                if (u + 2 < nv) read(at(u + 2), x[0]);
-                token(at(u + 1), x[1]);
-            }
-        }
-        __syncthreads();
-        const int64_t row0 = ((b * a.L + t0) * a.H + h) * a.P + p0;
-#pragma unroll
-        for (int u = 0; u < TT * PT / 128; u++) {
-            const int e = tid + 128 * u, t = e / PT, c = e % PT;
-            if (t < nv && c < pleft) {
-                const int64_t to = row0 + t * a.H * a.P + c;
-                const float y = s_o[t][c];
-                if (MODE != kWalkY) w.rows[to] = y;
-                if (MODE != kWalkKeep) st(static_cast<T*>(w.y) + to, MODE == kWalkBack ? s_beta[t] * y : y);
-            }
+                for (int t = 0; t < kFour; t++)
+                    if (o + t < nv) {
+                        const int64_t to = row0 + (o + t) * a.H * a.P;
+                        if (MODE != kWalkY) w.rows[to] = x[t];
+                        if (MODE != kWalkKeep) st(static_cast<T*>(w.y) + to, MODE == kWalkBack ? beta[t] * x[t] : x[t]);
+                    }
         }
     }
     if (MODE != kWalkKeep)  // rows that do not count
-        for (int64_t t = len + tid / 32; t < a.L; t += 4)
+        for (int64_t t = len + tid / 32; t < a.L; t += NT / 32)
             for (int c = lane; c < pleft; c += 32) st(static_cast<T*>(w.y) + ((b * a.L + t) * a.H + h) * a.P + p0 + c, 0.0f);
     if (w.last) state(w.last + bh * NPel, true);
 }
-template <typename T, int LN> __global__ void __launch_bounds__(128) k_walk(WalkArgs w) { walk<T, LN, kWalkY>(w, blockIdx.x); }
-template <typename T, int LN> __global__ void __launch_bounds__(128) k_walks(WalkArgs keep, WalkArgs back) {
+template <typename T, int LN> __global__ void __launch_bounds__(64) k_walk(WalkArgs w) { walk<T, LN, kWalkY>(w, blockIdx.x); }
+template <typename T, int LN> __global__ void __launch_bounds__(64) k_walks(WalkArgs keep, WalkArgs back) {
     if (blockIdx.y == 0) walk<T, LN, kWalkKeep>(keep, blockIdx.x);
     else walk<T, LN, kWalkBack>(back, blockIdx.x);
 }
@@ -529,9 +605,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) k_chunk(Chu
 }
 
 template <typename T, int LN> cudaError_t walk_go(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
-    const unsigned grid = (unsigned)(ceil_div(w.a.P, 128 / LN) * w.a.H * w.a.Bsz);
-    if (back) k_walks<T, LN><<<dim3(grid, 2), 128, 0, st>>>(w, *back);
-    else k_walk<T, LN><<<grid, 128, 0, st>>>(w);
+    const unsigned grid = (unsigned)(ceil_div(w.a.P, 64 / LN) * w.a.H * w.a.Bsz);
+    if (back) k_walks<T, LN><<<dim3(grid, 2), 64, 0, st>>>(w, *back);
+    else k_walk<T, LN><<<grid, 64, 0, st>>>(w);
     return cudaGetLastError();
 }
 template <typename T> cudaError_t walk_io(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
@@ -556,11 +632,11 @@ template <typename T> cudaError_t chunk_io(const ChunkArgs& c, cudaStream_t st) 
     return chunk_n<T, 8>(c, st);
 }
 
-// Whether every run of four values of q, k, v, dy is whole and aligned.
+// Whether q, k, v and dy are f32 and every run of four values is whole and aligned.
 bool fours(const Args& a) {
-    const uintptr_t bytes = a.dtype == 0 ? 16 : 8;
+    if (a.dtype != 0) return false;
     for (const In* x : {&a.q, &a.k, &a.v, &a.dy})
-        if (reinterpret_cast<uintptr_t>(x->p) % bytes != 0 || x->token % 4 != 0 || x->batch % 4 != 0) return false;
+        if (reinterpret_cast<uintptr_t>(x->p) % 16 != 0 || x->token % 4 != 0 || x->batch % 4 != 0) return false;
     return a.N % 4 == 0 && a.P % 4 == 0;
 }
 
@@ -577,6 +653,14 @@ static cudaError_t go(WalkArgs w, const WalkArgs* back, cudaStream_t st) {
     if (w.a.dtype == 0) return walk_io<float>(w, back, st);
     if (w.a.dtype == 1) return walk_io<__half>(w, back, st);
     return walk_io<__nv_bfloat16>(w, back, st);
+}
+cudaError_t launch_pairs(const Args& a, Pairs* pairs, cudaStream_t st) {
+    const int64_t tiles = ceil_div(a.L, kWalkT);
+    const unsigned grid = (unsigned)(a.Bsz * a.H * tiles);
+    if (a.dtype == 0) k_pairs<float><<<grid, 128, 0, st>>>(a, pairs, tiles);
+    else if (a.dtype == 1) k_pairs<__half><<<grid, 128, 0, st>>>(a, pairs, tiles);
+    else k_pairs<__nv_bfloat16><<<grid, 128, 0, st>>>(a, pairs, tiles);
+    return cudaGetLastError();
 }
 cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st) { return go(w, nullptr, st); }
 cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st) { return go(keep, &back, st); }
