@@ -100,7 +100,7 @@ struct NormArgs {
     int flags, dtype;
 };
 // Blocks of each side; a pure function of its arguments.
-int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N);
+int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N, bool backward);
 cudaError_t launch_qknorm(const NormArgs& a, bool backward, cudaStream_t st);
 
 }  // namespace gdr

@@ -21,16 +21,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr uint64_t kNoAngle = ~0ull;  // a frequency that is not finite (fractions end at 2^64 - 2^11)
 constexpr int kTable = 2048;  // angles a tile of tokens may need (16 KB)
+constexpr int kTile = 256;    // tokens of a tile at most
 
 template <typename T, int V> struct Run {  // V values moved at once
     using M = typename std::conditional<sizeof(T) * V == 16, uint4, typename std::conditional<sizeof(T) * V == 8, uint2, T>::type>::type;
 };
-template <typename T, int V> __device__ __forceinline__ void get(const T* p, float (&f)[V]) {
+template <typename T, int V> __device__ __forceinline__ void widen(const typename Run<T, V>::M& m, float (&f)[V]) {
     union {
         typename Run<T, V>::M m;
         T t[V];
     } u;
-    u.m = *reinterpret_cast<const typename Run<T, V>::M*>(p);
+    u.m = m;
 #pragma unroll
     for (int e = 0; e < V; e++) f[e] = ldf(&u.t[e]);
 }
@@ -50,6 +51,7 @@ template <typename T, int V, int LPR, int SPT, bool BWD>
 __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, int64_t blocks_q) {
     constexpr int RPB = kThreads / LPR;  // rows at once
     __shared__ float2 s_turn[kTable];
+    __shared__ int64_t s_at[BWD ? 2 : 1][kTile];  // where each token of the tile begins in x (and in d)
     __shared__ uint64_t s_freq[la::kMaxN];
     __shared__ float s_dw[BWD ? 2 * V * SPT * kThreads : 1];
     const int sd = blockIdx.x >= blocks_q;
@@ -108,9 +110,18 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
         }
     };
     const float inv = l2 ? 1.0f : 1.0f / (float)N;
+    using M = typename Run<T, V>::M;
+    struct Raw {
+        M x[SPT][2], d[BWD ? SPT : 1][2];
+    };
     for (int64_t t0 = block * tile; t0 < tokens; t0 += blocks * tile) {
         const int nt = (int)min(tile, tokens - t0), rows = nt * heads;
         __syncthreads();
+        for (int i = tid; i < nt; i += kThreads) {
+            const int64_t b = (t0 + i) / a.L, tb = t0 + i - b * a.L;
+            s_at[0][i] = b * z.x.batch + tb * z.x.token;
+            if (BWD) s_at[BWD][i] = b * z.d.batch + tb * z.d.token;
+        }
         for (int i = tid; i < nt * pairs; i += kThreads) {
             const int64_t t = t0 + i / pairs;
             const int64_t pos = a.positions ? (int64_t)a.positions[t] : t % a.L;
@@ -121,31 +132,39 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
             s_turn[i] = f == kNoAngle ? make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)) : make_float2(cs, sn);
         }
         __syncthreads();
+        auto fetch = [&](int r, Raw& raw) {  // a row's runs on their way
+            const int tl = r < rows ? r / heads : 0, h = r < rows ? r - tl * heads : 0;
+            const T* xp = static_cast<const T*>(z.x.p) + s_at[0][tl] + (int64_t)h * N;
+            const T* dp = BWD ? static_cast<const T*>(z.d.p) + s_at[BWD][tl] + (int64_t)h * N : nullptr;
+#pragma unroll
+            for (int s = 0; s < SPT; s++) {
+                raw.x[s][0] = raw.x[s][1] = M{};
+                if (on[s]) raw.x[s][0] = *reinterpret_cast<const M*>(xp + ia[s]);
+                if (onb[s]) raw.x[s][1] = *reinterpret_cast<const M*>(xp + ib[s]);
+                if (BWD) {
+                    raw.d[BWD ? s : 0][0] = raw.d[BWD ? s : 0][1] = M{};
+                    if (on[s]) raw.d[BWD ? s : 0][0] = *reinterpret_cast<const M*>(dp + ia[s]);
+                    if (onb[s]) raw.d[BWD ? s : 0][1] = *reinterpret_cast<const M*>(dp + ib[s]);
+                }
+            }
+        };
+        Raw next;
+        fetch(slot, next);
         for (int r0 = 0; r0 < rows; r0 += RPB) {
             const int r = r0 + slot;
             const bool have = r < rows;
             const int tl = have ? r / heads : 0, h = have ? r - tl * heads : 0;
-            const int64_t t = t0 + tl, b = t / a.L, tb = t - b * a.L;
-            const T* xp = static_cast<const T*>(z.x.p) + b * z.x.batch + tb * z.x.token + (int64_t)h * N;
+            const int64_t t = t0 + tl;
             float x[SPT][2][V], d[SPT][2][V];
             float sum = 0.0f;
 #pragma unroll
-            for (int s = 0; s < SPT; s++) {
+            for (int s = 0; s < SPT; s++)
 #pragma unroll
-                for (int e = 0; e < V; e++) x[s][0][e] = x[s][1][e] = 0.0f;
-                if (have && on[s]) get<T, V>(xp + ia[s], x[s][0]);
-                if (have && onb[s]) get<T, V>(xp + ib[s], x[s][1]);
-            }
-            if (BWD) {
-                const T* dp = static_cast<const T*>(z.d.p) + b * z.d.batch + tb * z.d.token + (int64_t)h * N;
-#pragma unroll
-                for (int s = 0; s < SPT; s++) {
-#pragma unroll
-                    for (int e = 0; e < V; e++) d[s][0][e] = d[s][1][e] = 0.0f;
-                    if (have && on[s]) get<T, V>(dp + ia[s], d[s][0]);
-                    if (have && onb[s]) get<T, V>(dp + ib[s], d[s][1]);
+                for (int c = 0; c < 2; c++) {
+                    widen<T, V>(next.x[s][c], x[s][c]);
+                    if (BWD) widen<T, V>(next.d[BWD ? s : 0][c], d[s][c]);
                 }
-            }
+            if (r0 + RPB < rows) fetch(r + RPB, next);
 #pragma unroll
             for (int s = 0; s < SPT; s++)
 #pragma unroll
@@ -219,23 +238,24 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
     }
 }
 
-// Weights' gradients: the blocks' parts in order.  Block: 32 channels of one side, 8 warps
-// taking every eighth part.
-__global__ void __launch_bounds__(256) k_weights(NormArgs a, int64_t blocks_q, int64_t blocks) {
-    __shared__ float s[8][32];
+// Weights' gradients: the blocks' parts in order.  Block: 32 channels of one side, 32 warps
+// taking every 32nd part.
+__global__ void __launch_bounds__(1024) k_weights(NormArgs a, int64_t blocks_q, int64_t blocks) {
+    __shared__ float s[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sd = blockIdx.y;
     const int64_t n = (int64_t)blockIdx.x * 32 + lane;
     float* out = a.side[sd].dweight;
     if (!out) return;
     float v = 0.0f;
     if (n < a.N)
-        for (int64_t i = (sd ? blocks_q : 0) + warp; i < (sd ? blocks : blocks_q); i += 8) v += a.part[i * a.N + n];
+#pragma unroll 16
+        for (int64_t i = (sd ? blocks_q : 0) + warp; i < (sd ? blocks : blocks_q); i += 32) v += a.part[i * a.N + n];
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && n < a.N) {
         float t = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 8; u++) t += s[u][lane];
+        for (int u = 0; u < 32; u++) t += s[u][lane];
         out[n] = t;
     }
 }
@@ -244,11 +264,12 @@ __global__ void __launch_bounds__(256) k_weights(NormArgs a, int64_t blocks_q, i
 int64_t tile_tokens(int64_t heads, int64_t pairs, int lanes) {
     int64_t t = ceil_div(4 * (kThreads / lanes), heads);
     if (pairs > 0 && t * pairs > kTable) t = kTable / pairs;
+    if (t > kTile) t = kTile;
     return t < 1 ? 1 : t;
 }
 
 template <typename T, int V, int LPR, int SPT> cudaError_t launch(const NormArgs& a, bool bwd, cudaStream_t st) {
-    const int64_t tokens = a.Bsz * a.L, bq = norm_blocks(tokens, a.side[0].heads, a.N), bk = norm_blocks(tokens, a.side[1].heads, a.N);
+    const int64_t tokens = a.Bsz * a.L, bq = norm_blocks(tokens, a.side[0].heads, a.N, bwd), bk = norm_blocks(tokens, a.side[1].heads, a.N, bwd);
     const int64_t most = a.side[0].heads > a.side[1].heads ? a.side[0].heads : a.side[1].heads;
     const int64_t tile = tile_tokens(most, a.pairs, LPR);
     const unsigned grid = (unsigned)(bq + bk);
@@ -258,7 +279,7 @@ template <typename T, int V, int LPR, int SPT> cudaError_t launch(const NormArgs
     }
     k_qknorm<T, V, LPR, SPT, true><<<grid, kThreads, 0, st>>>(a, tile, bq);
     if (a.side[0].dweight || a.side[1].dweight)
-        k_weights<<<dim3((unsigned)ceil_div(a.N, 32), 2), 256, 0, st>>>(a, bq, bq + bk);
+        k_weights<<<dim3((unsigned)ceil_div(a.N, 32), 2), 1024, 0, st>>>(a, bq, bq + bk);
     return cudaGetLastError();
 }
 
@@ -291,11 +312,12 @@ template <typename T> cudaError_t launch_io(const NormArgs& a, bool bwd, cudaStr
 
 }  // namespace
 
-// Blocks enough for eight on every SM, no more than there is work for (a block's least: 16
-// rows of 128 channels).
-int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N) {
-    const int64_t n = ceil_div(tokens * heads * N, 2048);
-    return n < 1 ? 1 : (n > 8 * kSms ? 8 * kSms : n);
+// No more blocks of a side than there is work for (a block's least: 16 rows of 128 channels), nor than eight an
+// SM; the backward's leave a part of the weights' gradients each, which one small kernel adds up, and two of them fit an
+// SM: two (2 x 4096 tokens, 16 + 16 heads of 128: that kernel takes PLACEHOLDER us, 20 with eight).
+int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N, bool backward) {
+    const int64_t n = ceil_div(tokens * heads * N, 2048), most = (backward ? 2 : 8) * kSms;
+    return n < 1 ? 1 : (n > most ? most : n);
 }
 
 cudaError_t launch_qknorm(const NormArgs& a, bool bwd, cudaStream_t st) {
