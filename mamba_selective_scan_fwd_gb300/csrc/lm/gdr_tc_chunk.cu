@@ -29,7 +29,10 @@ using la::unpack2;
 using la::wait_or_fail;
 
 constexpr int C = kChunk;
-constexpr int kThreads = 256;
+constexpr int kWorkers = 256, kThreads = kWorkers + 128;  // one thread of the last 128 loads and issues the products
+// Registers a thread: 168 at launch; the workers take what the others leave (2 x 216 + 72 of 3 x 168).
+__device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+__device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 
 template <int NB> struct ChunkSmem {
     // K and Q by turns; [X; dY] in high and low parts, two blocks of 64 columns each; U, high and low by turns; H or R,
@@ -39,6 +42,12 @@ template <int NB> struct ChunkSmem {
 };
 constexpr uint32_t cE = 0, cQK = 64, cT = 0, cZ = 128, cR = 256, cK = 384;
 
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint64_t* bar) {  // a warp's
+    la::tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) la::mbar_arrive(bar);
+}
 __device__ __forceinline__ float warp_max(float v) {
     uint32_t m;
     asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(__float_as_uint(v)));
@@ -79,7 +88,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     using L = ChunkSmem<NB>;
     constexpr int W = 32 * NB;  // states of a thread
     constexpr int EP = la::kF16<T> ? 2 : 1;  // parts of E and F in dq's and dk's products
-    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_c1, s_c2[2], s_c3, s_c4;
+    // landed: K and Q; an item's tiles; H or R.  Workers: dY is f16; E and F stand; H is copied; the item's tiles are read.
+    // Products: E; H's; R's; the pairs'
+    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_ready, s_ef, s_copied, s_read, s_c1, s_c2[2], s_c3, s_c4;
     __shared__ uint32_t s_tm, s_fail;
     __shared__ Two s_c[C];
     __shared__ __align__(16) float s_tail[C];
@@ -100,10 +111,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     const bool q_side = r >= C;
     const int tok = r & (C - 1);
     const int n0 = half * W;  // this thread's states
-    float acc[W];
-#pragma unroll
-    for (int n = 0; n < W; n++) acc[n] = 0.0f;
-    auto put_out = [&] {  // dq's or dk's row
+    auto put_out = [&](const float (&acc)[W]) {  // dq's or dk's row
         if (tok >= nt) return;
         const int64_t at = ((b * a.L + t0 + tok) * a.G + gq) * a.N + n0;
         const bool on = tok < nv;
@@ -129,7 +137,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             *reinterpret_cast<uint4*>(static_cast<T*>(w.dv) + ((b * a.L + t0 + row) * a.H + h) * a.P + p0 + 8 * u) = x;
     };
     if (nv == 0) {
-        put_out();
+        const float zero[W] = {};
+        if (tid < kWorkers) put_out(zero);
         for (int64_t h = h_lo; h < h_hi; h++) {
             for (int64_t p0 = 0; p0 < a.P; p0 += kTileP)
                 for (int i = tid; i < C * 16; i += kThreads) put_dv(h, p0, i >> 4, i & 15, make_uint4(0, 0, 0, 0));
@@ -145,6 +154,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + L::head);
     if (tid == 0) {
         for (uint64_t* bar : {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_ready, &s_ef, &s_copied, &s_read}) mbar_init(bar, kWorkers / 32);
         s_fail = 0;
         fence_proxy_async_smem();
     }
@@ -176,12 +186,90 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         }
         for (int n = 0; n < NB; n++) load_states(w.before, im, n);
     };
-    if (tid == 0) {
-        mbar_expect_tx(&s_key, NB * 16384);
-        bulk_load(KQ, w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384), NB * 16384, &s_key);
-        load(0);
-    }
-    __syncwarp();
+    if (warp >= kWorkers / 32) {
+        leave_regs();
+        if (tid == kWorkers) {
+            constexpr uint32_t kk = la::mma_desc<__half>(128, C, false, false), kr = la::mma_desc<__half>(128, C, false, true),
+                               rr = la::mma_desc<__half>(128, C, true, true);
+            const uint32_t keys_at = smem_addr(KQ), z_at = smem_addr(Z), zl_at = smem_addr(Zl), u_at = smem_addr(U), s_at = smem_addr(S), ef_at = smem_addr(EF);
+            mbar_expect_tx(&s_key, NB * 16384);
+            bulk_load(KQ, w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384), NB * 16384, &s_key);
+            load(0);
+            wait_or_fail(&s_key, 0, &s_fail);
+            for (int item = 0; item < items; item++) {
+                const uint32_t ph = item & 1;
+                if (!wait_or_fail(&s_in, ph, &s_fail) || !wait_or_fail(&s_ready, ph, &s_fail)) break;
+                la::tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < 4 * NB; s++) {
+                    const uint32_t x = keys_at + (s >> 2) * 16384 + (s & 3) * 32;
+                    la::mma(tm + cQK, la::smem_desc(x), la::smem_desc(x), kk, s > 0);
+                }
+#pragma unroll 1
+                for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
+#pragma unroll
+                    for (int s = 0; s < 8; s++) {
+                        const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
+                        la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + x), la::smem_desc(u_at + (o == 1 ? kTileBytes : 0) + x), kk, o > 0 || s > 0);
+                    }
+                la::mma_commit(&s_c1);
+#pragma unroll 1
+                for (int n = 0; n < NB; n++) {
+                    if (!wait_or_fail(&s_h[n], 0, &s_fail)) break;
+#pragma unroll 1
+                    for (int o = 0; o < 3; o++)
+#pragma unroll
+                        for (int s = 0; s < 8; s++) {
+                            const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
+                            la::mma(tm + cZ + 64 * n, la::smem_desc((o == 0 ? zl_at : z_at) + x),
+                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr, o > 0 || s > 0);
+                        }
+                    la::mma_commit(&s_c2[n]);
+                }
+                // R takes H's place
+                if (!wait_or_fail(&s_copied, ph, &s_fail)) break;
+#pragma unroll 1
+                for (int n = 0; n < NB; n++) {
+                    wait_or_fail(&s_c2[n], ph, &s_fail);
+                    load_states(w.after, image_of(item), n);
+                }
+                if (!wait_or_fail(&s_ef, ph, &s_fail)) break;
+                la::tc_fence_after();
+#pragma unroll 1
+                for (int n = 0; n < NB; n++)
+#pragma unroll 1
+                    for (int part = EP - 1; part >= 0; part--) {
+                        const uint32_t left = part ? zl_at : ef_at;
+#pragma unroll
+                        for (int s = 0; s < 4; s++)
+                            la::mma(tm + cK + 64 * n, la::smem_desc(left + s * 32), la::smem_desc(keys_at + n * 16384 + s * 2048), kr, part < EP - 1 || s > 0);
+#pragma unroll
+                        for (int s = 0; s < 8; s++)
+                            la::mma(tm + cT + 64 * n, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + n * 16384 + s * 2048), rr, part < EP - 1 || s > 0);
+                    }
+                la::mma_commit(&s_c4);
+#pragma unroll 1
+                for (int n = 0; n < NB; n++) {
+                    if (!wait_or_fail(&s_h[n], 1, &s_fail)) break;
+                    // rows 64 .. 127 of what starts at U's low part are other tiles: those lanes are not read
+#pragma unroll 1
+                    for (int o = 0; o < 3; o++)
+#pragma unroll
+                        for (int s = 0; s < 8; s++)
+                            la::mma(tm + cR + 64 * n, la::smem_desc(u_at + (o == 0 ? kTileBytes : 0) + (s >> 2) * 16384 + (s & 3) * 32),
+                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr, o > 0 || s > 0);
+                }
+                la::mma_commit(&s_c3);
+                if (item + 1 < items) {  // (E's and F's low part stands in Z's)
+                    if (!wait_or_fail(&s_read, ph, &s_fail) || !wait_or_fail(&s_c3, ph, &s_fail) || (EP > 1 && !wait_or_fail(&s_c4, ph, &s_fail))) break;
+                    load(item + 1);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+    take_regs();
+    float acc[W] = {};
     bool ok = true;
     for (int item = 0; item < items; item++) {
         const uint32_t ph = item & 1;
@@ -195,6 +283,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             }
             if (tid >= 64 && tid < 64 + C) s_a[tid - 64] = s_b[tid - 64] = s_db[tid - 64] = 0.0f;
             if (tid >= 128 && tid < 136) s_thr[tid - 128] = 0.0f;
+        }
+        uint4 vv[4];  // v, for x . v: unit (tid + 256 i) & 15 of row (tid + 256 i) >> 4
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int row = (tid + 256 * i) >> 4, u = tid & 15;
+            vv[i] = make_uint4(0, 0, 0, 0);
+            if (row < nv && p0 + 8 * u < a.P)
+                vv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + row) * a.v.token + h * a.P + p0 + 8 * u);
         }
         ok = wait_or_fail(&s_in, ph, &s_fail) && ok;
         // dY as f16: four units a thread of rows 64 .. 127 of Z's two blocks
@@ -216,7 +312,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             }
             most = warp_max(most);
             if (lane == 0) s_max[0][warp] = most;
-            __syncthreads();
+            workers_sync();
 #pragma unroll
             for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[0][i]);
             dy_scale = la::f16_scale(most);
@@ -233,49 +329,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             }
         }
         fence_proxy_async_smem();
-        __syncthreads();
-        constexpr uint32_t kk = la::mma_desc<__half>(128, C, false, false), kr = la::mma_desc<__half>(128, C, false, true),
-                           rr = la::mma_desc<__half>(128, C, true, true);
-        const uint32_t keys_at = smem_addr(KQ), z_at = smem_addr(Z), zl_at = smem_addr(Zl), u_at = smem_addr(U), s_at = smem_addr(S), ef_at = smem_addr(EF);
-        if (tid == 0) {
-            wait_or_fail(&s_key, 0, &s_fail);
-            la::tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < 4 * NB; s++) {
-                const uint32_t x = keys_at + (s >> 2) * 16384 + (s & 3) * 32;
-                la::mma(tm + cQK, la::smem_desc(x), la::smem_desc(x), kk, s > 0);
-            }
-#pragma unroll
-            for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
-#pragma unroll
-                for (int s = 0; s < 8; s++) {
-                    const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
-                    la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + x), la::smem_desc(u_at + (o == 1 ? kTileBytes : 0) + x), kk, o > 0 || s > 0);
-                }
-            la::mma_commit(&s_c1);
-            for (int n = 0; n < NB; n++) {
-                wait_or_fail(&s_h[n], 0, &s_fail);
-#pragma unroll
-                for (int o = 0; o < 3; o++)
-#pragma unroll
-                    for (int s = 0; s < 8; s++) {
-                        const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
-                        la::mma(tm + cZ + 64 * n, la::smem_desc((o == 0 ? zl_at : z_at) + x), la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr,
-                                o > 0 || s > 0);
-                    }
-                la::mma_commit(&s_c2[n]);
-            }
-        }
-        __syncwarp();
+        arrive(&s_ready);
         // dv, and x . v: 16 threads a row, two passes of columns' blocks
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const int at = tid + 256 * i, row = at >> 4, u = at & 15;
             const uint4 hi = *unit(Z + (u >> 3) * 16384, row, u & 7), lo = *unit(Zl + (u >> 3) * 16384, row, u & 7);
-            uint4 vv = make_uint4(0, 0, 0, 0);
-            if (row < nv && p0 + 8 * u < a.P)
-                vv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + row) * a.v.token + h * a.P + p0 + 8 * u);
-            const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {vv.x, vv.y, vv.z, vv.w};
+            const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {vv[i].x, vv[i].y, vv[i].z, vv[i].w};
             const float beta = head->beta[row];
             uint32_t out[4];
             float sum = 0.0f;
@@ -331,7 +391,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             s_col[warp][lane] = column_sums(k);
             most = warp_max(rho * most);
             if (lane == 0) s_max[1][warp] = most;
-            __syncthreads();
+            workers_sync();
 #pragma unroll
             for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[1][i]);
             ef_scale = la::f16_scale(most) * rho;
@@ -360,24 +420,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             s_b[tid] += col - (rows_q - head->beta[tid] * rows_k);
             s_db[tid] -= rows_k;
         }
-        la::tc_fence_before();
         fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            la::tc_fence_after();
-            for (int n = 0; n < NB; n++)
-                for (int part = EP - 1; part >= 0; part--) {
-                    const uint32_t left = part ? zl_at : ef_at;
-#pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        la::mma(tm + cK + 64 * n, la::smem_desc(left + s * 32), la::smem_desc(keys_at + n * 16384 + s * 2048), kr, part < EP - 1 || s > 0);
-#pragma unroll
-                    for (int s = 0; s < 8; s++)
-                        la::mma(tm + cT + 64 * n, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + n * 16384 + s * 2048), rr, part < EP - 1 || s > 0);
-                }
-            la::mma_commit(&s_c4);
-        }
-        __syncwarp();
+        arrive(&s_ef);
         // H's products; its tiles go to registers (for <R, H>) and make room for R's
         uint4 hs[NB][8];
 #pragma unroll
@@ -389,10 +433,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
         }
         la::tc_fence_after();
-        __syncthreads();
-        if (tid == 0)
-            for (int n = 0; n < NB; n++) load_states(w.after, im, n);
-        __syncwarp();
+        arrive(&s_copied);
         const float up = head->up[tok], down = head->down[tok];
         {
             const float f = before_inv * (q_side ? a.scale * up / dy_scale : -beta * up * x_inv);
@@ -409,21 +450,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             s_dot[0][half][r] = (q_side ? inv_q * f : inv_k * f) * dot;                        // a
             if (!q_side) s_dot[1][half][r] = -inv_k * before_inv * up * x_inv * dot;           // dbeta's share
         }
-        if (tid == 0) {
-            for (int n = 0; n < NB; n++) {
-                wait_or_fail(&s_h[n], 1, &s_fail);
-                la::tc_fence_after();
-                // rows 64 .. 127 of what starts at U's low part are other tiles: those lanes are not read
-#pragma unroll
-                for (int o = 0; o < 3; o++)
-#pragma unroll
-                    for (int s = 0; s < 8; s++)
-                        la::mma(tm + cR + 64 * n, la::smem_desc(u_at + (o == 0 ? kTileBytes : 0) + (s >> 2) * 16384 + (s & 3) * 32),
-                                la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr, o > 0 || s > 0);
-            }
-            la::mma_commit(&s_c3);
-        }
-        __syncwarp();
         if (w.dg) {
             float through = 0.0f;
 #pragma unroll
@@ -446,6 +472,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             through = lane_sum<32>(through);
             if (lane == 0) s_thr[warp] += through * (before_inv * after_inv);
         }
+        arrive(&s_read);  // (R's products are waited for where the next tiles are loaded)
         ok = wait_or_fail(&s_c3, ph, &s_fail) && ok;
         ok = wait_or_fail(&s_c4, ph, &s_fail) && ok;
         la::tc_fence_after();
@@ -472,17 +499,15 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             }
             if (!q_side) s_dot[2][half][r] = inv_k * fr * dot;  // b
         }
-        la::tc_fence_before();
-        __syncthreads();  // all of the item's tiles and products are read
+        workers_sync();
         if (EP > 1)  // dY has no low part
-            for (int i = tid; i < C * 8; i += kThreads) *reinterpret_cast<uint4*>(Zl + kTileBytes + i * 16) = make_uint4(0, 0, 0, 0);
-        if (tid == 0 && item + 1 < items) load(item + 1);
+            for (int i = tid; i < C * 8; i += kWorkers) *reinterpret_cast<uint4*>(Zl + kTileBytes + i * 16) = make_uint4(0, 0, 0, 0);
         if (tid < C) {
             s_a[tid] += (s_dot[0][0][tid] + s_dot[0][1][tid]) + (s_dot[0][0][64 + tid] + s_dot[0][1][64 + tid]);
             s_b[tid] += s_dot[2][0][tid] + s_dot[2][1][tid];
             s_db[tid] += s_dot[1][0][tid] + s_dot[1][1][tid];
         }
-        __syncthreads();
+        workers_sync();
         if (pt == ptiles - 1 && warp == 0) {
             float sum = 0.0f;
 #pragma unroll
@@ -509,9 +534,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                     w.dbeta[at] = t + e < nv ? s_db[t + e] : 0.0f;
                 }
         }
-        __syncthreads();
+        workers_sync();
     }
-    if (ok) put_out();
+    if (ok) put_out(acc);
+    }
     uint64_t* const bars[9] = {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4};
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
