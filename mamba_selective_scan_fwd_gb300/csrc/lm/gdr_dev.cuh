@@ -45,5 +45,33 @@ __device__ __forceinline__ Pair chunk_decays(const Args& a, int64_t b, int64_t t
     return p;
 }
 
+// x[j] *= f e^{c_i - c_{j0 + j}} for columns up to `last`, 0 beyond: by runs of 16 with one exponential each where `flat` allows it
+// (a factor beyond `last` may overflow: it is not used), else an exponential each.
+template <int N>
+__device__ __forceinline__ void pair_factors(float (&x)[N], const la::Two* c, const float* tail, bool flat, int j0, la::Two ci, float f, int last) {
+    if (flat) {
+#pragma unroll
+        for (int r = 0; r < N; r += 16) {
+            const float2 by = splat2(f * ex2a(la::two_diff(ci, c[j0 + r + 15])));
+#pragma unroll
+            for (int j = r; j < r + 16; j += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(tail + j0 + j);
+                const float2 u = mul2(make_float2(x[j], x[j + 1]), mul2(by, make_float2(t.x, t.y)));
+                const float2 v = mul2(make_float2(x[j + 2], x[j + 3]), mul2(by, make_float2(t.z, t.w)));
+                x[j] = j0 + j <= last ? u.x : 0.0f;
+                x[j + 1] = j0 + j + 1 <= last ? u.y : 0.0f;
+                x[j + 2] = j0 + j + 2 <= last ? v.x : 0.0f;
+                x[j + 3] = j0 + j + 3 <= last ? v.y : 0.0f;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const float e = f * ex2a(la::two_diff(ci, c[j0 + j])) * x[j];
+            x[j] = j0 + j <= last ? e : 0.0f;
+        }
+    }
+}
+
 }  // namespace gdr
 }  // namespace ss

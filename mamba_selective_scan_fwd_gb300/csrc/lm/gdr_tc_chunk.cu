@@ -349,6 +349,16 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             sum = lane_sum<16>(sum);
             if ((lane & 15) == 0) s_db[row] += sum;
         }
+        // H's tiles go to registers, for <R, H>, and make room for R's
+        uint4 hs[NB][8];
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            ok = wait_or_fail(&s_h[n], 0, &s_fail) && ok;
+            if (w.dg)
+#pragma unroll
+                for (int i = 0; i < 8; i++) hs[n][i] = *reinterpret_cast<const uint4*>(S + n * 32768 + (tid + 256 * i) * 16);
+        }
+        arrive(&s_copied);
         ok = wait_or_fail(&s_c1, ph, &s_fail) && ok;
         la::tc_fence_after();
         const float inv_k = head->inv_k, inv_q = head->inv_q, beta = head->beta[tok], rho = q_side ? inv_q / inv_k : 1.0f;
@@ -360,22 +370,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             const Two ci = s_c[tok];
             const float f = u_inv * (q_side ? a.scale / dy_scale : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
             const int last = q_side ? tok : tok - 1;
-#pragma unroll
-            for (int c0 = 0; c0 < 32; c0 += 16) {
-                const int col0 = 32 * half + c0;
-                if (col0 <= (tok | 15) && (s_flat || col0 + 16 <= (tok & ~15))) {
-                    const float by = f * ex2a(two_diff(ci, s_c[col0 + 15]));
-#pragma unroll
-                    for (int j = 0; j < 16; j++) e[c0 + j] = col0 + j <= last ? e[c0 + j] * (by * s_tail[col0 + j]) : 0.0f;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        float x = 0.0f;
-                        if (col0 + j <= last) x = f * ex2a(two_diff(ci, s_c[col0 + j])) * e[c0 + j];
-                        e[c0 + j] = x;
-                    }
-                }
-            }
+            pair_factors(e, s_c, s_tail, s_flat, 32 * half, ci, f, last);
             // of a key's row: e^{c_i - c_j} x_i . u_j so far
             float row = 0.0f, most = 0.0f;
             const float sign = q_side ? 1.0f : -beta;
@@ -422,18 +417,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         }
         fence_proxy_async_smem();
         arrive(&s_ef);
-        // H's products; its tiles go to registers (for <R, H>) and make room for R's
-        uint4 hs[NB][8];
+        // H's products
 #pragma unroll
-        for (int n = 0; n < NB; n++) {
-            ok = wait_or_fail(&s_h[n], 0, &s_fail) && ok;
-            if (w.dg)
-#pragma unroll
-                for (int i = 0; i < 8; i++) hs[n][i] = *reinterpret_cast<const uint4*>(S + n * 32768 + (tid + 256 * i) * 16);
-            ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
-        }
+        for (int n = 0; n < NB; n++) ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
         la::tc_fence_after();
-        arrive(&s_copied);
         const float up = head->up[tok], down = head->down[tok];
         {
             const float f = before_inv * (q_side ? a.scale * up / dy_scale : -beta * up * x_inv);

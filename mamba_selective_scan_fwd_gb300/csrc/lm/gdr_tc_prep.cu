@@ -253,8 +253,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
         for (int64_t h = h0; h < min(h_hi, h0 + kHeads); h++) {
             const int hl = (int)(h - h0);
             if (__syncthreads_or(!ok)) break;  // (and: the last head's image has left, s_max is free)
-            // thread: row i of K K^T (warps 0, 1) or Q K^T.  A run of 16 columns takes e^{c_i - c_e} e^{c_e - c_j} with e
-            // its end; the row's own, where that could leave f32's range, an exponential each.
+            // thread: row i of K K^T (warps 0, 1) or Q K^T
             const bool is_q = tid >= C;
             const int i = tid & 63, last = is_q ? i : i - 1;
             float s[C];
@@ -262,29 +261,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
             la::tmem_ld32(tm + my + 32, *reinterpret_cast<float(*)[32]>(s + 32));
             const Two ci = s_c[hl][i];
             const float f = is_q ? 1.0f : s_beta[hl][i];
-#pragma unroll
-            for (int c0 = 0; c0 < C; c0 += 16) {
-                if (c0 <= (i | 15) && (s_flat[hl] || c0 + 16 <= (i & ~15))) {
-                    const float by = f * ex2a(two_diff(ci, s_c[hl][c0 + 15]));
-#pragma unroll
-                    for (int j = c0; j < c0 + 16; j += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(&s_tail[hl][j]);
-                        const float2 x = mul2(make_float2(s[j], s[j + 1]), mul2(splat2(by), make_float2(t.x, t.y)));
-                        const float2 y = mul2(make_float2(s[j + 2], s[j + 3]), mul2(splat2(by), make_float2(t.z, t.w)));
-                        s[j] = j <= last ? x.x : 0.0f;
-                        s[j + 1] = j + 1 <= last ? x.y : 0.0f;
-                        s[j + 2] = j + 2 <= last ? y.x : 0.0f;
-                        s[j + 3] = j + 3 <= last ? y.y : 0.0f;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = c0; j < c0 + 16; j++) {
-                        float x = 0.0f;
-                        if (j <= last) x = f * ex2a(two_diff(ci, s_c[hl][j])) * s[j];
-                        s[j] = x;
-                    }
-                }
-            }
+            pair_factors(s, s_c[hl], s_tail[hl], s_flat[hl], 0, ci, f, last);
             if (i >= nv)  // (whatever the row holds)
 #pragma unroll
                 for (int j = 0; j < C; j++) s[j] = 0.0f;
