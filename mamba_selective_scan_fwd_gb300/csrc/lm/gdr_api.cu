@@ -174,7 +174,7 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
 struct BwdTc {
     int64_t chunks;
     int splits;
-    size_t keys, images, before, after, us, xs, before_inv, after_inv, u_inv, x_inv, dq, dk;
+    size_t keys, images, before, after, us, xs, dys, before_inv, after_inv, u_inv, x_inv, dy_inv, dq, dk;
 };
 BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     BwdTc f;
@@ -187,7 +187,8 @@ BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     f.after = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
     f.us = l.take(tiles * kRowsBytes);
     f.xs = l.take(tiles * kRowsBytes);
-    for (size_t* x : {&f.before_inv, &f.after_inv, &f.u_inv, &f.x_inv}) *x = l.take(tiles * 4);
+    f.dys = l.take(tiles * kPieceBytes);
+    for (size_t* x : {&f.before_inv, &f.after_inv, &f.u_inv, &f.x_inv, &f.dy_inv}) *x = l.take(tiles * 4);
     const size_t part = f.splits > 1 ? (size_t)f.splits * Bsz * L * G * N * 4 : 0;
     f.dq = l.take(part);
     f.dk = l.take(part);
@@ -211,7 +212,7 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     TcBackArgs r = {};
     TcChunkArgs c = {};
     if (!tc_map(encode, &p.q, a.q, a.G, a.N, a.L, a.Bsz, a.dtype) || !tc_map(encode, &p.k, a.k, a.G, a.N, a.L, a.Bsz, a.dtype) ||
-        !tc_map(encode, &w.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype) || !tc_map(encode, &r.dy, a.dy, a.H, a.P, a.L, a.Bsz, a.dtype))
+        !tc_map(encode, &w.v, a.v, a.H, a.P, a.L, a.Bsz, a.dtype))
         return SS_OK;
     const int rc = device_status_word(&w.status);
     if (rc != SS_OK) return rc;
@@ -238,7 +239,8 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     r.xs = ws + f.xs;
     r.state_inv = f32(f.after_inv);
     r.x_inv = f32(f.x_inv);
-    c.dy = r.dy;
+    r.dys = ws + f.dys;
+    r.dy_inv = f32(f.dy_inv);
     c.a = a;
     c.chunks = f.chunks;
     c.splits = f.splits;
@@ -248,10 +250,12 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     c.after = r.states;
     c.us = w.us;
     c.xs = r.xs;
+    c.dys = r.dys;
     c.before_inv = w.state_inv;
     c.after_inv = r.state_inv;
     c.u_inv = w.u_inv;
     c.x_inv = r.x_inv;
+    c.dy_inv = r.dy_inv;
     c.dq = d.dq;
     c.dk = d.dk;
     c.dv = d.dv;
@@ -260,7 +264,7 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     c.dg = d.dg;
     c.dbeta = d.dbeta;
     c.status = w.status;
-    if (launch_prep(p, 2, st) != cudaSuccess || launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_prep(p, 2, st) != cudaSuccess || launch_dy(a, f.chunks, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess || launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
     if (f.splits > 1 &&
         la::launch_sum_parts(c.dq_part, d.dq, c.dk_part, d.dk, f.splits, a.Bsz * a.L * a.G * a.N, a.dtype, st) != cudaSuccess)
         return SS_ERR_CUDA;

@@ -54,6 +54,12 @@ struct PrepArgs {
 };
 cudaError_t launch_prep(const PrepArgs& w, int parts, cudaStream_t st);
 
+// f16 images as the walks hold them, transposed: pieces of 128 value channels p by 64, one scale each image.  The
+// state (or its adjoint): [part][64 states n][p][64].  U and X: [part][p][64 tokens].  dY: [p][64 tokens], exact.
+constexpr int kPieceBytes = 2 * kTileBytes;
+__host__ __device__ constexpr int state_bytes(int nb) { return 2 * nb * kPieceBytes; }
+constexpr int kRowsBytes = 2 * kPieceBytes;
+
 // How the walks over time are cut: K segments of seg chunks.  All but the last are first walked
 // for what they do to a state: from zero (E), and without v from the identity (Phi), so that
 // S -> Phi S + E.
@@ -79,29 +85,26 @@ struct TcWalkArgs {
 // The backward's walk over the chunks from the last: x and, as images like the forward's, the state's
 // adjoint after each chunk and X.
 struct TcBackArgs {
-    CUtensorMap dy;
+    const char* dys;    // images of dY
+    const float* dy_inv;
     const float* init;  // gradient of the last state, or null
     float* last;        // dh0, or null
     char *states, *xs;
     float *state_inv, *x_inv;
 };
+cudaError_t launch_dy(const Args& a, int64_t chunks, char* dys, float* dy_inv, cudaStream_t st);
 // What is left of the backward, one chunk at a time.
 struct TcChunkArgs {
-    CUtensorMap dy;
     Args a;
     int64_t chunks;
     int splits;         // parts a group's heads are divided into
-    const char *keys, *images, *before, *after, *us, *xs;
-    const float *before_inv, *after_inv, *u_inv, *x_inv;
+    const char *keys, *images, *before, *after, *us, *xs, *dys;
+    const float *before_inv, *after_inv, *u_inv, *x_inv, *dy_inv;
     void *dq, *dk, *dv;
     float *dq_part, *dk_part;  // [splits, Bsz, L, G, N], with splits > 1
     float *dg, *dbeta;
     int* status;
 };
-// f16 images in two parts, one scale each: the state transposed, [part][64 columns n][128 rows p][64], and U, [part][64
-// columns p][64 rows t][64].
-__host__ __device__ constexpr int state_bytes(int nb) { return 2 * nb * 2 * kTileBytes; }
-constexpr int kRowsBytes = 4 * kTileBytes;
 // kTcY: y and the last state.  kTcSum: what each segment does to a state.  kTcKeep: for the backward, the
 // state before each chunk and U, as operand images.
 enum TcWalkMode { kTcY, kTcSum, kTcKeep };

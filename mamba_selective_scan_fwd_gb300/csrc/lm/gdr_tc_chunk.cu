@@ -35,8 +35,8 @@ __device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.
 __device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 
 template <int NB> struct ChunkSmem {
-    // K and Q by turns; [X; dY] in high and low parts, two blocks of 64 columns each; U, high and low by turns; H or R,
-    // for each 64 states high and low; [F; E]
+    // K and Q by turns; X and dY (high parts); X's low part and zeros (dY has none); U, high and low; H or R, for each 64
+    // states high and low; [F; E]
     static constexpr int keys = 0, z = NB * 16384, zl = z + 32768, u = zl + 32768, s = u + 32768, ef = s + NB * 32768, head = ef + 16384,
                          total = head + 2048;
 };
@@ -88,14 +88,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     using L = ChunkSmem<NB>;
     constexpr int W = 32 * NB;  // states of a thread
     constexpr int EP = la::kF16<T> ? 2 : 1;  // parts of E and F in dq's and dk's products
-    // landed: K and Q; an item's tiles; H or R.  Workers: dY is f16; E and F stand; H is copied; the item's tiles are read.
+    // landed: K and Q; an item's tiles; H or R.  Workers: E and F stand; H is copied; the item's tiles are read, its products.
     // Products: E; H's; R's; the pairs'
-    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_ready, s_ef, s_copied, s_read, s_c1, s_c2[2], s_c3, s_c4;
+    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_ef, s_copied, s_read, s_done, s_c1, s_c2[2], s_c3, s_c4;
     __shared__ uint32_t s_tm, s_fail;
     __shared__ Two s_c[C];
     __shared__ __align__(16) float s_tail[C];
     __shared__ bool s_flat;
-    __shared__ float s_max[2][8], s_row[2][128], s_col[8][32], s_dot[3][2][128], s_a[C], s_b[C], s_db[C], s_thr[8];
+    __shared__ float s_max[8], s_xv[4][C], s_row[2][128], s_col[8][32], s_dot[3][2][128], s_a[C], s_b[C], s_db[C], s_thr[8];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = tid & 127, half = tid >> 7;
     int64_t id = blockIdx.x;
@@ -154,13 +154,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + L::head);
     if (tid == 0) {
         for (uint64_t* bar : {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&s_ready, &s_ef, &s_copied, &s_read}) mbar_init(bar, kWorkers / 32);
+        for (uint64_t* bar : {&s_ef, &s_copied, &s_read, &s_done}) mbar_init(bar, kWorkers / 32);
         s_fail = 0;
         fence_proxy_async_smem();
     }
     if (warp == 0) la::tmem_alloc(&s_tm, 512);
-    for (int i = tid; i < 2 * C * 8; i += kThreads)  // dY has no low part
-        *reinterpret_cast<uint4*>(Zl + (i >> 9) * 16384 + kTileBytes + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kPieceBytes / 16; i += kThreads) *reinterpret_cast<uint4*>(Zl + kPieceBytes + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
     __syncthreads();
     la::tc_fence_after();
     const uint32_t tm = s_tm, my = (uint32_t)(tid & 96) << 16;
@@ -173,17 +173,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             bulk_load(S + n * 32768 + part * 16384, images + im * state_bytes(NB) + (part * NB + n) * 16384, 16384, &s_h[n]);
     };
     auto load = [&](int item) {
-        const int64_t h = h_lo + item / ptiles, p0 = item % ptiles * kTileP, im = image_of(item);
-        mbar_expect_tx(&s_in, 10 * kTileBytes + (int)sizeof(ImageHead));
+        const int64_t h = h_lo + item / ptiles, im = image_of(item);
+        mbar_expect_tx(&s_in, 2 * kRowsBytes + kPieceBytes + (int)sizeof(ImageHead));
         bulk_load(sm + L::head, w.images + ((b * a.H + h) * w.chunks + chunk) * image_bytes(2) + 4 * kTileBytes, (int)sizeof(ImageHead), &s_in);
-#pragma unroll
-        for (int p = 0; p < 2; p++) {
-            la::tma_load_4d(Z + p * 16384 + kTileBytes, &w.dy, (int)p0 + 64 * p, (int)h, (int)t0, (int)b, &s_in);
-            bulk_load(Z + p * 16384, w.xs + im * kRowsBytes + p * kTileBytes, kTileBytes, &s_in);
-            bulk_load(Zl + p * 16384, w.xs + im * kRowsBytes + (2 + p) * kTileBytes, kTileBytes, &s_in);
-            bulk_load(U + p * 16384, w.us + im * kRowsBytes + p * kTileBytes, kTileBytes, &s_in);
-            bulk_load(U + p * 16384 + kTileBytes, w.us + im * kRowsBytes + (2 + p) * kTileBytes, kTileBytes, &s_in);
-        }
+        bulk_load(Z, w.xs + im * kRowsBytes, kPieceBytes, &s_in);
+        bulk_load(Zl, w.xs + im * kRowsBytes + kPieceBytes, kPieceBytes, &s_in);
+        bulk_load(Z + kPieceBytes, w.dys + im * kPieceBytes, kPieceBytes, &s_in);
+        bulk_load(U, w.us + im * kRowsBytes, kRowsBytes, &s_in);
         for (int n = 0; n < NB; n++) load_states(w.before, im, n);
     };
     if (warp >= kWorkers / 32) {
@@ -198,7 +194,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             wait_or_fail(&s_key, 0, &s_fail);
             for (int item = 0; item < items; item++) {
                 const uint32_t ph = item & 1;
-                if (!wait_or_fail(&s_in, ph, &s_fail) || !wait_or_fail(&s_ready, ph, &s_fail)) break;
+                if (!wait_or_fail(&s_in, ph, &s_fail) || (item > 0 && !wait_or_fail(&s_done, ph ^ 1, &s_fail))) break;
                 la::tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < 4 * NB; s++) {
@@ -208,10 +204,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
 #pragma unroll 1
                 for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
-                    for (int s = 0; s < 8; s++) {
-                        const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
-                        la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + x), la::smem_desc(u_at + (o == 1 ? kTileBytes : 0) + x), kk, o > 0 || s > 0);
-                    }
+                    for (int s = 0; s < 8; s++)
+                        la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes), la::smem_desc(u_at + (o == 1 ? kPieceBytes : 0) + s * 2048), rr,
+                                o > 0 || s > 0);
                 la::mma_commit(&s_c1);
 #pragma unroll 1
                 for (int n = 0; n < NB; n++) {
@@ -219,11 +214,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
 #pragma unroll 1
                     for (int o = 0; o < 3; o++)
 #pragma unroll
-                        for (int s = 0; s < 8; s++) {
-                            const uint32_t x = (s >> 2) * 16384 + (s & 3) * 32;
-                            la::mma(tm + cZ + 64 * n, la::smem_desc((o == 0 ? zl_at : z_at) + x),
-                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr, o > 0 || s > 0);
-                        }
+                        for (int s = 0; s < 8; s++)
+                            la::mma(tm + cZ + 64 * n, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes),
+                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? kPieceBytes : 0) + s * 2048), rr, o > 0 || s > 0);
                     la::mma_commit(&s_c2[n]);
                 }
                 // R takes H's place
@@ -251,13 +244,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
 #pragma unroll 1
                 for (int n = 0; n < NB; n++) {
                     if (!wait_or_fail(&s_h[n], 1, &s_fail)) break;
-                    // rows 64 .. 127 of what starts at U's low part are other tiles: those lanes are not read
+                    // (the 64 tokens twice)
 #pragma unroll 1
                     for (int o = 0; o < 3; o++)
 #pragma unroll
                         for (int s = 0; s < 8; s++)
-                            la::mma(tm + cR + 64 * n, la::smem_desc(u_at + (o == 0 ? kTileBytes : 0) + (s >> 2) * 16384 + (s & 3) * 32),
-                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? 16384 : 0) + s * 2048), kr, o > 0 || s > 0);
+                            la::mma(tm + cR + 64 * n, la::smem_desc(u_at + (o == 0 ? kPieceBytes : 0) + s * 2048, 0),
+                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? kPieceBytes : 0) + s * 2048), rr, o > 0 || s > 0);
                 }
                 la::mma_commit(&s_c3);
                 if (item + 1 < items) {  // (E's and F's low part stands in Z's)
@@ -274,7 +267,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     for (int item = 0; item < items; item++) {
         const uint32_t ph = item & 1;
         const int64_t h = h_lo + item / ptiles, pt = item % ptiles, p0 = pt * kTileP, im = image_of(item);
-        const float x_inv = w.x_inv[im], u_inv = w.u_inv[im], before_inv = w.before_inv[im], after_inv = w.after_inv[im];
+        const float x_inv = w.x_inv[im], dy_inv = w.dy_inv[im], u_inv = w.u_inv[im], before_inv = w.before_inv[im], after_inv = w.after_inv[im];
         if (pt == 0) {
             if (warp == 0) {
                 bool flat;
@@ -284,70 +277,39 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             if (tid >= 64 && tid < 64 + C) s_a[tid - 64] = s_b[tid - 64] = s_db[tid - 64] = 0.0f;
             if (tid >= 128 && tid < 136) s_thr[tid - 128] = 0.0f;
         }
-        uint4 vv[4];  // v, for x . v: unit (tid + 256 i) & 15 of row (tid + 256 i) >> 4
+        // dv, and x . v: token tid & 63, a quarter of the channels
+        const int vt = tid & (C - 1), vp = (tid >> 6) * 32;
+        uint4 vv[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int row = (tid + 256 * i) >> 4, u = tid & 15;
-            vv[i] = make_uint4(0, 0, 0, 0);
-            if (row < nv && p0 + 8 * u < a.P)
-                vv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + row) * a.v.token + h * a.P + p0 + 8 * u);
+        for (int u = 0; u < 4; u++) {
+            vv[u] = make_uint4(0, 0, 0, 0);
+            if (vt < nv && p0 + vp + 8 * u < a.P)
+                vv[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + vt) * a.v.token + h * a.P + p0 + vp + 8 * u);
         }
         ok = wait_or_fail(&s_in, ph, &s_fail) && ok;
-        // dY as f16: four units a thread of rows 64 .. 127 of Z's two blocks
-        float dy_scale = 1.0f;
         {
-            uint4 x[4];
-            float most = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int at = tid + 256 * (i & 1);
-                x[i] = *reinterpret_cast<const uint4*>(Z + (i >> 1) * 16384 + kTileBytes + at * 16);
-                if (at >> 3 >= nv) x[i] = make_uint4(0, 0, 0, 0);
-                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float2 f = unpack2<T>(v[e]);
-                    most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-            }
-            most = warp_max(most);
-            if (lane == 0) s_max[0][warp] = most;
-            workers_sync();
-#pragma unroll
-            for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[0][i]);
-            dy_scale = la::f16_scale(most);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t y[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float2 f = mul2(unpack2<T>(v[e]), splat2(dy_scale));
-                    y[e] = pack2<__half>(f.x, f.y);
-                }
-                *reinterpret_cast<uint4*>(Z + (i >> 1) * 16384 + kTileBytes + (tid + 256 * (i & 1)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-        }
-        fence_proxy_async_smem();
-        arrive(&s_ready);
-        // dv, and x . v: 16 threads a row, two passes of columns' blocks
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int at = tid + 256 * i, row = at >> 4, u = at & 15;
-            const uint4 hi = *unit(Z + (u >> 3) * 16384, row, u & 7), lo = *unit(Zl + (u >> 3) * 16384, row, u & 7);
-            const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {vv[i].x, vv[i].y, vv[i].z, vv[i].w};
-            const float beta = head->beta[row];
-            uint32_t out[4];
+            const float beta = head->beta[vt];
             float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float2 f = mul2(splat2(x_inv), add2(unpack2<__half>(x[e]), unpack2<__half>(y[e]))), g = unpack2<T>(v[e]);
-                sum = fmaf(f.x, g.x, fmaf(f.y, g.y, sum));
-                out[e] = row < nv ? pack2<T>(beta * f.x, beta * f.y) : 0;
+            for (int u = 0; u < 4; u++) {
+                const uint32_t v[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w};
+                uint32_t out[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    float f[2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int p = vp + 8 * u + 2 * e + i;
+                        const int at = p * 128 + (((vt >> 3) ^ (p & 7)) << 4) + (vt & 7) * 2;
+                        f[i] = x_inv * (__half2float(*reinterpret_cast<const __half*>(Z + at)) + __half2float(*reinterpret_cast<const __half*>(Zl + at)));
+                    }
+                    const float2 g = unpack2<T>(v[e]);
+                    sum = fmaf(f[0], g.x, fmaf(f[1], g.y, sum));
+                    out[e] = vt < nv ? pack2<T>(beta * f[0], beta * f[1]) : 0;
+                }
+                put_dv(h, p0, vt, vp / 8 + u, make_uint4(out[0], out[1], out[2], out[3]));
             }
-            put_dv(h, p0, row, u, make_uint4(out[0], out[1], out[2], out[3]));
-            sum = lane_sum<16>(sum);
-            if ((lane & 15) == 0) s_db[row] += sum;
+            s_xv[tid >> 6][vt] = sum;
         }
         // H's tiles go to registers, for <R, H>, and make room for R's
         uint4 hs[NB][8];
@@ -368,7 +330,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             la::tmem_ld32(tm + my + cE + 32 * half, e);
             la::tmem_ld32(tm + my + cQK + 32 * half, k);
             const Two ci = s_c[tok];
-            const float f = u_inv * (q_side ? a.scale / dy_scale : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
+            const float f = u_inv * (q_side ? a.scale * dy_inv : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
             const int last = q_side ? tok : tok - 1;
             pair_factors(e, s_c, s_tail, s_flat, 32 * half, ci, f, last);
             // of a key's row: e^{c_i - c_j} x_i . u_j so far
@@ -385,10 +347,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             s_row[half][r] = row;  // (without the sign: dbeta takes a key's as it is)
             s_col[warp][lane] = column_sums(k);
             most = warp_max(rho * most);
-            if (lane == 0) s_max[1][warp] = most;
+            if (lane == 0) s_max[warp] = most;
             workers_sync();
 #pragma unroll
-            for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[1][i]);
+            for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[i]);
             ef_scale = la::f16_scale(most) * rho;
             if (EP > 1) {  // the low part takes Z's, which H's product is done with
                 for (int n = 0; n < NB; n++) ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
@@ -413,7 +375,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
 #pragma unroll
             for (int i = 0; i < 4; i++) col += s_col[(tid >> 5) * 4 + i][tid & 31];
             s_b[tid] += col - (rows_q - head->beta[tid] * rows_k);
-            s_db[tid] -= rows_k;
+            s_db[tid] += ((s_xv[0][tid] + s_xv[1][tid]) + (s_xv[2][tid] + s_xv[3][tid])) - rows_k;
         }
         fence_proxy_async_smem();
         arrive(&s_ef);
@@ -423,7 +385,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         la::tc_fence_after();
         const float up = head->up[tok], down = head->down[tok];
         {
-            const float f = before_inv * (q_side ? a.scale * up / dy_scale : -beta * up * x_inv);
+            const float f = before_inv * (q_side ? a.scale * up * dy_inv : -beta * up * x_inv);
             float dot = 0.0f;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
@@ -486,9 +448,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             }
             if (!q_side) s_dot[2][half][r] = inv_k * fr * dot;  // b
         }
+        arrive(&s_done);
         workers_sync();
-        if (EP > 1)  // dY has no low part
-            for (int i = tid; i < C * 8; i += kWorkers) *reinterpret_cast<uint4*>(Zl + kTileBytes + i * 16) = make_uint4(0, 0, 0, 0);
         if (tid < C) {
             s_a[tid] += (s_dot[0][0][tid] + s_dot[0][1][tid]) + (s_dot[0][0][64 + tid] + s_dot[0][1][64 + tid]);
             s_b[tid] += s_dot[2][0][tid] + s_dot[2][1][tid];

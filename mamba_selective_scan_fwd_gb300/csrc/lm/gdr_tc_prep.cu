@@ -335,6 +335,54 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     la::end_block(&s_fail, w.status, bars, tm, 64);
 }
 
+// dY's image: 64 tokens of 128 value channels of one head, transposed, f16 under the scale of its largest value; tokens past
+// the row's length zero.  Bound by HBM (2 x 4096 tokens, 32 heads of 128: PLACEHOLDER us, copying 20).
+template <typename T> __global__ void __launch_bounds__(256) k_dy(Args a, int64_t chunks, char* dys, float* dy_inv) {
+    constexpr int LD = 132;  // (a row's 16-byte units spread over the banks)
+    __shared__ __align__(16) T s[C][LD];
+    __shared__ float s_max[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t ptiles = (a.P + 127) / 128;
+    int64_t id = blockIdx.x;
+    const int64_t chunk = id % chunks;
+    id /= chunks;
+    const int64_t p0 = id % ptiles * 128, bh = id / ptiles, b = bh / a.H, h = bh % a.H, t0 = chunk * C;
+    const int nv = (int)max((int64_t)0, min((int64_t)C, row_length(a, b) - t0));
+    if (nv == 0) return;
+    const T* from = static_cast<const T*>(a.dy.p) + b * a.dy.batch + t0 * a.dy.token + h * a.P + p0;
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int t = (tid + 256 * i) >> 4, u = tid & 15;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t < nv && p0 + 8 * u < a.P) x = *reinterpret_cast<const uint4*>(from + t * a.dy.token + 8 * u);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float2 f = unpack2<T>(v[e]);
+            most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        *reinterpret_cast<uint2*>(&s[t][8 * u]) = make_uint2(x.x, x.y);
+        *reinterpret_cast<uint2*>(&s[t][8 * u + 4]) = make_uint2(x.z, x.w);
+    }
+    most = warp_max(most);
+    if (lane == 0) s_max[warp] = most;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[i]);
+    const float scale = la::f16_scale(most);
+    char* to = dys + (int64_t)blockIdx.x * kPieceBytes;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int at = tid + 256 * i, p = at >> 3, u = (at & 7) ^ (p & 7);
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = pack2<__half>(scale * ldf(&s[8 * u + 2 * e][p]), scale * ldf(&s[8 * u + 2 * e + 1][p]));
+        *reinterpret_cast<uint4*>(to + at * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    if (tid == 0) dy_inv[blockIdx.x] = 1.0f / scale;
+}
+
 template <typename T, int NB, int PARTS> cudaError_t prep_go(const PrepArgs& w, cudaStream_t st) {
     constexpr int bytes = PrepSmem<NB, PARTS>::total;
     const cudaError_t e = la::allow_smem<k_prep<T, NB, PARTS>>(bytes);
@@ -347,6 +395,13 @@ template <typename T, int NB> cudaError_t prep_parts(const PrepArgs& w, int part
 }
 
 }  // namespace
+
+cudaError_t launch_dy(const Args& a, int64_t chunks, char* dys, float* dy_inv, cudaStream_t st) {
+    const unsigned grid = (unsigned)(a.Bsz * a.H * ceil_div(a.P, kTileP) * chunks);
+    if (a.dtype == 1) k_dy<__half><<<grid, 256, 0, st>>>(a, chunks, dys, dy_inv);
+    else k_dy<bf16><<<grid, 256, 0, st>>>(a, chunks, dys, dy_inv);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_prep(const PrepArgs& w, int parts, cudaStream_t st) {
     if (w.a.dtype == 1) return w.a.N <= 64 ? prep_parts<__half, 1>(w, parts, st) : prep_parts<__half, 2>(w, parts, st);

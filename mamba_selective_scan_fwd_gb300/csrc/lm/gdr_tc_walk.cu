@@ -102,6 +102,35 @@ __device__ __forceinline__ float group_min(float v, uint32_t* red, int id) {
     return __uint_as_float(m);
 }
 
+// The images' pieces leave through a ring of places in shared memory, one warpgroup writing a row of 128 bytes a
+// thread: 32 columns of tensor memory (or registers) of pairs of f16, times a power of two.
+constexpr int kRing = 3;
+struct Ring {
+    char* place;
+    int next;
+    __device__ __forceinline__ void put(const uint32_t (&x)[32], uint32_t f, char* to) {
+        const int pl = threadIdx.x & 127;
+        char* at = place + next * kPieceBytes;
+        next = next + 1 == kRing ? 0 : next + 1;
+        if (pl == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kRing - 1) : "memory");
+        named_sync(5, 128);  // the place is free
+#pragma unroll
+        for (int u = 0; u < 8; u++) *unit(at, pl, u) = make_uint4(hmul2(x[4 * u], f), hmul2(x[4 * u + 1], f), hmul2(x[4 * u + 2], f), hmul2(x[4 * u + 3], f));
+        fence_proxy_async_smem();
+        named_sync(5, 128);
+        if (pl == 0) {
+            la::bulk_store(to, at, kPieceBytes);
+            la::bulk_commit();
+        }
+    }
+};
+__device__ __forceinline__ void tmem_bits(uint32_t addr, uint32_t (&r)[32]) {
+    float x[32];
+    la::tmem_ld32(addr, x);
+#pragma unroll
+    for (int i = 0; i < 32; i++) r[i] = __float_as_uint(x[i]);
+}
+
 // blockIdx.y of kTcSum: 0 walks from zero (E), 1 from the identity without v (Phi).
 template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void walk(const TcWalkArgs& w, char* sm) {
     constexpr bool SUM = MODE == kTcSum, OUT = MODE == kTcY, KEEP = MODE == kTcKeep;
@@ -362,63 +391,35 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     *reinterpret_cast<uint4*>(yp + t * a.H * a.P + p) = make_uint4(0, 0, 0, 0);
         }
         if (KEEP) {
+            Ring ring = {staging, 0};
             for (int ch = 0; ch < chunks; ch++) {
                 const uint32_t ph = ch & 1;
                 const int64_t image = (bh * ptiles + pt) * w.chunks + c_begin + ch;
+                uint32_t x[32];
                 wait_or_fail(&s_s[0], ph, &s_fail);
                 wait_or_fail(&s_s[1], ph, &s_fail);
                 la::tc_fence_after();
                 // the parts of S under one scale: what the largest channel's is
                 float own = s_ss[ph][pl], all = group_min(own, s_red, 5);
                 uint32_t f = pack2<__half>(all / own, all / own);
-#pragma unroll
-                for (int c = 0; c < 2 * NB; c++) {  // 32 columns: 64 states of one part
-                    float x[32];
-                    la::tmem_ld32(tm + my + kS + 32 * c, x);
-#pragma unroll
-                    for (int u = 0; u < 8; u++)
-                        *unit(staging + c * 2 * kTileBytes, pl, u) =
-                            make_uint4(hmul2(__float_as_uint(x[4 * u]), f), hmul2(__float_as_uint(x[4 * u + 1]), f),
-                                       hmul2(__float_as_uint(x[4 * u + 2]), f), hmul2(__float_as_uint(x[4 * u + 3]), f));
-                }
-                arrive(&s_early);
-                fence_proxy_async_smem();
-                named_sync(5, 128);
-                if (first) {
-                    la::bulk_store(w.states + image * state_bytes(NB), staging, state_bytes(NB));
-                    la::bulk_commit();
-                    w.state_inv[image] = 1.0f / all;
+                if (first) w.state_inv[image] = 1.0f / all;
+#pragma unroll 1
+                for (int c = 0; c < 2 * NB; c++) {
+                    tmem_bits(tm + my + kS + 32 * c, x);
+                    if (c == 2 * NB - 1) arrive(&s_early);
+                    ring.put(x, f, w.states + image * state_bytes(NB) + c * kPieceBytes);
                 }
                 wait_or_fail(&s_uy, ph, &s_fail);
                 la::tc_fence_after();
                 own = s_us[ph][pl], all = group_min(own, s_red, 5);
                 f = pack2<__half>(all / own, all / own);
-                char* to = staging + state_bytes(NB) + (pl >> 6) * kTileBytes + (pl & 7) * 2;
-                const int cu = (pl & 63) >> 3;
-#pragma unroll
+                if (first) w.u_inv[image] = 1.0f / all;
+#pragma unroll 1
                 for (int part = 0; part < 2; part++) {
-                    float x[32];
-                    la::tmem_ld32(tm + my + kD1 + 32 * part, x);
-#pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const uint32_t r = hmul2(__float_as_uint(x[j]), f);
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const int t = 2 * j + e;
-                            *reinterpret_cast<uint16_t*>(to + part * 2 * kTileBytes + t * 128 + ((cu ^ (t & 7)) << 4)) = (uint16_t)(e ? r >> 16 : r);
-                        }
-                    }
+                    tmem_bits(tm + my + kD1 + 32 * part, x);
+                    if (part == 1) arrive(&s_late);
+                    ring.put(x, f, w.us + image * kRowsBytes + part * kPieceBytes);
                 }
-                arrive(&s_late);
-                fence_proxy_async_smem();
-                named_sync(5, 128);
-                if (first) {
-                    la::bulk_store(w.us + image * kRowsBytes, staging + state_bytes(NB), kRowsBytes);
-                    la::bulk_commit();
-                    w.u_inv[image] = 1.0f / all;
-                    la::bulk_wait_read();
-                }
-                named_sync(5, 128);
             }
         }
         if (first) la::bulk_wait_all();
@@ -529,22 +530,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_walk(const __grid_constant__ Tc
 //   D0 = dY^T P              D1 = R^T K^T          dU = scale D0 + e^{cl - c} D1      (the adjoint of U)
 //   D2 = dU M = X^T          (the adjoint of beta (v - ..), transposed)
 //   Dq = (scale e^c dY)^T Q  D3 = (-beta e^c X)^T K     R <- e^{cl} R + Dq + D3
-// D0 and Dq do not wait for R: the third warpgroup makes their left operands (dY is exact in one f16
-// part under its channel's scale), and copies the parts of R and X that the chunk kernel reads.
+// D0 and Dq do not wait for R.  D0's left operand is dY's image, exact; the third warpgroup makes Dq's, and copies the
+// parts of R and X that the chunk kernel reads.
 template <int NB> struct BackStage {
     static constexpr int block = 2 * kTileBytes, dy = NB * block, image = dy + 2 * kTileBytes, head = image + 4 * kTileBytes,
                          bytes = head + 2048;
 };
-// columns: D1, then parts of X; D0, then D2; Dq, then D3; parts of R; dY, then parts of dU, then of -beta e^c X; parts
-// of scale e^c dY
+// columns: D1, then parts of X; D0, then D2; Dq, then D3; parts of R; parts of dU, then of -beta e^c X; parts of
+// scale e^c dY
 constexpr uint32_t bD1 = 0, bD0 = 64, bD3 = 128, bR = 256, bX = 384, bDq = 448;
 
-template <typename T, int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w, const CUtensorMap* dy_map, const TcBackArgs& r, int64_t id, char* sm) {
+template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w, const TcBackArgs& r, int64_t id, char* sm) {
     constexpr int W = 32 * NB;
     using L = BackStage<NB>;
-    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r[2], s_d1, s_dq, s_x, s_d2, s_u, s_d3[2], s_dy, s_dyq, s_xi, s_early, s_late;
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r[2], s_d1, s_dq, s_x, s_d2, s_u, s_d3[2], s_dyq, s_xi, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
-    __shared__ float s_most[2][128], s_ud[2][128], s_rs[2][128], s_xsc[2][128], s_dys[2][128], s_dqs[2][128];
+    __shared__ float s_most[2][128], s_ud[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, warp = tid >> 5, pl = tid & 127;
     const int64_t ptiles = (a.P + kTileP - 1) / kTileP, pt = id % ptiles, p0 = pt * kTileP, bh = id / ptiles;
@@ -553,7 +554,7 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
     if (tid == 0) {
         for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3[0], &s_d3[1]}) mbar_init(bar, 1);
         for (uint64_t* bar : {&s_x, &s_u, &s_xi}) mbar_init(bar, kStateThreads / 32);
-        for (uint64_t* bar : {&s_r[0], &s_r[1], &s_dy, &s_dyq, &s_early, &s_late}) mbar_init(bar, 4);
+        for (uint64_t* bar : {&s_r[0], &s_r[1], &s_dyq, &s_early, &s_late}) mbar_init(bar, 4);
         for (uint64_t* bar : {&s_free[0], &s_free[1]}) mbar_init(bar, kStateThreads / 32 + 4);
         s_fail = 0;
         fence_proxy_async_smem();
@@ -564,6 +565,7 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
     const uint32_t tm = s_tm, my = (uint32_t)((warp & 3) * 32) << 16;
     char* staging = sm + 2 * L::bytes;
     auto chunk_of = [&](int i) { return chunks - 1 - i; };
+    const int64_t images = (bh * ptiles + pt) * w.chunks;
 
     if (warp < kStateThreads / 32) {
         take_regs<168>();
@@ -585,7 +587,7 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
             const uint32_t ph = i & 1;
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
-            const float rs = scale_of(bound);
+            const float rs = scale_of(bound), dy_inv = r.dy_inv[images + chunk_of(i)];
             if (i > 0) ok = ok && wait_or_fail(&s_early, ph ^ 1, &s_fail);
             if (half == 0) s_rs[ph][pl] = rs;
 #pragma unroll
@@ -602,7 +604,7 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
             const float k_most = 16384.0f * head->inv_k, inv1 = head->inv_k / rs;
             ok = ok && wait_or_fail(&s_d1, ph, &s_fail);  // D0 and D1
             la::tc_fence_after();
-            const float dys = s_dys[ph][pl], inv0 = a.scale * head->inv_p / dys;
+            const float inv0 = a.scale * head->inv_p * dy_inv;
             float x[32], d[32];
             la::tmem_ld32(tm + my + bD1 + 32 * half, x);
             la::tmem_ld32(tm + my + bD0 + 32 * half, d);
@@ -616,7 +618,7 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
                 x[j + 2] = z.x;
                 x[j + 3] = z.y;
             }
-            const float x_bound = fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * 16384.0f * head->inv_p * (16384.0f / dys)),
+            const float x_bound = fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * 16384.0f * head->inv_p * (16384.0f * dy_inv)),
                         xs = scale_of(x_bound);
             {
                 const uint32_t to = tm + my + bX + 16 * half;
@@ -697,110 +699,65 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
     } else if (warp < kStateThreads / 32 + 4) {
         leave_regs<112>();
         const bool first = tid == kStateThreads;
+        Ring ring = {staging, 0};
         for (int i = 0; i < chunks; i++) {
             const uint32_t ph = i & 1;
-            const int ch = chunk_of(i), nv = (int)min((int64_t)C, len - (int64_t)ch * C);
-            const int64_t image = (bh * ptiles + pt) * w.chunks + ch;
+            const int64_t image = images + chunk_of(i);
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
+            const float dy_scale = a.scale * r.dy_inv[image];
             wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail);
-            float y[64];
-            {
-                const char* tile = at + L::dy + (pl >> 6) * kTileBytes + (pl & 7) * 2;
-                const int c = (pl & 63) >> 3;
+            auto scaled = [&](int hf, float (&z)[32]) {  // scale e^c dY of 32 tokens
 #pragma unroll
-                for (int t = 0; t < 64; t++) {
-                    const float v = ldf(reinterpret_cast<const T*>(tile + t * 128 + ((c ^ (t & 7)) << 4)));
-                    y[t] = t < nv ? v : 0.0f;
+                for (int u = 0; u < 4; u++) {
+                    const uint4 v = *unit(at + L::dy, pl, 4 * hf + u);
+                    const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float2 f = mul2(mul2(splat2(dy_scale), *reinterpret_cast<const float2*>(&head->up[32 * hf + 8 * u + 2 * e])), unpack2<__half>(y[e]));
+                        z[8 * u + 2 * e] = f.x;
+                        z[8 * u + 2 * e + 1] = f.y;
+                    }
                 }
-            }
-            float sc = scale_of(max_abs<64>(y));
-            s_dys[ph][pl] = sc;
-            if (i > 0) {  // what the last products read makes room
-                wait_or_fail(&s_d3[0], ph ^ 1, &s_fail);
-                wait_or_fail(&s_d3[1], ph ^ 1, &s_fail);
+            };
+            {
+                float z[2][32];
+                scaled(0, z[0]);
+                scaled(1, z[1]);
+                arrive(&s_free[ph]);
+                const float dqs = scale_of(fmaxf(max_abs<32>(z[0]), max_abs<32>(z[1])));
+                s_dqs[ph][pl] = dqs;
+                if (i > 0) wait_or_fail(&s_dq, ph ^ 1, &s_fail);  // the last parts are used
                 la::tc_fence_after();
+                put2(tm + my + bDq, tm + my + bDq + 32, z[0], dqs);
+                put2(tm + my + bDq + 16, tm + my + bDq + 48, z[1], dqs);
             }
-            put1(tm + my + bX, y, sc);
-            put1(tm + my + bX + 16, y + 32, sc);
-            la::tmem_wait_st();
-            arrive(&s_dy);
-#pragma unroll
-            for (int t = 0; t < 64; t += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&head->up[t]);
-                y[t] *= a.scale * f.x;
-                y[t + 1] *= a.scale * f.y;
-                y[t + 2] *= a.scale * f.z;
-                y[t + 3] *= a.scale * f.w;
-            }
-            arrive(&s_free[ph]);
-            sc = scale_of(max_abs<64>(y));
-            s_dqs[ph][pl] = sc;
-            put2(tm + my + bDq, tm + my + bDq + 32, y, sc);
-            put2(tm + my + bDq + 16, tm + my + bDq + 48, y + 32, sc);
             la::tmem_wait_st();
             arrive(&s_dyq);
-            // the parts of R under one scale
+            // R's and X's parts under one scale each: what the largest channel's is
             wait_or_fail(&s_r[0], ph, &s_fail);
             wait_or_fail(&s_r[1], ph, &s_fail);
             la::tc_fence_after();
+            uint32_t x[32], z[32];
             float own = s_rs[ph][pl], all = group_min(own, s_red, 5);
             uint32_t f = pack2<__half>(all / own, all / own);
-#pragma unroll
-            for (int part = 0; part < 2; part++) {
-                if (first) la::bulk_wait_read();
-                named_sync(5, 128);  // the staging tiles are free
-#pragma unroll
-                for (int n = 0; n < NB; n++) {
-                    float x[32];
-                    la::tmem_ld32(tm + my + bR + 32 * (part * NB + n), x);
-#pragma unroll
-                    for (int u = 0; u < 8; u++)
-                        *unit(staging + n * 2 * kTileBytes, pl, u) =
-                            make_uint4(hmul2(__float_as_uint(x[4 * u]), f), hmul2(__float_as_uint(x[4 * u + 1]), f),
-                                       hmul2(__float_as_uint(x[4 * u + 2]), f), hmul2(__float_as_uint(x[4 * u + 3]), f));
-                }
-                if (part == 1) arrive(&s_early);
-                fence_proxy_async_smem();
-                named_sync(5, 128);
-                if (first) {
-                    la::bulk_store(r.states + image * state_bytes(NB) + part * NB * 2 * kTileBytes, staging, NB * 2 * kTileBytes);
-                    la::bulk_commit();
-                }
-            }
             if (first) r.state_inv[image] = 1.0f / all;
+#pragma unroll 1
+            for (int c = 0; c < 2 * NB; c++) {
+                tmem_bits(tm + my + bR + 32 * c, x);
+                if (c == 2 * NB - 1) arrive(&s_early);
+                ring.put(x, f, r.states + image * state_bytes(NB) + c * kPieceBytes);
+            }
             wait_or_fail(&s_xi, ph, &s_fail);
             la::tc_fence_after();
             own = s_xsc[ph][pl], all = group_min(own, s_red, 5);
             f = pack2<__half>(all / own, all / own);
-            char* to = staging + NB * 2 * kTileBytes + (pl >> 6) * kTileBytes + (pl & 7) * 2;
-            const int cu = (pl & 63) >> 3;
-#pragma unroll
-            for (int part = 0; part < 2; part++) {
-                if (part == 1) {
-                    if (first) la::bulk_wait_read();
-                    named_sync(5, 128);
-                }
-                float x[32];
-                la::tmem_ld32(tm + my + bD1 + 32 * part, x);
-                if (part == 1) arrive(&s_late);
-#pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    const uint32_t v = hmul2(__float_as_uint(x[j]), f);
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int t = 2 * j + e;
-                        *reinterpret_cast<uint16_t*>(to + t * 128 + ((cu ^ (t & 7)) << 4)) = (uint16_t)(e ? v >> 16 : v);
-                    }
-                }
-                fence_proxy_async_smem();
-                named_sync(5, 128);
-                if (first) {
-                    la::bulk_store(r.xs + image * kRowsBytes + part * 2 * kTileBytes, staging + NB * 2 * kTileBytes, 2 * kTileBytes);
-                    la::bulk_commit();
-                }
-            }
             if (first) r.x_inv[image] = 1.0f / all;
+            tmem_bits(tm + my + bD1, x);
+            tmem_bits(tm + my + bD1 + 32, z);
+            arrive(&s_late);
+            ring.put(x, f, r.xs + image * kRowsBytes);
+            ring.put(z, f, r.xs + image * kRowsBytes + kPieceBytes);
         }
         if (first) la::bulk_wait_all();
     } else {
@@ -810,11 +767,10 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
                 if (i > 1 && !wait_or_fail(&s_free[i & 1], ((i >> 1) + 1) & 1, &s_fail)) break;
                 char* at = sm + (i & 1) * L::bytes;
                 uint64_t* bar = &s_full[i & 1];
-                const int ch = chunk_of(i), t0 = ch * C;
+                const int ch = chunk_of(i);
                 mbar_expect_tx(bar, NB * L::block + 6 * kTileBytes + (int)sizeof(ImageHead));
                 bulk_load(at, w.keys + ((b * w.chunks + ch) * a.G + hq) * (NB * 2 * kTileBytes), NB * L::block, bar);
-                la::tma_load_4d(at + L::dy, dy_map, (int)p0, (int)h, t0, (int)b, bar);
-                la::tma_load_4d(at + L::dy + kTileBytes, dy_map, (int)p0 + 64, (int)h, t0, (int)b, bar);
+                bulk_load(at + L::dy, r.dys + (images + ch) * kPieceBytes, kPieceBytes, bar);
                 bulk_load(at + L::image, w.images + (bh * w.chunks + ch) * image_bytes(2), 4 * kTileBytes + (int)sizeof(ImageHead), bar);
             }
         } else if (tid == kThreads - 128) {  // products
@@ -822,13 +778,14 @@ template <typename T, int NB> __device__ __forceinline__ void walk_back(const Tc
                 const uint32_t ph = i & 1;
                 const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
                 constexpr uint32_t dK = la::mma_desc<__half>(128, C, false, false), dR = la::mma_desc<__half>(128, C, false, true);
-                if (!wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail) || !wait_or_fail(&s_dy, ph, &s_fail)) break;
+                if (!wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail)) break;
+                if (i > 0 && !wait_or_fail(&s_u, ph ^ 1, &s_fail)) break;  // D2 is read
                 la::tc_fence_after();
 #pragma unroll
                 for (int part = 1; part >= 0; part--)
 #pragma unroll
                     for (int s = 0; s < 4; s++)
-                        la::mma_ts(tm + bD0, tm + bX + 8 * s, la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
+                        la::mma(tm + bD0, la::smem_desc(at + L::dy + s * 32), la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
                 if (i > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
 #pragma unroll
                 for (int half = 0; half < 2; half++) {
@@ -885,7 +842,7 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(kThreads, 1) k_walks(const __grid_constant__ TcWalkArgs w, const __grid_constant__ TcBackArgs r, int forward) {
     extern __shared__ __align__(1024) char sm[];
     if ((int)blockIdx.x < forward) walk<T, NB, kTcKeep>(w, sm);
-    else walk_back<T, NB>(w, &r.dy, r, blockIdx.x - forward, sm);
+    else walk_back<NB>(w, r, blockIdx.x - forward, sm);
 }
 
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
@@ -960,8 +917,7 @@ template <typename T, int NB, TcWalkMode MODE> cudaError_t walk_go(const TcWalkA
     return cudaGetLastError();
 }
 template <typename T, int NB> cudaError_t walks_go(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
-    constexpr int keep = 2 * Stage<NB, kPParts<T>, false>::bytes + state_bytes(NB) + kRowsBytes,
-                  back = 2 * BackStage<NB>::bytes + NB * 2 * kTileBytes + 2 * kTileBytes, bytes = keep > back ? keep : back;
+    constexpr int keep = 2 * Stage<NB, kPParts<T>, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = (keep > back ? keep : back) + kRing * kPieceBytes;
     const cudaError_t e = la::allow_smem<k_walks<T, NB>>(bytes);
     if (e != cudaSuccess) return e;
     const int64_t units = ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H;
