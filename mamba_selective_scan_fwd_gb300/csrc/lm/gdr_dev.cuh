@@ -19,17 +19,14 @@ __device__ __forceinline__ float log_decay(const Args& a, int64_t b, int64_t t, 
     return a.g ? la::clamp_g(a.g[(b * a.L + t) * a.H + h]) : 0.0f;
 }
 
-// One warp, lane = tokens 2 lane and 2 lane + 1 of a chunk: its cumulative log2 decays c, tail = e^{c_e - c_t} with e
+// One warp, lane = tokens 2 lane and 2 lane + 1 of a chunk, x: their log2 decays; the chunk's cumulative log2 decays c, tail = e^{c_e - c_t} with e
 // the end of the token's run of 16, and whether no run leaves 2^-64 .. 2^64 (then e^{c_i - c_j} inside one may be
 // taken as e^{c_i - c_e} e^{c_e - c_j}).  Returns this lane's c.
 struct Pair {
     la::Two c[2];
 };
-__device__ __forceinline__ Pair chunk_decays(const Args& a, int64_t b, int64_t t0, int64_t h, int nv, la::Two* c, float* tail, bool& flat) {
+__device__ __forceinline__ Pair chunk_decays(const float (&x)[2], la::Two* c, float* tail, bool& flat) {
     const int lane = threadIdx.x & 31;
-    float x[2];
-#pragma unroll
-    for (int i = 0; i < 2; i++) x[i] = 2 * lane + i < nv ? log_decay(a, b, t0 + 2 * lane + i, h) * la::kLog2e : 0.0f;
     Pair p;
     la::warp_cumsum<2>(x, p.c);
     const la::Two end = {__shfl_sync(kFull, p.c[1].h, lane | 7), __shfl_sync(kFull, p.c[1].l, lane | 7)};

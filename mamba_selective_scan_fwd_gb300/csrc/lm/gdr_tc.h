@@ -32,13 +32,16 @@ struct ImageHead {
     float down[kChunk];  // e^{cl - c_t}
     float beta[kChunk];
     float beta_up[kChunk];  // beta_t e^{c_t}
+    float tail[kChunk];     // e^{c_e - c_t}, e the end of the token's run of 16 (chunk_decays)
+    float2 c[kChunk];       // c_t in units of log 2, the sum of two floats
     float by;            // the chunk's decay as la::Decay
     int32_t weak;
     float inv_k, inv_q, inv_m, inv_p;  // what undoes the scales of K, Q, M and P
     float most_bu, most_down;  // largest |beta_up|, largest down
-    float pad[56];
+    int32_t flat;              // whether tail may stand for differences inside a run
+    float pad[55];
 };
-static_assert(sizeof(ImageHead) == 1280, "bulk copies are multiples of 16 bytes");
+static_assert(sizeof(ImageHead) == 2048, "bulk copies are multiples of 16 bytes");
 __host__ __device__ constexpr int image_bytes(int parts) { return (2 + parts) * kTileBytes + (int)sizeof(ImageHead); }
 // parts of P: y is good to the io type's half step with one for bf16, with two for f16
 constexpr int fwd_parts(int dtype) { return dtype == 1 ? 2 : 1; }

@@ -30,9 +30,9 @@ using la::wait_or_fail;
 
 constexpr int C = kChunk;
 constexpr int kWorkers = 256, kThreads = kWorkers + 128;  // one thread of the last 128 loads and issues the products
-// Registers a thread: 168 at launch; the workers take what the others leave (2 x 216 + 72 of 3 x 168).
-__device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
-__device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+// Registers a thread: 168 at launch; the workers take what the others leave (2 x 224 + 56 of 3 x 168).
+__device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 
 template <int NB> struct ChunkSmem {
     // K and Q by turns; X and dY (high parts); X's low part and zeros (dY has none); U, high and low; H or R, for each 64
@@ -90,11 +90,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     constexpr int EP = la::kF16<T> ? 2 : 1;  // parts of E and F in dq's and dk's products
     // landed: K and Q; an item's tiles; H or R.  Workers: E and F stand; H is copied; the item's tiles are read, its products.
     // Products: E; H's; R's; the pairs'
-    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_ef, s_copied, s_read, s_done, s_c1, s_c2[2], s_c3, s_c4;
+    __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_ef, s_copied, s_read, s_done, s_c1, s_c2, s_c3, s_c4;
     __shared__ uint32_t s_tm, s_fail;
-    __shared__ Two s_c[C];
-    __shared__ __align__(16) float s_tail[C];
-    __shared__ bool s_flat;
     __shared__ float s_max[8], s_xv[4][C], s_row[2][128], s_col[8][32], s_dot[3][2][128], s_a[C], s_b[C], s_db[C], s_thr[8];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = tid & 127, half = tid >> 7;
@@ -153,7 +150,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     char *KQ = sm + L::keys, *Z = sm + L::z, *Zl = sm + L::zl, *U = sm + L::u, *S = sm + L::s, *EF = sm + L::ef;
     const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + L::head);
     if (tid == 0) {
-        for (uint64_t* bar : {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2, &s_c3, &s_c4}) mbar_init(bar, 1);
         for (uint64_t* bar : {&s_ef, &s_copied, &s_read, &s_done}) mbar_init(bar, kWorkers / 32);
         s_fail = 0;
         fence_proxy_async_smem();
@@ -185,8 +182,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     if (warp >= kWorkers / 32) {
         leave_regs();
         if (tid == kWorkers) {
-            constexpr uint32_t kk = la::mma_desc<__half>(128, C, false, false), kr = la::mma_desc<__half>(128, C, false, true),
-                               rr = la::mma_desc<__half>(128, C, true, true);
+            constexpr uint32_t kk = la::mma_desc<__half>(128, C, false, false), kw = la::mma_desc<__half>(128, 64 * NB, false, true),
+                               rr = la::mma_desc<__half>(128, C, true, true), rw = la::mma_desc<__half>(128, 64 * NB, true, true);
             const uint32_t keys_at = smem_addr(KQ), z_at = smem_addr(Z), zl_at = smem_addr(Zl), u_at = smem_addr(U), s_at = smem_addr(S), ef_at = smem_addr(EF);
             mbar_expect_tx(&s_key, NB * 16384);
             bulk_load(KQ, w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384), NB * 16384, &s_key);
@@ -208,50 +205,41 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                         la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes), la::smem_desc(u_at + (o == 1 ? kPieceBytes : 0) + s * 2048), rr,
                                 o > 0 || s > 0);
                 la::mma_commit(&s_c1);
+                for (int n = 0; n < NB; n++) wait_or_fail(&s_h[n], 0, &s_fail);
+                // (all states at once: the left operand is read from shared memory half as often)
 #pragma unroll 1
-                for (int n = 0; n < NB; n++) {
-                    if (!wait_or_fail(&s_h[n], 0, &s_fail)) break;
-#pragma unroll 1
-                    for (int o = 0; o < 3; o++)
+                for (int o = 0; o < 3; o++)
 #pragma unroll
-                        for (int s = 0; s < 8; s++)
-                            la::mma(tm + cZ + 64 * n, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes),
-                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? kPieceBytes : 0) + s * 2048), rr, o > 0 || s > 0);
-                    la::mma_commit(&s_c2[n]);
-                }
+                    for (int s = 0; s < 8; s++)
+                        la::mma(tm + cZ, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes),
+                                la::smem_desc(s_at + (o == 1 ? kPieceBytes : 0) + s * 2048, 2 * kPieceBytes), rw, o > 0 || s > 0);
+                la::mma_commit(&s_c2);
                 // R takes H's place
                 if (!wait_or_fail(&s_copied, ph, &s_fail)) break;
 #pragma unroll 1
-                for (int n = 0; n < NB; n++) {
-                    wait_or_fail(&s_c2[n], ph, &s_fail);
-                    load_states(w.after, image_of(item), n);
-                }
+                wait_or_fail(&s_c2, ph, &s_fail);
+                for (int n = 0; n < NB; n++) load_states(w.after, image_of(item), n);
                 if (!wait_or_fail(&s_ef, ph, &s_fail)) break;
                 la::tc_fence_after();
 #pragma unroll 1
-                for (int n = 0; n < NB; n++)
-#pragma unroll 1
-                    for (int part = EP - 1; part >= 0; part--) {
-                        const uint32_t left = part ? zl_at : ef_at;
+                for (int part = EP - 1; part >= 0; part--) {
+                    const uint32_t left = part ? zl_at : ef_at;
 #pragma unroll
-                        for (int s = 0; s < 4; s++)
-                            la::mma(tm + cK + 64 * n, la::smem_desc(left + s * 32), la::smem_desc(keys_at + n * 16384 + s * 2048), kr, part < EP - 1 || s > 0);
+                    for (int s = 0; s < 4; s++)
+                        la::mma(tm + cK, la::smem_desc(left + s * 32), la::smem_desc(keys_at + s * 2048, 16384), kw, part < EP - 1 || s > 0);
 #pragma unroll
-                        for (int s = 0; s < 8; s++)
-                            la::mma(tm + cT + 64 * n, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + n * 16384 + s * 2048), rr, part < EP - 1 || s > 0);
-                    }
-                la::mma_commit(&s_c4);
-#pragma unroll 1
-                for (int n = 0; n < NB; n++) {
-                    if (!wait_or_fail(&s_h[n], 1, &s_fail)) break;
-                    // (the 64 tokens twice)
-#pragma unroll 1
-                    for (int o = 0; o < 3; o++)
-#pragma unroll
-                        for (int s = 0; s < 8; s++)
-                            la::mma(tm + cR + 64 * n, la::smem_desc(u_at + (o == 0 ? kPieceBytes : 0) + s * 2048, 0),
-                                    la::smem_desc(s_at + n * 32768 + (o == 1 ? kPieceBytes : 0) + s * 2048), rr, o > 0 || s > 0);
+                    for (int s = 0; s < 8; s++)
+                        la::mma(tm + cT, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + s * 2048, 16384), rw, part < EP - 1 || s > 0);
                 }
+                la::mma_commit(&s_c4);
+                for (int n = 0; n < NB; n++) wait_or_fail(&s_h[n], 1, &s_fail);
+                // (the 64 tokens twice)
+#pragma unroll 1
+                for (int o = 0; o < 3; o++)
+#pragma unroll
+                    for (int s = 0; s < 8; s++)
+                        la::mma(tm + cR, la::smem_desc(u_at + (o == 0 ? kPieceBytes : 0) + s * 2048, 0),
+                                la::smem_desc(s_at + (o == 1 ? kPieceBytes : 0) + s * 2048, 2 * kPieceBytes), rw, o > 0 || s > 0);
                 la::mma_commit(&s_c3);
                 if (item + 1 < items) {  // (E's and F's low part stands in Z's)
                     if (!wait_or_fail(&s_read, ph, &s_fail) || !wait_or_fail(&s_c3, ph, &s_fail) || (EP > 1 && !wait_or_fail(&s_c4, ph, &s_fail))) break;
@@ -269,11 +257,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         const int64_t h = h_lo + item / ptiles, pt = item % ptiles, p0 = pt * kTileP, im = image_of(item);
         const float x_inv = w.x_inv[im], dy_inv = w.dy_inv[im], u_inv = w.u_inv[im], before_inv = w.before_inv[im], after_inv = w.after_inv[im];
         if (pt == 0) {
-            if (warp == 0) {
-                bool flat;
-                chunk_decays(a, b, t0, h, nv, s_c, s_tail, flat);
-                if (lane == 0) s_flat = flat;
-            }
             if (tid >= 64 && tid < 64 + C) s_a[tid - 64] = s_b[tid - 64] = s_db[tid - 64] = 0.0f;
             if (tid >= 128 && tid < 136) s_thr[tid - 128] = 0.0f;
         }
@@ -329,10 +312,11 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             float e[32], k[32];
             la::tmem_ld32(tm + my + cE + 32 * half, e);
             la::tmem_ld32(tm + my + cQK + 32 * half, k);
-            const Two ci = s_c[tok];
+            const Two* c = reinterpret_cast<const Two*>(head->c);
+            const Two ci = c[tok];
             const float f = u_inv * (q_side ? a.scale * dy_inv : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
             const int last = q_side ? tok : tok - 1;
-            pair_factors(e, s_c, s_tail, s_flat, 32 * half, ci, f, last);
+            pair_factors(e, c, head->tail, head->flat != 0, 32 * half, ci, f, last);
             // of a key's row: e^{c_i - c_j} x_i . u_j so far
             float row = 0.0f, most = 0.0f;
             const float sign = q_side ? 1.0f : -beta;
@@ -353,7 +337,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[i]);
             ef_scale = la::f16_scale(most) * rho;
             if (EP > 1) {  // the low part takes Z's, which H's product is done with
-                for (int n = 0; n < NB; n++) ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
+                ok = wait_or_fail(&s_c2, ph, &s_fail) && ok;
             }
 #pragma unroll
             for (int u = 0; u < 4; u++) {
@@ -380,10 +364,9 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         fence_proxy_async_smem();
         arrive(&s_ef);
         // H's products
-#pragma unroll
-        for (int n = 0; n < NB; n++) ok = wait_or_fail(&s_c2[n], ph, &s_fail) && ok;
+        ok = wait_or_fail(&s_c2, ph, &s_fail) && ok;
         la::tc_fence_after();
-        const float up = head->up[tok], down = head->down[tok];
+        const float up = head->up[tok], down = head->down[tok], all = head->up[C - 1];
         {
             const float f = before_inv * (q_side ? a.scale * up * dy_inv : -beta * up * x_inv);
             float dot = 0.0f;
@@ -460,8 +443,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             float sum = 0.0f;
 #pragma unroll
             for (int u = 0; u < 8; u++) sum += s_thr[u];
-            const Two cl = s_c[C - 1];
-            sum *= la::ex2(cl.h + cl.l);
+            sum *= all;
             const int t = 2 * lane;
             const float a0 = s_a[t], a1 = s_a[t + 1], b0 = s_b[t], b1 = s_b[t + 1];
             float A = a0 + a1, B = b0 + b1;  // suffix of a, prefix of b over lanes
@@ -486,7 +468,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     }
     if (ok) put_out(acc);
     }
-    uint64_t* const bars[9] = {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2[0], &s_c2[1], &s_c3, &s_c4};
+    uint64_t* const bars[8] = {&s_key, &s_in, &s_h[0], &s_h[1], &s_c1, &s_c2, &s_c3, &s_c4};
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
 

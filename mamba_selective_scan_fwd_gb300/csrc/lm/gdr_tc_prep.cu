@@ -141,14 +141,29 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     __shared__ bool s_flat[kHeads];  // no run of 16 leaves 2^-64 .. 2^64
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t id = blockIdx.x;
-    const int64_t split = id % w.splits;
+    unsigned id = blockIdx.x;
+    const int split = id % w.splits;
     id /= w.splits;
-    const int64_t gq = id % a.G;
-    id /= a.G;
-    const int64_t chunk = id % w.chunks, b = id / w.chunks, t0 = chunk * C, rep = a.H / a.G;
+    const int gq = id % (unsigned)a.G;
+    id /= (unsigned)a.G;
+    const int64_t chunk = id % (unsigned)w.chunks, b = id / (unsigned)w.chunks, t0 = chunk * C;
+    const int rep = (int)(a.H / a.G), h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
     const int nv = (int)max((int64_t)0, min((int64_t)C, row_length(a, b) - t0));
     if (nv == 0) return;  // no walk gets here
+    // this warp's head of the first few: what its decays come from, on its way before all else
+    float g[2], beta_t[2];
+    auto fetch = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int t = 2 * lane + i;
+            g[i] = beta_t[i] = 0.0f;
+            if (t < nv && h < h_hi) {
+                if (a.g) g[i] = a.g[(b * a.L + t0 + t) * a.H + h];
+                beta_t[i] = a.beta[(b * a.L + t0 + t) * a.H + h];
+            }
+        }
+    };
+    fetch(h_lo + warp);
     char *KQ = sm + L::kq, *I = sm + L::image;
     float* A = reinterpret_cast<float*>(sm + L::a);
     ImageHead* head = reinterpret_cast<ImageHead*>(I + (2 + PARTS) * kTileBytes);
@@ -165,18 +180,16 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
         }
     }
     if (warp == 1) la::tmem_alloc(&s_tm, 64);
-    const int64_t h_lo = gq * rep + rep * split / w.splits, h_hi = gq * rep + rep * (split + 1) / w.splits;
-    auto decays = [&](int64_t h) {  // this warp's head
+    auto decays = [&] {  // this warp's head
+        const float x[2] = {la::clamp_g(g[0]) * la::kLog2e, la::clamp_g(g[1]) * la::kLog2e};
         bool flat;
-        const Pair p = chunk_decays(a, b, t0, h, nv, s_c[warp], s_tail[warp], flat);
+        const Pair p = chunk_decays(x, s_c[warp], s_tail[warp], flat);
         const Two(&c)[2] = p.c;
         float bu = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const int t = 2 * lane + i;
-            const float beta = t < nv ? a.beta[(b * a.L + t0 + t) * a.H + h] : 0.0f;
-            s_beta[warp][t] = beta;
-            bu = fmaxf(bu, fabsf(beta * ex2a(c[i].h)));
+            s_beta[warp][2 * lane + i] = beta_t[i];
+            bu = fmaxf(bu, fabsf(beta_t[i] * ex2a(c[i].h)));
         }
         bu = warp_max(bu);
         const Two cl = {__shfl_sync(kFull, c[1].h, 31), __shfl_sync(kFull, c[1].l, 31)};
@@ -189,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
         // the chunk's decay, in natural units from the same sum (rounded once more: 2^-24 of cl)
         if (lane == 31) s_by[warp] = la::decay_of((c[1].h + c[1].l) * kLn2);
     };
-    if (h_lo + warp < h_hi) decays(h_lo + warp);
+    if (h_lo + warp < h_hi) decays();
     __syncthreads();
     la::tc_fence_after();
     const uint32_t tm = s_tm, my = (uint32_t)(tid & 96) << 16;
@@ -207,51 +220,60 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     __syncwarp();
     // K and Q as f16: unit tid + 128 i of the 512 of each tile
     float scale_k, scale_q;
-    char* keys = w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384);
+    {
+        uint4 x[2][4 * NB];
+        float most[2] = {};
 #pragma unroll
-    for (int side = 0; side < 2; side++) {
-        float most = 0.0f;
-        uint4 x[4 * NB];
-#pragma unroll
-        for (int i = 0; i < 4 * NB; i++) {
-            const int at = tid + 128 * (i & 3);
-            x[i] = *reinterpret_cast<const uint4*>(KQ + (i >> 2) * 16384 + side * kTileBytes + at * 16);
-            if (at >> 3 >= nv) x[i] = make_uint4(0, 0, 0, 0);
-            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float2 f = unpack2<T>(v[e]);
-                most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-        }
-        most = warp_max(most);
-        if (lane == 0) s_max[side][warp] = most;
-        __syncthreads();
-        const float scale = la::f16_scale(max4(s_max[side]));
-        if (side) scale_q = scale;
-        else scale_k = scale;
-        if (split == 0)
+        for (int side = 0; side < 2; side++)
 #pragma unroll
             for (int i = 0; i < 4 * NB; i++) {
-                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t r[4];
+                const int at = tid + 128 * (i & 3);
+                uint4& y = x[side][i];
+                y = *reinterpret_cast<const uint4*>(KQ + (i >> 2) * 16384 + side * kTileBytes + at * 16);
+                if (at >> 3 >= nv) y = make_uint4(0, 0, 0, 0);
+                const uint32_t v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const float2 f = mul2(unpack2<T>(v[e]), splat2(scale));
-                    r[e] = pack2<__half>(f.x, f.y);
+                    const float2 f = unpack2<T>(v[e]);
+                    most[side] = fmaxf(most[side], fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
-                *reinterpret_cast<uint4*>(keys + (i >> 2) * 16384 + side * kTileBytes + (tid + 128 * (i & 3)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
             }
+#pragma unroll
+        for (int side = 0; side < 2; side++) {
+            const float m = warp_max(most[side]);
+            if (lane == 0) s_max[side][warp] = m;
+        }
+        __syncthreads();
+        scale_k = la::f16_scale(max4(s_max[0]));
+        scale_q = la::f16_scale(max4(s_max[1]));
+        char* keys = w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384);
+        if (split == 0)
+#pragma unroll
+            for (int side = 0; side < 2; side++)
+#pragma unroll
+                for (int i = 0; i < 4 * NB; i++) {
+                    const uint4& y = x[side][i];
+                    const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+                    const float2 scale = splat2(side ? scale_q : scale_k);
+                    uint32_t r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float2 f = mul2(unpack2<T>(v[e]), scale);
+                        r[e] = pack2<__half>(f.x, f.y);
+                    }
+                    *reinterpret_cast<uint4*>(keys + (i >> 2) * 16384 + side * kTileBytes + (tid + 128 * (i & 3)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+                }
     }
     ok = la::wait_or_fail(&s_mma, 0, &s_fail) && ok;
     la::tc_fence_after();
-    for (int64_t h0 = h_lo; h0 < h_hi; h0 += kHeads) {
+    for (int h0 = h_lo; h0 < h_hi; h0 += kHeads) {
         if (h0 > h_lo) {
+            fetch(h0 + warp);
             __syncthreads();
-            if (h0 + warp < h_hi) decays(h0 + warp);
+            if (h0 + warp < h_hi) decays();
         }
-        for (int64_t h = h0; h < min(h_hi, h0 + kHeads); h++) {
-            const int hl = (int)(h - h0);
+        for (int h = h0; h < min(h_hi, h0 + kHeads); h++) {
+            const int hl = h - h0;
             if (__syncthreads_or(!ok)) break;  // (and: the last head's image has left, s_max is free)
             // thread: row i of K K^T (warps 0, 1) or Q K^T
             const bool is_q = tid >= C;
@@ -283,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 head->beta_up[tid] = s_beta[hl][tid] * up;
                 head->down[tid] = ex2a(two_diff(cl, c));
                 head->beta[tid] = s_beta[hl][tid];
+                head->tail[tid] = s_tail[hl][tid];
+                head->c[tid] = make_float2(c.h, c.l);
             }
             __syncthreads();
             const float scale_p = la::f16_scale(fmaxf(s_max[0][2], s_max[0][3]));
@@ -315,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                     head->most_bu = s_bu[hl];
                     head->most_down = s_down[hl];
                     head->weak = s_by[hl].weak;
+                    head->flat = s_flat[hl];
                     head->inv_k = 1.0f / scale_k;
                     head->inv_q = 1.0f / scale_q;
                     head->inv_m = 1.0f / scale_m;

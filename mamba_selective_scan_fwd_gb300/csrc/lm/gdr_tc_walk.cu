@@ -846,18 +846,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_walks(const __grid_constant__ T
 }
 
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
-// from.  A block: 8 columns of one head's state, in shared memory, thread = row and four of them; the next Phi
-// (transposed) is on its way while one is used.  65536 tokens x 8 heads, 19 segments: PLACEHOLDER us.
+// from.  A block: 8 columns of one head's state, in shared memory.  Warp w takes the terms of states w, w + 8, ..: a lane
+// four rows and all columns; the warps' sums are added in order.  The next Phi (transposed) is on its way while one is
+// used.  Bound by reading shared memory.  65536 tokens, 8 heads, 19 segments: PLACEHOLDER us.
 constexpr int kCarryCols = 8;
 __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
-    extern __shared__ __align__(16) float phi[];  // [2][N][N]
-    __shared__ __align__(16) float s[2][la::kMaxN][kCarryCols];
+    extern __shared__ __align__(16) float phi[];  // [2][N][N], then the warps' sums [8][N][8]
+    __shared__ __align__(16) float s[la::kMaxN][kCarryCols];
     __shared__ __align__(8) uint64_t s_full[2];
     __shared__ uint32_t s_fail;
     const Args& a = w.a;
-    const int tid = threadIdx.x, N = (int)a.N, n = tid >> 1, c = (tid & 1) * 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = (int)a.N, n = tid >> 1, c = (tid & 1) * 4;
     const int64_t ptiles = (a.P + kCarryCols - 1) / kCarryCols, p0 = blockIdx.x % ptiles * kCarryCols, bh = blockIdx.x / ptiles;
     const int K = (int)w.plan.K;
+    float* sums = phi + 2 * N * N;
     if (tid == 0) {
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
@@ -878,25 +880,44 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
         float4 e = {0.0f, 0.0f, 0.0f, 0.0f};
         if (mine) {
             if (k + 1 < K) e = *at;
-            *reinterpret_cast<float4*>(&s[k & 1][n][c]) = x;
+            *reinterpret_cast<float4*>(&s[n][c]) = x;
             *at = x;
         }
         if (k + 1 == K) break;
         __syncthreads();  // (the Phi before is used)
         if (tid == 0 && k + 2 < K) load(k + 1);
         wait_or_fail(&s_full[k & 1], (k >> 1) & 1, &s_fail);
-        const float* f = phi + (k & 1) * N * N + n;
-        float4 y[2] = {e, {0.0f, 0.0f, 0.0f, 0.0f}};
-        if (mine)
-#pragma unroll 8
-            for (int m = 0; m < N; m += 2)
+        const float* f = phi + (k & 1) * N * N;
+        float2 y[4][kCarryCols / 2] = {};  // rows 4 lane ..
+        if (4 * lane < N)
+#pragma unroll 4
+            for (int m = warp; m < N; m += 8) {
+                const float4 p = *reinterpret_cast<const float4*>(f + m * N + 4 * lane), z0 = *reinterpret_cast<const float4*>(&s[m][0]),
+                             z1 = *reinterpret_cast<const float4*>(&s[m][4]);
+                const float ps[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    const float p = f[(m + u) * N];
-                    const float4 z = *reinterpret_cast<const float4*>(&s[k & 1][m + u][c]);
-                    y[u] = make_float4(fmaf(p, z.x, y[u].x), fmaf(p, z.y, y[u].y), fmaf(p, z.z, y[u].z), fmaf(p, z.w, y[u].w));
+                for (int r = 0; r < 4; r++) {
+                    y[r][0] = fma2(splat2(ps[r]), make_float2(z0.x, z0.y), y[r][0]);
+                    y[r][1] = fma2(splat2(ps[r]), make_float2(z0.z, z0.w), y[r][1]);
+                    y[r][2] = fma2(splat2(ps[r]), make_float2(z1.x, z1.y), y[r][2]);
+                    y[r][3] = fma2(splat2(ps[r]), make_float2(z1.z, z1.w), y[r][3]);
                 }
-        x = make_float4(y[0].x + y[1].x, y[0].y + y[1].y, y[0].z + y[1].z, y[0].w + y[1].w);
+            }
+        if (4 * lane < N)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int j = 0; j < 4; j += 2)
+                    *reinterpret_cast<float4*>(sums + (warp * N + 4 * lane + r) * kCarryCols + 2 * j) = make_float4(y[r][j].x, y[r][j].y, y[r][j + 1].x, y[r][j + 1].y);
+        __syncthreads();
+        if (mine) {
+            x = e;
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const float4 z = *reinterpret_cast<const float4*>(sums + (u * N + n) * kCarryCols + c);
+                x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+            }
+        }
     }
     __syncthreads();
     if (tid == 0 && s_fail) {
@@ -942,8 +963,8 @@ cudaError_t launch_tc_walks(const TcWalkArgs& w, const TcBackArgs& r, cudaStream
 }
 
 cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st) {
-    const int bytes = 2 * (int)(w.a.N * w.a.N) * 4;
-    const cudaError_t e = la::allow_smem<k_carry>(2 * la::kMaxN * la::kMaxN * 4);
+    const int N = (int)w.a.N, bytes = (2 * N * N + 8 * N * kCarryCols) * 4;
+    const cudaError_t e = la::allow_smem<k_carry>((2 * la::kMaxN * la::kMaxN + 8 * la::kMaxN * kCarryCols) * 4);
     if (e != cudaSuccess) return e;
     k_carry<<<(unsigned)(ceil_div(w.a.P, kCarryCols) * w.a.Bsz * w.a.H), 256, bytes, st>>>(w);
     return cudaGetLastError();
