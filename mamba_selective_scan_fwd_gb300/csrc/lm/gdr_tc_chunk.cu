@@ -216,7 +216,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                 la::mma_commit(&s_c2);
                 // R takes H's place
                 if (!wait_or_fail(&s_copied, ph, &s_fail)) break;
-#pragma unroll 1
                 wait_or_fail(&s_c2, ph, &s_fail);
                 for (int n = 0; n < NB; n++) load_states(w.after, image_of(item), n);
                 if (!wait_or_fail(&s_ef, ph, &s_fail)) break;

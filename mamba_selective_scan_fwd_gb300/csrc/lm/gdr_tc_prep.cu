@@ -56,27 +56,49 @@ __device__ __forceinline__ float warp_max(float v) {  // v >= 0
 }
 __device__ __forceinline__ float max4(const float* x) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }
 
-// One warp: the products of rows i, i + 8 of `left` with columns c .. c + 3 of `right`, n terms (a multiple of 4).
-__device__ __forceinline__ void product16(const float* left, const float* right, int n, float4 (&out)[2]) {
-    const int i = (threadIdx.x & 31) >> 2, c = (threadIdx.x & 3) * 4;
-    out[0] = out[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = 0; k < n; k += 4) {
-        const float4 l0 = *reinterpret_cast<const float4*>(left + i * LDA + k), l1 = *reinterpret_cast<const float4*>(left + (i + 8) * LDA + k);
-        const float a0[4] = {l0.x, l0.y, l0.z, l0.w}, a1[4] = {l1.x, l1.y, l1.z, l1.w};
+// A value as two tf32 parts (22 bits).
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// One warp: 16 x 16 of left right, n terms (a multiple of 8), operands in two tf32 parts.  (A warp's matrix instruction, because
+// such a product is too small for a tensor-memory one and its operands are f32 in shared memory, whose reads
+// bound this kernel: as products of four by two values a thread it took four times the reads; 4 x 4096 tokens, 32 heads: 133
+// us so, PLACEHOLDER with it.)
+__device__ __forceinline__ void product16(const float* left, const float* right, int n, float (&out)[2][4]) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const float4 r = *reinterpret_cast<const float4*>(right + (k + u) * LDA + c);
-            out[0] = make_float4(fmaf(a0[u], r.x, out[0].x), fmaf(a0[u], r.y, out[0].y), fmaf(a0[u], r.z, out[0].z), fmaf(a0[u], r.w, out[0].w));
-            out[1] = make_float4(fmaf(a1[u], r.x, out[1].x), fmaf(a1[u], r.y, out[1].y), fmaf(a1[u], r.z, out[1].z), fmaf(a1[u], r.w, out[1].w));
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) out[j][e] = 0.0f;
+#pragma unroll 2
+    for (int k = 0; k < n; k += 8) {
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) split_tf32(left[(g + 8 * (e & 1)) * LDA + k + t + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) split_tf32(right[(k + t + 4 * e) * LDA + 8 * j + g], bh[e], bl[e]);
+            mma_tf32(out[j], al, bh);
+            mma_tf32(out[j], ah, bl);
+            mma_tf32(out[j], ah, bh);
         }
     }
 }
-__device__ __forceinline__ void put16(float* to, const float4 (&x)[2], float sign) {
-    const int i = (threadIdx.x & 31) >> 2, c = (threadIdx.x & 3) * 4;
+__device__ __forceinline__ void put16(float* to, const float (&x)[2][4], float sign) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
-    for (int r = 0; r < 2; r++)
-        *reinterpret_cast<float4*>(to + (i + 8 * r) * LDA + c) = make_float4(sign * x[r].x, sign * x[r].y, sign * x[r].z, sign * x[r].w);
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+            *reinterpret_cast<float2*>(to + (g + 8 * r) * LDA + 8 * j + 2 * t) = make_float2(sign * x[j][2 * r], sign * x[j][2 * r + 1]);
 }
 
 // A (64 x 64, below the diagonal; zeros elsewhere) becomes M = (I + A)^{-1} in place, four warps: blocks of 16 by
@@ -103,7 +125,7 @@ __device__ __forceinline__ void invert(float* A) {
 #pragma unroll
         for (int i = 0; i < 16; i++) A[(d + i) * LDA + d + j] = x[i];
         __syncwarp();
-        float4 t[2];  // warp w: the block below the diagonal's, between its two
+        float t[2][4];  // warp w: the block below the diagonal's, between its two
         float *a = A + 32 * warp * (LDA + 1), *below = a + 16 * LDA;
         product16(below, a, 16, t);
         __syncwarp();
@@ -116,7 +138,7 @@ __device__ __forceinline__ void invert(float* A) {
     __syncthreads();
     const int r = 16 * (warp >> 1), c = 16 * (warp & 1);  // warp: a block of the lower left 32 x 32
     float* quarter = A + 32 * LDA;
-    float4 t[2];
+    float t[2][4];
     product16(quarter + r * LDA + c, A + c * LDA + c, 32 - c, t);  // (a is zero above its blocks' diagonal)
     __syncthreads();
     put16(quarter + r * LDA + c, t, 1.0f);

@@ -57,6 +57,19 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {  // a warp's
 }
 __device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
+// 32 columns at each of two places, one wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t a, float (&x)[32], uint32_t b, float (&y)[32]) {
+    uint32_t r[32], q[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15]), "=r"(q[16]), "=r"(q[17]), "=r"(q[18]), "=r"(q[19]), "=r"(q[20]), "=r"(q[21]), "=r"(q[22]), "=r"(q[23]), "=r"(q[24]), "=r"(q[25]), "=r"(q[26]), "=r"(q[27]), "=r"(q[28]), "=r"(q[29]), "=r"(q[30]), "=r"(q[31])
+                 : "r"(a), "r"(b));
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+        x[i] = __uint_as_float(r[i]);
+        y[i] = __uint_as_float(q[i]);
+    }
+}
+
 // 32 values times s as two f16 parts: 16 columns of tensor memory each
 __device__ __forceinline__ void put2(uint32_t hi, uint32_t lo, const float* x, float s) {
     uint32_t r[16], q[16];
@@ -192,6 +205,39 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         auto pair_sync = [&] { named_sync(1 + (warp & 3), 64); };
         auto max_over = [&](const float (&m)[2][128]) { return fmaxf(m[0][pl], m[1][pl]); };
         bool ok = true;
+        // beta V of a chunk, and the largest value of the channel's, while S^T K^T is on its way
+        float x[32], x_most = 0.0f;
+        auto values = [&](int ch) {
+            char* at = sm + (ch & 1) * L::bytes;
+            const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
+            ok = ok && wait_or_fail(&s_full[ch & 1], (ch >> 1) & 1, &s_fail);
+            if (phi) {
+#pragma unroll
+                for (int j = 0; j < 32; j++) x[j] = 0.0f;
+            } else {
+                const char* tile = at + L::v + (pl >> 6) * kTileBytes + (pl & 7) * 2;
+                const int c = (pl & 63) >> 3;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 be = *reinterpret_cast<const float4*>(&head->beta[32 * half + j]);
+                    const float bs[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int t = 32 * half + j + e;
+                        x[j + e] = bs[e] * ldf(reinterpret_cast<const T*>(tile + t * 128 + ((c ^ (t & 7)) << 4)));
+                    }
+                }
+                const int nv = valid(ch);
+                if (nv < C) {
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        if (32 * half + j >= nv) x[j] = 0.0f;
+                }
+            }
+            s_most[1][half][pl] = max_abs<32>(x);
+            pair_sync();
+            x_most = max_over(s_most[1]);
+        };
         s_most[0][half][pl] = max_abs<W>(S);
         pair_sync();
         float bound = max_over(s_most[0]);  // of |S|
@@ -211,31 +257,9 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             }
             la::tmem_wait_st();
             arrive(&s_s[half]);
-            ok = ok && wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
-            const float inv1 = -head->inv_k / ss;
-            float x[32];
-            if (phi) {
-#pragma unroll
-                for (int j = 0; j < 32; j++) x[j] = 0.0f;
-            } else {
-                const char* tile = at + L::v + (pl >> 6) * kTileBytes + (pl & 7) * 2;
-                const int c = (pl & 63) >> 3;
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 be = *reinterpret_cast<const float4*>(&head->beta[32 * half + j]);
-                    const float bs[4] = {be.x, be.y, be.z, be.w};
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int t = 32 * half + j + e;
-                        x[j + e] = bs[e] * ldf(reinterpret_cast<const T*>(tile + t * 128 + ((c ^ (t & 7)) << 4)));
-                    }
-                }
-            }
-            s_most[0][half][pl] = max_abs<W>(S);
-            s_most[1][half][pl] = max_abs<32>(x);
-            pair_sync();
-            const float k_most = 16384.0f * head->inv_k, s_most_ = max_over(s_most[0]);
-            const float x_bound = fmaf(head->most_bu * (64 * NB) * k_most, s_most_, max_over(s_most[1])), xs = scale_of(x_bound);
+            values(ch);
+            const float inv1 = -head->inv_k / ss, k_most = 16384.0f * head->inv_k;
+            const float x_bound = fmaf(head->most_bu * (64 * NB) * k_most, bound, x_most), xs = scale_of(x_bound);
             ok = ok && wait_or_fail(&s_d1, ph, &s_fail);
             la::tc_fence_after();
             float d[32];
@@ -250,7 +274,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 x[j + 2] = z.x;
                 x[j + 3] = z.y;
             }
-            if (nv < C) {
+            if (nv < C) {  // (whatever S^T k is there)
 #pragma unroll
                 for (int j = 0; j < 32; j++)
                     if (32 * half + j >= nv) x[j] = 0.0f;
@@ -262,10 +286,10 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             la::tmem_wait_st();
             arrive(&s_x);
             const float inv2 = head->inv_m / xs;
+            s_most[0][half][pl] = max_abs<W>(S);
             ok = ok && wait_or_fail(&s_d2, ph, &s_fail);
             la::tc_fence_after();
-            la::tmem_ld32(tm + my + kD3 + 64 + 32 * half, x);
-            la::tmem_ld32(tm + my + kD3 + 32 * half, d);
+            tmem_ld64(tm + my + kD3 + 64 + 32 * half, x, tm + my + kD3 + 32 * half, d);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
                 const float2 f = mul2(splat2(inv2), add2(make_float2(d[j], d[j + 1]), make_float2(x[j], x[j + 1])));
@@ -290,7 +314,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             }
             la::tmem_wait_st();
             const float by = head->by, keep = head->weak ? 1.0f : 0.0f, inv3 = head->inv_k / us;
-            bound = fmaf(64.0f * k_most, ud_most, s_most_ * (keep + fabsf(by)));
+            bound = fmaf(64.0f * k_most, ud_most, max_over(s_most[0]) * (keep + fabsf(by)));
             arrive(&s_u);
             if (!SUM) {
                 const float uy = scale_of(64.0f * 16384.0f * head->inv_m * x_bound);
@@ -606,8 +630,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             la::tc_fence_after();
             const float inv0 = a.scale * head->inv_p * dy_inv;
             float x[32], d[32];
-            la::tmem_ld32(tm + my + bD1 + 32 * half, x);
-            la::tmem_ld32(tm + my + bD0 + 32 * half, d);
+            tmem_ld64(tm + my + bD1 + 32 * half, x, tm + my + bD0 + 32 * half, d);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&head->down[32 * half + j]);
