@@ -12,10 +12,8 @@
 //
 // Roundings: E and F enter dq's and dk's products as one f16 (2^-12 of terms of a bf16 output; f16 io: in two parts).
 // H, R, U and X come in two f16 parts (22 bits), and dg and dbeta take all else in f32.
-#include "gdr_tc.h"
 #include "../simd.cuh"
-#include "tc.cuh"
-#include "gdr_dev.cuh"
+#include "gdr_tc.cuh"
 
 namespace ss {
 namespace gdr {
@@ -26,7 +24,6 @@ using la::Two;
 using la::two_diff;
 using la::unit;
 using la::unpack2;
-using la::wait_or_fail;
 
 constexpr int C = kChunk;
 constexpr int kWorkers = 256, kThreads = kWorkers + 128;  // one thread of the last 128 loads and issues the products
@@ -160,7 +157,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     fence_proxy_async_smem();
     __syncthreads();
     la::tc_fence_after();
-    const uint32_t tm = s_tm, my = (uint32_t)(tid & 96) << 16;
+    const uint32_t tm = __shfl_sync(kFull, s_tm, 0), my = (uint32_t)(tid & 96) << 16;
     const int items = (int)((h_hi - h_lo) * ptiles);
     auto image_of = [&](int item) { return ((b * a.H + h_lo + item / ptiles) * ptiles + item % ptiles) * w.chunks + chunk; };
     auto load_states = [&](const char* images, int64_t im, int n) {  // 64 of the states, two parts
@@ -181,46 +178,57 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     };
     if (warp >= kWorkers / 32) {
         leave_regs();
-        if (tid == kWorkers) {
+        if (__shfl_sync(kFull, warp, 0) == kWorkers / 32) {
             constexpr uint32_t kk = la::mma_desc<__half>(128, C, false, false), kw = la::mma_desc<__half>(128, 64 * NB, false, true),
                                rr = la::mma_desc<__half>(128, C, true, true), rw = la::mma_desc<__half>(128, 64 * NB, true, true);
             const uint32_t keys_at = smem_addr(KQ), z_at = smem_addr(Z), zl_at = smem_addr(Zl), u_at = smem_addr(U), s_at = smem_addr(S), ef_at = smem_addr(EF);
-            mbar_expect_tx(&s_key, NB * 16384);
-            bulk_load(KQ, w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384), NB * 16384, &s_key);
-            load(0);
-            wait_or_fail(&s_key, 0, &s_fail);
-            for (int item = 0; item < items; item++) {
+            if (lane == 0) {
+                mbar_expect_tx(&s_key, NB * 16384);
+                bulk_load(KQ, w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384), NB * 16384, &s_key);
+                load(0);
+            }
+            __syncwarp();
+            const int steps = __shfl_sync(kFull, items, 0);
+            warp_wait(&s_key, 0, &s_fail);
+            for (int item = 0; item < steps; item++) {
                 const uint32_t ph = item & 1;
-                if (!wait_or_fail(&s_in, ph, &s_fail) || (item > 0 && !wait_or_fail(&s_done, ph ^ 1, &s_fail))) break;
+                if (!warp_wait(&s_in, ph, &s_fail) || (item > 0 && !warp_wait(&s_done, ph ^ 1, &s_fail))) break;
                 la::tc_fence_after();
+                if (elect()) {
 #pragma unroll
                 for (int s = 0; s < 4 * NB; s++) {
                     const uint32_t x = keys_at + (s >> 2) * 16384 + (s & 3) * 32;
                     la::mma(tm + cQK, la::smem_desc(x), la::smem_desc(x), kk, s > 0);
                 }
-#pragma unroll 1
+#pragma unroll
                 for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
                     for (int s = 0; s < 8; s++)
                         la::mma(tm + cE, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes), la::smem_desc(u_at + (o == 1 ? kPieceBytes : 0) + s * 2048), rr,
                                 o > 0 || s > 0);
                 la::mma_commit(&s_c1);
-                for (int n = 0; n < NB; n++) wait_or_fail(&s_h[n], 0, &s_fail);
+                }
+                for (int n = 0; n < NB; n++) warp_wait(&s_h[n], 0, &s_fail);
                 // (all states at once: the left operand is read from shared memory half as often)
-#pragma unroll 1
+                if (elect()) {
+#pragma unroll
                 for (int o = 0; o < 3; o++)
 #pragma unroll
                     for (int s = 0; s < 8; s++)
                         la::mma(tm + cZ, la::smem_desc((o == 0 ? zl_at : z_at) + s * 2048, kPieceBytes),
                                 la::smem_desc(s_at + (o == 1 ? kPieceBytes : 0) + s * 2048, 2 * kPieceBytes), rw, o > 0 || s > 0);
                 la::mma_commit(&s_c2);
+                }
                 // R takes H's place
-                if (!wait_or_fail(&s_copied, ph, &s_fail)) break;
-                wait_or_fail(&s_c2, ph, &s_fail);
-                for (int n = 0; n < NB; n++) load_states(w.after, image_of(item), n);
-                if (!wait_or_fail(&s_ef, ph, &s_fail)) break;
+                if (!warp_wait(&s_copied, ph, &s_fail)) break;
+                warp_wait(&s_c2, ph, &s_fail);
+                if (lane == 0)
+                    for (int n = 0; n < NB; n++) load_states(w.after, image_of(item), n);
+                __syncwarp();
+                if (!warp_wait(&s_ef, ph, &s_fail)) break;
                 la::tc_fence_after();
-#pragma unroll 1
+                if (elect()) {
+#pragma unroll
                 for (int part = EP - 1; part >= 0; part--) {
                     const uint32_t left = part ? zl_at : ef_at;
 #pragma unroll
@@ -231,18 +239,22 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                         la::mma(tm + cT, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + s * 2048, 16384), rw, part < EP - 1 || s > 0);
                 }
                 la::mma_commit(&s_c4);
-                for (int n = 0; n < NB; n++) wait_or_fail(&s_h[n], 1, &s_fail);
+                }
+                for (int n = 0; n < NB; n++) warp_wait(&s_h[n], 1, &s_fail);
                 // (the 64 tokens twice)
-#pragma unroll 1
+                if (elect()) {
+#pragma unroll
                 for (int o = 0; o < 3; o++)
 #pragma unroll
                     for (int s = 0; s < 8; s++)
                         la::mma(tm + cR, la::smem_desc(u_at + (o == 0 ? kPieceBytes : 0) + s * 2048, 0),
                                 la::smem_desc(s_at + (o == 1 ? kPieceBytes : 0) + s * 2048, 2 * kPieceBytes), rw, o > 0 || s > 0);
                 la::mma_commit(&s_c3);
-                if (item + 1 < items) {  // (E's and F's low part stands in Z's)
-                    if (!wait_or_fail(&s_read, ph, &s_fail) || !wait_or_fail(&s_c3, ph, &s_fail) || (EP > 1 && !wait_or_fail(&s_c4, ph, &s_fail))) break;
-                    load(item + 1);
+                }
+                if (item + 1 < steps) {  // (E's and F's low part stands in Z's)
+                    if (!warp_wait(&s_read, ph, &s_fail) || !warp_wait(&s_c3, ph, &s_fail) || (EP > 1 && !warp_wait(&s_c4, ph, &s_fail))) break;
+                    if (lane == 0) load(item + 1);
+                    __syncwarp();
                 }
             }
         }
@@ -268,7 +280,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             if (vt < nv && p0 + vp + 8 * u < a.P)
                 vv[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + vt) * a.v.token + h * a.P + p0 + vp + 8 * u);
         }
-        ok = wait_or_fail(&s_in, ph, &s_fail) && ok;
+        ok = wait(&s_in, ph, &s_fail) && ok;
         {
             const float beta = head->beta[vt];
             float sum = 0.0f;
@@ -297,13 +309,13 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         uint4 hs[NB][8];
 #pragma unroll
         for (int n = 0; n < NB; n++) {
-            ok = wait_or_fail(&s_h[n], 0, &s_fail) && ok;
+            ok = wait(&s_h[n], 0, &s_fail) && ok;
             if (w.dg)
 #pragma unroll
                 for (int i = 0; i < 8; i++) hs[n][i] = *reinterpret_cast<const uint4*>(S + n * 32768 + (tid + 256 * i) * 16);
         }
         arrive(&s_copied);
-        ok = wait_or_fail(&s_c1, ph, &s_fail) && ok;
+        ok = wait(&s_c1, ph, &s_fail) && ok;
         la::tc_fence_after();
         const float inv_k = head->inv_k, inv_q = head->inv_q, beta = head->beta[tok], rho = q_side ? inv_q / inv_k : 1.0f;
         float ef_scale;
@@ -336,7 +348,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[i]);
             ef_scale = la::f16_scale(most) * rho;
             if (EP > 1) {  // the low part takes Z's, which H's product is done with
-                ok = wait_or_fail(&s_c2, ph, &s_fail) && ok;
+                ok = wait(&s_c2, ph, &s_fail) && ok;
             }
 #pragma unroll
             for (int u = 0; u < 4; u++) {
@@ -363,7 +375,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
         fence_proxy_async_smem();
         arrive(&s_ef);
         // H's products
-        ok = wait_or_fail(&s_c2, ph, &s_fail) && ok;
+        ok = wait(&s_c2, ph, &s_fail) && ok;
         la::tc_fence_after();
         const float up = head->up[tok], down = head->down[tok], all = head->up[C - 1];
         {
@@ -385,7 +397,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             float through = 0.0f;
 #pragma unroll
             for (int n = 0; n < NB; n++) {
-                ok = wait_or_fail(&s_h[n], 1, &s_fail) && ok;
+                ok = wait(&s_h[n], 1, &s_fail) && ok;
                 // units tid + 256 i: the high part for i < 4, the low part of the same values 1024 units on
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -404,8 +416,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
             if (lane == 0) s_thr[warp] += through * (before_inv * after_inv);
         }
         arrive(&s_read);  // (R's products are waited for where the next tiles are loaded)
-        ok = wait_or_fail(&s_c3, ph, &s_fail) && ok;
-        ok = wait_or_fail(&s_c4, ph, &s_fail) && ok;
+        ok = wait(&s_c3, ph, &s_fail) && ok;
+        ok = wait(&s_c4, ph, &s_fail) && ok;
         la::tc_fence_after();
         {
             const float fk = inv_k / ef_scale, fr = down * u_inv * after_inv, ft = fk;  // (a key's row: rho is 1)

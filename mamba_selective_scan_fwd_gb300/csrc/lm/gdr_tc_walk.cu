@@ -4,7 +4,7 @@
 // with the state transposed: the value channels are the 128 lanes of tensor memory, so that
 // a thread owns a channel (half of its N states, half of a chunk's tokens) and every
 // left operand is written by the thread that will read the product's row:
-//   D1 = S^T K^T             [128 x 64]   S in two f16 parts, from tensor memory
+//   D1 = S^T [K; Q]^T        [128 x 128]  S in two f16 parts, from tensor memory
 //   X = beta (V^T - e^c D1)               two parts
 //   D2 = X M^T = U^T         [128 x 2 x 64]  hi [hi; lo] + lo hi
 //   D3 = (e^{cl - c} U)^T K  [128 x N]    two parts;  S <- e^{cl} S + D3, f32 in registers
@@ -16,10 +16,8 @@
 // from the channel's largest value, which its two threads exchange; the f32 state stays good to
 // a few 1e-7.  P and U enter y's product with one part each for bf16 io (2^-12 of a y that is
 // rounded to 2^-9), with two for f16.
-#include "gdr_tc.h"
 #include "../simd.cuh"
-#include "tc.cuh"
-#include "gdr_dev.cuh"
+#include "gdr_tc.cuh"
 
 namespace ss {
 namespace gdr {
@@ -29,7 +27,6 @@ using la::kF16;
 using la::pack2;
 using la::unit;
 using la::unpack2;
-using la::wait_or_fail;
 
 constexpr int C = kChunk;
 constexpr int kStateThreads = 256, kThreads = 512;  // state; output; loads and products (one thread of the last 128)
@@ -37,7 +34,7 @@ constexpr int kStateThreads = 256, kThreads = 512;  // state; output; loads and 
 template <int N> __device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// columns of tensor memory: S^T K^T, then parts of U; S^T Q^T; X M^T in two halves, then D3; U^T P^T; parts of S;
+// columns of tensor memory: S^T K^T, then parts of U; S^T Q^T (one product with it); X M^T in two halves, then D3; U^T P^T; parts of S;
 // parts of X, then of e U
 constexpr uint32_t kD1 = 0, kQ = 64, kD3 = 128, kY = 256, kS = 320, kX = 448;
 
@@ -150,8 +147,8 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
     // (the backward's images hold P in two parts)
     constexpr int W = 32 * NB, PP = kPParts<T>, IP = KEEP ? 2 : PP;
     using L = Stage<NB, PP, OUT>;
-    // landed; stage free; S (each half); D1; X; D2; U; D3; S^T Q^T; U^T P^T; read by the third warpgroup: early, late
-    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s[2], s_d1, s_x, s_d2, s_u, s_d3[2], s_q, s_uy, s_y, s_early, s_late;
+    // landed; stage free; S; D1; X; D2; e U; D3; U; U^T P^T; read by the third warpgroup: early, late
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_uy, s_y, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
     __shared__ float s_most[2][2][128], s_ud[2][128], s_ss[2][128], s_us[2][128];
     const Args& a = w.a;
@@ -169,9 +166,9 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
     const int chunks = (int)max((int64_t)0, (min(len, t_end) - t_begin + C - 1) / C);
 
     if (tid == 0) {
-        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3[0], &s_d3[1], &s_q, &s_y}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&s_x, &s_u, &s_uy}) mbar_init(bar, kStateThreads / 32);
-        for (uint64_t* bar : {&s_s[0], &s_s[1], &s_early, &s_late}) mbar_init(bar, 4);
+        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_y}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_s, &s_x, &s_u, &s_uy}) mbar_init(bar, kStateThreads / 32);
+        for (uint64_t* bar : {&s_early, &s_late}) mbar_init(bar, 4);
         for (uint64_t* bar : {&s_free[0], &s_free[1]}) mbar_init(bar, OUT ? 4 : kStateThreads / 32);
         s_fail = 0;
         fence_proxy_async_smem();
@@ -179,7 +176,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
     if (warp == 0) la::tmem_alloc(&s_tm, 512);
     __syncthreads();
     la::tc_fence_after();
-    const uint32_t tm = s_tm, my = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tm = __shfl_sync(kFull, s_tm, 0), my = (uint32_t)((warp & 3) * 32) << 16;
     char* staging = sm + 2 * L::bytes;
     auto valid = [&](int ch) { return (int)min((int64_t)C, len - (t_begin + (int64_t)ch * C)); };
 
@@ -210,7 +207,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         auto values = [&](int ch) {
             char* at = sm + (ch & 1) * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
-            ok = ok && wait_or_fail(&s_full[ch & 1], (ch >> 1) & 1, &s_fail);
+            ok = ok && wait(&s_full[ch & 1], (ch >> 1) & 1, &s_fail);
             if (phi) {
 #pragma unroll
                 for (int j = 0; j < 32; j++) x[j] = 0.0f;
@@ -248,7 +245,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const int nv = valid(ch);
             const float ss = scale_of(bound);
-            if (KEEP && ch > 0) ok = ok && wait_or_fail(&s_early, ph ^ 1, &s_fail);  // the last parts have been copied
+            if (KEEP && ch > 0) ok = ok && wait(&s_early, ph ^ 1, &s_fail);  // the last parts have been copied
             if (!SUM && half == 0) s_ss[ph][pl] = ss;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
@@ -256,11 +253,11 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 put2(to, to + 32 * NB, S + 32 * c, ss);
             }
             la::tmem_wait_st();
-            arrive(&s_s[half]);
+            arrive(&s_s);
             values(ch);
             const float inv1 = -head->inv_k / ss, k_most = 16384.0f * head->inv_k;
             const float x_bound = fmaf(head->most_bu * (64 * NB) * k_most, bound, x_most), xs = scale_of(x_bound);
-            ok = ok && wait_or_fail(&s_d1, ph, &s_fail);
+            ok = ok && wait(&s_d1, ph, &s_fail);
             la::tc_fence_after();
             float d[32];
             la::tmem_ld32(tm + my + kD1 + 32 * half, d);
@@ -287,7 +284,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             arrive(&s_x);
             const float inv2 = head->inv_m / xs;
             s_most[0][half][pl] = max_abs<W>(S);
-            ok = ok && wait_or_fail(&s_d2, ph, &s_fail);
+            ok = ok && wait(&s_d2, ph, &s_fail);
             la::tc_fence_after();
             tmem_ld64(tm + my + kD3 + 64 + 32 * half, x, tm + my + kD3 + 32 * half, d);
 #pragma unroll
@@ -325,7 +322,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 la::tmem_wait_st();
                 arrive(&s_uy);
             }
-            ok = ok && wait_or_fail(&s_d3[half], ph, &s_fail);
+            ok = ok && wait(&s_d3, ph, &s_fail);
             la::tc_fence_after();
             if (!OUT) arrive(&s_free[ph]);
 #pragma unroll
@@ -365,8 +362,8 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 const uint32_t ph = ch & 1;
                 const ImageHead* head = reinterpret_cast<const ImageHead*>(sm + ph * L::bytes + L::head);
                 const int nv = valid(ch);
-                wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail);
-                wait_or_fail(&s_q, ph, &s_fail);
+                wait(&s_full[ph], (ch >> 1) & 1, &s_fail);
+                wait(&s_d1, ph, &s_fail);
                 la::tc_fence_after();
                 float q[64];
                 {
@@ -382,7 +379,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 arrive(&s_early);
                 if (first) la::bulk_wait_read();
                 named_sync(5, 128);  // the staging tiles are free
-                wait_or_fail(&s_y, ph, &s_fail);
+                wait(&s_y, ph, &s_fail);
                 la::tc_fence_after();
                 const float inv = a.scale * head->inv_p / s_us[ph][pl];
                 char* tile = staging + (pl >> 6) * kTileBytes + (pl & 7) * 2;
@@ -420,8 +417,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 const uint32_t ph = ch & 1;
                 const int64_t image = (bh * ptiles + pt) * w.chunks + c_begin + ch;
                 uint32_t x[32];
-                wait_or_fail(&s_s[0], ph, &s_fail);
-                wait_or_fail(&s_s[1], ph, &s_fail);
+                wait(&s_s, ph, &s_fail);
                 la::tc_fence_after();
                 // the parts of S under one scale: what the largest channel's is
                 float own = s_ss[ph][pl], all = group_min(own, s_red, 5);
@@ -433,7 +429,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     if (c == 2 * NB - 1) arrive(&s_early);
                     ring.put(x, f, w.states + image * state_bytes(NB) + c * kPieceBytes);
                 }
-                wait_or_fail(&s_uy, ph, &s_fail);
+                wait(&s_uy, ph, &s_fail);
                 la::tc_fence_after();
                 own = s_us[ph][pl], all = group_min(own, s_red, 5);
                 f = pack2<__half>(all / own, all / own);
@@ -449,7 +445,8 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         if (first) la::bulk_wait_all();
     } else {
         leave_regs<56>();
-        if (tid == kThreads - 96) {  // loads
+        const int role = __shfl_sync(kFull, warp, 0) - (kThreads - 128) / 32, steps = __shfl_sync(kFull, chunks, 0);
+        if (role == 1 && lane == 0) {  // loads
         const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
         const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(IP);
         auto load = [&](int ch) {
@@ -470,76 +467,67 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             bulk_load(at + L::head, im + (2 + IP) * kTileBytes, (int)sizeof(ImageHead), bar);
         };
         for (int ch = 0; ch < chunks; ch++) {
-            if (ch > 1 && !wait_or_fail(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
+            if (ch > 1 && !wait(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
             load(ch);
         }
-        } else if (tid == kThreads - 128) {  // products
-        for (int ch = 0; ch < chunks; ch++) {
-            const uint32_t ph = ch & 1;
-            const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
-            constexpr uint32_t d2 = la::mma_desc<__half>(128, 2 * C, false, false),
-                               dP = la::mma_desc<__half>(128, C, false, false), d3 = la::mma_desc<__half>(128, 64, false, true);
-            if (!wait_or_fail(&s_full[ph], (ch >> 1) & 1, &s_fail)) break;
-            // terms of half the states: the halves arrive one after the other, as D3's did
-            auto with_state = [&](uint32_t to, uint32_t tile, int parts, int half) {
-                for (int part = parts - 1; part >= 0; part--)
-#pragma unroll
-                    for (int i = 0; i < 2 * NB; i++) {
-                        const int s = half * 2 * NB + i;
-                        la::mma_ts(tm + to, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(tile + (s >> 2) * L::block + (s & 3) * 32), dP,
-                                   half > 0 || part < parts - 1 || i > 0);
-                    }
-            };
-            // U of the chunk before has left its columns
-            if (!SUM && ch > 0 && !wait_or_fail(OUT ? &s_y : &s_late, ph ^ 1, &s_fail)) break;
-            if (!wait_or_fail(&s_s[0], ph, &s_fail)) break;
-            la::tc_fence_after();
-            with_state(kD1, at, 2, 0);
-            if (!wait_or_fail(&s_s[1], ph, &s_fail)) break;
-            la::tc_fence_after();
-            with_state(kD1, at, 2, 1);
-            la::mma_commit(&s_d1);
-            if (OUT) {  // Q's product of the chunk before is read
-                if (ch > 0 && !wait_or_fail(&s_early, ph ^ 1, &s_fail)) break;
-                with_state(kQ, at + kTileBytes, PP, 0);
-                with_state(kQ, at + kTileBytes, PP, 1);
-                la::mma_commit(&s_q);
-            }
-            if (!wait_or_fail(&s_x, ph, &s_fail)) break;
-            la::tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < 4; s++) la::mma_ts(tm + kD3, tm + kX + 8 * s, la::smem_desc(M + s * 32), d2, s > 0);  // hi [hi; lo]
-#pragma unroll
-            for (int s = 0; s < 4; s++) la::mma_ts(tm + kD3 + 64, tm + kX + 32 + 8 * s, la::smem_desc(M + s * 32), dP, true);  // lo hi
-            la::mma_commit(&s_d2);
-            if (!wait_or_fail(&s_u, ph, &s_fail)) break;
-            la::tc_fence_after();
-#pragma unroll
-            for (int n = 0; n < NB; n++) {
-#pragma unroll
-                for (int part = 1; part >= 0; part--)
-#pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        la::mma_ts(tm + kD3 + 64 * n, tm + kX + part * 32 + 8 * s, la::smem_desc(at + n * L::block + s * 2048), d3, part < 1 || s > 0);
-                la::mma_commit(&s_d3[n]);
-            }
-            if (NB == 1) la::mma_commit(&s_d3[1]);
-            if (OUT) {
-                if (!wait_or_fail(&s_uy, ph, &s_fail) || (ch > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail))) break;
+        } else if (role == 0) {  // products
+            // (a product takes as long with 128 columns of the right operand as with 64: its left operand is read either way)
+            for (int ch = 0; ch < steps; ch++) {
+                const uint32_t ph = ch & 1;
+                const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
+                constexpr uint32_t d1 = la::mma_desc<__half>(128, OUT ? 2 * C : C, false, false), d2 = la::mma_desc<__half>(128, 2 * C, false, false),
+                                   dP = la::mma_desc<__half>(128, C, false, false), d3 = la::mma_desc<__half>(128, 64 * NB, false, true);
+                if (!warp_wait(&s_full[ph], (ch >> 1) & 1, &s_fail)) break;
+                // U of the chunk before has left its columns, and so has Q's product
+                if (!SUM && ch > 0 && !warp_wait(OUT ? &s_y : &s_late, ph ^ 1, &s_fail)) break;
+                if (OUT && ch > 0 && !warp_wait(&s_early, ph ^ 1, &s_fail)) break;
+                if (!warp_wait(&s_s, ph, &s_fail)) break;
                 la::tc_fence_after();
+                if (elect()) {
 #pragma unroll
-                for (int o = PP > 1 ? 0 : 2; o < 3; o++)  // lo hi, hi lo, hi hi
+                    for (int part = 1; part >= 0; part--)
 #pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        la::mma_ts(tm + kY, tm + kD1 + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(P + (o == 1 ? kTileBytes : 0) + s * 32), dP,
-                                   o > (PP > 1 ? 0 : 2) || s > 0);
-                la::mma_commit(&s_y);
+                        for (int s = 0; s < 4 * NB; s++)
+                            la::mma_ts(tm + kD1, tm + kS + part * 32 * NB + 8 * s, la::smem_desc(at + (s >> 2) * L::block + (s & 3) * 32), d1, part < 1 || s > 0);
+                    la::mma_commit(&s_d1);
+                }
+                if (!warp_wait(&s_x, ph, &s_fail)) break;
+                la::tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int s = 0; s < 4; s++) la::mma_ts(tm + kD3, tm + kX + 8 * s, la::smem_desc(M + s * 32), d2, s > 0);  // hi [hi; lo]
+#pragma unroll
+                    for (int s = 0; s < 4; s++) la::mma_ts(tm + kD3 + 64, tm + kX + 32 + 8 * s, la::smem_desc(M + s * 32), dP, true);  // lo hi
+                    la::mma_commit(&s_d2);
+                }
+                if (!warp_wait(&s_u, ph, &s_fail)) break;
+                la::tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int part = 1; part >= 0; part--)
+#pragma unroll
+                        for (int s = 0; s < 4; s++)
+                            la::mma_ts(tm + kD3, tm + kX + part * 32 + 8 * s, la::smem_desc(at + s * 2048, L::block), d3, part < 1 || s > 0);
+                    la::mma_commit(&s_d3);
+                }
+                if (OUT) {
+                    if (!warp_wait(&s_uy, ph, &s_fail) || (ch > 0 && !warp_wait(&s_late, ph ^ 1, &s_fail))) break;
+                    la::tc_fence_after();
+                    if (elect()) {
+#pragma unroll
+                        for (int o = PP > 1 ? 0 : 2; o < 3; o++)  // lo hi, hi lo, hi hi
+#pragma unroll
+                            for (int s = 0; s < 4; s++)
+                                la::mma_ts(tm + kY, tm + kD1 + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(P + (o == 1 ? kTileBytes : 0) + s * 32), dP,
+                                           o > (PP > 1 ? 0 : 2) || s > 0);
+                        la::mma_commit(&s_y);
+                    }
+                }
             }
-        }
         }
     }
     __syncwarp();
-    uint64_t* const bars[8] = {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3[0], &s_d3[1], &s_q, &s_y};
+    uint64_t* const bars[6] = {&s_full[0], &s_full[1], &s_d1, &s_d2, &s_d3, &s_y};
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
 
@@ -567,7 +555,7 @@ constexpr uint32_t bD1 = 0, bD0 = 64, bD3 = 128, bR = 256, bX = 384, bDq = 448;
 template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w, const TcBackArgs& r, int64_t id, char* sm) {
     constexpr int W = 32 * NB;
     using L = BackStage<NB>;
-    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r[2], s_d1, s_dq, s_x, s_d2, s_u, s_d3[2], s_dyq, s_xi, s_early, s_late;
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r, s_d1, s_dq, s_x, s_d2, s_u, s_d3, s_dyq, s_xi, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
     __shared__ float s_most[2][128], s_ud[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
     const Args& a = w.a;
@@ -576,9 +564,9 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
     const int64_t b = bh / a.H, h = bh % a.H, hq = h / (a.H / a.G), len = row_length(a, b);
     const int chunks = (int)((len + C - 1) / C);
     if (tid == 0) {
-        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3[0], &s_d3[1]}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&s_x, &s_u, &s_xi}) mbar_init(bar, kStateThreads / 32);
-        for (uint64_t* bar : {&s_r[0], &s_r[1], &s_dyq, &s_early, &s_late}) mbar_init(bar, 4);
+        for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&s_r, &s_x, &s_u, &s_xi}) mbar_init(bar, kStateThreads / 32);
+        for (uint64_t* bar : {&s_dyq, &s_early, &s_late}) mbar_init(bar, 4);
         for (uint64_t* bar : {&s_free[0], &s_free[1]}) mbar_init(bar, kStateThreads / 32 + 4);
         s_fail = 0;
         fence_proxy_async_smem();
@@ -586,7 +574,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
     if (warp == 0) la::tmem_alloc(&s_tm, 512);
     __syncthreads();
     la::tc_fence_after();
-    const uint32_t tm = s_tm, my = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tm = __shfl_sync(kFull, s_tm, 0), my = (uint32_t)((warp & 3) * 32) << 16;
     char* staging = sm + 2 * L::bytes;
     auto chunk_of = [&](int i) { return chunks - 1 - i; };
     const int64_t images = (bh * ptiles + pt) * w.chunks;
@@ -612,7 +600,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const float rs = scale_of(bound), dy_inv = r.dy_inv[images + chunk_of(i)];
-            if (i > 0) ok = ok && wait_or_fail(&s_early, ph ^ 1, &s_fail);
+            if (i > 0) ok = ok && wait(&s_early, ph ^ 1, &s_fail);
             if (half == 0) s_rs[ph][pl] = rs;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
@@ -620,13 +608,13 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 put2(to, to + 32 * NB, R + 32 * c, rs);
             }
             la::tmem_wait_st();
-            arrive(&s_r[half]);
+            arrive(&s_r);
             s_most[half][pl] = max_abs<W>(R);
             pair_sync();
             const float r_most = max_over(s_most);
-            ok = ok && wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail);
+            ok = ok && wait(&s_full[ph], (i >> 1) & 1, &s_fail);
             const float k_most = 16384.0f * head->inv_k, inv1 = head->inv_k / rs;
-            ok = ok && wait_or_fail(&s_d1, ph, &s_fail);  // D0 and D1
+            ok = ok && wait(&s_d1, ph, &s_fail);  // D0 and D1
             la::tc_fence_after();
             const float inv0 = a.scale * head->inv_p * dy_inv;
             float x[32], d[32];
@@ -650,7 +638,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             la::tmem_wait_st();
             arrive(&s_x);
             // Dq, while D2 is on its way
-            ok = ok && wait_or_fail(&s_dq, ph, &s_fail);
+            ok = ok && wait(&s_dq, ph, &s_fail);
             la::tc_fence_after();
             const float by = head->by, keep = head->weak ? 1.0f : 0.0f, dqs = s_dqs[ph][pl], invq = head->inv_q / dqs;
 #pragma unroll
@@ -665,7 +653,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 }
             }
             const float inv2 = head->inv_m / xs;
-            ok = ok && wait_or_fail(&s_d2, ph, &s_fail);
+            ok = ok && wait(&s_d2, ph, &s_fail);
             la::tc_fence_after();
             la::tmem_ld32(tm + my + bD0 + 32 * half, x);
 #pragma unroll
@@ -699,7 +687,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 la::tmem_wait_st();
                 arrive(&s_xi);
             }
-            ok = ok && wait_or_fail(&s_d3[half], ph, &s_fail);
+            ok = ok && wait(&s_d3, ph, &s_fail);
             la::tc_fence_after();
             arrive(&s_free[ph]);
 #pragma unroll
@@ -729,7 +717,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const float dy_scale = a.scale * r.dy_inv[image];
-            wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail);
+            wait(&s_full[ph], (i >> 1) & 1, &s_fail);
             auto scaled = [&](int hf, float (&z)[32]) {  // scale e^c dY of 32 tokens
 #pragma unroll
                 for (int u = 0; u < 4; u++) {
@@ -750,7 +738,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 arrive(&s_free[ph]);
                 const float dqs = scale_of(fmaxf(max_abs<32>(z[0]), max_abs<32>(z[1])));
                 s_dqs[ph][pl] = dqs;
-                if (i > 0) wait_or_fail(&s_dq, ph ^ 1, &s_fail);  // the last parts are used
+                if (i > 0) wait(&s_dq, ph ^ 1, &s_fail);  // the last parts are used
                 la::tc_fence_after();
                 put2(tm + my + bDq, tm + my + bDq + 32, z[0], dqs);
                 put2(tm + my + bDq + 16, tm + my + bDq + 48, z[1], dqs);
@@ -758,8 +746,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             la::tmem_wait_st();
             arrive(&s_dyq);
             // R's and X's parts under one scale each: what the largest channel's is
-            wait_or_fail(&s_r[0], ph, &s_fail);
-            wait_or_fail(&s_r[1], ph, &s_fail);
+            wait(&s_r, ph, &s_fail);
             la::tc_fence_after();
             uint32_t x[32], z[32];
             float own = s_rs[ph][pl], all = group_min(own, s_red, 5);
@@ -771,7 +758,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 if (c == 2 * NB - 1) arrive(&s_early);
                 ring.put(x, f, r.states + image * state_bytes(NB) + c * kPieceBytes);
             }
-            wait_or_fail(&s_xi, ph, &s_fail);
+            wait(&s_xi, ph, &s_fail);
             la::tc_fence_after();
             own = s_xsc[ph][pl], all = group_min(own, s_red, 5);
             f = pack2<__half>(all / own, all / own);
@@ -785,9 +772,10 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
         if (first) la::bulk_wait_all();
     } else {
         leave_regs<56>();
-        if (tid == kThreads - 96) {  // loads
+        const int role = __shfl_sync(kFull, warp, 0) - (kThreads - 128) / 32, steps = __shfl_sync(kFull, chunks, 0);
+        if (role == 1 && (tid & 31) == 0) {  // loads
             for (int i = 0; i < chunks; i++) {
-                if (i > 1 && !wait_or_fail(&s_free[i & 1], ((i >> 1) + 1) & 1, &s_fail)) break;
+                if (i > 1 && !wait(&s_free[i & 1], ((i >> 1) + 1) & 1, &s_fail)) break;
                 char* at = sm + (i & 1) * L::bytes;
                 uint64_t* bar = &s_full[i & 1];
                 const int ch = chunk_of(i);
@@ -796,67 +784,67 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 bulk_load(at + L::dy, r.dys + (images + ch) * kPieceBytes, kPieceBytes, bar);
                 bulk_load(at + L::image, w.images + (bh * w.chunks + ch) * image_bytes(2), 4 * kTileBytes + (int)sizeof(ImageHead), bar);
             }
-        } else if (tid == kThreads - 128) {  // products
-            for (int i = 0; i < chunks; i++) {
+        } else if (role == 0) {  // products
+            for (int i = 0; i < steps; i++) {
                 const uint32_t ph = i & 1;
                 const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
-                constexpr uint32_t dK = la::mma_desc<__half>(128, C, false, false), dR = la::mma_desc<__half>(128, C, false, true);
-                if (!wait_or_fail(&s_full[ph], (i >> 1) & 1, &s_fail)) break;
-                if (i > 0 && !wait_or_fail(&s_u, ph ^ 1, &s_fail)) break;  // D2 is read
+                constexpr uint32_t dK = la::mma_desc<__half>(128, C, false, false), dR = la::mma_desc<__half>(128, C, false, true),
+                                   dN = la::mma_desc<__half>(128, 64 * NB, false, true);
+                if (!warp_wait(&s_full[ph], (i >> 1) & 1, &s_fail)) break;
+                if (i > 0 && !warp_wait(&s_u, ph ^ 1, &s_fail)) break;  // D2 is read
                 la::tc_fence_after();
+                if (elect()) {
 #pragma unroll
                 for (int part = 1; part >= 0; part--)
 #pragma unroll
                     for (int s = 0; s < 4; s++)
                         la::mma(tm + bD0, la::smem_desc(at + L::dy + s * 32), la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
-                if (i > 0 && !wait_or_fail(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
-#pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    if (!wait_or_fail(&s_r[half], ph, &s_fail)) break;
-                    la::tc_fence_after();
+                }
+                if (i > 0 && !warp_wait(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
+                if (!warp_wait(&s_r, ph, &s_fail)) break;
+                la::tc_fence_after();
+                if (elect()) {
 #pragma unroll
                     for (int part = 1; part >= 0; part--)
 #pragma unroll
-                        for (int e = 0; e < 2 * NB; e++) {
-                            const int s = half * 2 * NB + e;
-                            la::mma_ts(tm + bD1, tm + bR + part * 32 * NB + 8 * s, la::smem_desc(at + (s >> 2) * L::block + (s & 3) * 32), dK,
-                                       half > 0 || part < 1 || e > 0);
-                        }
+                        for (int s = 0; s < 4 * NB; s++)
+                            la::mma_ts(tm + bD1, tm + bR + part * 32 * NB + 8 * s, la::smem_desc(at + (s >> 2) * L::block + (s & 3) * 32), dK, part < 1 || s > 0);
+                    la::mma_commit(&s_d1);
                 }
-                la::mma_commit(&s_d1);
-                if (!wait_or_fail(&s_dyq, ph, &s_fail)) break;
+                if (!warp_wait(&s_dyq, ph, &s_fail)) break;
                 la::tc_fence_after();
-                auto update = [&](uint32_t left, uint32_t keys, int n) {  // 64 of the states, two parts
+                auto update = [&](uint32_t left, uint32_t keys) {  // two parts
 #pragma unroll
                     for (int part = 1; part >= 0; part--)
 #pragma unroll
                         for (int s = 0; s < 4; s++)
-                            la::mma_ts(tm + bD3 + 64 * n, tm + left + part * 32 + 8 * s, la::smem_desc(keys + n * L::block + s * 2048), dR, part < 1 || s > 0);
+                            la::mma_ts(tm + bD3, tm + left + part * 32 + 8 * s, la::smem_desc(keys + s * 2048, L::block), dN, part < 1 || s > 0);
                 };
-#pragma unroll
-                for (int n = 0; n < NB; n++) update(bDq, at + kTileBytes, n);
-                la::mma_commit(&s_dq);
-                if (!wait_or_fail(&s_x, ph, &s_fail)) break;
+                if (elect()) {
+                    update(bDq, at + kTileBytes);
+                    la::mma_commit(&s_dq);
+                }
+                if (!warp_wait(&s_x, ph, &s_fail)) break;
                 la::tc_fence_after();
+                if (elect()) {
 #pragma unroll
                 for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
                     for (int s = 0; s < 4; s++)
                         la::mma_ts(tm + bD0, tm + bX + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(M + (o == 1 ? kTileBytes : 0) + s * 2048), dR, o > 0 || s > 0);
                 la::mma_commit(&s_d2);
-                if (!wait_or_fail(&s_u, ph, &s_fail)) break;
-                la::tc_fence_after();
-#pragma unroll
-                for (int n = 0; n < NB; n++) {
-                    update(bX, at, n);
-                    la::mma_commit(&s_d3[n]);
                 }
-                if (NB == 1) la::mma_commit(&s_d3[1]);
+                if (!warp_wait(&s_u, ph, &s_fail)) break;
+                la::tc_fence_after();
+                if (elect()) {
+                    update(bX, at);
+                    la::mma_commit(&s_d3);
+                }
             }
         }
     }
     __syncwarp();
-    uint64_t* const bars[7] = {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3[0], &s_d3[1]};
+    uint64_t* const bars[6] = {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3};
     la::end_block(&s_fail, w.status, bars, tm, 512);
 }
 
@@ -909,7 +897,7 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
         if (k + 1 == K) break;
         __syncthreads();  // (the Phi before is used)
         if (tid == 0 && k + 2 < K) load(k + 1);
-        wait_or_fail(&s_full[k & 1], (k >> 1) & 1, &s_fail);
+        wait(&s_full[k & 1], (k >> 1) & 1, &s_fail);
         const float* f = phi + (k & 1) * N * N;
         float2 y[4][kCarryCols / 2] = {};  // rows 4 lane ..
         if (4 * lane < N)
