@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     }
     __syncwarp();
     // K and Q as f16: unit tid + 128 i of the 512 of each tile
-    float scale_k, scale_q;
+    float scale_k, scale_q, most_k, most_q;
     {
         uint4 x[2][4 * NB];
         float most[2] = {};
@@ -266,8 +266,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
             if (lane == 0) s_max[side][warp] = m;
         }
         __syncthreads();
-        scale_k = la::f16_scale(max4(s_max[0]));
-        scale_q = la::f16_scale(max4(s_max[1]));
+        most_k = max4(s_max[0]);
+        most_q = max4(s_max[1]);
+        scale_k = la::f16_scale(most_k);
+        scale_q = la::f16_scale(most_q);
         char* keys = w.keys + ((b * w.chunks + chunk) * a.G + gq) * (NB * 16384);
         if (split == 0)
 #pragma unroll
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 head->c[tid] = make_float2(c.h, c.l);
             }
             __syncthreads();
-            const float scale_p = la::f16_scale(fmaxf(s_max[0][2], s_max[0][3]));
+            const float most_p = fmaxf(s_max[0][2], s_max[0][3]), scale_p = la::f16_scale(most_p);
             if (is_q) {
                 char* hi = I + 2 * kTileBytes;
 #pragma unroll
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 most = warp_max(most);
                 if (lane == 0) s_max[1][warp] = most;
                 __syncthreads();
-                const float scale_m = la::f16_scale(max4(s_max[1]));
+                const float most_m = max4(s_max[1]), scale_m = la::f16_scale(most_m);
                 put_parts(I, I + kTileBytes, i, j0 / 8, x, scale_m);
                 put_parts(I, I + kTileBytes, i, j0 / 8 + 2, x + 16, scale_m);
                 if (tid == 0) {
@@ -366,6 +368,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                     head->inv_q = 1.0f / scale_q;
                     head->inv_m = 1.0f / scale_m;
                     head->inv_p = 1.0f / scale_p;
+                    head->most_k = most_k;
+                    head->most_q = most_q;
+                    head->most_p = most_p;
+                    head->most_m = most_m;
                 }
             }
             fence_proxy_async_smem();
@@ -427,7 +433,7 @@ template <typename T> __global__ void __launch_bounds__(256) k_dy(Args a, int64_
         for (int e = 0; e < 4; e++) x[e] = pack2<__half>(scale * ldf(&s[8 * u + 2 * e][p]), scale * ldf(&s[8 * u + 2 * e + 1][p]));
         *reinterpret_cast<uint4*>(to + at * 16) = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    if (tid == 0) dy_inv[blockIdx.x] = 1.0f / scale;
+    if (tid == 0) dy_inv[blockIdx.x] = most == 0.0f ? 0.0f : 1.0f / scale;  // (zeros bound nothing)
 }
 
 template <typename T, int NB, int PARTS> cudaError_t prep_go(const PrepArgs& w, cudaStream_t st) {

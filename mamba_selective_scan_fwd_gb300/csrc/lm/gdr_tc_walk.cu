@@ -150,7 +150,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
     // landed; stage free; S; D1; X; D2; e U; D3; U; U^T P^T; read by the third warpgroup: early, late
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_uy, s_y, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
-    __shared__ float s_most[2][2][128], s_ud[2][128], s_ss[2][128], s_us[2][128];
+    __shared__ float s_most[2][2][128], s_ud[2][128], s_um[2][128], s_ss[2][128], s_us[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pl = tid & 127;
     const bool phi = SUM && blockIdx.y == 1;
@@ -197,7 +197,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         }
         // (a wait that ran out ends no loop here: the others wait at its barriers)
         // Scales come from bounds that are known before they are needed: the largest values of S and beta V, which
-        // the channel's two threads exchange while a product runs, |k| <= 2^14 inv_k and |M| <= 2^14 inv_m.  Only e U's is
+        // the channel's two threads exchange while a product runs, and the largest of K and M.  Only e U's is
         // its own largest value: under strong decays that is what is left of the state.
         auto pair_sync = [&] { named_sync(1 + (warp & 3), 64); };
         auto max_over = [&](const float (&m)[2][128]) { return fmaxf(m[0][pl], m[1][pl]); };
@@ -255,7 +255,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             la::tmem_wait_st();
             arrive(&s_s);
             values(ch);
-            const float inv1 = -head->inv_k / ss, k_most = 16384.0f * head->inv_k;
+            const float inv1 = -head->inv_k / ss, k_most = head->most_k;
             const float x_bound = fmaf(head->most_bu * (64 * NB) * k_most, bound, x_most), xs = scale_of(x_bound);
             ok = ok && wait(&s_d1, ph, &s_fail);
             la::tc_fence_after();
@@ -314,7 +314,15 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             bound = fmaf(64.0f * k_most, ud_most, max_over(s_most[0]) * (keep + fabsf(by)));
             arrive(&s_u);
             if (!SUM) {
-                const float uy = scale_of(64.0f * 16384.0f * head->inv_m * x_bound);
+                // U's image is what the backward sums products of: its own largest value, off the chain.  For y the bound
+                // of a bound does: parts of f16 keep 22 bits of rows that are 2^14 below theirs.
+                float most = 64.0f * head->most_m * x_bound;
+                if (KEEP) {
+                    s_um[half][pl] = max_abs<32>(x);
+                    pair_sync();
+                    most = max_over(s_um);
+                }
+                const float uy = scale_of(most);
                 if (half == 0) s_us[ph][pl] = uy;
                 const uint32_t to = tm + my + kD1 + 16 * half;
                 if (KEEP || PP > 1) put2(to, to + 32, x, uy);
@@ -557,7 +565,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
     using L = BackStage<NB>;
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r, s_d1, s_dq, s_x, s_d2, s_u, s_d3, s_dyq, s_xi, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
-    __shared__ float s_most[2][128], s_ud[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
+    __shared__ float s_most[2][128], s_ud[2][128], s_xm[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, warp = tid >> 5, pl = tid & 127;
     const int64_t ptiles = (a.P + kTileP - 1) / kTileP, pt = id % ptiles, p0 = pt * kTileP, bh = id / ptiles;
@@ -613,7 +621,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             pair_sync();
             const float r_most = max_over(s_most);
             ok = ok && wait(&s_full[ph], (i >> 1) & 1, &s_fail);
-            const float k_most = 16384.0f * head->inv_k, inv1 = head->inv_k / rs;
+            const float k_most = head->most_k, inv1 = head->inv_k / rs;
             ok = ok && wait(&s_d1, ph, &s_fail);  // D0 and D1
             la::tc_fence_after();
             const float inv0 = a.scale * head->inv_p * dy_inv;
@@ -629,7 +637,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 x[j + 2] = z.x;
                 x[j + 3] = z.y;
             }
-            const float x_bound = fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * 16384.0f * head->inv_p * (16384.0f * dy_inv)),
+            const float x_bound = fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * head->most_p * (16384.0f * dy_inv)),
                         xs = scale_of(x_bound);
             {
                 const uint32_t to = tm + my + bX + 16 * half;
@@ -677,10 +685,12 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 put2(to, to + 32, d, us);
             }
             la::tmem_wait_st();
-            bound = fmaf(64.0f * k_most, ud_most, fmaf(64.0f * 16384.0f * head->inv_q, 16384.0f / dqs, r_most * (keep + fabsf(by))));
+            bound = fmaf(64.0f * k_most, ud_most, fmaf(64.0f * head->most_q, 16384.0f / dqs, r_most * (keep + fabsf(by))));
             arrive(&s_u);
             {
-                const float xi = scale_of(64.0f * 16384.0f * head->inv_m * x_bound);
+                s_xm[half][pl] = max_abs<32>(x);
+                pair_sync();
+                const float xi = scale_of(max_over(s_xm));
                 if (half == 0) s_xsc[ph][pl] = xi;
                 const uint32_t to = tm + my + bD1 + 16 * half;
                 put2(to, to + 32, x, xi);
