@@ -99,8 +99,11 @@ struct NormArgs {
     float eps;
     int flags, dtype;
 };
-// Blocks of each side; a pure function of its arguments.
-int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N, bool backward);
+// Blocks of a side with `heads` heads beside `others` of the other: its part of what fits the SMs at once (a further
+// block would wait for one of them to end), no more than there is work for (16 rows of 128 channels a block).  With
+// kNormBlocks, the most that a launch takes, it sizes the workspace.
+constexpr int kNormBlocks = 8;
+int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t others, int64_t N, int64_t per_sm);
 cudaError_t launch_qknorm(const NormArgs& a, bool backward, cudaStream_t st);
 
 }  // namespace gdr

@@ -454,7 +454,7 @@ int ss_qknorm_fwd(const ss_qknorm_fwd_desc* d, void* stream) {
 
 size_t ss_qknorm_bwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t Hq, int64_t Hk, int64_t N, int dtype) {
     if (check_norm(Bsz, L, Hq, Hk, N, 0, 0.0f, 0, dtype) != SS_OK || empty(Bsz, L)) return 0;
-    return (size_t)(norm_blocks(Bsz * L, Hq, N, true) + norm_blocks(Bsz * L, Hk, N, true)) * N * 4;
+    return (size_t)(norm_blocks(Bsz * L, Hq, Hk, N, kNormBlocks) + norm_blocks(Bsz * L, Hk, Hq, N, kNormBlocks)) * N * 4;
 }
 
 int ss_qknorm_bwd(const ss_qknorm_bwd_desc* d, void* stream) {

@@ -10,6 +10,12 @@
 // memory, used by all heads; position * frequency is reduced to a fraction of a turn by a
 // 64-bit product (the frequency as a fraction of 2^64 turns a token), which keeps the
 // angle to 2^-32 turns wherever the frequency's own rounding allows.
+//
+// A row's loads are on their way while the row before it is worked on, over the tiles' ends too: the next
+// tile's tables are made first.  Measured: 4 x 4096 tokens, 16 + 16 heads of 128, 64 channels turned: 48 us, copying 40
+// (tables and loads begun anew at each tile: 55); backward of half of it 41 + 3, three streams at the copy rate 30
+// (50 + 6): 123 registers let two blocks of 256 fit an SM, and the same with 64 registers and runs of half the width
+// takes 57.  All 128 channels turned: 29 us for 20 of copying; few heads a token: bound by the angles.
 #include "../simd.cuh"
 #include "gdr_dev.cuh"
 #include "ss_gdr.h"
@@ -20,8 +26,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint64_t kNoAngle = ~0ull;  // a frequency that is not finite (fractions end at 2^64 - 2^11)
-constexpr int kTable = 2048;  // angles a tile of tokens may need (16 KB)
-constexpr int kTile = 256;    // tokens of a tile at most
+constexpr int kTable = 1024;  // angles a tile of tokens may need (8 KB)
+constexpr int kTile = 128;    // tokens of a tile at most
 
 template <typename T, int V> struct Run {  // V values moved at once
     using M = typename std::conditional<sizeof(T) * V == 16, uint4, typename std::conditional<sizeof(T) * V == 8, uint2, T>::type>::type;
@@ -50,8 +56,10 @@ template <typename T, int V> __device__ __forceinline__ void put(T* p, const flo
 template <typename T, int V, int LPR, int SPT, bool BWD>
 __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, int64_t blocks_q) {
     constexpr int RPB = kThreads / LPR;  // rows at once
-    __shared__ float2 s_turn[kTable];
-    __shared__ int64_t s_at[BWD ? 2 : 1][kTile];  // where each token of the tile begins in x (and in d)
+    // three tiles' tables: of the one in work, of the next (its rows are fetched before this one's end), and of the one
+    // before, which slower warps may still read.  One barrier a tile.
+    __shared__ float2 s_turn[3][kTable];
+    __shared__ int64_t s_at[3][BWD ? 2 : 1][kTile];  // where each token of the tile begins in x (and in d)
     __shared__ uint64_t s_freq[la::kMaxN];
     __shared__ float s_dw[BWD ? 2 * V * SPT * kThreads : 1];
     const int sd = blockIdx.x >= blocks_q;
@@ -114,46 +122,60 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
     struct Raw {
         M x[SPT][2], d[BWD ? SPT : 1][2];
     };
-    for (int64_t t0 = block * tile; t0 < tokens; t0 += blocks * tile) {
-        const int nt = (int)min(tile, tokens - t0), rows = nt * heads;
-        __syncthreads();
+    auto tables = [&](int at, int64_t t0) {
+        const int nt = (int)min(tile, tokens - t0);
+        const int64_t b0 = t0 / a.L, first = t0 - b0 * a.L;  // (divisions of 64 bits: once a tile)
         for (int i = tid; i < nt; i += kThreads) {
-            const int64_t b = (t0 + i) / a.L, tb = t0 + i - b * a.L;
-            s_at[0][i] = b * z.x.batch + tb * z.x.token;
-            if (BWD) s_at[BWD][i] = b * z.d.batch + tb * z.d.token;
+            const int64_t over = first + i >= a.L ? (a.L >= tile ? 1 : (first + i) / a.L) : 0;
+            const int64_t b = b0 + over, tb = first + i - over * a.L;
+            s_at[at][0][i] = b * z.x.batch + tb * z.x.token;
+            if (BWD) s_at[at][BWD][i] = b * z.d.batch + tb * z.d.token;
         }
         for (int i = tid; i < nt * pairs; i += kThreads) {
-            const int64_t t = t0 + i / pairs;
-            const int64_t pos = a.positions ? (int64_t)a.positions[t] : t % a.L;
-            const uint64_t f = s_freq[i % pairs];
+            const int tl = i / pairs;
+            int64_t pos = first + tl;
+            if (a.positions) pos = a.positions[t0 + tl];
+            else if (pos >= a.L) pos = a.L >= tile ? pos - a.L : pos % a.L;
+            const uint64_t f = s_freq[i - tl * pairs];
             const float part = (float)(int32_t)(((uint64_t)pos * f + 0x80000000ull) >> 32) * 4.656612873077393e-10f;  // half turns
             float sn, cs;
             sincospif(part, &sn, &cs);
-            s_turn[i] = f == kNoAngle ? make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)) : make_float2(cs, sn);
+            s_turn[at][i] = f == kNoAngle ? make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)) : make_float2(cs, sn);
         }
-        __syncthreads();
-        auto fetch = [&](int r, Raw& raw) {  // a row's runs on their way
-            const int tl = r < rows ? r / heads : 0, h = r < rows ? r - tl * heads : 0;
-            const T* xp = static_cast<const T*>(z.x.p) + s_at[0][tl] + (int64_t)h * N;
-            const T* dp = BWD ? static_cast<const T*>(z.d.p) + s_at[BWD][tl] + (int64_t)h * N : nullptr;
+    };
+    auto fetch = [&](int at, int tl, int h, bool have, Raw& raw) {  // a row's runs on their way
+        const T* xp = static_cast<const T*>(z.x.p) + (have ? s_at[at][0][tl] + (int64_t)h * N : 0);
+        const T* dp = BWD ? static_cast<const T*>(z.d.p) + (have ? s_at[at][BWD][tl] + (int64_t)h * N : 0) : nullptr;
 #pragma unroll
-            for (int s = 0; s < SPT; s++) {
-                raw.x[s][0] = raw.x[s][1] = M{};
-                if (on[s]) raw.x[s][0] = *reinterpret_cast<const M*>(xp + ia[s]);
-                if (onb[s]) raw.x[s][1] = *reinterpret_cast<const M*>(xp + ib[s]);
-                if (BWD) {
-                    raw.d[BWD ? s : 0][0] = raw.d[BWD ? s : 0][1] = M{};
-                    if (on[s]) raw.d[BWD ? s : 0][0] = *reinterpret_cast<const M*>(dp + ia[s]);
-                    if (onb[s]) raw.d[BWD ? s : 0][1] = *reinterpret_cast<const M*>(dp + ib[s]);
-                }
+        for (int s = 0; s < SPT; s++) {
+            raw.x[s][0] = raw.x[s][1] = M{};
+            if (have && on[s]) raw.x[s][0] = *reinterpret_cast<const M*>(xp + ia[s]);
+            if (have && onb[s]) raw.x[s][1] = *reinterpret_cast<const M*>(xp + ib[s]);
+            if (BWD) {
+                raw.d[BWD ? s : 0][0] = raw.d[BWD ? s : 0][1] = M{};
+                if (have && on[s]) raw.d[BWD ? s : 0][0] = *reinterpret_cast<const M*>(dp + ia[s]);
+                if (have && onb[s]) raw.d[BWD ? s : 0][1] = *reinterpret_cast<const M*>(dp + ib[s]);
             }
-        };
-        Raw next;
-        fetch(slot, next);
+        }
+    };
+    const int tl0 = slot / heads, h0 = slot - tl0 * heads, dt = RPB / heads, dh = RPB - dt * heads;
+    Raw next;
+    int at = 0;
+    __syncthreads();  // the frequencies
+    if (block * tile < tokens) {
+        tables(0, block * tile);
+        __syncthreads();
+        fetch(0, tl0, h0, tl0 < min(tile, tokens - block * tile), next);
+    }
+    for (int64_t t0 = block * tile; t0 < tokens; t0 += blocks * tile) {
+        const int nt = (int)min(tile, tokens - t0), rows = nt * heads;
+        const int64_t t1 = t0 + blocks * tile;
+        const int nt1 = (int)max((int64_t)0, min(tile, tokens - t1)), at1 = at == 2 ? 0 : at + 1;
+        if (nt1 > 0) tables(at1, t1);
+        __syncthreads();
+        int tl = tl0, h = h0;
         for (int r0 = 0; r0 < rows; r0 += RPB) {
-            const int r = r0 + slot;
-            const bool have = r < rows;
-            const int tl = have ? r / heads : 0, h = have ? r - tl * heads : 0;
+            const bool have = tl < nt;
             const int64_t t = t0 + tl;
             float x[SPT][2][V], d[SPT][2][V];
             float sum = 0.0f;
@@ -164,7 +186,15 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
                     widen<T, V>(next.x[s][c], x[s][c]);
                     if (BWD) widen<T, V>(next.d[BWD ? s : 0][c], d[s][c]);
                 }
-            if (r0 + RPB < rows) fetch(r + RPB, next);
+            const int now = tl, head = h;
+            h += dh;
+            tl += dt;
+            if (h >= heads) {
+                h -= heads;
+                tl++;
+            }
+            if (r0 + RPB < rows) fetch(at, tl, h, tl < nt, next);
+            else fetch(at1, tl0, h0, tl0 < nt1, next);
 #pragma unroll
             for (int s = 0; s < SPT; s++)
 #pragma unroll
@@ -172,8 +202,8 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
             const float rs = rsqrtf(fmaf(sum, inv, a.eps));
-            const float2* cs = s_turn + tl * pairs;
-            T* op = static_cast<T*>(z.out) + (t * heads + h) * N;
+            const float2* cs = s_turn[at] + (have ? now * pairs : 0);
+            T* op = static_cast<T*>(z.out) + (t * heads + head) * N;
             if (!BWD) {
 #pragma unroll
                 for (int s = 0; s < SPT; s++) {
@@ -215,6 +245,7 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
                 }
             }
         }
+        at = at1;
     }
     if (BWD && z.dweight) {  // the block's sum over its rows, slots in order
         __syncthreads();
@@ -268,19 +299,20 @@ int64_t tile_tokens(int64_t heads, int64_t pairs, int lanes) {
     return t < 1 ? 1 : t;
 }
 
-template <typename T, int V, int LPR, int SPT> cudaError_t launch(const NormArgs& a, bool bwd, cudaStream_t st) {
-    const int64_t tokens = a.Bsz * a.L, bq = norm_blocks(tokens, a.side[0].heads, a.N, bwd), bk = norm_blocks(tokens, a.side[1].heads, a.N, bwd);
-    const int64_t most = a.side[0].heads > a.side[1].heads ? a.side[0].heads : a.side[1].heads;
-    const int64_t tile = tile_tokens(most, a.pairs, LPR);
-    const unsigned grid = (unsigned)(bq + bk);
-    if (!bwd) {
-        k_qknorm<T, V, LPR, SPT, false><<<grid, kThreads, 0, st>>>(a, tile, bq);
-        return cudaGetLastError();
-    }
-    k_qknorm<T, V, LPR, SPT, true><<<grid, kThreads, 0, st>>>(a, tile, bq);
-    if (a.side[0].dweight || a.side[1].dweight)
+template <typename T, int V, int LPR, int SPT, bool BWD> cudaError_t launch(const NormArgs& a, cudaStream_t st) {
+    static const int fit = [] {
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_qknorm<T, V, LPR, SPT, BWD>, kThreads, 0) == cudaSuccess && n > 0 ? n : 1;
+    }();
+    const int64_t tokens = a.Bsz * a.L, hq = a.side[0].heads, hk = a.side[1].heads, per_sm = fit < kNormBlocks ? fit : kNormBlocks;
+    const int64_t bq = norm_blocks(tokens, hq, hk, a.N, per_sm), bk = norm_blocks(tokens, hk, hq, a.N, per_sm);
+    k_qknorm<T, V, LPR, SPT, BWD><<<(unsigned)(bq + bk), kThreads, 0, st>>>(a, tile_tokens(hq > hk ? hq : hk, a.pairs, LPR), bq);
+    if (BWD && (a.side[0].dweight || a.side[1].dweight))
         k_weights<<<dim3((unsigned)ceil_div(a.N, 32), 2), 1024, 0, st>>>(a, bq, bq + bk);
     return cudaGetLastError();
+}
+template <typename T, int V, int LPR, int SPT> cudaError_t launch(const NormArgs& a, bool bwd, cudaStream_t st) {
+    return bwd ? launch<T, V, LPR, SPT, true>(a, st) : launch<T, V, LPR, SPT, false>(a, st);
 }
 
 bool runs_of(const NormArgs& a, bool bwd, int64_t v, int64_t esz) {
@@ -312,12 +344,9 @@ template <typename T> cudaError_t launch_io(const NormArgs& a, bool bwd, cudaStr
 
 }  // namespace
 
-// No more blocks of a side than there is work for (a block's least: 16 rows of 128 channels), nor than eight an
-// SM; the backward's leave a part of the weights' gradients each, which one small kernel adds up, and two of them fit an
-// SM: two (2 x 4096 tokens, 16 + 16 heads of 128: that kernel takes PLACEHOLDER us, 20 with eight).
-int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t N, bool backward) {
-    const int64_t n = ceil_div(tokens * heads * N, 2048), most = (backward ? 2 : 8) * kSms;
-    return n < 1 ? 1 : (n > most ? most : n);
+int64_t norm_blocks(int64_t tokens, int64_t heads, int64_t others, int64_t N, int64_t per_sm) {
+    const int64_t n = ceil_div(tokens * heads * N, 2048), most = per_sm * kSms * heads / (heads + others);
+    return n < 1 || most < 1 ? 1 : (n > most ? most : n);
 }
 
 cudaError_t launch_qknorm(const NormArgs& a, bool bwd, cudaStream_t st) {

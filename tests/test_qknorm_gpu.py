@@ -133,3 +133,26 @@ def test_graph_stream_and_repeats(io):
     torch.cuda.synchronize()
     for o, e in ((out2, d2), (out3, d3)):
         assert all(torch.equal(a, b) for a, b in zip(o, out)) and all(torch.equal(e[n], d[n]) for n in d)
+
+
+# one head of 64 channels: 32 tokens a tile, 64 rows at once, so that slots without a row go through every tile; 60011
+# tokens: three tiles a block, all three tables.  700 rows of 7 tokens: tiles over several rows' ends, without positions
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 60011, 1, 1, 64, 32), (700, 7, 1, 2, 64, 16), (3, 5000, 1, 3, 32, 16), (900, 1, 4, 1, 80, 40)], ids=str)
+def test_many_tiles_a_block(shape, io):
+    x = inputs(*shape, weight=True, io=io, seed=5)
+    check(x, io)
+    B, L = shape[:2]
+    x["positions"] = torch.arange(L, dtype=torch.int32, device="cuda").repeat(B, 1)
+    (q, k), _ = check(x, io)
+    got = ss.ss_qknorm_fwd(x["q"], x["k"], x["qw"], x["kw"], freqs=x["freqs"])
+    assert torch.equal(got[0], q) and torch.equal(got[1], k)
+
+
+def test_in_place_over_many_tiles():
+    """Rows are read a tile ahead of the writes."""
+    x = inputs(2, 9000, 3, 2, 128, 32, True, "bf16", seed=6)
+    kw = dict(q_weight=x["qw"], k_weight=x["kw"], positions=x["positions"], freqs=x["freqs"])
+    q, k = ss.ss_qknorm_fwd(x["q"], x["k"], **kw)
+    ss.ss_qknorm_fwd(x["q"], x["k"], **kw, q_out=x["q"], k_out=x["k"])
+    assert torch.equal(x["q"], q) and torch.equal(x["k"], k)
