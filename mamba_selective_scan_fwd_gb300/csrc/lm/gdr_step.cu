@@ -19,8 +19,9 @@ template <int VEC> struct F;
 template <> struct F<4> { using T = float4; };
 template <> struct F<1> { using T = float; };
 
-template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128, LPR == 16 ? 4 : 0) k_step(StepArgs s) {
-    constexpr int RP = 128 / LPR;  // state rows the block touches at once
+template <typename T, int VEC, int LPR, int THREADS = 128>
+__global__ void __launch_bounds__(THREADS, VEC == 4 && LPR >= 16 ? 512 / THREADS : 0) k_step(StepArgs s) {
+    constexpr int RP = THREADS / LPR;  // state rows the block touches at once
     constexpr int NI = kMaxN / RP;
     constexpr int PT = LPR * VEC;
     __shared__ float s_q[kMaxN], s_k[kMaxN], s_qk[4];
@@ -53,12 +54,14 @@ template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128, L
         qn = ldf(static_cast<const T*>(s.q) + b * s.q_batch + hq * s.N + tid);
         kn = ldf(static_cast<const T*>(s.k) + b * s.k_batch + hq * s.N + tid);
     }
-    s_q[tid] = qn;
-    s_k[tid] = kn;
+    if (tid < kMaxN) {
+        s_q[tid] = qn;
+        s_k[tid] = kn;
+    }
     float qk = qn * kn;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(kFull, qk, o);
-    if ((tid & 31) == 0) s_qk[tid >> 5] = qk;
+    if ((tid & 31) == 0 && tid < kMaxN) s_qk[tid >> 5] = qk;
     const la::Decay a = la::decay_of(s.g ? la::clamp_g(s.g[b * s.H + h]) : 0.0f);
     const float beta = s.beta[b * s.H + h];
     __syncthreads();
@@ -84,7 +87,7 @@ template <typename T, int VEC, int LPR> __global__ void __launch_bounds__(128, L
         s_d[1][row][l * VEC + e] = dq[e];
     }
     __syncthreads();
-    for (int c = tid; c < PT; c += 128)
+    for (int c = tid; c < PT; c += THREADS)
         if (pt + c < s.P) {
             float k_s = 0.0f, q_s = 0.0f;
 #pragma unroll 8
@@ -117,7 +120,10 @@ template <typename T> cudaError_t step_io(const StepArgs& s, cudaStream_t st) {
     // rows of the state must be whole float4s (the pool itself is 16-byte aligned)
     if (s.P % 4 != 0) k_step<T, 1, 32><<<blocks(32), 128, 0, st>>>(s);
     else if (BH * ceil_div(s.P, 64) < kSms) k_step<T, 4, 4><<<blocks(16), 128, 0, st>>>(s);
-    else k_step<T, 4, 16><<<blocks(64), 128, 0, st>>>(s);
+    // 128 channels at once where they cost no idle lanes over 64: whole rows of 512 bytes (256 rows of 32 heads, N = P = 128:
+    // 174 us, 184 with 64, 192 with 32; copying 159)
+    else if (ceil_div(s.P, 64) % 2 == 1) k_step<T, 4, 16><<<blocks(64), 128, 0, st>>>(s);
+    else k_step<T, 4, 32, 256><<<blocks(128), 256, 0, st>>>(s);
     return cudaGetLastError();
 }
 
