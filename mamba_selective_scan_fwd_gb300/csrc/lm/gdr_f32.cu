@@ -115,7 +115,8 @@ template <typename T> __global__ void __launch_bounds__(128) k_pairs(Args a, Pai
 //   miss_t = v_t - e^{c_t} S^T k_t - sum_{j < t} e^{c_t - c_j} (k_t . k_j) u_j,   u_t = beta_t miss_t
 //   y_t = e^{c_t} S^T q_t + sum_{j <= t} e^{c_t - c_j} (q_t . k_j) u_j,   S <- e^{cl} S + sum_j e^{cl - c_j} k_j u_j^T
 // so that a chain of sums over the lanes is paid once for four tokens.  The backward's walk is the same from
-// the other end.  2 x 1000 tokens, 24 heads, N = P = 64: PLACEHOLDER us (token by token 228).
+// the other end.  2 x 1000 tokens, 24 heads, N = P = 64: 146 us beside 13 for the pairs' products (token by token 228;
+// with four interleaved chains of sums and q held in registers 149).
 template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void walk(const WalkArgs& w, int64_t id) {
     constexpr int NT = 64, NP = 16 * LN, PT = NT / LN, TT = kWalkT;
     struct Stage {

@@ -9,11 +9,16 @@
 //   D2 = X M^T = U^T         [128 x 2 x 64]  hi [hi; lo] + lo hi
 //   D3 = (e^{cl - c} U)^T K  [128 x N]    two parts;  S <- e^{cl} S + D3, f32 in registers
 //   y = scale (e^c S^T Q^T + U^T P^T)     off the chain: a third warpgroup writes it
-// One thread copies a chunk's tiles one chunk ahead and issues all products.  The chain of a
-// chunk is three products and three passes through the registers, and bounds the walk.
+// One thread copies a chunk's tiles one chunk ahead, one warp issues all products.  The chain of a
+// chunk is three products and three passes through the registers, and bounds the walk: of some 6900 cycles
+// S's parts take 920, D1 1800, X 860, D2 800, U 1000, D3 980, the update 500 (the state's threads' clocks), the
+// products themselves 2950.  One block fills an SM's registers, so that nothing runs in the gaps.
+// 4 x 4096 tokens, 32 heads, N = P = 128, bf16: 245 us.  65536 tokens, 8 heads in 19 segments: 355 us for
+// the sums, 221 for the walk.
 //
-// Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken
-// from the channel's largest value, which its two threads exchange; the f32 state stays good to
+// Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken from a bound that
+// is known beforehand (bounds up to 2^14 above the largest value cost none of the 22 bits) or from the channel's
+// largest value, which its two threads exchange; the f32 state stays good to
 // a few 1e-7.  P and U enter y's product with one part each for bf16 io (2^-12 of a y that is
 // rounded to 2^-9), with two for f16.
 #include "../simd.cuh"
@@ -455,31 +460,33 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         leave_regs<56>();
         const int role = __shfl_sync(kFull, warp, 0) - (kThreads - 128) / 32, steps = __shfl_sync(kFull, chunks, 0);
         if (role == 1 && lane == 0) {  // loads
-        const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
-        const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(IP);
-        auto load = [&](int ch) {
-            char* at = sm + (ch & 1) * L::bytes;
-            uint64_t* bar = &s_full[ch & 1];
-            const int t0 = (int)(t_begin + (int64_t)ch * C);
-            mbar_expect_tx(bar, (OUT ? 2 : 1) * NB * kTileBytes + (phi ? 0 : 2 * kTileBytes) + (2 + (OUT ? PP : 0)) * kTileBytes +
-                                    (int)sizeof(ImageHead));
-            const char* kq = keys + ch * a.G * (NB * 2 * kTileBytes);
+            const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
+            const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(IP);
+            auto load = [&](int ch) {
+                char* at = sm + (ch & 1) * L::bytes;
+                uint64_t* bar = &s_full[ch & 1];
+                const int t0 = (int)(t_begin + (int64_t)ch * C);
+                mbar_expect_tx(bar, (OUT ? 2 : 1) * NB * kTileBytes + (phi ? 0 : 2 * kTileBytes) + (2 + (OUT ? PP : 0)) * kTileBytes +
+                                        (int)sizeof(ImageHead));
+                const char* kq = keys + ch * a.G * (NB * 2 * kTileBytes);
 #pragma unroll
-            for (int n = 0; n < NB; n++) bulk_load(at + n * L::block, kq + n * 2 * kTileBytes, L::block, bar);
-            if (!phi) {
-                la::tma_load_4d(at + L::v, &w.v, (int)p0, (int)h, t0, (int)b, bar);
-                la::tma_load_4d(at + L::v + kTileBytes, &w.v, (int)p0 + 64, (int)h, t0, (int)b, bar);
+                for (int n = 0; n < NB; n++) bulk_load(at + n * L::block, kq + n * 2 * kTileBytes, L::block, bar);
+                if (!phi) {
+                    la::tma_load_4d(at + L::v, &w.v, (int)p0, (int)h, t0, (int)b, bar);
+                    la::tma_load_4d(at + L::v + kTileBytes, &w.v, (int)p0 + 64, (int)h, t0, (int)b, bar);
+                }
+                const char* im = images + (int64_t)ch * image_bytes(IP);
+                bulk_load(at + L::image, im, (2 + (OUT ? PP : 0)) * kTileBytes, bar);
+                bulk_load(at + L::head, im + (2 + IP) * kTileBytes, (int)sizeof(ImageHead), bar);
+            };
+            for (int ch = 0; ch < chunks; ch++) {
+                if (ch > 1 && !wait(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
+                load(ch);
             }
-            const char* im = images + (int64_t)ch * image_bytes(IP);
-            bulk_load(at + L::image, im, (2 + (OUT ? PP : 0)) * kTileBytes, bar);
-            bulk_load(at + L::head, im + (2 + IP) * kTileBytes, (int)sizeof(ImageHead), bar);
-        };
-        for (int ch = 0; ch < chunks; ch++) {
-            if (ch > 1 && !wait(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
-            load(ch);
-        }
         } else if (role == 0) {  // products
-            // (a product takes as long with 128 columns of the right operand as with 64: its left operand is read either way)
+            // (A product of 16 terms takes 94 cycles with 128 columns of the right operand, 79 with 64.  Handing the high parts
+            // over before the low ones are made: 248 -> 244 us on 4 x 4096 tokens, 32 heads, but the backward's walks 270 -> 283,
+            // since stores and products share tensor memory.)
             for (int ch = 0; ch < steps; ch++) {
                 const uint32_t ph = ch & 1;
                 const uint32_t at = smem_addr(sm + ph * L::bytes), M = at + L::image, P = M + 2 * kTileBytes;
@@ -805,10 +812,10 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 la::tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                for (int part = 1; part >= 0; part--)
+                    for (int part = 1; part >= 0; part--)
 #pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        la::mma(tm + bD0, la::smem_desc(at + L::dy + s * 32), la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
+                        for (int s = 0; s < 4; s++)
+                            la::mma(tm + bD0, la::smem_desc(at + L::dy + s * 32), la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
                 }
                 if (i > 0 && !warp_wait(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
                 if (!warp_wait(&s_r, ph, &s_fail)) break;
@@ -838,11 +845,11 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 la::tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
+                    for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        la::mma_ts(tm + bD0, tm + bX + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(M + (o == 1 ? kTileBytes : 0) + s * 2048), dR, o > 0 || s > 0);
-                la::mma_commit(&s_d2);
+                        for (int s = 0; s < 4; s++)
+                            la::mma_ts(tm + bD0, tm + bX + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(M + (o == 1 ? kTileBytes : 0) + s * 2048), dR, o > 0 || s > 0);
+                    la::mma_commit(&s_d2);
                 }
                 if (!warp_wait(&s_u, ph, &s_fail)) break;
                 la::tc_fence_after();
@@ -869,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_walks(const __grid_constant__ T
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
 // from.  A block: 8 columns of one head's state, in shared memory.  Warp w takes the terms of states w, w + 8, ..: a lane
 // four rows and all columns; the warps' sums are added in order.  The next Phi (transposed) is on its way while one is
-// used.  Bound by reading shared memory.  65536 tokens, 8 heads, 19 segments: PLACEHOLDER us.
+// used.  Bound by reading shared memory.  65536 tokens, 8 heads, 19 segments: 51 us (sums over states in single threads: 86).
 constexpr int kCarryCols = 8;
 __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
     extern __shared__ __align__(16) float phi[];  // [2][N][N], then the warps' sums [8][N][8]
