@@ -102,6 +102,8 @@ template <int N> __device__ __forceinline__ float max_abs(const float* x) {
 // The power of two for a row whose largest value is `most`; of a row of zeros it is the largest there is, so
 // that it never decides a scale common to more rows.
 __device__ __forceinline__ float scale_of(float most) { return most == 0.0f ? 8.507059173023462e37f : la::f16_scale(most); }
+// (bounds of values near f32's largest pass it, the values do not)
+__device__ __forceinline__ float finite(float bound) { return fminf(bound, 3.4028234e38f); }
 __device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
     const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
     return *reinterpret_cast<const uint32_t*>(&z);
@@ -261,7 +263,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             arrive(&s_s);
             values(ch);
             const float inv1 = -head->inv_k / ss, k_most = head->most_k;
-            const float x_bound = fmaf(head->most_bu * (64 * NB) * k_most, bound, x_most), xs = scale_of(x_bound);
+            const float x_bound = finite(fmaf(head->most_bu * (64 * NB) * k_most, bound, x_most)), xs = scale_of(x_bound);
             ok = ok && wait(&s_d1, ph, &s_fail);
             la::tc_fence_after();
             float d[32];
@@ -316,12 +318,12 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             }
             la::tmem_wait_st();
             const float by = head->by, keep = head->weak ? 1.0f : 0.0f, inv3 = head->inv_k / us;
-            bound = fmaf(64.0f * k_most, ud_most, max_over(s_most[0]) * (keep + fabsf(by)));
+            bound = finite(fmaf(64.0f * k_most, ud_most, max_over(s_most[0]) * (keep + fabsf(by))));
             arrive(&s_u);
             if (!SUM) {
                 // U's image is what the backward sums products of: its own largest value, off the chain.  For y the bound
                 // of a bound does: parts of f16 keep 22 bits of rows that are 2^14 below theirs.
-                float most = 64.0f * head->most_m * x_bound;
+                float most = finite(64.0f * head->most_m * x_bound);
                 if (KEEP) {
                     s_um[half][pl] = max_abs<32>(x);
                     pair_sync();
@@ -644,8 +646,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 x[j + 2] = z.x;
                 x[j + 3] = z.y;
             }
-            const float x_bound = fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * head->most_p * (16384.0f * dy_inv)),
-                        xs = scale_of(x_bound);
+            const float xs = scale_of(finite(fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * head->most_p * (16384.0f * dy_inv))));
             {
                 const uint32_t to = tm + my + bX + 16 * half;
                 put2(to, to + 32, x, xs);
@@ -692,7 +693,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 put2(to, to + 32, d, us);
             }
             la::tmem_wait_st();
-            bound = fmaf(64.0f * k_most, ud_most, fmaf(64.0f * head->most_q, 16384.0f / dqs, r_most * (keep + fabsf(by))));
+            bound = finite(fmaf(64.0f * k_most, ud_most, fmaf(64.0f * head->most_q, 16384.0f / dqs, r_most * (keep + fabsf(by)))));
             arrive(&s_u);
             {
                 s_xm[half][pl] = max_abs<32>(x);

@@ -24,6 +24,20 @@ def test_values_of_any_size(io, size):
     check_bwd(x, io)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("big,small", [("v", "dy"), ("dy", "v")])
+def test_values_near_the_largest_of_32_bits(io, big, small):
+    """What the rule makes of values of 10^36 stays below 3.4 10^38, bounds on it need not.  (The small ones keep their
+    products with them in range.)"""
+    x = ref.gdr_inputs(1, 200, 2, 1, 128, 128, seed=31)
+    for key, size in ((big, 1e36), (small, 1e-6)):
+        x[key] = (x[key] * np.float32(size)).astype(np.float32)
+        state = {"v": "h0", "dy": "dlast"}[key]
+        x[state] = (x[state] * np.float32(size)).astype(np.float32)
+    check_fwd(x, io)
+    check_bwd(x, io)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
 def test_long_keys_with_small_rates(io):
     """Keys of length 5 and rates that keep beta |k|^2 below one; queries of length 30."""

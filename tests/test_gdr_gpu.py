@@ -197,7 +197,8 @@ def test_no_tokens(io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("shape", [(1, 2, 1, 128, 128), (7, 4, 2, 64, 80), (3, 3, 1, 5, 7), (40, 8, 4, 128, 128), (2, 2, 2, 33, 66)],
+@pytest.mark.parametrize("shape", [(1, 2, 1, 128, 128), (7, 4, 2, 64, 80), (3, 3, 1, 5, 7), (40, 8, 4, 128, 128), (2, 2, 2, 33, 66),
+                                   (40, 8, 4, 64, 64), (60, 4, 4, 40, 72), (30, 6, 1, 16, 132)],
                          ids=str)
 def test_step(shape, io):
     B, H, G, N, P = shape
