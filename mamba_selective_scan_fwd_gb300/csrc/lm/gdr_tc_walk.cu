@@ -13,13 +13,13 @@
 // chunk is three products and three passes through the registers, and bounds the walk: of some 6900 cycles
 // S's parts take 920, D1 1800, X 860, D2 800, U 1000, D3 980, the update 500 (the state's threads' clocks), the
 // products themselves 2950.  One block fills an SM's registers, so that nothing runs in the gaps.
-// 4 x 4096 tokens, 32 heads, N = P = 128, bf16: 245 us.  65536 tokens, 8 heads in 19 segments: 355 us for
+// 4 x 4096 tokens, 32 heads, N = P = 128, bf16: 250 us.  65536 tokens, 8 heads in 19 segments: 355 us for
 // the sums, 221 for the walk.
 //
-// Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken from a bound that
-// is known beforehand (bounds up to 2^14 above the largest value cost none of the 22 bits) or from the channel's
-// largest value, which its two threads exchange; the f32 state stays good to
-// a few 1e-7.  P and U enter y's product with one part each for bf16 io (2^-12 of a y that is
+// Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken from the channel's
+// largest value, which its two threads exchange (for X by a bound instead: 245 us for 250, but a state of which a chunk leaves
+// 2^-15 is off by 10^-4 of that), or for S and R from a bound of some 2^5 above it, which costs none of the 22 bits;
+// the f32 state stays good to a few 1e-7.  P and U enter y's product with one part each for bf16 io (2^-12 of a y that is
 // rounded to 2^-9), with two for f16.
 #include "../simd.cuh"
 #include "gdr_tc.cuh"
@@ -157,7 +157,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
     // landed; stage free; S; D1; X; D2; e U; D3; U; U^T P^T; read by the third warpgroup: early, late
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_uy, s_y, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
-    __shared__ float s_most[2][2][128], s_ud[2][128], s_um[2][128], s_ss[2][128], s_us[2][128];
+    __shared__ float s_most[2][128], s_ud[2][128], s_xm[2][128], s_um[2][128], s_ss[2][128], s_us[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pl = tid & 127;
     const bool phi = SUM && blockIdx.y == 1;
@@ -203,14 +203,14 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             for (int n = 0; n < W; n++) S[n] = from && mine && half * W + n < a.N ? from[(half * W + n) * a.P + p] : 0.0f;
         }
         // (a wait that ran out ends no loop here: the others wait at its barriers)
-        // Scales come from bounds that are known before they are needed: the largest values of S and beta V, which
-        // the channel's two threads exchange while a product runs, and the largest of K and M.  Only e U's is
-        // its own largest value: under strong decays that is what is left of the state.
+        // X's and e U's scales are their own largest values, which the channel's two threads exchange: after strong decays
+        // or corrections what is left of them is far below any bound.  S's comes from a bound that is known when the
+        // update is done, by its largest value before.
         auto pair_sync = [&] { named_sync(1 + (warp & 3), 64); };
         auto max_over = [&](const float (&m)[2][128]) { return fmaxf(m[0][pl], m[1][pl]); };
         bool ok = true;
         // beta V of a chunk, and the largest value of the channel's, while S^T K^T is on its way
-        float x[32], x_most = 0.0f;
+        float x[32];
         auto values = [&](int ch) {
             char* at = sm + (ch & 1) * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
@@ -238,13 +238,10 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                         if (32 * half + j >= nv) x[j] = 0.0f;
                 }
             }
-            s_most[1][half][pl] = max_abs<32>(x);
-            pair_sync();
-            x_most = max_over(s_most[1]);
         };
-        s_most[0][half][pl] = max_abs<W>(S);
+        s_most[half][pl] = max_abs<W>(S);
         pair_sync();
-        float bound = max_over(s_most[0]);  // of |S|
+        float bound = max_over(s_most);  // of |S|
         pair_sync();
         for (int ch = 0; ch < chunks; ch++) {
             const uint32_t ph = ch & 1;
@@ -263,7 +260,6 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             arrive(&s_s);
             values(ch);
             const float inv1 = -head->inv_k / ss, k_most = head->most_k;
-            const float x_bound = finite(fmaf(head->most_bu * (64 * NB) * k_most, bound, x_most)), xs = scale_of(x_bound);
             ok = ok && wait(&s_d1, ph, &s_fail);
             la::tc_fence_after();
             float d[32];
@@ -283,6 +279,9 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 for (int j = 0; j < 32; j++)
                     if (32 * half + j >= nv) x[j] = 0.0f;
             }
+            s_xm[half][pl] = max_abs<32>(x);
+            pair_sync();
+            const float x_most = max_over(s_xm), xs = scale_of(x_most);
             {
                 const uint32_t to = tm + my + kX + 16 * half;
                 put2(to, to + 32, x, xs);
@@ -290,7 +289,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             la::tmem_wait_st();
             arrive(&s_x);
             const float inv2 = head->inv_m / xs;
-            s_most[0][half][pl] = max_abs<W>(S);
+            s_most[half][pl] = max_abs<W>(S);
             ok = ok && wait(&s_d2, ph, &s_fail);
             la::tc_fence_after();
             tmem_ld64(tm + my + kD3 + 64 + 32 * half, x, tm + my + kD3 + 32 * half, d);
@@ -318,12 +317,12 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
             }
             la::tmem_wait_st();
             const float by = head->by, keep = head->weak ? 1.0f : 0.0f, inv3 = head->inv_k / us;
-            bound = finite(fmaf(64.0f * k_most, ud_most, max_over(s_most[0]) * (keep + fabsf(by))));
+            bound = finite(fmaf(64.0f * k_most, ud_most, max_over(s_most) * (keep + fabsf(by))));
             arrive(&s_u);
             if (!SUM) {
-                // U's image is what the backward sums products of: its own largest value, off the chain.  For y the bound
-                // of a bound does: parts of f16 keep 22 bits of rows that are 2^14 below theirs.
-                float most = finite(64.0f * head->most_m * x_bound);
+                // U's image is what the backward sums products of: its own largest value, off the chain.  For y a bound
+                // does: parts of f16 keep 22 bits of rows that are 2^14 below theirs.
+                float most = finite(64.0f * head->most_m * x_most);
                 if (KEEP) {
                     s_um[half][pl] = max_abs<32>(x);
                     pair_sync();
@@ -574,7 +573,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
     using L = BackStage<NB>;
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r, s_d1, s_dq, s_x, s_d2, s_u, s_d3, s_dyq, s_xi, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
-    __shared__ float s_most[2][128], s_ud[2][128], s_xm[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
+    __shared__ float s_most[2][128], s_ud[2][128], s_xe[2][128], s_xm[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, warp = tid >> 5, pl = tid & 127;
     const int64_t ptiles = (a.P + kTileP - 1) / kTileP, pt = id % ptiles, p0 = pt * kTileP, bh = id / ptiles;
@@ -646,7 +645,9 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 x[j + 2] = z.x;
                 x[j + 3] = z.y;
             }
-            const float xs = scale_of(finite(fmaf(head->most_down * (64 * NB) * k_most, r_most, fabsf(a.scale) * 64.0f * head->most_p * (16384.0f * dy_inv))));
+            s_xe[half][pl] = max_abs<32>(x);
+            pair_sync();
+            const float xs = scale_of(max_over(s_xe));
             {
                 const uint32_t to = tm + my + bX + 16 * half;
                 put2(to, to + 32, x, xs);

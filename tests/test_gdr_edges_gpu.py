@@ -38,6 +38,19 @@ def test_values_near_the_largest_of_32_bits(io, big, small):
     check_bwd(x, io)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("how", ["decays", "corrections"])
+def test_small_states_after_large_ones(io, how):
+    """Values fall by 10^5 inside a chunk, and decays of e^-25 or corrections in eight dimensions take the larger
+    state out: what is left has to be good by its own size."""
+    x = ref.gdr_inputs(3, 128, 2, 1, 8, 64, seed=33)
+    x["v"][:, 80:] *= np.float32(1e-5)
+    if how == "decays":
+        x["g"] = (x["g"] * np.float32(50)).astype(np.float32)
+    check_fwd(x, io)
+    check_bwd(x, io)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
 def test_long_keys_with_small_rates(io):
     """Keys of length 5 and rates that keep beta |k|^2 below one; queries of length 30."""
@@ -178,3 +191,17 @@ def test_given_outputs_are_used_and_checked():
     assert d["dq"] is out["dq"] and d["dbeta"] is out["dbeta"] and d["dh0"] is None
     with pytest.raises(ValueError, match="dk"):
         ss.ss_gdr_bwd(*args, t["dy"], out={"dk": torch.empty(1, 40, 1, 8, device="cuda")})
+
+
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(70, 140, 4, 2, 64, 64), (30, 200, 6, 2, 128, 136)], ids=str)
+def test_many_ragged_rows(shape, io):
+    """More chunks than the chunk kernel has blocks, so that each takes several, some of them without a token."""
+    B, L = shape[:2]
+    lengths = [(0, L, 1, 64, 65, 128, 129, 17)[i % 8] for i in range(B)]
+    x = ref.gdr_inputs(*shape, seed=41)
+    check_fwd(x, io, lengths=lengths)
+    got = check_bwd(x, io, lengths=lengths)
+    for name in ("dq", "dk", "dv", "dg", "dbeta"):
+        for b in range(0, B, 8):
+            assert not got[name][b].any(), name
