@@ -41,7 +41,16 @@ struct Pairs {
 };
 static_assert(sizeof(Pairs) == 768, "whole 16-byte units");
 
-enum WalkMode { kWalkY, kWalkKeep, kWalkBack };
+// How the walks over time are cut: K segments of seg tiles, whole chunks.  They are first walked for what they do to a
+// state: from zero (E), and without v from the identity (Phi), so that S -> Phi S + E, and for the adjoint from the end
+// R -> Phi^T R + E'.
+struct WalkPlan {
+    int64_t K, seg;
+};
+WalkPlan walk_plan(int64_t heads, int64_t N, int64_t P, int64_t L, bool backward);
+
+// kWalkSum: E or Phi; kWalkBackSum: E'
+enum WalkMode { kWalkY, kWalkKeep, kWalkBack, kWalkSum, kWalkBackSum };
 struct WalkArgs {
     Args a;
     const Pairs* pairs; // [Bsz, H, tiles of 16 tokens]
@@ -52,6 +61,9 @@ struct WalkArgs {
     float* states;      // kWalkKeep: before each chunk; kWalkBack: adjoint after it; f32 [Bsz, H, chunks, N, P]
     int64_t chunks;
     bool vec;           // f32, and runs of four values are whole and aligned: asynchronous copies
+    WalkPlan plan;
+    float* seg_state;   // f32 [Bsz, H, K, N, P], plan.K > 1: E (E'), then (after the carry) what each segment starts from
+    float* seg_phi;     // f32 [Bsz, H, K, N, N]
 };
 
 struct ChunkArgs {
@@ -67,6 +79,8 @@ struct ChunkArgs {
 cudaError_t launch_pairs(const Args& a, Pairs* pairs, cudaStream_t st);
 cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st);                          // kWalkY
 cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st);  // the backward's two, at once
+// What comes before them with plan.K > 1: the sums and the carry (back: of both directions).
+cudaError_t launch_segments(const WalkArgs& w, const WalkArgs* back, cudaStream_t st);
 cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st);
 
 struct StepArgs {

@@ -42,8 +42,27 @@ size_t pairs_bytes(int64_t Bsz, int64_t L, int64_t H) { return (size_t)Bsz * H *
 // The FP32 backward's workspace.
 struct Bwd32 {
     int64_t chunks;
-    size_t pairs, miss, x, before, after, dq, dk;
+    WalkPlan plan;
+    size_t pairs, miss, x, before, after, dq, dk, starts, ends, phi;
 };
+// The FP32 walks' segments, behind what else is there.
+void segments(Layout& l, const WalkPlan& p, int64_t rows, int64_t N, int64_t P, size_t* starts, size_t* ends, size_t* phi) {
+    const bool cut = p.K > 1;
+    *starts = l.take(cut ? (size_t)rows * p.K * N * P * 4 : 0);
+    if (ends) *ends = l.take(cut ? (size_t)rows * p.K * N * P * 4 : 0);
+    *phi = l.take(cut ? (size_t)rows * p.K * N * N * 4 : 0);
+}
+struct Fwd32 {
+    WalkPlan plan;
+    size_t pairs, starts, phi;
+};
+Fwd32 fwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t N, int64_t P) {
+    Fwd32 f;
+    f.plan = walk_plan(Bsz * H, N, P, L, false);
+    f.pairs = l.take(pairs_bytes(Bsz, L, H));
+    segments(l, f.plan, Bsz * H, N, P, &f.starts, nullptr, &f.phi);
+    return f;
+}
 Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     Bwd32 b;
     b.chunks = ceil_div(L, kChunk);
@@ -56,6 +75,8 @@ Bwd32 bwd32_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     const size_t part = H > G ? (size_t)(H / G) * Bsz * L * G * N * 4 : 0;
     b.dq = l.take(part);
     b.dk = l.take(part);
+    b.plan = walk_plan(Bsz * H, N, P, L, true);
+    segments(l, b.plan, Bsz * H, N, P, &b.starts, &b.ends, &b.phi);
     return b;
 }
 
@@ -324,7 +345,7 @@ size_t ss_gdr_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, 
     if (check_sizes(Bsz, L, H, G, N, P, dtype) != SS_OK || empty(Bsz, L)) return 0;
     // the larger of what the two paths need: strides and pointers, which decide between them, are not known here
     Layout l, t;
-    l.take(pairs_bytes(Bsz, L, H));
+    fwd32_layout(l, Bsz, L, H, N, P);
     if (tc_sizes(L, N, P, dtype)) fwdtc_layout(t, Bsz, L, H, G, N, P, dtype);
     return l.total > t.total ? l.total : t.total;
 }
@@ -346,13 +367,21 @@ int ss_gdr_fwd(const ss_gdr_fwd_desc* d, void* stream) {
     bool ran;
     const int tc = tc_forward(a, d->y, d->last_state, static_cast<char*>(d->workspace), st, &ran);
     if (ran || tc != SS_OK) return tc;
+    char* ws = static_cast<char*>(d->workspace);
+    Layout l;
+    const Fwd32 f = fwd32_layout(l, a.Bsz, a.L, a.H, a.N, a.P);
     WalkArgs w = {};
     w.a = a;
-    w.pairs = static_cast<const Pairs*>(d->workspace);
+    Pairs* pairs = reinterpret_cast<Pairs*>(ws + f.pairs);
+    w.pairs = pairs;
     w.init = a.h0;
     w.last = d->last_state;
     w.y = d->y;
-    if (launch_pairs(a, static_cast<Pairs*>(d->workspace), st) != cudaSuccess) return SS_ERR_CUDA;
+    w.plan = f.plan;
+    w.seg_state = reinterpret_cast<float*>(ws + f.starts);
+    w.seg_phi = reinterpret_cast<float*>(ws + f.phi);
+    if (launch_pairs(a, pairs, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (w.plan.K > 1 && launch_segments(w, nullptr, st) != cudaSuccess) return SS_ERR_CUDA;
     return launch_walk(w, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -404,7 +433,13 @@ int ss_gdr_bwd(const ss_gdr_bwd_desc* d, void* stream) {
     back.y = d->dv;
     back.rows = f32(bl.x);
     back.states = f32(bl.after);
-    if (launch_pairs(a, pairs, st) != cudaSuccess || launch_walks(keep, back, st) != cudaSuccess) return SS_ERR_CUDA;
+    keep.plan = back.plan = bl.plan;
+    keep.seg_state = f32(bl.starts);
+    back.seg_state = f32(bl.ends);
+    keep.seg_phi = back.seg_phi = f32(bl.phi);
+    if (launch_pairs(a, pairs, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (bl.plan.K > 1 && launch_segments(keep, &back, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_walks(keep, back, st) != cudaSuccess) return SS_ERR_CUDA;
     ChunkArgs c = {};
     c.a = a;
     c.miss = f32(bl.miss);

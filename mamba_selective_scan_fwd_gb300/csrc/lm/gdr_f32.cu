@@ -117,26 +117,36 @@ template <typename T> __global__ void __launch_bounds__(128) k_pairs(Args a, Pai
 // so that a chain of sums over the lanes is paid once for four tokens.  The backward's walk is the same from
 // the other end.  2 x 1000 tokens, 24 heads, N = P = 64: 146 us beside 13 for the pairs' products (token by token 228;
 // with four interleaved chains of sums and q held in registers 149).
-template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void walk(const WalkArgs& w, int64_t id) {
+//
+// Few heads of many tokens are cut into segments (walk_plan): the same walk takes their sums, whose columns (N of Phi, P of E)
+// are as independent, a carry joins them, and the walk proper starts from what it left.
+template <int LN, WalkMode MODE> struct WalkStage {
+    static constexpr bool Q = MODE != kWalkSum && MODE != kWalkKeep;
+    float k[kWalkT][16 * LN], q[Q ? kWalkT : 1][16 * LN], v[kWalkT][64 / LN];
+    Pairs p;
+};
+// phi (kWalkSum): from the identity without v, else from zero
+template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void walk(const WalkArgs& w, int64_t id, bool phi = false) {
+    using Stage = WalkStage<LN, MODE>;
+    constexpr bool SUM = MODE == kWalkSum, BACK = MODE == kWalkBack || MODE == kWalkBackSum, NOQ = !Stage::Q;
     constexpr int NT = 64, NP = 16 * LN, PT = NT / LN, TT = kWalkT;
-    struct Stage {
-        float k[TT][NP], q[MODE == kWalkKeep ? 1 : TT][NP], v[TT][PT];
-        Pairs p;
-    };
-    __shared__ __align__(16) Stage s_stage[2];
+    extern __shared__ __align__(16) char smem[];
+    Stage* s_stage = reinterpret_cast<Stage*>(smem);
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, ln = lane % LN;
-    const int64_t ptiles = (a.P + PT - 1) / PT;
-    const int64_t p0 = (id % ptiles) * PT;
-    id /= ptiles;
+    const int64_t width = phi ? a.N : a.P, ptiles = (a.P + PT - 1) / PT, tiles_of = phi ? (a.N + PT - 1) / PT : ptiles;
+    const int64_t p0 = (id % tiles_of) * PT;
+    id /= tiles_of;
+    const int64_t seg = id % w.plan.K;
+    id /= w.plan.K;
     const int64_t h = id % a.H, b = id / a.H, hq = h / (a.H / a.G), bh = b * a.H + h;
-    const int N = (int)a.N, pleft = (int)min((int64_t)PT, a.P - p0);
+    const int N = (int)a.N, pleft = (int)min((int64_t)PT, width - p0);
     const int col = tid / LN;  // of the block's channels
     const int64_t len = row_length(a, b), NPel = a.N * a.P;
-    const In& vin = MODE == kWalkBack ? a.dy : a.v;
+    const In& vin = BACK ? a.dy : a.v;
     const T* kp = static_cast<const T*>(a.k.p) + b * a.k.batch + hq * a.N;
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.batch + hq * a.N;
-    const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P + p0;
+    const T* vp = static_cast<const T*>(vin.p) + b * vin.batch + h * a.P + (phi ? 0 : p0);
     const int64_t all_tiles = (a.L + TT - 1) / TT;
 
     float2 S[8];  // [2 j + e / 2]
@@ -145,20 +155,29 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
         for (int i = 0; i < 8; i++) {
             const int n = 4 * (ln + LN * (i / 2)) + 2 * (i & 1);
             const bool ok = p && col < pleft;
-            float* q = p + n * a.P + p0 + col;
+            float* q = p + n * width + p0 + col;
             if (put) {
                 if (ok && n < N) q[0] = S[i].x;
-                if (ok && n + 1 < N) q[a.P] = S[i].y;
+                if (ok && n + 1 < N) q[width] = S[i].y;
             } else {
                 S[i].x = ok && n < N ? q[0] : 0.0f;
-                S[i].y = ok && n + 1 < N ? q[a.P] : 0.0f;
+                S[i].y = ok && n + 1 < N ? q[width] : 0.0f;
             }
         }
     };
-    state(w.init ? const_cast<float*>(w.init) + bh * NPel : nullptr, false);
+    float* const seg_state = w.plan.K > 1 ? w.seg_state + (bh * w.plan.K + seg) * NPel : nullptr;
+    if (phi) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int64_t n = 4 * (ln + LN * (i / 2)) + 2 * (i & 1), c = p0 + col;
+            S[i] = make_float2(n == c ? 1.0f : 0.0f, n + 1 == c ? 1.0f : 0.0f);
+        }
+    } else {
+        state(SUM || MODE == kWalkBackSum ? nullptr : seg_state ? seg_state : w.init ? const_cast<float*>(w.init) + bh * NPel : nullptr, false);
+    }
 
-    const int64_t tiles = (len + TT - 1) / TT;
-    auto start = [&](int64_t i) { return (MODE == kWalkBack ? tiles - 1 - i : i) * TT; };
+    const int64_t first = seg * w.plan.seg, tiles = max((int64_t)0, min((len + TT - 1) / TT, first + w.plan.seg) - first);
+    auto start = [&](int64_t i) { return (first + (BACK ? tiles - 1 - i : i)) * TT; };
     auto fetch = [&](int64_t i) {
         Stage& s = s_stage[i & 1];
         const int64_t t0 = start(i);
@@ -172,13 +191,13 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
                 const bool on = t < nv && n < N;
                 const int64_t tt = on ? t0 + t : 0;
                 copy16(&s.k[t][n], kp + tt * a.k.token + (on ? n : 0), on);
-                if (MODE != kWalkKeep) copy16(&s.q[t][n], qp + tt * a.q.token + (on ? n : 0), on);
+                if (!NOQ) copy16(&s.q[t][n], qp + tt * a.q.token + (on ? n : 0), on);
             }
 #pragma unroll
             for (int e = 0; e < (TT * PT / 4 + NT - 1) / NT; e++) {
                 const int x = tid + NT * e, t = x / (PT / 4), c = x % (PT / 4) * 4;
                 if (t >= TT) break;
-                const bool on = t < nv && c < pleft;
+                const bool on = !phi && t < nv && c < pleft;
                 copy16(&s.v[t][c], vp + (on ? t0 + t : 0) * vin.token + (on ? c : 0), on);
             }
         } else {
@@ -187,12 +206,12 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
                 const int t = x / NP, n = x % NP;
                 const bool on = t < nv && n < N;
                 s.k[t][n] = on ? ldf(kp + (t0 + t) * a.k.token + n) : 0.0f;
-                if (MODE != kWalkKeep) s.q[t][n] = on ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
+                if (!NOQ) s.q[t][n] = on ? ldf(qp + (t0 + t) * a.q.token + n) : 0.0f;
             }
 #pragma unroll 4
             for (int x = tid; x < TT * PT; x += NT) {
                 const int t = x / PT, c = x % PT;
-                s.v[t][c] = t < nv && c < pleft ? ldf(vp + (t0 + t) * vin.token + c) : 0.0f;
+                s.v[t][c] = !phi && t < nv && c < pleft ? ldf(vp + (t0 + t) * vin.token + c) : 0.0f;
             }
         }
         copy_commit();
@@ -227,7 +246,7 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
         const int64_t row0 = ((b * a.L + t0) * a.H + h) * a.P + p0 + col;
 #pragma unroll 1
         for (int u = 0; u < fours; u++) {
-            const int o = kFour * (MODE == kWalkBack ? fours - 1 - u : u);
+            const int o = kFour * (BACK ? fours - 1 - u : u);
             float2 k[kFour][8];
             float ks[kFour], qs[kFour];
 #pragma unroll
@@ -261,14 +280,14 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
             for (int t = 0; t < kFour; t++) {
                 v[t] = s.v[o + t][col];
                 if (t > 0) row(kk[t], s.p.kk[o + t]);
-                if (MODE != kWalkKeep) row(qk[t], s.p.qk[o + t]);
+                if (!NOQ) row(qk[t], s.p.qk[o + t]);
             }
             row(up, &s.p.up[o]);
             row(down, &s.p.down[o]);
             row(beta, &s.p.beta[o]);
             const float by = s.p.by[o >> 2];
             const bool weak = s.p.weak[o >> 2];
-            if (MODE == kWalkBack) {
+            if (BACK) {
 #pragma unroll
                 for (int t = kFour - 1; t >= 0; t--) {
                     float z = down[t] * ks[t];
@@ -308,10 +327,10 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
             }
 #pragma unroll
             for (int t = 0; t < kFour; t++) {
-                const float2 f = splat2(MODE == kWalkBack ? -up[t] * beta[t] * x[t] : ks[t]);
+                const float2 f = splat2(BACK ? -up[t] * beta[t] * x[t] : ks[t]);
 #pragma unroll
                 for (int j = 0; j < 8; j++) S[j] = fma2(k[t][j], f, S[j]);
-                if (MODE == kWalkBack) {
+                if (BACK) {
                     float2 q[8];
                     read(s.q[o + t], q);
                     const float2 y = splat2(a.scale * up[t] * v[t]);
@@ -319,7 +338,7 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
                     for (int j = 0; j < 8; j++) S[j] = fma2(q[j], y, S[j]);
                 }
             }
-            if (ln == 0 && col < pleft)
+            if (MODE != kWalkSum && MODE != kWalkBackSum && ln == 0 && col < pleft)
 #pragma unroll
                 for (int t = 0; t < kFour; t++)
                     if (o + t < nv) {
@@ -329,15 +348,82 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
                     }
         }
     }
-    if (MODE != kWalkKeep)  // rows that do not count
-        for (int64_t t = len + tid / 32; t < a.L; t += NT / 32)
+    if (MODE == kWalkY || MODE == kWalkBack)  // rows that do not count
+        for (int64_t t = max(len, first * TT) + tid / 32; t < min(a.L, (first + w.plan.seg) * TT); t += NT / 32)
             for (int c = lane; c < pleft; c += 32) st(static_cast<T*>(w.y) + ((b * a.L + t) * a.H + h) * a.P + p0 + c, 0.0f);
-    if (w.last) state(w.last + bh * NPel, true);
+    if (phi) state(w.seg_phi + (bh * w.plan.K + seg) * a.N * a.N, true);
+    else if (SUM || MODE == kWalkBackSum) state(seg_state, true);
+    else if (w.last && seg == (BACK ? 0 : w.plan.K - 1)) state(w.last + bh * NPel, true);
 }
 template <typename T, int LN> __global__ void __launch_bounds__(64) k_walk(WalkArgs w) { walk<T, LN, kWalkY>(w, blockIdx.x); }
 template <typename T, int LN> __global__ void __launch_bounds__(64) k_walks(WalkArgs keep, WalkArgs back) {
     if (blockIdx.y == 0) walk<T, LN, kWalkKeep>(keep, blockIdx.x);
     else walk<T, LN, kWalkBack>(back, blockIdx.x);
+}
+// blockIdx.y: 0 Phi, 1 E, 2 E'.  Nothing follows the last segment, nothing comes before the first.
+template <typename T, int LN> __global__ void __launch_bounds__(64) k_sums(WalkArgs w, WalkArgs back) {
+    constexpr int PT = 64 / LN;
+    const int64_t wide = ((blockIdx.y == 0 ? w.a.N : w.a.P) + PT - 1) / PT, K = w.plan.K, seg = blockIdx.x / wide % K;
+    if (blockIdx.x >= wide * K * w.a.H * w.a.Bsz) return;
+    if (blockIdx.y == 2 ? seg == 0 : seg == K - 1 && (blockIdx.y == 1 || gridDim.y == 2)) return;
+    if (blockIdx.y < 2) walk<T, LN, kWalkSum>(w, blockIdx.x, blockIdx.y == 0);
+    else walk<T, LN, kWalkBackSum>(back, blockIdx.x);
+}
+
+// S <- Phi S + E over the segments from the first (blockIdx.y 0), R <- Phi^T R + E' from the last (1); the sums' places receive
+// what each segment starts from.  A block: 8 columns of one head, two threads a state; the next Phi is on its way while
+// one is used.
+constexpr int kCarryCols = 8;
+__global__ void __launch_bounds__(256) k_carry32(WalkArgs w, WalkArgs r) {
+    extern __shared__ __align__(16) char smem[];
+    float* phi = reinterpret_cast<float*>(smem);  // [2][N][N + 1]
+    __shared__ __align__(16) float s_x[2][la::kMaxN][kCarryCols];
+    const bool back = blockIdx.y == 1;
+    const WalkArgs& a = back ? r : w;
+    const int tid = threadIdx.x, N = (int)w.a.N, LD = N + 1, n = tid >> 1, c0 = (tid & 1) * 4, K = (int)w.plan.K;
+    const int64_t P = w.a.P, ptiles = (P + kCarryCols - 1) / kCarryCols, p0 = blockIdx.x % ptiles * kCarryCols + c0, bh = blockIdx.x / ptiles;
+    auto load = [&](int i) {
+        const float* from = w.seg_phi + (bh * K + (back ? K - 1 - i : i)) * N * N;
+        float* to = phi + (i & 1) * N * LD;
+        for (int e = tid; e < N * N; e += 256)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to + e / N * LD + e % N)), "l"(from + e) : "memory");
+        copy_commit();
+    };
+    float x[4];
+#pragma unroll
+    for (int c = 0; c < 4; c++) x[c] = n < N && p0 + c < P && a.init ? a.init[(bh * N + n) * P + p0 + c] : 0.0f;
+    load(0);
+    for (int i = 0; i < K; i++) {
+        float* at = a.seg_state + ((bh * K + (back ? K - 1 - i : i)) * N + n) * P + p0;
+        float e[4] = {};
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+            if (n < N && p0 + c < P) {
+                if (i + 1 < K) e[c] = at[c];
+                at[c] = x[c];
+            }
+        if (i + 1 == K) break;
+        if (n < N) *reinterpret_cast<float4*>(&s_x[i & 1][n][c0]) = make_float4(x[0], x[1], x[2], x[3]);
+        copy_wait();
+        __syncthreads();  // (and: the Phi before is used)
+        if (i + 2 < K) load(i + 1);
+        if (n < N) {
+            const float* f = phi + (i & 1) * N * LD + (back ? n : n * LD);
+            const int step = back ? LD : 1;
+            float y[4] = {};
+#pragma unroll 8
+            for (int m = 0; m < N; m++) {
+                const float p = f[m * step];
+                const float4 z = at4(&s_x[i & 1][m][c0]);
+                y[0] = fmaf(p, z.x, y[0]);
+                y[1] = fmaf(p, z.y, y[1]);
+                y[2] = fmaf(p, z.z, y[2]);
+                y[3] = fmaf(p, z.w, y[3]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; c++) x[c] = e[c] + y[c];
+        }
+    }
 }
 
 // ---------------------------------------------------------------- one chunk of one head
@@ -605,18 +691,22 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) k_chunk(Chu
     }
 }
 
-template <typename T, int LN> cudaError_t walk_go(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
-    const unsigned grid = (unsigned)(ceil_div(w.a.P, 64 / LN) * w.a.H * w.a.Bsz);
-    if (back) k_walks<T, LN><<<dim3(grid, 2), 64, 0, st>>>(w, *back);
-    else k_walk<T, LN><<<grid, 64, 0, st>>>(w);
+enum Launch { kOne, kBoth, kSums };
+template <typename T, int LN> cudaError_t walk_go(Launch what, const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
+    constexpr int y = 2 * sizeof(WalkStage<LN, kWalkY>), sum = 2 * sizeof(WalkStage<LN, kWalkSum>);
+    const int64_t rows = w.a.H * w.a.Bsz * w.plan.K, wide = ceil_div(w.a.P, 64 / LN), deep = ceil_div(w.a.N, 64 / LN);
+    const unsigned grid = (unsigned)(wide * rows);
+    if (what == kOne) k_walk<T, LN><<<grid, 64, y, st>>>(w);
+    else if (what == kBoth) k_walks<T, LN><<<dim3(grid, 2), 64, y, st>>>(w, *back);
+    else k_sums<T, LN><<<dim3((unsigned)((wide > deep ? wide : deep) * rows), back ? 3 : 2), 64, back ? y : sum, st>>>(w, back ? *back : w);
     return cudaGetLastError();
 }
-template <typename T> cudaError_t walk_io(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
+template <typename T> cudaError_t walk_io(Launch what, const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
     switch (walk_lanes(w.a.N)) {
-        case 1: return walk_go<T, 1>(w, back, st);
-        case 2: return walk_go<T, 2>(w, back, st);
-        case 4: return walk_go<T, 4>(w, back, st);
-        default: return walk_go<T, 8>(w, back, st);
+        case 1: return walk_go<T, 1>(what, w, back, st);
+        case 2: return walk_go<T, 2>(what, w, back, st);
+        case 4: return walk_go<T, 4>(what, w, back, st);
+        default: return walk_go<T, 8>(what, w, back, st);
     }
 }
 
@@ -643,7 +733,7 @@ bool fours(const Args& a) {
 
 }  // namespace
 
-static cudaError_t go(WalkArgs w, const WalkArgs* back, cudaStream_t st) {
+static cudaError_t go(Launch what, WalkArgs w, const WalkArgs* back, cudaStream_t st) {
     w.vec = fours(w.a);
     WalkArgs r;
     if (back) {
@@ -651,9 +741,9 @@ static cudaError_t go(WalkArgs w, const WalkArgs* back, cudaStream_t st) {
         r.vec = w.vec;
         back = &r;
     }
-    if (w.a.dtype == 0) return walk_io<float>(w, back, st);
-    if (w.a.dtype == 1) return walk_io<__half>(w, back, st);
-    return walk_io<__nv_bfloat16>(w, back, st);
+    if (w.a.dtype == 0) return walk_io<float>(what, w, back, st);
+    if (w.a.dtype == 1) return walk_io<__half>(what, w, back, st);
+    return walk_io<__nv_bfloat16>(what, w, back, st);
 }
 cudaError_t launch_pairs(const Args& a, Pairs* pairs, cudaStream_t st) {
     const int64_t tiles = ceil_div(a.L, kWalkT);
@@ -663,8 +753,37 @@ cudaError_t launch_pairs(const Args& a, Pairs* pairs, cudaStream_t st) {
     else k_pairs<__nv_bfloat16><<<grid, 128, 0, st>>>(a, pairs, tiles);
     return cudaGetLastError();
 }
-cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st) { return go(w, nullptr, st); }
-cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st) { return go(keep, &back, st); }
+cudaError_t launch_walk(const WalkArgs& w, cudaStream_t st) { return go(kOne, w, nullptr, st); }
+cudaError_t launch_walks(const WalkArgs& keep, const WalkArgs& back, cudaStream_t st) { return go(kBoth, keep, &back, st); }
+cudaError_t launch_segments(const WalkArgs& w, const WalkArgs* back, cudaStream_t st) {
+    cudaError_t e = go(kSums, w, back, st);
+    if (e != cudaSuccess) return e;
+    e = la::allow_smem<k_carry32>(2 * la::kMaxN * (la::kMaxN + 1) * 4);
+    if (e != cudaSuccess) return e;
+    const int N = (int)w.a.N;
+    k_carry32<<<dim3((unsigned)(ceil_div(w.a.P, kCarryCols) * w.a.Bsz * w.a.H), back ? 2 : 1), 256, 2 * N * (N + 1) * 4, st>>>(w, back ? *back : w);
+    return cudaGetLastError();
+}
+
+// Costs in tiles walked by one block; some two blocks an SM walk as fast as one.  A segment's carry is most of a tile's
+// time, three launches four.
+WalkPlan walk_plan(int64_t heads, int64_t N, int64_t P, int64_t L, bool backward) {
+    const int64_t pt = 64 / walk_lanes(N), wide = ceil_div(P, pt), deep = ceil_div(N, pt), tiles = ceil_div(L, kWalkT), chunk = kChunk / kWalkT;
+    const int64_t both = backward ? 2 : 1;
+    auto rounds = [](int64_t blocks) { return blocks <= 2 * kSms ? 1.0 : (double)blocks / (2 * kSms); };
+    WalkPlan best = {1, tiles};
+    double least = rounds(heads * wide * both) * tiles;
+    for (int64_t K = 2; K <= 64 && 2 * K * chunk <= tiles; K++) {
+        const int64_t seg = ceil_div(ceil_div(tiles, K), chunk) * chunk;
+        if (ceil_div(tiles, seg) != K) continue;
+        const double cost = (rounds(heads * (wide * both + deep) * K) + rounds(heads * wide * both * K)) * seg + 0.8 * K + 4;
+        if (cost < 0.9 * least) {
+            least = cost;
+            best = {K, seg};
+        }
+    }
+    return best;
+}
 
 cudaError_t launch_chunks(const ChunkArgs& c, cudaStream_t st) {
     if (c.a.dtype == 0) return chunk_io<float>(c, st);

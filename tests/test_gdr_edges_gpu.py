@@ -205,3 +205,20 @@ def test_many_ragged_rows(shape, io):
     for name in ("dq", "dk", "dv", "dg", "dbeta"):
         for b in range(0, B, 8):
             assert not got[name][b].any(), name
+
+
+@pytest.mark.parametrize("io,shape", [("f32", (1, 3000, 2, 1, 64, 64)), ("f32", (2, 1501, 1, 1, 128, 40)), ("f32", (1, 1200, 1, 1, 16, 130)),
+                                      ("f32", (3, 999, 1, 1, 32, 8)), ("bf16", (1, 1100, 2, 2, 33, 66)), ("f16", (2, 900, 2, 1, 5, 7))], ids=str)
+def test_sequences_cut_in_time_without_tensor_cores(io, shape):
+    """Few heads of many tokens: segments, their sums and both carries; with and without rows that end early or hold nothing."""
+    B, L = shape[:2]
+    x = ref.gdr_inputs(*shape, seed=51)
+    check_fwd(x, io)
+    check_bwd(x, io)
+    for lengths in ([L // 3] * B, [0] * B, [(L, 130, 64)[i % 3] for i in range(B)]):
+        check_fwd(x, io, lengths=lengths)
+        check_bwd(x, io, lengths=lengths)
+    for key in ("h0", "dlast", "g"):
+        x[key] = None
+    check_fwd(x, io)
+    check_bwd(x, io)
