@@ -765,18 +765,23 @@ cudaError_t launch_segments(const WalkArgs& w, const WalkArgs* back, cudaStream_
     return cudaGetLastError();
 }
 
-// Costs in tiles walked by one block; some two blocks an SM walk as fast as one.  A segment's carry is most of a tile's
-// time, three launches four.
+// Costs in tiles walked by a block alone on its SM.  Blocks beside it, measured: two take 1.05 to 1.18 of its time, three 1.34 to
+// 1.48, four 1.4 to 1.8, and further ones begin another round.  A segment's carry is most of a tile's time, two launches two.
 WalkPlan walk_plan(int64_t heads, int64_t N, int64_t P, int64_t L, bool backward) {
     const int64_t pt = 64 / walk_lanes(N), wide = ceil_div(P, pt), deep = ceil_div(N, pt), tiles = ceil_div(L, kWalkT), chunk = kChunk / kWalkT;
     const int64_t both = backward ? 2 : 1;
-    auto rounds = [](int64_t blocks) { return blocks <= 2 * kSms ? 1.0 : (double)blocks / (2 * kSms); };
+    auto rounds = [](int64_t blocks) {
+        constexpr double beside[4] = {0.0, 1.0, 1.1, 1.4};
+        const int64_t n = ceil_div(blocks, kSms);
+        return 1.65 * (double)(n / 4) + beside[n % 4];
+    };
     WalkPlan best = {1, tiles};
     double least = rounds(heads * wide * both) * tiles;
     for (int64_t K = 2; K <= 64 && 2 * K * chunk <= tiles; K++) {
         const int64_t seg = ceil_div(ceil_div(tiles, K), chunk) * chunk;
         if (ceil_div(tiles, seg) != K) continue;
-        const double cost = (rounds(heads * (wide * both + deep) * K) + rounds(heads * wide * both * K)) * seg + 0.8 * K + 4;
+        const int64_t sums = heads * (wide * both * (K - 1) + deep * (backward ? K : K - 1));
+        const double cost = (rounds(sums) + rounds(heads * wide * both * K)) * seg + 0.8 * K + 2;
         if (cost < 0.9 * least) {
             least = cost;
             best = {K, seg};
