@@ -112,14 +112,16 @@ bool tc_input(const In& x, int64_t L, int64_t Bsz) {
 // tile) units than SMs, or a last round of them leaves SMs idle.  Costs in chunks walked by one
 // block: the walk itself, the segments' two sums before it, two a segment for the carry, four for
 // the launches.
-TcPlan tc_plan(int64_t heads, int64_t ptiles, int64_t chunks) {
+TcPlan tc_plan(int64_t heads, int64_t ptiles, int64_t chunks, bool backward) {
+    const int64_t wide = backward ? 2 * ptiles : ptiles;  // both directions' walks
     auto rounds = [](int64_t blocks) { return ceil_div(blocks, kSms); };
     TcPlan best = {1, chunks};
-    double least = (double)(rounds(heads * ptiles) * chunks);
+    double least = (double)(rounds(heads * wide) * chunks);
     for (int64_t K = 2; K <= 128 && 2 * K <= chunks; K++) {
         const int64_t per = ceil_div(chunks, K);
         if (ceil_div(chunks, per) != K) continue;
-        const double cost = (double)((rounds(heads * ptiles * K) + rounds(heads * (ptiles + 1) * (K - 1))) * per + 2 * K + 4);
+        const int64_t sums = heads * (wide * (K - 1) + (backward ? K : K - 1));
+        const double cost = (double)((rounds(heads * wide * K) + rounds(sums)) * per + 2 * K + 4);
         if (cost < 0.95 * least) {
             least = cost;
             best = {K, per};
@@ -136,7 +138,7 @@ struct FwdTc {
 FwdTc fwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
     FwdTc f;
     f.chunks = ceil_div(L, kChunk);
-    f.plan = tc_plan(Bsz * H, ceil_div(P, kTileP), f.chunks);
+    f.plan = tc_plan(Bsz * H, ceil_div(P, kTileP), f.chunks, false);
     f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
     f.images = l.take((size_t)Bsz * H * f.chunks * image_bytes(fwd_parts(dtype)));
     const bool cut = f.plan.K > 1;
@@ -187,20 +189,26 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     w.seg_state = reinterpret_cast<float*>(ws + f.state);
     w.seg_phi = reinterpret_cast<float*>(ws + f.phi);
     w.yp = y;
+    w.parts = fwd_parts(a.dtype);
     if (launch_prep(p, fwd_parts(a.dtype), st) != cudaSuccess) return SS_ERR_CUDA;
-    if (w.plan.K > 1 && (launch_tc_walk(w, kTcSum, st) != cudaSuccess || launch_tc_carry(w, st) != cudaSuccess)) return SS_ERR_CUDA;
+    if (w.plan.K > 1 && (launch_tc_walk(w, kTcSum, st) != cudaSuccess || launch_tc_carry(w, nullptr, st) != cudaSuccess)) return SS_ERR_CUDA;
     return launch_tc_walk(w, kTcY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 struct BwdTc {
+    TcPlan plan;
     int64_t chunks;
     int splits;
-    size_t keys, images, before, after, us, xs, dys, before_inv, after_inv, u_inv, x_inv, dy_inv, dq, dk;
+    size_t starts, ends, phi, phi_t, keys, images, before, after, us, xs, dys, before_inv, after_inv, u_inv, x_inv, dy_inv, dq, dk;
 };
 BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     BwdTc f;
     f.chunks = ceil_div(L, kChunk);
     f.splits = prep_splits(Bsz * f.chunks * G, H / G);
+    f.plan = tc_plan(Bsz * H, ceil_div(P, kTileP), f.chunks, true);
+    const size_t segs = f.plan.K > 1 ? (size_t)Bsz * H * f.plan.K : 0;
+    for (size_t* x : {&f.starts, &f.ends}) *x = l.take(segs * N * P * 4);
+    for (size_t* x : {&f.phi, &f.phi_t}) *x = l.take(segs * N * N * 4);
     const size_t heads = (size_t)Bsz * H * f.chunks, tiles = heads * ceil_div(P, kTileP);
     f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
     f.images = l.take(heads * image_bytes(2));
@@ -245,7 +253,12 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     p.images = ws + f.images;
     p.status = w.status;
     w.a = a;
-    w.plan = {1, f.chunks};
+    w.plan = f.plan;
+    w.seg_state = f32(f.starts);
+    w.seg_phi = f32(f.phi);
+    w.seg_phi_t = f32(f.phi_t);
+    w.parts = 2;
+    r.seg_state = f32(f.ends);
     w.chunks = f.chunks;
     w.keys = p.keys;
     w.images = p.images;
@@ -285,7 +298,9 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     c.dg = d.dg;
     c.dbeta = d.dbeta;
     c.status = w.status;
-    if (launch_prep(p, 2, st) != cudaSuccess || launch_dy(a, f.chunks, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess || launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_prep(p, 2, st) != cudaSuccess || launch_dy(a, f.chunks, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess) return SS_ERR_CUDA;
+    if (w.plan.K > 1 && (launch_tc_sums(w, r, st) != cudaSuccess || launch_tc_carry(w, &r, st) != cudaSuccess)) return SS_ERR_CUDA;
+    if (launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
     if (f.splits > 1 &&
         la::launch_sum_parts(c.dq_part, d.dq, c.dk_part, d.dk, f.splits, a.Bsz * a.L * a.G * a.N, a.dtype, st) != cudaSuccess)
         return SS_ERR_CUDA;

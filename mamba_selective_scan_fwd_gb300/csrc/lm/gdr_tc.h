@@ -80,7 +80,9 @@ struct TcWalkArgs {
     const float* init;  // h0, or null (plan.K == 1)
     float* last;        // or null
     float* seg_state;   // [Bsz, H, K, N, P]: E of each segment, then (after the carry) the states they start from
-    float* seg_phi;     // [Bsz, H, K, N, N]
+    float* seg_phi;     // [Bsz, H, K, N, N], transposed
+    float* seg_phi_t;   // the backward's: the same as it is
+    int parts;          // of P in the images
     void* yp;           // y again, for rows that no copy writes
     char *states, *us;  // kTcKeep: images [Bsz, H, value tiles, chunks]
     float *state_inv, *u_inv;  // what undoes each image's scale
@@ -95,6 +97,7 @@ struct TcBackArgs {
     float* last;        // dh0, or null
     char *states, *xs;
     float *state_inv, *x_inv;
+    float* seg_state;   // what a segment does to an adjoint of zero, then the adjoints they start from
 };
 cudaError_t launch_dy(const Args& a, int64_t chunks, char* dys, float* dy_inv, cudaStream_t st);
 // What is left of the backward, one chunk at a time.
@@ -113,7 +116,8 @@ struct TcChunkArgs {
 // state before each chunk and U, as operand images.
 enum TcWalkMode { kTcY, kTcSum, kTcKeep };
 cudaError_t launch_tc_walk(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st);
-cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st);
+cudaError_t launch_tc_sums(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st);  // the backward's, plan.K > 1
+cudaError_t launch_tc_carry(const TcWalkArgs& w, const TcBackArgs* r, cudaStream_t st);
 cudaError_t launch_tc_walks(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st);  // kTcKeep and the backward's, at once
 cudaError_t launch_tc_chunks(const TcChunkArgs& c, cudaStream_t st);
 

@@ -151,8 +151,7 @@ __device__ __forceinline__ void tmem_bits(uint32_t addr, uint32_t (&r)[32]) {
 // blockIdx.y of kTcSum: 0 walks from zero (E), 1 from the identity without v (Phi).
 template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void walk(const TcWalkArgs& w, char* sm) {
     constexpr bool SUM = MODE == kTcSum, OUT = MODE == kTcY, KEEP = MODE == kTcKeep;
-    // (the backward's images hold P in two parts)
-    constexpr int W = 32 * NB, PP = kPParts<T>, IP = KEEP ? 2 : PP;
+    constexpr int W = 32 * NB, PP = kPParts<T>;
     using L = Stage<NB, PP, OUT>;
     // landed; stage free; S; D1; X; D2; e U; D3; U; U^T P^T; read by the third warpgroup: early, late
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_uy, s_y, s_early, s_late;
@@ -167,6 +166,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
     id /= ptiles;
     if (phi && pt > 0) return;  // N <= 128 columns
     const int64_t bh = id % (a.Bsz * a.H), seg = id / (a.Bsz * a.H);
+    if (SUM && !phi && seg == w.plan.K - 1) return;  // nothing follows it
     const int64_t b = bh / a.H, h = bh % a.H, hq = h / (a.H / a.G);
     const int64_t len = row_length(a, b);
     const int64_t c_begin = seg * w.plan.seg, t_begin = c_begin * C, t_end = min(a.L, (c_begin + w.plan.seg) * C);
@@ -359,6 +359,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
 #pragma unroll
                 for (int n = 0; n < W; n += 4)
                     if (half * W + n < a.N) *reinterpret_cast<float4*>(col + half * W + n) = make_float4(S[n], S[n + 1], S[n + 2], S[n + 3]);
+                if (w.seg_phi_t) to = w.seg_phi_t + (bh * w.plan.K + seg) * a.N * a.N;
             } else if (SUM) to = w.seg_state + (bh * w.plan.K + seg) * a.N * a.P;
             else if (seg == w.plan.K - 1 && w.last) to = w.last + bh * a.N * a.P;
             if (to)
@@ -462,7 +463,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         const int role = __shfl_sync(kFull, warp, 0) - (kThreads - 128) / 32, steps = __shfl_sync(kFull, chunks, 0);
         if (role == 1 && lane == 0) {  // loads
             const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
-            const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(IP);
+            const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(w.parts);
             auto load = [&](int ch) {
                 char* at = sm + (ch & 1) * L::bytes;
                 uint64_t* bar = &s_full[ch & 1];
@@ -476,9 +477,9 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     la::tma_load_4d(at + L::v, &w.v, (int)p0, (int)h, t0, (int)b, bar);
                     la::tma_load_4d(at + L::v + kTileBytes, &w.v, (int)p0 + 64, (int)h, t0, (int)b, bar);
                 }
-                const char* im = images + (int64_t)ch * image_bytes(IP);
+                const char* im = images + (int64_t)ch * image_bytes(w.parts);
                 bulk_load(at + L::image, im, (2 + (OUT ? PP : 0)) * kTileBytes, bar);
-                bulk_load(at + L::head, im + (2 + IP) * kTileBytes, (int)sizeof(ImageHead), bar);
+                bulk_load(at + L::head, im + (2 + w.parts) * kTileBytes, (int)sizeof(ImageHead), bar);
             };
             for (int ch = 0; ch < chunks; ch++) {
                 if (ch > 1 && !wait(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
@@ -568,7 +569,8 @@ template <int NB> struct BackStage {
 // scale e^c dY
 constexpr uint32_t bD1 = 0, bD0 = 64, bD3 = 128, bR = 256, bX = 384, bDq = 448;
 
-template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w, const TcBackArgs& r, int64_t id, char* sm) {
+// SUM: a segment's, from an adjoint of zero; no images.
+template <int NB, bool SUM> __device__ __forceinline__ void walk_back(const TcWalkArgs& w, const TcBackArgs& r, int64_t id, char* sm) {
     constexpr int W = 32 * NB;
     using L = BackStage<NB>;
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_r, s_d1, s_dq, s_x, s_d2, s_u, s_d3, s_dyq, s_xi, s_early, s_late;
@@ -576,9 +578,10 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
     __shared__ float s_most[2][128], s_ud[2][128], s_xe[2][128], s_xm[2][128], s_rs[2][128], s_xsc[2][128], s_dqs[2][128];
     const Args& a = w.a;
     const int tid = threadIdx.x, warp = tid >> 5, pl = tid & 127;
-    const int64_t ptiles = (a.P + kTileP - 1) / kTileP, pt = id % ptiles, p0 = pt * kTileP, bh = id / ptiles;
-    const int64_t b = bh / a.H, h = bh % a.H, hq = h / (a.H / a.G), len = row_length(a, b);
-    const int chunks = (int)((len + C - 1) / C);
+    const int64_t ptiles = (a.P + kTileP - 1) / kTileP, pt = id % ptiles, p0 = pt * kTileP, bh = id / ptiles % (a.Bsz * a.H), seg = id / ptiles / (a.Bsz * a.H);
+    const int64_t b = bh / a.H, h = bh % a.H, hq = h / (a.H / a.G), len = row_length(a, b), c_begin = seg * w.plan.seg;
+    if (SUM && seg == 0) return;  // nothing comes before it
+    const int chunks = (int)max((int64_t)0, min((len + C - 1) / C, c_begin + w.plan.seg) - c_begin);
     if (tid == 0) {
         for (uint64_t* bar : {&s_full[0], &s_full[1], &s_d1, &s_dq, &s_d2, &s_d3}) mbar_init(bar, 1);
         for (uint64_t* bar : {&s_r, &s_x, &s_u, &s_xi}) mbar_init(bar, kStateThreads / 32);
@@ -592,7 +595,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
     la::tc_fence_after();
     const uint32_t tm = __shfl_sync(kFull, s_tm, 0), my = (uint32_t)((warp & 3) * 32) << 16;
     char* staging = sm + 2 * L::bytes;
-    auto chunk_of = [&](int i) { return chunks - 1 - i; };
+    auto chunk_of = [&](int i) { return (int)c_begin + chunks - 1 - i; };
     const int64_t images = (bh * ptiles + pt) * w.chunks;
 
     if (warp < kStateThreads / 32) {
@@ -601,7 +604,8 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
         const int64_t p = p0 + pl;
         const bool mine = p < a.P;
         float R[W];
-        const float* from = r.init ? r.init + bh * a.N * a.P : nullptr;
+        float* const seg_state = w.plan.K > 1 ? r.seg_state + (bh * w.plan.K + seg) * a.N * a.P : nullptr;
+        const float* from = SUM ? nullptr : seg_state ? seg_state : r.init ? r.init + bh * a.N * a.P : nullptr;
 #pragma unroll
         for (int n = 0; n < W; n++) R[n] = from && mine && half * W + n < a.N ? from[(half * W + n) * a.P + p] : 0.0f;
         auto pair_sync = [&] { named_sync(1 + (warp & 3), 64); };
@@ -616,7 +620,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             char* at = sm + ph * L::bytes;
             const ImageHead* head = reinterpret_cast<const ImageHead*>(at + L::head);
             const float rs = scale_of(bound), dy_inv = r.dy_inv[images + chunk_of(i)];
-            if (i > 0) ok = ok && wait(&s_early, ph ^ 1, &s_fail);
+            if (!SUM && i > 0) ok = ok && wait(&s_early, ph ^ 1, &s_fail);
             if (half == 0) s_rs[ph][pl] = rs;
 #pragma unroll
             for (int c = 0; c < NB; c++) {
@@ -696,7 +700,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             la::tmem_wait_st();
             bound = finite(fmaf(64.0f * k_most, ud_most, fmaf(64.0f * head->most_q, 16384.0f / dqs, r_most * (keep + fabsf(by)))));
             arrive(&s_u);
-            {
+            if (!SUM) {
                 s_xm[half][pl] = max_abs<32>(x);
                 pair_sync();
                 const float xi = scale_of(max_over(s_xm));
@@ -720,8 +724,8 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                 }
             }
         }
-        if (mine && ok && r.last) {
-            float* to = r.last + bh * a.N * a.P;
+        if (mine && ok && (SUM || (r.last && seg == 0))) {
+            float* to = SUM ? seg_state : r.last + bh * a.N * a.P;
 #pragma unroll
             for (int n = 0; n < W; n++)
                 if (half * W + n < a.N) to[(half * W + n) * a.P + p] = R[n];
@@ -764,6 +768,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
             }
             la::tmem_wait_st();
             arrive(&s_dyq);
+            if (SUM) continue;
             // R's and X's parts under one scale each: what the largest channel's is
             wait(&s_r, ph, &s_fail);
             la::tc_fence_after();
@@ -819,7 +824,7 @@ template <int NB> __device__ __forceinline__ void walk_back(const TcWalkArgs& w,
                         for (int s = 0; s < 4; s++)
                             la::mma(tm + bD0, la::smem_desc(at + L::dy + s * 32), la::smem_desc(P + part * kTileBytes + s * 2048), dR, part < 1 || s > 0);
                 }
-                if (i > 0 && !warp_wait(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
+                if (!SUM && i > 0 && !warp_wait(&s_late, ph ^ 1, &s_fail)) break;  // X has left D1's columns
                 if (!warp_wait(&s_r, ph, &s_fail)) break;
                 la::tc_fence_after();
                 if (elect()) {
@@ -872,15 +877,22 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(kThreads, 1) k_walks(const __grid_constant__ TcWalkArgs w, const __grid_constant__ TcBackArgs r, int forward) {
     extern __shared__ __align__(1024) char sm[];
     if ((int)blockIdx.x < forward) walk<T, NB, kTcKeep>(w, sm);
-    else walk_back<NB>(w, r, blockIdx.x - forward, sm);
+    else walk_back<NB, false>(w, r, blockIdx.x - forward, sm);
+}
+// blockIdx.y: E, Phi, E'
+template <typename T, int NB>
+__global__ void __launch_bounds__(kThreads, 1) k_sums(const __grid_constant__ TcWalkArgs w, const __grid_constant__ TcBackArgs r) {
+    extern __shared__ __align__(1024) char sm[];
+    if (blockIdx.y < 2) walk<T, NB, kTcSum>(w, sm);
+    else walk_back<NB, true>(w, r, blockIdx.x, sm);
 }
 
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
-// from.  A block: 8 columns of one head's state, in shared memory.  Warp w takes the terms of states w, w + 8, ..: a lane
+// from.  blockIdx.y 1: R <- Phi^T R + E' from the last.  A block: 8 columns of one head's state, in shared memory.  Warp w takes the terms of states w, w + 8, ..: a lane
 // four rows and all columns; the warps' sums are added in order.  The next Phi (transposed) is on its way while one is
 // used.  Bound by reading shared memory.  65536 tokens, 8 heads, 19 segments: 51 us (sums over states in single threads: 86).
 constexpr int kCarryCols = 8;
-__global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
+__global__ void __launch_bounds__(256) k_carry(TcWalkArgs w, TcBackArgs r) {
     extern __shared__ __align__(16) float phi[];  // [2][N][N], then the warps' sums [8][N][8]
     __shared__ __align__(16) float s[la::kMaxN][kCarryCols];
     __shared__ __align__(8) uint64_t s_full[2];
@@ -888,7 +900,11 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = (int)a.N, n = tid >> 1, c = (tid & 1) * 4;
     const int64_t ptiles = (a.P + kCarryCols - 1) / kCarryCols, p0 = blockIdx.x % ptiles * kCarryCols, bh = blockIdx.x / ptiles;
+    const bool back = blockIdx.y == 1;
+    const float *phis = back ? w.seg_phi_t : w.seg_phi, *init = back ? r.init : w.init;
+    float* const states = back ? r.seg_state : w.seg_state;
     const int K = (int)w.plan.K;
+    auto segment = [&](int k) { return bh * K + (back ? K - 1 - k : k); };
     float* sums = phi + 2 * N * N;
     if (tid == 0) {
         mbar_init(&s_full[0], 1);
@@ -898,15 +914,15 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w) {
     }
     auto load = [&](int k) {
         mbar_expect_tx(&s_full[k & 1], N * N * 4);
-        bulk_load(phi + (k & 1) * N * N, w.seg_phi + (bh * K + k) * N * N, N * N * 4, &s_full[k & 1]);
+        bulk_load(phi + (k & 1) * N * N, phis + segment(k) * N * N, N * N * 4, &s_full[k & 1]);
     };
     const bool mine = n < N;  // (P is a multiple of 8)
     float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (mine && w.init) x = *reinterpret_cast<const float4*>(w.init + (bh * N + n) * a.P + p0 + c);
+    if (mine && init) x = *reinterpret_cast<const float4*>(init + (bh * N + n) * a.P + p0 + c);
     __syncthreads();
     if (tid == 0) load(0);
     for (int k = 0; k < K; k++) {
-        float4* at = reinterpret_cast<float4*>(w.seg_state + ((bh * K + k) * N + n) * a.P + p0 + c);
+        float4* at = reinterpret_cast<float4*>(states + (segment(k) * N + n) * a.P + p0 + c);
         float4 e = {0.0f, 0.0f, 0.0f, 0.0f};
         if (mine) {
             if (k + 1 < K) e = *at;
@@ -971,8 +987,15 @@ template <typename T, int NB> cudaError_t walks_go(const TcWalkArgs& w, const Tc
     constexpr int keep = 2 * Stage<NB, kPParts<T>, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = (keep > back ? keep : back) + kRing * kPieceBytes;
     const cudaError_t e = la::allow_smem<k_walks<T, NB>>(bytes);
     if (e != cudaSuccess) return e;
-    const int64_t units = ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H;
+    const int64_t units = ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H * w.plan.K;
     k_walks<T, NB><<<(unsigned)(2 * units), kThreads, bytes, st>>>(w, r, (int)units);
+    return cudaGetLastError();
+}
+template <typename T, int NB> cudaError_t sums_go(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
+    constexpr int fwd = 2 * Stage<NB, kPParts<T>, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = fwd > back ? fwd : back;
+    const cudaError_t e = la::allow_smem<k_sums<T, NB>>(bytes);
+    if (e != cudaSuccess) return e;
+    k_sums<T, NB><<<dim3((unsigned)(ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H * w.plan.K), 3), kThreads, bytes, st>>>(w, r);
     return cudaGetLastError();
 }
 template <typename T, int NB> cudaError_t walk_mode(const TcWalkArgs& w, TcWalkMode mode, cudaStream_t st) {
@@ -992,11 +1015,16 @@ cudaError_t launch_tc_walks(const TcWalkArgs& w, const TcBackArgs& r, cudaStream
     return w.a.N <= 64 ? walks_go<__nv_bfloat16, 1>(w, r, st) : walks_go<__nv_bfloat16, 2>(w, r, st);
 }
 
-cudaError_t launch_tc_carry(const TcWalkArgs& w, cudaStream_t st) {
+cudaError_t launch_tc_sums(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
+    if (w.a.dtype == 1) return w.a.N <= 64 ? sums_go<__half, 1>(w, r, st) : sums_go<__half, 2>(w, r, st);
+    return w.a.N <= 64 ? sums_go<__nv_bfloat16, 1>(w, r, st) : sums_go<__nv_bfloat16, 2>(w, r, st);
+}
+
+cudaError_t launch_tc_carry(const TcWalkArgs& w, const TcBackArgs* r, cudaStream_t st) {
     const int N = (int)w.a.N, bytes = (2 * N * N + 8 * N * kCarryCols) * 4;
     const cudaError_t e = la::allow_smem<k_carry>((2 * la::kMaxN * la::kMaxN + 8 * la::kMaxN * kCarryCols) * 4);
     if (e != cudaSuccess) return e;
-    k_carry<<<(unsigned)(ceil_div(w.a.P, kCarryCols) * w.a.Bsz * w.a.H), 256, bytes, st>>>(w);
+    k_carry<<<dim3((unsigned)(ceil_div(w.a.P, kCarryCols) * w.a.Bsz * w.a.H), r ? 2 : 1), 256, bytes, st>>>(w, r ? *r : TcBackArgs{});
     return cudaGetLastError();
 }
 

@@ -222,3 +222,17 @@ def test_sequences_cut_in_time_without_tensor_cores(io, shape):
         x[key] = None
     check_fwd(x, io)
     check_bwd(x, io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(1, 3001, 2, 1, 128, 128), (2, 2900, 1, 1, 64, 200), (1, 4097, 3, 3, 16, 64)], ids=str)
+def test_backward_of_sequences_cut_in_time(shape, io):
+    """Segments of both directions, rows that end in the first one or hold nothing, and no states at either end."""
+    B, L = shape[:2]
+    x = ref.gdr_inputs(*shape, seed=61)
+    check_bwd(x, io)
+    check_bwd(x, io, lengths=[(L // 4, 0)[i % 2] for i in range(B)])
+    check_bwd(x, io, lengths=[L - 70] * B)
+    for key in ("h0", "dlast"):
+        x[key] = None
+    check_bwd(x, io)
