@@ -110,8 +110,8 @@ bool tc_input(const In& x, int64_t L, int64_t Bsz) {
 
 // Segments that the walks over time are cut into: where there are fewer (batch row, head, value
 // tile) units than SMs, or a last round of them leaves SMs idle.  Costs in chunks walked by one
-// block: the walk itself, the segments' two sums before it, two a segment for the carry, four for
-// the launches.
+// block: the walks themselves, the segments' sums before them (backward: of both directions), two a segment for the carry,
+// four for the launches.
 TcPlan tc_plan(int64_t heads, int64_t ptiles, int64_t chunks, bool backward) {
     const int64_t wide = backward ? 2 * ptiles : ptiles;  // both directions' walks
     auto rounds = [](int64_t blocks) { return ceil_div(blocks, kSms); };

@@ -119,7 +119,8 @@ template <typename T> __global__ void __launch_bounds__(128) k_pairs(Args a, Pai
 // with four interleaved chains of sums and q held in registers 149).
 //
 // Few heads of many tokens are cut into segments (walk_plan): the same walk takes their sums, whose columns (N of Phi, P of E)
-// are as independent, a carry joins them, and the walk proper starts from what it left.
+// are as independent, a carry joins them, and the walk proper starts from what it left.  Backward of 777 tokens, 16 heads, N 32,
+// P 64: 92 us in one piece, sums 31, carry 7 and walks 34 in four.
 template <int LN, WalkMode MODE> struct WalkStage {
     static constexpr bool Q = MODE != kWalkSum && MODE != kWalkKeep;
     float k[kWalkT][16 * LN], q[Q ? kWalkT : 1][16 * LN], v[kWalkT][64 / LN];
