@@ -356,13 +356,15 @@ template <typename T, int LN, WalkMode MODE> __device__ __forceinline__ void wal
     else if (SUM || MODE == kWalkBackSum) state(seg_state, true);
     else if (w.last && seg == (BACK ? 0 : w.plan.K - 1)) state(w.last + bh * NPel, true);
 }
-template <typename T, int LN> __global__ void __launch_bounds__(64) k_walk(WalkArgs w) { walk<T, LN, kWalkY>(w, blockIdx.x); }
-template <typename T, int LN> __global__ void __launch_bounds__(64) k_walks(WalkArgs keep, WalkArgs back) {
+// FIT blocks an SM: left alone the walk takes 200 registers and more and four blocks fit; held to six it is 2 to 3 % slower where
+// there are few, and from five on faster (112 tokens, N = P = 128, four blocks an SM 30.6 and 31.3 us, six 59.5 and 39.7).
+template <typename T, int LN, int FIT> __global__ void __launch_bounds__(64, FIT) k_walk(WalkArgs w) { walk<T, LN, kWalkY>(w, blockIdx.x); }
+template <typename T, int LN, int FIT> __global__ void __launch_bounds__(64, FIT) k_walks(WalkArgs keep, WalkArgs back) {
     if (blockIdx.y == 0) walk<T, LN, kWalkKeep>(keep, blockIdx.x);
     else walk<T, LN, kWalkBack>(back, blockIdx.x);
 }
 // blockIdx.y: 0 Phi, 1 E, 2 E'.  Nothing follows the last segment, nothing comes before the first.
-template <typename T, int LN> __global__ void __launch_bounds__(64) k_sums(WalkArgs w, WalkArgs back) {
+template <typename T, int LN> __global__ void __launch_bounds__(64, 6) k_sums(WalkArgs w, WalkArgs back) {
     constexpr int PT = 64 / LN;
     const int64_t wide = ((blockIdx.y == 0 ? w.a.N : w.a.P) + PT - 1) / PT, K = w.plan.K, seg = blockIdx.x / wide % K;
     if (blockIdx.x >= wide * K * w.a.H * w.a.Bsz) return;
@@ -697,8 +699,8 @@ template <typename T, int LN> cudaError_t walk_go(Launch what, const WalkArgs& w
     constexpr int y = 2 * sizeof(WalkStage<LN, kWalkY>), sum = 2 * sizeof(WalkStage<LN, kWalkSum>);
     const int64_t rows = w.a.H * w.a.Bsz * w.plan.K, wide = ceil_div(w.a.P, 64 / LN), deep = ceil_div(w.a.N, 64 / LN);
     const unsigned grid = (unsigned)(wide * rows);
-    if (what == kOne) k_walk<T, LN><<<grid, 64, y, st>>>(w);
-    else if (what == kBoth) k_walks<T, LN><<<dim3(grid, 2), 64, y, st>>>(w, *back);
+    if (what == kOne) (grid > 4 * kSms ? k_walk<T, LN, 6> : k_walk<T, LN, 1>)<<<grid, 64, y, st>>>(w);
+    else if (what == kBoth) (2 * (int64_t)grid > 4 * kSms ? k_walks<T, LN, 6> : k_walks<T, LN, 1>)<<<dim3(grid, 2), 64, y, st>>>(w, *back);
     else k_sums<T, LN><<<dim3((unsigned)((wide > deep ? wide : deep) * rows), back ? 3 : 2), 64, back ? y : sum, st>>>(w, back ? *back : w);
     return cudaGetLastError();
 }
@@ -767,14 +769,14 @@ cudaError_t launch_segments(const WalkArgs& w, const WalkArgs* back, cudaStream_
 }
 
 // Costs in tiles walked by a block alone on its SM.  Blocks beside it, measured: two take 1.05 to 1.18 of its time, three 1.34 to
-// 1.48, four 1.4 to 1.8, and further ones begin another round.  A segment's carry is most of a tile's time, two launches two.
+// 1.48, four 1.4 to 1.8, five 1.9 to 2.1, six 1.9 to 2.3, and further ones begin another round.  A segment's carry is most of a tile's time, two launches two.
 WalkPlan walk_plan(int64_t heads, int64_t N, int64_t P, int64_t L, bool backward) {
     const int64_t pt = 64 / walk_lanes(N), wide = ceil_div(P, pt), deep = ceil_div(N, pt), tiles = ceil_div(L, kWalkT), chunk = kChunk / kWalkT;
     const int64_t both = backward ? 2 : 1;
     auto rounds = [](int64_t blocks) {
-        constexpr double beside[4] = {0.0, 1.0, 1.1, 1.4};
+        constexpr double beside[6] = {0.0, 1.0, 1.1, 1.4, 1.65, 2.0};
         const int64_t n = ceil_div(blocks, kSms);
-        return 1.65 * (double)(n / 4) + beside[n % 4];
+        return 2.2 * (double)(n / 6) + beside[n % 6];
     };
     WalkPlan best = {1, tiles};
     double least = rounds(heads * wide * both) * tiles;
