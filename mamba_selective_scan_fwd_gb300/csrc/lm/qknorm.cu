@@ -25,7 +25,8 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint64_t kNoAngle = ~0ull;  // a frequency that is not finite (fractions end at 2^64 - 2^11)
+// A frequency that is not finite.  (No fraction is this: those of 2^62 and more come from 53 bits and are multiples of 2^10.)
+constexpr uint64_t kNoAngle = (1ull << 62) + 1;
 constexpr int kTable = 1024;  // angles a tile of tokens may need (8 KB)
 constexpr int kTile = 128;    // tokens of a tile at most
 
@@ -71,8 +72,9 @@ __global__ void __launch_bounds__(kThreads) k_qknorm(NormArgs a, int64_t tile, i
     const int64_t tokens = a.Bsz * a.L;
     for (int i = tid; i < pairs; i += kThreads) {
         const double t = (double)a.freqs[i] * 0.15915494309189533577;  // turns a token
-        const double f = t - floor(t);
-        s_freq[i] = isfinite(t) ? (uint64_t)(f * 18446744073709551616.0) : kNoAngle;
+        double f = t - rint(t);  // exact: the distance to the whole turn below would round tiny negative ones to one
+        if (f >= 0.5) f -= 1.0;  // -1/2 .. 1/2, what 64 bits hold with their sign
+        s_freq[i] = isfinite(t) ? (uint64_t)(int64_t)(f * 18446744073709551616.0) : kNoAngle;
     }
     // the lane's runs: channels ia .. + V - 1 and ib ..; turned: the angles i0 .. (of the row's table), V or V / 2 a run
     int ia[SPT], ib[SPT], i0[SPT];
