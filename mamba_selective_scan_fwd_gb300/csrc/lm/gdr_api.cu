@@ -135,12 +135,12 @@ struct FwdTc {
     int64_t chunks;
     size_t keys, images, state, phi;
 };
-FwdTc fwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P, int dtype) {
+FwdTc fwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     FwdTc f;
     f.chunks = ceil_div(L, kChunk);
     f.plan = tc_plan(Bsz * H, ceil_div(P, kTileP), f.chunks, false);
     f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
-    f.images = l.take((size_t)Bsz * H * f.chunks * image_bytes(fwd_parts(dtype)));
+    f.images = l.take((size_t)Bsz * H * f.chunks * kImageBytes);
     const bool cut = f.plan.K > 1;
     f.state = l.take(cut ? (size_t)Bsz * H * f.plan.K * N * P * 4 : 0);
     f.phi = l.take(cut ? (size_t)Bsz * H * f.plan.K * N * N * 4 : 0);
@@ -163,7 +163,7 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     const auto encode = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (!encode) return SS_OK;
     Layout l;
-    const FwdTc f = fwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P, a.dtype);
+    const FwdTc f = fwdtc_layout(l, a.Bsz, a.L, a.H, a.G, a.N, a.P);
     TcWalkArgs w = {};
     PrepArgs p = {};
     const In yo = {y, a.H * a.P, a.L * a.H * a.P};
@@ -189,8 +189,7 @@ int tc_forward(const Args& a, void* y, float* last, char* ws, cudaStream_t st, b
     w.seg_state = reinterpret_cast<float*>(ws + f.state);
     w.seg_phi = reinterpret_cast<float*>(ws + f.phi);
     w.yp = y;
-    w.parts = fwd_parts(a.dtype);
-    if (launch_prep(p, fwd_parts(a.dtype), st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_prep(p, st) != cudaSuccess) return SS_ERR_CUDA;
     if (w.plan.K > 1 && (launch_tc_walk(w, kTcSum, st) != cudaSuccess || launch_tc_carry(w, nullptr, st) != cudaSuccess)) return SS_ERR_CUDA;
     return launch_tc_walk(w, kTcY, st) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
@@ -211,7 +210,7 @@ BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     for (size_t* x : {&f.phi, &f.phi_t}) *x = l.take(segs * N * N * 4);
     const size_t heads = (size_t)Bsz * H * f.chunks, tiles = heads * ceil_div(P, kTileP);
     f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
-    f.images = l.take(heads * image_bytes(2));
+    f.images = l.take(heads * kImageBytes);
     f.before = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
     f.after = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
     f.us = l.take(tiles * kRowsBytes);
@@ -257,7 +256,6 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     w.seg_state = f32(f.starts);
     w.seg_phi = f32(f.phi);
     w.seg_phi_t = f32(f.phi_t);
-    w.parts = 2;
     r.seg_state = f32(f.ends);
     w.chunks = f.chunks;
     w.keys = p.keys;
@@ -298,7 +296,7 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     c.dg = d.dg;
     c.dbeta = d.dbeta;
     c.status = w.status;
-    if (launch_prep(p, 2, st) != cudaSuccess || launch_dy(a, f.chunks, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_prep(p, st) != cudaSuccess || launch_dy(a, f.chunks, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess) return SS_ERR_CUDA;
     if (w.plan.K > 1 && (launch_tc_sums(w, r, st) != cudaSuccess || launch_tc_carry(w, &r, st) != cudaSuccess)) return SS_ERR_CUDA;
     if (launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
     if (f.splits > 1 &&
@@ -361,7 +359,7 @@ size_t ss_gdr_fwd_workspace_bytes(int64_t Bsz, int64_t L, int64_t H, int64_t G, 
     // the larger of what the two paths need: strides and pointers, which decide between them, are not known here
     Layout l, t;
     fwd32_layout(l, Bsz, L, H, N, P);
-    if (tc_sizes(L, N, P, dtype)) fwdtc_layout(t, Bsz, L, H, G, N, P, dtype);
+    if (tc_sizes(L, N, P, dtype)) fwdtc_layout(t, Bsz, L, H, G, N, P);
     return l.total > t.total ? l.total : t.total;
 }
 

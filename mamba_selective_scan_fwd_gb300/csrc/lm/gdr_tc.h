@@ -25,8 +25,7 @@ constexpr int kTileBytes = 8192;  // 64 rows of 64 16-bit values
 // Keys: per (batch row, chunk, head of q and k), for each 64 columns a tile of K and one of Q,
 // rows past the row's length zero.
 constexpr int key_bytes(int64_t N) { return (N > 64 ? 4 : 2) * kTileBytes; }
-// Image: per (batch row, head, chunk) tiles of M in two parts and of P in `parts`, then the
-// chunk's factors.
+// Image: per (batch row, head, chunk) tiles of M and of P, two parts each, then the chunk's factors.
 struct ImageHead {
     float up[kChunk];    // e^{c_t}
     float down[kChunk];  // e^{cl - c_t}
@@ -43,9 +42,7 @@ struct ImageHead {
     float pad[51];
 };
 static_assert(sizeof(ImageHead) == 2048, "bulk copies are multiples of 16 bytes");
-__host__ __device__ constexpr int image_bytes(int parts) { return (2 + parts) * kTileBytes + (int)sizeof(ImageHead); }
-// parts of P: y is good to the io type's half step with one for bf16, with two for f16
-constexpr int fwd_parts(int dtype) { return dtype == 1 ? 2 : 1; }
+constexpr int kImageBytes = 4 * kTileBytes + (int)sizeof(ImageHead);
 
 struct PrepArgs {
     CUtensorMap q, k;  // {width, heads, L, Bsz}, boxes of 64 columns x 64 tokens
@@ -56,7 +53,7 @@ struct PrepArgs {
     char* images;      // [Bsz, H, chunks]
     int* status;
 };
-cudaError_t launch_prep(const PrepArgs& w, int parts, cudaStream_t st);
+cudaError_t launch_prep(const PrepArgs& w, cudaStream_t st);
 
 // f16 images as the walks hold them, transposed: pieces of 128 value channels p by 64, one scale each image.  The
 // state (or its adjoint): [part][64 states n][p][64].  U and X: [part][p][64 tokens].  dY: [p][64 tokens], exact.
@@ -82,7 +79,6 @@ struct TcWalkArgs {
     float* seg_state;   // [Bsz, H, K, N, P]: E of each segment, then (after the carry) the states they start from
     float* seg_phi;     // [Bsz, H, K, N, N], transposed
     float* seg_phi_t;   // the backward's: the same as it is
-    int parts;          // of P in the images
     void* yp;           // y again, for rows that no copy writes
     char *states, *us;  // kTcKeep: images [Bsz, H, value tiles, chunks]
     float *state_inv, *u_inv;  // what undoes each image's scale

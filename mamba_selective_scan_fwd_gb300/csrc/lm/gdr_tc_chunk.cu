@@ -166,7 +166,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     auto load = [&](const Unit& u, int item) {
         const int64_t h = u.h_lo + item / ptiles, im = image_of(u, item);
         mbar_expect_tx(&s_in, 2 * kRowsBytes + kPieceBytes + (int)sizeof(ImageHead));
-        bulk_load(sm + L::head, w.images + ((u.b * a.H + h) * w.chunks + u.chunk) * image_bytes(2) + 4 * kTileBytes, (int)sizeof(ImageHead), &s_in);
+        bulk_load(sm + L::head, w.images + ((u.b * a.H + h) * w.chunks + u.chunk) * kImageBytes + 4 * kTileBytes, (int)sizeof(ImageHead), &s_in);
         bulk_load(Z, w.xs + im * kRowsBytes, kPieceBytes, &s_in);
         bulk_load(Zl, w.xs + im * kRowsBytes + kPieceBytes, kPieceBytes, &s_in);
         bulk_load(Z + kPieceBytes, w.dys + im * kPieceBytes, kPieceBytes, &s_in);

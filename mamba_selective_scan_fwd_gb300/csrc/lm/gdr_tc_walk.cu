@@ -19,8 +19,9 @@
 // Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken from the channel's
 // largest value, which its two threads exchange (for X by a bound instead: 245 us for 250, but a state of which a chunk leaves
 // 2^-15 is off by 10^-4 of that), or for S and R from a bound of some 2^5 above it, which costs none of the 22 bits;
-// the f32 state stays good to a few 1e-7.  P and U enter y's product with one part each for bf16 io (2^-12 of a y that is
-// rounded to 2^-9), with two for f16.
+// the f32 state stays good to a few 1e-7.  P and U too, for either io type: with one part each a bf16 y would be rounded twice
+// (2.6e-4 of itself off before its own 1.66e-3), for 1 to 3 % less time: 4 x 4096 tokens, 32 heads 383 us for 387, 65536 tokens,
+// 8 heads 758 for 780.
 #include "../simd.cuh"
 #include "gdr_tc.cuh"
 
@@ -28,7 +29,6 @@ namespace ss {
 namespace gdr {
 namespace {
 
-using la::kF16;
 using la::pack2;
 using la::unit;
 using la::unpack2;
@@ -43,12 +43,10 @@ template <int N> __device__ __forceinline__ void leave_regs() { asm volatile("se
 // parts of X, then of e U
 constexpr uint32_t kD1 = 0, kQ = 64, kD3 = 128, kY = 256, kS = 320, kX = 448;
 
-template <typename T> constexpr int kPParts = kF16<T> ? 2 : 1;  // of P and U in y's product
-
 // A stage of shared memory: tiles of K and Q by turns (not Q: kTcSum, kTcKeep), V, the image
-template <int NB, int PP, bool Q> struct Stage {
+template <int NB, bool Q> struct Stage {
     static constexpr int block = (Q ? 2 : 1) * kTileBytes;  // K (and Q) of 64 columns
-    static constexpr int v = NB * block, image = v + 2 * kTileBytes, head = image + (2 + (Q ? PP : 0)) * kTileBytes,
+    static constexpr int v = NB * block, image = v + 2 * kTileBytes, head = image + (Q ? 4 : 2) * kTileBytes,
                          bytes = head + 2048;
 };
 
@@ -84,12 +82,6 @@ __device__ __forceinline__ void put2(uint32_t hi, uint32_t lo, const float* x, f
     }
     la::tmem_st16(hi, r);
     la::tmem_st16(lo, q);
-}
-__device__ __forceinline__ void put1(uint32_t to, const float* x, float s) {
-    uint32_t r[16];
-#pragma unroll
-    for (int i = 0; i < 16; i++) r[i] = pack2<__half>(s * x[2 * i], s * x[2 * i + 1]);
-    la::tmem_st16(to, r);
 }
 template <int N> __device__ __forceinline__ float max_abs(const float* x) {
     float m[4] = {};
@@ -151,8 +143,8 @@ __device__ __forceinline__ void tmem_bits(uint32_t addr, uint32_t (&r)[32]) {
 // blockIdx.y of kTcSum: 0 walks from zero (E), 1 from the identity without v (Phi).
 template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void walk(const TcWalkArgs& w, char* sm) {
     constexpr bool SUM = MODE == kTcSum, OUT = MODE == kTcY, KEEP = MODE == kTcKeep;
-    constexpr int W = 32 * NB, PP = kPParts<T>;
-    using L = Stage<NB, PP, OUT>;
+    constexpr int W = 32 * NB;
+    using L = Stage<NB, OUT>;
     // landed; stage free; S; D1; X; D2; e U; D3; U; U^T P^T; read by the third warpgroup: early, late
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], s_s, s_d1, s_x, s_d2, s_u, s_d3, s_uy, s_y, s_early, s_late;
     __shared__ uint32_t s_tm, s_fail, s_red[4];
@@ -331,8 +323,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 const float uy = scale_of(most);
                 if (half == 0) s_us[ph][pl] = uy;
                 const uint32_t to = tm + my + kD1 + 16 * half;
-                if (KEEP || PP > 1) put2(to, to + 32, x, uy);
-                else put1(to, x, uy);
+                put2(to, to + 32, x, uy);
                 la::tmem_wait_st();
                 arrive(&s_uy);
             }
@@ -463,12 +454,12 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
         const int role = __shfl_sync(kFull, warp, 0) - (kThreads - 128) / 32, steps = __shfl_sync(kFull, chunks, 0);
         if (role == 1 && lane == 0) {  // loads
             const char* keys = w.keys + ((b * w.chunks + c_begin) * a.G + hq) * (NB * 2 * kTileBytes);
-            const char* images = w.images + (bh * w.chunks + c_begin) * image_bytes(w.parts);
+            const char* images = w.images + (bh * w.chunks + c_begin) * kImageBytes;
             auto load = [&](int ch) {
                 char* at = sm + (ch & 1) * L::bytes;
                 uint64_t* bar = &s_full[ch & 1];
                 const int t0 = (int)(t_begin + (int64_t)ch * C);
-                mbar_expect_tx(bar, (OUT ? 2 : 1) * NB * kTileBytes + (phi ? 0 : 2 * kTileBytes) + (2 + (OUT ? PP : 0)) * kTileBytes +
+                mbar_expect_tx(bar, (OUT ? 2 : 1) * NB * kTileBytes + (phi ? 0 : 2 * kTileBytes) + (OUT ? 4 : 2) * kTileBytes +
                                         (int)sizeof(ImageHead));
                 const char* kq = keys + ch * a.G * (NB * 2 * kTileBytes);
 #pragma unroll
@@ -477,9 +468,9 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     la::tma_load_4d(at + L::v, &w.v, (int)p0, (int)h, t0, (int)b, bar);
                     la::tma_load_4d(at + L::v + kTileBytes, &w.v, (int)p0 + 64, (int)h, t0, (int)b, bar);
                 }
-                const char* im = images + (int64_t)ch * image_bytes(w.parts);
-                bulk_load(at + L::image, im, (2 + (OUT ? PP : 0)) * kTileBytes, bar);
-                bulk_load(at + L::head, im + (2 + w.parts) * kTileBytes, (int)sizeof(ImageHead), bar);
+                const char* im = images + (int64_t)ch * kImageBytes;
+                bulk_load(at + L::image, im, (OUT ? 4 : 2) * kTileBytes, bar);
+                bulk_load(at + L::head, im + 4 * kTileBytes, (int)sizeof(ImageHead), bar);
             };
             for (int ch = 0; ch < chunks; ch++) {
                 if (ch > 1 && !wait(&s_free[ch & 1], ((ch >> 1) + 1) & 1, &s_fail)) break;
@@ -532,11 +523,11 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     la::tc_fence_after();
                     if (elect()) {
 #pragma unroll
-                        for (int o = PP > 1 ? 0 : 2; o < 3; o++)  // lo hi, hi lo, hi hi
+                        for (int o = 0; o < 3; o++)  // lo hi, hi lo, hi hi
 #pragma unroll
                             for (int s = 0; s < 4; s++)
                                 la::mma_ts(tm + kY, tm + kD1 + (o == 0 ? 32 : 0) + 8 * s, la::smem_desc(P + (o == 1 ? kTileBytes : 0) + s * 32), dP,
-                                           o > (PP > 1 ? 0 : 2) || s > 0);
+                                           o > 0 || s > 0);
                         la::mma_commit(&s_y);
                     }
                 }
@@ -806,7 +797,7 @@ template <int NB, bool SUM> __device__ __forceinline__ void walk_back(const TcWa
                 mbar_expect_tx(bar, NB * L::block + 6 * kTileBytes + (int)sizeof(ImageHead));
                 bulk_load(at, w.keys + ((b * w.chunks + ch) * a.G + hq) * (NB * 2 * kTileBytes), NB * L::block, bar);
                 bulk_load(at + L::dy, r.dys + (images + ch) * kPieceBytes, kPieceBytes, bar);
-                bulk_load(at + L::image, w.images + (bh * w.chunks + ch) * image_bytes(2), 4 * kTileBytes + (int)sizeof(ImageHead), bar);
+                bulk_load(at + L::image, w.images + (bh * w.chunks + ch) * kImageBytes, 4 * kTileBytes + (int)sizeof(ImageHead), bar);
             }
         } else if (role == 0) {  // products
             for (int i = 0; i < steps; i++) {
@@ -974,7 +965,7 @@ __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w, TcBackArgs r) {
 }
 
 template <typename T, int NB, TcWalkMode MODE> cudaError_t walk_go(const TcWalkArgs& w, cudaStream_t st) {
-    constexpr int bytes = 2 * Stage<NB, kPParts<T>, MODE == kTcY>::bytes +
+    constexpr int bytes = 2 * Stage<NB, MODE == kTcY>::bytes +
                           (MODE == kTcY ? 2 * kTileBytes : 0);
     const cudaError_t e = la::allow_smem<k_walk<T, NB, MODE>>(bytes);
     if (e != cudaSuccess) return e;
@@ -984,7 +975,7 @@ template <typename T, int NB, TcWalkMode MODE> cudaError_t walk_go(const TcWalkA
     return cudaGetLastError();
 }
 template <typename T, int NB> cudaError_t walks_go(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
-    constexpr int keep = 2 * Stage<NB, kPParts<T>, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = (keep > back ? keep : back) + kRing * kPieceBytes;
+    constexpr int keep = 2 * Stage<NB, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = (keep > back ? keep : back) + kRing * kPieceBytes;
     const cudaError_t e = la::allow_smem<k_walks<T, NB>>(bytes);
     if (e != cudaSuccess) return e;
     const int64_t units = ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H * w.plan.K;
@@ -992,7 +983,7 @@ template <typename T, int NB> cudaError_t walks_go(const TcWalkArgs& w, const Tc
     return cudaGetLastError();
 }
 template <typename T, int NB> cudaError_t sums_go(const TcWalkArgs& w, const TcBackArgs& r, cudaStream_t st) {
-    constexpr int fwd = 2 * Stage<NB, kPParts<T>, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = fwd > back ? fwd : back;
+    constexpr int fwd = 2 * Stage<NB, false>::bytes, back = 2 * BackStage<NB>::bytes, bytes = fwd > back ? fwd : back;
     const cudaError_t e = la::allow_smem<k_sums<T, NB>>(bytes);
     if (e != cudaSuccess) return e;
     k_sums<T, NB><<<dim3((unsigned)(ceil_div(w.a.P, kTileP) * w.a.Bsz * w.a.H * w.plan.K), 3), kThreads, bytes, st>>>(w, r);
