@@ -15,8 +15,8 @@
 // tiles under the last item's end.  2 x 4096 tokens, 32 heads, N = P = 128, bf16: 310 us (a block a unit: 350; tiles sent to the
 // L2 cache ahead: 328 to 339).
 //
-// Roundings: E and F enter dq's and dk's products as one f16 (2^-12 of terms of a bf16 output; f16 io: in two parts).
-// H, R, U and X come in two f16 parts (22 bits), and dg and dbeta take all else in f32.
+// Roundings: H, R, U, X and the E and F of dq's and dk's products are f16 in two parts (22 bits), and dg and dbeta take all else
+// in f32.  (E and F as one part: 315 us for 346, but dq and dk of bf16 io 2^-12 off before their own rounding.)
 #include "../simd.cuh"
 #include "gdr_tc.cuh"
 
@@ -93,7 +93,6 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
     extern __shared__ __align__(1024) char sm[];
     using L = ChunkSmem<NB>;
     constexpr int W = 32 * NB;  // states of a thread
-    constexpr int EP = la::kF16<T> ? 2 : 1;  // parts of E and F in dq's and dk's products
     // landed: K and Q; an item's tiles; H or R.  Workers: E and F stand; H is copied; the item's tiles are read, its products.
     // Products: E; H's; R's; the pairs'
     __shared__ __align__(8) uint64_t s_key, s_in, s_h[2], s_ef, s_copied, s_read, s_done, s_c1, s_c2, s_c3, s_c4;
@@ -247,14 +246,14 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                     la::tc_fence_after();
                     if (elect()) {
 #pragma unroll
-                        for (int part = EP - 1; part >= 0; part--) {
+                        for (int part = 1; part >= 0; part--) {
                             const uint32_t left = part ? zl_at : ef_at;
 #pragma unroll
                             for (int s = 0; s < 4; s++)
-                                la::mma(tm + cK, la::smem_desc(left + s * 32), la::smem_desc(keys_at + s * 2048, 16384), kw, part < EP - 1 || s > 0);
+                                la::mma(tm + cK, la::smem_desc(left + s * 32), la::smem_desc(keys_at + s * 2048, 16384), kw, part < 1 || s > 0);
 #pragma unroll
                             for (int s = 0; s < 8; s++)
-                                la::mma(tm + cT, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + s * 2048, 16384), rw, part < EP - 1 || s > 0);
+                                la::mma(tm + cT, la::smem_desc(left + s * 2048, 0), la::smem_desc(keys_at + s * 2048, 16384), rw, part < 1 || s > 0);
                         }
                         la::mma_commit(&s_c4);
                     }
@@ -270,7 +269,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                         la::mma_commit(&s_c3);
                     }
                     if (item + 1 < steps || id < units) {  // (E's and F's low part stands in Z's)
-                        if (!warp_wait(&s_read, ph, &s_fail) || !warp_wait(&s_c3, ph, &s_fail) || (EP > 1 && !warp_wait(&s_c4, ph, &s_fail))) break;
+                        if (!warp_wait(&s_read, ph, &s_fail) || !warp_wait(&s_c3, ph, &s_fail) || !warp_wait(&s_c4, ph, &s_fail)) break;
                         if (lane == 0) {
                             if (item + 1 < steps) load(work, item + 1);
                             else load(next, 0);
@@ -398,9 +397,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
 #pragma unroll
                     for (int i = 0; i < 8; i++) most = fmaxf(most, s_max[i]);
                     ef_scale = la::f16_scale(most) * rho;
-                    if (EP > 1) {  // the low part takes Z's, which H's product is done with
-                        ok = wait(&s_c2, ph, &s_fail) && ok;
-                    }
+                    ok = wait(&s_c2, ph, &s_fail) && ok;  // the low part takes Z's, which H's product is done with
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
                         uint32_t x[4], y[4];
@@ -412,7 +409,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                             y[i] = pack2<__half>(f.x, f.y);
                         }
                         *unit(EF, r, 4 * half + u) = make_uint4(x[0], x[1], x[2], x[3]);
-                        if (EP > 1) *unit(Zl, r, 4 * half + u) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *unit(Zl, r, 4 * half + u) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
                 if (tid < C) {

@@ -4,7 +4,7 @@ Operands that the tensor cores take are f16 in two parts: 22 bits, 2^-23 of a va
 * 16-bit outputs, each element: half a step of its own, and beside it what the operands' roundings leave.  A y passes some
   seven of them (S, X, M, U, P and the two products that leave out low times low) and sums of f32; the correction's
   inverse doubles them at these inputs (unit keys in 64 and more dimensions, rates below one): 2 (7 + 2) 2^-23 = 2.1e-6 of
-  the largest y, 2^-18 allowed.  (One part, 11 bits, is 2^-12: 2e-4.)
+  the largest y, 2^-18 allowed.  Gradients join two such chains: 2^-17.  (One part, 11 bits, is 2^-12: 2e-4.)
 * f32 outputs, norm of the error over the norm: roundings of 2^-24.8 root mean square, twenty of them in quadrature (dg
   and dbeta join two walks), doubled as above: 3e-7; the products' f32 sums, cut after each 16 terms: up to twenty-four
   of 2^-24 one way, 1.4e-6 if all fell on every value alike, half of which stays for steps of both signs: 1e-6 in all.
@@ -64,6 +64,16 @@ def test_y_is_rounded_once(shape, lengths, io):
     B, L = shape[:2]
     got, want = run(shape, io, lengths and [(2 * L // 3, 0, L)[i % 3] for i in range(B)])
     assert beyond_half_a_step(got["y"], want["y"], io) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("lengths", [None, "ragged"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_gradients_are_rounded_once(shape, lengths, io):
+    B, L = shape[:2]
+    got, want = run(shape, io, lengths and [(2 * L // 3, 0, L)[i % 3] for i in range(B)])
+    bad = {n: e for n in ("dq", "dk", "dv") if not (e := beyond_half_a_step(got[n], want[n], io)) <= 2.0 ** -17}
+    assert not bad, bad
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
