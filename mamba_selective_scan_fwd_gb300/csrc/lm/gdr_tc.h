@@ -36,10 +36,9 @@ struct ImageHead {
     float by;            // the chunk's decay as la::Decay
     int32_t weak;
     float inv_k, inv_q, inv_m, inv_p;  // what undoes the scales of K, Q, M and P
-    float most_bu, most_down;  // largest |beta_up|, largest down
-    float most_k, most_q, most_p, most_m;  // largest values of K, Q, P and M
+    float most_k, most_q, most_m;  // largest values of K, Q and M
     int32_t flat;              // whether tail may stand for differences inside a run
-    float pad[51];
+    float pad[54];
 };
 static_assert(sizeof(ImageHead) == 2048, "bulk copies are multiples of 16 bytes");
 constexpr int kImageBytes = 4 * kTileBytes + (int)sizeof(ImageHead);

@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     __shared__ __align__(16) float s_tail[kHeads][C];  // e^{c_e - c_t}, e the end of the token's run of 16
     __shared__ float s_beta[kHeads][C], s_max[2][4];
     __shared__ la::Decay s_by[kHeads];
-    __shared__ float s_bu[kHeads], s_down[kHeads];
     __shared__ bool s_flat[kHeads];  // no run of 16 leaves 2^-64 .. 2^64
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -206,23 +205,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
         const float x[2] = {la::clamp_g(g[0]) * la::kLog2e, la::clamp_g(g[1]) * la::kLog2e};
         bool flat;
         const Pair p = chunk_decays(x, s_c[warp], s_tail[warp], flat);
-        const Two(&c)[2] = p.c;
-        float bu = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            s_beta[warp][2 * lane + i] = beta_t[i];
-            bu = fmaxf(bu, fabsf(beta_t[i] * ex2a(c[i].h)));
-        }
-        bu = warp_max(bu);
-        const Two cl = {__shfl_sync(kFull, c[1].h, 31), __shfl_sync(kFull, c[1].l, 31)};
-        const float down = warp_max(fmaxf(ex2a(two_diff(cl, c[0])), ex2a(two_diff(cl, c[1]))));
-        if (lane == 0) {
-            s_flat[warp] = flat;
-            s_bu[warp] = bu;
-            s_down[warp] = down;
-        }
+        for (int i = 0; i < 2; i++) s_beta[warp][2 * lane + i] = beta_t[i];
+        if (lane == 0) s_flat[warp] = flat;
         // the chunk's decay, in natural units from the same sum (rounded once more: 2^-24 of cl)
-        if (lane == 31) s_by[warp] = la::decay_of((c[1].h + c[1].l) * kLn2);
+        if (lane == 31) s_by[warp] = la::decay_of((p.c[1].h + p.c[1].l) * kLn2);
     };
     if (h_lo + warp < h_hi) decays();
     __syncthreads();
@@ -333,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 head->c[tid] = make_float2(c.h, c.l);
             }
             __syncthreads();
-            const float most_p = fmaxf(s_max[0][2], s_max[0][3]), scale_p = la::f16_scale(most_p);
+            const float scale_p = la::f16_scale(fmaxf(s_max[0][2], s_max[0][3]));
             if (is_q) {
                 char* hi = I + 2 * kTileBytes;
 #pragma unroll
@@ -363,8 +350,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 put_parts(I, I + kTileBytes, i, j0 / 8 + 2, x + 16, scale_m);
                 if (tid == 0) {
                     head->by = s_by[hl].by;
-                    head->most_bu = s_bu[hl];
-                    head->most_down = s_down[hl];
                     head->weak = s_by[hl].weak;
                     head->flat = s_flat[hl];
                     head->inv_k = 1.0f / scale_k;
@@ -373,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                     head->inv_p = 1.0f / scale_p;
                     head->most_k = most_k;
                     head->most_q = most_q;
-                    head->most_p = most_p;
                     head->most_m = most_m;
                 }
             }
