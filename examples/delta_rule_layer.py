@@ -16,6 +16,7 @@ import sys
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
@@ -32,6 +33,7 @@ class QKNorm(torch.autograd.Function):
         return ss.ss_qknorm_fwd(q, k, q_weight, k_weight, positions, freqs, l2=True)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, positions, freqs = ctx.saved_tensors
         d = ss.ss_qknorm_bwd(q, k, dq.contiguous(), dk.contiguous(), q_weight, k_weight, positions, freqs, l2=True)
@@ -49,6 +51,7 @@ class GatedDeltaRule(torch.autograd.Function):
         return y, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dlast):
         q, k, v, g, beta, h0, lengths = ctx.saved_tensors
         d = ss.ss_gdr_bwd(q, k, v, g, beta, dy.contiguous(), scale=ctx.scale, h0=h0, dlast_state=dlast.contiguous(),

@@ -15,6 +15,7 @@ import sys
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import mamba_selective_scan_fwd_gb300 as ss  # noqa: E402
@@ -31,6 +32,7 @@ class LinearAttention(torch.autograd.Function):
         return y, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dlast):
         q, k, v, g, h0, lengths = ctx.saved_tensors
         d = ss.ss_la_bwd(q, k, v, g, dy.contiguous(), scale=ctx.scale, h0=h0, dlast_state=dlast.contiguous(),
@@ -48,6 +50,7 @@ class GatedNorm(torch.autograd.Function):
         return ss.ss_gnorm_fwd(x, weight, bias, z, groups=groups)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x, weight, bias, z = ctx.saved_tensors
         d = ss.ss_gnorm_bwd(x, weight, bias, dout.contiguous(), z=z, groups=ctx.groups)
