@@ -312,6 +312,8 @@ def _workspace(nbytes, device, workspace):
 
     if workspace is None and nbytes > 0:
         workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
+    elif workspace is not None and not (workspace.device == device and workspace.is_contiguous()):
+        _require(workspace, "workspace", workspace.shape, workspace.dtype, device)
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return workspace, size
 
