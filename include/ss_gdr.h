@@ -25,11 +25,20 @@
  * are contiguous, *_token / *_batch are distances in elements.  Outputs are
  * contiguous and overlap no input.
  *
- * exp(g) = 0 (g = -inf or below -128) resets the state.  g <= 0 and any finite
- * beta are in range; positive g lets the state grow, and is in range as long as no
- * run of tokens inside 64 adds up to more than 60.  Tokens of 64 share matrix
- * products: a non-finite q, k, v, g or beta may reach any y of its 64 tokens, and
- * all later ones.
+ * exp(g) = 0 (g = -inf or below -128) resets the state.  g <= 0 is in range, and
+ * so is positive g, which lets the state grow, as long as no run of tokens inside
+ * 64 adds up to more than 60.  Any finite beta is in range on f32 inputs, and on
+ * 16-bit ones as long as rates with beta |k|^2 > 2 do not multiply the state by more
+ * than 2^16 inside 64 tokens.  Tokens of 64 share matrix products: a non-finite q,
+ * k, v, g or beta may reach any y of its 64 tokens, and all later ones.
+ *
+ * Precision.  f32 inputs: as f32 sums have it.  16-bit inputs: every value that the
+ * chunks of 64 tokens make has 22 bits, 16-bit outputs are rounded once, f32 ones
+ * are good to 1e-6 of their norm.  A channel's values in a chunk (v's and the
+ * state's share, and the adjoints) have 22 bits down to 2^-16 of the largest of
+ * them and lose one a power of two below: what is left of a state, or of an adjoint,
+ * that 64 tokens take below that is good by what it was, not by itself.  q and k of
+ * bf16 are exact down to 2^-27 of the largest in their 64 tokens and head.
  *
  * io is f32, f16 or bf16 (`dtype`, as in ss.h); states, decays, rates, sums, dg,
  * dbeta and dh0 are f32, dq, dk and dv have the io type.  Any 1 <= N <= 128 and

@@ -198,7 +198,7 @@ struct BwdTc {
     TcPlan plan;
     int64_t chunks;
     int splits;
-    size_t starts, ends, phi, phi_t, keys, images, before, after, us, xs, dys, before_inv, after_inv, u_inv, x_inv, dy_inv, dq, dk;
+    size_t starts, ends, phi, phi_t, keys, images, turned, before, after, us, xs, dys, before_inv, after_inv, u_inv, x_inv, dy_inv, dq, dk;
 };
 BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
     BwdTc f;
@@ -211,6 +211,7 @@ BwdTc bwdtc_layout(Layout& l, int64_t Bsz, int64_t L, int64_t H, int64_t G, int6
     const size_t heads = (size_t)Bsz * H * f.chunks, tiles = heads * ceil_div(P, kTileP);
     f.keys = l.take((size_t)Bsz * f.chunks * G * key_bytes(N));
     f.images = l.take(heads * kImageBytes);
+    f.turned = l.take(heads * kTurnedBytes);
     f.before = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
     f.after = l.take(tiles * state_bytes(N > 64 ? 2 : 1));
     f.us = l.take(tiles * kRowsBytes);
@@ -250,6 +251,7 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     p.splits = f.splits;
     p.keys = ws + f.keys;
     p.images = ws + f.images;
+    p.turned = ws + f.turned;
     p.status = w.status;
     w.a = a;
     w.plan = f.plan;
@@ -271,6 +273,7 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     r.xs = ws + f.xs;
     r.state_inv = f32(f.after_inv);
     r.x_inv = f32(f.x_inv);
+    r.turned = p.turned;
     r.dys = ws + f.dys;
     r.dy_inv = f32(f.dy_inv);
     c.a = a;
@@ -296,7 +299,7 @@ int tc_backward(const Args& a, const ss_gdr_bwd_desc& d, cudaStream_t st, bool* 
     c.dg = d.dg;
     c.dbeta = d.dbeta;
     c.status = w.status;
-    if (launch_prep(p, st) != cudaSuccess || launch_dy(a, f.chunks, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess) return SS_ERR_CUDA;
+    if (launch_prep(p, st) != cudaSuccess || launch_dy(a, f.chunks, p.images, ws + f.dys, f32(f.dy_inv), st) != cudaSuccess) return SS_ERR_CUDA;
     if (w.plan.K > 1 && (launch_tc_sums(w, r, st) != cudaSuccess || launch_tc_carry(w, &r, st) != cudaSuccess)) return SS_ERR_CUDA;
     if (launch_tc_walks(w, r, st) != cudaSuccess || launch_tc_chunks(c, st) != cudaSuccess) return SS_ERR_CUDA;
     if (f.splits > 1 &&

@@ -4,7 +4,7 @@
 // before it, A_ij = beta_i e^{c_i - c_j} k_i . k_j (j < i) and M = (I + A)^{-1}:
 //   U = M beta (V - e^c K H),   y = scale (e^c Q H + P U),   P_ij = e^{c_i - c_j} q_i . k_j (j <= i)
 //   H <- e^{cl} H + (e^{cl - c} K)^T U
-// M and P do not depend on the state: a first kernel makes them for all chunks at once
+// (where decays grow, c and all values of a token less its growth: gdr_dev.cuh.)  M and P do not depend on the state: a first kernel makes them for all chunks at once
 // (an "image" per chunk and head), a second walks the chunks.
 #pragma once
 
@@ -29,19 +29,25 @@ constexpr int key_bytes(int64_t N) { return (N > 64 ? 4 : 2) * kTileBytes; }
 struct ImageHead {
     float up[kChunk];    // e^{c_t}
     float down[kChunk];  // e^{cl - c_t}
-    float beta[kChunk];
+    float beta[kChunk];     // beta_t / grow_t
     float beta_up[kChunk];  // beta_t e^{c_t}
     float tail[kChunk];     // e^{c_e - c_t}, e the end of the token's run of 16 (chunk_decays)
     float2 c[kChunk];       // c_t in units of log 2, the sum of two floats
+    __nv_bfloat16 grow[kChunk];  // growth: a token's values are in units of this power of two, 2^{d_t}
     float by;            // the chunk's decay as la::Decay
     int32_t weak;
     float inv_k, inv_q, inv_m, inv_p;  // what undoes the scales of K, Q, M and P
     float most_k, most_q, most_m;  // largest values of K, Q and M
     int32_t flat;              // whether tail may stand for differences inside a run
-    float pad[54];
+    int32_t grown;             // whether any token's growth is not one
+    int8_t rise[kChunk];       // log2 of the unit of values over that of adjoints
+    float pad[5];
 };
 static_assert(sizeof(ImageHead) == 2048, "bulk copies are multiples of 16 bytes");
 constexpr int kImageBytes = 4 * kTileBytes + (int)sizeof(ImageHead);
+// The backward's images hold P in the adjoints' units.  Where a chunk grows, M and the factors in those units are in a place
+// of their own beside the images, which only the walk of the adjoints reads.
+constexpr int kTurnedBytes = 2 * kTileBytes + (int)sizeof(ImageHead);
 
 struct PrepArgs {
     CUtensorMap q, k;  // {width, heads, L, Bsz}, boxes of 64 columns x 64 tokens
@@ -50,6 +56,7 @@ struct PrepArgs {
     int splits;        // blocks the heads of a group are divided into
     char* keys;        // [Bsz, chunks, G]
     char* images;      // [Bsz, H, chunks]
+    char* turned;      // the same, of chunks that grow; null: forward
     int* status;
 };
 cudaError_t launch_prep(const PrepArgs& w, cudaStream_t st);
@@ -86,6 +93,7 @@ struct TcWalkArgs {
 // The backward's walk over the chunks from the last: x and, as images like the forward's, the state's
 // adjoint after each chunk and X.
 struct TcBackArgs {
+    const char* turned;
     const char* dys;    // images of dY
     const float* dy_inv;
     const float* init;  // gradient of the last state, or null
@@ -94,7 +102,7 @@ struct TcBackArgs {
     float *state_inv, *x_inv;
     float* seg_state;   // what a segment does to an adjoint of zero, then the adjoints they start from
 };
-cudaError_t launch_dy(const Args& a, int64_t chunks, char* dys, float* dy_inv, cudaStream_t st);
+cudaError_t launch_dy(const Args& a, int64_t chunks, const char* images, char* dys, float* dy_inv, cudaStream_t st);
 // What is left of the backward, one chunk at a time.
 struct TcChunkArgs {
     Args a;

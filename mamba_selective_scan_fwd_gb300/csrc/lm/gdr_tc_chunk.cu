@@ -331,8 +331,10 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                         vv[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + b * a.v.batch + (t0 + vt) * a.v.token + h * a.P + p0 + vp + 8 * u);
                 }
                 ok = wait(&s_in, ph, &s_fail) && ok;
+                // X and dY are in the adjoints' units, U in the values'
+                auto rise = [&](int t) { return head->grown ? power2(head->rise[t]) : 1.0f; };
                 {
-                    const float beta = head->beta[vt];
+                    const float beta = head->beta[vt] * rise(vt);
                     float sum = 0.0f;
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
@@ -353,7 +355,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                         }
                         put_dv(h, p0, vt, vp / 8 + u, make_uint4(out[0], out[1], out[2], out[3]));
                     }
-                    s_xv[tid >> 6][vt] = sum;
+                    s_xv[tid >> 6][vt] = head->grown ? sum * rise(vt) / la::ldf(&head->grow[vt]) : sum;
                 }
                 // H's tiles go to registers, for <R, H>, and make room for R's
                 uint4 hs[NB][8];
@@ -367,7 +369,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                 arrive(&s_copied);
                 ok = wait(&s_c1, ph, &s_fail) && ok;
                 la::tc_fence_after();
-                const float inv_k = head->inv_k, inv_q = head->inv_q, beta = head->beta[tok], rho = q_side ? inv_q / inv_k : 1.0f;
+                auto rate = [&](int t) { return head->grown ? head->beta[t] * la::ldf(&head->grow[t]) : head->beta[t]; };
+                const float inv_k = head->inv_k, inv_q = head->inv_q, beta = rate(tok), rho = q_side ? inv_q / inv_k : 1.0f;
                 float ef_scale;
                 {
                     float e[32], k[32];
@@ -375,7 +378,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                     la::tmem_ld32(tm + my + cQK + 32 * half, k);
                     const Two* c = reinterpret_cast<const Two*>(head->c);
                     const Two ci = c[tok];
-                    const float f = u_inv * (q_side ? a.scale * dy_inv : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
+                    const float f = rise(tok) * u_inv * (q_side ? a.scale * dy_inv : x_inv), kf = (q_side ? inv_q : inv_k) * inv_k;
                     const int last = q_side ? tok : tok - 1;
                     pair_factors(e, c, head->tail, head->flat != 0, 32 * half, ci, f, last);
                     // of a key's row: e^{c_i - c_j} x_i . u_j so far
@@ -417,7 +420,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                     float col = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; i++) col += s_col[(tid >> 5) * 4 + i][tid & 31];
-                    s_b[tid] += col - (rows_q - head->beta[tid] * rows_k);
+                    s_b[tid] += col - (rows_q - rate(tid) * rows_k);
                     s_db[tid] += ((s_xv[0][tid] + s_xv[1][tid]) + (s_xv[2][tid] + s_xv[3][tid])) - rows_k;
                 }
                 fence_proxy_async_smem();
@@ -425,7 +428,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(kThreads, 1) k_c
                 // H's products
                 ok = wait(&s_c2, ph, &s_fail) && ok;
                 la::tc_fence_after();
-                const float up = head->up[tok], down = head->down[tok], all = head->up[C - 1];
+                const float up = head->up[tok] * rise(tok), down = head->down[tok], all = head->up[C - 1] * la::ldf(&head->grow[C - 1]);
                 {
                     const float f = before_inv * (q_side ? a.scale * up * dy_inv : -beta * up * x_inv);
                     float dot = 0.0f;

@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     __shared__ float s_beta[kHeads][C], s_max[2][4];
     __shared__ la::Decay s_by[kHeads];
     __shared__ bool s_flat[kHeads];  // no run of 16 leaves 2^-64 .. 2^64
+    __shared__ int8_t s_grow[kHeads][C], s_rise[kHeads][C];
+    __shared__ bool s_grown[kHeads];
     const Args& a = w.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned id = blockIdx.x;
@@ -206,10 +208,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
         bool flat;
         const Pair p = chunk_decays(x, s_c[warp], s_tail[warp], flat);
 #pragma unroll
-        for (int i = 0; i < 2; i++) s_beta[warp][2 * lane + i] = beta_t[i];
-        if (lane == 0) s_flat[warp] = flat;
+        for (int i = 0; i < 2; i++) {
+            s_beta[warp][2 * lane + i] = beta_t[i];
+            s_grow[warp][2 * lane + i] = (int8_t)p.grow[i];
+            s_rise[warp][2 * lane + i] = (int8_t)p.rise[i];
+        }
+        const bool grown = __any_sync(kFull, p.grow[0] | p.grow[1] | p.rise[0] | p.rise[1]);
+        if (lane == 0) {
+            s_flat[warp] = flat;
+            s_grown[warp] = grown;
+        }
         // the chunk's decay, in natural units from the same sum (rounded once more: 2^-24 of cl)
-        if (lane == 31) s_by[warp] = la::decay_of((p.c[1].h + p.c[1].l) * kLn2);
+        if (lane == 31) s_by[warp] = la::decay_of((p.sum.h + p.sum.l) * kLn2);
     };
     if (h_lo + warp < h_hi) decays();
     __syncthreads();
@@ -298,8 +308,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
             if (i >= nv)  // (whatever the row holds)
 #pragma unroll
                 for (int j = 0; j < C; j++) s[j] = 0.0f;
+            const bool turned = w.turned && s_grown[hl];
             float most = 0.0f;
             if (is_q) {
+                if (turned)
+#pragma unroll
+                    for (int j = 0; j < C; j++) s[j] *= power2(s_rise[hl][i] - s_rise[hl][j]);
 #pragma unroll
                 for (int j = 0; j < C; j++) most = fmaxf(most, fabsf(s[j]));
                 most = warp_max(most);
@@ -314,8 +328,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                 const float up = ex2a(c.h + c.l);
                 head->up[tid] = up;
                 head->beta_up[tid] = s_beta[hl][tid] * up;
-                head->down[tid] = ex2a(two_diff(cl, c));
-                head->beta[tid] = s_beta[hl][tid];
+                head->down[tid] = ex2a(two_diff(cl, c)) * power2(s_grow[hl][C - 1]);
+                head->beta[tid] = s_beta[hl][tid] * power2(-s_grow[hl][tid]);
+                head->grow[tid] = __float2bfloat16(power2(s_grow[hl][tid]));
+                head->rise[tid] = s_rise[hl][tid];
                 head->tail[tid] = s_tail[hl][tid];
                 head->c[tid] = make_float2(c.h, c.l);
             }
@@ -352,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
                     head->by = s_by[hl].by;
                     head->weak = s_by[hl].weak;
                     head->flat = s_flat[hl];
+                    head->grown = s_grown[hl];
                     head->inv_k = 1.0f / scale_k;
                     head->inv_q = 1.0f / scale_q;
                     head->inv_m = 1.0f / scale_m;
@@ -366,7 +383,43 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
             if (tid == 0) {
                 la::bulk_store(w.images + ((b * a.H + h) * w.chunks + chunk) * kImageBytes, I, kImageBytes);
                 la::bulk_commit();
-                if (h + 1 < h_hi) la::bulk_wait_read();
+                if (turned || h + 1 < h_hi) la::bulk_wait_read();
+            }
+            if (turned) {  // M and the factors in the adjoints' units
+                __syncthreads();
+                if (tid < C) {
+                    const float by = power2(s_rise[hl][tid]);
+                    head->up[tid] *= by;
+                    head->beta_up[tid] *= by;
+                    head->down[tid] *= power2(-s_rise[hl][tid]);
+                }
+                const int i = tid >> 1, j0 = (tid & 1) * 32;
+                float most = 0.0f;
+#pragma unroll 1
+                for (int j = j0; j < j0 + 32; j++) {
+                    float& x = A[i * LDA + j];
+                    x *= power2(s_rise[hl][i] - s_rise[hl][j]);
+                    most = fmaxf(most, fabsf(x));
+                }
+                most = warp_max(most);
+                if (lane == 0) s_max[1][warp] = most;
+                __syncthreads();
+                const float most_m = max4(s_max[1]), scale_m = la::f16_scale(most_m);
+#pragma unroll 1
+                for (int j = j0; j < j0 + 32; j += 16) put_parts(I, I + kTileBytes, i, j / 8, A + i * LDA + j, scale_m);
+                if (tid == 0) {
+                    head->inv_m = 1.0f / scale_m;
+                    head->most_m = most_m;
+                }
+                fence_proxy_async_smem();
+                __syncthreads();
+                if (tid == 0) {
+                    char* to = w.turned + ((b * a.H + h) * w.chunks + chunk) * kTurnedBytes;
+                    la::bulk_store(to, I, 2 * kTileBytes);
+                    la::bulk_store(to + 2 * kTileBytes, head, sizeof(ImageHead));
+                    la::bulk_commit();
+                    if (h + 1 < h_hi) la::bulk_wait_read();
+                }
             }
         }
     }
@@ -375,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
     la::end_block(&s_fail, w.status, bars, tm, 64);
 }
 
-// dY's image: 64 tokens of 128 value channels of one head, transposed, f16 under the scale of its largest value; tokens past
-// the row's length zero.  Bound by HBM (2 x 4096 tokens, 32 heads of 128: 32.5 us, copying 20).
-template <typename T> __global__ void __launch_bounds__(256) k_dy(Args a, int64_t chunks, char* dys, float* dy_inv) {
+// dY's image: 64 tokens of 128 value channels of one head, transposed, in the adjoints' units, f16 under the scale of its largest
+// value; tokens past the row's length zero.  Bound by HBM (2 x 4096 tokens, 32 heads of 128: 32.5 us, copying 20).
+template <typename T> __global__ void __launch_bounds__(256, 8) k_dy(Args a, int64_t chunks, const char* images, char* dys, float* dy_inv) {
     constexpr int LD = 132;  // (a row's 16-byte units spread over the banks)
     __shared__ __align__(16) T s[C][LD];
     __shared__ float s_max[8];
@@ -390,7 +443,10 @@ template <typename T> __global__ void __launch_bounds__(256) k_dy(Args a, int64_
     const int nv = (int)max((int64_t)0, min((int64_t)C, row_length(a, b) - t0));
     if (nv == 0) return;
     const T* from = static_cast<const T*>(a.dy.p) + b * a.dy.batch + t0 * a.dy.token + h * a.P + p0;
-    float most = 0.0f;
+    const ImageHead* head = reinterpret_cast<const ImageHead*>(images + (bh * chunks + chunk) * kImageBytes + 4 * kTileBytes);
+    const bool grown = head->grown;
+    auto unit_of = [&](int t) { return ldf(&head->grow[t]) * power2(-head->rise[t]); };
+    float m[4] = {}, most = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int t = (tid + 256 * i) >> 4, u = tid & 15;
@@ -400,11 +456,13 @@ template <typename T> __global__ void __launch_bounds__(256) k_dy(Args a, int64_
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const float2 f = unpack2<T>(v[e]);
-            most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+            m[i] = fmaxf(m[i], fmaxf(fabsf(f.x), fabsf(f.y)));
         }
         *reinterpret_cast<uint2*>(&s[t][8 * u]) = make_uint2(x.x, x.y);
         *reinterpret_cast<uint2*>(&s[t][8 * u + 4]) = make_uint2(x.z, x.w);
     }
+#pragma unroll
+    for (int i = 0; i < 4; i++) most = fmaxf(most, grown ? m[i] * unit_of((tid + 256 * i) >> 4) : m[i]);
     most = warp_max(most);
     if (lane == 0) s_max[warp] = most;
     __syncthreads();
@@ -416,8 +474,16 @@ template <typename T> __global__ void __launch_bounds__(256) k_dy(Args a, int64_
     for (int i = 0; i < 4; i++) {
         const int at = tid + 256 * i, p = at >> 3, u = (at & 7) ^ (p & 7);
         uint32_t x[4];
+        if (!grown) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) x[e] = pack2<__half>(scale * ldf(&s[8 * u + 2 * e][p]), scale * ldf(&s[8 * u + 2 * e + 1][p]));
+            for (int e = 0; e < 4; e++) x[e] = pack2<__half>(scale * ldf(&s[8 * u + 2 * e][p]), scale * ldf(&s[8 * u + 2 * e + 1][p]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int t = 8 * u + 2 * e;
+                x[e] = pack2<__half>(scale * unit_of(t) * ldf(&s[t][p]), scale * unit_of(t + 1) * ldf(&s[t + 1][p]));
+            }
+        }
         *reinterpret_cast<uint4*>(to + at * 16) = make_uint4(x[0], x[1], x[2], x[3]);
     }
     if (tid == 0) dy_inv[blockIdx.x] = most == 0.0f ? 0.0f : 1.0f / scale;  // (zeros bound nothing)
@@ -433,10 +499,10 @@ template <typename T, int NB> cudaError_t prep_go(const PrepArgs& w, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_dy(const Args& a, int64_t chunks, char* dys, float* dy_inv, cudaStream_t st) {
+cudaError_t launch_dy(const Args& a, int64_t chunks, const char* images, char* dys, float* dy_inv, cudaStream_t st) {
     const unsigned grid = (unsigned)(a.Bsz * a.H * ceil_div(a.P, kTileP) * chunks);
-    if (a.dtype == 1) k_dy<__half><<<grid, 256, 0, st>>>(a, chunks, dys, dy_inv);
-    else k_dy<bf16><<<grid, 256, 0, st>>>(a, chunks, dys, dy_inv);
+    if (a.dtype == 1) k_dy<__half><<<grid, 256, 0, st>>>(a, chunks, images, dys, dy_inv);
+    else k_dy<bf16><<<grid, 256, 0, st>>>(a, chunks, images, dys, dy_inv);
     return cudaGetLastError();
 }
 

@@ -35,7 +35,8 @@ using la::unpack2;
 
 constexpr int C = kChunk;
 constexpr int kStateThreads = 256, kThreads = 512;  // state; output; loads and products (one thread of the last 128)
-// Registers a thread: 128 at launch; the state's threads take what the others leave (2 x 168 + 112 + 56 of 4 x 128).
+// Registers a thread: 128 at launch; the state's threads take what the others leave (2 x 168 + 112 + 56 of 4 x 128, 120 for
+// the threads that write y).
 template <int N> __device__ __forceinline__ void take_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void leave_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -359,7 +360,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     if (half * W + n < a.N) to[(half * W + n) * width + p] = S[n];
         }
     } else if (warp < kStateThreads / 32 + 4) {
-        leave_regs<112>();
+        leave_regs<OUT ? 120 : 112>();
         const bool first = tid == kStateThreads;
         if (OUT) {
             T* yp = static_cast<T*>(w.yp) + (b * a.L * a.H + h) * a.P;
@@ -371,15 +372,16 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 wait(&s_full[ph], (ch >> 1) & 1, &s_fail);
                 wait(&s_d1, ph, &s_fail);
                 la::tc_fence_after();
-                float q[64];
+                float2 q[32];
                 {
-                    const float inv = a.scale * head->inv_q / s_ss[ph][pl];
+                    const float2 inv = splat2(a.scale * head->inv_q / s_ss[ph][pl]);
 #pragma unroll
                     for (int hf = 0; hf < 2; hf++) {
                         float x[32];
                         la::tmem_ld32(tm + my + kQ + 32 * hf, x);
 #pragma unroll
-                        for (int j = 0; j < 32; j++) q[32 * hf + j] = inv * head->up[32 * hf + j] * x[j];
+                        for (int j = 0; j < 32; j += 2)
+                            q[16 * hf + j / 2] = mul2(mul2(inv, *reinterpret_cast<const float2*>(&head->up[32 * hf + j])), make_float2(x[j], x[j + 1]));
                     }
                 }
                 arrive(&s_early);
@@ -387,7 +389,7 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                 named_sync(5, 128);  // the staging tiles are free
                 wait(&s_y, ph, &s_fail);
                 la::tc_fence_after();
-                const float inv = a.scale * head->inv_p / s_us[ph][pl];
+                const float2 inv = splat2(a.scale * head->inv_p / s_us[ph][pl]);
                 char* tile = staging + (pl >> 6) * kTileBytes + (pl & 7) * 2;
                 const int cu = (pl & 63) >> 3;
 #pragma unroll
@@ -395,10 +397,11 @@ template <typename T, int NB, TcWalkMode MODE> __device__ __forceinline__ void w
                     float y[32];
                     la::tmem_ld32(tm + my + kY + 32 * hf, y);
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
+                    for (int j = 0; j < 32; j += 2) {
                         const int t = 32 * hf + j;
-                        const float x = fmaf(inv, y[j], q[t]);
-                        st(reinterpret_cast<T*>(tile + t * 128 + ((cu ^ (t & 7)) << 4)), t < nv ? x : 0.0f);
+                        const float2 x = mul2(fma2(inv, make_float2(y[j], y[j + 1]), q[t / 2]), unpack2<__nv_bfloat16>(*reinterpret_cast<const uint32_t*>(&head->grow[t])));
+                        st(reinterpret_cast<T*>(tile + t * 128 + ((cu ^ (t & 7)) << 4)), t < nv ? x.x : 0.0f);
+                        st(reinterpret_cast<T*>(tile + (t + 1) * 128 + ((cu ^ ((t + 1) & 7)) << 4)), t + 1 < nv ? x.y : 0.0f);
                     }
                 }
                 arrive(&s_late);
@@ -789,7 +792,11 @@ template <int NB, bool SUM> __device__ __forceinline__ void walk_back(const TcWa
         leave_regs<56>();
         const int role = __shfl_sync(kFull, warp, 0) - (kThreads - 128) / 32, steps = __shfl_sync(kFull, chunks, 0);
         if (role == 1 && (tid & 31) == 0) {  // loads
+            auto image = [&](int i) { return w.images + (bh * w.chunks + chunk_of(i)) * kImageBytes; };
+            auto grows = [&](int i) { return i < chunks ? reinterpret_cast<const ImageHead*>(image(i) + 4 * kTileBytes)->grown : 0; };
+            int grown = grows(0);
             for (int i = 0; i < chunks; i++) {
+                const int next = grows(i + 1);  // (on its way while the stage is waited for)
                 if (i > 1 && !wait(&s_free[i & 1], ((i >> 1) + 1) & 1, &s_fail)) break;
                 char* at = sm + (i & 1) * L::bytes;
                 uint64_t* bar = &s_full[i & 1];
@@ -797,7 +804,15 @@ template <int NB, bool SUM> __device__ __forceinline__ void walk_back(const TcWa
                 mbar_expect_tx(bar, NB * L::block + 6 * kTileBytes + (int)sizeof(ImageHead));
                 bulk_load(at, w.keys + ((b * w.chunks + ch) * a.G + hq) * (NB * 2 * kTileBytes), NB * L::block, bar);
                 bulk_load(at + L::dy, r.dys + (images + ch) * kPieceBytes, kPieceBytes, bar);
-                bulk_load(at + L::image, w.images + (bh * w.chunks + ch) * kImageBytes, 4 * kTileBytes + (int)sizeof(ImageHead), bar);
+                if (!grown) {
+                    bulk_load(at + L::image, image(i), kImageBytes, bar);
+                } else {
+                    const char* turned = r.turned + (bh * w.chunks + ch) * kTurnedBytes;
+                    bulk_load(at + L::image, turned, 2 * kTileBytes, bar);
+                    bulk_load(at + L::image + 2 * kTileBytes, image(i) + 2 * kTileBytes, 2 * kTileBytes, bar);
+                    bulk_load(at + L::head, turned + 2 * kTileBytes, (int)sizeof(ImageHead), bar);
+                }
+                grown = next;
             }
         } else if (role == 0) {  // products
             for (int i = 0; i < steps; i++) {
