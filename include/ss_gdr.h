@@ -42,7 +42,11 @@
  *
  * io is f32, f16 or bf16 (`dtype`, as in ss.h); states, decays, rates, sums, dg,
  * dbeta and dh0 are f32, dq, dk and dv have the io type.  Any 1 <= N <= 128 and
- * P >= 1, any strides, any token-aligned pointers.
+ * P >= 1, any strides.  Inputs of q's, k's, v's and dy's kind, g, beta, lengths and
+ * slots may start at any element; states, outputs and workspaces (h0, last_state,
+ * dlast_state, state, y, dq, dk, dv, dg, dbeta, dh0) start on 16 bytes, else
+ * SS_ERR_UNSUPPORTED: a view such as pool[i:i+1] does where H * N * P is a multiple
+ * of four.
  */
 #ifndef SS_GDR_H
 #define SS_GDR_H
@@ -139,7 +143,9 @@ int ss_gdr_step(const ss_gdr_step_desc *desc, void *stream);
  *
  * q io [Bsz, L, Hq, N], k io [Bsz, L, Hk, N], slices of a wider projection allowed;
  * the outputs are contiguous, and may be the inputs themselves where those are.
- * 1 <= N <= 256, 2 * pairs <= N.
+ * 1 <= N <= 256, 2 * pairs <= N.  All pointers but the workspace's may start at any
+ * element.  Sums of squares are f32: the norm of a head is out of range above 1e19,
+ * and below 1e-19 with eps = 0.
  */
 enum { SS_QKNORM_L2 = 1, SS_QKNORM_INTERLEAVED = 2 };
 typedef struct {
