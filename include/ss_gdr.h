@@ -138,8 +138,8 @@ int ss_gdr_step(const ss_gdr_step_desc *desc, void *stream);
  *   (a, b) -> (a cos - b sin, b cos + a sin)
  * freqs f32 [pairs] (radians a token; NULL with pairs = 0: no rotation), positions
  * int32 [Bsz, L], or NULL: token t of each row stands at t.  The product of position
- * and frequency is reduced to a fraction of a turn in integers, so that far
- * positions keep the angle's accuracy.
+ * and frequency is reduced to a fraction of a turn in integers: the angle is good to
+ * 2^-26 turns and 2^-52 of the turns made, 2^-23 a radian a token and 2^31 tokens on.
  *
  * q io [Bsz, L, Hq, N], k io [Bsz, L, Hk, N], slices of a wider projection allowed;
  * the outputs are contiguous, and may be the inputs themselves where those are.
