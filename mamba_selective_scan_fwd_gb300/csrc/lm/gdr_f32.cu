@@ -115,12 +115,12 @@ template <typename T> __global__ void __launch_bounds__(128) k_pairs(Args a, Pai
 //   miss_t = v_t - e^{c_t} S^T k_t - sum_{j < t} e^{c_t - c_j} (k_t . k_j) u_j,   u_t = beta_t miss_t
 //   y_t = e^{c_t} S^T q_t + sum_{j <= t} e^{c_t - c_j} (q_t . k_j) u_j,   S <- e^{cl} S + sum_j e^{cl - c_j} k_j u_j^T
 // so that a chain of sums over the lanes is paid once for four tokens.  The backward's walk is the same from
-// the other end.  2 x 1000 tokens, 24 heads, N = P = 64: 146 us beside 13 for the pairs' products (token by token 228;
+// the other end.  2 x 1000 tokens, 24 heads, N = P = 64: 143 us beside 17 for the pairs' products (token by token 228;
 // with four interleaved chains of sums and q held in registers 149).
 //
 // Few heads of many tokens are cut into segments (walk_plan): the same walk takes their sums, whose columns (N of Phi, P of E)
 // are as independent, a carry joins them, and the walk proper starts from what it left.  Backward of 777 tokens, 16 heads, N 32,
-// P 64: 92 us in one piece, sums 31, carry 7 and walks 34 in four.
+// P 64: 92 us in one piece, sums 30, carry 7 and walks 32 in four.
 template <int LN, WalkMode MODE> struct WalkStage {
     static constexpr bool Q = MODE != kWalkSum && MODE != kWalkKeep;
     float k[kWalkT][16 * LN], q[Q ? kWalkT : 1][16 * LN], v[kWalkT][64 / LN];

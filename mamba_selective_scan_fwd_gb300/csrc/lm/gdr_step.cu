@@ -119,6 +119,7 @@ template <typename T> cudaError_t step_io(const StepArgs& s, cudaStream_t st) {
     auto blocks = [&](int64_t pt) { return (unsigned)(BH * ceil_div(s.P, pt)); };
     // rows of the state must be whole float4s (the pool itself is 16-byte aligned)
     if (s.P % 4 != 0) k_step<T, 1, 32><<<blocks(32), 128, 0, st>>>(s);
+    // fewer channels a block where there are SMs for them (one row of 32 heads, N = P = 128: 3.6 us, 4.5 with 64)
     else if (BH * ceil_div(s.P, 64) < kSms) k_step<T, 4, 4><<<blocks(16), 128, 0, st>>>(s);
     // 128 channels at once where they cost no idle lanes over 64: whole rows of 512 bytes (256 rows of 32 heads, N = P = 128:
     // 174 us, 184 with 64, 192 with 32; copying 159)

@@ -11,12 +11,13 @@
 // (k_i . k_j) (x_i . u_j);  dg is made of every path's two ends (gdr_f32.cu has the formula).
 //
 // An item's tiles fill shared memory, so one block an SM, and its products, the passes over their results and the loads of the
-// next tiles wait for one another: 15 thousand cycles an item.  Blocks therefore stay on their SM and load the next unit's
-// tiles under the last item's end.  2 x 4096 tokens, 32 heads, N = P = 128, bf16: 310 us (a block a unit: 350; tiles sent to the
-// L2 cache ahead: 328 to 339).
+// next tiles wait for one another: 23 thousand cycles an item (28 of them in 333 us at 1.96 GHz), and the workers' registers
+// spill some 500 bytes.  Blocks therefore stay on their SM and load the next unit's tiles under the last item's end.  2 x 4096
+// tokens, 32 heads, N = P = 128, bf16: 346 us (with E and F in one part 310, and then a block a unit 350, tiles sent to the L2
+// cache ahead 328 to 339).
 //
 // Roundings: H, R, U, X and the E and F of dq's and dk's products are f16 in two parts (22 bits), and dg and dbeta take all else
-// in f32.  (E and F as one part: 315 us for 346, but dq and dk of bf16 io 2^-12 off before their own rounding.)
+// in f32.  (E and F as one part are 10 % faster, but leave dq and dk of bf16 io 2^-12 off before their own rounding.)
 #include "../simd.cuh"
 #include "gdr_tc.cuh"
 

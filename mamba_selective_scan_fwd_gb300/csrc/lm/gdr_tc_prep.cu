@@ -4,7 +4,8 @@
 // One block: one chunk of the heads that share a head of q and k.  [K; Q] K^T is one
 // product of 128 rows.  Per head A = beta e^{c_i - c_j} k_i . k_j below the diagonal;
 // M = (I + A)^{-1} in f32 by forward substitution, in blocks (not by a series in A, whose
-// powers may be large where M is not).  One head at a time in a block of four warps: a block's
+// powers may be large where M is not).  4 x 4096 tokens, 32 heads in 16 groups, N = 128: 137 us, of which its 134 MB read and 420
+// written are 82.  One head at a time in a block of four warps: a block's
 // steps wait for one another, and four blocks on an SM cover that.
 #include "gdr_tc.h"
 #include "../simd.cuh"
@@ -68,8 +69,8 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 }
 // One warp: 16 x 16 of left right, n terms (a multiple of 8), operands in two tf32 parts.  (A warp's matrix instruction, because
 // such a product is too small for a tensor-memory one and its operands are f32 in shared memory, whose reads
-// bound this kernel: as products of four by two values a thread it took four times the reads; 4 x 4096 tokens, 32 heads: 133
-// us so, 127 with it.)
+// bound this kernel: as products of four by two values a thread it took four times the reads; 4 x 4096 tokens, 32 heads, P in
+// one part: 133 us so, 127 with it.)
 __device__ __forceinline__ void product16(const float* left, const float* right, int n, float (&out)[2][4]) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_prep(const __grid_constant__ Pr
 }
 
 // dY's image: 64 tokens of 128 value channels of one head, transposed, in the adjoints' units, f16 under the scale of its largest
-// value; tokens past the row's length zero.  Bound by HBM (2 x 4096 tokens, 32 heads of 128: 32.5 us, copying 20).
+// value; tokens past the row's length zero.  Bound by HBM (2 x 4096 tokens, 32 heads of 128: 30 us, copying 20).
 template <typename T> __global__ void __launch_bounds__(256, 8) k_dy(Args a, int64_t chunks, const char* images, char* dys, float* dy_inv) {
     constexpr int LD = 132;  // (a row's 16-byte units spread over the banks)
     __shared__ __align__(16) T s[C][LD];

@@ -10,11 +10,11 @@
 //   D3 = (e^{cl - c} U)^T K  [128 x N]    two parts;  S <- e^{cl} S + D3, f32 in registers
 //   y = scale (e^c S^T Q^T + U^T P^T)     off the chain: a third warpgroup writes it
 // One thread copies a chunk's tiles one chunk ahead, one warp issues all products.  The chain of a
-// chunk is three products and three passes through the registers, and bounds the walk: of some 6900 cycles
-// S's parts take 920, D1 1800, X 860, D2 800, U 1000, D3 980, the update 500 (the state's threads' clocks), the
-// products themselves 2950.  One block fills an SM's registers, so that nothing runs in the gaps.
-// 4 x 4096 tokens, 32 heads, N = P = 128, bf16: 250 us.  65536 tokens, 8 heads in 19 segments: 355 us for
-// the sums, 221 for the walk.
+// chunk is three products and three passes through the registers, and bounds the walk: of some 7100 cycles
+// (at 1.96 GHz) S's parts take 920, D1 1800, X 860, D2 800, U 1000, D3 980, the update 500 (the state's threads' clocks, of 6900
+// then), the products themselves 2950.  One block fills an SM's registers, so that nothing runs in the gaps.
+// 4 x 4096 tokens, 32 heads, N = P = 128, bf16: 242 us.  65536 tokens, 8 heads in 18 segments: 361 us for
+// the sums, 235 for the walk.
 //
 // Every operand made here is f16 in two parts (22 bits) under a power of two per channel, taken from the channel's
 // largest value, which its two threads exchange (for X by a bound instead: 245 us for 250, but a state of which a chunk leaves
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_sums(const __grid_constant__ Tc
 // S <- Phi S + E over the segments, from h0; seg_state receives the state each segment starts
 // from.  blockIdx.y 1: R <- Phi^T R + E' from the last.  A block: 8 columns of one head's state, in shared memory.  Warp w takes the terms of states w, w + 8, ..: a lane
 // four rows and all columns; the warps' sums are added in order.  The next Phi (transposed) is on its way while one is
-// used.  Bound by reading shared memory.  65536 tokens, 8 heads, 19 segments: 51 us (sums over states in single threads: 86).
+// used.  Bound by reading shared memory.  65536 tokens, 8 heads, 18 segments: 50 us (sums over states in single threads, 19 segments: 86).
 constexpr int kCarryCols = 8;
 __global__ void __launch_bounds__(256) k_carry(TcWalkArgs w, TcBackArgs r) {
     extern __shared__ __align__(16) float phi[];  // [2][N][N], then the warps' sums [8][N][8]
